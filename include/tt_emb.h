@@ -347,6 +347,135 @@ int tt_emb_timing_read(tt_emb_t h, double *ms, int32_t *count);
 /* Static name of a timer id (NULL if out of range). */
 const char *tt_emb_timer_name(int32_t id);
 
+/* ------------------------------------------------------------------------
+ * Operators around the table: what a language model (or a next-item model)
+ * needs beside its TT table, from token ids to the update of the weights.
+ * They take no handle.  All work is enqueued on `stream` of the current
+ * device; nothing allocates or synchronises.
+ *
+ * Types: TT_EMB_DTYPE_*.  A matrix argument is rows of contiguous elements,
+ * row i beginning at base + i * ld elements (ld >= columns); any element
+ * alignment is accepted, 16-byte aligned rows are fastest.  Sums and
+ * statistics are fp32 (or wider) whatever the types.
+ *
+ * Workspaces: the calls that need scratch take (ws, ws_bytes), 256-byte
+ * aligned, sized by the operator's *_workspace_size.  The first
+ * TT_EMB_STATUS_BYTES of a workspace must be zero before its first use; the
+ * library keeps its status word and counters there.  One workspace may serve
+ * any of these operators in turn on one stream; calls that may overlap need
+ * workspaces of their own.  Device-detected errors (a token or target out of
+ * range) set the status word and stay there until tt_emb_poll_status reads
+ * them; the offending row then counts as padding (or as ignored) and every
+ * kernel stays in bounds.
+ * Argument errors are returned before anything is enqueued. */
+enum {
+    TT_EMB_DTYPE_FLOAT = 0, /* fp32 */
+    TT_EMB_DTYPE_BFLOAT = 1, /* bfloat16 */
+    TT_EMB_DTYPE_HALF = 2   /* fp16 */
+};
+#define TT_EMB_STATUS_BYTES ((size_t)256)
+
+/* Synchronise the stream, then report and clear the status word of a
+ * workspace (TT_EMB_OK, or TT_EMB_ERR_INDEX). */
+int tt_emb_poll_status(void *ws, void *stream);
+
+/* Lookup: out[i] = scale * weight[tokens[i]] for i < n; weight [V][D] and out
+ * [n][D] of one type, tokens int64.  D <= 65536, V <= 2^31 - 2, n < 2^31.  A
+ * token outside [0, V) gives a row of zeros and TT_EMB_ERR_INDEX (ws needs
+ * TT_EMB_STATUS_BYTES). */
+int tt_emb_lookup_forward(const void *weight, int64_t ld_weight, const int64_t *tokens, int64_t n, int64_t V,
+                          int64_t D, int32_t dtype, float scale, void *out, int64_t ld_out, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* Its gradient: grad_weight[v] = scale * sum of grad_out[i] over the i with
+ * tokens[i] = v, zero rows where there is none, or added to what grad_weight
+ * holds when accumulate != 0 (only the touched rows are then read and
+ * written).  A token equal to padding_idx (negative: none) gives no gradient.
+ * Tokens are sorted stably and each row is summed in fp32 in an order that
+ * depends on the sorted tokens alone: results are bit-reproducible. */
+int tt_emb_lookup_backward(const void *grad_out, int64_t ld_grad, const int64_t *tokens, int64_t n, int64_t V,
+                           int64_t D, int32_t dtype, float scale, int64_t padding_idx, int32_t accumulate,
+                           void *grad_weight, int64_t ld_weight, void *ws, size_t ws_bytes, void *stream);
+int tt_emb_lookup_workspace_size(int64_t n, int64_t V, int64_t D, size_t *bytes);
+
+/* Layer norm over the last axis of x [n][D], D <= 16384:
+ *   mean_i = sum_j x_ij / D,  rstd_i = 1 / sqrt(sum_j (x_ij - mean_i)^2 / D + eps)
+ *   y_ij = (x_ij - mean_i) rstd_i gamma_j + beta_j
+ * x, y of `dtype`; gamma, beta [D] of `param_dtype` (dtype or fp32), each may
+ * be NULL (1 and 0); mean, rstd fp32 [n], each may be NULL. */
+int tt_emb_norm_forward(const void *x, int64_t ld_x, int64_t n, int64_t D, int32_t dtype, const void *gamma,
+                        const void *beta, int32_t param_dtype, float eps, void *y, int64_t ld_y, float *mean,
+                        float *rstd, void *stream);
+
+/* Its gradients, with a_ij = dy_ij gamma_j and xhat = (x - mean) rstd:
+ *   dx_ij = rstd_i (a_ij - sum_j a_ij / D - xhat_ij sum_j a_ij xhat_ij / D)
+ *   dgamma_j = sum_i dy_ij xhat_ij,  dbeta_j = sum_i dy_ij
+ * dgamma, dbeta of param_dtype, overwritten, each may be NULL; the sums over
+ * rows are taken in fp32 in a fixed order (bit-reproducible). */
+int tt_emb_norm_backward(const void *grad_y, int64_t ld_grad, const void *x, int64_t ld_x, int64_t n, int64_t D,
+                         int32_t dtype, const void *gamma, int32_t param_dtype, const float *mean,
+                         const float *rstd, void *grad_x, int64_t ld_grad_x, void *dgamma, void *dbeta, void *ws,
+                         size_t ws_bytes, void *stream);
+int tt_emb_norm_workspace_size(int64_t n, int64_t D, size_t *bytes);
+
+/* Softmax cross entropy of n hidden rows against a vocabulary of V rows:
+ *   z_iv = hidden_i . weight_v,  lse_i = log sum_v exp(z_iv)
+ *   loss_i = lse_i - z_{i,target_i}, or 0 where target_i = ignore_index
+ * hidden [n][D], weight [V][D] of one type (fp32 or bf16; others give
+ * TT_EMB_ERR_UNSUPPORTED), targets int64, loss and lse fp32 [n].  The logits
+ * are never stored: a tile of them lives in registers until its rows' running
+ * maximum and sum are known.  A target outside [0, V) that is not
+ * ignore_index counts as ignored and sets TT_EMB_ERR_INDEX.
+ * D <= 16384, n and V < 2^31. */
+int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weight, int64_t ld_weight,
+                        const int64_t *targets, int64_t n, int64_t V, int64_t D, int32_t dtype,
+                        int64_t ignore_index, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* The loss and both gradients in one call, for grad_loss fp32 [n] = dL/dloss_i
+ * (0 for ignored rows whatever it holds):
+ *   d_iv = grad_loss_i (exp(z_iv - lse_i) - [v = target_i])
+ *   grad_hidden_i = sum_v d_iv weight_v,  grad_weight_v = sum_i d_iv hidden_i
+ * both of `dtype`, overwritten.  The vocabulary is taken in pieces whose d
+ * (bf16 for bf16 inputs; split into three bf16 terms, 24 bits, for fp32
+ * inputs) is in ws; sums are fp32.  A larger ws allows larger pieces: any
+ * ws_bytes from *least of tt_emb_xent_workspace_size on is accepted, *bytes
+ * is the size past which nothing is gained. */
+int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *weight, int64_t ld_weight,
+                          const int64_t *targets, const float *grad_loss, int64_t n, int64_t V, int64_t D,
+                          int32_t dtype, int64_t ignore_index, float *loss, float *lse, void *grad_hidden,
+                          int64_t ld_grad_hidden, void *grad_weight, int64_t ld_grad_weight, void *ws,
+                          size_t ws_bytes, void *stream);
+/* with_grad != 0: for tt_emb_xent_loss_grad, else for tt_emb_xent_forward
+ * (one size: *least = *bytes).  Either pointer may be NULL. */
+int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t with_grad, size_t *bytes,
+                               size_t *least);
+
+/* One AdamW step (decoupled weight decay) over `count` fp32 tensors:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr mhat / (sqrt(vhat) + eps)
+ * with mhat = m / (1 - beta1^step), vhat = v / (1 - beta2^step), step >= 1.
+ * params, grads, copies, numel are HOST arrays; grads are of grad_dtype;
+ * copies (bf16 tensors that receive the updated values, rounded) may be NULL.
+ * exp_avg (m) and exp_avg_sq (v) are single device buffers in which each
+ * tensor begins at a multiple of 256 elements, in list order
+ * (tt_emb_adamw_state_size gives their length):
+ *   state_bits 32: fp32, the scales are ignored;
+ *   state_bits 8: m in e4m3 and v in e5m2 with one fp32 scale per 256
+ *     elements (the block's largest magnitude times 1/448 or 1/57344).  Values are
+ *     rounded to one of their two neighbours with a probability in proportion
+ *     to the distance, from 16 bits of a hash of (element, seed, step):
+ *     rounding to nearest would stop v, whose steps of (1 - beta2) are far
+ *     below half a spacing.  A v that is not 0 is not stored as 0.  p is
+ *     updated from the values before rounding.  A NaN or infinity in a
+ *     gradient makes its block's moments NaN.
+ * The same arguments give the same bits. */
+int tt_emb_adamw_update(int32_t count, float *const *params, const void *const *grads, int32_t grad_dtype,
+                        void *const *copies, const int64_t *numel, void *exp_avg, void *exp_avg_sq,
+                        float *exp_avg_scale, float *exp_avg_sq_scale, int32_t state_bits, double lr,
+                        double beta1, double beta2, double eps, double weight_decay, int64_t step, uint64_t seed,
+                        void *stream);
+int tt_emb_adamw_state_size(int32_t count, const int64_t *numel, int64_t *elements);
+
 #ifdef __cplusplus
 }
 #endif

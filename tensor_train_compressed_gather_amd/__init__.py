@@ -13,6 +13,9 @@ import math
 import os
 import threading
 
+from . import lm as _lm
+from .lm import LM_EXPORTED, AdamW, LayerNorm, TokenEmbedding, VocabCrossEntropy  # noqa: F401
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # TT_EMB_LIB names another build of the same library (the host-sanitizer build
 # the CPU tests make); there is no fallback either way
@@ -41,7 +44,7 @@ EXPORTED = (
     "tt_emb_backward", "tt_emb_sgd_update", "tt_emb_grouping_view", "tt_emb_poll_error",
     "tt_emb_status_string", "tt_emb_timing_enable", "tt_emb_timing_read", "tt_emb_timer_name",
     "tt_emb_block_stats", "tt_emb_victim_order", "tt_emb_peak_mfma",
-)
+) + LM_EXPORTED
 BLOCK_STAT_KERNELS = ("fwd_r8", "fwd_r16", "fwd_r32", "fwd_r64", "bwd_r8", "bwd_r16", "bwd_r32", "bwd_r64")
 TIMER_NAMES = ("group_sort", "group_rle", "contract", "pool", "bwd_gather", "bwd_contract",
                "bwd_reduce", "sgd", "fwd_r8", "fwd_r16", "fwd_r32", "fwd_r64",
@@ -105,6 +108,7 @@ def lib():
             L.tt_emb_timing_read.argtypes = [p, p, p]
             L.tt_emb_timer_name.argtypes = [i32]
             L.tt_emb_timer_name.restype = C.c_char_p
+            _lm.declare(L)
             for name in EXPORTED:
                 if name not in ("tt_emb_status_string", "tt_emb_timer_name"):
                     getattr(L, name).restype = C.c_int

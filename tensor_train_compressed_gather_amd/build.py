@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtt_emb.so")
-SOURCES = ["api.hip", "group.hip", "forward.hip", "backward.hip", "kcores.hip", "misc.hip", "peak.hip"]
+SOURCES = ["api.hip", "group.hip", "forward.hip", "backward.hip", "kcores.hip", "misc.hip", "peak.hip",
+           "lookup.hip", "norm.hip", "adamw.hip", "xent.hip", "lm_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "-O3", "--offload-arch=gfx950", "-fPIC", "-std=c++17",
@@ -67,15 +68,20 @@ def asan_runtime() -> str:
 
 
 def build_host_sanitized(path: str) -> str:
-    """libtt_emb.so with api.hip's host code under ASan + UBSan, written to path."""
+    """libtt_emb.so with the host code of api.hip and lm_api.hip under ASan +
+    UBSan, written to path."""
     if not all(os.path.exists(os.path.join(BUILD, os.path.splitext(f)[0] + ".o")) for f in SOURCES):
         build(verbose=False)
-    obj = path + ".api.o"
-    cmd = [HIPCC, *FLAGS, "-O1", "-g", *SAN_HOST, "-c", os.path.join(CSRC, "api.hip"), "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc (sanitized api.hip) failed:\n{r.stderr[-4000:]}")
-    objs = [obj] + [os.path.join(BUILD, os.path.splitext(f)[0] + ".o") for f in SOURCES if f != "api.hip"]
+    entry = ("api.hip", "lm_api.hip")
+    objs = []
+    for src in entry:
+        obj = f"{path}.{os.path.splitext(src)[0]}.o"
+        cmd = [HIPCC, *FLAGS, "-O1", "-g", *SAN_HOST, "-c", os.path.join(CSRC, src), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc (sanitized {src}) failed:\n{r.stderr[-4000:]}")
+        objs.append(obj)
+    objs += [os.path.join(BUILD, os.path.splitext(f)[0] + ".o") for f in SOURCES if f not in entry]
     cmd = [HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *SAN_HOST[:4], "-shared-libsan", "-o", path, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

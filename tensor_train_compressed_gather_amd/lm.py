@@ -1,0 +1,510 @@
+"""Operators around the table, from token ids to the update of the weights:
+embedding lookup with its gradient, layer norm, softmax cross entropy over a
+large vocabulary and AdamW (C ABI in ``include/tt_emb.h``).
+
+The classes marshal arguments only: they check what the library cannot see
+from raw pointers, allocate outputs on the stream the work runs on, and keep
+one workspace per stream.  Matrices may be views whose rows are further apart
+than their columns; the last axis has to be contiguous.
+"""
+
+from __future__ import annotations
+
+import ctypes as C
+
+TT_EMB_DTYPE_FLOAT, TT_EMB_DTYPE_BFLOAT, TT_EMB_DTYPE_HALF = 0, 1, 2
+TT_EMB_STATUS_BYTES = 256
+
+LM_EXPORTED = (
+    "tt_emb_poll_status",
+    "tt_emb_lookup_forward", "tt_emb_lookup_backward", "tt_emb_lookup_workspace_size",
+    "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_norm_workspace_size",
+    "tt_emb_xent_forward", "tt_emb_xent_loss_grad", "tt_emb_xent_workspace_size",
+    "tt_emb_adamw_update", "tt_emb_adamw_state_size",
+)
+
+
+def declare(L):
+    """Argument types of this module's entry points on the loaded library."""
+    p, i32, i64, f32, f64, u64, size = (C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_uint64,
+                                        C.c_size_t)
+    sizes = C.POINTER(size)
+    L.tt_emb_poll_status.argtypes = [p, p]
+    L.tt_emb_lookup_forward.argtypes = [p, i64, p, i64, i64, i64, i32, f32, p, i64, p, size, p]
+    L.tt_emb_lookup_backward.argtypes = [p, i64, p, i64, i64, i64, i32, f32, i64, i32, p, i64, p, size, p]
+    L.tt_emb_lookup_workspace_size.argtypes = [i64, i64, i64, sizes]
+    L.tt_emb_norm_forward.argtypes = [p, i64, i64, i64, i32, p, p, i32, f32, p, i64, p, p, p]
+    L.tt_emb_norm_backward.argtypes = [p, i64, p, i64, i64, i64, i32, p, i32, p, p, p, i64, p, p, p, size, p]
+    L.tt_emb_norm_workspace_size.argtypes = [i64, i64, sizes]
+    L.tt_emb_xent_forward.argtypes = [p, i64, p, i64, p, i64, i64, i64, i32, i64, p, p, p, size, p]
+    L.tt_emb_xent_loss_grad.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i32, i64, p, p, p, i64, p, i64, p, size,
+                                        p]
+    L.tt_emb_xent_workspace_size.argtypes = [i64, i64, i64, i32, i32, sizes, sizes]
+    L.tt_emb_adamw_update.argtypes = [i32, p, p, i32, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64, p]
+    L.tt_emb_adamw_state_size.argtypes = [i32, p, C.POINTER(i64)]
+
+
+def _package():
+    from . import TTEmbError, _check, lib
+
+    return TTEmbError, _check, lib()
+
+
+def _bad(where: str, what: str):
+    TTEmbError, _, _ = _package()
+    return TTEmbError(-1, f"{where}: {what}")
+
+
+def _dtype(t, where: str, name: str) -> int:
+    import torch
+
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise _bad(where, f"{name}: dtype {t.dtype}, expected float32, bfloat16 or float16")
+    return code
+
+
+def _matrix(t, where: str, name: str, cols: int, rows: int | None = None, dtype=None, device=None):
+    """Check a [rows][cols] argument and return the distance of its rows."""
+    import torch
+
+    if not torch.is_tensor(t):
+        raise _bad(where, f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise _bad(where, f"{name}: shape {tuple(t.shape)}, expected [{'n' if rows is None else rows}, {cols}]")
+    if dtype is not None and t.dtype != dtype:
+        raise _bad(where, f"{name}: dtype {t.dtype}, expected {dtype}")
+    ld = t.stride(0) if t.shape[0] > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise _bad(where, f"{name}: strides {t.stride()}, expected contiguous rows that do not overlap")
+    _on(t, where, name, device)
+    return ld
+
+
+def _vector(t, where: str, name: str, length: int, dtypes, device=None):
+    import torch
+
+    if not torch.is_tensor(t):
+        raise _bad(where, f"{name}: expected a torch tensor, got {type(t).__name__}")
+    if t.dim() != 1 or t.shape[0] != length:
+        raise _bad(where, f"{name}: shape {tuple(t.shape)}, expected [{length}]")
+    if t.dtype not in dtypes:
+        raise _bad(where, f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if length > 1 and t.stride(0) != 1:
+        raise _bad(where, f"{name}: not contiguous")
+    _on(t, where, name, device)
+
+
+def _on(t, where: str, name: str, device):
+    if t.device.type != "cuda":
+        raise _bad(where, f"{name}: on {t.device}, expected a GPU tensor")
+    if device is not None and t.device != device:
+        raise _bad(where, f"{name}: on {t.device}, expected {device} like the others")
+
+
+class _Streams:
+    """The stream of one call: the device of its tensors made current, outputs
+    allocated on the stream that writes them."""
+
+    def __init__(self, device, stream):
+        import torch
+
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+            self.stream = None
+        else:
+            self.stream = (torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int)
+                           else stream)
+            self.handle = self.stream.cuda_stream
+        self.guard = None
+        if self.stream is not None:
+            self.guard = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            return self.guard.__exit__(*exc)
+        return None
+
+
+class _Operator:
+    """What the operators with a workspace share: one growing buffer per
+    (device, stream), whose status words are zero from the start."""
+
+    def __init__(self, device):
+        import torch
+
+        self.device = torch.device(device)
+        self._ws = {}
+
+    def _workspace(self, device, handle: int, need: int):
+        import torch
+
+        key = (device.index, handle)
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < need:
+            new = torch.empty(need, dtype=torch.uint8, device=device)
+            # the status of earlier calls stays readable
+            if ws is None:
+                new[:TT_EMB_STATUS_BYTES].zero_()
+            else:
+                new[:TT_EMB_STATUS_BYTES].copy_(ws[:TT_EMB_STATUS_BYTES])
+            self._ws[key] = ws = new
+        return ws
+
+    def poll_error(self) -> int:
+        """Synchronises; the first device-detected error of any stream's
+        calls since the last poll (0 = ok), cleared by reading it."""
+        import torch
+
+        _, _, L = _package()
+        rc = 0
+        for (index, handle), ws in self._ws.items():
+            with torch.cuda.device(index):
+                got = int(L.tt_emb_poll_status(ws.data_ptr(), handle))
+            rc = rc or got
+        return rc
+
+
+def _size(fn, where: str, *args) -> int:
+    _, check, _ = _package()
+    out = C.c_size_t()
+    check(fn(*args, C.byref(out)), where)
+    return int(out.value)
+
+
+class TokenEmbedding(_Operator):
+    """Rows of a dense [V][D] table for token ids, times ``scale``.
+
+    forward(weight, tokens) -> [*tokens.shape, D] of the weight's type.
+    backward(grad_out, tokens) -> the gradient of the weight, summed by sorted
+    tokens (bit-reproducible); tokens equal to ``padding_idx`` (negative: none)
+    give none.  With accumulate=True it is added to ``grad_weight``, for a
+    table that the output layer shares."""
+
+    def __init__(self, V: int, D: int, scale: float = 1.0, padding_idx: int = -1, device="cuda"):
+        super().__init__(device)
+        self.V, self.D, self.scale, self.padding_idx = int(V), int(D), float(scale), int(padding_idx)
+        _size(_package()[2].tt_emb_lookup_workspace_size, "TokenEmbedding", 0, self.V, self.D)
+
+    def _tokens(self, tokens, where, device):
+        import torch
+
+        if not torch.is_tensor(tokens) or tokens.dtype != torch.int64:
+            raise _bad(where, "tokens: expected an int64 tensor")
+        if not tokens.is_contiguous():
+            raise _bad(where, "tokens: not contiguous")
+        _on(tokens, where, "tokens", device)
+        return tokens.numel()
+
+    def forward(self, weight, tokens, out=None, stream=None):
+        import torch
+
+        where = "TokenEmbedding.forward"
+        _, check, L = _package()
+        ld_w = _matrix(weight, where, "weight", self.D, self.V)
+        dt = _dtype(weight, where, "weight")
+        device = weight.device
+        n = self._tokens(tokens, where, device)
+        with _Streams(device, stream) as s:
+            shape = None
+            if out is None:
+                out = torch.empty((n, self.D), dtype=weight.dtype, device=device)
+                shape = (*tokens.shape, self.D)
+            ld_o = _matrix(out, where, "out", self.D, n, weight.dtype, device)
+            ws = self._workspace(device, s, TT_EMB_STATUS_BYTES)
+            check(L.tt_emb_lookup_forward(weight.data_ptr(), ld_w, tokens.data_ptr(), n, self.V, self.D, dt,
+                                          self.scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel(), s), where)
+        return out if shape is None or len(shape) == 2 else out.view(shape)
+
+    def backward(self, grad_out, tokens, grad_weight=None, accumulate: bool = False, stream=None):
+        import torch
+
+        where = "TokenEmbedding.backward"
+        _, check, L = _package()
+        if torch.is_tensor(grad_out) and grad_out.dim() > 2:
+            if grad_out.shape[:-1] != tokens.shape:
+                raise _bad(where, f"grad_out: shape {tuple(grad_out.shape)}, tokens {tuple(tokens.shape)}")
+            grad_out = grad_out.view(-1, grad_out.shape[-1])
+        ld_g = _matrix(grad_out, where, "grad_out", self.D)
+        dt = _dtype(grad_out, where, "grad_out")
+        device = grad_out.device
+        n = self._tokens(tokens, where, device)
+        if grad_out.shape[0] != n:
+            raise _bad(where, f"grad_out: {grad_out.shape[0]} rows for {n} tokens")
+        if grad_weight is None and accumulate:
+            raise _bad(where, "accumulate needs grad_weight")
+        need = _size(L.tt_emb_lookup_workspace_size, where, n, self.V, self.D)
+        with _Streams(device, stream) as s:
+            if grad_weight is None:
+                grad_weight = torch.empty((self.V, self.D), dtype=grad_out.dtype, device=device)
+            ld_w = _matrix(grad_weight, where, "grad_weight", self.D, self.V, grad_out.dtype, device)
+            ws = self._workspace(device, s, need)
+            check(L.tt_emb_lookup_backward(grad_out.data_ptr(), ld_g, tokens.data_ptr(), n, self.V, self.D, dt,
+                                           self.scale, self.padding_idx, 1 if accumulate else 0,
+                                           grad_weight.data_ptr(), ld_w, ws.data_ptr(), ws.numel(), s), where)
+        return grad_weight
+
+
+class LayerNorm(_Operator):
+    """Layer norm over rows of D elements.
+
+    forward(x, gamma, beta) -> (y, mean, rstd), y of x's type and the
+    statistics fp32; gamma and beta (x's type or fp32) may be None.
+    backward(grad_y, x, gamma, mean, rstd) -> (grad_x, dgamma, dbeta), the
+    last two of gamma's type (fp32 without gamma)."""
+
+    def __init__(self, D: int, eps: float = 1e-5, device="cuda"):
+        super().__init__(device)
+        self.D, self.eps = int(D), float(eps)
+        _size(_package()[2].tt_emb_norm_workspace_size, "LayerNorm", 0, self.D)
+
+    def _param(self, p, name, where, x):
+        import torch
+
+        if p is not None:
+            _vector(p, where, name, self.D, (torch.float32, x.dtype), x.device)
+
+    def forward(self, x, gamma=None, beta=None, out=None, stream=None):
+        import torch
+
+        where = "LayerNorm.forward"
+        _, check, L = _package()
+        ld_x = _matrix(x, where, "x", self.D)
+        dt = _dtype(x, where, "x")
+        n, device = x.shape[0], x.device
+        self._param(gamma, "gamma", where, x)
+        self._param(beta, "beta", where, x)
+        if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+            raise _bad(where, f"beta: dtype {beta.dtype}, expected {gamma.dtype} like gamma")
+        param = gamma if gamma is not None else beta
+        pdt = 0 if param is None else _dtype(param, where, "gamma")
+        with _Streams(device, stream) as s:
+            if out is None:
+                out = torch.empty((n, self.D), dtype=x.dtype, device=device)
+            ld_y = _matrix(out, where, "out", self.D, n, x.dtype, device)
+            stats = torch.empty((2, n), dtype=torch.float32, device=device)
+            mean, rstd = stats[0], stats[1]
+            check(L.tt_emb_norm_forward(x.data_ptr(), ld_x, n, self.D, dt,
+                                        None if gamma is None else gamma.data_ptr(),
+                                        None if beta is None else beta.data_ptr(), pdt, self.eps, out.data_ptr(),
+                                        ld_y, mean.data_ptr(), rstd.data_ptr(), s), where)
+        return out, mean, rstd
+
+    def backward(self, grad_y, x, gamma, mean, rstd, stream=None):
+        import torch
+
+        where = "LayerNorm.backward"
+        _, check, L = _package()
+        ld_x = _matrix(x, where, "x", self.D)
+        dt = _dtype(x, where, "x")
+        n, device = x.shape[0], x.device
+        ld_g = _matrix(grad_y, where, "grad_y", self.D, n, x.dtype, device)
+        self._param(gamma, "gamma", where, x)
+        pdt = 0 if gamma is None else _dtype(gamma, where, "gamma")
+        _vector(mean, where, "mean", n, (torch.float32,), device)
+        _vector(rstd, where, "rstd", n, (torch.float32,), device)
+        need = _size(L.tt_emb_norm_workspace_size, where, n, self.D)
+        with _Streams(device, stream) as s:
+            dx = torch.empty((n, self.D), dtype=x.dtype, device=device)
+            sums = torch.empty((2, self.D), dtype=torch.float32 if gamma is None else gamma.dtype, device=device)
+            dgamma, dbeta = sums[0], sums[1]
+            ws = self._workspace(device, s, need)
+            check(L.tt_emb_norm_backward(grad_y.data_ptr(), ld_g, x.data_ptr(), ld_x, n, self.D, dt,
+                                         None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(),
+                                         rstd.data_ptr(), dx.data_ptr(), self.D, dgamma.data_ptr(),
+                                         dbeta.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
+        return dx, dgamma, dbeta
+
+
+class VocabCrossEntropy(_Operator):
+    """Softmax cross entropy of hidden rows [n][D] against a vocabulary
+    [V][D] (both fp32 or both bf16) without keeping the logits.
+
+    forward(hidden, weight, targets) -> (loss, lse), fp32 [n]; 0 where the
+    target is ``ignore_index``.
+    loss_and_grad(hidden, weight, targets, grad_loss) -> (loss, lse,
+    grad_hidden, grad_weight) for fp32 grad_loss [n] = dL/dloss.
+    ``max_workspace`` bounds the scratch of loss_and_grad in bytes (smaller
+    pieces of the vocabulary at a time)."""
+
+    def __init__(self, V: int, D: int, ignore_index: int = -100, device="cuda", max_workspace: int | None = None):
+        super().__init__(device)
+        self.V, self.D, self.ignore_index = int(V), int(D), int(ignore_index)
+        self.max_workspace = None if max_workspace is None else int(max_workspace)
+        self._need(0, 0, False, "VocabCrossEntropy")
+
+    def _need(self, n: int, dt: int, grad: bool, where: str) -> int:
+        _, check, L = _package()
+        best, least = C.c_size_t(), C.c_size_t()
+        check(L.tt_emb_xent_workspace_size(n, self.V, self.D, dt, 1 if grad else 0, C.byref(best), C.byref(least)),
+              where)
+        if self.max_workspace is None or not grad:
+            return int(best.value)
+        if self.max_workspace < least.value:
+            raise _package()[0](-3, f"{where}: max_workspace {self.max_workspace}, at least {least.value} needed")
+        return min(int(best.value), self.max_workspace)
+
+    def _inputs(self, hidden, weight, targets, where):
+        import torch
+
+        ld_h = _matrix(hidden, where, "hidden", self.D)
+        dt = _dtype(hidden, where, "hidden")
+        n, device = hidden.shape[0], hidden.device
+        ld_w = _matrix(weight, where, "weight", self.D, self.V, hidden.dtype, device)
+        _vector(targets, where, "targets", n, (torch.int64,), device)
+        return ld_h, ld_w, dt, n, device
+
+    def forward(self, hidden, weight, targets, stream=None):
+        import torch
+
+        where = "VocabCrossEntropy.forward"
+        _, check, L = _package()
+        ld_h, ld_w, dt, n, device = self._inputs(hidden, weight, targets, where)
+        need = self._need(n, dt, False, where)
+        with _Streams(device, stream) as s:
+            rows = torch.empty((2, n), dtype=torch.float32, device=device)
+            ws = self._workspace(device, s, need)
+            check(L.tt_emb_xent_forward(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(), n,
+                                        self.V, self.D, dt, self.ignore_index, rows[0].data_ptr(),
+                                        rows[1].data_ptr(), ws.data_ptr(), ws.numel(), s), where)
+        return rows[0], rows[1]
+
+    def loss_and_grad(self, hidden, weight, targets, grad_loss, grad_weight=None, stream=None):
+        import torch
+
+        where = "VocabCrossEntropy.loss_and_grad"
+        _, check, L = _package()
+        ld_h, ld_w, dt, n, device = self._inputs(hidden, weight, targets, where)
+        _vector(grad_loss, where, "grad_loss", n, (torch.float32,), device)
+        need = self._need(n, dt, True, where)
+        with _Streams(device, stream) as s:
+            rows = torch.empty((2, n), dtype=torch.float32, device=device)
+            dh = torch.empty((n, self.D), dtype=hidden.dtype, device=device)
+            if grad_weight is None:
+                grad_weight = torch.empty((self.V, self.D), dtype=hidden.dtype, device=device)
+            ld_dw = _matrix(grad_weight, where, "grad_weight", self.D, self.V, hidden.dtype, device)
+            ws = self._workspace(device, s, need)
+            check(L.tt_emb_xent_loss_grad(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(),
+                                          grad_loss.data_ptr(), n, self.V, self.D, dt, self.ignore_index,
+                                          rows[0].data_ptr(), rows[1].data_ptr(), dh.data_ptr(), self.D,
+                                          grad_weight.data_ptr(), ld_dw, ws.data_ptr(), ws.numel(), s), where)
+        return rows[0], rows[1], dh, grad_weight
+
+
+class AdamW:
+    """AdamW over a list of fp32 tensors, in one launch per 88 of them.
+
+    ``state_bits`` 32 keeps both moments in fp32; 8 keeps them in e4m3 and
+    e5m2 with one fp32 scale per 256 elements and rounds at random, from
+    ``seed`` and the step's number.  ``copies``: bf16 tensors of the same
+    shapes that receive the updated values.  The state is ``exp_avg``,
+    ``exp_avg_sq`` (flat; each tensor begins at a multiple of 256 elements),
+    ``exp_avg_scale``, ``exp_avg_sq_scale`` and ``steps``."""
+
+    BLOCK = 256
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 state_bits: int = 32, copies=None, seed: int = 0):
+        import torch
+
+        where = "AdamW"
+        self.params = list(params)
+        if not self.params:
+            raise _bad(where, "no parameters")
+        if state_bits not in (8, 32):
+            raise _bad(where, f"state_bits {state_bits}, expected 8 or 32")
+        device = None
+        for i, p in enumerate(self.params):
+            self._tensor(p, f"params[{i}]", torch.float32, None, device)
+            device = p.device
+        self.copies = None if copies is None else list(copies)
+        if self.copies is not None:
+            if len(self.copies) != len(self.params):
+                raise _bad(where, f"{len(self.copies)} copies for {len(self.params)} parameters")
+            for i, (c, p) in enumerate(zip(self.copies, self.params)):
+                self._tensor(c, f"copies[{i}]", torch.bfloat16, p.shape, device)
+        self.lr, self.betas, self.eps, self.weight_decay = float(lr), tuple(betas), float(eps), float(weight_decay)
+        self.state_bits, self.seed, self.steps, self.device = int(state_bits), int(seed), 0, device
+        n = len(self.params)
+        self._numel = (C.c_int64 * n)(*[p.numel() for p in self.params])
+        self._shapes = [p.shape for p in self.params]
+        total = C.c_int64()
+        _, check, L = _package()
+        check(L.tt_emb_adamw_state_size(n, self._numel, C.byref(total)), where)
+        length = int(total.value)
+        kinds = (torch.float32, torch.float32) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+        size = 4 if state_bits == 32 else 1
+        self.exp_avg, self.exp_avg_sq = (torch.zeros(length * size, dtype=torch.uint8, device=device).view(k)
+                                         for k in kinds)
+        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        if state_bits == 8:
+            self.exp_avg_scale = torch.zeros(length // self.BLOCK, dtype=torch.float32, device=device)
+            self.exp_avg_sq_scale = torch.zeros_like(self.exp_avg_scale)
+
+    @staticmethod
+    def _tensor(t, name, dtype, shape, device):
+        import torch
+
+        where = "AdamW"
+        if not torch.is_tensor(t):
+            raise _bad(where, f"{name}: expected a torch tensor, got {type(t).__name__}")
+        if t.dtype != dtype:
+            raise _bad(where, f"{name}: dtype {t.dtype}, expected {dtype}")
+        if shape is not None and t.shape != shape:
+            raise _bad(where, f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise _bad(where, f"{name}: not contiguous")
+        _on(t, where, name, device)
+
+    def load_state(self, exp_avg, exp_avg_sq, steps: int, exp_avg_scale=None, exp_avg_sq_scale=None):
+        """Copies of a saved state: the moments (and scales) as this class
+        keeps them, and the number of steps taken."""
+        for mine, given, name in ((self.exp_avg, exp_avg, "exp_avg"), (self.exp_avg_sq, exp_avg_sq, "exp_avg_sq"),
+                                  (self.exp_avg_scale, exp_avg_scale, "exp_avg_scale"),
+                                  (self.exp_avg_sq_scale, exp_avg_sq_scale, "exp_avg_sq_scale")):
+            if (mine is None) != (given is None) or (mine is not None and (mine.shape != given.shape
+                                                                           or mine.dtype != given.dtype)):
+                raise _bad("AdamW.load_state", f"{name} does not match this state")
+        if int(steps) < 0:
+            raise _bad("AdamW.load_state", "steps is negative")
+        self.exp_avg.copy_(exp_avg)
+        self.exp_avg_sq.copy_(exp_avg_sq)
+        if self.exp_avg_scale is not None:
+            self.exp_avg_scale.copy_(exp_avg_scale)
+            self.exp_avg_sq_scale.copy_(exp_avg_sq_scale)
+        self.steps = int(steps)
+
+    def step(self, grads, lr: float | None = None, stream=None):
+        """One update from gradients shaped like the parameters (all of one
+        type: fp32, bf16 or fp16)."""
+        where = "AdamW.step"
+        _, check, L = _package()
+        grads = list(grads)
+        n = len(self.params)
+        if len(grads) != n:
+            raise _bad(where, f"{len(grads)} gradients for {n} parameters")
+        first = grads[0].dtype
+        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+            if g.dtype is not first or g.shape != shape or not g.is_contiguous() or g.device != self.device:
+                self._tensor(g, f"grads[{i}]", first, shape, self.device)
+        dt = _dtype(grads[0], where, "grads[0]")
+        # parameters may have been replaced (param.data = ...): their addresses are read anew
+        array = C.c_void_p * n
+        params = array(*[p.data_ptr() for p in self.params])
+        pointers = array(*[g.data_ptr() for g in grads])
+        copies = None if self.copies is None else array(*[c.data_ptr() for c in self.copies])
+        with _Streams(self.device, stream) as s:
+            check(L.tt_emb_adamw_update(
+                n, params, pointers, dt, copies, self._numel, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
+                None if self.exp_avg_scale is None else self.exp_avg_scale.data_ptr(),
+                None if self.exp_avg_sq_scale is None else self.exp_avg_sq_scale.data_ptr(), self.state_bits,
+                self.lr if lr is None else float(lr), self.betas[0], self.betas[1], self.eps, self.weight_decay,
+                self.steps + 1, self.seed & 0xFFFFFFFFFFFFFFFF, s), where)
+        self.steps += 1
