@@ -23,10 +23,14 @@ typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTile = 128;    // rows and columns of a product's tile
-constexpr int kTileK = 64;
-constexpr int kPad = 8;       // elements between rows of a tile in LDS
-constexpr int64_t kPiece = 16384; // columns of d at a time, at most
+constexpr int kTileK = 64;             // summed index per stage
+constexpr int kRowPitch = kTileK * 2 + 16; // bytes of a straight tile's row in LDS
+constexpr int kTurnPad = 32;           // bytes past a turned tile's row in LDS
+constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
+constexpr int64_t kPiece = 16384;      // columns of d at a time, at most
+constexpr int kRound = 256;            // rows and columns of d are padded to this
+
+constexpr int kLeast = 128;             // rows and columns of the smallest tile
 
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -53,7 +57,7 @@ struct Output {
     float *sum;               // dH in fp32, [n][D]
     void *out;                // dH or dW
     int64_t ld_out, D;
-    int out_f32, first, last;
+    int first, last;
 };
 
 // x as a sum of PL bf16 values
@@ -67,96 +71,239 @@ __device__ __forceinline__ void split(float x, bf16 (&t)[PL])
     }
 }
 
-// C[m][n] = sum_k X[m][k] Y[n][k] over tiles of 128 x 128; 32x32x16 matrix
-// instructions, two by two tiles per wave.  Lane l of a wave holds column
-// n = l % 32 and the rows m = 8 (r / 4) + 4 (l / 32) + r % 4, so the contiguous
-// output index is m and the row of the output is n.
-template <int PL, bool XT, bool YT, int OUT>
-__global__ __launch_bounds__(256) void k_product(Operand X, Operand Y, int64_t K, Output o)
-{
-    __shared__ bf16 xs[kTile][kTileK + kPad], ys[kTile][kTileK + kPad];
-    __shared__ float red[2][2][kTile];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
-    const int64_t m0 = (int64_t)blockIdx.x * kTile, n0 = (int64_t)blockIdx.y * kTile;
-    f32x16 acc[2][2];
+// How an operand's tile of R outputs and 64 summed values lies in LDS.
+// Straight: R rows of 64 values, 144 bytes apart, so that the 16-byte reads of
+// sixteen lanes (sixteen rows) meet different banks.  Turned: 64 rows of R
+// values, 32 bytes more than R apart, so that the four rows a transposing read
+// touches at a time do.
+template <bool TURNED, int R>
+struct TileLds {
+    static constexpr int pitch = TURNED ? R * 2 + kTurnPad : kRowPitch;
+    static constexpr int bytes = TURNED ? kTileK * pitch : R * pitch;
+    static constexpr int vecs = R * kTileK / 8 / 256; // 16-byte pieces per thread
+};
+
+template <bool TURNED, int R>
+struct TileLoader {
+    static constexpr int N = TileLds<TURNED, R>::vecs;
+    const bf16 *p;   // plane 0, moved to the tile's first row (straight) or column (turned)
+    int64_t ld, plane, rows;
+    int off[N];      // straight: element offsets of this thread's pieces
+    int k, col;      // turned: first row of the thread's pieces in a stage, column
+    bf16x8 v[N];
+
+    __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0)
+    {
+        const int tid = threadIdx.x;
+        ld = a.ld;
+        plane = a.plane;
+        rows = a.rows;
+        if constexpr (!TURNED) {
+            p = a.p + r0 * a.ld;
+            k = (tid & 7) * 8;
+            const int64_t last = a.rows - 1 - r0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    auto stage = [&](const Operand &a, bool turned, int plane, int64_t r0, int64_t k0, bf16 (*dst)[kTileK + kPad]) {
-        const bf16 *p = a.p + plane * a.plane;
-        if (!turned) {
-#pragma unroll
-            for (int i = 0; i < kTile * kTileK / 8 / 256; ++i) {
-                const int c = tid + i * 256, r = c / (kTileK / 8), k = (c % (kTileK / 8)) * 8;
-                const int64_t row = r0 + r < a.rows ? r0 + r : a.rows - 1;
-                *reinterpret_cast<bf16x8 *>(&dst[r][k]) = *reinterpret_cast<const bf16x8 *>(p + row * a.ld + k0 + k);
+            for (int i = 0; i < N; ++i) {
+                const int64_t r = tid / 8 + i * 32;
+                off[i] = (int)((r < last ? r : last) * a.ld) + k;
             }
         } else {
-#pragma unroll
-            for (int i = 0; i < kTile * kTileK / 8 / 256; ++i) {
-                const int c = tid + i * 256, k = c / (kTile / 8), r = (c % (kTile / 8)) * 8;
-                const int64_t row = k0 + k < a.rows ? k0 + k : a.rows - 1;
-                const int64_t col = r0 + r < a.cols - 8 ? r0 + r : a.cols - 8;
-                const bf16x8 v = *reinterpret_cast<const bf16x8 *>(p + row * a.ld + col);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dst[r + j][k] = v[j];
-            }
+            p = a.p + r0;
+            k = tid / (R / 8);
+            col = (tid % (R / 8)) * 8;
+            const int64_t last = a.cols - 8 - r0;
+            if (col > last) col = (int)last;
         }
-    };
-    // products of terms, the small ones first
-    constexpr int SEG = PL == 1 ? 1 : 6;
-    constexpr int sx[6] = {2, 0, 1, 1, 0, 0}, sy[6] = {0, 2, 1, 0, 1, 0};
-    for (int g = 0; g < SEG; ++g) {
-        const int px = PL == 1 ? 0 : sx[g], py = PL == 1 ? 0 : sy[g];
-        for (int64_t k0 = 0; k0 < K; k0 += kTileK) {
-            __syncthreads();
-            stage(X, XT, px, m0, k0, xs);
-            stage(Y, YT, py, n0, k0, ys);
-            __syncthreads();
+    }
+    __device__ __forceinline__ void load(int pl, int64_t k0)
+    {
+        if constexpr (!TURNED) {
+            const bf16 *q = p + pl * plane + k0;
 #pragma unroll
-            for (int k = 0; k < kTileK; k += 16) {
-                bf16x8 a[2], b[2];
+            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const bf16x8 *>(q + off[i]);
+        } else {
+            const bf16 *q = p + pl * plane + k0 * ld;
+            const int last = (int)(rows - 1 - k0 < kTileK ? rows - 1 - k0 : kTileK);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    a[i] = *reinterpret_cast<const bf16x8 *>(&xs[wm * 64 + i * 32 + (lane & 31)][k + (lane >> 5) * 8]);
-                    b[i] = *reinterpret_cast<const bf16x8 *>(&ys[wn * 64 + i * 32 + (lane & 31)][k + (lane >> 5) * 8]);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+            for (int i = 0; i < N; ++i) {
+                const int r = k + i * (256 / (R / 8));
+                v[i] = *reinterpret_cast<const bf16x8 *>(q + (int64_t)(r < last ? r : last) * ld + col);
             }
         }
     }
-    auto row_of = [&](int i, int r) { return wm * 64 + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + (r % 4); };
-    if constexpr (OUT == OUT_STATS) {
+    __device__ __forceinline__ void store(char *lds) const
+    {
+        const int tid = threadIdx.x;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int nl = wn * 64 + j * 32 + (lane & 31);
+        for (int i = 0; i < N; ++i) {
+            int at;
+            if constexpr (!TURNED) at = (tid / 8 + i * 32) * kRowPitch + (tid & 7) * 16;
+            else at = (tid / (R / 8) + i * (256 / (R / 8))) * TileLds<TURNED, R>::pitch + (tid % (R / 8)) * 16;
+            *reinterpret_cast<bf16x8 *>(lds + at) = v[i];
+        }
+    }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Fragments of N 32-row blocks from row `r0` of a tile, summed values
+// [ks * 16, ks * 16 + 16): lane l gets row l % 32, values 8 (l / 32) .. + 7.
+// A transposing read gives each of sixteen lanes one column of the four rows
+// that the sixteen lanes' 8-byte addresses name.
+template <bool TURNED, int R, int N>
+__device__ __forceinline__ void fragments(const char *lds, int r0, int ks, bf16x8 (&f)[N])
+{
+    const int l = threadIdx.x & 63;
+    if constexpr (!TURNED) {
+        const char *q = lds + (r0 + (l & 31)) * kRowPitch + ks * 32 + (l >> 5) * 16;
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = *reinterpret_cast<const bf16x8 *>(q + i * 32 * kRowPitch);
+    } else {
+        constexpr int P = TileLds<TURNED, R>::pitch;
+        const char *q = lds + (ks * 16 + (l >> 5) * 8 + ((l & 15) >> 2)) * P +
+                        (r0 + ((l >> 4) & 1) * 16 + (l & 3) * 4) * 2;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(q + i * 64));
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(q + i * 64 + 4 * P));
+            f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+}
+
+// Tile of a thread block: consecutive blocks go to the eight XCDs in turn, so
+// each XCD takes patches of kPatchM x kPatchN tiles (its 32 compute units) whose
+// operands meet in its L2, and the patches that run at the same time lie along
+// n, where they share the X operand in the memory-side cache.
+__device__ __forceinline__ bool tile_of(int64_t mt, int64_t nt, int64_t &m, int64_t &n)
+{
+    constexpr int P = kPatchM * kPatchN;
+    const int64_t b = blockIdx.x, local = b >> 3;
+    const int64_t patch = local / P * 8 + (b & 7), in = local % P;
+    const int64_t pn = (nt + kPatchN - 1) / kPatchN;
+    m = patch / pn * kPatchM + in % kPatchM;
+    n = patch % pn * kPatchN + in / kPatchM;
+    return m < mt && n < nt;
+}
+inline unsigned tile_grid(int64_t mt, int64_t nt)
+{
+    const int64_t patches = ((mt + kPatchM - 1) / kPatchM) * ((nt + kPatchN - 1) / kPatchN);
+    return (unsigned)(up(patches, 8) * kPatchM * kPatchN);
+}
+
+// C[m][n] = sum_k X[m][k] Y[n][k] over tiles of (64 NI) x (64 NJ); four waves,
+// 32x32x16 matrix instructions, NI x NJ of them per wave.  Lane l of a wave
+// holds column n = l % 32 and the rows m = 8 (r / 4) + 4 (l / 32) + r % 4 of
+// each, so the contiguous output index is m and the row of the output is n.
+//
+// Tiles go from memory to registers a stage ahead and from there to one of two
+// LDS buffers, and fragments are read one step of 16 ahead of the matrix
+// instructions that use them; the one barrier per stage stands before its last
+// step, whose fragments are in registers by then.
+template <int PL, bool XT, bool YT, int OUT, int NI, int NJ>
+__global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_t K, int64_t mt, int64_t nt, Output o)
+{
+    constexpr int TM = 64 * NI, TN = 64 * NJ;
+    constexpr int XB = TileLds<XT, TM>::bytes, YB = TileLds<YT, TN>::bytes, STAGE = XB + YB;
+    __shared__ __align__(16) char lds[2 * STAGE];
+    int64_t mi, ni;
+    if (!tile_of(mt, nt, mi, ni)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
+    const int64_t m0 = mi * TM, n0 = ni * TN;
+    f32x16 acc[NI][NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    {
+        TileLoader<XT, TM> x(X, m0);
+        TileLoader<YT, TN> y(Y, n0);
+        // products of terms, the small ones first
+        constexpr int SEG = PL == 1 ? 1 : 6;
+        const int per = (int)(K / kTileK), stages = SEG * per;
+        int seg = 0, in = 0; // of the next stage to load
+        auto load = [&]() {
+            // planes (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), two bits each
+            const int px = PL == 1 ? 0 : (0x052 >> (2 * seg)) & 3, py = PL == 1 ? 0 : (0x118 >> (2 * seg)) & 3;
+            x.load(px, (int64_t)in * kTileK);
+            y.load(py, (int64_t)in * kTileK);
+            if (++in == per) {
+                in = 0;
+                ++seg;
+            }
+        };
+        auto mma = [&](const bf16x8 (&a)[NI], const bf16x8 (&b)[NJ]) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        };
+        load();
+        x.store(lds);
+        y.store(lds + XB);
+        if (stages > 1) load();
+        __syncthreads();
+        bf16x8 a0[NI], b0[NJ], a1[NI], b1[NJ];
+        const int rx = wm * (TM / 2), ry = wn * (TN / 2);
+        fragments<XT, TM>(lds, rx, 0, a0);
+        fragments<YT, TN>(lds + XB, ry, 0, b0);
+        int cur = 0;
+        for (int t = 0; t < stages; ++t) {
+            const char *here = lds + cur;
+            char *next = lds + (STAGE - cur);
+            fragments<XT, TM>(here, rx, 1, a1);
+            fragments<YT, TN>(here + XB, ry, 1, b1);
+            mma(a0, b0);
+            if (t + 1 < stages) {
+                x.store(next);
+                y.store(next + XB);
+            }
+            fragments<XT, TM>(here, rx, 2, a0);
+            fragments<YT, TN>(here + XB, ry, 2, b0);
+            if (t + 2 < stages) load();
+            mma(a1, b1);
+            fragments<XT, TM>(here, rx, 3, a1);
+            fragments<YT, TN>(here + XB, ry, 3, b1);
+            mma(a0, b0);
+            __syncthreads();
+            if (t + 1 < stages) {
+                fragments<XT, TM>(next, rx, 0, a0);
+                fragments<YT, TN>(next + XB, ry, 0, b0);
+            }
+            mma(a1, b1);
+            cur = STAGE - cur;
+        }
+    }
+    auto row_of = [&](int i, int r) { return wm * (TM / 2) + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + (r % 4); };
+    if constexpr (OUT == OUT_STATS) {
+        float(*red)[2][TN] = reinterpret_cast<float(*)[2][TN]>(lds);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int nl = wn * (TN / 2) + j * 32 + (lane & 31);
             const int64_t i = n0 + nl;
-            const int64_t t = i < o.n ? o.targets[i] : -1;
+            const int64_t t = i < o.n ? o.targets[i] - m0 : -1;
+            const int64_t left = o.V - m0;
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int a = 0; a < NI; ++a)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int64_t v = m0 + row_of(a, r);
-                    if (v < o.V) {
-                        top = fmaxf(top, acc[a][j][r]);
-                        if (v == t) o.target_logit[i] = acc[a][j][r];
-                    }
+                    const int v = row_of(a, r);
+                    if (v >= left) acc[a][j][r] = -INFINITY;
+                    top = fmaxf(top, acc[a][j][r]);
+                    if (v == t) o.target_logit[i] = acc[a][j][r];
                 }
             top = fmaxf(top, __shfl_xor(top, 32, 64));
             const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int a = 0; a < NI; ++a)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (m0 + row_of(a, r) < o.V) sum += __expf(acc[a][j][r] - ref);
+                for (int r = 0; r < 16; ++r) sum += __expf(acc[a][j][r] - ref);
             sum += __shfl_xor(sum, 32, 64);
             if (lane < 32) {
                 red[0][wm][nl] = top;
@@ -164,28 +311,29 @@ __global__ __launch_bounds__(256) void k_product(Operand X, Operand Y, int64_t K
             }
         }
         __syncthreads();
-        if (tid < kTile && n0 + tid < o.n) {
+        if (tid < TN && n0 + tid < o.n) {
             const float a = red[0][0][tid], b = red[0][1][tid], top = fmaxf(a, b);
             const float ref = top == -INFINITY ? 0.f : top;
             const float s = red[1][0][tid] * __expf(a - ref) + red[1][1][tid] * __expf(b - ref);
-            o.part[(int64_t)blockIdx.x * o.n + n0 + tid] = make_float2(top, s);
+            o.part[mi * o.n + n0 + tid] = make_float2(top, s);
         }
     } else {
+        const float scale = *o.top_grad;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t i = n0 + wn * 64 + j * 32 + (lane & 31);
+        for (int j = 0; j < NJ; ++j) {
+            const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
             float lse = 0.f, g = 0.f;
             int64_t t = -1;
             if constexpr (OUT == OUT_D) {
                 if (i < o.n) {
                     t = o.targets[i] - o.v0;
                     const bool counts = o.targets[i] != o.ignore && o.targets[i] >= 0 && o.targets[i] < o.V;
-                    g = counts ? o.grad[i] / *o.top_grad : 0.f;
+                    g = counts ? o.grad[i] / scale : 0.f;
                     lse = o.lse[i];
                 }
             }
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+            for (int a = 0; a < NI; ++a)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int64_t m = m0 + row_of(a, 4 * q);
@@ -206,29 +354,31 @@ __global__ __launch_bounds__(256) void k_product(Operand X, Operand Y, int64_t K
 #pragma unroll
                         for (int q2 = 0; q2 < PL; ++q2)
                             *reinterpret_cast<bf16x4 *>(o.d + q2 * o.plane_d + i * o.ldd + m) = w[q2];
-                    } else if constexpr (OUT == OUT_HIDDEN) {
-                        if (i >= o.n) continue;
-                        const float scale = *o.top_grad;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if (m + r >= o.D) continue;
-                            float *s = o.sum + i * o.D + m + r;
-                            float v = o.first ? x[r] : *s + x[r];
-                            if (o.last) v *= scale;
-                            if (!o.last) *s = v;
-                            else if (o.out_f32) static_cast<float *>(o.out)[i * o.ld_out + m + r] = v;
-                            else static_cast<bf16 *>(o.out)[i * o.ld_out + m + r] = (bf16)v;
-                        }
                     } else {
-                        if (o.v0 + i >= o.V) continue;
-                        const float scale = *o.top_grad;
+                        const int left = (int)(o.D - m < 4 ? o.D - m : 4);
+                        if (left <= 0) continue;
+                        int64_t row = i;
+                        if constexpr (OUT == OUT_HIDDEN) {
+                            if (i >= o.n) continue;
+                            float *s = o.sum + i * o.D + m;
+                            if (!o.first) {
+                                float old[4];
+                                load_part<float, 4>(s, left, old);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if (m + r >= o.D) continue;
-                            const int64_t at = (o.v0 + i) * o.ld_out + m + r;
-                            if (o.out_f32) static_cast<float *>(o.out)[at] = x[r] * scale;
-                            else static_cast<bf16 *>(o.out)[at] = (bf16)(x[r] * scale);
+                                for (int r = 0; r < 4; ++r) x[r] += old[r];
+                            }
+                            if (!o.last) {
+                                store_part<float, 4>(s, left, x);
+                                continue;
+                            }
+                        } else {
+                            row = o.v0 + i;
+                            if (row >= o.V) continue;
                         }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[r] *= scale;
+                        if (PL > 1) store_part<float, 4>(static_cast<float *>(o.out) + row * o.ld_out + m, left, x);
+                        else store_part<bf16, 4>(static_cast<bf16 *>(o.out) + row * o.ld_out + m, left, x);
                     }
                 }
         }
@@ -348,11 +498,11 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     };
     XentPlan p{};
     p.Kp = up(D, kTileK);
-    p.nr = up(n, kTile);
+    p.nr = up(n, kRound);
     p.piece = piece;
     p.target_logit = (float *)take(4 * n);
     p.top_grad = (float *)take(4);
-    p.part = (float2 *)take(8 * (size_t)n * ((V + kTile - 1) / kTile));
+    p.part = (float2 *)take(8 * (size_t)n * ((V + kLeast - 1) / kLeast));
     p.h = (bf16 *)take((size_t)PL * n * p.Kp * 2);
     p.w = (bf16 *)take((size_t)PL * V * p.Kp * 2);
     if (piece) {
@@ -363,7 +513,7 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     return p;
 }
 
-int64_t best_piece(int64_t V) { return up(V < kPiece ? V : kPiece, kTile); }
+int64_t best_piece(int64_t V) { return up(V < kPiece ? V : kPiece, kRound); }
 
 template <class T, int PL>
 Operand operand(const T *src, int64_t ld, int64_t rows, int64_t D, bf16 *room, int64_t Kp, hipStream_t s)
@@ -379,16 +529,33 @@ Operand operand(const T *src, int64_t ld, int64_t rows, int64_t D, bf16 *room, i
     return Operand{room, Kp, rows * Kp, rows, Kp};
 }
 
+// A product with M contiguous outputs in each of N rows; returns the tiles
+// along M.  256 x 256 tiles read each operand least often; where they would
+// leave compute units idle, 128 x 128 ones spread the work further.
+template <int PL, bool XT, bool YT, int OUT>
+int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s)
+{
+    const int64_t mt = (M + 255) / 256, nt = (N + 255) / 256;
+    if (mt * nt >= kCUs) {
+        hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, 4, 4>), dim3(tile_grid(mt, nt)), dim3(256), 0, s, x, y, K, mt,
+                           nt, o);
+        return mt;
+    }
+    const int64_t ms = (M + 127) / 128, ns = (N + 127) / 128;
+    hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, 2, 2>), dim3(tile_grid(ms, ns)), dim3(256), 0, s, x, y, K, ms, ns,
+                       o);
+    return ms;
+}
+
 template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
     int64_t piece = grad ? best_piece(a.V) : 0;
-    while (piece > kTile && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
-        piece = up(piece / 2, kTile);
+    while (piece > kRound && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
+        piece = up(piece / 2, kRound);
     const XentPlan p = plan_xent(a.n, a.V, a.D, PL, piece, a.ws);
     const Operand h = operand<T, PL>(static_cast<const T *>(a.hidden), a.ld_h, a.n, a.D, p.h, p.Kp, s);
     const Operand w = operand<T, PL>(static_cast<const T *>(a.weight), a.ld_w, a.V, a.D, p.w, p.Kp, s);
-    const unsigned nt = (unsigned)(p.nr / kTile);
     Output o{};
     o.n = a.n;
     o.V = a.V;
@@ -404,34 +571,29 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.ldd = piece;
     o.plane_d = p.nr * piece;
     o.sum = p.sum;
-    o.out_f32 = sizeof(T) == 4;
-    const int64_t tiles = (a.V + kTile - 1) / kTile;
-    hipLaunchKernelGGL((k_product<PL, false, false, OUT_STATS>), dim3((unsigned)tiles, nt), dim3(256), 0, s, w, h,
-                       p.Kp, o);
+    const int64_t tiles = product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, p.part, tiles, a.n, a.V,
                        a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
     if (!grad) return hipGetLastError();
     hipLaunchKernelGGL(k_xent_top_grad, dim3(1), dim3(1024), 0, s, a.grad_loss, a.targets, a.ignore, a.n, a.V,
                        p.top_grad);
-    const unsigned dt = (unsigned)((a.D + kTile - 1) / kTile);
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
-        const int64_t here = a.V - v0 < piece ? a.V - v0 : piece, cols = up(here, kTile);
+        const int64_t here = a.V - v0 < piece ? a.V - v0 : piece, cols = up(here, kRound);
         Operand wp = w;
         wp.p += v0 * w.ld;
         wp.rows = here;
         o.v0 = v0;
         o.first = v0 == 0;
         o.last = v0 + piece >= a.V;
-        hipLaunchKernelGGL((k_product<PL, false, false, OUT_D>), dim3((unsigned)(cols / kTile), nt), dim3(256), 0, s,
-                           wp, h, p.Kp, o);
+        // d of whole 256 x 256 blocks: what lies past the rows and the vocabulary is written as zeros
+        product<PL, false, false, OUT_D>(wp, h, cols, p.nr, p.Kp, o, s);
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
         o.out = a.dh;
         o.ld_out = a.ld_dh;
-        hipLaunchKernelGGL((k_product<PL, true, false, OUT_HIDDEN>), dim3(dt, nt), dim3(256), 0, s, wp, d, cols, o);
+        product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s);
         o.out = a.dw;
         o.ld_out = a.ld_dw;
-        hipLaunchKernelGGL((k_product<PL, true, true, OUT_WEIGHT>), dim3(dt, (unsigned)(cols / kTile)), dim3(256), 0,
-                           s, h, d, p.nr, o);
+        product<PL, true, true, OUT_WEIGHT>(h, d, a.D, here, p.nr, o, s);
     }
     return hipGetLastError();
 }
@@ -442,7 +604,7 @@ void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_
 {
     const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 3 : 1;
     if (best) *best = plan_xent(n, V, D, PL, grad ? best_piece(V) : 0, nullptr).bytes;
-    if (least) *least = plan_xent(n, V, D, PL, grad ? kTile : 0, nullptr).bytes;
+    if (least) *least = plan_xent(n, V, D, PL, grad ? kRound : 0, nullptr).bytes;
 }
 
 hipError_t launch_xent_forward(const XentArgs &a, int dtype, hipStream_t s)
