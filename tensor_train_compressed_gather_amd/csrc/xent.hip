@@ -21,13 +21,15 @@ namespace {
 
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTileK = 64;             // summed index per stage
 constexpr int kRowPitch = kTileK * 2 + 16; // bytes of a straight tile's row in LDS
 constexpr int kTurnPad = 32;           // bytes past a turned tile's row in LDS
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
-constexpr int64_t kPiece = 16384;      // columns of d at a time, at most
+constexpr size_t kPieceBytes = (size_t)256 << 20; // d of one piece of the vocabulary, at most
+constexpr int kSplitK = 1024;          // least summed values of a split of dH
 constexpr int kRound = 256;            // rows and columns of d are padded to this
 
 constexpr int kLeast = 128;             // rows and columns of the smallest tile
@@ -54,10 +56,11 @@ struct Output {
     const float *top_grad;    // the largest |grad| of a row that counts
     bf16 *d;                  // [planes][rows][ldd]
     int64_t ldd, plane_d;
-    float *sum;               // dH in fp32, [n][D]
-    void *out;                // dH or dW
+    float *sum;               // dH in fp32, [splits][n][D]
+    int64_t split_k;          // summed values per split of dH
+    void *out;                // dW
     int64_t ld_out, D;
-    int first, last;
+    int first;                // dH's first piece
 };
 
 // x as a sum of PL bf16 values
@@ -83,64 +86,46 @@ struct TileLds {
     static constexpr int vecs = R * kTileK / 8 / 256; // 16-byte pieces per thread
 };
 
+// One operand's way from memory to registers to LDS.  Loads go through a
+// buffer descriptor that ends with the matrix, so rows past it (of the outputs
+// or of the summed index) read as zeros and no address needs a clamp.
 template <bool TURNED, int R>
 struct TileLoader {
     static constexpr int N = TileLds<TURNED, R>::vecs;
-    const bf16 *p;   // plane 0, moved to the tile's first row (straight) or column (turned)
-    int64_t ld, plane, rows;
-    int off[N];      // straight: element offsets of this thread's pieces
-    int k, col;      // turned: first row of the thread's pieces in a stage, column
-    bf16x8 v[N];
+    static constexpr int ROWV = TURNED ? R / 8 : kTileK / 8; // pieces in a tile's row
+    const bf16 *p;  // plane 0, moved to the tile's first row (straight) or column (turned)
+    int64_t ld, plane, end; // end: elements from p to the end of plane 0
+    int off;        // byte offset of this thread's first piece; the others are 256 / ROWV rows apart
+    int step;
+    u32x4 v[N];
 
     __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0)
     {
-        const int tid = threadIdx.x;
         ld = a.ld;
         plane = a.plane;
-        rows = a.rows;
-        if constexpr (!TURNED) {
-            p = a.p + r0 * a.ld;
-            k = (tid & 7) * 8;
-            const int64_t last = a.rows - 1 - r0;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int64_t r = tid / 8 + i * 32;
-                off[i] = (int)((r < last ? r : last) * a.ld) + k;
-            }
-        } else {
-            p = a.p + r0;
-            k = tid / (R / 8);
-            col = (tid % (R / 8)) * 8;
-            const int64_t last = a.cols - 8 - r0;
-            if (col > last) col = (int)last;
-        }
+        p = a.p + (TURNED ? r0 : r0 * a.ld);
+        end = (a.rows - 1) * a.ld + a.cols - (TURNED ? r0 : r0 * a.ld);
+        const int t = threadIdx.x;
+        off = ((t / ROWV) * (int)ld + (t % ROWV) * 8) * 2;
+        step = 256 / ROWV * (int)ld * 2;
     }
     __device__ __forceinline__ void load(int pl, int64_t k0)
     {
-        if constexpr (!TURNED) {
-            const bf16 *q = p + pl * plane + k0;
+        const int64_t skip = TURNED ? k0 * ld : k0;
+        const int64_t left = (end - skip) * 2;
+        const unsigned bytes = left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<bf16 *>(p + pl * plane + skip), 0, bytes, 0x00027000);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = *reinterpret_cast<const bf16x8 *>(q + off[i]);
-        } else {
-            const bf16 *q = p + pl * plane + k0 * ld;
-            const int last = (int)(rows - 1 - k0 < kTileK ? rows - 1 - k0 : kTileK);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int r = k + i * (256 / (R / 8));
-                v[i] = *reinterpret_cast<const bf16x8 *>(q + (int64_t)(r < last ? r : last) * ld + col);
-            }
-        }
+        for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, off, i * step, 0);
     }
     __device__ __forceinline__ void store(char *lds) const
     {
-        const int tid = threadIdx.x;
+        const int t = threadIdx.x;
+        constexpr int P = TileLds<TURNED, R>::pitch;
+        char *q = lds + (t / ROWV) * P + (t % ROWV) * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            int at;
-            if constexpr (!TURNED) at = (tid / 8 + i * 32) * kRowPitch + (tid & 7) * 16;
-            else at = (tid / (R / 8) + i * (256 / (R / 8))) * TileLds<TURNED, R>::pitch + (tid % (R / 8)) * 16;
-            *reinterpret_cast<bf16x8 *>(lds + at) = v[i];
-        }
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(q + i * (256 / ROWV) * P) = v[i];
     }
 };
 
@@ -192,6 +177,24 @@ inline unsigned tile_grid(int64_t mt, int64_t nt)
     return (unsigned)(up(patches, 8) * kPatchM * kPatchN);
 }
 
+// Order of a step's instructions: after each matrix instruction the A and B
+// others that fall to it, so that neither the matrix core nor LDS waits for
+// the other's whole batch.
+constexpr int kMfma = 0x008, kVmRead = 0x020, kDsRead = 0x100, kDsWrite = 0x200;
+template <int M, int A, int MA, int B, int MB>
+__device__ __forceinline__ void interleave()
+{
+    constexpr int per_a = (A + M - 1) / M, every_a = A >= M || A == 0 ? 1 : M / A;
+    constexpr int per_b = B ? (B + M - 1) / M : 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        if (i % every_a == 0) __builtin_amdgcn_sched_group_barrier(MA, per_a, 0);
+        if constexpr (B > 0) __builtin_amdgcn_sched_group_barrier(MB, per_b, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // C[m][n] = sum_k X[m][k] Y[n][k] over tiles of (64 NI) x (64 NJ); four waves,
 // 32x32x16 matrix instructions, NI x NJ of them per wave.  Lane l of a wave
 // holds column n = l % 32 and the rows m = 8 (r / 4) + 4 (l / 32) + r % 4 of
@@ -209,6 +212,15 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
     __shared__ __align__(16) char lds[2 * STAGE];
     int64_t mi, ni;
     if (!tile_of(mt, nt, mi, ni)) return;
+    if constexpr (OUT == OUT_HIDDEN) { // this split's part of the sum
+        const int64_t k0 = blockIdx.y * o.split_k;
+        if (k0 >= K) return;
+        X.p += k0 * X.ld;
+        X.rows -= k0;
+        Y.p += k0;
+        K = K - k0 < o.split_k ? K - k0 : o.split_k;
+        o.sum += blockIdx.y * o.n * o.D;
+    }
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
     const int64_t m0 = mi * TM, n0 = ni * TN;
     f32x16 acc[NI][NJ];
@@ -224,16 +236,15 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         // products of terms, the small ones first
         constexpr int SEG = PL == 1 ? 1 : 6;
         const int per = (int)(K / kTileK), stages = SEG * per;
-        int seg = 0, in = 0; // of the next stage to load
+        int seg = 0, in = 0; // of the next stage to load; the last one is loaded again past the end
         auto load = [&]() {
             // planes (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), two bits each
             const int px = PL == 1 ? 0 : (0x052 >> (2 * seg)) & 3, py = PL == 1 ? 0 : (0x118 >> (2 * seg)) & 3;
             x.load(px, (int64_t)in * kTileK);
             y.load(py, (int64_t)in * kTileK);
-            if (++in == per) {
-                in = 0;
-                ++seg;
-            }
+            const bool over = in + 1 == per, more = !over || seg + 1 < SEG;
+            seg += over && more;
+            in = over ? (more ? 0 : in) : in + 1;
         };
         auto mma = [&](const bf16x8 (&a)[NI], const bf16x8 (&b)[NJ]) {
 #pragma unroll
@@ -245,12 +256,14 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         load();
         x.store(lds);
         y.store(lds + XB);
-        if (stages > 1) load();
+        load();
         __syncthreads();
         bf16x8 a0[NI], b0[NJ], a1[NI], b1[NJ];
         const int rx = wm * (TM / 2), ry = wn * (TN / 2);
         fragments<XT, TM>(lds, rx, 0, a0);
         fragments<YT, TN>(lds + XB, ry, 0, b0);
+        // reads of a step's fragments, pieces moved and matrix instructions of a step
+        constexpr int RD = NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1), MV = (TM + TN) / 32, MM = NI * NJ;
         int cur = 0;
         for (int t = 0; t < stages; ++t) {
             const char *here = lds + cur;
@@ -258,23 +271,24 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             fragments<XT, TM>(here, rx, 1, a1);
             fragments<YT, TN>(here + XB, ry, 1, b1);
             mma(a0, b0);
-            if (t + 1 < stages) {
-                x.store(next);
-                y.store(next + XB);
-            }
+            interleave<MM, RD, kDsRead, 0, 0>();
             fragments<XT, TM>(here, rx, 2, a0);
             fragments<YT, TN>(here + XB, ry, 2, b0);
-            if (t + 2 < stages) load();
+            x.store(next);
+            y.store(next + XB);
             mma(a1, b1);
+            interleave<MM, RD, kDsRead, MV, kDsWrite>();
             fragments<XT, TM>(here, rx, 3, a1);
             fragments<YT, TN>(here + XB, ry, 3, b1);
+            load();
             mma(a0, b0);
+            interleave<MM, RD, kDsRead, MV, kVmRead>();
             __syncthreads();
-            if (t + 1 < stages) {
-                fragments<XT, TM>(next, rx, 0, a0);
-                fragments<YT, TN>(next + XB, ry, 0, b0);
-            }
+            __builtin_amdgcn_sched_barrier(0); // the last step's products stay behind the barrier
+            fragments<XT, TM>(next, rx, 0, a0);
+            fragments<YT, TN>(next + XB, ry, 0, b0);
             mma(a1, b1);
+            interleave<MM, RD, kDsRead, 0, 0>();
             cur = STAGE - cur;
         }
     }
@@ -357,7 +371,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                     } else {
                         const int left = (int)(o.D - m < 4 ? o.D - m : 4);
                         if (left <= 0) continue;
-                        int64_t row = i;
+                        const int64_t row = o.v0 + i;
                         if constexpr (OUT == OUT_HIDDEN) {
                             if (i >= o.n) continue;
                             float *s = o.sum + i * o.D + m;
@@ -367,14 +381,10 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) x[r] += old[r];
                             }
-                            if (!o.last) {
-                                store_part<float, 4>(s, left, x);
-                                continue;
-                            }
-                        } else {
-                            row = o.v0 + i;
-                            if (row >= o.V) continue;
+                            store_part<float, 4>(s, left, x);
+                            continue;
                         }
+                        if (row >= o.V) continue;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) x[r] *= scale;
                         if (PL > 1) store_part<float, 4>(static_cast<float *>(o.out) + row * o.ld_out + m, left, x);
@@ -382,6 +392,29 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                     }
                 }
         }
+    }
+}
+
+// dH from the splits' sums, in order, in units of the loss.
+template <class T>
+__global__ __launch_bounds__(256) void k_xent_hidden(const float *sum, int splits, int64_t n, int64_t D,
+                                                     const float *top_grad, T *out, int64_t ld)
+{
+    const int64_t chunks = (D + 3) / 4, step = (int64_t)gridDim.x * 256;
+    const float scale = *top_grad;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < n * chunks; c += step) {
+        const int64_t i = c / chunks, k = (c - i * chunks) * 4;
+        const int left = (int)(D - k < 4 ? D - k : 4);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < splits; ++q) {
+            float y[4];
+            load_part<float, 4>(sum + ((int64_t)q * n + i) * D + k, left, y);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] += y[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] *= scale;
+        store_part<T, 4>(out + i * ld + k, left, x);
     }
 }
 
@@ -482,8 +515,22 @@ struct XentPlan {
     float *sum;
     bf16 *d;
     int64_t Kp, nr, piece;
+    int splits;
     size_t bytes;
 };
+
+// Rows and columns of a product's tile, and how often dH's sum over a piece of
+// the vocabulary is split: its output is small (n x D) beside what it adds up,
+// so where its tiles are fewer than the compute units the sum is shared out.
+inline int64_t tile_side(int64_t size) { return size <= 128 ? 128 : 256; }
+int hidden_splits(int64_t n, int64_t D, int64_t piece)
+{
+    const int64_t tm = tile_side(D), tn = tile_side(n);
+    const int64_t tiles = ((D + tm - 1) / tm) * ((n + tn - 1) / tn);
+    int64_t s = kCUs / tiles;
+    if (s > piece / kSplitK) s = piece / kSplitK;
+    return (int)(s < 1 ? 1 : s);
+}
 
 // `piece` columns of d (0: forward only).  Packed copies of the operands are
 // planned whether or not an aligned bf16 operand needs them, so that the size
@@ -506,14 +553,20 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     p.h = (bf16 *)take((size_t)PL * n * p.Kp * 2);
     p.w = (bf16 *)take((size_t)PL * V * p.Kp * 2);
     if (piece) {
-        p.sum = (float *)take(4 * (size_t)n * D);
+        p.splits = hidden_splits(n, D, piece);
+        p.sum = (float *)take(4 * (size_t)p.splits * n * D);
         p.d = (bf16 *)take((size_t)PL * p.nr * piece * 2);
     }
     p.bytes = off;
     return p;
 }
 
-int64_t best_piece(int64_t V) { return up(V < kPiece ? V : kPiece, kRound); }
+int64_t best_piece(int64_t n, int64_t V, int PL)
+{
+    int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * up(n, kRound) * 2)) / kRound * kRound;
+    if (c < 8 * kRound) c = 8 * kRound;
+    return up(V < c ? V : c, kRound);
+}
 
 template <class T, int PL>
 Operand operand(const T *src, int64_t ld, int64_t rows, int64_t D, bf16 *room, int64_t Kp, hipStream_t s)
@@ -530,27 +583,38 @@ Operand operand(const T *src, int64_t ld, int64_t rows, int64_t D, bf16 *room, i
 }
 
 // A product with M contiguous outputs in each of N rows; returns the tiles
-// along M.  256 x 256 tiles read each operand least often; where they would
-// leave compute units idle, 128 x 128 ones spread the work further.
+// along M.  256 x 256 tiles read each operand least often; a side of at most
+// 128 takes half of that, and where the tiles would leave compute units idle
+// 128 x 128 ones spread the work further.
 template <int PL, bool XT, bool YT, int OUT>
-int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s)
+int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s,
+                int splits = 1)
 {
-    const int64_t mt = (M + 255) / 256, nt = (N + 255) / 256;
-    if (mt * nt >= kCUs) {
-        hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, 4, 4>), dim3(tile_grid(mt, nt)), dim3(256), 0, s, x, y, K, mt,
-                           nt, o);
-        return mt;
+    const int64_t tm = tile_side(M), tn = tile_side(N);
+    int64_t mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
+    const bool small = mt * nt * splits < kCUs;
+    if (small) {
+        mt = (M + 127) / 128;
+        nt = (N + 127) / 128;
     }
-    const int64_t ms = (M + 127) / 128, ns = (N + 127) / 128;
-    hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, 2, 2>), dim3(tile_grid(ms, ns)), dim3(256), 0, s, x, y, K, ms, ns,
-                       o);
-    return ms;
+    const dim3 grid(tile_grid(mt, nt), (unsigned)splits);
+    auto go = [&](auto i, auto j) {
+        constexpr int NI = decltype(i)::value, NJ = decltype(j)::value;
+        hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, NI, NJ>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
+    };
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    if (!small && tm == 256 && tn == 256) go(four, four);
+    else if (!small && tm == 256) go(four, two);
+    else if (!small && tn == 256) go(two, four);
+    else go(two, two);
+    return mt;
 }
 
 template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
-    int64_t piece = grad ? best_piece(a.V) : 0;
+    int64_t piece = grad ? best_piece(a.n, a.V, PL) : 0;
     while (piece > kRound && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
         piece = up(piece / 2, kRound);
     const XentPlan p = plan_xent(a.n, a.V, a.D, PL, piece, a.ws);
@@ -584,17 +648,22 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         wp.rows = here;
         o.v0 = v0;
         o.first = v0 == 0;
-        o.last = v0 + piece >= a.V;
         // d of whole 256 x 256 blocks: what lies past the rows and the vocabulary is written as zeros
         product<PL, false, false, OUT_D>(wp, h, cols, p.nr, p.Kp, o, s);
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
-        o.out = a.dh;
-        o.ld_out = a.ld_dh;
-        product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s);
+        o.split_k = up((cols + p.splits - 1) / p.splits, kTileK);
+        product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s, p.splits);
         o.out = a.dw;
         o.ld_out = a.ld_dw;
         product<PL, true, true, OUT_WEIGHT>(h, d, a.D, here, p.nr, o, s);
     }
+    // splits past the first piece's end have written nothing
+    const int64_t first = up(a.V < piece ? a.V : piece, kRound);
+    const int64_t per = up((first + p.splits - 1) / p.splits, kTileK);
+    int64_t blocks = (a.n * ((a.D + 3) / 4) + 255) / 256;
+    if (blocks > 65536) blocks = 65536;
+    hipLaunchKernelGGL(k_xent_hidden<T>, dim3((unsigned)blocks), dim3(256), 0, s, p.sum, (int)((first + per - 1) / per),
+                       a.n, a.D, p.top_grad, static_cast<T *>(a.dh), a.ld_dh);
     return hipGetLastError();
 }
 
@@ -603,7 +672,8 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_t *best, size_t *least)
 {
     const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 3 : 1;
-    if (best) *best = plan_xent(n, V, D, PL, grad ? best_piece(V) : 0, nullptr).bytes;
+    if (n < 1) n = 1; // no rows: the least workspace
+    if (best) *best = plan_xent(n, V, D, PL, grad ? best_piece(n, V, PL) : 0, nullptr).bytes;
     if (least) *least = plan_xent(n, V, D, PL, grad ? kRound : 0, nullptr).bytes;
 }
 

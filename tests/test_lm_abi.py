@@ -175,3 +175,13 @@ def test_binding_declares_every_entry_point():
     assert set(lm.LM_EXPORTED) <= set(tt.EXPORTED)
     for name in lm.LM_EXPORTED:
         assert getattr(tt.lib(), name).argtypes is not None, name
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("n", [0, 1, 129, 100000])
+@pytest.mark.parametrize("V,D", [(1, 1), (300, 128), (10 ** 6, 129), (2 ** 31 - 2, 16384)])
+def test_xent_workspace_of_any_size(n, V, D, dtype):
+    best, least = C.c_size_t(), C.c_size_t()
+    for grad in (0, 1):
+        assert tt.lib().tt_emb_xent_workspace_size(n, V, D, dtype, grad, C.byref(best), C.byref(least)) == 0
+        assert 256 <= least.value <= best.value
