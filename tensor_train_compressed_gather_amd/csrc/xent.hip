@@ -26,7 +26,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTileK = 64;             // summed index per stage
 constexpr int kRowPitch = kTileK * 2 + 16; // bytes of a straight tile's row in LDS
-constexpr int kTurnPad = 32;           // bytes past a turned tile's row in LDS
+constexpr int kTurnPad = 64;           // bytes past a turned tile's row in LDS
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
 constexpr size_t kPieceBytes = (size_t)256 << 20; // d of one piece of the vocabulary, at most
 constexpr int kSplitK = 1024;          // least summed values of a split of dH
@@ -77,8 +77,8 @@ __device__ __forceinline__ void split(float x, bf16 (&t)[PL])
 // How an operand's tile of R outputs and 64 summed values lies in LDS.
 // Straight: R rows of 64 values, 144 bytes apart, so that the 16-byte reads of
 // sixteen lanes (sixteen rows) meet different banks.  Turned: 64 rows of R
-// values, 32 bytes more than R apart, so that the four rows a transposing read
-// touches at a time do.
+// values and 64 bytes, so that the four rows of 64 bytes that half a wave's
+// transposing read touches do.
 template <bool TURNED, int R>
 struct TileLds {
     static constexpr int pitch = TURNED ? R * 2 + kTurnPad : kRowPitch;
@@ -177,20 +177,24 @@ inline unsigned tile_grid(int64_t mt, int64_t nt)
     return (unsigned)(up(patches, 8) * kPatchM * kPatchN);
 }
 
-// Order of a step's instructions: after each matrix instruction the A and B
-// others that fall to it, so that neither the matrix core nor LDS waits for
-// the other's whole batch.
-constexpr int kMfma = 0x008, kVmRead = 0x020, kDsRead = 0x100, kDsWrite = 0x200;
-template <int M, int A, int MA, int B, int MB>
+// Order of a step's instructions: the reads of the next step's fragments two
+// to a matrix instruction, so that they are there when that step begins; then
+// the stores of a stage's pieces to LDS, each followed by the load of the same
+// piece of a later stage (a whole stage ahead of its use).
+template <int M, int READS, int PIECES>
 __device__ __forceinline__ void interleave()
 {
-    constexpr int per_a = (A + M - 1) / M, every_a = A >= M || A == 0 ? 1 : M / A;
-    constexpr int per_b = B ? (B + M - 1) / M : 0;
+    constexpr int mfma = 0x008, vmem_read = 0x020, ds_read = 0x100, ds_write = 0x200;
+    constexpr int by = (READS + 1) / 2 < M ? 2 : (READS + M - 1) / M, first = READS / by;
+    constexpr int rest = M - first > 0 ? M - first : 1, each = (PIECES + rest - 1) / rest;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-        if (i % every_a == 0) __builtin_amdgcn_sched_group_barrier(MA, per_a, 0);
-        if constexpr (B > 0) __builtin_amdgcn_sched_group_barrier(MB, per_b, 0);
+        __builtin_amdgcn_sched_group_barrier(mfma, 1, 0);
+        if (i < first) __builtin_amdgcn_sched_group_barrier(ds_read, by, 0);
+        else if (PIECES) {
+            __builtin_amdgcn_sched_group_barrier(ds_write, each, 0);
+            __builtin_amdgcn_sched_group_barrier(vmem_read, each, 0);
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -237,11 +241,10 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         constexpr int SEG = PL == 1 ? 1 : 6;
         const int per = (int)(K / kTileK), stages = SEG * per;
         int seg = 0, in = 0; // of the next stage to load; the last one is loaded again past the end
-        auto load = [&]() {
-            // planes (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), two bits each
-            const int px = PL == 1 ? 0 : (0x052 >> (2 * seg)) & 3, py = PL == 1 ? 0 : (0x118 >> (2 * seg)) & 3;
-            x.load(px, (int64_t)in * kTileK);
-            y.load(py, (int64_t)in * kTileK);
+        // planes (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), two bits each
+        auto load_x = [&]() { x.load(PL == 1 ? 0 : (0x052 >> (2 * seg)) & 3, (int64_t)in * kTileK); };
+        auto load_y = [&]() {
+            y.load(PL == 1 ? 0 : (0x118 >> (2 * seg)) & 3, (int64_t)in * kTileK);
             const bool over = in + 1 == per, more = !over || seg + 1 < SEG;
             seg += over && more;
             in = over ? (more ? 0 : in) : in + 1;
@@ -253,42 +256,45 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                 for (int j = 0; j < NJ; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
         };
-        load();
+        load_x();
+        load_y();
         x.store(lds);
         y.store(lds + XB);
-        load();
+        load_x();
+        load_y();
         __syncthreads();
         bf16x8 a0[NI], b0[NJ], a1[NI], b1[NJ];
         const int rx = wm * (TM / 2), ry = wn * (TN / 2);
         fragments<XT, TM>(lds, rx, 0, a0);
         fragments<YT, TN>(lds + XB, ry, 0, b0);
-        // reads of a step's fragments, pieces moved and matrix instructions of a step
-        constexpr int RD = NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1), MV = (TM + TN) / 32, MM = NI * NJ;
+        // reads of a step's fragments, pieces of an operand moved, matrix instructions of a step
+        constexpr int RD = NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1), XV = TM / 32, YV = TN / 32, MM = NI * NJ;
         int cur = 0;
         for (int t = 0; t < stages; ++t) {
             const char *here = lds + cur;
             char *next = lds + (STAGE - cur);
             fragments<XT, TM>(here, rx, 1, a1);
             fragments<YT, TN>(here + XB, ry, 1, b1);
+            x.store(next);
+            load_x();
             mma(a0, b0);
-            interleave<MM, RD, kDsRead, 0, 0>();
+            interleave<MM, RD, XV>();
             fragments<XT, TM>(here, rx, 2, a0);
             fragments<YT, TN>(here + XB, ry, 2, b0);
-            x.store(next);
             y.store(next + XB);
+            load_y();
             mma(a1, b1);
-            interleave<MM, RD, kDsRead, MV, kDsWrite>();
+            interleave<MM, RD, YV>();
             fragments<XT, TM>(here, rx, 3, a1);
             fragments<YT, TN>(here + XB, ry, 3, b1);
-            load();
             mma(a0, b0);
-            interleave<MM, RD, kDsRead, MV, kVmRead>();
+            interleave<MM, RD, 0>();
             __syncthreads();
             __builtin_amdgcn_sched_barrier(0); // the last step's products stay behind the barrier
             fragments<XT, TM>(next, rx, 0, a0);
             fragments<YT, TN>(next + XB, ry, 0, b0);
             mma(a1, b1);
-            interleave<MM, RD, kDsRead, 0, 0>();
+            interleave<MM, RD, 0>();
             cur = STAGE - cur;
         }
     }
