@@ -436,8 +436,10 @@ int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weigh
  *   d_iv = grad_loss_i (exp(z_iv - lse_i) - [v = target_i])
  *   grad_hidden_i = sum_v d_iv weight_v,  grad_weight_v = sum_i d_iv hidden_i
  * both of `dtype`, overwritten.  The vocabulary is taken in pieces whose d
- * (bf16 for bf16 inputs; split into three bf16 terms, 24 bits, for fp32
- * inputs) is in ws; sums are fp32.  A larger ws allows larger pieces: any
+ * (bf16 for bf16 inputs; two fp16 terms, 22 bits, for fp32 inputs, whose
+ * own values are scaled by powers of two and split the same way) is in ws;
+ * sums are fp32.  An ignored row's hidden values do not reach the gradients,
+ * whatever they hold.  A larger ws allows larger pieces: any
  * ws_bytes from *least of tt_emb_xent_workspace_size on is accepted, *bytes
  * is the size past which nothing is gained. */
 int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *weight, int64_t ld_weight,

@@ -9,9 +9,12 @@
 // the gradients a piece of the vocabulary's logits is made again, turned into
 // d, and multiplied into both gradients before the next piece.
 //
-// fp32 inputs are split into three bf16 terms (24 bits of mantissa) and the
-// six products of terms that matter at 2^-24 are added up, which is more than
-// twice the rate of the fp32 matrix instructions; d is split the same way.
+// fp32 inputs are scaled by powers of two (each hidden row, and the weight as a
+// whole, to a largest magnitude in [2^14, 2^15)) and split into two fp16 terms
+// of 11 bits each, and the three products of terms above 2^-22 are added up:
+// five times the rate of the fp32 matrix instructions.  d, at most 1 in its
+// units, is split the same way in units of 2^-15.  A value keeps 22 bits, or an
+// absolute 2^-39 of the largest where that is more.
 #include "lm.h"
 #include "primitives.h"
 
@@ -19,29 +22,65 @@ namespace ttemb {
 
 namespace {
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8))); // a fragment: eight bf16 or fp16 values
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTileK = 64;             // summed index per stage
-constexpr int kRowPitch = kTileK * 2 + 16; // bytes of a straight tile's row in LDS
 constexpr int kTurnPad = 64;           // bytes past a turned tile's row in LDS
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
 constexpr size_t kPieceBytes = (size_t)256 << 20; // d of one piece of the vocabulary, at most
-constexpr int kSplitK = 1024;          // least summed values of a split of dH
+constexpr int kSplitK = 512;           // least summed values of a split of dH
 constexpr int kRound = 256;            // rows and columns of d are padded to this
-
-constexpr int kLeast = 128;             // rows and columns of the smallest tile
+constexpr int kLeast = 128;            // rows and columns of the smallest tile
+constexpr int kPadK = 64;              // packed rows are padded to this
+constexpr int kMaxParts = 1024;        // blocks of the weight's largest magnitude
+constexpr int kUnitExp = 15;           // fp16 terms: d is kept in units of 2^-15
 
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// An operand of a product: `planes` bf16 matrices.  Straight: row r holds the
-// summed index.  Turned: row k of the summed index holds the outputs.
+// PL planes of 16-bit terms: one of bf16, or two of fp16.
+template <int PL>
+struct Terms {
+    typedef bf16 type;
+    static constexpr int stage = 64; // summed values per stage
+    static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                       0, 0, 0);
+    }
+};
+template <>
+struct Terms<2> {
+    typedef f16 type;
+    static constexpr int stage = 32;
+    static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
+                                                      0, 0, 0);
+    }
+};
+
+// x as a sum of PL terms
+template <int PL>
+__device__ __forceinline__ void split(float x, short (&t)[PL])
+{
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const typename Terms<PL>::type y = (typename Terms<PL>::type)x;
+        t[i] = __builtin_bit_cast(short, y);
+        x -= (float)y;
+    }
+}
+
+// An operand of a product: PL matrices of 16-bit values.  Straight: row r holds
+// the summed index.  Turned: row k of the summed index holds the outputs.
 struct Operand {
-    const bf16 *p;
-    int64_t ld, plane; // elements between rows, between planes
-    int64_t rows, cols; // of the stored matrix; reads past them are clamped
+    const short *p;
+    int64_t ld, plane;  // elements between rows, between planes
+    int64_t rows, cols; // of the stored matrix; what lies past them reads as zero
 };
 
 enum { OUT_STATS, OUT_D, OUT_HIDDEN, OUT_WEIGHT };
@@ -53,51 +92,43 @@ struct Output {
     float2 *part;             // [vocabulary tiles][n] maximum and sum
     float *target_logit;      // [n]
     const float *lse, *grad;  // [n]
-    const float *top_grad;    // the largest |grad| of a row that counts
-    bf16 *d;                  // [planes][rows][ldd]
+    const float *top_grad;    // the unit of d
+    const int *h_exp, *w_exp; // fp16 terms: exponents the rows and the weight were scaled by
+    short *d;                 // [planes][rows][ldd]
     int64_t ldd, plane_d;
     float *sum;               // dH in fp32, [splits][n][D]
-    int64_t split_k;          // summed values per split of dH
+    int splits;               // of dH's sum
+    int64_t split_k;          // summed values of each
     void *out;                // dW
     int64_t ld_out, D;
     int first;                // dH's first piece
 };
 
-// x as a sum of PL bf16 values
-template <int PL>
-__device__ __forceinline__ void split(float x, bf16 (&t)[PL])
-{
-#pragma unroll
-    for (int i = 0; i < PL; ++i) {
-        t[i] = (bf16)x;
-        x -= (float)t[i];
-    }
-}
-
-// How an operand's tile of R outputs and 64 summed values lies in LDS.
-// Straight: R rows of 64 values, 144 bytes apart, so that the 16-byte reads of
-// sixteen lanes (sixteen rows) meet different banks.  Turned: 64 rows of R
+// How one plane of an operand's tile, R outputs and BK summed values, lies in
+// LDS.  Straight: R rows of BK values and 16 bytes, so that the 16-byte reads
+// of sixteen lanes (sixteen rows) meet different banks.  Turned: BK rows of R
 // values and 64 bytes, so that the four rows of 64 bytes that half a wave's
 // transposing read touches do.
-template <bool TURNED, int R>
+template <bool TURNED, int R, int BK>
 struct TileLds {
-    static constexpr int pitch = TURNED ? R * 2 + kTurnPad : kRowPitch;
-    static constexpr int bytes = TURNED ? kTileK * pitch : R * pitch;
-    static constexpr int vecs = R * kTileK / 8 / 256; // 16-byte pieces per thread
+    static constexpr int pitch = TURNED ? R * 2 + kTurnPad : BK * 2 + 16;
+    static constexpr int bytes = (TURNED ? BK : R) * pitch;
+    static constexpr int vecs = R * BK / 8 / 256; // 16-byte pieces per thread
 };
 
 // One operand's way from memory to registers to LDS.  Loads go through a
 // buffer descriptor that ends with the matrix, so rows past it (of the outputs
 // or of the summed index) read as zeros and no address needs a clamp.
-template <bool TURNED, int R>
+template <bool TURNED, int R, int PL>
 struct TileLoader {
-    static constexpr int N = TileLds<TURNED, R>::vecs;
-    static constexpr int ROWV = TURNED ? R / 8 : kTileK / 8; // pieces in a tile's row
-    const bf16 *p;  // plane 0, moved to the tile's first row (straight) or column (turned)
+    static constexpr int BK = Terms<PL>::stage, P = TileLds<TURNED, R, BK>::pitch;
+    static constexpr int N = TileLds<TURNED, R, BK>::vecs;
+    static constexpr int ROWV = (TURNED ? R : BK) / 8; // pieces in a tile's row
+    const short *p; // plane 0, moved to the tile's first row (straight) or column (turned)
     int64_t ld, plane, end; // end: elements from p to the end of plane 0
     int off;        // byte offset of this thread's first piece; the others are 256 / ROWV rows apart
     int step;
-    u32x4 v[N];
+    u32x4 v[PL][N];
 
     __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0)
     {
@@ -109,70 +140,91 @@ struct TileLoader {
         off = ((t / ROWV) * (int)ld + (t % ROWV) * 8) * 2;
         step = 256 / ROWV * (int)ld * 2;
     }
-    __device__ __forceinline__ void load(int pl, int64_t k0)
+    __device__ __forceinline__ void load(int64_t k0)
     {
         const int64_t skip = TURNED ? k0 * ld : k0;
         const int64_t left = (end - skip) * 2;
         const unsigned bytes = left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left;
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<bf16 *>(p + pl * plane + skip), 0, bytes, 0x00027000);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __builtin_amdgcn_raw_buffer_load_b128(r, off, i * step, 0);
+        for (int q = 0; q < PL; ++q) {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<short *>(p + q * plane + skip), 0, bytes, 0x00027000);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[q][i] = __builtin_amdgcn_raw_buffer_load_b128(r, off, i * step, 0);
+        }
     }
     __device__ __forceinline__ void store(char *lds) const
     {
         const int t = threadIdx.x;
-        constexpr int P = TileLds<TURNED, R>::pitch;
-        char *q = lds + (t / ROWV) * P + (t % ROWV) * 16;
+        char *to = lds + (t / ROWV) * P + (t % ROWV) * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4 *>(q + i * (256 / ROWV) * P) = v[i];
+        for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                *reinterpret_cast<u32x4 *>(to + q * TileLds<TURNED, R, BK>::bytes + i * (256 / ROWV) * P) = v[q][i];
     }
 };
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // Fragments of N 32-row blocks from row `r0` of a tile, summed values
 // [ks * 16, ks * 16 + 16): lane l gets row l % 32, values 8 (l / 32) .. + 7.
 // A transposing read gives each of sixteen lanes one column of the four rows
 // that the sixteen lanes' 8-byte addresses name.
-template <bool TURNED, int R, int N>
-__device__ __forceinline__ void fragments(const char *lds, int r0, int ks, bf16x8 (&f)[N])
+template <bool TURNED, int R, int PL, int N>
+__device__ __forceinline__ void fragments(const char *lds, int r0, int ks, s16x8 (&f)[PL][N])
 {
+    constexpr int BK = Terms<PL>::stage, P = TileLds<TURNED, R, BK>::pitch;
     const int l = threadIdx.x & 63;
-    if constexpr (!TURNED) {
-        const char *q = lds + (r0 + (l & 31)) * kRowPitch + ks * 32 + (l >> 5) * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = *reinterpret_cast<const bf16x8 *>(q + i * 32 * kRowPitch);
-    } else {
-        constexpr int P = TileLds<TURNED, R>::pitch;
-        const char *q = lds + (ks * 16 + (l >> 5) * 8 + ((l & 15) >> 2)) * P +
-                        (r0 + ((l >> 4) & 1) * 16 + (l & 3) * 4) * 2;
+    for (int q = 0; q < PL; ++q) {
+        const char *from = lds + q * TileLds<TURNED, R, BK>::bytes;
+        if constexpr (!TURNED) {
+            from += (r0 + (l & 31)) * P + ks * 32 + (l >> 5) * 16;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
-            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(q + i * 64));
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(q + i * 64 + 4 * P));
-            f[i] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+            for (int i = 0; i < N; ++i) f[q][i] = *reinterpret_cast<const s16x8 *>(from + i * 32 * P);
+        } else {
+            from += (ks * 16 + (l >> 5) * 8 + ((l & 15) >> 2)) * P + (r0 + ((l >> 4) & 1) * 16 + (l & 3) * 4) * 2;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
+                const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + i * 64));
+                const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + i * 64 + 4 * P));
+                f[q][i] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
         }
     }
 }
 
-// Tile of a thread block: consecutive blocks go to the eight XCDs in turn, so
-// each XCD takes patches of kPatchM x kPatchN tiles (its 32 compute units) whose
-// operands meet in its L2, and the patches that run at the same time lie along
-// n, where they share the X operand in the memory-side cache.
-__device__ __forceinline__ bool tile_of(int64_t mt, int64_t nt, int64_t &m, int64_t &n)
+// Tile (and split of the sum) of a thread block.  Consecutive blocks go to the
+// eight XCDs in turn.  Grids of many rounds: each XCD takes patches of kPatchM x
+// kPatchN tiles (its 32 compute units) whose operands meet in its L2, and the
+// patches that run at the same time lie along n, where they share the X operand
+// in the memory-side cache.  Smaller grids: each XCD takes an eighth of the
+// tiles in a row, split by split.
+__host__ __device__ inline bool in_patches(int64_t mt, int64_t nt)
 {
-    constexpr int P = kPatchM * kPatchN;
-    const int64_t b = blockIdx.x, local = b >> 3;
-    const int64_t patch = local / P * 8 + (b & 7), in = local % P;
-    const int64_t pn = (nt + kPatchN - 1) / kPatchN;
-    m = patch / pn * kPatchM + in % kPatchM;
-    n = patch % pn * kPatchN + in / kPatchM;
-    return m < mt && n < nt;
+    return mt >= kPatchM && nt >= kPatchN && mt * nt >= 4 * kCUs;
 }
-inline unsigned tile_grid(int64_t mt, int64_t nt)
+__device__ __forceinline__ bool tile_of(int64_t mt, int64_t nt, int splits, int64_t &m, int64_t &n, int &split)
 {
+    const int64_t b = blockIdx.x, local = b >> 3;
+    split = 0;
+    if (in_patches(mt, nt)) {
+        constexpr int P = kPatchM * kPatchN;
+        const int64_t patch = local / P * 8 + (b & 7), in = local % P;
+        const int64_t pn = (nt + kPatchN - 1) / kPatchN;
+        m = patch / pn * kPatchM + in % kPatchM;
+        n = patch % pn * kPatchN + in / kPatchM;
+        return m < mt && n < nt;
+    }
+    const int64_t id = (b & 7) * (gridDim.x >> 3) + local, t = id % (mt * nt);
+    split = (int)(id / (mt * nt));
+    m = t % mt;
+    n = t / mt;
+    return split < splits;
+}
+inline unsigned tile_grid(int64_t mt, int64_t nt, int splits)
+{
+    if (!in_patches(mt, nt)) return (unsigned)up(mt * nt * splits, 8);
     const int64_t patches = ((mt + kPatchM - 1) / kPatchM) * ((nt + kPatchN - 1) / kPatchN);
     return (unsigned)(up(patches, 8) * kPatchM * kPatchN);
 }
@@ -206,24 +258,26 @@ __device__ __forceinline__ void interleave()
 //
 // Tiles go from memory to registers a stage ahead and from there to one of two
 // LDS buffers, and fragments are read one step of 16 ahead of the matrix
-// instructions that use them; the one barrier per stage stands before its last
-// step, whose fragments are in registers by then.
+// instructions that use them; the one barrier per stage stands before products
+// whose fragments are in registers by then.
 template <int PL, bool XT, bool YT, int OUT, int NI, int NJ>
 __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_t K, int64_t mt, int64_t nt, Output o)
 {
-    constexpr int TM = 64 * NI, TN = 64 * NJ;
-    constexpr int XB = TileLds<XT, TM>::bytes, YB = TileLds<YT, TN>::bytes, STAGE = XB + YB;
+    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Terms<PL>::stage;
+    constexpr int XB = PL * TileLds<XT, TM, BK>::bytes, YB = PL * TileLds<YT, TN, BK>::bytes, STAGE = XB + YB;
     __shared__ __align__(16) char lds[2 * STAGE];
     int64_t mi, ni;
-    if (!tile_of(mt, nt, mi, ni)) return;
+    int sp;
+    if (!tile_of(mt, nt, OUT == OUT_HIDDEN ? o.splits : 1, mi, ni, sp)) return;
     if constexpr (OUT == OUT_HIDDEN) { // this split's part of the sum
-        const int64_t k0 = blockIdx.y * o.split_k;
+        const int64_t k0 = sp * o.split_k;
         if (k0 >= K) return;
         X.p += k0 * X.ld;
         X.rows -= k0;
         Y.p += k0;
+        Y.cols -= k0;
         K = K - k0 < o.split_k ? K - k0 : o.split_k;
-        o.sum += blockIdx.y * o.n * o.D;
+        o.sum += sp * o.n * o.D;
     }
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
     const int64_t m0 = mi * TM, n0 = ni * TN;
@@ -235,26 +289,20 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     {
-        TileLoader<XT, TM> x(X, m0);
-        TileLoader<YT, TN> y(Y, n0);
-        // products of terms, the small ones first
-        constexpr int SEG = PL == 1 ? 1 : 6;
-        const int per = (int)(K / kTileK), stages = SEG * per;
-        int seg = 0, in = 0; // of the next stage to load; the last one is loaded again past the end
-        // planes (2,0) (0,2) (1,1) (1,0) (0,1) (0,0), two bits each
-        auto load_x = [&]() { x.load(PL == 1 ? 0 : (0x052 >> (2 * seg)) & 3, (int64_t)in * kTileK); };
+        TileLoader<XT, TM, PL> x(X, m0);
+        TileLoader<YT, TN, PL> y(Y, n0);
+        const int stages = (int)(K / BK);
+        int in = 0; // next stage to load; the last one is loaded again past the end
+        auto load_x = [&]() { x.load((int64_t)in * BK); };
         auto load_y = [&]() {
-            y.load(PL == 1 ? 0 : (0x118 >> (2 * seg)) & 3, (int64_t)in * kTileK);
-            const bool over = in + 1 == per, more = !over || seg + 1 < SEG;
-            seg += over && more;
-            in = over ? (more ? 0 : in) : in + 1;
+            y.load((int64_t)in * BK);
+            in = in + 1 < stages ? in + 1 : in;
         };
-        auto mma = [&](const bf16x8 (&a)[NI], const bf16x8 (&b)[NJ]) {
+        auto mma = [&](const s16x8 (&a)[NI], const s16x8 (&b)[NJ]) {
 #pragma unroll
             for (int i = 0; i < NI; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < NJ; ++j) acc[i][j] = Terms<PL>::mma(a[i], b[j], acc[i][j]);
         };
         load_x();
         load_y();
@@ -263,38 +311,57 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         load_x();
         load_y();
         __syncthreads();
-        bf16x8 a0[NI], b0[NJ], a1[NI], b1[NJ];
+        s16x8 a0[PL][NI], b0[PL][NJ], a1[PL][NI], b1[PL][NJ];
         const int rx = wm * (TM / 2), ry = wn * (TN / 2);
-        fragments<XT, TM>(lds, rx, 0, a0);
-        fragments<YT, TN>(lds + XB, ry, 0, b0);
-        // reads of a step's fragments, pieces of an operand moved, matrix instructions of a step
-        constexpr int RD = NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1), XV = TM / 32, YV = TN / 32, MM = NI * NJ;
+        fragments<XT, TM, PL>(lds, rx, 0, a0);
+        fragments<YT, TN, PL>(lds + XB, ry, 0, b0);
+        // reads of a step's fragments, pieces of an operand moved, matrix instructions of a product
+        constexpr int RD = PL * (NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1)), MM = NI * NJ;
+        constexpr int XV = PL * TileLds<XT, TM, BK>::vecs, YV = PL * TileLds<YT, TN, BK>::vecs;
         int cur = 0;
         for (int t = 0; t < stages; ++t) {
             const char *here = lds + cur;
             char *next = lds + (STAGE - cur);
-            fragments<XT, TM>(here, rx, 1, a1);
-            fragments<YT, TN>(here + XB, ry, 1, b1);
+            fragments<XT, TM, PL>(here, rx, 1, a1);
+            fragments<YT, TN, PL>(here + XB, ry, 1, b1);
             x.store(next);
             load_x();
-            mma(a0, b0);
-            interleave<MM, RD, XV>();
-            fragments<XT, TM>(here, rx, 2, a0);
-            fragments<YT, TN>(here + XB, ry, 2, b0);
-            y.store(next + XB);
-            load_y();
-            mma(a1, b1);
-            interleave<MM, RD, YV>();
-            fragments<XT, TM>(here, rx, 3, a1);
-            fragments<YT, TN>(here + XB, ry, 3, b1);
-            mma(a0, b0);
-            interleave<MM, RD, 0>();
-            __syncthreads();
-            __builtin_amdgcn_sched_barrier(0); // the last step's products stay behind the barrier
-            fragments<XT, TM>(next, rx, 0, a0);
-            fragments<YT, TN>(next + XB, ry, 0, b0);
-            mma(a1, b1);
-            interleave<MM, RD, 0>();
+            if constexpr (PL == 1) {
+                mma(a0[0], b0[0]);
+                interleave<MM, RD, XV>();
+                fragments<XT, TM, PL>(here, rx, 2, a0);
+                fragments<YT, TN, PL>(here + XB, ry, 2, b0);
+                y.store(next + XB);
+                load_y();
+                mma(a1[0], b1[0]);
+                interleave<MM, RD, YV>();
+                fragments<XT, TM, PL>(here, rx, 3, a1);
+                fragments<YT, TN, PL>(here + XB, ry, 3, b1);
+                mma(a0[0], b0[0]);
+                interleave<MM, RD, 0>();
+                __syncthreads();
+                __builtin_amdgcn_sched_barrier(0); // the last step's products stay behind the barrier
+                fragments<XT, TM, PL>(next, rx, 0, a0);
+                fragments<YT, TN, PL>(next + XB, ry, 0, b0);
+                mma(a1[0], b1[0]);
+                interleave<MM, RD, 0>();
+            } else { // the products of terms, the small ones first
+                y.store(next + XB);
+                load_y();
+                mma(a0[1], b0[0]);
+                mma(a0[0], b0[1]);
+                mma(a0[0], b0[0]);
+                interleave<3 * MM, RD, XV + YV>();
+                mma(a1[1], b1[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                __syncthreads();
+                __builtin_amdgcn_sched_barrier(0);
+                fragments<XT, TM, PL>(next, rx, 0, a0);
+                fragments<YT, TN, PL>(next + XB, ry, 0, b0);
+                mma(a1[0], b1[1]);
+                mma(a1[0], b1[0]);
+                interleave<2 * MM, RD, 0>();
+            }
             cur = STAGE - cur;
         }
     }
@@ -308,12 +375,14 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             const int64_t i = n0 + nl;
             const int64_t t = i < o.n ? o.targets[i] - m0 : -1;
             const int64_t left = o.V - m0;
+            const int e = PL == 2 && i < o.n ? -(o.h_exp[i] + *o.w_exp) : 0;
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int a = 0; a < NI; ++a)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int v = row_of(a, r);
+                    if (PL == 2) acc[a][j][r] = ldexpf(acc[a][j][r], e);
                     if (v >= left) acc[a][j][r] = -INFINITY;
                     top = fmaxf(top, acc[a][j][r]);
                     if (v == t) o.target_logit[i] = acc[a][j][r];
@@ -338,18 +407,25 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             o.part[mi * o.n + n0 + tid] = make_float2(top, s);
         }
     } else {
-        const float scale = *o.top_grad;
+        const float unit = *o.top_grad;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
             float lse = 0.f, g = 0.f;
             int64_t t = -1;
+            int e = 0;
             if constexpr (OUT == OUT_D) {
                 if (i < o.n) {
                     t = o.targets[i] - o.v0;
                     const bool counts = o.targets[i] != o.ignore && o.targets[i] >= 0 && o.targets[i] < o.V;
-                    g = counts ? o.grad[i] / scale : 0.f;
                     lse = o.lse[i];
+                    if constexpr (PL == 2) {
+                        e = -(o.h_exp[i] + *o.w_exp);
+                        // at most 2^kUnitExp: the unit is the largest of these quotients
+                        g = counts ? ldexpf(o.grad[i], -o.h_exp[i]) / unit * (float)(1 << kUnitExp) : 0.f;
+                    } else {
+                        g = counts ? o.grad[i] / unit : 0.f;
+                    }
                 }
             }
 #pragma unroll
@@ -361,19 +437,20 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 #pragma unroll
                     for (int r = 0; r < 4; ++r) x[r] = acc[a][j][4 * q + r];
                     if constexpr (OUT == OUT_D) {
-                        bf16x4 w[PL];
+                        s16x4 w[PL];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const bool in = g != 0.f && o.v0 + m + r < o.V;
-                            const float d = in ? g * (__expf(x[r] - lse) - (m + r == t ? 1.f : 0.f)) : 0.f;
-                            bf16 s[PL];
+                            const float z = PL == 2 ? ldexpf(x[r], e) : x[r];
+                            const float d = in ? g * (__expf(z - lse) - (m + r == t ? 1.f : 0.f)) : 0.f;
+                            short s[PL];
                             split<PL>(d, s);
 #pragma unroll
                             for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
                         }
 #pragma unroll
                         for (int q2 = 0; q2 < PL; ++q2)
-                            *reinterpret_cast<bf16x4 *>(o.d + q2 * o.plane_d + i * o.ldd + m) = w[q2];
+                            *reinterpret_cast<s16x4 *>(o.d + q2 * o.plane_d + i * o.ldd + m) = w[q2];
                     } else {
                         const int left = (int)(o.D - m < 4 ? o.D - m : 4);
                         if (left <= 0) continue;
@@ -392,8 +469,8 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                         }
                         if (row >= o.V) continue;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] *= scale;
-                        if (PL > 1) store_part<float, 4>(static_cast<float *>(o.out) + row * o.ld_out + m, left, x);
+                        for (int r = 0; r < 4; ++r) x[r] *= PL == 2 ? unit * (1.f / (float)(1 << kUnitExp)) : unit;
+                        if (PL == 2) store_part<float, 4>(static_cast<float *>(o.out) + row * o.ld_out + m, left, x);
                         else store_part<bf16, 4>(static_cast<bf16 *>(o.out) + row * o.ld_out + m, left, x);
                     }
                 }
@@ -404,13 +481,15 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 // dH from the splits' sums, in order, in units of the loss.
 template <class T>
 __global__ __launch_bounds__(256) void k_xent_hidden(const float *sum, int splits, int64_t n, int64_t D,
-                                                     const float *top_grad, T *out, int64_t ld)
+                                                     const float *top_grad, const int *h_exp, const int *w_exp,
+                                                     T *out, int64_t ld)
 {
     const int64_t chunks = (D + 3) / 4, step = (int64_t)gridDim.x * 256;
-    const float scale = *top_grad;
+    const float unit = *top_grad;
     for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < n * chunks; c += step) {
         const int64_t i = c / chunks, k = (c - i * chunks) * 4;
         const int left = (int)(D - k < 4 ? D - k : 4);
+        const int e = h_exp ? h_exp[i] - *w_exp - kUnitExp : 0;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         for (int q = 0; q < splits; ++q) {
             float y[4];
@@ -419,33 +498,120 @@ __global__ __launch_bounds__(256) void k_xent_hidden(const float *sum, int split
             for (int r = 0; r < 4; ++r) x[r] += y[r];
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] *= scale;
+        for (int r = 0; r < 4; ++r) x[r] = h_exp ? ldexpf(x[r] * unit, e) : x[r] * unit;
         store_part<T, 4>(out + i * ld + k, left, x);
     }
 }
 
-// Rows of a matrix as PL bf16 planes with `ld` columns, zero past D.
-template <class T, int PL>
-__global__ __launch_bounds__(256) void k_pack(const T *src, int64_t ld_src, int64_t rows, int64_t D, bf16 *dst,
-                                              int64_t ld, int64_t plane)
+// The exponent that brings a largest magnitude into [2^14, 2^15).
+__device__ __forceinline__ int scale_exp(float top)
 {
-    const int64_t chunks = ld / 8;
-    const int64_t step = (int64_t)gridDim.x * 256;
+    return top > 0.f ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+}
+__device__ __forceinline__ float finite_abs(float x)
+{
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.f;
+}
+
+// One piece of a row, scaled and split.
+template <class T, int PL>
+__device__ __forceinline__ void pack_piece(const T *src, int64_t left, int e, bool clear, short *dst, int64_t plane)
+{
+    float x[8];
+    load_part<T, 8>(src, (int)(left < 0 ? 0 : left < 8 ? left : 8), x);
+    s16x8 w[PL];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        short s[PL];
+        split<PL>(clear ? 0.f : PL == 2 ? ldexpf(x[i], e) : x[i], s);
+#pragma unroll
+        for (int q = 0; q < PL; ++q) w[q][i] = s[q];
+    }
+#pragma unroll
+    for (int q = 0; q < PL; ++q) *reinterpret_cast<s16x8 *>(dst + q * plane) = w[q];
+}
+
+// Hidden rows as planes with `ld` columns, zero past D; a wave per row.  fp16
+// terms: each row scaled by a power of two of its own.  With targets: a row
+// that is ignored and holds a value that is not finite is taken as zeros, so
+// that its zero gradient stays zero in the weight's.
+template <class T, int PL>
+__global__ __launch_bounds__(256) void k_pack_rows(const T *src, int64_t ld_src, int64_t rows, int64_t D, short *dst,
+                                                   int64_t ld, int64_t plane, int *exps, const int64_t *targets,
+                                                   int64_t ignore, int64_t V)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t step = (int64_t)gridDim.x * 4;
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += step) {
+        const T *row = src + r * ld_src;
+        int e = 0;
+        bool clear = false;
+        if (PL == 2 || targets) {
+            float top = 0.f;
+            bool odd = false;
+            for (int64_t k = lane * 8; k < D; k += 512) {
+                float x[8];
+                load_part<T, 8>(row + k, (int)(D - k < 8 ? D - k : 8), x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    top = fmaxf(top, finite_abs(x[i]));
+                    odd = odd || !(fabsf(x[i]) < INFINITY);
+                }
+            }
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+            if (targets) {
+                const int64_t t = targets[r];
+                clear = __any(odd) && (t == ignore || t < 0 || t >= V);
+            }
+            e = PL == 2 && !clear ? scale_exp(top) : 0;
+            if (exps && lane == 0) exps[r] = e;
+        }
+        for (int64_t k = lane * 8; k < ld; k += 512)
+            pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, clear, dst + r * ld + k, plane);
+    }
+}
+
+// Largest finite magnitude of the weight, per block.
+__global__ __launch_bounds__(256) void k_weight_top(const float *src, int64_t ld, int64_t rows, int64_t D, float *part)
+{
+    __shared__ float sm[4];
+    const int64_t chunks = (D + 7) / 8, step = (int64_t)gridDim.x * 256;
+    float top = 0.f;
     for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
         const int64_t r = c / chunks, k = (c - r * chunks) * 8;
         float x[8];
-        const int left = D - k < 8 ? (int)(D - k < 0 ? 0 : D - k) : 8;
-        load_part<T, 8>(src + r * ld_src + (left ? k : 0), left, x);
-        bf16x8 w[PL];
+        load_part<float, 8>(src + r * ld + k, (int)(D - k < 8 ? D - k : 8), x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            bf16 s[PL];
-            split<PL>(x[i], s);
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(x[i]));
+    }
 #pragma unroll
-            for (int q = 0; q < PL; ++q) w[q][i] = s[q];
-        }
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) part[blockIdx.x] = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+}
+
+// The weight as planes with `ld` columns, zero past D.  fp16 terms: scaled by
+// one power of two, from the largest of the `parts` magnitudes.
+template <class T, int PL>
+__global__ __launch_bounds__(256) void k_pack_weight(const T *src, int64_t ld_src, int64_t rows, int64_t D, short *dst,
+                                                     int64_t ld, int64_t plane, const float *part, int parts, int *exp)
+{
+    int e = 0;
+    if constexpr (PL == 2) {
+        float top = 0.f;
+        for (int i = threadIdx.x & 63; i < parts; i += 64) top = fmaxf(top, part[i]);
 #pragma unroll
-        for (int q = 0; q < PL; ++q) *reinterpret_cast<bf16x8 *>(dst + q * plane + r * ld + k) = w[q];
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        e = scale_exp(top);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *exp = e;
+    }
+    const int64_t chunks = ld / 8, step = (int64_t)gridDim.x * 256;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
+        const int64_t r = c / chunks, k = (c - r * chunks) * 8;
+        pack_piece<T, PL>(src + r * ld_src + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
     }
 }
 
@@ -483,18 +649,19 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *part, int64_t t
     loss[i] = in && t != ignore ? z - target_logit[i] : 0.f;
 }
 
-// The largest |grad_loss| of the rows that count.  d is kept in units of it:
-// with equal gradients (a mean over the rows) d is exp(z - lse) - [v = target],
-// and the target's -1 + p, the largest term of both gradients, rounds to bf16
-// without error for small p.  1 where there is nothing to scale.
+// The unit of d: the largest |grad_loss| of the rows that count (fp16 terms:
+// divided by the power of two the row was scaled by, which d then carries).
+// With equal gradients (a mean over the rows) d is exp(z - lse) - [v = target]
+// in this unit, and the target's -1 + p, the largest term of both gradients,
+// rounds to bf16 without error for small p.  1 where there is nothing to scale.
 __global__ __launch_bounds__(1024) void k_xent_top_grad(const float *grad, const int64_t *targets, int64_t ignore,
-                                                        int64_t n, int64_t V, float *top)
+                                                        int64_t n, int64_t V, const int *h_exp, float *top)
 {
     __shared__ float sm[16];
     float m = 0.f;
     for (int64_t i = threadIdx.x; i < n; i += 1024) {
         const int64_t t = targets[i];
-        if (t != ignore && t >= 0 && t < V) m = fmaxf(m, fabsf(grad[i]));
+        if (t != ignore && t >= 0 && t < V) m = fmaxf(m, fabsf(h_exp ? ldexpf(grad[i], -h_exp[i]) : grad[i]));
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
@@ -515,11 +682,12 @@ __global__ __launch_bounds__(256) void k_xent_clear(T *p, int64_t ld, int64_t ro
 }
 
 struct XentPlan {
-    float *target_logit, *top_grad;
+    float *target_logit, *top_grad, *w_part;
+    int *h_exp, *w_exp;
     float2 *part;
-    bf16 *h, *w;     // packed operands (nullptr: used in place)
+    short *h, *w; // packed operands (the weight's unused where it serves in place)
     float *sum;
-    bf16 *d;
+    short *d;
     int64_t Kp, nr, piece;
     int splits;
     size_t bytes;
@@ -550,18 +718,21 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
         return r;
     };
     XentPlan p{};
-    p.Kp = up(D, kTileK);
+    p.Kp = up(D, kPadK);
     p.nr = up(n, kRound);
     p.piece = piece;
     p.target_logit = (float *)take(4 * n);
     p.top_grad = (float *)take(4);
     p.part = (float2 *)take(8 * (size_t)n * ((V + kLeast - 1) / kLeast));
-    p.h = (bf16 *)take((size_t)PL * n * p.Kp * 2);
-    p.w = (bf16 *)take((size_t)PL * V * p.Kp * 2);
+    p.w_part = (float *)take(4 * kMaxParts);
+    p.h_exp = (int *)take(4 * n);
+    p.w_exp = (int *)take(4);
+    p.h = (short *)take((size_t)PL * n * p.Kp * 2);
+    p.w = (short *)take((size_t)PL * V * p.Kp * 2);
     if (piece) {
         p.splits = hidden_splits(n, D, piece);
         p.sum = (float *)take(4 * (size_t)p.splits * n * D);
-        p.d = (bf16 *)take((size_t)PL * p.nr * piece * 2);
+        p.d = (short *)take((size_t)PL * p.nr * piece * 2);
     }
     p.bytes = off;
     return p;
@@ -575,17 +746,16 @@ int64_t best_piece(int64_t n, int64_t V, int PL)
 }
 
 template <class T, int PL>
-Operand operand(const T *src, int64_t ld, int64_t rows, int64_t D, bf16 *room, int64_t Kp, hipStream_t s)
+bool in_place(const T *src, int64_t ld, int64_t D, int64_t Kp)
 {
-    if constexpr (PL == 1) {
-        if (D == Kp && ld % 8 == 0 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0)
-            return Operand{src, ld, 0, rows, D};
-    }
-    int64_t blocks = (rows * (Kp / 8) + 255) / 256;
-    if (blocks > 65536) blocks = 65536;
-    hipLaunchKernelGGL((k_pack<T, PL>), dim3((unsigned)blocks), dim3(256), 0, s, src, ld, rows, D, room, Kp,
-                       rows * Kp);
-    return Operand{room, Kp, rows * Kp, rows, Kp};
+    // (a tile of rows further apart would pass the 31 bits of its loads)
+    return PL == 1 && D == Kp && ld % 8 == 0 && ld <= (1 << 20) && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+}
+
+unsigned blocks_for(int64_t threads)
+{
+    const int64_t b = (threads + 255) / 256;
+    return (unsigned)(b < 65536 ? b : 65536);
 }
 
 // A product with M contiguous outputs in each of N rows; returns the tiles
@@ -593,17 +763,17 @@ Operand operand(const T *src, int64_t ld, int64_t rows, int64_t D, bf16 *room, i
 // 128 takes half of that, and where the tiles would leave compute units idle
 // 128 x 128 ones spread the work further.
 template <int PL, bool XT, bool YT, int OUT>
-int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s,
-                int splits = 1)
+int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s)
 {
     const int64_t tm = tile_side(M), tn = tile_side(N);
     int64_t mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
+    const int splits = OUT == OUT_HIDDEN ? o.splits : 1;
     const bool small = mt * nt * splits < kCUs;
     if (small) {
         mt = (M + 127) / 128;
         nt = (N + 127) / 128;
     }
-    const dim3 grid(tile_grid(mt, nt), (unsigned)splits);
+    const dim3 grid(tile_grid(mt, nt, splits));
     auto go = [&](auto i, auto j) {
         constexpr int NI = decltype(i)::value, NJ = decltype(j)::value;
         hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, NI, NJ>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
@@ -624,8 +794,25 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     while (piece > kRound && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
         piece = up(piece / 2, kRound);
     const XentPlan p = plan_xent(a.n, a.V, a.D, PL, piece, a.ws);
-    const Operand h = operand<T, PL>(static_cast<const T *>(a.hidden), a.ld_h, a.n, a.D, p.h, p.Kp, s);
-    const Operand w = operand<T, PL>(static_cast<const T *>(a.weight), a.ld_w, a.V, a.D, p.w, p.Kp, s);
+    const T *hs = static_cast<const T *>(a.hidden), *ws = static_cast<const T *>(a.weight);
+    Operand h{reinterpret_cast<const short *>(hs), a.ld_h, 0, a.n, a.D};
+    if (grad || !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp)) {
+        h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
+        hipLaunchKernelGGL((k_pack_rows<T, PL>), dim3(blocks_for(a.n * 64)), dim3(256), 0, s, hs, a.ld_h, a.n, a.D, p.h,
+                           p.Kp, a.n * p.Kp, p.h_exp, grad ? a.targets : nullptr, a.ignore, a.V);
+    }
+    Operand w{reinterpret_cast<const short *>(ws), a.ld_w, 0, a.V, a.D};
+    if (!in_place<T, PL>(ws, a.ld_w, a.D, p.Kp)) {
+        w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
+        unsigned parts = 0;
+        if constexpr (PL == 2) {
+            parts = blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1);
+            if (parts > (unsigned)kMaxParts) parts = kMaxParts;
+            hipLaunchKernelGGL(k_weight_top, dim3(parts), dim3(256), 0, s, ws, a.ld_w, a.V, a.D, p.w_part);
+        }
+        hipLaunchKernelGGL((k_pack_weight<T, PL>), dim3(blocks_for(a.V * (p.Kp / 8))), dim3(256), 0, s, ws, a.ld_w, a.V,
+                           a.D, p.w, p.Kp, a.V * p.Kp, p.w_part, (int)parts, p.w_exp);
+    }
     Output o{};
     o.n = a.n;
     o.V = a.V;
@@ -637,6 +824,9 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.lse = a.lse;
     o.grad = a.grad_loss;
     o.top_grad = p.top_grad;
+    o.h_exp = p.h_exp;
+    o.w_exp = p.w_exp;
+    o.splits = p.splits;
     o.d = p.d;
     o.ldd = piece;
     o.plane_d = p.nr * piece;
@@ -646,7 +836,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
                        a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
     if (!grad) return hipGetLastError();
     hipLaunchKernelGGL(k_xent_top_grad, dim3(1), dim3(1024), 0, s, a.grad_loss, a.targets, a.ignore, a.n, a.V,
-                       p.top_grad);
+                       PL == 2 ? p.h_exp : nullptr, p.top_grad);
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t here = a.V - v0 < piece ? a.V - v0 : piece, cols = up(here, kRound);
         Operand wp = w;
@@ -657,19 +847,18 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         // d of whole 256 x 256 blocks: what lies past the rows and the vocabulary is written as zeros
         product<PL, false, false, OUT_D>(wp, h, cols, p.nr, p.Kp, o, s);
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
-        o.split_k = up((cols + p.splits - 1) / p.splits, kTileK);
-        product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s, p.splits);
+        o.split_k = up((cols + p.splits - 1) / p.splits, kPadK);
+        product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s);
         o.out = a.dw;
         o.ld_out = a.ld_dw;
         product<PL, true, true, OUT_WEIGHT>(h, d, a.D, here, p.nr, o, s);
     }
     // splits past the first piece's end have written nothing
     const int64_t first = up(a.V < piece ? a.V : piece, kRound);
-    const int64_t per = up((first + p.splits - 1) / p.splits, kTileK);
-    int64_t blocks = (a.n * ((a.D + 3) / 4) + 255) / 256;
-    if (blocks > 65536) blocks = 65536;
-    hipLaunchKernelGGL(k_xent_hidden<T>, dim3((unsigned)blocks), dim3(256), 0, s, p.sum, (int)((first + per - 1) / per),
-                       a.n, a.D, p.top_grad, static_cast<T *>(a.dh), a.ld_dh);
+    const int64_t per = up((first + p.splits - 1) / p.splits, kPadK);
+    hipLaunchKernelGGL(k_xent_hidden<T>, dim3(blocks_for(a.n * ((a.D + 3) / 4))), dim3(256), 0, s, p.sum,
+                       (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.h_exp : nullptr, p.w_exp,
+                       static_cast<T *>(a.dh), a.ld_dh);
     return hipGetLastError();
 }
 
@@ -677,7 +866,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 
 void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_t *best, size_t *least)
 {
-    const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 3 : 1;
+    const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1;
     if (n < 1) n = 1; // no rows: the least workspace
     if (best) *best = plan_xent(n, V, D, PL, grad ? best_piece(n, V, PL) : 0, nullptr).bytes;
     if (least) *least = plan_xent(n, V, D, PL, grad ? kRound : 0, nullptr).bytes;
@@ -686,7 +875,7 @@ void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_
 hipError_t launch_xent_forward(const XentArgs &a, int dtype, hipStream_t s)
 {
     if (a.n == 0) return hipSuccess;
-    return dtype == TT_EMB_DTYPE_FLOAT ? xent<float, 3>(a, false, s) : xent<bf16, 1>(a, false, s);
+    return dtype == TT_EMB_DTYPE_FLOAT ? xent<float, 2>(a, false, s) : xent<bf16, 1>(a, false, s);
 }
 
 hipError_t launch_xent_loss_grad(const XentArgs &a, int dtype, hipStream_t s)
@@ -701,7 +890,7 @@ hipError_t launch_xent_loss_grad(const XentArgs &a, int dtype, hipStream_t s)
                                a.V, a.D);
         return hipGetLastError();
     }
-    return dtype == TT_EMB_DTYPE_FLOAT ? xent<float, 3>(a, true, s) : xent<bf16, 1>(a, true, s);
+    return dtype == TT_EMB_DTYPE_FLOAT ? xent<float, 2>(a, true, s) : xent<bf16, 1>(a, true, s);
 }
 
 } // namespace ttemb
