@@ -375,24 +375,35 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             const int64_t i = n0 + nl;
             const int64_t t = i < o.n ? o.targets[i] - m0 : -1;
             const int64_t left = o.V - m0;
-            const int e = PL == 2 && i < o.n ? -(o.h_exp[i] + *o.w_exp) : 0;
+            // the accumulators are logits times a power of two; the maximum is
+            // taken and subtracted before they are scaled
+            const float unit = PL == 2 && i < o.n ? ldexpf(1.f, -(o.h_exp[i] + *o.w_exp)) : 1.f;
+            if (left < TM) { // the vocabulary ends in this tile
+#pragma unroll
+                for (int a = 0; a < NI; ++a)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row_of(a, r) >= left) acc[a][j][r] = -INFINITY;
+            }
+            if (__any(t >= wm * (TM / 2) && t < (wm + 1) * (TM / 2))) {
+#pragma unroll
+                for (int a = 0; a < NI; ++a)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row_of(a, r) == t) o.target_logit[i] = acc[a][j][r] * unit;
+            }
             float top = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int a = 0; a < NI; ++a)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int v = row_of(a, r);
-                    if (PL == 2) acc[a][j][r] = ldexpf(acc[a][j][r], e);
-                    if (v >= left) acc[a][j][r] = -INFINITY;
-                    top = fmaxf(top, acc[a][j][r]);
-                    if (v == t) o.target_logit[i] = acc[a][j][r];
-                }
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[a][j][r]);
             top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float ref = top == -INFINITY ? 0.f : top;
+            const float ref = top == -INFINITY ? 0.f : top, base = unit * 1.44269504f;
 #pragma unroll
             for (int a = 0; a < NI; ++a)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) sum += __expf(acc[a][j][r] - ref);
+                for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[a][j][r] - ref) * base);
+            top *= unit;
             sum += __shfl_xor(sum, 32, 64);
             if (lane < 32) {
                 red[0][wm][nl] = top;
@@ -406,28 +417,72 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             const float s = red[1][0][tid] * __expf(a - ref) + red[1][1][tid] * __expf(b - ref);
             o.part[mi * o.n + n0 + tid] = make_float2(top, s);
         }
+    } else if constexpr (OUT == OUT_D) {
+        // 64 rows of d at a time pass through LDS, so that they are written in
+        // whole lines: a lane holds four columns of one row, a wave 32 rows
+        constexpr int P = TM * 2 + 16, PART = 64 * P, PIECES = 64 * (TM / 8) / 256;
+        constexpr bool TWO = 2 * PL * PART <= 2 * STAGE; // one part is written while the last is read
+        static_assert(PL * PART <= 2 * STAGE, "a part fits the tiles' space");
+        const float unit = *o.top_grad;
+        const int64_t left = o.V - o.v0 - m0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
+            // rows that do not count, or lie past the last: d = 0 (exp - 0)
+            float lse = 0.f, g = 0.f, scale = 1.f;
+            int64_t t = -1;
+            if (i < o.n) {
+                const int64_t target = o.targets[i];
+                lse = o.lse[i];
+                if constexpr (PL == 2) scale = ldexpf(1.f, -(o.h_exp[i] + *o.w_exp));
+                if (target != o.ignore && target >= 0 && target < o.V) {
+                    t = target - o.v0 - m0;
+                    // fp16 terms: at most 2^kUnitExp, the unit is the largest of these quotients
+                    g = PL == 2 ? ldexpf(o.grad[i], -o.h_exp[i]) / unit * (float)(1 << kUnitExp) : o.grad[i] / unit;
+                } else {
+                    lse = INFINITY;
+                }
+            }
+            char *part = lds + (TWO ? (j & 1) * PL * PART : 0);
+            if (!TWO && j) __syncthreads();
+            const bool here = __any(t >= wm * (TM / 2) && t < (wm + 1) * (TM / 2));
+#pragma unroll
+            for (int a = 0; a < NI; ++a)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int m = row_of(a, 4 * q);
+                    s16x4 w[PL];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float p = __builtin_amdgcn_exp2f(fmaf(acc[a][j][4 * q + r], scale, -lse) * 1.44269504f);
+                        if (here) p -= m + r == t ? 1.f : 0.f;
+                        if (left < TM && m + r >= left) p = 0.f;
+                        short s[PL];
+                        split<PL>(g * p, s);
+#pragma unroll
+                        for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
+                    }
+#pragma unroll
+                    for (int q2 = 0; q2 < PL; ++q2)
+                        *reinterpret_cast<s16x4 *>(part + q2 * PART + (wn * 32 + (lane & 31)) * P + m * 2) = w[q2];
+                }
+            __syncthreads();
+#pragma unroll
+            for (int q2 = 0; q2 < PL; ++q2)
+#pragma unroll
+                for (int k = 0; k < PIECES; ++k) {
+                    const int c = tid + k * 256, r = c / (TM / 8), x = c % (TM / 8);
+                    const int64_t row = n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31);
+                    *reinterpret_cast<u32x4 *>(o.d + q2 * o.plane_d + row * o.ldd + m0 + x * 8) =
+                        *reinterpret_cast<const u32x4 *>(part + q2 * PART + r * P + x * 16);
+                }
+        }
     } else {
         const float unit = *o.top_grad;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
-            float lse = 0.f, g = 0.f;
-            int64_t t = -1;
-            int e = 0;
-            if constexpr (OUT == OUT_D) {
-                if (i < o.n) {
-                    t = o.targets[i] - o.v0;
-                    const bool counts = o.targets[i] != o.ignore && o.targets[i] >= 0 && o.targets[i] < o.V;
-                    lse = o.lse[i];
-                    if constexpr (PL == 2) {
-                        e = -(o.h_exp[i] + *o.w_exp);
-                        // at most 2^kUnitExp: the unit is the largest of these quotients
-                        g = counts ? ldexpf(o.grad[i], -o.h_exp[i]) / unit * (float)(1 << kUnitExp) : 0.f;
-                    } else {
-                        g = counts ? o.grad[i] / unit : 0.f;
-                    }
-                }
-            }
 #pragma unroll
             for (int a = 0; a < NI; ++a)
 #pragma unroll
@@ -436,37 +491,20 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                     float x[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) x[r] = acc[a][j][4 * q + r];
-                    if constexpr (OUT == OUT_D) {
-                        s16x4 w[PL];
+                    const int left = (int)(o.D - m < 4 ? o.D - m : 4);
+                    if (left <= 0) continue;
+                    if constexpr (OUT == OUT_HIDDEN) {
+                        if (i >= o.n) continue;
+                        float *s = o.sum + i * o.D + m;
+                        if (!o.first) {
+                            float old[4];
+                            load_part<float, 4>(s, left, old);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const bool in = g != 0.f && o.v0 + m + r < o.V;
-                            const float z = PL == 2 ? ldexpf(x[r], e) : x[r];
-                            const float d = in ? g * (__expf(z - lse) - (m + r == t ? 1.f : 0.f)) : 0.f;
-                            short s[PL];
-                            split<PL>(d, s);
-#pragma unroll
-                            for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
+                            for (int r = 0; r < 4; ++r) x[r] += old[r];
                         }
-#pragma unroll
-                        for (int q2 = 0; q2 < PL; ++q2)
-                            *reinterpret_cast<s16x4 *>(o.d + q2 * o.plane_d + i * o.ldd + m) = w[q2];
+                        store_part<float, 4>(s, left, x);
                     } else {
-                        const int left = (int)(o.D - m < 4 ? o.D - m : 4);
-                        if (left <= 0) continue;
                         const int64_t row = o.v0 + i;
-                        if constexpr (OUT == OUT_HIDDEN) {
-                            if (i >= o.n) continue;
-                            float *s = o.sum + i * o.D + m;
-                            if (!o.first) {
-                                float old[4];
-                                load_part<float, 4>(s, left, old);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) x[r] += old[r];
-                            }
-                            store_part<float, 4>(s, left, x);
-                            continue;
-                        }
                         if (row >= o.V) continue;
 #pragma unroll
                         for (int r = 0; r < 4; ++r) x[r] *= PL == 2 ? unit * (1.f / (float)(1 << kUnitExp)) : unit;
