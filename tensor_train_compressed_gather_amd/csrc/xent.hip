@@ -653,32 +653,39 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T *src, int64_t ld_sr
     }
 }
 
-// lse and loss of sixteen rows per block from the tiles' maxima and sums.
-__global__ __launch_bounds__(256) void k_xent_join(const float2 *part, int64_t tiles, int64_t n, int64_t V,
-                                                   const int64_t *targets, int64_t ignore, const float *target_logit,
-                                                   float *loss, float *lse, int *status)
+// Two (maximum, sum of exponentials relative to it) as one.
+__device__ __forceinline__ float2 join_sums(float2 a, float2 b)
 {
-    __shared__ float2 sm[16][16];
+    const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
+    return make_float2(m, a.y * __expf(a.x - ref) + b.y * __expf(b.x - ref));
+}
+
+// lse and loss of sixteen rows per block from the tiles' maxima and sums, 64
+// groups of tiles joined in order.
+__global__ __launch_bounds__(1024) void k_xent_join(const float2 *part, int64_t tiles, int64_t n, int64_t V,
+                                                    const int64_t *targets, int64_t ignore, const float *target_logit,
+                                                    float *loss, float *lse, int *status)
+{
+    __shared__ float2 sm[64][16];
     const int r = threadIdx.x & 15, g = threadIdx.x >> 4;
     const int64_t i = (int64_t)blockIdx.x * 16 + r, ic = i < n ? i : n - 1;
-    float top = -INFINITY, sum = 0.f;
-    for (int64_t t = g; t < tiles; t += 16) {
-        const float2 p = part[t * n + ic];
-        const float m = fmaxf(top, p.x);
-        const float ref = m == -INFINITY ? 0.f : m;
-        sum = sum * __expf(top - ref) + p.y * __expf(p.x - ref);
-        top = m;
+    float2 all = make_float2(-INFINITY, 0.f);
+    for (int64_t t = g; t < tiles; t += 4 * 64) {
+        float2 p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            p[u] = part[(t + u * 64 < tiles ? t + u * 64 : t) * n + ic];
+            if (t + u * 64 >= tiles) p[u] = make_float2(-INFINITY, 0.f);
+        }
+        all = join_sums(all, join_sums(join_sums(p[0], p[1]), join_sums(p[2], p[3])));
     }
-    sm[r][g] = make_float2(top, sum);
+    sm[g][r] = all;
     __syncthreads();
     if (g || i >= n) return;
-    for (int q = 1; q < 16; ++q) {
-        const float2 p = sm[r][q];
-        const float m = fmaxf(top, p.x);
-        const float ref = m == -INFINITY ? 0.f : m;
-        sum = sum * __expf(top - ref) + p.y * __expf(p.x - ref);
-        top = m;
-    }
+    float top = -INFINITY, sum = 0.f;
+    for (int q = 0; q < 64; ++q) top = fmaxf(top, sm[q][r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int q = 0; q < 64; ++q) sum += sm[q][r].y * __expf(sm[q][r].x - ref);
     const float z = (top == -INFINITY ? 0.f : top) + logf(sum);
     const int64_t t = targets[i];
     const bool in = t >= 0 && t < V;
@@ -731,17 +738,35 @@ struct XentPlan {
     size_t bytes;
 };
 
-// Rows and columns of a product's tile, and how often dH's sum over a piece of
-// the vocabulary is split: its output is small (n x D) beside what it adds up,
-// so where its tiles are fewer than the compute units the sum is shared out.
-inline int64_t tile_side(int64_t size) { return size <= 128 ? 128 : 256; }
+// Side of a product's tiles.  256 x 256 tiles read each operand least often
+// (logits of 8192 x 16384, bf16: K = 4096 at 1254 TFLOP/s, against 1040 in tiles
+// of 128).  Tiles of 128, of which a compute unit holds two, hide the start and
+// the end of one behind the products of the other and win where those are long
+// beside the sum (K = 512: 806 against 599; equal at 1024), and take outputs
+// with a side of at most 128 and grids that would leave compute units idle.
+constexpr int64_t kShortSum = 512;
+inline int64_t tile_side(int64_t M, int64_t N, int64_t K, int splits, bool of_logits)
+{
+    if (M <= 128 || N <= 128 || (of_logits && K <= kShortSum)) return 128;
+    return ((M + 255) / 256) * ((N + 255) / 256) * splits < kCUs ? 128 : 256;
+}
+
+// How often dH's sum over a piece of the vocabulary is split: its output is
+// small (n x D) beside what it adds up, so where its tiles are fewer than the
+// compute units take at a time the sum is shared out.
 int hidden_splits(int64_t n, int64_t D, int64_t piece)
 {
-    const int64_t tm = tile_side(D), tn = tile_side(n);
-    const int64_t tiles = ((D + tm - 1) / tm) * ((n + tn - 1) / tn);
-    int64_t s = kCUs / tiles;
+    const bool small = n <= 128 || D <= 128;
+    const int64_t side = small ? 128 : 256, slots = small ? 2 * kCUs : kCUs;
+    int64_t s = slots / (((D + side - 1) / side) * ((n + side - 1) / side));
     if (s > piece / kSplitK) s = piece / kSplitK;
     return (int)(s < 1 ? 1 : s);
+}
+int64_t best_piece(int64_t n, int64_t V, int PL)
+{
+    int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * up(n, kRound) * 2)) / kRound * kRound;
+    if (c < 8 * kRound) c = 8 * kRound;
+    return up(V < c ? V : c, kRound);
 }
 
 // `piece` columns of d (0: forward only).  Packed copies of the operands are
@@ -776,13 +801,6 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     return p;
 }
 
-int64_t best_piece(int64_t n, int64_t V, int PL)
-{
-    int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * up(n, kRound) * 2)) / kRound * kRound;
-    if (c < 8 * kRound) c = 8 * kRound;
-    return up(V < c ? V : c, kRound);
-}
-
 template <class T, int PL>
 bool in_place(const T *src, int64_t ld, int64_t D, int64_t Kp)
 {
@@ -796,32 +814,18 @@ unsigned blocks_for(int64_t threads)
     return (unsigned)(b < 65536 ? b : 65536);
 }
 
-// A product with M contiguous outputs in each of N rows; returns the tiles
-// along M.  256 x 256 tiles read each operand least often; a side of at most
-// 128 takes half of that, and where the tiles would leave compute units idle
-// 128 x 128 ones spread the work further.
+// A product with M contiguous outputs in each of N rows; returns the tiles along M.
 template <int PL, bool XT, bool YT, int OUT>
 int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s)
 {
-    const int64_t tm = tile_side(M), tn = tile_side(N);
-    int64_t mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
     const int splits = OUT == OUT_HIDDEN ? o.splits : 1;
-    const bool small = mt * nt * splits < kCUs;
-    if (small) {
-        mt = (M + 127) / 128;
-        nt = (N + 127) / 128;
-    }
+    const int64_t side = tile_side(M, N, K, splits, OUT == OUT_STATS || OUT == OUT_D);
+    const int64_t mt = (M + side - 1) / side, nt = (N + side - 1) / side;
     const dim3 grid(tile_grid(mt, nt, splits));
-    auto go = [&](auto i, auto j) {
-        constexpr int NI = decltype(i)::value, NJ = decltype(j)::value;
-        hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, NI, NJ>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
-    };
-    const std::integral_constant<int, 2> two;
-    const std::integral_constant<int, 4> four;
-    if (!small && tm == 256 && tn == 256) go(four, four);
-    else if (!small && tm == 256) go(four, two);
-    else if (!small && tn == 256) go(two, four);
-    else go(two, two);
+    if (side == 256)
+        hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, 4, 4>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
+    else
+        hipLaunchKernelGGL((k_product<PL, XT, YT, OUT, 2, 2>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
     return mt;
 }
 
@@ -870,7 +874,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.plane_d = p.nr * piece;
     o.sum = p.sum;
     const int64_t tiles = product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
-    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(256), 0, s, p.part, tiles, a.n, a.V,
+    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(1024), 0, s, p.part, tiles, a.n, a.V,
                        a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
     if (!grad) return hipGetLastError();
     hipLaunchKernelGGL(k_xent_top_grad, dim3(1), dim3(1024), 0, s, a.grad_loss, a.targets, a.ignore, a.n, a.V,
