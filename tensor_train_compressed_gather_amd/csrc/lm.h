@@ -6,6 +6,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/tt_emb.h"
 
@@ -65,13 +66,49 @@ __device__ __forceinline__ void store_part(T *p, int left, const float (&x)[N])
         if (i < left) p[i] = (T)x[i];
 }
 
-// Parameter j of an array whose type is known at run time (read once per block).
-__device__ __forceinline__ float load_param(const void *p, int dtype, int64_t j, float none)
+// Vector at column c of a row of D elements, zero past its end, still in its
+// own type.  WHOLE: D is a multiple of N, so a vector is inside or outside; it
+// is then read without a condition (from the row's start where it is outside),
+// because a load under a condition is waited for before the next one is issued.
+template <class T, int N, bool WHOLE>
+__device__ __forceinline__ typename VecOf<T, N>::raw load_row(const T *row, int64_t c, int64_t D)
 {
-    if (!p) return none;
-    if (dtype == TT_EMB_DTYPE_FLOAT) return static_cast<const float *>(p)[j];
-    if (dtype == TT_EMB_DTYPE_BFLOAT) return (float)static_cast<const bf16 *>(p)[j];
-    return (float)static_cast<const f16 *>(p)[j];
+    typedef typename VecOf<T, N>::type vec;
+    typename VecOf<T, N>::raw v;
+    if constexpr (WHOLE) {
+        v = *reinterpret_cast<const vec *>(row + (c < D ? c : 0));
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = c < D ? v[i] : (T)0.f;
+    } else if (c + N <= D) {
+        v = *reinterpret_cast<const vec *>(row + c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = c + i < D ? row[c + i] : (T)0.f;
+    }
+    return v;
+}
+
+// Columns c .. c + N - 1 of a parameter row whose type is known at run time:
+// `none` where there is no array, 0 past the row's end.
+template <int N, bool WHOLE>
+__device__ __forceinline__ void load_params(const void *p, int dtype, int64_t c, int64_t D, float none, float (&x)[N])
+{
+    auto take = [&](auto *q) {
+        typedef std::remove_const_t<std::remove_pointer_t<decltype(q)>> T;
+        const typename VecOf<T, N>::raw v = load_row<T, N, WHOLE>(q, c, D);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = (float)v[i];
+    };
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = c + i < D ? none : 0.f;
+    } else if (dtype == TT_EMB_DTYPE_FLOAT) {
+        take(static_cast<const float *>(p));
+    } else if (dtype == TT_EMB_DTYPE_BFLOAT) {
+        take(static_cast<const bf16 *>(p));
+    } else {
+        take(static_cast<const f16 *>(p));
+    }
 }
 __device__ __forceinline__ void store_param(void *p, int dtype, int64_t j, float x)
 {

@@ -12,8 +12,8 @@ namespace ttemb {
 
 namespace {
 
-constexpr int kNormMaxBlocks = 2048;   // forward: 8 blocks of 256 threads per CU
-constexpr int kNormGradBlocks = 1024;  // backward: rows of partial column sums (at most)
+constexpr int kNormBlocks = 5 * kCUs;      // forward: blocks at most, all of them resident
+constexpr int kNormGradBlocks = 4 * kCUs;  // backward: rows of partial column sums, at most
 
 template <int TPR>
 struct NormShape {
@@ -49,39 +49,45 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*sm)[16][2], int &
     }
 }
 
-template <class T, int TPR, int NV>
+// The next row is on its way while this one is reduced.
+template <class T, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_fwd(NormArgs a)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
     __shared__ float sm[2][16][2];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int D = (int)a.D;
+    const int64_t step = (int64_t)gridDim.x * NormShape<TPR>::rows, last = a.n - 1;
+    int64_t r0 = (int64_t)blockIdx.x * NormShape<TPR>::rows;
+    typename VecOf<T, VEC>::raw next[NV];
+    auto load = [&](int64_t row) {
+        const T *x = static_cast<const T *>(a.x) + (row < a.n ? row : last) * a.ld_x;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) next[j] = load_row<T, VEC, WHOLE>(x, (t + j * TPR) * VEC, D);
+    };
+    load(r0 + sub);
     float gam[NV][VEC], bet[NV][VEC];
     int left[NV]; // elements of each vector that exist
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (t + j * TPR) * VEC;
         left[j] = D - c;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            gam[j][i] = c + i < D ? load_param(a.gamma, a.param_dtype, c + i, 1.f) : 0.f;
-            bet[j][i] = c + i < D ? load_param(a.beta, a.param_dtype, c + i, 0.f) : 0.f;
-        }
+        load_params<VEC, WHOLE>(a.gamma, a.param_dtype, c, D, 1.f, gam[j]);
+        load_params<VEC, WHOLE>(a.beta, a.param_dtype, c, D, 0.f, bet[j]);
     }
     int slot = 0;
-    const int64_t step = (int64_t)gridDim.x * NormShape<TPR>::rows;
-    for (int64_t r0 = (int64_t)blockIdx.x * NormShape<TPR>::rows; r0 < a.n; r0 += step) {
-        const bool live = r0 + sub < a.n;
-        const int64_t r = live ? r0 + sub : a.n - 1;
-        const T *x = static_cast<const T *>(a.x) + r * a.ld_x;
+    for (; r0 < a.n; r0 += step) {
+        const int64_t r = r0 + sub;
         float v[NV][VEC];
         float s[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j) load_part<T, VEC>(x + (t + j * TPR) * VEC, left[j], v[j]);
-#pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) s[0] += v[j][i];
+            for (int i = 0; i < VEC; ++i) {
+                v[j][i] = (float)next[j][i];
+                s[0] += v[j][i];
+            }
+        load(r + step);
         row_sum<TPR, 1>(s, sm, slot);
         // a division, so that a row of equal values has their exact mean
         const float mean0 = s[0] / (float)D;
@@ -99,7 +105,7 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_fwd(NormArgs a
         // offset is large beside its spread
         const float slip = q[0] / (float)D, mean = mean0 + slip;
         const float rstd = 1.f / sqrtf(fmaxf(fmaf(-slip, slip, q[1] / (float)D), 0.f) + a.eps);
-        if (!live) continue;
+        if (r >= a.n) continue;
         T *y = static_cast<T *>(a.y) + r * a.ld_y;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -117,46 +123,79 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_fwd(NormArgs a
 
 // Gradients of a block's rows; the block's sums over its rows of dy xhat and
 // dy go to part[0][block][D] and part[1][block][D].
-template <class T, int TPR, int NV>
+template <class T, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_bwd(NormArgs a, float *part)
 {
     constexpr int VEC = 16 / (int)sizeof(T);
+    // sixteen waves have 128 registers each: with 16 elements per thread
+    // nothing is loaded ahead and the column sums live in LDS
+    constexpr bool LEAN = TPR == 1024 && NV * VEC == 16;
+    __shared__ float col_sums[LEAN ? 2 * NV * VEC : 1][LEAN ? 1024 : 1];
     __shared__ float sm[2][16][2];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int D = (int)a.D;
     const float invD = 1.f / (float)D;
+    const int64_t step = (int64_t)gridDim.x * NormShape<TPR>::rows, last = a.n - 1;
+    int64_t r0 = (int64_t)blockIdx.x * NormShape<TPR>::rows;
+    typename VecOf<T, VEC>::raw nx[NV], ng[NV];
+    float nmean, nrstd;
+    auto load = [&](int64_t row) {
+        const int64_t r = row < a.n ? row : last;
+        const T *x = static_cast<const T *>(a.x) + r * a.ld_x, *dy = static_cast<const T *>(a.dy) + r * a.ld_dy;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            nx[j] = load_row<T, VEC, WHOLE>(x, (t + j * TPR) * VEC, D);
+            ng[j] = load_row<T, VEC, WHOLE>(dy, (t + j * TPR) * VEC, D);
+        }
+        nmean = a.mean[r];
+        nrstd = a.rstd[r];
+    };
+    if constexpr (!LEAN) load(r0 + sub);
     float gam[NV][VEC], sg[NV][VEC], sb[NV][VEC];
     int left[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (t + j * TPR) * VEC;
         left[j] = D - c;
+        load_params<VEC, WHOLE>(a.gamma, a.param_dtype, c, D, 1.f, gam[j]);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            gam[j][i] = c + i < D ? load_param(a.gamma, a.param_dtype, c + i, 1.f) : 0.f;
-            sg[j][i] = sb[j][i] = 0.f;
+            if constexpr (LEAN) {
+                col_sums[2 * (j * VEC + i)][threadIdx.x] = 0.f;
+                col_sums[2 * (j * VEC + i) + 1][threadIdx.x] = 0.f;
+            } else {
+                sg[j][i] = sb[j][i] = 0.f;
+            }
         }
     }
     int slot = 0;
-    const int64_t step = (int64_t)gridDim.x * NormShape<TPR>::rows;
-    for (int64_t r0 = (int64_t)blockIdx.x * NormShape<TPR>::rows; r0 < a.n; r0 += step) {
-        const bool live = r0 + sub < a.n;
-        const int64_t r = live ? r0 + sub : a.n - 1;
-        const T *x = static_cast<const T *>(a.x) + r * a.ld_x, *dy = static_cast<const T *>(a.dy) + r * a.ld_dy;
+    for (; r0 < a.n; r0 += step) {
+        const int64_t r = r0 + sub;
+        const bool live = r < a.n;
+        if constexpr (LEAN) load(r);
+        const float mean = nmean, rstd = nrstd;
         float xh[NV][VEC], g[NV][VEC];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            load_part<T, VEC>(x + (t + j * TPR) * VEC, left[j], xh[j]);
-            load_part<T, VEC>(dy + (t + j * TPR) * VEC, left[j], g[j]);
-        }
-        const float mean = a.mean[r], rstd = a.rstd[r];
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                xh[j][i] = (float)nx[j][i];
+                g[j][i] = (float)ng[j][i];
+            }
+        if constexpr (!LEAN) load(r + step);
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 xh[j][i] = (xh[j][i] - mean) * rstd;
-                if (live && i < left[j]) {
+                if constexpr (LEAN) {
+                    if (i < left[j]) {
+                        float *c = &col_sums[2 * (j * VEC + i)][threadIdx.x];
+                        c[0] = fmaf(g[j][i], xh[j][i], c[0]);
+                        c[1024] += g[j][i];
+                    }
+                } else if (live && i < left[j]) {
                     sg[j][i] = fmaf(g[j][i], xh[j][i], sg[j][i]);
                     sb[j][i] += g[j][i];
                 }
@@ -177,6 +216,15 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_bwd(NormArgs a
         }
     }
     if (!part) return;
+    if constexpr (LEAN) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                sg[j][i] = col_sums[2 * (j * VEC + i)][threadIdx.x];
+                sb[j][i] = col_sums[2 * (j * VEC + i) + 1][threadIdx.x];
+            }
+    }
     // the block's sums: sub-rows of one wave by shuffles, the waves through LDS
     if constexpr (NormShape<TPR>::rows > 1) {
         constexpr int W = TPR < 64 ? TPR : 64, COLS = TPR * NV * VEC, WAVES = NormShape<TPR>::threads / 64;
@@ -242,8 +290,12 @@ __global__ __launch_bounds__(1024) void k_norm_cols(const float *part, int block
 // Threads per row and vectors per thread: the fewest threads that hold a row
 // of nv vectors with at most 16 elements each (80 registers in the backward).
 template <class T, class F>
-hipError_t norm_shape(int64_t D, F &&f)
+hipError_t norm_shape(int64_t D, F &&g)
 {
+    auto f = [&](auto tpr, auto nv) {
+        if (D % (16 / (int)sizeof(T)) == 0) return g(tpr, nv, std::true_type());
+        return g(tpr, nv, std::false_type());
+    };
     constexpr int VEC = 16 / (int)sizeof(T), MAX = 16 / VEC;
     const int64_t nv = (D + VEC - 1) / VEC;
     auto one = [&](auto tpr) {
@@ -264,11 +316,11 @@ hipError_t norm_shape(int64_t D, F &&f)
 template <class T>
 hipError_t norm_forward(const NormArgs &a, hipStream_t s)
 {
-    return norm_shape<T>(a.D, [&](auto tpr, auto nv) {
+    return norm_shape<T>(a.D, [&](auto tpr, auto nv, auto whole) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
         const int64_t need = (a.n + NormShape<TPR>::rows - 1) / NormShape<TPR>::rows;
-        const int grid = (int)(need < kNormMaxBlocks ? need : kNormMaxBlocks);
-        hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a);
+        const int grid = (int)(need < kNormBlocks ? need : kNormBlocks);
+        hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, decltype(whole)::value>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a);
         return hipGetLastError();
     });
 }
@@ -276,12 +328,12 @@ hipError_t norm_forward(const NormArgs &a, hipStream_t s)
 template <class T>
 hipError_t norm_backward(const NormArgs &a, hipStream_t s)
 {
-    return norm_shape<T>(a.D, [&](auto tpr, auto nv) {
+    return norm_shape<T>(a.D, [&](auto tpr, auto nv, auto whole) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
         const int64_t need = (a.n + NormShape<TPR>::rows - 1) / NormShape<TPR>::rows;
         const int grid = (int)(need < kNormGradBlocks ? need : kNormGradBlocks);
         float *part = (a.dgamma || a.dbeta) ? reinterpret_cast<float *>(a.ws + TT_EMB_STATUS_BYTES) : nullptr;
-        hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a, part);
+        hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV, decltype(whole)::value>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a, part);
         if (part)
             hipLaunchKernelGGL(k_norm_cols, dim3((unsigned)((a.D + 63) / 64), 2), dim3(1024), 0, s, part, grid,
                                (int)a.D, a.dgamma, a.dbeta, a.param_dtype);

@@ -44,21 +44,36 @@ def declare(L):
     L.tt_emb_adamw_state_size.argtypes = [i32, p, C.POINTER(i64)]
 
 
-def _package():
-    from . import TTEmbError, _check, lib
+torch = None       # imported with the first operator: the package itself does without
+_L = _check = None  # the loaded library, the status check
+_raw_stream = None
+_DTYPES = {}
 
-    return TTEmbError, _check, lib()
+
+def _bind():
+    """Import torch, load the library (once)."""
+    global torch, _L, _check, _raw_stream
+    if _L is None:
+        import torch as t
+
+        from . import _check as check, lib
+
+        torch, _check = t, check
+        _DTYPES.update({t.float32: 0, t.bfloat16: 1, t.float16: 2})
+        # the current stream's handle without a Stream object around it
+        _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: t.cuda.current_stream(index).cuda_stream)
+        _L = lib()
 
 
-def _bad(where: str, what: str):
-    TTEmbError, _, _ = _package()
-    return TTEmbError(-1, f"{where}: {what}")
+def _bad(where: str, what: str, status: int = -1):
+    from . import TTEmbError
+
+    return TTEmbError(status, f"{where}: {what}")
 
 
 def _dtype(t, where: str, name: str) -> int:
-    import torch
-
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise _bad(where, f"{name}: dtype {t.dtype}, expected float32, bfloat16 or float16")
     return code
@@ -66,33 +81,34 @@ def _dtype(t, where: str, name: str) -> int:
 
 def _matrix(t, where: str, name: str, cols: int, rows: int | None = None, dtype=None, device=None):
     """Check a [rows][cols] argument and return the distance of its rows."""
-    import torch
-
-    if not torch.is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise _bad(where, f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise _bad(where, f"{name}: shape {tuple(t.shape)}, expected [{'n' if rows is None else rows}, {cols}]")
-    if dtype is not None and t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise _bad(where, f"{name}: shape {tuple(shape)}, expected [{'n' if rows is None else rows}, {cols}]")
+    if dtype is not None and t.dtype is not dtype:
         raise _bad(where, f"{name}: dtype {t.dtype}, expected {dtype}")
-    ld = t.stride(0) if t.shape[0] > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
-        raise _bad(where, f"{name}: strides {t.stride()}, expected contiguous rows that do not overlap")
-    _on(t, where, name, device)
+    strides = t.stride()
+    ld = strides[0] if shape[0] > 1 else cols
+    if (cols > 1 and strides[1] != 1) or ld < cols:
+        raise _bad(where, f"{name}: strides {strides}, expected contiguous rows that do not overlap")
+    if not t.is_cuda or (device is not None and t.device != device):
+        _on(t, where, name, device)
     return ld
 
 
 def _vector(t, where: str, name: str, length: int, dtypes, device=None):
-    import torch
-
-    if not torch.is_tensor(t):
+    if not isinstance(t, torch.Tensor):
         raise _bad(where, f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dim() != 1 or t.shape[0] != length:
-        raise _bad(where, f"{name}: shape {tuple(t.shape)}, expected [{length}]")
+    shape = t.shape
+    if len(shape) != 1 or shape[0] != length:
+        raise _bad(where, f"{name}: shape {tuple(shape)}, expected [{length}]")
     if t.dtype not in dtypes:
         raise _bad(where, f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if length > 1 and t.stride(0) != 1:
         raise _bad(where, f"{name}: not contiguous")
-    _on(t, where, name, device)
+    if not t.is_cuda or (device is not None and t.device != device):
+        _on(t, where, name, device)
 
 
 def _on(t, where: str, name: str, device):
@@ -102,35 +118,18 @@ def _on(t, where: str, name: str, device):
         raise _bad(where, f"{name}: on {t.device}, expected {device} like the others")
 
 
-class _Streams:
-    """The stream of one call: the device of its tensors made current, outputs
-    allocated on the stream that writes them."""
-
-    def __init__(self, device, stream):
-        import torch
-
-        if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-            self.stream = None
-        else:
-            self.stream = (torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int)
-                           else stream)
-            self.handle = self.stream.cuda_stream
-        self.guard = None
-        if self.stream is not None:
-            self.guard = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            return self.guard.__exit__(*exc)
-        return None
+def _guard(device, stream, where: str):
+    """What has to be entered before a call's work is enqueued: nothing where
+    it goes to the current stream of the current device, else the given
+    stream (a torch stream or a handle) or the tensors' device.  Outputs and
+    workspaces then belong to the stream that writes them."""
+    if stream is None:
+        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise _bad(where, f"stream: of {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
 class _Operator:
@@ -138,14 +137,11 @@ class _Operator:
     (device, stream), whose status words are zero from the start."""
 
     def __init__(self, device):
-        import torch
-
+        _bind()
         self.device = torch.device(device)
         self._ws = {}
 
     def _workspace(self, device, handle: int, need: int):
-        import torch
-
         key = (device.index, handle)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
@@ -161,21 +157,17 @@ class _Operator:
     def poll_error(self) -> int:
         """Synchronises; the first device-detected error of any stream's
         calls since the last poll (0 = ok), cleared by reading it."""
-        import torch
-
-        _, _, L = _package()
         rc = 0
         for (index, handle), ws in self._ws.items():
             with torch.cuda.device(index):
-                got = int(L.tt_emb_poll_status(ws.data_ptr(), handle))
+                got = int(_L.tt_emb_poll_status(ws.data_ptr(), handle))
             rc = rc or got
         return rc
 
 
 def _size(fn, where: str, *args) -> int:
-    _, check, _ = _package()
     out = C.c_size_t()
-    check(fn(*args, C.byref(out)), where)
+    _check(fn(*args, C.byref(out)), where)
     return int(out.value)
 
 
@@ -191,46 +183,43 @@ class TokenEmbedding(_Operator):
     def __init__(self, V: int, D: int, scale: float = 1.0, padding_idx: int = -1, device="cuda"):
         super().__init__(device)
         self.V, self.D, self.scale, self.padding_idx = int(V), int(D), float(scale), int(padding_idx)
-        _size(_package()[2].tt_emb_lookup_workspace_size, "TokenEmbedding", 0, self.V, self.D)
+        _size(_L.tt_emb_lookup_workspace_size, "TokenEmbedding", 0, self.V, self.D)
 
     def _tokens(self, tokens, where, device):
-        import torch
-
-        if not torch.is_tensor(tokens) or tokens.dtype != torch.int64:
+        if not isinstance(tokens, torch.Tensor) or tokens.dtype is not torch.int64:
             raise _bad(where, "tokens: expected an int64 tensor")
         if not tokens.is_contiguous():
             raise _bad(where, "tokens: not contiguous")
-        _on(tokens, where, "tokens", device)
+        if tokens.device != device:
+            _on(tokens, where, "tokens", device)
         return tokens.numel()
 
     def forward(self, weight, tokens, out=None, stream=None):
-        import torch
-
         where = "TokenEmbedding.forward"
-        _, check, L = _package()
         ld_w = _matrix(weight, where, "weight", self.D, self.V)
         dt = _dtype(weight, where, "weight")
         device = weight.device
         n = self._tokens(tokens, where, device)
-        with _Streams(device, stream) as s:
-            shape = None
-            if out is None:
-                out = torch.empty((n, self.D), dtype=weight.dtype, device=device)
-                shape = (*tokens.shape, self.D)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.forward(weight, tokens, out)
+        s = _raw_stream(device.index)
+        made = out is None
+        if made:
+            out, ld_o = torch.empty((n, self.D), dtype=weight.dtype, device=device), self.D
+        else:
             ld_o = _matrix(out, where, "out", self.D, n, weight.dtype, device)
-            ws = self._workspace(device, s, TT_EMB_STATUS_BYTES)
-            check(L.tt_emb_lookup_forward(weight.data_ptr(), ld_w, tokens.data_ptr(), n, self.V, self.D, dt,
-                                          self.scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel(), s), where)
-        return out if shape is None or len(shape) == 2 else out.view(shape)
+        ws = self._workspace(device, s, TT_EMB_STATUS_BYTES)
+        _check(_L.tt_emb_lookup_forward(weight.data_ptr(), ld_w, tokens.data_ptr(), n, self.V, self.D, dt,
+                                      self.scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel(), s), where)
+        return out.view(*tokens.shape, self.D) if made and tokens.dim() != 1 else out
 
     def backward(self, grad_out, tokens, grad_weight=None, accumulate: bool = False, stream=None):
-        import torch
-
         where = "TokenEmbedding.backward"
-        _, check, L = _package()
         if torch.is_tensor(grad_out) and grad_out.dim() > 2:
-            if grad_out.shape[:-1] != tokens.shape:
-                raise _bad(where, f"grad_out: shape {tuple(grad_out.shape)}, tokens {tuple(tokens.shape)}")
+            if grad_out.shape[:-1] != getattr(tokens, "shape", None):
+                raise _bad(where, f"grad_out: shape {tuple(grad_out.shape)}, not that of tokens and {self.D}")
             grad_out = grad_out.view(-1, grad_out.shape[-1])
         ld_g = _matrix(grad_out, where, "grad_out", self.D)
         dt = _dtype(grad_out, where, "grad_out")
@@ -240,15 +229,19 @@ class TokenEmbedding(_Operator):
             raise _bad(where, f"grad_out: {grad_out.shape[0]} rows for {n} tokens")
         if grad_weight is None and accumulate:
             raise _bad(where, "accumulate needs grad_weight")
-        need = _size(L.tt_emb_lookup_workspace_size, where, n, self.V, self.D)
-        with _Streams(device, stream) as s:
-            if grad_weight is None:
-                grad_weight = torch.empty((self.V, self.D), dtype=grad_out.dtype, device=device)
-            ld_w = _matrix(grad_weight, where, "grad_weight", self.D, self.V, grad_out.dtype, device)
-            ws = self._workspace(device, s, need)
-            check(L.tt_emb_lookup_backward(grad_out.data_ptr(), ld_g, tokens.data_ptr(), n, self.V, self.D, dt,
-                                           self.scale, self.padding_idx, 1 if accumulate else 0,
-                                           grad_weight.data_ptr(), ld_w, ws.data_ptr(), ws.numel(), s), where)
+        need = _size(_L.tt_emb_lookup_workspace_size, where, n, self.V, self.D)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.backward(grad_out, tokens, grad_weight, accumulate)
+        s = _raw_stream(device.index)
+        if grad_weight is None:
+            grad_weight = torch.empty((self.V, self.D), dtype=grad_out.dtype, device=device)
+        ld_w = _matrix(grad_weight, where, "grad_weight", self.D, self.V, grad_out.dtype, device)
+        ws = self._workspace(device, s, need)
+        _check(_L.tt_emb_lookup_backward(grad_out.data_ptr(), ld_g, tokens.data_ptr(), n, self.V, self.D, dt,
+                                       self.scale, self.padding_idx, 1 if accumulate else 0,
+                                       grad_weight.data_ptr(), ld_w, ws.data_ptr(), ws.numel(), s), where)
         return grad_weight
 
 
@@ -263,19 +256,14 @@ class LayerNorm(_Operator):
     def __init__(self, D: int, eps: float = 1e-5, device="cuda"):
         super().__init__(device)
         self.D, self.eps = int(D), float(eps)
-        _size(_package()[2].tt_emb_norm_workspace_size, "LayerNorm", 0, self.D)
+        _size(_L.tt_emb_norm_workspace_size, "LayerNorm", 0, self.D)
 
     def _param(self, p, name, where, x):
-        import torch
-
         if p is not None:
             _vector(p, where, name, self.D, (torch.float32, x.dtype), x.device)
 
     def forward(self, x, gamma=None, beta=None, out=None, stream=None):
-        import torch
-
         where = "LayerNorm.forward"
-        _, check, L = _package()
         ld_x = _matrix(x, where, "x", self.D)
         dt = _dtype(x, where, "x")
         n, device = x.shape[0], x.device
@@ -285,23 +273,25 @@ class LayerNorm(_Operator):
             raise _bad(where, f"beta: dtype {beta.dtype}, expected {gamma.dtype} like gamma")
         param = gamma if gamma is not None else beta
         pdt = 0 if param is None else _dtype(param, where, "gamma")
-        with _Streams(device, stream) as s:
-            if out is None:
-                out = torch.empty((n, self.D), dtype=x.dtype, device=device)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.forward(x, gamma, beta, out)
+        s = _raw_stream(device.index)
+        if out is None:
+            out, ld_y = torch.empty((n, self.D), dtype=x.dtype, device=device), self.D
+        else:
             ld_y = _matrix(out, where, "out", self.D, n, x.dtype, device)
-            stats = torch.empty((2, n), dtype=torch.float32, device=device)
-            mean, rstd = stats[0], stats[1]
-            check(L.tt_emb_norm_forward(x.data_ptr(), ld_x, n, self.D, dt,
-                                        None if gamma is None else gamma.data_ptr(),
-                                        None if beta is None else beta.data_ptr(), pdt, self.eps, out.data_ptr(),
-                                        ld_y, mean.data_ptr(), rstd.data_ptr(), s), where)
+        stats = torch.empty((2, n), dtype=torch.float32, device=device)
+        mean, rstd = stats.unbind(0)
+        _check(_L.tt_emb_norm_forward(x.data_ptr(), ld_x, n, self.D, dt,
+                                    None if gamma is None else gamma.data_ptr(),
+                                    None if beta is None else beta.data_ptr(), pdt, self.eps, out.data_ptr(),
+                                    ld_y, mean.data_ptr(), rstd.data_ptr(), s), where)
         return out, mean, rstd
 
     def backward(self, grad_y, x, gamma, mean, rstd, stream=None):
-        import torch
-
         where = "LayerNorm.backward"
-        _, check, L = _package()
         ld_x = _matrix(x, where, "x", self.D)
         dt = _dtype(x, where, "x")
         n, device = x.shape[0], x.device
@@ -310,16 +300,20 @@ class LayerNorm(_Operator):
         pdt = 0 if gamma is None else _dtype(gamma, where, "gamma")
         _vector(mean, where, "mean", n, (torch.float32,), device)
         _vector(rstd, where, "rstd", n, (torch.float32,), device)
-        need = _size(L.tt_emb_norm_workspace_size, where, n, self.D)
-        with _Streams(device, stream) as s:
-            dx = torch.empty((n, self.D), dtype=x.dtype, device=device)
-            sums = torch.empty((2, self.D), dtype=torch.float32 if gamma is None else gamma.dtype, device=device)
-            dgamma, dbeta = sums[0], sums[1]
-            ws = self._workspace(device, s, need)
-            check(L.tt_emb_norm_backward(grad_y.data_ptr(), ld_g, x.data_ptr(), ld_x, n, self.D, dt,
-                                         None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(),
-                                         rstd.data_ptr(), dx.data_ptr(), self.D, dgamma.data_ptr(),
-                                         dbeta.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
+        need = _size(_L.tt_emb_norm_workspace_size, where, n, self.D)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.backward(grad_y, x, gamma, mean, rstd)
+        s = _raw_stream(device.index)
+        dx = torch.empty((n, self.D), dtype=x.dtype, device=device)
+        sums = torch.empty((2, self.D), dtype=torch.float32 if gamma is None else gamma.dtype, device=device)
+        dgamma, dbeta = sums.unbind(0)
+        ws = self._workspace(device, s, need)
+        _check(_L.tt_emb_norm_backward(grad_y.data_ptr(), ld_g, x.data_ptr(), ld_x, n, self.D, dt,
+                                     None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(),
+                                     rstd.data_ptr(), dx.data_ptr(), self.D, dgamma.data_ptr(),
+                                     dbeta.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
         return dx, dgamma, dbeta
 
 
@@ -341,19 +335,16 @@ class VocabCrossEntropy(_Operator):
         self._need(0, 0, False, "VocabCrossEntropy")
 
     def _need(self, n: int, dt: int, grad: bool, where: str) -> int:
-        _, check, L = _package()
         best, least = C.c_size_t(), C.c_size_t()
-        check(L.tt_emb_xent_workspace_size(n, self.V, self.D, dt, 1 if grad else 0, C.byref(best), C.byref(least)),
+        _check(_L.tt_emb_xent_workspace_size(n, self.V, self.D, dt, 1 if grad else 0, C.byref(best), C.byref(least)),
               where)
         if self.max_workspace is None or not grad:
             return int(best.value)
         if self.max_workspace < least.value:
-            raise _package()[0](-3, f"{where}: max_workspace {self.max_workspace}, at least {least.value} needed")
+            raise _bad(where, f"max_workspace {self.max_workspace}, at least {least.value} needed", -3)
         return min(int(best.value), self.max_workspace)
 
     def _inputs(self, hidden, weight, targets, where):
-        import torch
-
         ld_h = _matrix(hidden, where, "hidden", self.D)
         dt = _dtype(hidden, where, "hidden")
         n, device = hidden.shape[0], hidden.device
@@ -362,40 +353,42 @@ class VocabCrossEntropy(_Operator):
         return ld_h, ld_w, dt, n, device
 
     def forward(self, hidden, weight, targets, stream=None):
-        import torch
-
         where = "VocabCrossEntropy.forward"
-        _, check, L = _package()
         ld_h, ld_w, dt, n, device = self._inputs(hidden, weight, targets, where)
         need = self._need(n, dt, False, where)
-        with _Streams(device, stream) as s:
-            rows = torch.empty((2, n), dtype=torch.float32, device=device)
-            ws = self._workspace(device, s, need)
-            check(L.tt_emb_xent_forward(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(), n,
-                                        self.V, self.D, dt, self.ignore_index, rows[0].data_ptr(),
-                                        rows[1].data_ptr(), ws.data_ptr(), ws.numel(), s), where)
-        return rows[0], rows[1]
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.forward(hidden, weight, targets)
+        s = _raw_stream(device.index)
+        loss, lse = torch.empty((2, n), dtype=torch.float32, device=device).unbind(0)
+        ws = self._workspace(device, s, need)
+        _check(_L.tt_emb_xent_forward(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(), n,
+                                    self.V, self.D, dt, self.ignore_index, loss.data_ptr(),
+                                    lse.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
+        return loss, lse
 
     def loss_and_grad(self, hidden, weight, targets, grad_loss, grad_weight=None, stream=None):
-        import torch
-
         where = "VocabCrossEntropy.loss_and_grad"
-        _, check, L = _package()
         ld_h, ld_w, dt, n, device = self._inputs(hidden, weight, targets, where)
         _vector(grad_loss, where, "grad_loss", n, (torch.float32,), device)
         need = self._need(n, dt, True, where)
-        with _Streams(device, stream) as s:
-            rows = torch.empty((2, n), dtype=torch.float32, device=device)
-            dh = torch.empty((n, self.D), dtype=hidden.dtype, device=device)
-            if grad_weight is None:
-                grad_weight = torch.empty((self.V, self.D), dtype=hidden.dtype, device=device)
-            ld_dw = _matrix(grad_weight, where, "grad_weight", self.D, self.V, hidden.dtype, device)
-            ws = self._workspace(device, s, need)
-            check(L.tt_emb_xent_loss_grad(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(),
-                                          grad_loss.data_ptr(), n, self.V, self.D, dt, self.ignore_index,
-                                          rows[0].data_ptr(), rows[1].data_ptr(), dh.data_ptr(), self.D,
-                                          grad_weight.data_ptr(), ld_dw, ws.data_ptr(), ws.numel(), s), where)
-        return rows[0], rows[1], dh, grad_weight
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.loss_and_grad(hidden, weight, targets, grad_loss, grad_weight)
+        s = _raw_stream(device.index)
+        loss, lse = torch.empty((2, n), dtype=torch.float32, device=device).unbind(0)
+        dh = torch.empty((n, self.D), dtype=hidden.dtype, device=device)
+        if grad_weight is None:
+            grad_weight = torch.empty((self.V, self.D), dtype=hidden.dtype, device=device)
+        ld_dw = _matrix(grad_weight, where, "grad_weight", self.D, self.V, hidden.dtype, device)
+        ws = self._workspace(device, s, need)
+        _check(_L.tt_emb_xent_loss_grad(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(),
+                                      grad_loss.data_ptr(), n, self.V, self.D, dt, self.ignore_index,
+                                      loss.data_ptr(), lse.data_ptr(), dh.data_ptr(), self.D,
+                                      grad_weight.data_ptr(), ld_dw, ws.data_ptr(), ws.numel(), s), where)
+        return loss, lse, dh, grad_weight
 
 
 class AdamW:
@@ -412,8 +405,7 @@ class AdamW:
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  state_bits: int = 32, copies=None, seed: int = 0):
-        import torch
-
+        _bind()
         where = "AdamW"
         self.params = list(params)
         if not self.params:
@@ -436,8 +428,7 @@ class AdamW:
         self._numel = (C.c_int64 * n)(*[p.numel() for p in self.params])
         self._shapes = [p.shape for p in self.params]
         total = C.c_int64()
-        _, check, L = _package()
-        check(L.tt_emb_adamw_state_size(n, self._numel, C.byref(total)), where)
+        _check(_L.tt_emb_adamw_state_size(n, self._numel, C.byref(total)), where)
         length = int(total.value)
         kinds = (torch.float32, torch.float32) if state_bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
         size = 4 if state_bits == 32 else 1
@@ -450,8 +441,6 @@ class AdamW:
 
     @staticmethod
     def _tensor(t, name, dtype, shape, device):
-        import torch
-
         where = "AdamW"
         if not torch.is_tensor(t):
             raise _bad(where, f"{name}: expected a torch tensor, got {type(t).__name__}")
@@ -485,11 +474,12 @@ class AdamW:
         """One update from gradients shaped like the parameters (all of one
         type: fp32, bf16 or fp16)."""
         where = "AdamW.step"
-        _, check, L = _package()
         grads = list(grads)
         n = len(self.params)
         if len(grads) != n:
             raise _bad(where, f"{len(grads)} gradients for {n} parameters")
+        if not all(isinstance(g, torch.Tensor) for g in grads):
+            raise _bad(where, "grads: expected torch tensors")
         first = grads[0].dtype
         for i, (g, shape) in enumerate(zip(grads, self._shapes)):
             if g.dtype is not first or g.shape != shape or not g.is_contiguous() or g.device != self.device:
@@ -500,11 +490,15 @@ class AdamW:
         params = array(*[p.data_ptr() for p in self.params])
         pointers = array(*[g.data_ptr() for g in grads])
         copies = None if self.copies is None else array(*[c.data_ptr() for c in self.copies])
-        with _Streams(self.device, stream) as s:
-            check(L.tt_emb_adamw_update(
-                n, params, pointers, dt, copies, self._numel, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
-                None if self.exp_avg_scale is None else self.exp_avg_scale.data_ptr(),
-                None if self.exp_avg_sq_scale is None else self.exp_avg_sq_scale.data_ptr(), self.state_bits,
-                self.lr if lr is None else float(lr), self.betas[0], self.betas[1], self.eps, self.weight_decay,
-                self.steps + 1, self.seed & 0xFFFFFFFFFFFFFFFF, s), where)
+        guard = _guard(self.device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.step(grads, lr)
+        s = _raw_stream(self.device.index)
+        _check(_L.tt_emb_adamw_update(
+            n, params, pointers, dt, copies, self._numel, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
+            None if self.exp_avg_scale is None else self.exp_avg_scale.data_ptr(),
+            None if self.exp_avg_sq_scale is None else self.exp_avg_sq_scale.data_ptr(), self.state_bits,
+            self.lr if lr is None else float(lr), self.betas[0], self.betas[1], self.eps, self.weight_decay,
+            self.steps + 1, self.seed & 0xFFFFFFFFFFFFFFFF, s), where)
         self.steps += 1

@@ -100,6 +100,45 @@ def test_lookup_gradient_of_runs_at_tile_edges(n):
             assert torch.equal(dw, ref), (n, head, run)
 
 
+@pytest.mark.parametrize("n,V", [(7, 2 ** 21 + 3), (2048, 2 ** 20), (2049, 2 ** 20 - 1), (2049, 2 ** 20), (4100, 700),
+                                 (70000, 5000), (131072, 1023), (131073, 1023), (150000, 2 ** 20 + 77)])
+def test_lookup_gradient_of_every_sort(n, V):
+    # token counts and vocabularies on both sides of each sort's limits; half
+    # of the tokens are few, whole numbers sum exactly
+    D = 8
+    g = gen(n)
+    tok = torch.randint(0, V, (n,), device=DEV, generator=g)
+    few = torch.rand(n, device=DEV, generator=g) < 0.5
+    tok[few] = tok[few] % 13
+    dy = torch.randint(-8, 8, (n, D), device=DEV, generator=g).float()
+    e = tt.TokenEmbedding(V, D, padding_idx=3)
+    keep = tok != 3
+    ref = torch.zeros((V, D), device=DEV).index_add_(0, tok[keep], dy[keep])
+    assert torch.equal(e.backward(dy, tok), ref)
+    old = torch.randint(-8, 8, (V, D), device=DEV, generator=g).float()
+    assert torch.equal(e.backward(dy, tok, grad_weight=old.clone(), accumulate=True), ref + old)
+
+
+@pytest.mark.parametrize("n,D", [(100, 64), (3000, 130), (9000, 1030), (40000, 36)])
+def test_lookup_gradient_of_one_token(n, D):
+    dy = torch.randint(-8, 8, (n, D), device=DEV, generator=gen(n)).float()
+    dw = tt.TokenEmbedding(5, D).backward(dy, torch.full((n,), 2, device=DEV))
+    assert torch.equal(dw[2], dy.sum(0)) and int((dw != 0).any(1).sum()) <= 1
+
+
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 15, 16, 17, 24, 25, 40])
+def test_lookup_gradient_of_short_runs(n):
+    # runs of every length up to three tiles of eight, from every place in a tile
+    V, D = 12, 16
+    e = tt.TokenEmbedding(V, D)
+    for head in range(9):
+        for run in range(0, n - head + 1):
+            tok = torch.tensor([1] * head + [5] * run + [9] * (n - head - run), device=DEV, dtype=torch.int64)
+            dy = torch.randint(-8, 8, (n, D), device=DEV, generator=gen(run)).float()
+            ref = torch.zeros((V, D), device=DEV).index_add_(0, tok, dy)
+            assert torch.equal(e.backward(dy, tok), ref), (n, head, run)
+
+
 def test_lookup_of_no_tokens():
     e = tt.TokenEmbedding(6, 10)
     none = torch.zeros(0, dtype=torch.int64, device=DEV)
