@@ -282,17 +282,9 @@ __global__ __launch_bounds__(kTokThreads) void k_token_place(LookupArgs a, const
     }
 }
 
-// Whether the run of equal keys across the boundary b (a multiple of the
-// tile) is cut there: it is when it covers a whole tile next to b.  Shorter
-// runs belong to the worker of the tile they begin in, which reads past its
-// end (by less than a tile).
-__device__ __forceinline__ bool run_cut(const uint32_t *key, int64_t n, int64_t b, int tile)
-{
-    if (b <= 0 || b >= n) return false;
-    const uint32_t k = key[b];
-    if (key[b - 1] != k) return false;
-    return key[b - tile] == k || (b + tile - 1 < n && key[b + tile - 1] == k);
-}
+// The run of equal keys across a tile's edge is cut there when it covers a
+// whole tile next to the edge.  Shorter runs belong to the worker of the tile
+// they begin in, which reads past its end (by less than a tile).
 
 template <class T, int VEC, int NV>
 __device__ __forceinline__ void add_row_out(const LookupArgs &a, int64_t v, const int64_t (&c)[NV],
@@ -459,34 +451,39 @@ __global__ __launch_bounds__(256) void k_lookup_sum(LookupArgs a, const uint32_t
 
 // Runs that were cut: the block of 64 tiles and 256 columns adds up the runs
 // that begin in its tiles.  A wave takes a short run by itself; the sums of a
-// long one are shared out over the waves and joined in order.
+// long one are shared out over the waves and joined in order.  What bounds it
+// is the chain of dependent loads of one run, so the keys that say which runs
+// begin are read together, a row that is added to before its sum is known,
+// and where a row has fewer than 256 columns a wave's lanes take several slots
+// at a time.
 template <class T>
 __global__ __launch_bounds__(64 * kJoinGroups) void k_lookup_join(LookupArgs a, const uint32_t *key, int tile,
                                                                   int tiles, const float *slots)
 {
     constexpr int kShort = 2 * kJoinGroups;
     __shared__ float sm[kJoinGroups][256];
-    __shared__ int2 longs[64];
+    __shared__ int3 longs[64]; // tile, last tile, key
     __shared__ int count;
     if (threadIdx.x == 0) count = 0;
-    __syncthreads();
     const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
     const int64_t n = a.n, j0 = (int64_t)blockIdx.x * 64;
-    bool begins = false; // a cut run begins in this lane's tile
+    auto at = [&](int64_t p) { return key[p < 0 ? 0 : p < n ? p : n - 1]; };
+    bool begins; // a cut run begins in this lane's tile
+    uint32_t edge;
     {
         const int64_t j = j0 + lane, tb = j * tile, b = tb + tile;
-        if (j < tiles && run_cut(key, n, b, tile)) {
-            const uint32_t k = key[b];
-            begins = k != (uint32_t)a.V && !(tb > 0 && key[tb] == k && key[tb - 1] == k);
-        }
+        const uint32_t before = at(tb - 1), first = at(tb), last = at(b - 1), beyond = at(b + tile - 1);
+        edge = at(b);
+        const bool cut = b < n && last == edge && (first == edge || (b + tile - 1 < n && beyond == edge));
+        begins = cut && edge != (uint32_t)a.V && !(tb > 0 && first == edge && before == edge);
     }
+    __syncthreads();
     // the last tile that the run of tile j reaches: the next 64 tiles are
     // looked at together, then every 64th of those that follow
-    auto last_of = [&](int64_t j) {
-        const uint32_t k = key[(j + 1) * tile];
+    auto last_of = [&](int64_t j, uint32_t k) {
         auto reach = [&](int64_t q, int64_t by) { // how many of tiles q, q + by, .. begin in the run
-            const int64_t at = q + lane * by;
-            const uint64_t m = __ballot(at < tiles && key[(at < tiles ? at : tiles - 1) * tile] == k);
+            const int64_t p = q + lane * by;
+            const uint64_t m = __ballot(p < tiles && key[(p < tiles ? p : tiles - 1) * tile] == k);
             return m == ~0ull ? 64 : __builtin_ctzll(~m);
         };
         int64_t q = j + 1;
@@ -494,59 +491,72 @@ __global__ __launch_bounds__(64 * kJoinGroups) void k_lookup_join(LookupArgs a, 
             const int c = reach(q, 1);
             if (c < 64) return q + c - 1;
             const int steps = reach(q, 64); // tile q is in the run: at least one
-            q += (int64_t)(steps - 1) * 64;
-            if (steps == 1) q += 64;
+            q += (int64_t)(steps > 1 ? steps - 1 : 1) * 64;
         }
     };
-    const int64_t c = (int64_t)blockIdx.y * 256 + lane * 4;
+    // lanes side by side in a row of columns, and rows of lanes
+    const int64_t wide = a.D - (int64_t)blockIdx.y * 256;
+    const int across = wide > 128 ? 64 : wide > 64 ? 32 : 16, rows = 64 / across, sub = lane / across;
+    const int64_t c = (int64_t)blockIdx.y * 256 + lane % across * 4;
     const int left = (int)(a.D - c < 4 ? (a.D - c < 0 ? 0 : a.D - c) : 4);
     auto add = [&](int64_t j, int64_t from, int64_t to, int by, float (&s)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] = 0.f;
 #pragma unroll 8
-        for (int64_t q = from; q <= to; q += by) {
+        for (int64_t q = from + sub * by; q <= to; q += rows * by) {
             float x[4];
             load_part<float, 4>(slots + (2 * q + (q == j)) * a.D + (left ? c : 0), left, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[i] += x[i];
         }
-    };
-    auto out = [&](int64_t j, const float (&s)[4]) {
-        if (!left) return;
-        T *dst = static_cast<T *>(a.dst) + (int64_t)key[(j + 1) * tile] * a.ld_dst + c;
-        float o[4];
-        if (a.accumulate) load_part<T, 4>(dst, left, o);
+        for (int o = across; o < 64; o <<= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = a.accumulate ? fmaf(s[i], a.scale, o[i]) : s[i] * a.scale;
-        store_part<T, 4>(dst, left, o);
+            for (int i = 0; i < 4; ++i) s[i] += __shfl_xor(s[i], o, 64);
     };
-    float s[4];
+    auto row = [&](uint32_t k) { return static_cast<T *>(a.dst) + (int64_t)k * a.ld_dst + c; };
+    auto fetch = [&](uint32_t k, float (&o)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = 0.f;
+        if (a.accumulate) load_part<T, 4>(row(k), left, o);
+    };
+    auto out = [&](uint32_t k, const float (&s)[4], const float (&old)[4]) {
+        float o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(s[i], a.scale, old[i]);
+        if (sub == 0 && left) store_part<T, 4>(row(k), left, o);
+    };
+    float s[4], old[4];
     int turn = 0;
     for (uint64_t m = __ballot(begins); m; m &= m - 1, ++turn) {
         if (turn % kJoinGroups != grp) continue;
         const int t = __builtin_ctzll(m);
-        const int64_t last = last_of(j0 + t);
+        const uint32_t k = __shfl(edge, t, 64);
+        fetch(k, old);
+        const int64_t last = last_of(j0 + t, k);
         if (last - (j0 + t) >= kShort) { // left to all waves
-            if (lane == 0) longs[atomicAdd(&count, 1)] = make_int2(t, (int)last);
+            if (lane == 0) longs[atomicAdd(&count, 1)] = make_int3(t, (int)last, (int)k);
             continue;
         }
         add(j0 + t, j0 + t, last, 1, s);
-        out(j0 + t, s);
+        out(k, s, old);
     }
     __syncthreads();
     for (int i = 0; i < count; ++i) { // each is summed by itself: their order does not matter
         const int64_t j = j0 + longs[i].x;
+        const uint32_t k = (uint32_t)longs[i].z;
+        fetch(k, old);
         add(j, j + grp, longs[i].y, kJoinGroups, s);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sm[grp][lane * 4 + k] = s[k];
+        for (int q = 0; q < 4; ++q) sm[grp][lane * 4 + q] = s[q];
         __syncthreads();
         if (grp == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[k] = 0.f;
-                for (int g = 0; g < kJoinGroups; ++g) s[k] += sm[g][lane * 4 + k];
+            for (int q = 0; q < 4; ++q) {
+                s[q] = 0.f;
+#pragma unroll
+                for (int g = 0; g < kJoinGroups; ++g) s[q] += sm[g][lane * 4 + q];
             }
-            out(j, s);
+            out(k, s, old);
         }
         __syncthreads();
     }
