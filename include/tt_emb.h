@@ -426,7 +426,7 @@ int tt_emb_norm_workspace_size(int64_t n, int64_t D, size_t *bytes);
  * are never stored: a tile of them lives in registers until its rows' running
  * maximum and sum are known.  A target outside [0, V) that is not
  * ignore_index counts as ignored and sets TT_EMB_ERR_INDEX.
- * D <= 16384, n and V < 2^31. */
+ * D <= 16384, n and V < 2^31, n V below 2^37 (more rows: several calls). */
 int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weight, int64_t ld_weight,
                         const int64_t *targets, int64_t n, int64_t V, int64_t D, int32_t dtype,
                         int64_t ignore_index, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
@@ -438,7 +438,8 @@ int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weigh
  * both of `dtype`, overwritten.  The vocabulary is taken in pieces whose d
  * (bf16 for bf16 inputs; two fp16 terms, 22 bits, for fp32 inputs, whose
  * own values are scaled by powers of two and split the same way) is in ws;
- * sums are fp32.  An ignored row's hidden values do not reach the gradients,
+ * sums are fp32.  fp32 inputs: a value of the weight keeps 22 bits or an
+ * absolute 2^-39 of the weight's largest, whichever is more.  An ignored row's hidden values do not reach the gradients,
  * whatever they hold.  A larger ws allows larger pieces: any
  * ws_bytes from *least of tt_emb_xent_workspace_size on is accepted, *bytes
  * is the size past which nothing is gained. */

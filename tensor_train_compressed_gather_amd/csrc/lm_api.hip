@@ -28,6 +28,7 @@ int hip_status(hipError_t e) { return e == hipSuccess ? TT_EMB_OK : TT_EMB_ERR_H
 
 constexpr int64_t kMaxRows = 0x7ffffffe;
 constexpr int64_t kMaxLookupCols = 65536, kMaxNormCols = 16384, kMaxXentCols = 16384;
+constexpr int64_t kMaxXentTiles = (int64_t)1 << 23;
 
 int check_lookup(int64_t n, int64_t V, int64_t D, int32_t dtype)
 {
@@ -49,6 +50,8 @@ int check_xent(int64_t n, int64_t V, int64_t D, int32_t dtype)
     if (n < 0 || V <= 0 || D <= 0 || bad_dtype(dtype)) return TT_EMB_ERR_ARG;
     if (dtype == TT_EMB_DTYPE_HALF) return TT_EMB_ERR_UNSUPPORTED;
     if (n > kMaxRows || V > kMaxRows || D > kMaxXentCols) return TT_EMB_ERR_UNSUPPORTED;
+    // tiles of the logits: the blocks of one launch stay below 2^24
+    if (((n + 127) / 128) * ((V + 127) / 128) > kMaxXentTiles) return TT_EMB_ERR_UNSUPPORTED;
     return TT_EMB_OK;
 }
 

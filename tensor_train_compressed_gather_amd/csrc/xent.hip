@@ -9,12 +9,13 @@
 // the gradients a piece of the vocabulary's logits is made again, turned into
 // d, and multiplied into both gradients before the next piece.
 //
-// fp32 inputs are scaled by powers of two (each hidden row, and the weight as a
-// whole, to a largest magnitude in [2^14, 2^15)) and split into two fp16 terms
-// of 11 bits each, and the three products of terms above 2^-22 are added up:
-// five times the rate of the fp32 matrix instructions.  d, at most 1 in its
-// units, is split the same way in units of 2^-15.  A value keeps 22 bits, or an
-// absolute 2^-39 of the largest where that is more.
+// fp32 inputs are scaled by powers of two (to a largest magnitude in
+// [2^14, 2^15): each hidden row for the logits, the hidden rows that count as a
+// whole for the weight's gradient, the weight as a whole) and split into two
+// fp16 terms of 11 bits each, and the three products of terms above 2^-22 are
+// added up: five times the rate of the fp32 matrix instructions.  d, at most 1
+// in its units, is split the same way in units of 2^-15.  A value keeps 22
+// bits, or an absolute 2^-39 of the largest where that is more.
 #include "lm.h"
 #include "primitives.h"
 
@@ -33,7 +34,7 @@ constexpr int kTurnPad = 64;           // bytes past a turned tile's row in LDS
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
 constexpr size_t kPieceBytes = (size_t)256 << 20; // d of one piece of the vocabulary, at most
 constexpr int kSplitK = 512;           // least summed values of a split of dH
-constexpr int kRound = 256;            // rows and columns of d are padded to this
+constexpr int kRound = 256;            // columns of d are padded to this
 constexpr int kLeast = 128;            // rows and columns of the smallest tile
 constexpr int kPadK = 64;              // packed rows are padded to this
 constexpr int kMaxParts = 1024;        // blocks of the weight's largest magnitude
@@ -75,6 +76,11 @@ __device__ __forceinline__ void split(float x, short (&t)[PL])
     }
 }
 
+__device__ __forceinline__ bool row_counts(int64_t target, int64_t ignore, int64_t V)
+{
+    return target != ignore && target >= 0 && target < V;
+}
+
 // An operand of a product: PL matrices of 16-bit values.  Straight: row r holds
 // the summed index.  Turned: row k of the summed index holds the outputs.
 struct Operand {
@@ -93,7 +99,9 @@ struct Output {
     float *target_logit;      // [n]
     const float *lse, *grad;  // [n]
     const float *top_grad;    // the unit of d
-    const int *h_exp, *w_exp; // fp16 terms: exponents the rows and the weight were scaled by
+    // fp16 terms: exponents by which each row (for the logits), all rows (for
+    // the weight's gradient) and the weight were scaled
+    const int *h_exp, *all_exp, *w_exp;
     short *d;                 // [planes][rows][ldd]
     int64_t ldd, plane_d;
     float *sum;               // dH in fp32, [splits][n][D]
@@ -436,10 +444,9 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                 const int64_t target = o.targets[i];
                 lse = o.lse[i];
                 if constexpr (PL == 2) scale = ldexpf(1.f, -(o.h_exp[i] + *o.w_exp));
-                if (target != o.ignore && target >= 0 && target < o.V) {
+                if (row_counts(target, o.ignore, o.V)) {
                     t = target - o.v0 - m0;
-                    // fp16 terms: at most 2^kUnitExp, the unit is the largest of these quotients
-                    g = PL == 2 ? ldexpf(o.grad[i], -o.h_exp[i]) / unit * (float)(1 << kUnitExp) : o.grad[i] / unit;
+                    g = o.grad[i] / unit * (PL == 2 ? (float)(1 << kUnitExp) : 1.f);
                 } else {
                     lse = INFINITY;
                 }
@@ -479,7 +486,9 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                 }
         }
     } else {
-        const float unit = *o.top_grad;
+        float unit = 1.f;
+        if constexpr (OUT == OUT_WEIGHT)
+            unit = PL == 2 ? ldexpf(*o.top_grad, -(kUnitExp + *o.all_exp)) : *o.top_grad;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
@@ -507,7 +516,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                         const int64_t row = o.v0 + i;
                         if (row >= o.V) continue;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] *= PL == 2 ? unit * (1.f / (float)(1 << kUnitExp)) : unit;
+                        for (int r = 0; r < 4; ++r) x[r] *= unit;
                         if (PL == 2) store_part<float, 4>(static_cast<float *>(o.out) + row * o.ld_out + m, left, x);
                         else store_part<bf16, 4>(static_cast<bf16 *>(o.out) + row * o.ld_out + m, left, x);
                     }
@@ -519,15 +528,13 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 // dH from the splits' sums, in order, in units of the loss.
 template <class T>
 __global__ __launch_bounds__(256) void k_xent_hidden(const float *sum, int splits, int64_t n, int64_t D,
-                                                     const float *top_grad, const int *h_exp, const int *w_exp,
-                                                     T *out, int64_t ld)
+                                                     const float *top_grad, const int *w_exp, T *out, int64_t ld)
 {
     const int64_t chunks = (D + 3) / 4, step = (int64_t)gridDim.x * 256;
-    const float unit = *top_grad;
+    const float unit = w_exp ? ldexpf(*top_grad, -(kUnitExp + *w_exp)) : *top_grad;
     for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < n * chunks; c += step) {
         const int64_t i = c / chunks, k = (c - i * chunks) * 4;
         const int left = (int)(D - k < 4 ? D - k : 4);
-        const int e = h_exp ? h_exp[i] - *w_exp - kUnitExp : 0;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         for (int q = 0; q < splits; ++q) {
             float y[4];
@@ -536,7 +543,7 @@ __global__ __launch_bounds__(256) void k_xent_hidden(const float *sum, int split
             for (int r = 0; r < 4; ++r) x[r] += y[r];
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = h_exp ? ldexpf(x[r] * unit, e) : x[r] * unit;
+        for (int r = 0; r < 4; ++r) x[r] *= unit;
         store_part<T, 4>(out + i * ld + k, left, x);
     }
 }
@@ -571,13 +578,14 @@ __device__ __forceinline__ void pack_piece(const T *src, int64_t left, int e, bo
 }
 
 // Hidden rows as planes with `ld` columns, zero past D; a wave per row.  fp16
-// terms: each row scaled by a power of two of its own.  With targets: a row
-// that is ignored and holds a value that is not finite is taken as zeros, so
-// that its zero gradient stays zero in the weight's.
+// terms: each row scaled by a power of two of its own, and the largest
+// magnitude of each row that counts left in `tops`.  With targets: a row that
+// is ignored and holds a value that is not finite is taken as zeros, so that
+// its zero gradient stays zero.
 template <class T, int PL>
 __global__ __launch_bounds__(256) void k_pack_rows(const T *src, int64_t ld_src, int64_t rows, int64_t D, short *dst,
-                                                   int64_t ld, int64_t plane, int *exps, const int64_t *targets,
-                                                   int64_t ignore, int64_t V)
+                                                   int64_t ld, int64_t plane, int *exps, float *tops,
+                                                   const int64_t *targets, int64_t ignore, int64_t V)
 {
     const int lane = threadIdx.x & 63;
     const int64_t step = (int64_t)gridDim.x * 4;
@@ -600,14 +608,30 @@ __global__ __launch_bounds__(256) void k_pack_rows(const T *src, int64_t ld_src,
 #pragma unroll
             for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
             if (targets) {
-                const int64_t t = targets[r];
-                clear = __any(odd) && (t == ignore || t < 0 || t >= V);
+                const bool counts = row_counts(targets[r], ignore, V);
+                clear = __any(odd) && !counts;
+                if (PL == 2 && lane == 0) tops[r] = counts ? top : 0.f;
             }
             e = PL == 2 && !clear ? scale_exp(top) : 0;
-            if (exps && lane == 0) exps[r] = e;
+            if (PL == 2 && lane == 0) exps[r] = e;
         }
         for (int64_t k = lane * 8; k < ld; k += 512)
             pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, clear, dst + r * ld + k, plane);
+    }
+}
+
+// The rows that count as fp16 planes scaled by one power of two, the others as
+// zeros: the operand of the weight's gradient.
+__global__ __launch_bounds__(256) void k_pack_counting(const float *src, int64_t ld_src, int64_t rows, int64_t D,
+                                                       short *dst, int64_t ld, int64_t plane, const int *exp,
+                                                       const int64_t *targets, int64_t ignore, int64_t V)
+{
+    const int64_t chunks = ld / 8, step = (int64_t)gridDim.x * 256;
+    const int e = *exp;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
+        const int64_t r = c / chunks, k = (c - r * chunks) * 8;
+        pack_piece<float, 2>(src + r * ld_src + (k < D ? k : 0), D - k, e, !row_counts(targets[r], ignore, V),
+                             dst + r * ld + k, plane);
     }
 }
 
@@ -694,27 +718,38 @@ __global__ __launch_bounds__(1024) void k_xent_join(const float2 *part, int64_t 
     loss[i] = in && t != ignore ? z - target_logit[i] : 0.f;
 }
 
-// The unit of d: the largest |grad_loss| of the rows that count (fp16 terms:
-// divided by the power of two the row was scaled by, which d then carries).
-// With equal gradients (a mean over the rows) d is exp(z - lse) - [v = target]
-// in this unit, and the target's -1 + p, the largest term of both gradients,
-// rounds to bf16 without error for small p.  1 where there is nothing to scale.
-__global__ __launch_bounds__(1024) void k_xent_top_grad(const float *grad, const int64_t *targets, int64_t ignore,
-                                                        int64_t n, int64_t V, const int *h_exp, float *top)
+// The unit of d: the largest |grad_loss| of the rows that count.  With equal
+// gradients (a mean over the rows) d is exp(z - lse) - [v = target] in this
+// unit, and the target's -1 + p, the largest term of both gradients, rounds to
+// bf16 without error for small p.  1 where there is nothing to scale.  fp16
+// terms: also the exponent for all rows together, from their largest.
+__global__ __launch_bounds__(1024) void k_xent_units(const float *grad, const int64_t *targets, int64_t ignore,
+                                                     int64_t n, int64_t V, const float *tops, float *unit,
+                                                     int *all_exp)
 {
-    __shared__ float sm[16];
-    float m = 0.f;
+    __shared__ float sm[2][16];
+    float m = 0.f, h = 0.f;
     for (int64_t i = threadIdx.x; i < n; i += 1024) {
-        const int64_t t = targets[i];
-        if (t != ignore && t >= 0 && t < V) m = fmaxf(m, fabsf(h_exp ? ldexpf(grad[i], -h_exp[i]) : grad[i]));
+        if (row_counts(targets[i], ignore, V)) m = fmaxf(m, fabsf(grad[i]));
+        if (tops) h = fmaxf(h, tops[i]);
     }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+    for (int o = 32; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor(m, o, 64));
+        h = fmaxf(h, __shfl_xor(h, o, 64));
+    }
+    if ((threadIdx.x & 63) == 0) {
+        sm[0][threadIdx.x >> 6] = m;
+        sm[1][threadIdx.x >> 6] = h;
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 16; ++w) m = fmaxf(m, sm[w]);
-        *top = m > 0.f && m < INFINITY ? m : 1.f;
+        for (int w = 1; w < 16; ++w) {
+            m = fmaxf(m, sm[0][w]);
+            h = fmaxf(h, sm[1][w]);
+        }
+        *unit = m > 0.f && m < INFINITY ? m : 1.f;
+        *all_exp = scale_exp(h);
     }
 }
 
@@ -727,10 +762,10 @@ __global__ __launch_bounds__(256) void k_xent_clear(T *p, int64_t ld, int64_t ro
 }
 
 struct XentPlan {
-    float *target_logit, *top_grad, *w_part;
-    int *h_exp, *w_exp;
+    float *target_logit, *top_grad, *w_part, *tops;
+    int *h_exp, *all_exp, *w_exp;
     float2 *part;
-    short *h, *w; // packed operands (the weight's unused where it serves in place)
+    short *h, *h_all, *w; // packed operands (the weight's unused where it serves in place)
     float *sum;
     short *d;
     int64_t Kp, nr, piece;
@@ -762,9 +797,12 @@ int hidden_splits(int64_t n, int64_t D, int64_t piece)
     if (s > piece / kSplitK) s = piece / kSplitK;
     return (int)(s < 1 ? 1 : s);
 }
+// Rows of d: whole tiles, so that they are written without a test.
+inline int64_t d_rows(int64_t n) { return n <= 128 ? 128 : up(n, 256); }
+
 int64_t best_piece(int64_t n, int64_t V, int PL)
 {
-    int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * up(n, kRound) * 2)) / kRound * kRound;
+    int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * d_rows(n) * 2)) / kRound * kRound;
     if (c < 8 * kRound) c = 8 * kRound;
     return up(V < c ? V : c, kRound);
 }
@@ -782,7 +820,7 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     };
     XentPlan p{};
     p.Kp = up(D, kPadK);
-    p.nr = up(n, kRound);
+    p.nr = d_rows(n);
     p.piece = piece;
     p.target_logit = (float *)take(4 * n);
     p.top_grad = (float *)take(4);
@@ -790,9 +828,12 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     p.w_part = (float *)take(4 * kMaxParts);
     p.h_exp = (int *)take(4 * n);
     p.w_exp = (int *)take(4);
+    p.all_exp = (int *)take(4);
+    p.tops = (float *)take(4 * n);
     p.h = (short *)take((size_t)PL * n * p.Kp * 2);
     p.w = (short *)take((size_t)PL * V * p.Kp * 2);
     if (piece) {
+        if (PL == 2) p.h_all = (short *)take((size_t)PL * n * p.Kp * 2);
         p.splits = hidden_splits(n, D, piece);
         p.sum = (float *)take(4 * (size_t)p.splits * n * D);
         p.d = (short *)take((size_t)PL * p.nr * piece * 2);
@@ -841,7 +882,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     if (grad || !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp)) {
         h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
         hipLaunchKernelGGL((k_pack_rows<T, PL>), dim3(blocks_for(a.n * 64)), dim3(256), 0, s, hs, a.ld_h, a.n, a.D, p.h,
-                           p.Kp, a.n * p.Kp, p.h_exp, grad ? a.targets : nullptr, a.ignore, a.V);
+                           p.Kp, a.n * p.Kp, p.h_exp, p.tops, grad ? a.targets : nullptr, a.ignore, a.V);
     }
     Operand w{reinterpret_cast<const short *>(ws), a.ld_w, 0, a.V, a.D};
     if (!in_place<T, PL>(ws, a.ld_w, a.D, p.Kp)) {
@@ -868,6 +909,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.top_grad = p.top_grad;
     o.h_exp = p.h_exp;
     o.w_exp = p.w_exp;
+    o.all_exp = p.all_exp;
     o.splits = p.splits;
     o.d = p.d;
     o.ldd = piece;
@@ -877,8 +919,14 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(1024), 0, s, p.part, tiles, a.n, a.V,
                        a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
     if (!grad) return hipGetLastError();
-    hipLaunchKernelGGL(k_xent_top_grad, dim3(1), dim3(1024), 0, s, a.grad_loss, a.targets, a.ignore, a.n, a.V,
-                       PL == 2 ? p.h_exp : nullptr, p.top_grad);
+    hipLaunchKernelGGL(k_xent_units, dim3(1), dim3(1024), 0, s, a.grad_loss, a.targets, a.ignore, a.n, a.V,
+                       PL == 2 ? p.tops : nullptr, p.top_grad, p.all_exp);
+    Operand h_all = h;
+    if constexpr (PL == 2) {
+        h_all.p = p.h_all;
+        hipLaunchKernelGGL(k_pack_counting, dim3(blocks_for(a.n * (p.Kp / 8))), dim3(256), 0, s, hs, a.ld_h, a.n, a.D,
+                           p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.targets, a.ignore, a.V);
+    }
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t here = a.V - v0 < piece ? a.V - v0 : piece, cols = up(here, kRound);
         Operand wp = w;
@@ -886,20 +934,20 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         wp.rows = here;
         o.v0 = v0;
         o.first = v0 == 0;
-        // d of whole 256 x 256 blocks: what lies past the rows and the vocabulary is written as zeros
+        // d in whole tiles: what lies past the rows and the vocabulary is written as zeros
         product<PL, false, false, OUT_D>(wp, h, cols, p.nr, p.Kp, o, s);
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
         o.split_k = up((cols + p.splits - 1) / p.splits, kPadK);
         product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s);
         o.out = a.dw;
         o.ld_out = a.ld_dw;
-        product<PL, true, true, OUT_WEIGHT>(h, d, a.D, here, p.nr, o, s);
+        product<PL, true, true, OUT_WEIGHT>(h_all, d, a.D, here, up(a.n, kPadK), o, s);
     }
     // splits past the first piece's end have written nothing
     const int64_t first = up(a.V < piece ? a.V : piece, kRound);
     const int64_t per = up((first + p.splits - 1) / p.splits, kPadK);
     hipLaunchKernelGGL(k_xent_hidden<T>, dim3(blocks_for(a.n * ((a.D + 3) / 4))), dim3(256), 0, s, p.sum,
-                       (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.h_exp : nullptr, p.w_exp,
+                       (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr,
                        static_cast<T *>(a.dh), a.ld_dh);
     return hipGetLastError();
 }

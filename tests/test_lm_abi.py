@@ -86,6 +86,7 @@ XENT_G = dict(h=P, ld_h=8, w=Q, ld_w=8, t=R, g=R, n=4, V=10, D=8, dtype=1, ignor
     ("tt_emb_xent_forward", XENT_F, dict(dtype=2), UNSUPPORTED),
     ("tt_emb_xent_forward", XENT_F, dict(D=16385, ld_h=16385, ld_w=16385), UNSUPPORTED),
     ("tt_emb_xent_forward", XENT_F, dict(ws_bytes=256), WS),
+    ("tt_emb_xent_forward", XENT_F, dict(n=2 ** 20, V=2 ** 20), UNSUPPORTED),  # more tiles than a launch takes
     ("tt_emb_xent_loss_grad", XENT_G, dict(g=None), ARG),
     ("tt_emb_xent_loss_grad", XENT_G, dict(dh=None), ARG),
     ("tt_emb_xent_loss_grad", XENT_G, dict(dw=None), ARG),
@@ -178,8 +179,8 @@ def test_binding_declares_every_entry_point():
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
-@pytest.mark.parametrize("n", [0, 1, 129, 100000])
-@pytest.mark.parametrize("V,D", [(1, 1), (300, 128), (10 ** 6, 129), (2 ** 31 - 2, 16384)])
+@pytest.mark.parametrize("n,V,D", [(0, 1, 1), (1, 1, 1), (0, 2 ** 31 - 2, 16384), (129, 300, 128),
+                                   (60, 2 ** 30 - 2, 16384), (100000, 10 ** 6, 129), (2 ** 30, 100, 8)])
 def test_xent_workspace_of_any_size(n, V, D, dtype):
     best, least = C.c_size_t(), C.c_size_t()
     for grad in (0, 1):

@@ -49,6 +49,6 @@ def test_the_example_takes_the_gradient_of_its_loss():
     counts = (target != ex.IGNORE).sum()
     (ref.sum() / counts).backward()
     # fp32 sums of up to 64 x 1000 terms, each to 2^-22: far below 1e-4 of the largest value
-    assert float((loss.double() - ref).abs().max()) <= 1e-4
+    assert float((loss.double() - ref.detach()).abs().max()) <= 1e-4
     for g, leaf in zip(grads, leaves):
         assert float((g.double() - leaf.grad).abs().max()) <= 1e-4 * float(leaf.grad.abs().max())

@@ -364,6 +364,58 @@ def test_xent_and_gradients(n, V, D, gap, t):
 
 
 @pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("n,V,D,gap", [(1024, 33000, 1024, 0), (1100, 66000, 40, 0), (513, 20011, 600, 8)])
+def test_xent_in_large_tiles(n, V, D, gap, t):
+    # enough rows, vocabulary and columns for 256 x 256 tiles in every product,
+    # for tiles taken in patches, and for sums split over compute units
+    test_xent_and_gradients(n, V, D, gap, t)
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+def test_xent_ignores_what_ignored_rows_hold(t):
+    n, V, D = 70, 900, 96
+    h, w, target, grad = xent_inputs(n, V, D, t, 0, 15)
+    h = h.clone()
+    x = tt.VocabCrossEntropy(V, D)
+    target[5], target[40] = -100, -100
+    ref = x.loss_and_grad(h, w, target, grad)
+    h[5, 3], h[5, 7], h[40, 95] = float("nan"), float("inf"), float("-inf")
+    got = x.loss_and_grad(h, w, target, grad)
+    assert got[0][5] == 0 and got[0][40] == 0
+    keep = target != -100
+    assert all(torch.equal(p[keep], q[keep]) for p, q in zip(got[:3], ref[:3]))
+    assert (got[2][~keep] == 0).all()
+    # the two rows' zeros, instead of finite values, meet zero gradients: the same sums
+    assert torch.equal(got[3], ref[3])
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+def test_xent_of_rows_of_very_different_size(t):
+    # a hidden row 2^40 times another: each row's gradient keeps its own precision
+    n, V, D = 64, 500, 64
+    h, w, target, grad = xent_inputs(n, V, D, t, 0, 16)
+    size = torch.exp2(torch.linspace(-40, 0, n, device=DEV))[:, None]
+    h = (h * size).to(t)
+    grad = torch.full_like(grad, 1.0 / n)
+    z, lse, loss, d, mag = xent_reference(h, w, target, grad, -100)
+    x = tt.VocabCrossEntropy(V, D)
+    got = x.loss_and_grad(h, w, target, grad)
+    ez = (6 * D + 8) * U32 * (h.double().abs() @ w.double().abs().t()).amax(1)
+    es = ez + 210 * U32
+    close(got[1], lse, es + 4 * U32 * lse.abs(), "lse")
+    close(got[0], loss, es + ez + 4 * U32 * (lse.abs() + z.abs().amax(1)), "loss")
+    # d's rounding (two fp16 terms, 2^-22, or bf16's)
+    ed = ((u(BF16) if t == BF16 else 2.0 ** -21) + 2 * ez + 220 * U32)[:, None] * mag
+    ref = d @ w.double()
+    close(got[2], ref, ed @ w.double().abs() + 6 * (V + 8) * U32 * (mag @ w.double().abs()) + u(t) * ref.abs(), "dh")
+    # the hidden values' own floor beside the largest row (fp32 inputs): 2^-38 of it
+    ref = d.t() @ h.double()
+    ed = ((u(BF16) if t == BF16 else 2.0 ** -21) + 2 * ez + 220 * U32)[:, None] * mag
+    close(got[3], ref, ed.t() @ h.double().abs() + 6 * (n + 8) * U32 * (mag.t() @ h.double().abs())
+          + u(t) * ref.abs() + 2.0 ** -38 * h.double().abs().max() * mag.sum(0)[:, None], "dw")
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
 def test_xent_in_small_pieces_is_the_same(t):
     n, V, D = 150, 3000, 80
     h, w, target, grad = xent_inputs(n, V, D, t, 0, 5)
