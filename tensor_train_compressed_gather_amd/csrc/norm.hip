@@ -13,7 +13,12 @@ namespace ttemb {
 namespace {
 
 constexpr int kNormBlocks = 5 * kCUs;      // forward: blocks at most, all of them resident
-constexpr int kNormGradBlocks = 4 * kCUs;  // backward: rows of partial column sums, at most
+// Backward: rows of partial column sums, at most.  Two blocks on each compute
+// unit where a block holds one row (16384 x 4096 bf16: 84 us, 95 with four),
+// four where it holds several (32768 x 128 fp32: 10.6 us, 11.5 with two).
+constexpr int kNormGradBlocks = 4 * kCUs;
+template <int TPR>
+constexpr int norm_grad_blocks() { return TPR >= 256 ? 2 * kCUs : kNormGradBlocks; }
 
 template <int TPR>
 struct NormShape {
@@ -261,29 +266,39 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_bwd(NormArgs a
     }
 }
 
-// Column sums of the blocks' partials: 64 columns per block, 16 groups of
-// rows, joined in order.
+// Column sums of the blocks' partials: 64 columns per block, four per lane, 64
+// groups of rows; the four groups of a wave meet in shuffles, the waves in LDS,
+// always in the same order.
+template <bool WHOLE>
 __global__ __launch_bounds__(1024) void k_norm_cols(const float *part, int blocks, int D, void *dgamma, void *dbeta,
                                                     int param_dtype)
 {
     __shared__ float sm[16][64];
-    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane * 4;
     const float *p = part + (int64_t)blockIdx.y * blocks * D;
     void *dst = blockIdx.y ? dbeta : dgamma;
     if (!dst) return;
-    float s = 0.f;
-    if (c < D) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-        for (int b = grp; b < blocks; b += 16) s += p[(int64_t)b * D + c];
+    for (int b = grp; b < blocks; b += 64) {
+        const VecOf<float, 4>::raw v = load_row<float, 4, WHOLE>(p + (int64_t)b * D, c, D);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += v[i];
     }
-    sm[grp][lane] = s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] += __shfl_xor(s[i], 16, 64);
+        s[i] += __shfl_xor(s[i], 32, 64);
+        if ((threadIdx.x & 63) < 16) sm[wave][lane * 4 + i] = s[i];
+    }
     __syncthreads();
-    if (grp == 0 && c < D) {
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && col < D) {
         float t = 0.f;
 #pragma unroll
-        for (int g = 0; g < 16; ++g) t += sm[g][lane];
-        store_param(dst, param_dtype, c, t);
+        for (int w = 0; w < 16; ++w) t += sm[w][threadIdx.x];
+        store_param(dst, param_dtype, col, t);
     }
 }
 
@@ -331,12 +346,18 @@ hipError_t norm_backward(const NormArgs &a, hipStream_t s)
     return norm_shape<T>(a.D, [&](auto tpr, auto nv, auto whole) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
         const int64_t need = (a.n + NormShape<TPR>::rows - 1) / NormShape<TPR>::rows;
-        const int grid = (int)(need < kNormGradBlocks ? need : kNormGradBlocks);
+        const int grid = (int)(need < norm_grad_blocks<TPR>() ? need : norm_grad_blocks<TPR>());
         float *part = (a.dgamma || a.dbeta) ? reinterpret_cast<float *>(a.ws + TT_EMB_STATUS_BYTES) : nullptr;
         hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV, decltype(whole)::value>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a, part);
-        if (part)
-            hipLaunchKernelGGL(k_norm_cols, dim3((unsigned)((a.D + 63) / 64), 2), dim3(1024), 0, s, part, grid,
-                               (int)a.D, a.dgamma, a.dbeta, a.param_dtype);
+        if (part) {
+            const dim3 cols((unsigned)((a.D + 63) / 64), 2);
+            if (a.D % 4 == 0)
+                hipLaunchKernelGGL(k_norm_cols<true>, cols, dim3(1024), 0, s, part, grid, (int)a.D, a.dgamma, a.dbeta,
+                                   a.param_dtype);
+            else
+                hipLaunchKernelGGL(k_norm_cols<false>, cols, dim3(1024), 0, s, part, grid, (int)a.D, a.dgamma, a.dbeta,
+                                   a.param_dtype);
+        }
         return hipGetLastError();
     });
 }

@@ -33,7 +33,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kTurnPad = 64;           // bytes past a turned tile's row in LDS
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
 constexpr size_t kPieceBytes = (size_t)256 << 20; // d of one piece of the vocabulary, at most
-constexpr int kSplitK = 512;           // least summed values of a split of dH
+constexpr int kSplitK = 512;           // least summed values of a split
 constexpr int kRound = 256;            // columns of d are padded to this
 constexpr int kLeast = 128;            // rows and columns of the smallest tile
 constexpr int kPadK = 64;              // packed rows are padded to this
@@ -89,7 +89,9 @@ struct Operand {
     int64_t rows, cols; // of the stored matrix; what lies past them reads as zero
 };
 
-enum { OUT_STATS, OUT_D, OUT_HIDDEN, OUT_WEIGHT };
+// What a product's tiles become: maxima and sums of exponentials, d, partial
+// sums in fp32, or rows of the weight's gradient.
+enum { OUT_STATS, OUT_D, OUT_SUM, OUT_WEIGHT };
 
 struct Output {
     int64_t n, V, v0;         // rows, vocabulary, first column of this piece
@@ -104,12 +106,13 @@ struct Output {
     const int *h_exp, *all_exp, *w_exp;
     short *d;                 // [planes][rows][ldd]
     int64_t ldd, plane_d;
-    float *sum;               // dH in fp32, [splits][n][D]
-    int splits;               // of dH's sum
+    float *sum;               // fp32 sums, [splits][sum_rows][D]
+    int64_t sum_rows;
+    int splits;               // parts of the summed index
     int64_t split_k;          // summed values of each
+    int first;                // overwrite the sums, do not add to them
     void *out;                // dW
     int64_t ld_out, D;
-    int first;                // dH's first piece
 };
 
 // How one plane of an operand's tile, R outputs and BK summed values, lies in
@@ -276,16 +279,21 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
     __shared__ __align__(16) char lds[2 * STAGE];
     int64_t mi, ni;
     int sp;
-    if (!tile_of(mt, nt, OUT == OUT_HIDDEN ? o.splits : 1, mi, ni, sp)) return;
-    if constexpr (OUT == OUT_HIDDEN) { // this split's part of the sum
+    if (!tile_of(mt, nt, OUT == OUT_SUM ? o.splits : 1, mi, ni, sp)) return;
+    if constexpr (OUT == OUT_SUM) { // this split's part of the sum (X is turned)
         const int64_t k0 = sp * o.split_k;
         if (k0 >= K) return;
         X.p += k0 * X.ld;
         X.rows -= k0;
-        Y.p += k0;
-        Y.cols -= k0;
+        if constexpr (YT) {
+            Y.p += k0 * Y.ld;
+            Y.rows -= k0;
+        } else {
+            Y.p += k0;
+            Y.cols -= k0;
+        }
         K = K - k0 < o.split_k ? K - k0 : o.split_k;
-        o.sum += sp * o.n * o.D;
+        o.sum += sp * o.sum_rows * o.D;
     }
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
     const int64_t m0 = mi * TM, n0 = ni * TN;
@@ -425,14 +433,20 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             const float s = red[1][0][tid] * __expf(a - ref) + red[1][1][tid] * __expf(b - ref);
             o.part[mi * o.n + n0 + tid] = make_float2(top, s);
         }
-    } else if constexpr (OUT == OUT_D) {
-        // 64 rows of d at a time pass through LDS, so that they are written in
-        // whole lines: a lane holds four columns of one row, a wave 32 rows
-        constexpr int P = TM * 2 + 16, PART = 64 * P, PIECES = 64 * (TM / 8) / 256;
-        constexpr bool TWO = 2 * PL * PART <= 2 * STAGE; // one part is written while the last is read
-        static_assert(PL * PART <= 2 * STAGE, "a part fits the tiles' space");
-        const float unit = *o.top_grad;
-        const int64_t left = o.V - o.v0 - m0;
+    } else {
+        // 64 rows at a time pass through LDS, so that they are written in whole
+        // lines: a lane holds four columns of one row, a wave 32 rows
+        typedef std::conditional_t<OUT == OUT_D, short, std::conditional_t<OUT == OUT_WEIGHT && PL == 1, bf16, float>> E;
+        typedef E E4 __attribute__((ext_vector_type(4)));
+        constexpr int ES = (int)sizeof(E), EV = 16 / ES, PLANES = OUT == OUT_D ? PL : 1;
+        constexpr int P = TM * ES + 16, PART = 64 * P, ROWV = TM / EV, PIECES = 64 * ROWV / 256;
+        constexpr bool TWO = 2 * PLANES * PART <= 2 * STAGE; // one part is written while the last is read
+        static_assert(PLANES * PART <= 2 * STAGE, "a part fits the tiles' space");
+        float unit = 1.f;
+        if constexpr (OUT == OUT_D) unit = *o.top_grad;
+        if constexpr (OUT == OUT_WEIGHT)
+            unit = PL == 2 ? ldexpf(*o.top_grad, -(kUnitExp + *o.all_exp)) : *o.top_grad;
+        const int64_t left = o.V - o.v0 - m0; // of the vocabulary, in d
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -440,7 +454,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             // rows that do not count, or lie past the last: d = 0 (exp - 0)
             float lse = 0.f, g = 0.f, scale = 1.f;
             int64_t t = -1;
-            if (i < o.n) {
+            if (OUT == OUT_D && i < o.n) {
                 const int64_t target = o.targets[i];
                 lse = o.lse[i];
                 if constexpr (PL == 2) scale = ldexpf(1.f, -(o.h_exp[i] + *o.w_exp));
@@ -451,94 +465,85 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                     lse = INFINITY;
                 }
             }
-            char *part = lds + (TWO ? (j & 1) * PL * PART : 0);
-            if (!TWO && j) __syncthreads();
             const bool here = __any(t >= wm * (TM / 2) && t < (wm + 1) * (TM / 2));
+            char *part = lds + (TWO ? (j & 1) * PLANES * PART : 0);
+            if (!TWO && j) __syncthreads();
 #pragma unroll
             for (int a = 0; a < NI; ++a)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int m = row_of(a, 4 * q);
-                    s16x4 w[PL];
+                    E4 w[PLANES];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        float p = __builtin_amdgcn_exp2f(fmaf(acc[a][j][4 * q + r], scale, -lse) * 1.44269504f);
-                        if (here) p -= m + r == t ? 1.f : 0.f;
-                        if (left < TM && m + r >= left) p = 0.f;
-                        short s[PL];
-                        split<PL>(g * p, s);
+                        const float x = acc[a][j][4 * q + r];
+                        if constexpr (OUT == OUT_D) {
+                            float p = __builtin_amdgcn_exp2f(fmaf(x, scale, -lse) * 1.44269504f);
+                            if (here) p -= m + r == t ? 1.f : 0.f;
+                            if (left < TM && m + r >= left) p = 0.f;
+                            short s[PL];
+                            split<PL>(g * p, s);
 #pragma unroll
-                        for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
+                            for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
+                        } else {
+                            w[0][r] = (E)(x * unit);
+                        }
                     }
 #pragma unroll
-                    for (int q2 = 0; q2 < PL; ++q2)
-                        *reinterpret_cast<s16x4 *>(part + q2 * PART + (wn * 32 + (lane & 31)) * P + m * 2) = w[q2];
+                    for (int q2 = 0; q2 < PLANES; ++q2)
+                        *reinterpret_cast<E4 *>(part + q2 * PART + (wn * 32 + (lane & 31)) * P + m * ES) = w[q2];
                 }
             __syncthreads();
 #pragma unroll
-            for (int q2 = 0; q2 < PL; ++q2)
+            for (int q2 = 0; q2 < PLANES; ++q2)
 #pragma unroll
                 for (int k = 0; k < PIECES; ++k) {
-                    const int c = tid + k * 256, r = c / (TM / 8), x = c % (TM / 8);
-                    const int64_t row = n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31);
-                    *reinterpret_cast<u32x4 *>(o.d + q2 * o.plane_d + row * o.ldd + m0 + x * 8) =
-                        *reinterpret_cast<const u32x4 *>(part + q2 * PART + r * P + x * 16);
-                }
-        }
-    } else {
-        float unit = 1.f;
-        if constexpr (OUT == OUT_WEIGHT)
-            unit = PL == 2 ? ldexpf(*o.top_grad, -(kUnitExp + *o.all_exp)) : *o.top_grad;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
-#pragma unroll
-            for (int a = 0; a < NI; ++a)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t m = m0 + row_of(a, 4 * q);
-                    float x[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) x[r] = acc[a][j][4 * q + r];
-                    const int left = (int)(o.D - m < 4 ? o.D - m : 4);
-                    if (left <= 0) continue;
-                    if constexpr (OUT == OUT_HIDDEN) {
-                        if (i >= o.n) continue;
-                        float *s = o.sum + i * o.D + m;
-                        if (!o.first) {
-                            float old[4];
-                            load_part<float, 4>(s, left, old);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) x[r] += old[r];
-                        }
-                        store_part<float, 4>(s, left, x);
+                    const int c = tid + k * 256, r = c / ROWV;
+                    const int64_t row = n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31), m = m0 + c % ROWV * EV;
+                    const char *from = part + q2 * PART + r * P + c % ROWV * 16;
+                    if constexpr (OUT == OUT_D) {
+                        *reinterpret_cast<u32x4 *>(o.d + q2 * o.plane_d + row * o.ldd + m) =
+                            *reinterpret_cast<const u32x4 *>(from);
                     } else {
-                        const int64_t row = o.v0 + i;
-                        if (row >= o.V) continue;
+                        const int64_t to = OUT == OUT_WEIGHT ? o.v0 + row : row;
+                        if (to >= (OUT == OUT_WEIGHT ? o.V : o.sum_rows) || m >= o.D) continue;
+                        const int have = o.D - m < EV ? (int)(o.D - m) : EV;
+                        float x[EV];
+                        load_vec<E, EV>(reinterpret_cast<const E *>(from), x);
+                        if constexpr (OUT == OUT_SUM) {
+                            float *s = o.sum + to * o.D + m;
+                            if (!o.first) {
+                                float old[EV];
+                                load_part<float, EV>(s, have, old);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] *= unit;
-                        if (PL == 2) store_part<float, 4>(static_cast<float *>(o.out) + row * o.ld_out + m, left, x);
-                        else store_part<bf16, 4>(static_cast<bf16 *>(o.out) + row * o.ld_out + m, left, x);
+                                for (int e = 0; e < EV; ++e) x[e] += old[e];
+                            }
+                            store_part<float, EV>(s, have, x);
+                        } else {
+                            store_part<E, EV>(static_cast<E *>(o.out) + to * o.ld_out + m, have, x);
+                        }
                     }
                 }
         }
     }
 }
 
-// dH from the splits' sums, in order, in units of the loss.
+// A gradient from its splits' sums, in order, in units of the loss (`exp`: of
+// the operand's scale, for fp16 terms).
 template <class T>
-__global__ __launch_bounds__(256) void k_xent_hidden(const float *sum, int splits, int64_t n, int64_t D,
-                                                     const float *top_grad, const int *w_exp, T *out, int64_t ld)
+__global__ __launch_bounds__(256) void k_xent_sum(const float *sum, int splits, int64_t rows, int64_t D,
+                                                  const float *top_grad, const int *exp, T *out, int64_t ld)
 {
     const int64_t chunks = (D + 3) / 4, step = (int64_t)gridDim.x * 256;
-    const float unit = w_exp ? ldexpf(*top_grad, -(kUnitExp + *w_exp)) : *top_grad;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < n * chunks; c += step) {
+    const float unit = exp ? ldexpf(*top_grad, -(kUnitExp + *exp)) : *top_grad;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
         const int64_t i = c / chunks, k = (c - i * chunks) * 4;
         const int left = (int)(D - k < 4 ? D - k : 4);
         float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
         for (int q = 0; q < splits; ++q) {
             float y[4];
-            load_part<float, 4>(sum + ((int64_t)q * n + i) * D + k, left, y);
+            load_part<float, 4>(sum + ((int64_t)q * rows + i) * D + k, left, y);
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] += y[r];
         }
@@ -766,10 +771,10 @@ struct XentPlan {
     int *h_exp, *all_exp, *w_exp;
     float2 *part;
     short *h, *h_all, *w; // packed operands (the weight's unused where it serves in place)
-    float *sum;
+    float *sum, *w_sum;
     short *d;
     int64_t Kp, nr, piece;
-    int splits;
+    int splits, w_splits; // of the sums over the vocabulary (dH) and over the rows (dW)
     size_t bytes;
 };
 
@@ -777,26 +782,28 @@ struct XentPlan {
 // (logits of 8192 x 16384, bf16: K = 4096 at 1254 TFLOP/s, against 1040 in tiles
 // of 128).  Tiles of 128, of which a compute unit holds two, hide the start and
 // the end of one behind the products of the other and win where those are long
-// beside the sum (K = 512: 806 against 599; equal at 1024), and take outputs
-// with a side of at most 128 and grids that would leave compute units idle.
-constexpr int64_t kShortSum = 512;
+// beside the sum (K = 512: 806 against 599; equal at 1024; sums and the weight's
+// gradient, whose ends are shorter, are equal at 512), and take outputs with a
+// side of at most 128 and grids that would leave compute units idle.
+constexpr int64_t kShortSum = 512, kShorterSum = 256;
 inline int64_t tile_side(int64_t M, int64_t N, int64_t K, int splits, bool of_logits)
 {
-    if (M <= 128 || N <= 128 || (of_logits && K <= kShortSum)) return 128;
+    if (M <= 128 || N <= 128 || K <= (of_logits ? kShortSum : kShorterSum)) return 128;
     return ((M + 255) / 256) * ((N + 255) / 256) * splits < kCUs ? 128 : 256;
 }
 
-// How often dH's sum over a piece of the vocabulary is split: its output is
-// small (n x D) beside what it adds up, so where its tiles are fewer than the
-// compute units take at a time the sum is shared out.
-int hidden_splits(int64_t n, int64_t D, int64_t piece)
+// How often the sum of a gradient (D columns, `rows` rows, K summed values) is
+// split: where its tiles are fewer than the compute units take at a time, the
+// sum is shared out.
+int sum_splits(int64_t rows, int64_t D, int64_t K)
 {
-    const bool small = n <= 128 || D <= 128;
+    const bool small = rows <= 128 || D <= 128;
     const int64_t side = small ? 128 : 256, slots = small ? 2 * kCUs : kCUs;
-    int64_t s = slots / (((D + side - 1) / side) * ((n + side - 1) / side));
-    if (s > piece / kSplitK) s = piece / kSplitK;
+    int64_t s = slots / (((D + side - 1) / side) * ((rows + side - 1) / side));
+    if (s > K / kSplitK) s = K / kSplitK;
     return (int)(s < 1 ? 1 : s);
 }
+
 // Rows of d: whole tiles, so that they are written without a test.
 inline int64_t d_rows(int64_t n) { return n <= 128 ? 128 : up(n, 256); }
 
@@ -834,8 +841,10 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     p.w = (short *)take((size_t)PL * V * p.Kp * 2);
     if (piece) {
         if (PL == 2) p.h_all = (short *)take((size_t)PL * n * p.Kp * 2);
-        p.splits = hidden_splits(n, D, piece);
+        p.splits = sum_splits(n, D, piece);
         p.sum = (float *)take(4 * (size_t)p.splits * n * D);
+        p.w_splits = piece >= V ? sum_splits(V, D, n) : 1;
+        if (p.w_splits > 1) p.w_sum = (float *)take(4 * (size_t)p.w_splits * V * D);
         p.d = (short *)take((size_t)PL * p.nr * piece * 2);
     }
     p.bytes = off;
@@ -859,7 +868,7 @@ unsigned blocks_for(int64_t threads)
 template <int PL, bool XT, bool YT, int OUT>
 int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s)
 {
-    const int splits = OUT == OUT_HIDDEN ? o.splits : 1;
+    const int splits = OUT == OUT_SUM ? o.splits : 1;
     const int64_t side = tile_side(M, N, K, splits, OUT == OUT_STATS || OUT == OUT_D);
     const int64_t mt = (M + side - 1) / side, nt = (N + side - 1) / side;
     const dim3 grid(tile_grid(mt, nt, splits));
@@ -910,11 +919,9 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.h_exp = p.h_exp;
     o.w_exp = p.w_exp;
     o.all_exp = p.all_exp;
-    o.splits = p.splits;
     o.d = p.d;
     o.ldd = piece;
     o.plane_d = p.nr * piece;
-    o.sum = p.sum;
     const int64_t tiles = product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(1024), 0, s, p.part, tiles, a.n, a.V,
                        a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
@@ -937,16 +944,31 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         // d in whole tiles: what lies past the rows and the vocabulary is written as zeros
         product<PL, false, false, OUT_D>(wp, h, cols, p.nr, p.Kp, o, s);
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
+        o.sum = p.sum;
+        o.sum_rows = a.n;
+        o.splits = p.splits;
         o.split_k = up((cols + p.splits - 1) / p.splits, kPadK);
-        product<PL, true, false, OUT_HIDDEN>(wp, d, a.D, a.n, cols, o, s);
-        o.out = a.dw;
-        o.ld_out = a.ld_dw;
-        product<PL, true, true, OUT_WEIGHT>(h_all, d, a.D, here, up(a.n, kPadK), o, s);
+        product<PL, true, false, OUT_SUM>(wp, d, a.D, a.n, cols, o, s);
+        const int64_t rows = up(a.n, kPadK);
+        if (p.w_splits == 1) {
+            o.out = a.dw;
+            o.ld_out = a.ld_dw;
+            product<PL, true, true, OUT_WEIGHT>(h_all, d, a.D, here, rows, o, s);
+            continue;
+        }
+        o.sum = p.w_sum;
+        o.sum_rows = a.V;
+        o.splits = p.w_splits;
+        o.split_k = up((rows + p.w_splits - 1) / p.w_splits, kPadK);
+        product<PL, true, true, OUT_SUM>(h_all, d, a.D, a.V, rows, o, s);
+        hipLaunchKernelGGL(k_xent_sum<T>, dim3(blocks_for(a.V * ((a.D + 3) / 4))), dim3(256), 0, s, p.w_sum,
+                           (int)((rows + o.split_k - 1) / o.split_k), a.V, a.D, p.top_grad,
+                           PL == 2 ? p.all_exp : nullptr, static_cast<T *>(a.dw), a.ld_dw);
     }
     // splits past the first piece's end have written nothing
     const int64_t first = up(a.V < piece ? a.V : piece, kRound);
     const int64_t per = up((first + p.splits - 1) / p.splits, kPadK);
-    hipLaunchKernelGGL(k_xent_hidden<T>, dim3(blocks_for(a.n * ((a.D + 3) / 4))), dim3(256), 0, s, p.sum,
+    hipLaunchKernelGGL(k_xent_sum<T>, dim3(blocks_for(a.n * ((a.D + 3) / 4))), dim3(256), 0, s, p.sum,
                        (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr,
                        static_cast<T *>(a.dh), a.ld_dh);
     return hipGetLastError();
