@@ -38,6 +38,7 @@ constexpr int kRound = 256;            // columns of d are padded to this
 constexpr int kLeast = 128;            // rows and columns of the smallest tile
 constexpr int kPadK = 64;              // packed rows are padded to this
 constexpr int kMaxParts = 1024;        // blocks of the weight's largest magnitude
+constexpr int64_t kFewRows = 128;      // fp32 rows whose statistics take no packed operands
 constexpr int kUnitExp = 15;           // fp16 terms: d is kept in units of 2^-15
 
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -262,6 +263,53 @@ __device__ __forceinline__ void interleave()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Two (maximum, sum of exponentials relative to it) as one.
+__device__ __forceinline__ float2 join_sums(float2 a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
+    return make_float2(m, a.y * __expf(a.x - ref) + b.y * __expf(b.x - ref));
+}
+
+// Maximum and sum of exponentials of one column of a wave's NI 32 x 32 tiles of
+// logits (both halves of the wave), whose values are z / unit; the target's
+// logit is stored where it is among them.  `left`: rows of the tile that exist,
+// first: the wave's first row.  The maximum is taken and subtracted before the
+// values are scaled.
+template <int NI, int NJ, class R>
+__device__ __forceinline__ void column_stats(f32x16 (&acc)[NI][NJ], int j, R row_of, int64_t left, int tile_rows,
+                                             int64_t t, int first, float unit, float *target_logit, float &top,
+                                             float &sum)
+{
+    if (left < tile_rows) { // the vocabulary ends in this tile
+#pragma unroll
+        for (int a = 0; a < NI; ++a)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (row_of(a, r) >= left) acc[a][j][r] = -INFINITY;
+    }
+    if (__any(t >= first && t < first + 32 * NI)) {
+#pragma unroll
+        for (int a = 0; a < NI; ++a)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (row_of(a, r) == t) *target_logit = acc[a][j][r] * unit;
+    }
+    top = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int a = 0; a < NI; ++a)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[a][j][r]);
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float ref = top == -INFINITY ? 0.f : top, base = unit * 1.44269504f;
+#pragma unroll
+    for (int a = 0; a < NI; ++a)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[a][j][r] - ref) * base);
+    top *= unit;
+    sum += __shfl_xor(sum, 32, 64);
+}
+
 // C[m][n] = sum_k X[m][k] Y[n][k] over tiles of (64 NI) x (64 NJ); four waves,
 // 32x32x16 matrix instructions, NI x NJ of them per wave.  Lane l of a wave
 // holds column n = l % 32 and the rows m = 8 (r / 4) + 4 (l / 32) + r % 4 of
@@ -391,36 +439,11 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             const int64_t i = n0 + nl;
             const int64_t t = i < o.n ? o.targets[i] - m0 : -1;
             const int64_t left = o.V - m0;
-            // the accumulators are logits times a power of two; the maximum is
-            // taken and subtracted before they are scaled
+            // the accumulators are logits times a power of two
             const float unit = PL == 2 && i < o.n ? ldexpf(1.f, -(o.h_exp[i] + *o.w_exp)) : 1.f;
-            if (left < TM) { // the vocabulary ends in this tile
-#pragma unroll
-                for (int a = 0; a < NI; ++a)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (row_of(a, r) >= left) acc[a][j][r] = -INFINITY;
-            }
-            if (__any(t >= wm * (TM / 2) && t < (wm + 1) * (TM / 2))) {
-#pragma unroll
-                for (int a = 0; a < NI; ++a)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (row_of(a, r) == t) o.target_logit[i] = acc[a][j][r] * unit;
-            }
-            float top = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int a = 0; a < NI; ++a)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[a][j][r]);
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float ref = top == -INFINITY ? 0.f : top, base = unit * 1.44269504f;
-#pragma unroll
-            for (int a = 0; a < NI; ++a)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[a][j][r] - ref) * base);
-            top *= unit;
-            sum += __shfl_xor(sum, 32, 64);
+            float top, sum;
+            column_stats(acc, j, row_of, left, TM, t, wm * (TM / 2), unit, o.target_logit + (i < o.n ? i : 0), top,
+                         sum);
             if (lane < 32) {
                 red[0][wm][nl] = top;
                 red[1][wm][nl] = sum;
@@ -525,6 +548,89 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                     }
                 }
         }
+    }
+}
+
+// The statistics of at most 32 NB rows of fp32: the weight is read once, as it
+// is, by the fp32 matrix instructions.  Splitting it into fp16 terms first
+// costs three more passes over it, more than the slower products do here
+// (50000 x 1024: 1 row 60 us against 198, 64 rows 87 against 204).  A wave has 32
+// MA rows of the weight; a lane reads four values of a row at a time, and each
+// instruction takes the same one of the four from both halves of the wave.
+template <int MA, int NB>
+__global__ __launch_bounds__(256) void k_xent_few(const float *w, int64_t ld_w, const float *h, int64_t ld_h, int64_t D,
+                                                  Output o)
+{
+    constexpr int TM = 128 * MA, STEP = 32;
+    __shared__ float red[2][4][32 * NB];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = (lane >> 5) * 4;
+    const int64_t m0 = (int64_t)blockIdx.x * TM;
+    const float *wr[MA], *hr[NB];
+#pragma unroll
+    for (int a = 0; a < MA; ++a) {
+        const int64_t r = m0 + wave * 32 * MA + a * 32 + (lane & 31);
+        wr[a] = w + (r < o.V ? r : o.V - 1) * ld_w + half;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t r = b * 32 + (lane & 31);
+        hr[b] = h + (r < o.n ? r : o.n - 1) * ld_h + half;
+    }
+    f32x16 acc[MA][NB];
+#pragma unroll
+    for (int a = 0; a < MA; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+    auto steps = [&](int64_t k, auto whole) {
+        constexpr int C = STEP / 8;
+        float x[MA][C][4], y[NB][C][4];
+        auto take = [&](const float *p, int c, float (&v)[4]) {
+            const int64_t at = k + c * 8, left = D - half - at;
+            if constexpr (decltype(whole)::value) load_vec<float, 4>(p + at, v);
+            else load_part<float, 4>(p + (left > 0 ? at : 0), (int)(left < 0 ? 0 : left < 4 ? left : 4), v);
+        };
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int a = 0; a < MA; ++a) take(wr[a], c, x[a][c]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) take(hr[b], c, y[b][c]);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int a = 0; a < MA; ++a)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(x[a][c][e], y[b][c][e], acc[a][b], 0, 0, 0);
+    };
+    int64_t k = 0;
+    for (; k + STEP <= D; k += STEP) steps(k, std::true_type());
+    if (k < D) steps(k, std::false_type());
+    auto row_of = [&](int a, int r) { return wave * 32 * MA + a * 32 + 8 * (r / 4) + 4 * (lane >> 5) + (r % 4); };
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t i = b * 32 + (lane & 31);
+        const int64_t t = i < o.n ? o.targets[i] - m0 : -1;
+        float top, sum;
+        column_stats(acc, b, row_of, o.V - m0, TM, t, wave * 32 * MA, 1.f, o.target_logit + (i < o.n ? i : 0), top,
+                     sum);
+        if (lane < 32) {
+            red[0][wave][i] = top;
+            red[1][wave][i] = sum;
+        }
+    }
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i < 32 * NB && i < o.n) {
+        float2 all = make_float2(red[0][0][i], red[1][0][i]);
+#pragma unroll
+        for (int q = 1; q < 4; ++q) all = join_sums(all, make_float2(red[0][q][i], red[1][q][i]));
+        o.part[blockIdx.x * o.n + i] = all;
     }
 }
 
@@ -680,13 +786,6 @@ __global__ __launch_bounds__(256) void k_pack_weight(const T *src, int64_t ld_sr
         const int64_t r = c / chunks, k = (c - r * chunks) * 8;
         pack_piece<T, PL>(src + r * ld_src + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
     }
-}
-
-// Two (maximum, sum of exponentials relative to it) as one.
-__device__ __forceinline__ float2 join_sums(float2 a, float2 b)
-{
-    const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
-    return make_float2(m, a.y * __expf(a.x - ref) + b.y * __expf(b.x - ref));
 }
 
 // lse and loss of sixteen rows per block from the tiles' maxima and sums, 64
@@ -879,6 +978,18 @@ int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_
     return mt;
 }
 
+// Statistics of at most 128 fp32 rows without packed operands; returns the tiles.
+int64_t few_rows(const XentArgs &a, const Output &o, hipStream_t s)
+{
+    const float *w = static_cast<const float *>(a.weight), *h = static_cast<const float *>(a.hidden);
+    const int64_t side = a.n <= 32 ? 128 : 256, tiles = (a.V + side - 1) / side;
+    const dim3 grid((unsigned)tiles);
+    if (a.n <= 32) hipLaunchKernelGGL((k_xent_few<1, 1>), grid, dim3(256), 0, s, w, a.ld_w, h, a.ld_h, a.D, o);
+    else if (a.n <= 64) hipLaunchKernelGGL((k_xent_few<2, 2>), grid, dim3(256), 0, s, w, a.ld_w, h, a.ld_h, a.D, o);
+    else hipLaunchKernelGGL((k_xent_few<2, 4>), grid, dim3(256), 0, s, w, a.ld_w, h, a.ld_h, a.D, o);
+    return tiles;
+}
+
 template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
@@ -886,25 +997,6 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     while (piece > kRound && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
         piece = up(piece / 2, kRound);
     const XentPlan p = plan_xent(a.n, a.V, a.D, PL, piece, a.ws);
-    const T *hs = static_cast<const T *>(a.hidden), *ws = static_cast<const T *>(a.weight);
-    Operand h{reinterpret_cast<const short *>(hs), a.ld_h, 0, a.n, a.D};
-    if (grad || !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp)) {
-        h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
-        hipLaunchKernelGGL((k_pack_rows<T, PL>), dim3(blocks_for(a.n * 64)), dim3(256), 0, s, hs, a.ld_h, a.n, a.D, p.h,
-                           p.Kp, a.n * p.Kp, p.h_exp, p.tops, grad ? a.targets : nullptr, a.ignore, a.V);
-    }
-    Operand w{reinterpret_cast<const short *>(ws), a.ld_w, 0, a.V, a.D};
-    if (!in_place<T, PL>(ws, a.ld_w, a.D, p.Kp)) {
-        w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
-        unsigned parts = 0;
-        if constexpr (PL == 2) {
-            parts = blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1);
-            if (parts > (unsigned)kMaxParts) parts = kMaxParts;
-            hipLaunchKernelGGL(k_weight_top, dim3(parts), dim3(256), 0, s, ws, a.ld_w, a.V, a.D, p.w_part);
-        }
-        hipLaunchKernelGGL((k_pack_weight<T, PL>), dim3(blocks_for(a.V * (p.Kp / 8))), dim3(256), 0, s, ws, a.ld_w, a.V,
-                           a.D, p.w, p.Kp, a.V * p.Kp, p.w_part, (int)parts, p.w_exp);
-    }
     Output o{};
     o.n = a.n;
     o.V = a.V;
@@ -922,7 +1014,28 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.d = p.d;
     o.ldd = piece;
     o.plane_d = p.nr * piece;
-    const int64_t tiles = product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
+    const bool few = PL == 2 && a.n <= kFewRows;
+    const T *hs = static_cast<const T *>(a.hidden), *ws = static_cast<const T *>(a.weight);
+    Operand h{reinterpret_cast<const short *>(hs), a.ld_h, 0, a.n, a.D};
+    if (grad || (!few && !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp))) {
+        h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
+        hipLaunchKernelGGL((k_pack_rows<T, PL>), dim3(blocks_for(a.n * 64)), dim3(256), 0, s, hs, a.ld_h, a.n, a.D, p.h,
+                           p.Kp, a.n * p.Kp, p.h_exp, p.tops, grad ? a.targets : nullptr, a.ignore, a.V);
+    }
+    Operand w{reinterpret_cast<const short *>(ws), a.ld_w, 0, a.V, a.D};
+    if ((grad || !few) && !in_place<T, PL>(ws, a.ld_w, a.D, p.Kp)) {
+        w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
+        unsigned parts = 0;
+        if constexpr (PL == 2) {
+            parts = blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1);
+            if (parts > (unsigned)kMaxParts) parts = kMaxParts;
+            hipLaunchKernelGGL(k_weight_top, dim3(parts), dim3(256), 0, s, ws, a.ld_w, a.V, a.D, p.w_part);
+        }
+        hipLaunchKernelGGL((k_pack_weight<T, PL>), dim3(blocks_for(a.V * (p.Kp / 8))), dim3(256), 0, s, ws, a.ld_w, a.V,
+                           a.D, p.w, p.Kp, a.V * p.Kp, p.w_part, (int)parts, p.w_exp);
+    }
+    const int64_t tiles = few ? few_rows(a, o, s)
+                              : product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
     hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(1024), 0, s, p.part, tiles, a.n, a.V,
                        a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
     if (!grad) return hipGetLastError();

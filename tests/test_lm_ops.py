@@ -371,6 +371,21 @@ def test_xent_in_large_tiles(n, V, D, gap, t):
     test_xent_and_gradients(n, V, D, gap, t)
 
 
+@pytest.mark.parametrize("n", [1, 5, 31, 32, 33, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("V,D,gap", [(1, 5, 0), (127, 31, 3), (128, 32, 0), (257, 33, 1), (1000, 100, 0), (3001, 516, 4)])
+def test_xent_scores_of_few_rows(n, V, D, gap):
+    # fp32 rows up to 128 take the weight as it is, more are split into terms
+    h, w, target, grad = xent_inputs(n, V, D, F32, gap, n + V + D)
+    z, lse, loss, _, _ = xent_reference(h, w, target, grad, -100)
+    ez = (6 * D + 8) * U32 * (h.double().abs() @ w.double().abs().t()).amax(1)
+    es = ez + U32 * (204 + V / 1024 + 2 * (z - lse[:, None]).abs().amax(1))
+    x = tt.VocabCrossEntropy(V, D)
+    got_loss, got_lse = x.forward(h, w, target)
+    close(got_lse, lse, es + 4 * U32 * lse.abs(), "lse")
+    close(got_loss, loss, es + ez + 4 * U32 * (lse.abs() + z.abs().amax(1)), "loss")
+    assert x.poll_error() == 0
+
+
 @pytest.mark.parametrize("t", [F32, BF16])
 def test_xent_ignores_what_ignored_rows_hold(t):
     n, V, D = 70, 900, 96
