@@ -335,7 +335,8 @@ hipError_t norm_forward(const NormArgs &a, hipStream_t s)
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
         const int64_t need = (a.n + NormShape<TPR>::rows - 1) / NormShape<TPR>::rows;
         const int grid = (int)(need < kNormBlocks ? need : kNormBlocks);
-        hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, decltype(whole)::value>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a);
+        hipLaunchKernelGGL((k_norm_fwd<T, TPR, NV, decltype(whole)::value>), dim3(grid),
+                           dim3(NormShape<TPR>::threads), 0, s, a);
         return hipGetLastError();
     });
 }
@@ -348,7 +349,8 @@ hipError_t norm_backward(const NormArgs &a, hipStream_t s)
         const int64_t need = (a.n + NormShape<TPR>::rows - 1) / NormShape<TPR>::rows;
         const int grid = (int)(need < norm_grad_blocks<TPR>() ? need : norm_grad_blocks<TPR>());
         float *part = (a.dgamma || a.dbeta) ? reinterpret_cast<float *>(a.ws + TT_EMB_STATUS_BYTES) : nullptr;
-        hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV, decltype(whole)::value>), dim3(grid), dim3(NormShape<TPR>::threads), 0, s, a, part);
+        hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV, decltype(whole)::value>), dim3(grid),
+                           dim3(NormShape<TPR>::threads), 0, s, a, part);
         if (part) {
             const dim3 cols((unsigned)((a.D + 63) / 64), 2);
             if (a.D % 4 == 0)

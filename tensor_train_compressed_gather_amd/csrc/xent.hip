@@ -459,7 +459,8 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
     } else {
         // 64 rows at a time pass through LDS, so that they are written in whole
         // lines: a lane holds four columns of one row, a wave 32 rows
-        typedef std::conditional_t<OUT == OUT_D, short, std::conditional_t<OUT == OUT_WEIGHT && PL == 1, bf16, float>> E;
+        typedef std::conditional_t<OUT == OUT_WEIGHT && PL == 1, bf16, float> E32;
+        typedef std::conditional_t<OUT == OUT_D, short, E32> E;
         typedef E E4 __attribute__((ext_vector_type(4)));
         constexpr int ES = (int)sizeof(E), EV = 16 / ES, PLANES = OUT == OUT_D ? PL : 1;
         constexpr int P = TM * ES + 16, PART = 64 * P, ROWV = TM / EV, PIECES = 64 * ROWV / 256;
@@ -688,174 +689,256 @@ __device__ __forceinline__ void pack_piece(const T *src, int64_t left, int e, bo
     for (int q = 0; q < PL; ++q) *reinterpret_cast<s16x8 *>(dst + q * plane) = w[q];
 }
 
+// Jobs around the products, each done by blocks [0, blocks) of `threads`
+// threads.  Jobs that do not wait for each other share a launch: at small sizes
+// a launch costs more than they do.
+template <class A, class B>
+struct Both {
+    static constexpr int threads = A::threads;
+    static_assert(A::threads == B::threads, "one block size");
+    A a;
+    B b;
+    int na;
+    __device__ void operator()(int block, int blocks) const
+    {
+        if (block < na) a(block, na);
+        else b(block - na, blocks - na);
+    }
+};
+template <int THREADS>
+struct NoJobOf {
+    static constexpr int threads = THREADS;
+    __device__ void operator()(int, int) const {}
+};
+template <class F>
+__global__ __launch_bounds__(F::threads) void k_jobs(F f)
+{
+    f((int)blockIdx.x, (int)gridDim.x);
+}
+
 // Hidden rows as planes with `ld` columns, zero past D; a wave per row.  fp16
 // terms: each row scaled by a power of two of its own, and the largest
 // magnitude of each row that counts left in `tops`.  With targets: a row that
 // is ignored and holds a value that is not finite is taken as zeros, so that
 // its zero gradient stays zero.
 template <class T, int PL>
-__global__ __launch_bounds__(256) void k_pack_rows(const T *src, int64_t ld_src, int64_t rows, int64_t D, short *dst,
-                                                   int64_t ld, int64_t plane, int *exps, float *tops,
-                                                   const int64_t *targets, int64_t ignore, int64_t V)
-{
-    const int lane = threadIdx.x & 63;
-    const int64_t step = (int64_t)gridDim.x * 4;
-    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += step) {
-        const T *row = src + r * ld_src;
-        int e = 0;
-        bool clear = false;
-        if (PL == 2 || targets) {
-            float top = 0.f;
-            bool odd = false;
-            for (int64_t k = lane * 8; k < D; k += 512) {
-                float x[8];
-                load_part<T, 8>(row + k, (int)(D - k < 8 ? D - k : 8), x);
+struct PackRows {
+    static constexpr int threads = 256;
+    const T *src;
+    int64_t ld_src, rows, D;
+    short *dst;
+    int64_t ld, plane;
+    int *exps;
+    float *tops;
+    const int64_t *targets;
+    int64_t ignore, V;
+
+    __device__ void operator()(int block, int blocks) const
+    {
+        const int lane = threadIdx.x & 63;
+        for (int64_t r = (int64_t)block * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)blocks * 4) {
+            const T *row = src + r * ld_src;
+            int e = 0;
+            bool clear = false;
+            if (PL == 2 || targets) {
+                float top = 0.f;
+                bool odd = false;
+                for (int64_t k = lane * 8; k < D; k += 512) {
+                    float x[8];
+                    load_part<T, 8>(row + k, (int)(D - k < 8 ? D - k : 8), x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    top = fmaxf(top, finite_abs(x[i]));
-                    odd = odd || !(fabsf(x[i]) < INFINITY);
+                    for (int i = 0; i < 8; ++i) {
+                        top = fmaxf(top, finite_abs(x[i]));
+                        odd = odd || !(fabsf(x[i]) < INFINITY);
+                    }
                 }
-            }
 #pragma unroll
-            for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-            if (targets) {
-                const bool counts = row_counts(targets[r], ignore, V);
-                clear = __any(odd) && !counts;
-                if (PL == 2 && lane == 0) tops[r] = counts ? top : 0.f;
+                for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+                if (targets) {
+                    const bool counts = row_counts(targets[r], ignore, V);
+                    clear = __any(odd) && !counts;
+                    if (PL == 2 && lane == 0) tops[r] = counts ? top : 0.f;
+                }
+                e = PL == 2 && !clear ? scale_exp(top) : 0;
+                if (PL == 2 && lane == 0) exps[r] = e;
             }
-            e = PL == 2 && !clear ? scale_exp(top) : 0;
-            if (PL == 2 && lane == 0) exps[r] = e;
+            for (int64_t k = lane * 8; k < ld; k += 512)
+                pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, clear, dst + r * ld + k, plane);
         }
-        for (int64_t k = lane * 8; k < ld; k += 512)
-            pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, clear, dst + r * ld + k, plane);
     }
-}
+};
 
 // The rows that count as fp16 planes scaled by one power of two, the others as
 // zeros: the operand of the weight's gradient.
-__global__ __launch_bounds__(256) void k_pack_counting(const float *src, int64_t ld_src, int64_t rows, int64_t D,
-                                                       short *dst, int64_t ld, int64_t plane, const int *exp,
-                                                       const int64_t *targets, int64_t ignore, int64_t V)
-{
-    const int64_t chunks = ld / 8, step = (int64_t)gridDim.x * 256;
-    const int e = *exp;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
-        const int64_t r = c / chunks, k = (c - r * chunks) * 8;
-        pack_piece<float, 2>(src + r * ld_src + (k < D ? k : 0), D - k, e, !row_counts(targets[r], ignore, V),
-                             dst + r * ld + k, plane);
+struct PackCounting {
+    static constexpr int threads = 1024;
+    const float *src;
+    int64_t ld_src, rows, D;
+    short *dst;
+    int64_t ld, plane;
+    const int *exp;
+    const int64_t *targets;
+    int64_t ignore, V;
+
+    __device__ void operator()(int block, int blocks) const
+    {
+        const int64_t chunks = ld / 8, step = (int64_t)blocks * threads;
+        const int e = *exp;
+        for (int64_t c = (int64_t)block * threads + threadIdx.x; c < rows * chunks; c += step) {
+            const int64_t r = c / chunks, k = (c - r * chunks) * 8;
+            pack_piece<float, 2>(src + r * ld_src + (k < D ? k : 0), D - k, e, !row_counts(targets[r], ignore, V),
+                                 dst + r * ld + k, plane);
+        }
     }
-}
+};
 
 // Largest finite magnitude of the weight, per block.
-__global__ __launch_bounds__(256) void k_weight_top(const float *src, int64_t ld, int64_t rows, int64_t D, float *part)
-{
-    __shared__ float sm[4];
-    const int64_t chunks = (D + 7) / 8, step = (int64_t)gridDim.x * 256;
-    float top = 0.f;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
-        const int64_t r = c / chunks, k = (c - r * chunks) * 8;
-        float x[8];
-        load_part<float, 8>(src + r * ld + k, (int)(D - k < 8 ? D - k : 8), x);
+struct WeightTop {
+    static constexpr int threads = 256;
+    const float *src;
+    int64_t ld, rows, D;
+    float *part;
+
+    __device__ void operator()(int block, int blocks) const
+    {
+        __shared__ float sm[4];
+        const int64_t chunks = (D + 7) / 8, step = (int64_t)blocks * 256;
+        float top = 0.f;
+        for (int64_t c = (int64_t)block * 256 + threadIdx.x; c < rows * chunks; c += step) {
+            const int64_t r = c / chunks, k = (c - r * chunks) * 8;
+            float x[8];
+            load_part<float, 8>(src + r * ld + k, (int)(D - k < 8 ? D - k : 8), x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(x[i]));
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(x[i]));
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) part[block] = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) part[blockIdx.x] = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-}
+};
 
 // The weight as planes with `ld` columns, zero past D.  fp16 terms: scaled by
 // one power of two, from the largest of the `parts` magnitudes.
 template <class T, int PL>
-__global__ __launch_bounds__(256) void k_pack_weight(const T *src, int64_t ld_src, int64_t rows, int64_t D, short *dst,
-                                                     int64_t ld, int64_t plane, const float *part, int parts, int *exp)
-{
-    int e = 0;
-    if constexpr (PL == 2) {
-        float top = 0.f;
-        for (int i = threadIdx.x & 63; i < parts; i += 64) top = fmaxf(top, part[i]);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-        e = scale_exp(top);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *exp = e;
-    }
-    const int64_t chunks = ld / 8, step = (int64_t)gridDim.x * 256;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
-        const int64_t r = c / chunks, k = (c - r * chunks) * 8;
-        pack_piece<T, PL>(src + r * ld_src + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
-    }
-}
+struct PackWeight {
+    static constexpr int threads = 256;
+    const T *src;
+    int64_t ld_src, rows, D;
+    short *dst;
+    int64_t ld, plane;
+    const float *part;
+    int parts;
+    int *exp;
 
-// lse and loss of sixteen rows per block from the tiles' maxima and sums, 64
-// groups of tiles joined in order.
-__global__ __launch_bounds__(1024) void k_xent_join(const float2 *part, int64_t tiles, int64_t n, int64_t V,
-                                                    const int64_t *targets, int64_t ignore, const float *target_logit,
-                                                    float *loss, float *lse, int *status)
-{
-    __shared__ float2 sm[64][16];
-    const int r = threadIdx.x & 15, g = threadIdx.x >> 4;
-    const int64_t i = (int64_t)blockIdx.x * 16 + r, ic = i < n ? i : n - 1;
-    float2 all = make_float2(-INFINITY, 0.f);
-    for (int64_t t = g; t < tiles; t += 4 * 64) {
-        float2 p[4];
+    __device__ void operator()(int block, int blocks) const
+    {
+        int e = 0;
+        if constexpr (PL == 2) {
+            float top = 0.f;
+            for (int i = threadIdx.x & 63; i < parts; i += 64) top = fmaxf(top, part[i]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            p[u] = part[(t + u * 64 < tiles ? t + u * 64 : t) * n + ic];
-            if (t + u * 64 >= tiles) p[u] = make_float2(-INFINITY, 0.f);
+            for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+            e = scale_exp(top);
+            if (block == 0 && threadIdx.x == 0) *exp = e;
         }
-        all = join_sums(all, join_sums(join_sums(p[0], p[1]), join_sums(p[2], p[3])));
+        const int64_t chunks = ld / 8, step = (int64_t)blocks * 256;
+        for (int64_t c = (int64_t)block * 256 + threadIdx.x; c < rows * chunks; c += step) {
+            const int64_t r = c / chunks, k = (c - r * chunks) * 8;
+            pack_piece<T, PL>(src + r * ld_src + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
+        }
     }
-    sm[g][r] = all;
-    __syncthreads();
-    if (g || i >= n) return;
-    float top = -INFINITY, sum = 0.f;
-    for (int q = 0; q < 64; ++q) top = fmaxf(top, sm[q][r].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    for (int q = 0; q < 64; ++q) sum += sm[q][r].y * __expf(sm[q][r].x - ref);
-    const float z = (top == -INFINITY ? 0.f : top) + logf(sum);
-    const int64_t t = targets[i];
-    const bool in = t >= 0 && t < V;
-    if (!in && t != ignore) atomicOr(status + ST_ERR, (int)STB_INDEX);
-    lse[i] = z;
-    loss[i] = in && t != ignore ? z - target_logit[i] : 0.f;
-}
+};
 
 // The unit of d: the largest |grad_loss| of the rows that count.  With equal
 // gradients (a mean over the rows) d is exp(z - lse) - [v = target] in this
 // unit, and the target's -1 + p, the largest term of both gradients, rounds to
 // bf16 without error for small p.  1 where there is nothing to scale.  fp16
-// terms: also the exponent for all rows together, from their largest.
-__global__ __launch_bounds__(1024) void k_xent_units(const float *grad, const int64_t *targets, int64_t ignore,
-                                                     int64_t n, int64_t V, const float *tops, float *unit,
-                                                     int *all_exp)
-{
-    __shared__ float sm[2][16];
-    float m = 0.f, h = 0.f;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) {
-        if (row_counts(targets[i], ignore, V)) m = fmaxf(m, fabsf(grad[i]));
-        if (tops) h = fmaxf(h, tops[i]);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        m = fmaxf(m, __shfl_xor(m, o, 64));
-        h = fmaxf(h, __shfl_xor(h, o, 64));
-    }
-    if ((threadIdx.x & 63) == 0) {
-        sm[0][threadIdx.x >> 6] = m;
-        sm[1][threadIdx.x >> 6] = h;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 16; ++w) {
-            m = fmaxf(m, sm[0][w]);
-            h = fmaxf(h, sm[1][w]);
+// terms: also the exponent for all rows together, from their largest.  One block.
+struct Units {
+    static constexpr int threads = 256;
+    const float *grad;
+    const int64_t *targets;
+    int64_t ignore, n, V;
+    const float *tops;
+    float *unit;
+    int *all_exp;
+
+    __device__ void operator()(int, int) const
+    {
+        __shared__ float sm[2][4];
+        float m = 0.f, h = 0.f;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < n; i += 256) {
+            if (row_counts(targets[i], ignore, V)) m = fmaxf(m, fabsf(grad[i]));
+            if (tops) h = fmaxf(h, tops[i]);
         }
-        *unit = m > 0.f && m < INFINITY ? m : 1.f;
-        *all_exp = scale_exp(h);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            m = fmaxf(m, __shfl_xor(m, o, 64));
+            h = fmaxf(h, __shfl_xor(h, o, 64));
+        }
+        if ((threadIdx.x & 63) == 0) {
+            sm[0][threadIdx.x >> 6] = m;
+            sm[1][threadIdx.x >> 6] = h;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 4; ++w) {
+                m = fmaxf(m, sm[0][w]);
+                h = fmaxf(h, sm[1][w]);
+            }
+            *unit = m > 0.f && m < INFINITY ? m : 1.f;
+            *all_exp = scale_exp(h);
+        }
     }
-}
+};
+
+// lse and loss of sixteen rows per block from the tiles' maxima and sums, 64
+// groups of tiles joined in order.
+struct Join {
+    static constexpr int threads = 1024;
+    const float2 *part;
+    int64_t tiles, n, V;
+    const int64_t *targets;
+    int64_t ignore;
+    const float *target_logit;
+    float *loss, *lse;
+    int *status;
+
+    __device__ void operator()(int block, int) const
+    {
+        __shared__ float2 sm[64][16];
+        const int r = threadIdx.x & 15, g = threadIdx.x >> 4;
+        const int64_t i = (int64_t)block * 16 + r, ic = i < n ? i : n - 1;
+        float2 all = make_float2(-INFINITY, 0.f);
+        for (int64_t t = g; t < tiles; t += 4 * 64) {
+            float2 p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                p[u] = part[(t + u * 64 < tiles ? t + u * 64 : t) * n + ic];
+                if (t + u * 64 >= tiles) p[u] = make_float2(-INFINITY, 0.f);
+            }
+            all = join_sums(all, join_sums(join_sums(p[0], p[1]), join_sums(p[2], p[3])));
+        }
+        sm[g][r] = all;
+        __syncthreads();
+        if (g || i >= n) return;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+        for (int q = 0; q < 64; ++q) top = fmaxf(top, sm[q][r].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 8
+        for (int q = 0; q < 64; ++q) sum += sm[q][r].y * __expf(sm[q][r].x - ref);
+        const float z = (top == -INFINITY ? 0.f : top) + logf(sum);
+        const int64_t t = targets[i];
+        const bool in = t >= 0 && t < V;
+        if (!in && t != ignore) atomicOr(status + ST_ERR, (int)STB_INDEX);
+        lse[i] = z;
+        loss[i] = in && t != ignore ? z - target_logit[i] : 0.f;
+    }
+};
 
 template <class T>
 __global__ __launch_bounds__(256) void k_xent_clear(T *p, int64_t ld, int64_t rows, int64_t D)
@@ -978,6 +1061,15 @@ int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_
     return mt;
 }
 
+// One launch for two jobs of na and nb blocks (none for none).
+template <class A, class B>
+void run_jobs(const A &a, int na, const B &b, int nb, hipStream_t s)
+{
+    if (na + nb == 0) return;
+    typedef Both<A, B> F;
+    hipLaunchKernelGGL(k_jobs<F>, dim3((unsigned)(na + nb)), dim3(F::threads), 0, s, F{a, b, na});
+}
+
 // Statistics of at most 128 fp32 rows without packed operands; returns the tiles.
 int64_t few_rows(const XentArgs &a, const Output &o, hipStream_t s)
 {
@@ -1017,36 +1109,45 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     const bool few = PL == 2 && a.n <= kFewRows;
     const T *hs = static_cast<const T *>(a.hidden), *ws = static_cast<const T *>(a.weight);
     Operand h{reinterpret_cast<const short *>(hs), a.ld_h, 0, a.n, a.D};
-    if (grad || (!few && !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp))) {
-        h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
-        hipLaunchKernelGGL((k_pack_rows<T, PL>), dim3(blocks_for(a.n * 64)), dim3(256), 0, s, hs, a.ld_h, a.n, a.D, p.h,
-                           p.Kp, a.n * p.Kp, p.h_exp, p.tops, grad ? a.targets : nullptr, a.ignore, a.V);
-    }
     Operand w{reinterpret_cast<const short *>(ws), a.ld_w, 0, a.V, a.D};
-    if ((grad || !few) && !in_place<T, PL>(ws, a.ld_w, a.D, p.Kp)) {
-        w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
-        unsigned parts = 0;
-        if constexpr (PL == 2) {
-            parts = blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1);
-            if (parts > (unsigned)kMaxParts) parts = kMaxParts;
-            hipLaunchKernelGGL(k_weight_top, dim3(parts), dim3(256), 0, s, ws, a.ld_w, a.V, a.D, p.w_part);
-        }
-        hipLaunchKernelGGL((k_pack_weight<T, PL>), dim3(blocks_for(a.V * (p.Kp / 8))), dim3(256), 0, s, ws, a.ld_w, a.V,
-                           a.D, p.w, p.Kp, a.V * p.Kp, p.w_part, (int)parts, p.w_exp);
+    const bool pack_h = grad || (!few && !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp));
+    const bool pack_w = (grad || !few) && !in_place<T, PL>(ws, a.ld_w, a.D, p.Kp);
+    if (pack_h) h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
+    if (pack_w) w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
+    const int row_blocks = pack_h ? (int)blocks_for(a.n * 64) : 0;
+    const int unit_blocks = grad ? 1 : 0; // one block over all rows: begins first
+    const int w_blocks = pack_w ? (int)blocks_for(a.V * (p.Kp / 8)) : 0;
+    const PackRows<T, PL> rows_job{hs, a.ld_h, a.n, a.D, p.h, p.Kp, a.n * p.Kp, p.h_exp, p.tops,
+                                   grad ? a.targets : nullptr, a.ignore, a.V};
+    PackWeight<T, PL> w_job{ws, a.ld_w, a.V, a.D, p.w, p.Kp, a.V * p.Kp, p.w_part, 0, p.w_exp};
+    const Units units_job{a.grad_loss, a.targets, a.ignore, a.n, a.V, PL == 2 ? p.tops : nullptr, p.top_grad,
+                          p.all_exp};
+    if constexpr (PL == 2) {
+        // the rows and the weight's largest value, then the weight and the units
+        int parts = pack_w ? (int)blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1) : 0;
+        if (parts > kMaxParts) parts = kMaxParts;
+        w_job.parts = parts;
+        run_jobs(rows_job, row_blocks, WeightTop{ws, a.ld_w, a.V, a.D, p.w_part}, parts, s);
+        run_jobs(units_job, unit_blocks, w_job, w_blocks, s);
+    } else {
+        typedef Both<Units, PackWeight<T, PL>> First;
+        run_jobs(First{units_job, w_job, unit_blocks}, unit_blocks + w_blocks, rows_job, row_blocks, s);
     }
     const int64_t tiles = few ? few_rows(a, o, s)
                               : product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
-    hipLaunchKernelGGL(k_xent_join, dim3((unsigned)((a.n + 15) / 16)), dim3(1024), 0, s, p.part, tiles, a.n, a.V,
-                       a.targets, a.ignore, p.target_logit, a.loss, a.lse, reinterpret_cast<int *>(a.ws));
-    if (!grad) return hipGetLastError();
-    hipLaunchKernelGGL(k_xent_units, dim3(1), dim3(1024), 0, s, a.grad_loss, a.targets, a.ignore, a.n, a.V,
-                       PL == 2 ? p.tops : nullptr, p.top_grad, p.all_exp);
+    const Join join_job{p.part, tiles, a.n, a.V, a.targets, a.ignore, p.target_logit, a.loss, a.lse,
+                        reinterpret_cast<int *>(a.ws)};
+    const int join_blocks = (int)((a.n + 15) / 16);
     Operand h_all = h;
     if constexpr (PL == 2) {
         h_all.p = p.h_all;
-        hipLaunchKernelGGL(k_pack_counting, dim3(blocks_for(a.n * (p.Kp / 8))), dim3(256), 0, s, hs, a.ld_h, a.n, a.D,
-                           p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.targets, a.ignore, a.V);
+        const PackCounting count_job{hs, a.ld_h, a.n, a.D, p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.targets, a.ignore,
+                                     a.V};
+        run_jobs(join_job, join_blocks, count_job, grad ? (int)((blocks_for(a.n * (p.Kp / 8)) + 3) / 4) : 0, s);
+    } else {
+        run_jobs(join_job, join_blocks, NoJobOf<1024>(), 0, s);
     }
+    if (!grad) return hipGetLastError();
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t here = a.V - v0 < piece ? a.V - v0 : piece, cols = up(here, kRound);
         Operand wp = w;
