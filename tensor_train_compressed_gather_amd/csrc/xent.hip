@@ -105,6 +105,7 @@ struct Output {
     // fp16 terms: exponents by which each row (for the logits), all rows (for
     // the weight's gradient) and the weight were scaled
     const int *h_exp, *all_exp, *w_exp;
+    const float4 *rows;       // [n] scale, lse and gradient in the unit of d, of rows that are streamed
     short *d;                 // [planes][rows][ldd]
     int64_t ldd, plane_d;
     float *sum;               // fp32 sums, [splits][sum_rows][D]
@@ -552,6 +553,306 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
     }
 }
 
+// ------------------------------------------------- rows of at most 128 values
+//
+// With so short a sum a product's tile is over before its start and its end are
+// hidden, and d, written and read twice, costs more than the products.  Here a
+// wave keeps 32 NO rows of one operand in registers as fragments and streams
+// the rows of the other through LDS, 32 at a step: the logits of a step stay in
+// the wave's registers, where their layout (lane l: own row l % 32, streamed
+// rows 8 (r / 4) + 4 (l / 32) + r % 4) is the layout of the left operand of the
+// next product if that takes its summed index in the same order, which the
+// transposing reads of the streamed rows can.  So d is never written.
+//
+//   ROW_STATS  own: hidden rows, streamed: the weight.  Maximum and sum.
+//   ROW_GRAD   the same, and d times the streamed rows: dH of a part of the vocabulary.
+//   VOC_GRAD   own: rows of the weight, streamed: hidden rows: dW.
+//
+// The logits are made three times instead of twice, and matrix instructions
+// bound it: 2048 fp32 rows of 128 against 10^6, 7.2 ms with both gradients, of
+// which five sums of three products are 5.2 at the card's rate (10.7 by the
+// products above); bf16 3.3 ms, where the exponentials' vector instructions take
+// as long as the products.  fp16 terms: the hidden rows keep their own scales in
+// dW's product too, so there d_i carries the ratio to the largest row's scale,
+// at most 1.
+enum { ROW_STATS, ROW_GRAD, VOC_GRAD };
+constexpr int kNarrowStep = 32;
+constexpr int64_t kNarrowSteps = 8;    // least steps of a split
+constexpr int64_t kNarrow = 128;       // longest rows
+constexpr int64_t kNarrowRows = 1ll << 31;
+
+// Which of a streamed row's 16-byte pieces change places: sixteen rows' equal
+// pieces, and the 64 bytes of four neighbouring rows, lie in different banks.
+template <int KD>
+__device__ __forceinline__ int piece_turn(int row)
+{
+    return KD == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : ((row & 2) << 1) | ((row >> 2) & 3);
+}
+
+template <class T, int PL, int KD, int MODE, int NO>
+__global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int64_t owns, int64_t per, Output o)
+{
+    constexpr int KB = KD / 16, CB = KD / 32, P = KD * 2, PLANE = kNarrowStep * P, STAGE = PL * PLANE;
+    constexpr int PR = KD / 8, N = kNarrowStep * PR / 256;
+    constexpr bool VOC = MODE == VOC_GRAD;
+    __shared__ __align__(256) char lds[2 * STAGE];
+    __shared__ __align__(16) float of_row[2][3][kNarrowStep]; // VOC_GRAD: scale, lse and gradient of the streamed rows
+    __shared__ __align__(16) int hit_row[2][kNarrowStep];     // and their targets in this block's rows
+    const int64_t id = (int64_t)(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+    const int64_t sp = id / owns, ob = id % owns, all = (str.rows + kNarrowStep - 1) / kNarrowStep, s0 = sp * per;
+    if (s0 >= all) return;
+    const int steps = (int)(all - s0 < per ? all - s0 : per);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+    const int64_t block0 = ob * 128 * NO, own0 = block0 + wave * 32 * NO;
+
+    s16x8 of[PL][NO][KB];
+    float scale[NO], lse[NO], g[NO], top[NO], sum[NO];
+    int hit[NO], hit_row_of[NO]; // step of this row's target and its row there
+    const float unit = MODE != ROW_STATS ? *o.top_grad : 1.f;
+#pragma unroll
+    for (int b = 0; b < NO; ++b) {
+        const int64_t i = own0 + b * 32 + (lane & 31), ic = i < own.rows ? i : own.rows - 1;
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+                of[q][b][k] =
+                    *reinterpret_cast<const s16x8 *>(own.p + q * own.plane + ic * own.ld + k * 16 + half * 8);
+        scale[b] = 1.f;
+        lse[b] = g[b] = sum[b] = 0.f;
+        top[b] = -INFINITY;
+        hit[b] = -1;
+        hit_row_of[b] = 0;
+        if constexpr (!VOC) {
+            const int64_t target = o.targets[ic], t = target - s0 * kNarrowStep;
+            bool takes = i < own.rows && t >= 0 && t < (int64_t)steps * kNarrowStep;
+            if constexpr (PL == 2) scale[b] = ldexpf(1.f, -(o.h_exp[ic] + *o.w_exp));
+            if constexpr (MODE == ROW_GRAD) {
+                const bool counts = i < own.rows && row_counts(target, o.ignore, o.V);
+                lse[b] = counts ? o.lse[ic] : INFINITY;
+                g[b] = counts ? o.grad[ic] / unit * (PL == 2 ? (float)(1 << kUnitExp) : 1.f) : 0.f;
+                takes = takes && counts;
+            }
+            if (takes) {
+                hit[b] = (int)(t / kNarrowStep);
+                hit_row_of[b] = (int)(t % kNarrowStep);
+            }
+        }
+    }
+    f32x16 acc[MODE == ROW_STATS ? 1 : NO][CB];
+    if constexpr (MODE != ROW_STATS) {
+#pragma unroll
+        for (int b = 0; b < NO; ++b)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[b][c][r] = 0.f;
+    }
+
+    // streamed rows: memory to registers a step ahead, registers to one of two LDS buffers
+    const int64_t end = (str.rows - 1) * str.ld + str.cols;
+    const int off = ((tid / PR) * (int)str.ld + (tid % PR) * 8) * 2, apart = 256 / PR * (int)str.ld * 2;
+    u32x4 v[PL][N];
+    float4 c_row = make_float4(0.f, INFINITY, 0.f, 0.f);
+    int c_hit = -1;
+    auto load = [&](int st) {
+        const int64_t row0 = (s0 + st) * kNarrowStep, skip = row0 * str.ld, left = (end - skip) * 2;
+        const unsigned bytes = left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left;
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<short *>(str.p + q * str.plane + skip), 0, bytes, 0x00027000);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[q][i] = __builtin_amdgcn_raw_buffer_load_b128(r, off, i * apart, 0);
+        }
+        if constexpr (VOC) {
+            if (tid < kNarrowStep) {
+                const int64_t i = row0 + tid;
+                c_row = make_float4(0.f, INFINITY, 0.f, 0.f);
+                c_hit = -1;
+                if (i < str.rows) {
+                    c_row = o.rows[i];
+                    const int64_t target = o.targets[i], t = target - block0;
+                    if (row_counts(target, o.ignore, o.V) && t >= 0 && t < 128 * NO) c_hit = (int)t;
+                }
+            }
+        }
+    };
+    auto store = [&](int buf) {
+        char *to = lds + buf * STAGE;
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int row = tid / PR + i * (256 / PR);
+                *reinterpret_cast<u32x4 *>(to + q * PLANE + row * P + ((tid % PR) ^ piece_turn<KD>(row)) * 16) = v[q][i];
+            }
+        if constexpr (VOC) {
+            if (tid < kNarrowStep) {
+                of_row[buf][0][tid] = c_row.x;
+                of_row[buf][1][tid] = c_row.y;
+                of_row[buf][2][tid] = c_row.z;
+                hit_row[buf][tid] = c_hit;
+            }
+        }
+    };
+    auto row_of = [&](int r) { return 8 * (r / 4) + 4 * half + r % 4; };
+    const int straight = (lane & 31) * P, turn = (piece_turn<KD>(lane & 31) ^ half) * 16;
+    const int four = (lane & 15) >> 2, piece = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+    const int turned = (4 * half + four) * P + (((KD == 128 ? four : four >> 1) << 2 | (piece ^ half)) << 4) +
+                       (lane & 1) * 8;
+
+    load(0);
+    store(0);
+    load(steps > 1 ? 1 : 0);
+    __syncthreads();
+    for (int st = 0; st < steps; ++st) {
+        const int buf = st & 1;
+        const char *here = lds + buf * STAGE;
+        store(buf ^ 1);
+        load(st + 2 < steps ? st + 2 : steps - 1);
+        f32x16 z[NO];
+#pragma unroll
+        for (int b = 0; b < NO; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) z[b][r] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            s16x8 f[PL];
+#pragma unroll
+            for (int q = 0; q < PL; ++q)
+                f[q] = *reinterpret_cast<const s16x8 *>(here + straight + q * PLANE + ((k * 32) ^ turn));
+            if constexpr (PL == 2) {
+#pragma unroll
+                for (int b = 0; b < NO; ++b) z[b] = Terms<PL>::mma(f[PL - 1], of[0][b][k], z[b]);
+#pragma unroll
+                for (int b = 0; b < NO; ++b) z[b] = Terms<PL>::mma(f[0], of[PL - 1][b][k], z[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < NO; ++b) z[b] = Terms<PL>::mma(f[0], of[0][b][k], z[b]);
+        }
+        const int64_t left = str.rows - (s0 + st) * kNarrowStep; // streamed rows that exist
+        if constexpr (MODE == ROW_STATS) {
+#pragma unroll
+            for (int b = 0; b < NO; ++b) {
+                if (left < kNarrowStep) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row_of(r) >= left) z[b][r] = -INFINITY;
+                }
+                if (__any(hit[b] == st)) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (hit[b] == st && row_of(r) == hit_row_of[b])
+                            o.target_logit[own0 + b * 32 + (lane & 31)] = z[b][r] * scale[b];
+                }
+                float m = top[b];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) m = fmaxf(m, z[b][r]);
+                const float ref = m == -INFINITY ? 0.f : m, base = scale[b] * 1.44269504f;
+                float s = 0.f; // of the step first: a row's sum is as many additions long as it has steps
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f((z[b][r] - ref) * base);
+                sum[b] = fmaf(sum[b], __builtin_amdgcn_exp2f((top[b] - ref) * base), s);
+                top[b] = m;
+            }
+        } else {
+            s16x8 d[PL][NO][2];
+            bool here_hit[NO];
+#pragma unroll
+            for (int b = 0; b < NO; ++b) {
+                if constexpr (VOC) {
+                    const int t = hit_row[buf][lane & 31] - (wave * NO + b) * 32;
+                    here_hit[b] = __any(t >= 0 && t < 32);
+                } else {
+                    here_hit[b] = __any(hit[b] == st);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float ls[4], sc[4], gr[4];
+                int ht[4];
+                if constexpr (VOC) {
+                    const int at = 8 * e + 4 * half;
+                    load_vec<float, 4>(&of_row[buf][0][at], sc);
+                    load_vec<float, 4>(&of_row[buf][1][at], ls);
+                    load_vec<float, 4>(&of_row[buf][2][at], gr);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) ht[r] = hit_row[buf][at + r];
+                }
+#pragma unroll
+                for (int b = 0; b < NO; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float x = z[b][4 * e + r];
+                        float p;
+                        if constexpr (VOC) {
+                            p = __builtin_amdgcn_exp2f(fmaf(x, sc[r], -ls[r]) * 1.44269504f);
+                            if (here_hit[b]) p -= ht[r] == (wave * NO + b) * 32 + (lane & 31) ? 1.f : 0.f;
+                            p *= gr[r];
+                        } else {
+                            p = __builtin_amdgcn_exp2f(fmaf(x, scale[b], -lse[b]) * 1.44269504f);
+                            if (here_hit[b]) p -= hit[b] == st && row_of(4 * e + r) == hit_row_of[b] ? 1.f : 0.f;
+                            if (left < kNarrowStep && row_of(4 * e + r) >= left) p = 0.f;
+                            p *= g[b];
+                        }
+                        short w[PL];
+                        split<PL>(p, w);
+#pragma unroll
+                        for (int q = 0; q < PL; ++q) d[q][b][e >> 1][(e & 1) * 4 + r] = w[q];
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < CB; ++c) {
+                    s16x8 f[PL];
+#pragma unroll
+                    for (int q = 0; q < PL; ++q) {
+                        typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
+                        const char *from = here + q * PLANE + 16 * u * P;
+                        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + (turned ^ (c << 6))));
+                        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_s16x4)(from + 8 * P + (turned ^ (c << 6) ^ 32)));
+                        f[q] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    }
+                    if constexpr (PL == 2) {
+#pragma unroll
+                        for (int b = 0; b < NO; ++b) acc[b][c] = Terms<PL>::mma(d[PL - 1][b][u], f[0], acc[b][c]);
+#pragma unroll
+                        for (int b = 0; b < NO; ++b) acc[b][c] = Terms<PL>::mma(d[0][b][u], f[PL - 1], acc[b][c]);
+                    }
+#pragma unroll
+                    for (int b = 0; b < NO; ++b) acc[b][c] = Terms<PL>::mma(d[0][b][u], f[0], acc[b][c]);
+                }
+        }
+        __syncthreads();
+    }
+    if constexpr (MODE == ROW_STATS) {
+#pragma unroll
+        for (int b = 0; b < NO; ++b) {
+            const int64_t i = own0 + b * 32 + (lane & 31);
+            const float2 other = make_float2(__shfl_xor(top[b], 32, 64) * scale[b], __shfl_xor(sum[b], 32, 64));
+            const float2 both = join_sums(make_float2(top[b] * scale[b], sum[b]), other);
+            if (lane < 32 && i < own.rows) o.part[sp * o.n + i] = both;
+        }
+    } else {
+        const float by = PL == 2 && VOC ? ldexpf(unit, -(kUnitExp + *o.all_exp)) : unit;
+#pragma unroll
+        for (int b = 0; b < NO; ++b)
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int64_t i = own0 + b * 32 + row_of(r);
+                    const int k = c * 32 + (lane & 31);
+                    if (i >= own.rows || k >= o.D) continue;
+                    if (VOC && o.splits == 1) static_cast<T *>(o.out)[i * o.ld_out + k] = (T)(acc[b][c][r] * by);
+                    else o.sum[(sp * own.rows + i) * o.D + k] = acc[b][c][r];
+                }
+    }
+}
+
 // The statistics of at most 32 NB rows of fp32: the weight is read once, as it
 // is, by the fp32 matrix instructions.  Splitting it into fp16 terms first
 // costs three more passes over it, more than the slower products do here
@@ -635,28 +936,46 @@ __global__ __launch_bounds__(256) void k_xent_few(const float *w, int64_t ld_w, 
     }
 }
 
-// A gradient from its splits' sums, in order, in units of the loss (`exp`: of
-// the operand's scale, for fp16 terms).
+// A gradient from its splits' sums, in units of the loss (`exp`: of the
+// operand's scale, for fp16 terms).  `groups` (a power of two) threads share
+// four values and the splits, so that many splits of few rows are not one
+// thread's chain (512 of 40 x 64: 129 us by one, 10 by 32); their sums meet in
+// LDS in order.
 template <class T>
-__global__ __launch_bounds__(256) void k_xent_sum(const float *sum, int splits, int64_t rows, int64_t D,
+__global__ __launch_bounds__(256) void k_xent_sum(const float *sum, int splits, int groups, int64_t rows, int64_t D,
                                                   const float *top_grad, const int *exp, T *out, int64_t ld)
 {
-    const int64_t chunks = (D + 3) / 4, step = (int64_t)gridDim.x * 256;
+    __shared__ float4 part[256];
+    const int each = 256 / groups, grp = threadIdx.x / each, in = threadIdx.x % each;
+    const int64_t chunks = (D + 3) / 4, all = rows * chunks, step = (int64_t)gridDim.x * each;
     const float unit = exp ? ldexpf(*top_grad, -(kUnitExp + *exp)) : *top_grad;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * chunks; c += step) {
+    for (int64_t c0 = (int64_t)blockIdx.x * each; c0 < all; c0 += step) {
+        const int64_t c = c0 + in < all ? c0 + in : all - 1;
         const int64_t i = c / chunks, k = (c - i * chunks) * 4;
         const int left = (int)(D - k < 4 ? D - k : 4);
         float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-        for (int q = 0; q < splits; ++q) {
+        for (int q = grp; q < splits; q += groups) {
             float y[4];
             load_part<float, 4>(sum + ((int64_t)q * rows + i) * D + k, left, y);
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] += y[r];
         }
+        if (groups > 1) {
+            __syncthreads(); // the last round's parts have been read
+            part[threadIdx.x] = make_float4(x[0], x[1], x[2], x[3]);
+            __syncthreads();
+            for (int q = 1; q < groups && grp == 0; ++q) {
+                const float4 y = part[q * each + in];
+                x[0] += y.x;
+                x[1] += y.y;
+                x[2] += y.z;
+                x[3] += y.w;
+            }
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[r] *= unit;
-        store_part<T, 4>(out + i * ld + k, left, x);
+        if (grp == 0 && c0 + in < all) store_part<T, 4>(out + i * ld + k, left, x);
     }
 }
 
@@ -869,10 +1188,22 @@ struct Units {
     {
         __shared__ float sm[2][4];
         float m = 0.f, h = 0.f;
-#pragma unroll 4
-        for (int64_t i = threadIdx.x; i < n; i += 256) {
-            if (row_counts(targets[i], ignore, V)) m = fmaxf(m, fabsf(grad[i]));
-            if (tops) h = fmaxf(h, tops[i]);
+        constexpr int U = 16; // loads in flight: their latency is what the one block waits for
+        for (int64_t i0 = threadIdx.x; i0 < n; i0 += 256 * U) {
+            int64_t t[U];
+            float a[U], b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = i0 + u * 256 < n ? i0 + u * 256 : i0;
+                t[u] = targets[i];
+                a[u] = grad[i];
+                b[u] = tops ? tops[i] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (row_counts(t[u], ignore, V)) m = fmaxf(m, fabsf(a[u]));
+                h = fmaxf(h, b[u]);
+            }
         }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) {
@@ -906,6 +1237,10 @@ struct Join {
     const float *target_logit;
     float *loss, *lse;
     int *status;
+    // with `rows`: what the streamed rows of the weight's gradient need, too
+    float4 *rows;
+    const float *grad, *unit;
+    const int *h_exp, *w_exp, *all_exp; // null for bf16
 
     __device__ void operator()(int block, int) const
     {
@@ -937,6 +1272,15 @@ struct Join {
         if (!in && t != ignore) atomicOr(status + ST_ERR, (int)STB_INDEX);
         lse[i] = z;
         loss[i] = in && t != ignore ? z - target_logit[i] : 0.f;
+        if (!rows) return;
+        float4 c = make_float4(h_exp ? ldexpf(1.f, -(h_exp[i] + *w_exp)) : 1.f, INFINITY, 0.f, 0.f);
+        if (in && t != ignore) {
+            c.y = z;
+            c.z = grad[i] / *unit;
+            // (a row of zeros has a scale of its own, and no part in the sum)
+            if (h_exp) c.z = ldexpf(c.z, kUnitExp + (*all_exp < h_exp[i] ? *all_exp - h_exp[i] : 0));
+        }
+        rows[i] = c;
     }
 };
 
@@ -952,6 +1296,7 @@ struct XentPlan {
     float *target_logit, *top_grad, *w_part, *tops;
     int *h_exp, *all_exp, *w_exp;
     float2 *part;
+    float4 *rows;
     short *h, *h_all, *w; // packed operands (the weight's unused where it serves in place)
     float *sum, *w_sum;
     short *d;
@@ -989,16 +1334,44 @@ int sum_splits(int64_t rows, int64_t D, int64_t K)
 // Rows of d: whole tiles, so that they are written without a test.
 inline int64_t d_rows(int64_t n) { return n <= 128 ? 128 : up(n, 256); }
 
-int64_t best_piece(int64_t n, int64_t V, int PL)
+// Narrow kernels: 32-row blocks that a wave owns (as many as 256 registers hold;
+// a streamed fragment read from LDS serves all of them), and how often the streamed rows are split so that the blocks fill rounds of
+// two on each compute unit.
+constexpr int narrow_blocks(int PL, int mode, int64_t Kp)
 {
+    return mode == ROW_STATS || (PL == 1 && Kp == 64) ? 2 : 1;
+}
+inline bool narrow_rows(int64_t n, int64_t V, int64_t D) { return D <= kNarrow && n < kNarrowRows && V < kNarrowRows; }
+inline int whole_splits(int64_t streamed, int64_t s) // s, less the splits that equal parts leave empty
+{
+    const int64_t steps = (streamed + kNarrowStep - 1) / kNarrowStep;
+    if (s < 1) s = 1;
+    const int64_t per = (steps + s - 1) / s;
+    return (int)((steps + per - 1) / per);
+}
+int narrow_splits(int64_t own, int64_t streamed, int blocks)
+{
+    const int64_t owns = (own + 128 * blocks - 1) / (128 * blocks), slots = 2 * kCUs;
+    const int64_t steps = (streamed + kNarrowStep - 1) / kNarrowStep;
+    int64_t s = owns < slots ? slots / owns : 1;
+    auto full = [&](int64_t k) { return 4 * owns * k >= 3 * up(owns * k, slots); };
+    while (owns * s < 8 * slots && !full(s)) ++s;
+    if (s > steps / kNarrowSteps) s = steps / kNarrowSteps;
+    return whole_splits(streamed, s);
+}
+
+int64_t best_piece(int64_t n, int64_t V, int64_t D, int PL)
+{
+    if (narrow_rows(n, V, D)) return -narrow_splits(n, V, narrow_blocks(PL, ROW_GRAD, up(D, kPadK)));
     int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * d_rows(n) * 2)) / kRound * kRound;
     if (c < 8 * kRound) c = 8 * kRound;
     return up(V < c ? V : c, kRound);
 }
 
-// `piece` columns of d (0: forward only).  Packed copies of the operands are
-// planned whether or not an aligned bf16 operand needs them, so that the size
-// does not depend on the pointers.
+// `piece` columns of d (0: forward only; below 0: gradients by the narrow
+// kernels, -piece splits of dH).  Packed copies of the operands are planned
+// whether or not an aligned bf16 operand needs them, so that the size does not
+// depend on the pointers.
 XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char *base)
 {
     size_t off = TT_EMB_STATUS_BYTES;
@@ -1021,7 +1394,13 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     p.tops = (float *)take(4 * n);
     p.h = (short *)take((size_t)PL * n * p.Kp * 2);
     p.w = (short *)take((size_t)PL * V * p.Kp * 2);
-    if (piece) {
+    if (piece < 0) {
+        p.rows = (float4 *)take(16 * (size_t)n);
+        p.splits = (int)-piece;
+        p.sum = (float *)take(4 * (size_t)p.splits * n * D);
+        p.w_splits = narrow_splits(V, n, narrow_blocks(PL, VOC_GRAD, p.Kp));
+        if (p.w_splits > 1) p.w_sum = (float *)take(4 * (size_t)p.w_splits * V * D);
+    } else if (piece) {
         if (PL == 2) p.h_all = (short *)take((size_t)PL * n * p.Kp * 2);
         p.splits = sum_splits(n, D, piece);
         p.sum = (float *)take(4 * (size_t)p.splits * n * D);
@@ -1061,6 +1440,30 @@ int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_
     return mt;
 }
 
+template <class T>
+void sum_up(const float *sum, int splits, int64_t rows, int64_t D, const float *unit, const int *exp, void *out,
+            int64_t ld, hipStream_t s)
+{
+    const int groups = splits >= 64 ? 32 : splits >= 8 ? 8 : 1;
+    hipLaunchKernelGGL(k_xent_sum<T>, dim3(blocks_for(rows * ((D + 3) / 4) * groups)), dim3(256), 0, s, sum, splits,
+                       groups, rows, D, unit, exp, static_cast<T *>(out), ld);
+}
+
+// A pass of the narrow kernels; `splits` as planned.
+template <class T, int PL, int MODE>
+void narrow(const Operand &own, const Operand &streamed, int64_t Kp, int splits, const Output &o, hipStream_t s)
+{
+    auto run = [&](auto kd) {
+        constexpr int KD = decltype(kd)::value, NO = narrow_blocks(PL, MODE, KD);
+        const int64_t owns = (own.rows + 128 * NO - 1) / (128 * NO);
+        const int64_t steps = (streamed.rows + kNarrowStep - 1) / kNarrowStep, per = (steps + splits - 1) / splits;
+        hipLaunchKernelGGL((k_narrow<T, PL, KD, MODE, NO>), dim3((unsigned)up(owns * splits, 8)), dim3(256), 0, s, own,
+                           streamed, owns, per, o);
+    };
+    if (Kp == 64) run(std::integral_constant<int, 64>());
+    else run(std::integral_constant<int, 128>());
+}
+
 // One launch for two jobs of na and nb blocks (none for none).
 template <class A, class B>
 void run_jobs(const A &a, int na, const B &b, int nb, hipStream_t s)
@@ -1085,7 +1488,10 @@ int64_t few_rows(const XentArgs &a, const Output &o, hipStream_t s)
 template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
-    int64_t piece = grad ? best_piece(a.n, a.V, PL) : 0;
+    const bool narrow_all = narrow_rows(a.n, a.V, a.D);
+    int64_t piece = grad ? best_piece(a.n, a.V, a.D, PL) : 0;
+    while (piece < -1 && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
+        piece = -whole_splits(a.V, -piece / 2);
     while (piece > kRound && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
         piece = up(piece / 2, kRound);
     const XentPlan p = plan_xent(a.n, a.V, a.D, PL, piece, a.ws);
@@ -1133,21 +1539,54 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         typedef Both<Units, PackWeight<T, PL>> First;
         run_jobs(First{units_job, w_job, unit_blocks}, unit_blocks + w_blocks, rows_job, row_blocks, s);
     }
-    const int64_t tiles = few ? few_rows(a, o, s)
-                              : product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
-    const Join join_job{p.part, tiles, a.n, a.V, a.targets, a.ignore, p.target_logit, a.loss, a.lse,
-                        reinterpret_cast<int *>(a.ws)};
+    int64_t tiles;
+    if (few) {
+        tiles = few_rows(a, o, s);
+    } else if (narrow_all) {
+        tiles = narrow_splits(a.n, a.V, narrow_blocks(PL, ROW_STATS, p.Kp));
+        narrow<T, PL, ROW_STATS>(h, w, p.Kp, (int)tiles, o, s);
+    } else {
+        tiles = product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
+    }
+    Join join_job{p.part, tiles, a.n, a.V, a.targets, a.ignore, p.target_logit, a.loss, a.lse,
+                  reinterpret_cast<int *>(a.ws)};
+    if (piece < 0) {
+        join_job.rows = p.rows;
+        join_job.grad = a.grad_loss;
+        join_job.unit = p.top_grad;
+        if constexpr (PL == 2) {
+            join_job.h_exp = p.h_exp;
+            join_job.w_exp = p.w_exp;
+            join_job.all_exp = p.all_exp;
+        }
+    }
     const int join_blocks = (int)((a.n + 15) / 16);
     Operand h_all = h;
     if constexpr (PL == 2) {
         h_all.p = p.h_all;
         const PackCounting count_job{hs, a.ld_h, a.n, a.D, p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.targets, a.ignore,
                                      a.V};
-        run_jobs(join_job, join_blocks, count_job, grad ? (int)((blocks_for(a.n * (p.Kp / 8)) + 3) / 4) : 0, s);
+        run_jobs(join_job, join_blocks, count_job,
+                 piece > 0 ? (int)((blocks_for(a.n * (p.Kp / 8)) + 3) / 4) : 0, s);
     } else {
         run_jobs(join_job, join_blocks, NoJobOf<1024>(), 0, s);
     }
     if (!grad) return hipGetLastError();
+    if (piece < 0) {
+        o.rows = p.rows;
+        o.sum = p.sum;
+        o.splits = p.splits;
+        narrow<T, PL, ROW_GRAD>(h, w, p.Kp, p.splits, o, s);
+        o.sum = p.w_sum;
+        o.splits = p.w_splits;
+        o.out = a.dw;
+        o.ld_out = a.ld_dw;
+        narrow<T, PL, VOC_GRAD>(w, h, p.Kp, p.w_splits, o, s);
+        if (p.w_splits > 1)
+            sum_up<T>(p.w_sum, p.w_splits, a.V, a.D, p.top_grad, PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
+        sum_up<T>(p.sum, p.splits, a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr, a.dh, a.ld_dh, s);
+        return hipGetLastError();
+    }
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t here = a.V - v0 < piece ? a.V - v0 : piece, cols = up(here, kRound);
         Operand wp = w;
@@ -1175,16 +1614,14 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         o.splits = p.w_splits;
         o.split_k = up((rows + p.w_splits - 1) / p.w_splits, kPadK);
         product<PL, true, true, OUT_SUM>(h_all, d, a.D, a.V, rows, o, s);
-        hipLaunchKernelGGL(k_xent_sum<T>, dim3(blocks_for(a.V * ((a.D + 3) / 4))), dim3(256), 0, s, p.w_sum,
-                           (int)((rows + o.split_k - 1) / o.split_k), a.V, a.D, p.top_grad,
-                           PL == 2 ? p.all_exp : nullptr, static_cast<T *>(a.dw), a.ld_dw);
+        sum_up<T>(p.w_sum, (int)((rows + o.split_k - 1) / o.split_k), a.V, a.D, p.top_grad,
+                  PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
     }
     // splits past the first piece's end have written nothing
     const int64_t first = up(a.V < piece ? a.V : piece, kRound);
     const int64_t per = up((first + p.splits - 1) / p.splits, kPadK);
-    hipLaunchKernelGGL(k_xent_sum<T>, dim3(blocks_for(a.n * ((a.D + 3) / 4))), dim3(256), 0, s, p.sum,
-                       (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr,
-                       static_cast<T *>(a.dh), a.ld_dh);
+    sum_up<T>(p.sum, (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr, a.dh,
+              a.ld_dh, s);
     return hipGetLastError();
 }
 
@@ -1194,8 +1631,9 @@ void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_
 {
     const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1;
     if (n < 1) n = 1; // no rows: the least workspace
-    if (best) *best = plan_xent(n, V, D, PL, grad ? best_piece(n, V, PL) : 0, nullptr).bytes;
-    if (least) *least = plan_xent(n, V, D, PL, grad ? kRound : 0, nullptr).bytes;
+    const int64_t most = grad ? best_piece(n, V, D, PL) : 0;
+    if (best) *best = plan_xent(n, V, D, PL, most, nullptr).bytes;
+    if (least) *least = plan_xent(n, V, D, PL, most < 0 ? -1 : most > 0 ? kRound : 0, nullptr).bytes;
 }
 
 hipError_t launch_xent_forward(const XentArgs &a, int dtype, hipStream_t s)

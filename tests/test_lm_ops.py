@@ -371,6 +371,16 @@ def test_xent_in_large_tiles(n, V, D, gap, t):
     test_xent_and_gradients(n, V, D, gap, t)
 
 
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("n,V,D,gap", [(1, 33, 64, 0), (129, 257, 65, 0), (300, 5000, 128, 0), (4100, 40, 100, 3),
+                                       (70, 20011, 128, 8), (1000, 100, 1, 0), (257, 31, 64, 8), (33, 1, 127, 0),
+                                       (2000, 9001, 63, 1)])
+def test_xent_of_narrow_rows(n, V, D, gap, t):
+    # up to 128 columns: one operand in registers, the other streamed 32 rows at
+    # a step, in whole steps and not, once and in splits
+    test_xent_and_gradients(n, V, D, gap, t)
+
+
 @pytest.mark.parametrize("n", [1, 5, 31, 32, 33, 64, 65, 127, 128, 129])
 @pytest.mark.parametrize("V,D,gap", [(1, 5, 0), (127, 31, 3), (128, 32, 0), (257, 33, 1), (1000, 100, 0), (3001, 516, 4)])
 def test_xent_scores_of_few_rows(n, V, D, gap):
