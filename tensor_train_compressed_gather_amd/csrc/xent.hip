@@ -30,7 +30,6 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kTurnPad = 64;           // bytes past a turned tile's row in LDS
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
 constexpr size_t kPieceBytes = (size_t)256 << 20; // d of one piece of the vocabulary, at most
 constexpr int kSplitK = 512;           // least summed values of a split
@@ -43,11 +42,13 @@ constexpr int kUnitExp = 15;           // fp16 terms: d is kept in units of 2^-1
 
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+constexpr int kStage = 32; // summed values per stage: two steps of 16
+
 // PL planes of 16-bit terms: one of bf16, or two of fp16.
 template <int PL>
 struct Terms {
     typedef bf16 type;
-    static constexpr int stage = 64; // summed values per stage
+    static constexpr int buffers = 4; // stages in LDS
     static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
@@ -57,7 +58,7 @@ struct Terms {
 template <>
 struct Terms<2> {
     typedef f16 type;
-    static constexpr int stage = 32;
+    static constexpr int buffers = 2;
     static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
@@ -118,30 +119,38 @@ struct Output {
 };
 
 // How one plane of an operand's tile, R outputs and BK summed values, lies in
-// LDS.  Straight: R rows of BK values and 16 bytes, so that the 16-byte reads
-// of sixteen lanes (sixteen rows) meet different banks.  Turned: BK rows of R
-// values and 64 bytes, so that the four rows of 64 bytes that half a wave's
-// transposing read touches do.
-template <bool TURNED, int R, int BK>
+// LDS: rows of 16-byte pieces without gaps, as loads that go there directly
+// write them.  Straight: R rows of BK values; turned: BK rows of R values.
+// Which of a row's pieces change places (`turn`) is chosen so that the sixteen
+// rows that sixteen lanes read lie in different banks (straight), and so do
+// the four rows of 64 bytes that half a wave's transposing read touches.
+template <bool TURNED, int R>
 struct TileLds {
-    static constexpr int pitch = TURNED ? R * 2 + kTurnPad : BK * 2 + 16;
-    static constexpr int bytes = (TURNED ? BK : R) * pitch;
+    static constexpr int BK = kStage;
+    static constexpr int pitch = (TURNED ? R : BK) * 2;
+    static constexpr int bytes = R * BK * 2;
     static constexpr int vecs = R * BK / 8 / 256; // 16-byte pieces per thread
+    static __device__ __forceinline__ int turn(int row)
+    {
+        return TURNED ? (row & 3) << 2 : (row >> 2) & 3;
+    }
 };
 
-// One operand's way from memory to registers to LDS.  Loads go through a
-// buffer descriptor that ends with the matrix, so rows past it (of the outputs
-// or of the summed index) read as zeros and no address needs a clamp.
+typedef __attribute__((address_space(3))) void *lds_void;
+
+// One operand's way from memory to LDS, without registers between: a wave's
+// load fills 1 KB of LDS in the order of its lanes, so the pieces change places
+// by the address that each lane reads.  Loads go through a buffer descriptor
+// that ends with the matrix, so rows past it (of the outputs or of the summed
+// index) are written as zeros and no address needs a clamp.
 template <bool TURNED, int R, int PL>
 struct TileLoader {
-    static constexpr int BK = Terms<PL>::stage, P = TileLds<TURNED, R, BK>::pitch;
-    static constexpr int N = TileLds<TURNED, R, BK>::vecs;
-    static constexpr int ROWV = (TURNED ? R : BK) / 8; // pieces in a tile's row
+    typedef TileLds<TURNED, R> L;
+    static constexpr int N = L::vecs, ROWV = L::pitch / 16; // pieces in a tile's row
     const short *p; // plane 0, moved to the tile's first row (straight) or column (turned)
     int64_t ld, plane, end; // end: elements from p to the end of plane 0
     int off;        // byte offset of this thread's first piece; the others are 256 / ROWV rows apart
-    int step;
-    u32x4 v[PL][N];
+    int step, to;   // to: the wave's place in LDS
 
     __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0)
     {
@@ -149,34 +158,40 @@ struct TileLoader {
         plane = a.plane;
         p = a.p + (TURNED ? r0 : r0 * a.ld);
         end = (a.rows - 1) * a.ld + a.cols - (TURNED ? r0 : r0 * a.ld);
-        const int t = threadIdx.x;
-        off = ((t / ROWV) * (int)ld + (t % ROWV) * 8) * 2;
+        const int t = threadIdx.x, row = t / ROWV;
+        off = (row * (int)ld + ((t % ROWV) ^ L::turn(row)) * 8) * 2;
         step = 256 / ROWV * (int)ld * 2;
+        to = __builtin_amdgcn_readfirstlane(t >> 6) * 1024;
     }
-    __device__ __forceinline__ void load(int64_t k0)
+    __device__ __forceinline__ void load(int64_t k0, char *lds, bool there) const
     {
         const int64_t skip = TURNED ? k0 * ld : k0;
         const int64_t left = (end - skip) * 2;
-        const unsigned bytes = left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left;
+        // (without a branch, which would part the loads from the products around them)
+        const unsigned bytes = (left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left) & -(unsigned)there;
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<short *>(p + q * plane + skip), 0, bytes, 0x00027000);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[q][i] = __builtin_amdgcn_raw_buffer_load_b128(r, off, i * step, 0);
+            for (int i = 0; i < N; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(lds + q * L::bytes + i * 4096 + to), 16, off,
+                                                         i * step, 0, 0);
         }
     }
-    __device__ __forceinline__ void store(char *lds) const
-    {
-        const int t = threadIdx.x;
-        char *to = lds + (t / ROWV) * P + (t % ROWV) * 16;
-#pragma unroll
-        for (int q = 0; q < PL; ++q)
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                *reinterpret_cast<u32x4 *>(to + q * TileLds<TURNED, R, BK>::bytes + i * (256 / ROWV) * P) = v[q][i];
-    }
 };
+// Every wave's reads of LDS are done, and so are all but its last N loads.  A
+// barrier of the language would wait for every load in flight; the fences here
+// order the compiler's accesses and cost nothing.
+template <int N>
+__device__ __forceinline__ void loads_meet()
+{
+    static_assert(N < 64, "a counter of six bits");
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | (N >> 4) << 14); // lgkmcnt(0) vmcnt(N)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Fragments of N 32-row blocks from row `r0` of a tile, summed values
 // [ks * 16, ks * 16 + 16): lane l gets row l % 32, values 8 (l / 32) .. + 7.
@@ -185,25 +200,29 @@ struct TileLoader {
 template <bool TURNED, int R, int PL, int N>
 __device__ __forceinline__ void fragments(const char *lds, int r0, int ks, s16x8 (&f)[PL][N])
 {
-    constexpr int BK = Terms<PL>::stage, P = TileLds<TURNED, R, BK>::pitch;
-    const int l = threadIdx.x & 63;
+    typedef TileLds<TURNED, R> L;
+    constexpr int P = L::pitch;
+    const int l = threadIdx.x & 63, half = l >> 5;
+    if constexpr (!TURNED) {
+        const int at = (r0 + (l & 31)) * P + ((half ^ L::turn(l & 31)) * 16 ^ ks * 32);
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-        const char *from = lds + q * TileLds<TURNED, R, BK>::bytes;
-        if constexpr (!TURNED) {
-            from += (r0 + (l & 31)) * P + ks * 32 + (l >> 5) * 16;
+        for (int q = 0; q < PL; ++q)
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[q][i] = *reinterpret_cast<const s16x8 *>(from + i * 32 * P);
-        } else {
-            from += (ks * 16 + (l >> 5) * 8 + ((l & 15) >> 2)) * P + (r0 + ((l >> 4) & 1) * 16 + (l & 3) * 4) * 2;
+            for (int i = 0; i < N; ++i)
+                f[q][i] = *reinterpret_cast<const s16x8 *>(lds + at + q * L::bytes + i * 32 * P);
+    } else {
+        const int row = half * 8 + ((l & 15) >> 2);
+        const int at = row * P + ((r0 * 2 + ((l >> 4) & 1) * 32 + (l & 3) * 8) ^ L::turn(row) * 16);
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
-                const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + i * 64));
-                const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + i * 64 + 4 * P));
+                const char *from = lds + q * L::bytes + ks * 16 * P + (at ^ i * 64);
+                const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)from);
+                const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + 4 * P));
                 f[q][i] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
             }
-        }
     }
 }
 
@@ -244,22 +263,18 @@ inline unsigned tile_grid(int64_t mt, int64_t nt, int splits)
 
 // Order of a step's instructions: the reads of the next step's fragments two
 // to a matrix instruction, so that they are there when that step begins; then
-// the stores of a stage's pieces to LDS, each followed by the load of the same
-// piece of a later stage (a whole stage ahead of its use).
-template <int M, int READS, int PIECES>
+// the loads of a later stage.
+template <int M, int READS, int LOADS>
 __device__ __forceinline__ void interleave()
 {
-    constexpr int mfma = 0x008, vmem_read = 0x020, ds_read = 0x100, ds_write = 0x200;
+    constexpr int mfma = 0x008, vmem = 0x010, ds_read = 0x100;
     constexpr int by = (READS + 1) / 2 < M ? 2 : (READS + M - 1) / M, first = READS / by;
-    constexpr int rest = M - first > 0 ? M - first : 1, each = (PIECES + rest - 1) / rest;
+    constexpr int rest = M - first > 0 ? M - first : 1, each = (LOADS + rest - 1) / rest;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
         __builtin_amdgcn_sched_group_barrier(mfma, 1, 0);
         if (i < first) __builtin_amdgcn_sched_group_barrier(ds_read, by, 0);
-        else if (PIECES) {
-            __builtin_amdgcn_sched_group_barrier(ds_write, each, 0);
-            __builtin_amdgcn_sched_group_barrier(vmem_read, each, 0);
-        }
+        else if (LOADS) __builtin_amdgcn_sched_group_barrier(vmem, each, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -276,18 +291,31 @@ __device__ __forceinline__ float2 join_sums(float2 a, float2 b)
 // logit is stored where it is among them.  `left`: rows of the tile that exist,
 // first: the wave's first row.  The maximum is taken and subtracted before the
 // values are scaled.
+template <bool CUT, int NI, int NJ, class R>
+__device__ __forceinline__ void column_sums(const f32x16 (&acc)[NI][NJ], int j, R row_of, int64_t left, float unit,
+                                            float &top, float &sum)
+{
+    auto z = [&](int a, int r) { return CUT && row_of(a, r) >= left ? -INFINITY : acc[a][j][r]; };
+    top = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int a = 0; a < NI; ++a)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, z(a, r));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    const float ref = top == -INFINITY ? 0.f : top, base = unit * 1.44269504f;
+#pragma unroll
+    for (int a = 0; a < NI; ++a)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((z(a, r) - ref) * base);
+    top *= unit;
+    sum += __shfl_xor(sum, 32, 64);
+}
 template <int NI, int NJ, class R>
-__device__ __forceinline__ void column_stats(f32x16 (&acc)[NI][NJ], int j, R row_of, int64_t left, int tile_rows,
+__device__ __forceinline__ void column_stats(const f32x16 (&acc)[NI][NJ], int j, R row_of, int64_t left, int tile_rows,
                                              int64_t t, int first, float unit, float *target_logit, float &top,
                                              float &sum)
 {
-    if (left < tile_rows) { // the vocabulary ends in this tile
-#pragma unroll
-        for (int a = 0; a < NI; ++a)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (row_of(a, r) >= left) acc[a][j][r] = -INFINITY;
-    }
     if (__any(t >= first && t < first + 32 * NI)) {
 #pragma unroll
         for (int a = 0; a < NI; ++a)
@@ -295,20 +323,9 @@ __device__ __forceinline__ void column_stats(f32x16 (&acc)[NI][NJ], int j, R row
             for (int r = 0; r < 16; ++r)
                 if (row_of(a, r) == t) *target_logit = acc[a][j][r] * unit;
     }
-    top = -INFINITY;
-    sum = 0.f;
-#pragma unroll
-    for (int a = 0; a < NI; ++a)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[a][j][r]);
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float ref = top == -INFINITY ? 0.f : top, base = unit * 1.44269504f;
-#pragma unroll
-    for (int a = 0; a < NI; ++a)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f((acc[a][j][r] - ref) * base);
-    top *= unit;
-    sum += __shfl_xor(sum, 32, 64);
+    if (left < tile_rows) column_sums<true>(acc, j, row_of, left, unit, top, sum); // the vocabulary ends in this tile
+    else column_sums<false>(acc, j, row_of, left, unit, top, sum);
+    __builtin_amdgcn_sched_barrier(0); // a column at a time: the next one's values would not fit the registers
 }
 
 // C[m][n] = sum_k X[m][k] Y[n][k] over tiles of (64 NI) x (64 NJ); four waves,
@@ -316,16 +333,30 @@ __device__ __forceinline__ void column_stats(f32x16 (&acc)[NI][NJ], int j, R row
 // holds column n = l % 32 and the rows m = 8 (r / 4) + 4 (l / 32) + r % 4 of
 // each, so the contiguous output index is m and the row of the output is n.
 //
-// Tiles go from memory to registers a stage ahead and from there to one of two
-// LDS buffers, and fragments are read one step of 16 ahead of the matrix
-// instructions that use them; the one barrier per stage stands before products
-// whose fragments are in registers by then.
+// A stage of both tiles goes from memory to one of two LDS buffers a stage
+// ahead, and fragments are read one step of 16 ahead of the matrix instructions
+// that use them; the one barrier per stage stands before products whose
+// fragments are in registers by then, and the loads into the buffer that it
+// frees begin behind it.  The buffers are two variables and a round of the loop
+// is two stages, so that it is known which one a load or a read means.
 template <int PL, bool XT, bool YT, int OUT, int NI, int NJ>
 __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_t K, int64_t mt, int64_t nt, Output o)
 {
-    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Terms<PL>::stage;
-    constexpr int XB = PL * TileLds<XT, TM, BK>::bytes, YB = PL * TileLds<YT, TN, BK>::bytes, STAGE = XB + YB;
-    __shared__ __align__(16) char lds[2 * STAGE];
+    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = kStage, NB = Terms<PL>::buffers;
+    constexpr int XB = PL * TileLds<XT, TM>::bytes, YB = PL * TileLds<YT, TN>::bytes, STAGE = XB + YB;
+    // how the tile leaves through LDS: values E, in parts of 64 rows and all or
+    // half of each wave's TM / 2 columns, PW of them; pitch P
+    typedef std::conditional_t<OUT == OUT_WEIGHT && PL == 1, bf16, float> E32;
+    typedef std::conditional_t<OUT == OUT_D, short, E32> E;
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    constexpr int ES = (int)sizeof(E), EV = 16 / ES, PLANES = OUT == OUT_D ? PL : 1;
+    constexpr int PM = ES == 4 && NB == 4 ? 2 : 1, PW = TM / 2 / PM;
+    constexpr int P = 2 * PW * ES + 16, PART = 64 * P, ROWV = 2 * PW / EV, PIECES = 64 * ROWV / 256;
+    constexpr int BUFFER = OUT != OUT_STATS && PLANES * PART > STAGE ? PLANES * PART : STAGE;
+    __shared__ __align__(16) char lds0[BUFFER];
+    __shared__ __align__(16) char lds1[BUFFER];
+    __shared__ __align__(16) char lds2[NB == 4 ? STAGE : 16];
+    __shared__ __align__(16) char lds3[NB == 4 ? STAGE : 16];
     int64_t mi, ni;
     int sp;
     if (!tile_of(mt, nt, OUT == OUT_SUM ? o.splits : 1, mi, ni, sp)) return;
@@ -357,11 +388,11 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         TileLoader<XT, TM, PL> x(X, m0);
         TileLoader<YT, TN, PL> y(Y, n0);
         const int stages = (int)(K / BK);
-        int in = 0; // next stage to load; the last one is loaded again past the end
-        auto load_x = [&]() { x.load((int64_t)in * BK); };
-        auto load_y = [&]() {
-            y.load((int64_t)in * BK);
-            in = in + 1 < stages ? in + 1 : in;
+        int in = 0; // next stage to load; past the last one: zeros
+        auto load = [&](char *to) {
+            x.load((int64_t)in * BK, to, in < stages);
+            y.load((int64_t)in * BK, to + XB, in < stages);
+            ++in;
         };
         auto mma = [&](const s16x8 (&a)[NI], const s16x8 (&b)[NJ]) {
 #pragma unroll
@@ -369,70 +400,64 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) acc[i][j] = Terms<PL>::mma(a[i], b[j], acc[i][j]);
         };
-        load_x();
-        load_y();
-        x.store(lds);
-        y.store(lds + XB);
-        load_x();
-        load_y();
-        __syncthreads();
         s16x8 a0[PL][NI], b0[PL][NJ], a1[PL][NI], b1[PL][NJ];
         const int rx = wm * (TM / 2), ry = wn * (TN / 2);
-        fragments<XT, TM, PL>(lds, rx, 0, a0);
-        fragments<YT, TN, PL>(lds + XB, ry, 0, b0);
-        // reads of a step's fragments, pieces of an operand moved, matrix instructions of a product
+        // reads of a step's fragments, loads of a stage, matrix instructions of a product
         constexpr int RD = PL * (NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1)), MM = NI * NJ;
-        constexpr int XV = PL * TileLds<XT, TM, BK>::vecs, YV = PL * TileLds<YT, TN, BK>::vecs;
-        int cur = 0;
-        for (int t = 0; t < stages; ++t) {
-            const char *here = lds + cur;
-            char *next = lds + (STAGE - cur);
+        constexpr int LD = PL * (TileLds<XT, TM>::vecs + TileLds<YT, TN>::vecs);
+        auto stage = [&](char *here, char *next) {
             fragments<XT, TM, PL>(here, rx, 1, a1);
             fragments<YT, TN, PL>(here + XB, ry, 1, b1);
-            x.store(next);
-            load_x();
             if constexpr (PL == 1) {
                 mma(a0[0], b0[0]);
-                interleave<MM, RD, XV>();
-                fragments<XT, TM, PL>(here, rx, 2, a0);
-                fragments<YT, TN, PL>(here + XB, ry, 2, b0);
-                y.store(next + XB);
-                load_y();
-                mma(a1[0], b1[0]);
-                interleave<MM, RD, YV>();
-                fragments<XT, TM, PL>(here, rx, 3, a1);
-                fragments<YT, TN, PL>(here + XB, ry, 3, b1);
-                mma(a0[0], b0[0]);
-                interleave<MM, RD, 0>();
-                __syncthreads();
-                __builtin_amdgcn_sched_barrier(0); // the last step's products stay behind the barrier
-                fragments<XT, TM, PL>(next, rx, 0, a0);
-                fragments<YT, TN, PL>(next + XB, ry, 0, b0);
-                mma(a1[0], b1[0]);
                 interleave<MM, RD, 0>();
             } else { // the products of terms, the small ones first
-                y.store(next + XB);
-                load_y();
                 mma(a0[1], b0[0]);
                 mma(a0[0], b0[1]);
                 mma(a0[0], b0[0]);
-                interleave<3 * MM, RD, XV + YV>();
+                interleave<3 * MM, RD, 0>();
                 mma(a1[1], b1[0]);
                 __builtin_amdgcn_sched_barrier(0);
-                __syncthreads();
-                __builtin_amdgcn_sched_barrier(0);
-                fragments<XT, TM, PL>(next, rx, 0, a0);
-                fragments<YT, TN, PL>(next + XB, ry, 0, b0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            loads_meet<(NB - 2) * LD>();       // the next stage is there
+            __builtin_amdgcn_sched_barrier(0); // the last products stay behind the barrier
+            fragments<XT, TM, PL>(next, rx, 0, a0);
+            fragments<YT, TN, PL>(next + XB, ry, 0, b0);
+            load(here);
+            if constexpr (PL == 1) {
+                mma(a1[0], b1[0]);
+                interleave<MM, RD, LD>();
+            } else {
                 mma(a1[0], b1[1]);
                 mma(a1[0], b1[0]);
-                interleave<2 * MM, RD, 0>();
+                interleave<2 * MM, RD, LD>();
             }
-            cur = STAGE - cur;
+        };
+        load(lds0);
+        load(lds1);
+        if constexpr (NB == 4) {
+            load(lds2);
+            load(lds3);
         }
+        loads_meet<(NB - 1) * LD>();
+        fragments<XT, TM, PL>(lds0, rx, 0, a0);
+        fragments<YT, TN, PL>(lds0 + XB, ry, 0, b0);
+        for (int t = 0; t < stages; t += NB) { // (what the last round has too many are stages of zeros)
+            stage(lds0, lds1);
+            if constexpr (NB == 4) {
+                stage(lds1, lds2);
+                stage(lds2, lds3);
+                stage(lds3, lds0);
+            } else {
+                stage(lds1, lds0);
+            }
+        }
+        loads_meet<0>(); // none is on its way into the buffers that are used again below
     }
     auto row_of = [&](int i, int r) { return wm * (TM / 2) + i * 32 + 8 * (r / 4) + 4 * (lane >> 5) + (r % 4); };
     if constexpr (OUT == OUT_STATS) {
-        float(*red)[2][TN] = reinterpret_cast<float(*)[2][TN]>(lds);
+        float(*red)[2][TN] = reinterpret_cast<float(*)[2][TN]>(lds0);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -460,13 +485,6 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
     } else {
         // 64 rows at a time pass through LDS, so that they are written in whole
         // lines: a lane holds four columns of one row, a wave 32 rows
-        typedef std::conditional_t<OUT == OUT_WEIGHT && PL == 1, bf16, float> E32;
-        typedef std::conditional_t<OUT == OUT_D, short, E32> E;
-        typedef E E4 __attribute__((ext_vector_type(4)));
-        constexpr int ES = (int)sizeof(E), EV = 16 / ES, PLANES = OUT == OUT_D ? PL : 1;
-        constexpr int P = TM * ES + 16, PART = 64 * P, ROWV = TM / EV, PIECES = 64 * ROWV / 256;
-        constexpr bool TWO = 2 * PLANES * PART <= 2 * STAGE; // one part is written while the last is read
-        static_assert(PLANES * PART <= 2 * STAGE, "a part fits the tiles' space");
         float unit = 1.f;
         if constexpr (OUT == OUT_D) unit = *o.top_grad;
         if constexpr (OUT == OUT_WEIGHT)
@@ -490,65 +508,78 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                     lse = INFINITY;
                 }
             }
-            const bool here = __any(t >= wm * (TM / 2) && t < (wm + 1) * (TM / 2));
-            char *part = lds + (TWO ? (j & 1) * PLANES * PART : 0);
-            if (!TWO && j) __syncthreads();
+            const bool special = __any(t >= wm * (TM / 2) && t < (wm + 1) * (TM / 2)) || left < TM;
 #pragma unroll
-            for (int a = 0; a < NI; ++a)
+            for (int h = 0; h < PM; ++h) {
+                char *part = (j * PM + h) & 1 ? lds1 : lds0; // one is written while the last is read
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int m = row_of(a, 4 * q);
-                    E4 w[PLANES];
+                for (int a = h * (NI / PM); a < (h + 1) * (NI / PM); ++a)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = acc[a][j][4 * q + r];
+                    for (int q = 0; q < 4; ++q) {
+                        const int m = row_of(a, 4 * q), mp = m - h * PW - wm * (TM / 2 - PW);
+                        E4 w[PLANES];
+                        float x[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[r] = acc[a][j][4 * q + r];
                         if constexpr (OUT == OUT_D) {
-                            float p = __builtin_amdgcn_exp2f(fmaf(x, scale, -lse) * 1.44269504f);
-                            if (here) p -= m + r == t ? 1.f : 0.f;
-                            if (left < TM && m + r >= left) p = 0.f;
-                            short s[PL];
-                            split<PL>(g * p, s);
 #pragma unroll
-                            for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
-                        } else {
-                            w[0][r] = (E)(x * unit);
-                        }
-                    }
+                            for (int r = 0; r < 4; ++r)
+                                x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], scale, -lse) * 1.44269504f);
+                            if (special) { // a target, or the vocabulary's end
 #pragma unroll
-                    for (int q2 = 0; q2 < PLANES; ++q2)
-                        *reinterpret_cast<E4 *>(part + q2 * PART + (wn * 32 + (lane & 31)) * P + m * ES) = w[q2];
-                }
-            __syncthreads();
-#pragma unroll
-            for (int q2 = 0; q2 < PLANES; ++q2)
-#pragma unroll
-                for (int k = 0; k < PIECES; ++k) {
-                    const int c = tid + k * 256, r = c / ROWV;
-                    const int64_t row = n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31), m = m0 + c % ROWV * EV;
-                    const char *from = part + q2 * PART + r * P + c % ROWV * 16;
-                    if constexpr (OUT == OUT_D) {
-                        *reinterpret_cast<u32x4 *>(o.d + q2 * o.plane_d + row * o.ldd + m) =
-                            *reinterpret_cast<const u32x4 *>(from);
-                    } else {
-                        const int64_t to = OUT == OUT_WEIGHT ? o.v0 + row : row;
-                        if (to >= (OUT == OUT_WEIGHT ? o.V : o.sum_rows) || m >= o.D) continue;
-                        const int have = o.D - m < EV ? (int)(o.D - m) : EV;
-                        float x[EV];
-                        load_vec<E, EV>(reinterpret_cast<const E *>(from), x);
-                        if constexpr (OUT == OUT_SUM) {
-                            float *s = o.sum + to * o.D + m;
-                            if (!o.first) {
-                                float old[EV];
-                                load_part<float, EV>(s, have, old);
-#pragma unroll
-                                for (int e = 0; e < EV; ++e) x[e] += old[e];
+                                for (int r = 0; r < 4; ++r) {
+                                    if (m + r == t) x[r] -= 1.f;
+                                    if (m + r >= left) x[r] = 0.f;
+                                }
                             }
-                            store_part<float, EV>(s, have, x);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                short s[PL];
+                                split<PL>(g * x[r], s);
+#pragma unroll
+                                for (int q2 = 0; q2 < PL; ++q2) w[q2][r] = s[q2];
+                            }
                         } else {
-                            store_part<E, EV>(static_cast<E *>(o.out) + to * o.ld_out + m, have, x);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) w[0][r] = (E)(x[r] * unit);
+                        }
+#pragma unroll
+                        for (int q2 = 0; q2 < PLANES; ++q2)
+                            *reinterpret_cast<E4 *>(part + q2 * PART + (wn * 32 + (lane & 31)) * P + mp * ES) = w[q2];
+                    }
+                __syncthreads();
+#pragma unroll
+                for (int q2 = 0; q2 < PLANES; ++q2)
+#pragma unroll
+                    for (int k = 0; k < PIECES; ++k) {
+                        const int c = tid + k * 256, r = c / ROWV, mp = c % ROWV * EV;
+                        const int64_t row = n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31);
+                        const int64_t m = m0 + mp / PW * (TM / 2) + h * PW + mp % PW;
+                        const char *from = part + q2 * PART + r * P + c % ROWV * 16;
+                        if constexpr (OUT == OUT_D) {
+                            *reinterpret_cast<u32x4 *>(o.d + q2 * o.plane_d + row * o.ldd + m) =
+                                *reinterpret_cast<const u32x4 *>(from);
+                        } else {
+                            const int64_t to = OUT == OUT_WEIGHT ? o.v0 + row : row;
+                            if (to >= (OUT == OUT_WEIGHT ? o.V : o.sum_rows) || m >= o.D) continue;
+                            const int have = o.D - m < EV ? (int)(o.D - m) : EV;
+                            float x[EV];
+                            load_vec<E, EV>(reinterpret_cast<const E *>(from), x);
+                            if constexpr (OUT == OUT_SUM) {
+                                float *s = o.sum + to * o.D + m;
+                                if (!o.first) {
+                                    float old[EV];
+                                    load_part<float, EV>(s, have, old);
+#pragma unroll
+                                    for (int e = 0; e < EV; ++e) x[e] += old[e];
+                                }
+                                store_part<float, EV>(s, have, x);
+                            } else {
+                                store_part<E, EV>(static_cast<E *>(o.out) + to * o.ld_out + m, have, x);
+                            }
                         }
                     }
-                }
+            }
         }
     }
 }
@@ -768,36 +799,48 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
                     here_hit[b] = __any(hit[b] == st);
                 }
             }
+            // exponentials
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float ls[4], sc[4], gr[4];
-                int ht[4];
+                float ls[4], sc[4];
                 if constexpr (VOC) {
-                    const int at = 8 * e + 4 * half;
-                    load_vec<float, 4>(&of_row[buf][0][at], sc);
-                    load_vec<float, 4>(&of_row[buf][1][at], ls);
-                    load_vec<float, 4>(&of_row[buf][2][at], gr);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) ht[r] = hit_row[buf][at + r];
+                    load_vec<float, 4>(&of_row[buf][0][8 * e + 4 * half], sc);
+                    load_vec<float, 4>(&of_row[buf][1][8 * e + 4 * half], ls);
                 }
 #pragma unroll
                 for (int b = 0; b < NO; ++b)
 #pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        z[b][4 * e + r] = __builtin_amdgcn_exp2f(
+                            fmaf(z[b][4 * e + r], VOC ? sc[r] : scale[b], VOC ? -ls[r] : -lse[b]) * 1.44269504f);
+            }
+            // targets, and streamed rows past the vocabulary's end
+#pragma unroll
+            for (int b = 0; b < NO; ++b) {
+                if (here_hit[b]) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const bool is = VOC ? hit_row[buf][row_of(r)] == (wave * NO + b) * 32 + (lane & 31)
+                                            : hit[b] == st && row_of(r) == hit_row_of[b];
+                        if (is) z[b][r] -= 1.f;
+                    }
+                }
+                if (!VOC && left < kNarrowStep) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row_of(r) >= left) z[b][r] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float gr[4];
+                if constexpr (VOC) load_vec<float, 4>(&of_row[buf][2][8 * e + 4 * half], gr);
+#pragma unroll
+                for (int b = 0; b < NO; ++b)
+#pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float x = z[b][4 * e + r];
-                        float p;
-                        if constexpr (VOC) {
-                            p = __builtin_amdgcn_exp2f(fmaf(x, sc[r], -ls[r]) * 1.44269504f);
-                            if (here_hit[b]) p -= ht[r] == (wave * NO + b) * 32 + (lane & 31) ? 1.f : 0.f;
-                            p *= gr[r];
-                        } else {
-                            p = __builtin_amdgcn_exp2f(fmaf(x, scale[b], -lse[b]) * 1.44269504f);
-                            if (here_hit[b]) p -= hit[b] == st && row_of(4 * e + r) == hit_row_of[b] ? 1.f : 0.f;
-                            if (left < kNarrowStep && row_of(4 * e + r) >= left) p = 0.f;
-                            p *= g[b];
-                        }
                         short w[PL];
-                        split<PL>(p, w);
+                        split<PL>(z[b][4 * e + r] * (VOC ? gr[r] : g[b]), w);
 #pragma unroll
                         for (int q = 0; q < PL; ++q) d[q][b][e >> 1][(e & 1) * 4 + r] = w[q];
                     }
