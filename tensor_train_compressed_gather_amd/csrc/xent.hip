@@ -263,18 +263,24 @@ inline unsigned tile_grid(int64_t mt, int64_t nt, int splits)
 
 // Order of a step's instructions: the reads of the next step's fragments two
 // to a matrix instruction, so that they are there when that step begins; then
-// the loads of a later stage.
+// loads, evenly: where they follow each other faster than the cache delivers,
+// the wave waits at each.
 template <int M, int READS, int LOADS>
 __device__ __forceinline__ void interleave()
 {
     constexpr int mfma = 0x008, vmem = 0x010, ds_read = 0x100;
     constexpr int by = (READS + 1) / 2 < M ? 2 : (READS + M - 1) / M, first = READS / by;
-    constexpr int rest = M - first > 0 ? M - first : 1, each = (LOADS + rest - 1) / rest;
+    constexpr int rest = M - first > 0 ? M - first : 1;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
         __builtin_amdgcn_sched_group_barrier(mfma, 1, 0);
-        if (i < first) __builtin_amdgcn_sched_group_barrier(ds_read, by, 0);
-        else if (LOADS) __builtin_amdgcn_sched_group_barrier(vmem, each, 0);
+        if (i < first) {
+            __builtin_amdgcn_sched_group_barrier(ds_read, by, 0);
+        } else {
+            const int now = (i - first + 1) * LOADS / rest - (i - first) * LOADS / rest;
+#pragma unroll
+            for (int k = 0; k < now; ++k) __builtin_amdgcn_sched_group_barrier(vmem, 1, 0);
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -284,6 +290,18 @@ __device__ __forceinline__ float2 join_sums(float2 a, float2 b)
 {
     const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
     return make_float2(m, a.y * __expf(a.x - ref) + b.y * __expf(b.x - ref));
+}
+
+// Columns from `j` on stay in the accumulator registers: read there all at
+// once, behind the products, they would not fit the others and go to memory.
+template <int NI, int NJ>
+__device__ __forceinline__ void keep_columns(f32x16 (&acc)[NI][NJ], int j)
+{
+#pragma unroll
+    for (int a = 0; a < NI; ++a)
+#pragma unroll
+        for (int i = 0; i < NJ; ++i)
+            if (i >= j) asm volatile("" : "+a"(acc[a][i]));
 }
 
 // Maximum and sum of exponentials of one column of a wave's NI 32 x 32 tiles of
@@ -325,7 +343,6 @@ __device__ __forceinline__ void column_stats(const f32x16 (&acc)[NI][NJ], int j,
     }
     if (left < tile_rows) column_sums<true>(acc, j, row_of, left, unit, top, sum); // the vocabulary ends in this tile
     else column_sums<false>(acc, j, row_of, left, unit, top, sum);
-    __builtin_amdgcn_sched_barrier(0); // a column at a time: the next one's values would not fit the registers
 }
 
 // C[m][n] = sum_k X[m][k] Y[n][k] over tiles of (64 NI) x (64 NJ); four waves,
@@ -389,8 +406,8 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         TileLoader<YT, TN, PL> y(Y, n0);
         const int stages = (int)(K / BK);
         int in = 0; // next stage to load; past the last one: zeros
-        auto load = [&](char *to) {
-            x.load((int64_t)in * BK, to, in < stages);
+        auto load_x = [&](char *to) { x.load((int64_t)in * BK, to, in < stages); };
+        auto load_y = [&](char *to) {
             y.load((int64_t)in * BK, to + XB, in < stages);
             ++in;
         };
@@ -404,13 +421,16 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         const int rx = wm * (TM / 2), ry = wn * (TN / 2);
         // reads of a step's fragments, loads of a stage, matrix instructions of a product
         constexpr int RD = PL * (NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1)), MM = NI * NJ;
-        constexpr int LD = PL * (TileLds<XT, TM>::vecs + TileLds<YT, TN>::vecs);
-        auto stage = [&](char *here, char *next) {
+        constexpr int LX = PL * TileLds<XT, TM>::vecs, LY = PL * TileLds<YT, TN>::vecs;
+        // The loads into a buffer follow the barrier behind its last reads; of
+        // four buffers, Y's wait for the next stage's first step.
+        auto stage = [&](char *last, char *here, char *next) {
             fragments<XT, TM, PL>(here, rx, 1, a1);
             fragments<YT, TN, PL>(here + XB, ry, 1, b1);
             if constexpr (PL == 1) {
+                load_y(last);
                 mma(a0[0], b0[0]);
-                interleave<MM, RD, 0>();
+                interleave<MM, RD, LY>();
             } else { // the products of terms, the small ones first
                 mma(a0[1], b0[0]);
                 mma(a0[0], b0[1]);
@@ -420,37 +440,42 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                 __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            loads_meet<(NB - 2) * LD>();       // the next stage is there
-            __builtin_amdgcn_sched_barrier(0); // the last products stay behind the barrier
+            loads_meet<(NB - 2) * (LX + LY)>(); // the next stage is there
+            __builtin_amdgcn_sched_barrier(0);  // the last products stay behind the barrier
             fragments<XT, TM, PL>(next, rx, 0, a0);
             fragments<YT, TN, PL>(next + XB, ry, 0, b0);
-            load(here);
+            load_x(here);
             if constexpr (PL == 1) {
                 mma(a1[0], b1[0]);
-                interleave<MM, RD, LD>();
+                interleave<MM, RD, LX>();
             } else {
+                load_y(here);
                 mma(a1[0], b1[1]);
                 mma(a1[0], b1[0]);
-                interleave<2 * MM, RD, LD>();
+                interleave<2 * MM, RD, LX + LY>();
             }
         };
-        load(lds0);
-        load(lds1);
+        load_x(lds0);
+        load_y(lds0);
+        load_x(lds1);
+        load_y(lds1);
         if constexpr (NB == 4) {
-            load(lds2);
-            load(lds3);
+            load_x(lds2);
+            load_y(lds2);
+            load_x(lds3);
         }
-        loads_meet<(NB - 1) * LD>();
+        loads_meet<NB == 4 ? 3 * LX + 2 * LY : LX + LY>();
         fragments<XT, TM, PL>(lds0, rx, 0, a0);
         fragments<YT, TN, PL>(lds0 + XB, ry, 0, b0);
         for (int t = 0; t < stages; t += NB) { // (what the last round has too many are stages of zeros)
-            stage(lds0, lds1);
             if constexpr (NB == 4) {
-                stage(lds1, lds2);
-                stage(lds2, lds3);
-                stage(lds3, lds0);
+                stage(lds3, lds0, lds1);
+                stage(lds0, lds1, lds2);
+                stage(lds1, lds2, lds3);
+                stage(lds2, lds3, lds0);
             } else {
-                stage(lds1, lds0);
+                stage(lds1, lds0, lds1);
+                stage(lds0, lds1, lds0);
             }
         }
         loads_meet<0>(); // none is on its way into the buffers that are used again below
@@ -461,6 +486,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
+            keep_columns(acc, j);
             const int nl = wn * (TN / 2) + j * 32 + (lane & 31);
             const int64_t i = n0 + nl;
             const int64_t t = i < o.n ? o.targets[i] - m0 : -1;
@@ -493,6 +519,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
+            keep_columns(acc, j);
             const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
             // rows that do not count, or lie past the last: d = 0 (exp - 0)
             float lse = 0.f, g = 0.f, scale = 1.f;
