@@ -142,44 +142,60 @@ typedef __attribute__((address_space(3))) void *lds_void;
 // load fills 1 KB of LDS in the order of its lanes, so the pieces change places
 // by the address that each lane reads.  Loads go through a buffer descriptor
 // that ends with the matrix, so rows past it (of the outputs or of the summed
-// index) are written as zeros and no address needs a clamp.
+// index) are written as zeros and no address needs a clamp; so are stages past
+// the last.  What a stage's descriptor takes is kept up by additions.
 template <bool TURNED, int R, int PL>
 struct TileLoader {
     typedef TileLds<TURNED, R> L;
     static constexpr int N = L::vecs, ROWV = L::pitch / 16; // pieces in a tile's row
-    const short *p; // plane 0, moved to the tile's first row (straight) or column (turned)
-    int64_t ld, plane, end; // end: elements from p to the end of plane 0
-    int off;        // byte offset of this thread's first piece; the others are 256 / ROWV rows apart
-    int step, to;   // to: the wave's place in LDS
+    const short *p;     // plane 0, the next stage
+    int64_t plane, next; // elements to the next plane, to the next stage
+    int whole;          // stages to come that lie inside the matrix
+    unsigned bytes, rest; // of those, of the one at the matrix's end (turned)
+    int off;            // byte offset of this thread's first piece; the others are 256 / ROWV rows apart
+    int step, to;       // to: the wave's place in LDS
 
-    __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0)
+    __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0, int stages)
     {
-        ld = a.ld;
+        const int ld = (int)a.ld;
         plane = a.plane;
         p = a.p + (TURNED ? r0 : r0 * a.ld);
-        end = (a.rows - 1) * a.ld + a.cols - (TURNED ? r0 : r0 * a.ld);
+        next = TURNED ? kStage * a.ld : kStage;
+        if constexpr (TURNED) {
+            const int64_t full = a.rows / kStage;
+            const int cols = (int)(a.cols - r0 < R ? a.cols - r0 : R), left = (int)(a.rows - full * kStage);
+            whole = cols > 0 ? (int)(full < stages ? full : stages) : 0;
+            bytes = (unsigned)((kStage - 1) * ld + cols) * 2;
+            rest = full < stages && left && cols > 0 ? (unsigned)((left - 1) * ld + cols) * 2 : 0;
+        } else {
+            const int rows = (int)(a.rows - r0 < R ? a.rows - r0 : R);
+            whole = rows > 0 ? stages : 0; // (a tile of d's padding has none)
+            bytes = (unsigned)((rows - 1) * ld + (int)a.cols) * 2;
+            rest = 0;
+        }
         const int t = threadIdx.x, row = t / ROWV;
-        off = (row * (int)ld + ((t % ROWV) ^ L::turn(row)) * 8) * 2;
-        step = 256 / ROWV * (int)ld * 2;
+        off = (row * ld + ((t % ROWV) ^ L::turn(row)) * 8) * 2;
+        step = 256 / ROWV * ld * 2;
         to = __builtin_amdgcn_readfirstlane(t >> 6) * 1024;
     }
-    __device__ __forceinline__ void load(int64_t k0, char *lds, bool there) const
+    __device__ __forceinline__ void load(char *lds)
     {
-        const int64_t skip = TURNED ? k0 * ld : k0;
-        const int64_t left = (end - skip) * 2;
-        // (without a branch, which would part the loads from the products around them)
-        const unsigned bytes = (left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left) & -(unsigned)there;
+        const unsigned now = whole > 0 ? bytes : whole == 0 ? rest : 0;
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
-            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<short *>(p + q * plane + skip), 0, bytes, 0x00027000);
+            const __amdgpu_buffer_rsrc_t r =
+                __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(p + q * plane), 0, now, 0x00027000);
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(lds + q * L::bytes + i * 4096 + to), 16, off,
                                                          i * step, 0, 0);
         }
+        p += next;
+        --whole;
+        if constexpr (!TURNED) bytes -= kStage * 2;
     }
 };
+
 // Every wave's reads of LDS are done, and so are all but its last N loads.  A
 // barrier of the language would wait for every load in flight; the fences here
 // order the compiler's accesses and cost nothing.
@@ -402,15 +418,11 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     {
-        TileLoader<XT, TM, PL> x(X, m0);
-        TileLoader<YT, TN, PL> y(Y, n0);
         const int stages = (int)(K / BK);
-        int in = 0; // next stage to load; past the last one: zeros
-        auto load_x = [&](char *to) { x.load((int64_t)in * BK, to, in < stages); };
-        auto load_y = [&](char *to) {
-            y.load((int64_t)in * BK, to + XB, in < stages);
-            ++in;
-        };
+        TileLoader<XT, TM, PL> x(X, m0, stages);
+        TileLoader<YT, TN, PL> y(Y, n0, stages);
+        auto load_x = [&](char *to) { x.load(to); };
+        auto load_y = [&](char *to) { y.load(to + XB); };
         auto mma = [&](const s16x8 (&a)[NI], const s16x8 (&b)[NJ]) {
 #pragma unroll
             for (int i = 0; i < NI; ++i)
