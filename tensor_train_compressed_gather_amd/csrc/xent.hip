@@ -42,13 +42,10 @@ constexpr int kUnitExp = 15;           // fp16 terms: d is kept in units of 2^-1
 
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-constexpr int kStage = 32; // summed values per stage: two steps of 16
-
 // PL planes of 16-bit terms: one of bf16, or two of fp16.
 template <int PL>
 struct Terms {
     typedef bf16 type;
-    static constexpr int buffers = 4; // stages in LDS
     static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
@@ -58,7 +55,6 @@ struct Terms {
 template <>
 struct Terms<2> {
     typedef f16 type;
-    static constexpr int buffers = 2;
     static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c)
     {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
@@ -82,6 +78,16 @@ __device__ __forceinline__ bool row_counts(int64_t target, int64_t ignore, int64
 {
     return target != ignore && target >= 0 && target < V;
 }
+
+// Summed values per stage and stages in LDS.  Straight rows of 64 bf16 are
+// whole cache lines, and half the barriers; turned ones are lines anyway, and
+// more and shorter stages leave their loads more time (8192 rows, K = 4096 and
+// 8192: logits 7.24 ms with stages of 32, 6.86 of 64; the weight's gradient 770
+// and 826 us a piece).
+template <int PL, bool XT>
+struct Stages {
+    static constexpr int values = PL == 1 && !XT ? 64 : 32, buffers = PL == 1 && XT ? 4 : 2;
+};
 
 // An operand of a product: PL matrices of 16-bit values.  Straight: row r holds
 // the summed index.  Turned: row k of the summed index holds the outputs.
@@ -124,15 +130,14 @@ struct Output {
 // Which of a row's pieces change places (`turn`) is chosen so that the sixteen
 // rows that sixteen lanes read lie in different banks (straight), and so do
 // the four rows of 64 bytes that half a wave's transposing read touches.
-template <bool TURNED, int R>
+template <bool TURNED, int R, int BK>
 struct TileLds {
-    static constexpr int BK = kStage;
     static constexpr int pitch = (TURNED ? R : BK) * 2;
     static constexpr int bytes = R * BK * 2;
     static constexpr int vecs = R * BK / 8 / 256; // 16-byte pieces per thread
     static __device__ __forceinline__ int turn(int row)
     {
-        return TURNED ? (row & 3) << 2 : (row >> 2) & 3;
+        return TURNED ? (row & 3) << 2 : BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
     }
 };
 
@@ -144,9 +149,9 @@ typedef __attribute__((address_space(3))) void *lds_void;
 // that ends with the matrix, so rows past it (of the outputs or of the summed
 // index) are written as zeros and no address needs a clamp; so are stages past
 // the last.  What a stage's descriptor takes is kept up by additions.
-template <bool TURNED, int R, int PL>
+template <bool TURNED, int R, int BK, int PL>
 struct TileLoader {
-    typedef TileLds<TURNED, R> L;
+    typedef TileLds<TURNED, R, BK> L;
     static constexpr int N = L::vecs, ROWV = L::pitch / 16; // pieces in a tile's row
     const short *p;     // plane 0, the next stage
     int64_t plane, next; // elements to the next plane, to the next stage
@@ -160,12 +165,12 @@ struct TileLoader {
         const int ld = (int)a.ld;
         plane = a.plane;
         p = a.p + (TURNED ? r0 : r0 * a.ld);
-        next = TURNED ? kStage * a.ld : kStage;
+        next = TURNED ? BK * a.ld : BK;
         if constexpr (TURNED) {
-            const int64_t full = a.rows / kStage;
-            const int cols = (int)(a.cols - r0 < R ? a.cols - r0 : R), left = (int)(a.rows - full * kStage);
+            const int64_t full = a.rows / BK;
+            const int cols = (int)(a.cols - r0 < R ? a.cols - r0 : R), left = (int)(a.rows - full * BK);
             whole = cols > 0 ? (int)(full < stages ? full : stages) : 0;
-            bytes = (unsigned)((kStage - 1) * ld + cols) * 2;
+            bytes = (unsigned)((BK - 1) * ld + cols) * 2;
             rest = full < stages && left && cols > 0 ? (unsigned)((left - 1) * ld + cols) * 2 : 0;
         } else {
             const int rows = (int)(a.rows - r0 < R ? a.rows - r0 : R);
@@ -192,7 +197,7 @@ struct TileLoader {
         }
         p += next;
         --whole;
-        if constexpr (!TURNED) bytes -= kStage * 2;
+        if constexpr (!TURNED) bytes -= BK * 2;
     }
 };
 
@@ -213,10 +218,10 @@ __device__ __forceinline__ void loads_meet()
 // [ks * 16, ks * 16 + 16): lane l gets row l % 32, values 8 (l / 32) .. + 7.
 // A transposing read gives each of sixteen lanes one column of the four rows
 // that the sixteen lanes' 8-byte addresses name.
-template <bool TURNED, int R, int PL, int N>
+template <bool TURNED, int R, int BK, int PL, int N>
 __device__ __forceinline__ void fragments(const char *lds, int r0, int ks, s16x8 (&f)[PL][N])
 {
-    typedef TileLds<TURNED, R> L;
+    typedef TileLds<TURNED, R, BK> L;
     constexpr int P = L::pitch;
     const int l = threadIdx.x & 63, half = l >> 5;
     if constexpr (!TURNED) {
@@ -366,17 +371,18 @@ __device__ __forceinline__ void column_stats(const f32x16 (&acc)[NI][NJ], int j,
 // holds column n = l % 32 and the rows m = 8 (r / 4) + 4 (l / 32) + r % 4 of
 // each, so the contiguous output index is m and the row of the output is n.
 //
-// A stage of both tiles goes from memory to one of two LDS buffers a stage
-// ahead, and fragments are read one step of 16 ahead of the matrix instructions
-// that use them; the one barrier per stage stands before products whose
-// fragments are in registers by then, and the loads into the buffer that it
-// frees begin behind it.  The buffers are two variables and a round of the loop
-// is two stages, so that it is known which one a load or a read means.
+// Stages of both tiles go from memory to LDS buffers ahead of their use, and
+// fragments are read one step of 16 ahead of the matrix instructions that use
+// them; the one barrier per stage stands before products whose fragments are in
+// registers by then, and the loads into the buffer that it frees begin behind
+// it.  The buffers are variables and a round of the loop passes all of them, so
+// that the compiler knows which one a load or a read means and does not wait
+// for the others.
 template <int PL, bool XT, bool YT, int OUT, int NI, int NJ>
 __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_t K, int64_t mt, int64_t nt, Output o)
 {
-    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = kStage, NB = Terms<PL>::buffers;
-    constexpr int XB = PL * TileLds<XT, TM>::bytes, YB = PL * TileLds<YT, TN>::bytes, STAGE = XB + YB;
+    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Stages<PL, XT>::values, NB = Stages<PL, XT>::buffers;
+    constexpr int XB = PL * TileLds<XT, TM, BK>::bytes, YB = PL * TileLds<YT, TN, BK>::bytes, STAGE = XB + YB;
     // how the tile leaves through LDS: values E, in parts of 64 rows and all or
     // half of each wave's TM / 2 columns, PW of them; pitch P
     typedef std::conditional_t<OUT == OUT_WEIGHT && PL == 1, bf16, float> E32;
@@ -419,8 +425,8 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     {
         const int stages = (int)(K / BK);
-        TileLoader<XT, TM, PL> x(X, m0, stages);
-        TileLoader<YT, TN, PL> y(Y, n0, stages);
+        TileLoader<XT, TM, BK, PL> x(X, m0, stages);
+        TileLoader<YT, TN, BK, PL> y(Y, n0, stages);
         auto load_x = [&](char *to) { x.load(to); };
         auto load_y = [&](char *to) { y.load(to + XB); };
         auto mma = [&](const s16x8 (&a)[NI], const s16x8 (&b)[NJ]) {
@@ -433,29 +439,38 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         const int rx = wm * (TM / 2), ry = wn * (TN / 2);
         // reads of a step's fragments, loads of a stage, matrix instructions of a product
         constexpr int RD = PL * (NI * (XT ? 2 : 1) + NJ * (YT ? 2 : 1)), MM = NI * NJ;
-        constexpr int LX = PL * TileLds<XT, TM>::vecs, LY = PL * TileLds<YT, TN>::vecs;
-        // The loads into a buffer follow the barrier behind its last reads; of
-        // four buffers, Y's wait for the next stage's first step.
+        constexpr int LX = PL * TileLds<XT, TM, BK>::vecs, LY = PL * TileLds<YT, TN, BK>::vecs;
+        auto read = [&](const char *from, int ks, s16x8 (&a)[PL][NI], s16x8 (&b)[PL][NJ]) {
+            fragments<XT, TM, BK, PL>(from, rx, ks, a);
+            fragments<YT, TN, BK, PL>(from + XB, ry, ks, b);
+        };
+        // A buffer's loads begin behind the barrier that follows its last reads;
+        // bf16: X's there, Y's in the next stage's first step.
         auto stage = [&](char *last, char *here, char *next) {
-            fragments<XT, TM, PL>(here, rx, 1, a1);
-            fragments<YT, TN, PL>(here + XB, ry, 1, b1);
+            read(here, 1, a1, b1);
             if constexpr (PL == 1) {
                 load_y(last);
                 mma(a0[0], b0[0]);
                 interleave<MM, RD, LY>();
+                if constexpr (BK == 64) {
+                    read(here, 2, a0, b0);
+                    mma(a1[0], b1[0]);
+                    interleave<MM, RD, 0>();
+                    read(here, 3, a1, b1);
+                    mma(a0[0], b0[0]);
+                    interleave<MM, RD, 0>();
+                }
             } else { // the products of terms, the small ones first
                 mma(a0[1], b0[0]);
                 mma(a0[0], b0[1]);
                 mma(a0[0], b0[0]);
                 interleave<3 * MM, RD, 0>();
                 mma(a1[1], b1[0]);
-                __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_sched_barrier(0);
             loads_meet<(NB - 2) * (LX + LY)>(); // the next stage is there
             __builtin_amdgcn_sched_barrier(0);  // the last products stay behind the barrier
-            fragments<XT, TM, PL>(next, rx, 0, a0);
-            fragments<YT, TN, PL>(next + XB, ry, 0, b0);
+            read(next, 0, a0, b0);
             load_x(here);
             if constexpr (PL == 1) {
                 mma(a1[0], b1[0]);
@@ -467,18 +482,18 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                 interleave<2 * MM, RD, LX + LY>();
             }
         };
+        // all but the last buffer's Y, which the first stage asks for (bf16)
         load_x(lds0);
         load_y(lds0);
         load_x(lds1);
-        load_y(lds1);
+        if constexpr (NB == 4 || PL == 2) load_y(lds1);
         if constexpr (NB == 4) {
             load_x(lds2);
             load_y(lds2);
             load_x(lds3);
         }
-        loads_meet<NB == 4 ? 3 * LX + 2 * LY : LX + LY>();
-        fragments<XT, TM, PL>(lds0, rx, 0, a0);
-        fragments<YT, TN, PL>(lds0 + XB, ry, 0, b0);
+        loads_meet<(NB - 1) * (LX + LY) - (PL == 1 ? LY : 0)>();
+        read(lds0, 0, a0, b0);
         for (int t = 0; t < stages; t += NB) { // (what the last round has too many are stages of zeros)
             if constexpr (NB == 4) {
                 stage(lds3, lds0, lds1);
