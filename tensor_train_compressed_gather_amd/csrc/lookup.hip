@@ -7,6 +7,11 @@
 // sorted stably by token, fixed tiles of the sorted positions are summed by
 // one worker each, and only runs of one token that cover a whole tile are cut
 // and joined by a second kernel in a fixed order.
+//
+// Memory bounds the large sizes: 65536 tokens of 131072 x 1024 bf16 in 47 us
+// (268 MB), their gradient in 135 us, of which 92 are the sums and the rows of
+// zeros (402 MB), 28 the sort, 14 the joins.  32768 tokens of 64 fp32 columns
+// are bound by the chain of six dependent launches: 5 us and 43.
 #include "lm.h"
 #include "primitives.h"
 
@@ -91,7 +96,8 @@ __global__ __launch_bounds__(256) void k_lookup_keys(LookupArgs a, uint32_t *key
 // Stable LSD radix sort of up to kTokSortMax tokens in few launches, which is
 // what bounds so small a sort: digits of up to ten bits (two passes for
 // vocabularies below 2^20), every tile's block adding up the other tiles'
-// digit counts itself instead of a scan between two kernels.  One tile is
+// digit counts itself instead of a scan between two kernels (32768 tokens: 25 us
+// in four launches; tiles of 1024 take the same, of 512 longer).  One tile is
 // sorted in LDS by one launch.
 struct RankLds {
     uint16_t wave[kTokThreads / 64][kTokDigits];

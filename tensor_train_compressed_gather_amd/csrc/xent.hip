@@ -7,7 +7,13 @@
 // registers of the tile that makes them: a first pass keeps each row's maximum
 // and sum of exponentials per tile, from which lse and the loss follow; for
 // the gradients a piece of the vocabulary's logits is made again, turned into
-// d, and multiplied into both gradients before the next piece.
+// d, and multiplied into both gradients before the next piece.  Rows of up to
+// 128 values take kernels of their own, which never write d.
+//
+// Matrix instructions bound the large sizes, the weight's bytes those of few
+// rows, launches the smallest.  8192 rows against 131072 x 4096 in bf16: 26.1 ms
+// with both gradients, four products (the logits are made twice) of 8.8 TFLOP
+// at 1350 TFLOP/s; 5 rows, loss only: 179 us, 6.0 TB/s.
 //
 // fp32 inputs are scaled by powers of two (to a largest magnitude in
 // [2^14, 2^15): each hidden row for the logits, the hidden rows that count as a
@@ -654,15 +660,18 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 //   VOC_GRAD   own: rows of the weight, streamed: hidden rows: dW.
 //
 // The logits are made three times instead of twice, and matrix instructions
-// bound it: 2048 fp32 rows of 128 against 10^6, 7.2 ms with both gradients, of
+// bound it: 2048 fp32 rows of 128 against 10^6, 7.1 ms with both gradients, of
 // which five sums of three products are 5.2 at the card's rate (10.7 by the
-// products above); bf16 3.3 ms, where the exponentials' vector instructions take
+// products above); bf16 2.9 ms, where the exponentials' vector instructions take
 // as long as the products.  fp16 terms: the hidden rows keep their own scales in
 // dW's product too, so there d_i carries the ratio to the largest row's scale,
 // at most 1.
 enum { ROW_STATS, ROW_GRAD, VOC_GRAD };
 constexpr int kNarrowStep = 32;
 constexpr int64_t kNarrowSteps = 8;    // least steps of a split
+// fp32: steps after which a sum is added to memory.  Six additions a step to one
+// accumulator would round 10^6 rows' sum to 2^-19.6, in parts of 8192 rows to 2^-21.
+constexpr int kNarrowChain = 256;
 constexpr int64_t kNarrow = 128;       // longest rows
 constexpr int64_t kNarrowRows = 1ll << 31;
 
@@ -725,14 +734,6 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
         }
     }
     f32x16 acc[MODE == ROW_STATS ? 1 : NO][CB];
-    if constexpr (MODE != ROW_STATS) {
-#pragma unroll
-        for (int b = 0; b < NO; ++b)
-#pragma unroll
-            for (int c = 0; c < CB; ++c)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[b][c][r] = 0.f;
-    }
 
     // streamed rows: memory to registers a step ahead, registers to one of two LDS buffers
     const int64_t end = (str.rows - 1) * str.ld + str.cols;
@@ -770,7 +771,8 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int row = tid / PR + i * (256 / PR);
-                *reinterpret_cast<u32x4 *>(to + q * PLANE + row * P + ((tid % PR) ^ piece_turn<KD>(row)) * 16) = v[q][i];
+                char *at = to + q * PLANE + row * P + ((tid % PR) ^ piece_turn<KD>(row)) * 16;
+                *reinterpret_cast<u32x4 *>(at) = v[q][i];
             }
         if constexpr (VOC) {
             if (tid < kNarrowStep) {
@@ -791,7 +793,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
     store(0);
     load(steps > 1 ? 1 : 0);
     __syncthreads();
-    for (int st = 0; st < steps; ++st) {
+    auto step = [&](int st) {
         const int buf = st & 1;
         const char *here = lds + buf * STAGE;
         store(buf ^ 1);
@@ -908,7 +910,8 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
                     for (int q = 0; q < PL; ++q) {
                         typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
                         const char *from = here + q * PLANE + 16 * u * P;
-                        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(from + (turned ^ (c << 6))));
+                        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (lds_s16x4)(from + (turned ^ (c << 6))));
                         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                             (lds_s16x4)(from + 8 * P + (turned ^ (c << 6) ^ 32)));
                         f[q] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -924,8 +927,9 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
                 }
         }
         __syncthreads();
-    }
+    };
     if constexpr (MODE == ROW_STATS) {
+        for (int st = 0; st < steps; ++st) step(st);
 #pragma unroll
         for (int b = 0; b < NO; ++b) {
             const int64_t i = own0 + b * 32 + (lane & 31);
@@ -935,18 +939,35 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
         }
     } else {
         const float by = PL == 2 && VOC ? ldexpf(unit, -(kUnitExp + *o.all_exp)) : unit;
+        for (int first = 0; first < steps; first += kNarrowChain) {
+            const int last = PL == 2 && steps - first > kNarrowChain ? first + kNarrowChain : steps;
 #pragma unroll
-        for (int b = 0; b < NO; ++b)
+            for (int b = 0; b < NO; ++b)
 #pragma unroll
-            for (int c = 0; c < CB; ++c)
+                for (int c = 0; c < CB; ++c)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t i = own0 + b * 32 + row_of(r);
-                    const int k = c * 32 + (lane & 31);
-                    if (i >= own.rows || k >= o.D) continue;
-                    if (VOC && o.splits == 1) static_cast<T *>(o.out)[i * o.ld_out + k] = (T)(acc[b][c][r] * by);
-                    else o.sum[(sp * own.rows + i) * o.D + k] = acc[b][c][r];
-                }
+                    for (int r = 0; r < 16; ++r) acc[b][c][r] = 0.f;
+            for (int st = first; st < last; ++st) step(st);
+#pragma unroll
+            for (int b = 0; b < NO; ++b)
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int64_t i = own0 + b * 32 + row_of(r);
+                        const int k = c * 32 + (lane & 31);
+                        if (i >= own.rows || k >= o.D) continue;
+                        if (VOC && o.splits == 1) {
+                            T *to = static_cast<T *>(o.out) + i * o.ld_out + k;
+                            const float x = acc[b][c][r] * by;
+                            *to = (T)(PL == 2 && first ? (float)*to + x : x);
+                        } else {
+                            float *to = o.sum + (sp * own.rows + i) * o.D + k;
+                            *to = PL == 2 && first ? *to + acc[b][c][r] : acc[b][c][r];
+                        }
+                    }
+            if (PL == 1) break; // all steps
+        }
     }
 }
 
@@ -1403,16 +1424,17 @@ struct XentPlan {
 };
 
 // Side of a product's tiles.  256 x 256 tiles read each operand least often
-// (logits of 8192 x 16384, bf16: K = 4096 at 1254 TFLOP/s, against 1040 in tiles
+// (logits of 8192 x 16384, bf16: K = 4096 at 1315 TFLOP/s, against 1139 in tiles
 // of 128).  Tiles of 128, of which a compute unit holds two, hide the start and
 // the end of one behind the products of the other and win where those are long
-// beside the sum (K = 512: 806 against 599; equal at 1024; sums and the weight's
-// gradient, whose ends are shorter, are equal at 512), and take outputs with a
-// side of at most 128 and grids that would leave compute units idle.
-constexpr int64_t kShortSum = 512, kShorterSum = 256;
-inline int64_t tile_side(int64_t M, int64_t N, int64_t K, int splits, bool of_logits)
+// beside the sum (bf16 logits, K = 512: 170 us against 182, equal at 1024; fp32,
+// whose sums are three products long, K = 256: 256 against 261, 460 against 432
+// at 512; the other products' ends are shorter), and take outputs with a side of
+// at most 128 and grids that would leave compute units idle.
+constexpr int64_t kShortSum = 256, kShortLogits = 512;
+inline int64_t tile_side(int64_t M, int64_t N, int64_t K, int splits, bool short_terms)
 {
-    if (M <= 128 || N <= 128 || K <= (of_logits ? kShortSum : kShorterSum)) return 128;
+    if (M <= 128 || N <= 128 || K <= (short_terms ? kShortLogits : kShortSum)) return 128;
     return ((M + 255) / 256) * ((N + 255) / 256) * splits < kCUs ? 128 : 256;
 }
 
@@ -1432,8 +1454,10 @@ int sum_splits(int64_t rows, int64_t D, int64_t K)
 inline int64_t d_rows(int64_t n) { return n <= 128 ? 128 : up(n, 256); }
 
 // Narrow kernels: 32-row blocks that a wave owns (as many as 256 registers hold;
-// a streamed fragment read from LDS serves all of them), and how often the streamed rows are split so that the blocks fill rounds of
-// two on each compute unit.
+// a streamed fragment read from LDS serves all of them; bf16 rows of 128 with
+// gradients: 3.3 ms with one, 4.2 with two, which spill), and how often the
+// streamed rows are split so that the blocks fill rounds of two on each compute
+// unit.
 constexpr int narrow_blocks(int PL, int mode, int64_t Kp)
 {
     return mode == ROW_STATS || (PL == 1 && Kp == 64) ? 2 : 1;
@@ -1527,7 +1551,7 @@ template <int PL, bool XT, bool YT, int OUT>
 int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const Output &o, hipStream_t s)
 {
     const int splits = OUT == OUT_SUM ? o.splits : 1;
-    const int64_t side = tile_side(M, N, K, splits, OUT == OUT_STATS || OUT == OUT_D);
+    const int64_t side = tile_side(M, N, K, splits, PL == 1 && (OUT == OUT_STATS || OUT == OUT_D));
     const int64_t mt = (M + side - 1) / side, nt = (N + side - 1) / side;
     const dim3 grid(tile_grid(mt, nt, splits));
     if (side == 256)
