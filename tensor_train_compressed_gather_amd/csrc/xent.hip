@@ -660,9 +660,9 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 //   VOC_GRAD   own: rows of the weight, streamed: hidden rows: dW.
 //
 // The logits are made three times instead of twice, and matrix instructions
-// bound it: 2048 fp32 rows of 128 against 10^6, 7.1 ms with both gradients, of
+// bound it: 2048 fp32 rows of 128 against 10^6, 6.9 ms with both gradients, of
 // which five sums of three products are 5.2 at the card's rate (10.7 by the
-// products above); bf16 2.9 ms, where the exponentials' vector instructions take
+// products above); bf16 2.7 ms, where the exponentials' vector instructions take
 // as long as the products.  fp16 terms: the hidden rows keep their own scales in
 // dW's product too, so there d_i carries the ratio to the largest row's scale,
 // at most 1.
@@ -689,7 +689,8 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
     constexpr int KB = KD / 16, CB = KD / 32, P = KD * 2, PLANE = kNarrowStep * P, STAGE = PL * PLANE;
     constexpr int PR = KD / 8, N = kNarrowStep * PR / 256;
     constexpr bool VOC = MODE == VOC_GRAD;
-    __shared__ __align__(256) char lds[2 * STAGE];
+    __shared__ __align__(256) char lds0[STAGE];
+    __shared__ __align__(256) char lds1[STAGE];
     __shared__ __align__(16) float of_row[2][3][kNarrowStep]; // VOC_GRAD: scale, lse and gradient of the streamed rows
     __shared__ __align__(16) int hit_row[2][kNarrowStep];     // and their targets in this block's rows
     const int64_t id = (int64_t)(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
@@ -735,52 +736,53 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
     }
     f32x16 acc[MODE == ROW_STATS ? 1 : NO][CB];
 
-    // streamed rows: memory to registers a step ahead, registers to one of two LDS buffers
-    const int64_t end = (str.rows - 1) * str.ld + str.cols;
-    const int off = ((tid / PR) * (int)str.ld + (tid % PR) * 8) * 2, apart = 256 / PR * (int)str.ld * 2;
-    u32x4 v[PL][N];
+    // streamed rows: straight to one of two LDS buffers a step ahead, a round of
+    // the loop being two steps (as for tiles); rows past this split's are zeros
+    const int64_t rows_end = (s0 + steps) * kNarrowStep < str.rows ? (s0 + steps) * kNarrowStep : str.rows;
+    const short *sp_next = str.p + s0 * kNarrowStep * str.ld;
+    const int ld = (int)str.ld;
+    int rows_left = (int)(rows_end - s0 * kNarrowStep); // of the steps not asked for yet
+    const int off = ((tid / PR) * ld + ((tid % PR) ^ piece_turn<KD>(tid / PR)) * 8) * 2, apart = 256 / PR * ld * 2;
+    const int to_lds = __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
     float4 c_row = make_float4(0.f, INFINITY, 0.f, 0.f);
     int c_hit = -1;
-    auto load = [&](int st) {
-        const int64_t row0 = (s0 + st) * kNarrowStep, skip = row0 * str.ld, left = (end - skip) * 2;
-        const unsigned bytes = left > 0x7fffffff ? 0x7fffffffu : left < 0 ? 0u : (unsigned)left;
+    int64_t c_next = s0 * kNarrowStep;
+    auto load = [&](char *to) {
+        const int have = rows_left < kNarrowStep ? rows_left : kNarrowStep;
+        const unsigned bytes = have > 0 ? (unsigned)((have - 1) * ld + KD) * 2 : 0;
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<short *>(str.p + q * str.plane + skip), 0, bytes, 0x00027000);
+                const_cast<short *>(sp_next + q * str.plane), 0, bytes, 0x00027000);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[q][i] = __builtin_amdgcn_raw_buffer_load_b128(r, off, i * apart, 0);
+            for (int i = 0; i < N; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void)(to + q * PLANE + i * 4096 + to_lds), 16, off,
+                                                         i * apart, 0, 0);
         }
-        if constexpr (VOC) {
-            if (tid < kNarrowStep) {
-                const int64_t i = row0 + tid;
-                c_row = make_float4(0.f, INFINITY, 0.f, 0.f);
-                c_hit = -1;
-                if (i < str.rows) {
-                    c_row = o.rows[i];
-                    const int64_t target = o.targets[i], t = target - block0;
-                    if (row_counts(target, o.ignore, o.V) && t >= 0 && t < 128 * NO) c_hit = (int)t;
-                }
-            }
-        }
+        sp_next += kNarrowStep * str.ld;
+        rows_left -= kNarrowStep;
     };
-    auto store = [&](int buf) {
-        char *to = lds + buf * STAGE;
-#pragma unroll
-        for (int q = 0; q < PL; ++q)
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int row = tid / PR + i * (256 / PR);
-                char *at = to + q * PLANE + row * P + ((tid % PR) ^ piece_turn<KD>(row)) * 16;
-                *reinterpret_cast<u32x4 *>(at) = v[q][i];
+    // what the weight's gradient needs of the streamed rows: registers a step
+    // ahead, then LDS
+    auto load_rows = [&]() {
+        if (VOC && tid < kNarrowStep) {
+            const int64_t i = c_next + tid;
+            c_row = make_float4(0.f, INFINITY, 0.f, 0.f);
+            c_hit = -1;
+            if (i < rows_end) {
+                c_row = o.rows[i];
+                const int64_t target = o.targets[i], t = target - block0;
+                if (row_counts(target, o.ignore, o.V) && t >= 0 && t < 128 * NO) c_hit = (int)t;
             }
-        if constexpr (VOC) {
-            if (tid < kNarrowStep) {
-                of_row[buf][0][tid] = c_row.x;
-                of_row[buf][1][tid] = c_row.y;
-                of_row[buf][2][tid] = c_row.z;
-                hit_row[buf][tid] = c_hit;
-            }
+        }
+        c_next += kNarrowStep;
+    };
+    auto store_rows = [&](int buf) {
+        if (VOC && tid < kNarrowStep) {
+            of_row[buf][0][tid] = c_row.x;
+            of_row[buf][1][tid] = c_row.y;
+            of_row[buf][2][tid] = c_row.z;
+            hit_row[buf][tid] = c_hit;
         }
     };
     auto row_of = [&](int r) { return 8 * (r / 4) + 4 * half + r % 4; };
@@ -789,15 +791,17 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
     const int turned = (4 * half + four) * P + (((KD == 128 ? four : four >> 1) << 2 | (piece ^ half)) << 4) +
                        (lane & 1) * 8;
 
-    load(0);
-    store(0);
-    load(steps > 1 ? 1 : 0);
-    __syncthreads();
-    auto step = [&](int st) {
-        const int buf = st & 1;
-        const char *here = lds + buf * STAGE;
-        store(buf ^ 1);
-        load(st + 2 < steps ? st + 2 : steps - 1);
+    load_rows();
+    store_rows(0);
+    load_rows();
+    load(lds0);
+    loads_meet<0>();
+    auto step = [&](int st, auto which) {
+        constexpr int buf = decltype(which)::value;
+        char *here = buf ? lds1 : lds0;
+        load(buf ? lds0 : lds1); // (behind the barrier that ends its last reads)
+        store_rows(buf ^ 1);
+        load_rows();
         f32x16 z[NO];
 #pragma unroll
         for (int b = 0; b < NO; ++b)
@@ -818,7 +822,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
 #pragma unroll
             for (int b = 0; b < NO; ++b) z[b] = Terms<PL>::mma(f[0], of[0][b][k], z[b]);
         }
-        const int64_t left = str.rows - (s0 + st) * kNarrowStep; // streamed rows that exist
+        const int left = (int)(rows_end - s0 * kNarrowStep) - st * kNarrowStep; // streamed rows that exist
         if constexpr (MODE == ROW_STATS) {
 #pragma unroll
             for (int b = 0; b < NO; ++b) {
@@ -926,10 +930,18 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
                     for (int b = 0; b < NO; ++b) acc[b][c] = Terms<PL>::mma(d[0][b][u], f[0], acc[b][c]);
                 }
         }
-        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        loads_meet<0>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto run = [&](int first, int last) { // an odd number of steps ends with one of no rows
+        for (int st = first; st < last; st += 2) {
+            step(st, std::integral_constant<int, 0>());
+            step(st + 1, std::integral_constant<int, 1>());
+        }
     };
     if constexpr (MODE == ROW_STATS) {
-        for (int st = 0; st < steps; ++st) step(st);
+        run(0, steps);
 #pragma unroll
         for (int b = 0; b < NO; ++b) {
             const int64_t i = own0 + b * 32 + (lane & 31);
@@ -947,7 +959,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
                 for (int c = 0; c < CB; ++c)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[b][c][r] = 0.f;
-            for (int st = first; st < last; ++st) step(st);
+            run(first, last);
 #pragma unroll
             for (int b = 0; b < NO; ++b)
 #pragma unroll
