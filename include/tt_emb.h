@@ -435,14 +435,15 @@ int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weigh
  * (0 for ignored rows whatever it holds):
  *   d_iv = grad_loss_i (exp(z_iv - lse_i) - [v = target_i])
  *   grad_hidden_i = sum_v d_iv weight_v,  grad_weight_v = sum_i d_iv hidden_i
- * both of `dtype`, overwritten.  The vocabulary is taken in pieces whose d
- * (bf16 for bf16 inputs; two fp16 terms, 22 bits, for fp32 inputs, whose
- * own values are scaled by powers of two and split the same way) is in ws;
- * sums are fp32.  fp32 inputs: a value of the weight keeps 22 bits or an
- * absolute 2^-39 of the weight's largest, whichever is more.  An ignored row's hidden values do not reach the gradients,
- * whatever they hold.  A larger ws allows larger pieces: any
- * ws_bytes from *least of tt_emb_xent_workspace_size on is accepted, *bytes
- * is the size past which nothing is gained. */
+ * both of `dtype`, overwritten.  The vocabulary is taken in pieces whose d is in
+ * ws (D <= 128: d is not kept at all): bf16 for bf16 inputs, two fp16 terms, 22
+ * bits, for fp32 inputs, whose own values are scaled by powers of two and split
+ * the same way; sums are fp32.  fp32 inputs: a value of the weight keeps 22 bits
+ * or an absolute 2^-39 of the weight's largest, whichever is more.  An ignored
+ * row's hidden values do not reach the gradients, whatever they hold.  A larger
+ * ws allows larger pieces: any ws_bytes from *least of
+ * tt_emb_xent_workspace_size on is accepted, *bytes is the size past which
+ * nothing is gained. */
 int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *weight, int64_t ld_weight,
                           const int64_t *targets, const float *grad_loss, int64_t n, int64_t V, int64_t D,
                           int32_t dtype, int64_t ignore_index, float *loss, float *lse, void *grad_hidden,
