@@ -478,18 +478,20 @@ class AdamW:
         n = len(self.params)
         if len(grads) != n:
             raise _bad(where, f"{len(grads)} gradients for {n} parameters")
-        if not all(isinstance(g, torch.Tensor) for g in grads):
-            raise _bad(where, "grads: expected torch tensors")
-        first = grads[0].dtype
+        tensor, index = torch.Tensor, self.device.index
+        first = getattr(grads[0], "dtype", None)
         for i, (g, shape) in enumerate(zip(grads, self._shapes)):
-            if g.dtype is not first or g.shape != shape or not g.is_contiguous() or g.device != self.device:
+            if not isinstance(g, tensor):
+                raise _bad(where, "grads: expected torch tensors")
+            if g.dtype is not first or g.shape != shape or not g.is_contiguous() or g.get_device() != index:
                 self._tensor(g, f"grads[{i}]", first, shape, self.device)
         dt = _dtype(grads[0], where, "grads[0]")
         # parameters may have been replaced (param.data = ...): their addresses are read anew
         array = C.c_void_p * n
-        params = array(*[p.data_ptr() for p in self.params])
-        pointers = array(*[g.data_ptr() for g in grads])
-        copies = None if self.copies is None else array(*[c.data_ptr() for c in self.copies])
+        address = tensor.data_ptr
+        params = array(*map(address, self.params))
+        pointers = array(*map(address, grads))
+        copies = None if self.copies is None else array(*map(address, self.copies))
         guard = _guard(self.device, stream, where)
         if guard is not None:
             with guard:
