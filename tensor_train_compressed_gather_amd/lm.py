@@ -207,7 +207,7 @@ class TokenEmbedding(_Operator):
         s = _raw_stream(device.index)
         made = out is None
         if made:
-            out, ld_o = torch.empty((n, self.D), dtype=weight.dtype, device=device), self.D
+            out, ld_o = weight.new_empty((n, self.D)), self.D
         else:
             ld_o = _matrix(out, where, "out", self.D, n, weight.dtype, device)
         ws = self._workspace(device, s, TT_EMB_STATUS_BYTES)
@@ -279,11 +279,11 @@ class LayerNorm(_Operator):
                 return self.forward(x, gamma, beta, out)
         s = _raw_stream(device.index)
         if out is None:
-            out, ld_y = torch.empty((n, self.D), dtype=x.dtype, device=device), self.D
+            out, ld_y = x.new_empty((n, self.D)), self.D
         else:
             ld_y = _matrix(out, where, "out", self.D, n, x.dtype, device)
-        stats = torch.empty((2, n), dtype=torch.float32, device=device)
-        mean, rstd = stats.unbind(0)
+        mean = torch.empty(n, dtype=torch.float32, device=device)
+        rstd = torch.empty(n, dtype=torch.float32, device=device)
         _check(_L.tt_emb_norm_forward(x.data_ptr(), ld_x, n, self.D, dt,
                                     None if gamma is None else gamma.data_ptr(),
                                     None if beta is None else beta.data_ptr(), pdt, self.eps, out.data_ptr(),
@@ -306,9 +306,10 @@ class LayerNorm(_Operator):
             with guard:
                 return self.backward(grad_y, x, gamma, mean, rstd)
         s = _raw_stream(device.index)
-        dx = torch.empty((n, self.D), dtype=x.dtype, device=device)
-        sums = torch.empty((2, self.D), dtype=torch.float32 if gamma is None else gamma.dtype, device=device)
-        dgamma, dbeta = sums.unbind(0)
+        dx = x.new_empty((n, self.D))
+        kind = torch.float32 if gamma is None else gamma.dtype
+        dgamma = torch.empty(self.D, dtype=kind, device=device)
+        dbeta = torch.empty(self.D, dtype=kind, device=device)
         ws = self._workspace(device, s, need)
         _check(_L.tt_emb_norm_backward(grad_y.data_ptr(), ld_g, x.data_ptr(), ld_x, n, self.D, dt,
                                      None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(),
@@ -361,7 +362,8 @@ class VocabCrossEntropy(_Operator):
             with guard:
                 return self.forward(hidden, weight, targets)
         s = _raw_stream(device.index)
-        loss, lse = torch.empty((2, n), dtype=torch.float32, device=device).unbind(0)
+        loss = torch.empty(n, dtype=torch.float32, device=device)
+        lse = torch.empty(n, dtype=torch.float32, device=device)
         ws = self._workspace(device, s, need)
         _check(_L.tt_emb_xent_forward(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(), n,
                                     self.V, self.D, dt, self.ignore_index, loss.data_ptr(),
@@ -378,7 +380,8 @@ class VocabCrossEntropy(_Operator):
             with guard:
                 return self.loss_and_grad(hidden, weight, targets, grad_loss, grad_weight)
         s = _raw_stream(device.index)
-        loss, lse = torch.empty((2, n), dtype=torch.float32, device=device).unbind(0)
+        loss = torch.empty(n, dtype=torch.float32, device=device)
+        lse = torch.empty(n, dtype=torch.float32, device=device)
         dh = torch.empty((n, self.D), dtype=hidden.dtype, device=device)
         if grad_weight is None:
             grad_weight = torch.empty((self.V, self.D), dtype=hidden.dtype, device=device)
