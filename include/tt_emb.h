@@ -456,6 +456,21 @@ int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *wei
 int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t with_grad, size_t *bytes,
                                size_t *least);
 
+/* How tt_emb_xent_loss_grad sums grad_hidden over the vocabulary with a
+ * workspace of ws_bytes: in parts, each of the weight's rows [begin, end),
+ * that go to `slot` of several partial sums, overwriting it (first != 0) or
+ * adding to it; at the end slots 0 .. *slots - 1 are added up.  Writes the
+ * first `cap` parts in the order they are taken and their number to *count.
+ * The launches use the same functions; host only, no device work.  Sizes are
+ * refused as by tt_emb_xent_workspace_size, n = 0 with TT_EMB_ERR_ARG, less
+ * than *least bytes with TT_EMB_ERR_WORKSPACE. */
+typedef struct tt_emb_xent_part {
+    int64_t begin, end;
+    int32_t slot, first;
+} tt_emb_xent_part;
+int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, size_t ws_bytes, tt_emb_xent_part *parts,
+                      int64_t cap, int64_t *count, int32_t *slots);
+
 /* One AdamW step (decoupled weight decay) over `count` fp32 tensors:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr mhat / (sqrt(vhat) + eps)

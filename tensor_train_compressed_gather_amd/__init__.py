@@ -14,7 +14,8 @@ import os
 import threading
 
 from . import lm as _lm
-from .lm import LM_EXPORTED, AdamW, LayerNorm, TokenEmbedding, VocabCrossEntropy  # noqa: F401
+from .lm import (LM_EXPORTED, AdamW, LayerNorm, TokenEmbedding, VocabCrossEntropy,  # noqa: F401
+                 tt_emb_xent_parts)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # TT_EMB_LIB names another build of the same library (the host-sanitizer build

@@ -208,6 +208,19 @@ int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, i
     return TT_EMB_OK;
 }
 
+int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, size_t ws_bytes, tt_emb_xent_part *parts,
+                      int64_t cap, int64_t *count, int32_t *slots)
+{
+    const int rc = check_xent(n, V, D, dtype);
+    if (rc) return rc;
+    if (n == 0 || cap < 0 || (cap > 0 && !parts) || !count || !slots) return TT_EMB_ERR_ARG;
+    size_t least = 0;
+    xent_workspace(n, V, D, dtype, true, nullptr, &least);
+    if (ws_bytes < least) return TT_EMB_ERR_WORKSPACE;
+    *count = xent_parts(n, V, D, dtype, ws_bytes, parts, cap, slots);
+    return TT_EMB_OK;
+}
+
 int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weight, int64_t ld_weight,
                         const int64_t *targets, int64_t n, int64_t V, int64_t D, int32_t dtype,
                         int64_t ignore_index, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream)

@@ -173,8 +173,8 @@ struct TileLoader {
         p = a.p + (TURNED ? r0 : r0 * a.ld);
         next = TURNED ? BK * a.ld : BK;
         if constexpr (TURNED) {
-            const int64_t full = a.rows / BK;
-            const int cols = (int)(a.cols - r0 < R ? a.cols - r0 : R), left = (int)(a.rows - full * BK);
+            const int64_t have = a.rows > 0 ? a.rows : 0, full = have / BK; // (a part that begins past the rows has none)
+            const int cols = (int)(a.cols - r0 < R ? a.cols - r0 : R), left = (int)(have - full * BK);
             whole = cols > 0 ? (int)(full < stages ? full : stages) : 0;
             bytes = (unsigned)((BK - 1) * ld + cols) * 2;
             rest = full < stages && left && cols > 0 ? (unsigned)((left - 1) * ld + cols) * 2 : 0;
@@ -1462,6 +1462,18 @@ int sum_splits(int64_t rows, int64_t D, int64_t K)
     return (int)(s < 1 ? 1 : s);
 }
 
+// A sum over K values in at most `most` parts of `each` values (whole steps);
+// every part begins before K's end.
+struct SumParts {
+    int64_t each;
+    int parts;
+};
+inline SumParts sum_parts(int64_t K, int most)
+{
+    const int64_t each = up((K + most - 1) / most, kPadK);
+    return {each, (int)((K + each - 1) / each)};
+}
+
 // Rows of d: whole tiles, so that they are written without a test.
 inline int64_t d_rows(int64_t n) { return n <= 128 ? 128 : up(n, 256); }
 
@@ -1545,6 +1557,15 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     return p;
 }
 
+// The plan whose pieces fit the workspace.
+XentPlan fit_xent(int64_t n, int64_t V, int64_t D, int PL, bool grad, char *base, size_t ws_bytes)
+{
+    int64_t piece = grad ? best_piece(n, V, D, PL) : 0;
+    while (piece < -1 && plan_xent(n, V, D, PL, piece, nullptr).bytes > ws_bytes) piece = -whole_splits(V, -piece / 2);
+    while (piece > kRound && plan_xent(n, V, D, PL, piece, nullptr).bytes > ws_bytes) piece = up(piece / 2, kRound);
+    return plan_xent(n, V, D, PL, piece, base);
+}
+
 template <class T, int PL>
 bool in_place(const T *src, int64_t ld, int64_t D, int64_t Kp)
 {
@@ -1622,12 +1643,8 @@ template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
     const bool narrow_all = narrow_rows(a.n, a.V, a.D);
-    int64_t piece = grad ? best_piece(a.n, a.V, a.D, PL) : 0;
-    while (piece < -1 && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
-        piece = -whole_splits(a.V, -piece / 2);
-    while (piece > kRound && plan_xent(a.n, a.V, a.D, PL, piece, nullptr).bytes > a.ws_bytes)
-        piece = up(piece / 2, kRound);
-    const XentPlan p = plan_xent(a.n, a.V, a.D, PL, piece, a.ws);
+    const XentPlan p = fit_xent(a.n, a.V, a.D, PL, grad, a.ws, a.ws_bytes);
+    const int64_t piece = p.piece;
     Output o{};
     o.n = a.n;
     o.V = a.V;
@@ -1732,9 +1749,10 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
         o.sum = p.sum;
         o.sum_rows = a.n;
-        o.splits = p.splits;
-        o.split_k = up((cols + p.splits - 1) / p.splits, kPadK);
-        product<PL, true, false, OUT_SUM>(wp, d, a.D, a.n, cols, o, s);
+        const SumParts over_v = sum_parts(here, p.splits);
+        o.splits = over_v.parts;
+        o.split_k = over_v.each;
+        product<PL, true, false, OUT_SUM>(wp, d, a.D, a.n, up(here, kPadK), o, s);
         const int64_t rows = up(a.n, kPadK);
         if (p.w_splits == 1) {
             o.out = a.dw;
@@ -1744,17 +1762,14 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         }
         o.sum = p.w_sum;
         o.sum_rows = a.V;
-        o.splits = p.w_splits;
-        o.split_k = up((rows + p.w_splits - 1) / p.w_splits, kPadK);
+        const SumParts over_n = sum_parts(a.n, p.w_splits);
+        o.splits = over_n.parts;
+        o.split_k = over_n.each;
         product<PL, true, true, OUT_SUM>(h_all, d, a.D, a.V, rows, o, s);
-        sum_up<T>(p.w_sum, (int)((rows + o.split_k - 1) / o.split_k), a.V, a.D, p.top_grad,
-                  PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
+        sum_up<T>(p.w_sum, over_n.parts, a.V, a.D, p.top_grad, PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
     }
-    // splits past the first piece's end have written nothing
-    const int64_t first = up(a.V < piece ? a.V : piece, kRound);
-    const int64_t per = up((first + p.splits - 1) / p.splits, kPadK);
-    sum_up<T>(p.sum, (int)((first + per - 1) / per), a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr, a.dh,
-              a.ld_dh, s);
+    sum_up<T>(p.sum, sum_parts(a.V < piece ? a.V : piece, p.splits).parts, a.n, a.D, p.top_grad,
+              PL == 2 ? p.w_exp : nullptr, a.dh, a.ld_dh, s);
     return hipGetLastError();
 }
 
@@ -1767,6 +1782,36 @@ void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_
     const int64_t most = grad ? best_piece(n, V, D, PL) : 0;
     if (best) *best = plan_xent(n, V, D, PL, most, nullptr).bytes;
     if (least) *least = plan_xent(n, V, D, PL, most < 0 ? -1 : most > 0 ? kRound : 0, nullptr).bytes;
+}
+
+int64_t xent_parts(int64_t n, int64_t V, int64_t D, int dtype, size_t ws_bytes, tt_emb_xent_part *parts, int64_t cap,
+                   int32_t *slots)
+{
+    const XentPlan p = fit_xent(n, V, D, dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1, true, nullptr, ws_bytes);
+    int64_t count = 0;
+    auto add = [&](int64_t begin, int64_t end, int slot, bool first) {
+        if (count < cap) parts[count] = tt_emb_xent_part{begin, end, slot, first};
+        ++count;
+    };
+    if (p.piece < 0) { // narrow rows: whole steps of the streamed vocabulary
+        const int64_t steps = (V + kNarrowStep - 1) / kNarrowStep, per = (steps + p.splits - 1) / p.splits;
+        for (int q = 0; q < p.splits; ++q) {
+            const int64_t end = (q + 1) * per * kNarrowStep;
+            add(q * per * kNarrowStep, end < V ? end : V, q, true);
+        }
+        *slots = p.splits;
+        return count;
+    }
+    for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
+        const int64_t here = V - v0 < p.piece ? V - v0 : p.piece;
+        const SumParts over_v = sum_parts(here, p.splits);
+        for (int q = 0; q < over_v.parts; ++q) {
+            const int64_t end = (q + 1) * over_v.each;
+            add(v0 + q * over_v.each, v0 + (end < here ? end : here), q, v0 == 0);
+        }
+    }
+    *slots = sum_parts(V < p.piece ? V : p.piece, p.splits).parts;
+    return count;
 }
 
 hipError_t launch_xent_forward(const XentArgs &a, int dtype, hipStream_t s)

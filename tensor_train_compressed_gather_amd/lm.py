@@ -19,7 +19,7 @@ LM_EXPORTED = (
     "tt_emb_poll_status",
     "tt_emb_lookup_forward", "tt_emb_lookup_backward", "tt_emb_lookup_workspace_size",
     "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_norm_workspace_size",
-    "tt_emb_xent_forward", "tt_emb_xent_loss_grad", "tt_emb_xent_workspace_size",
+    "tt_emb_xent_forward", "tt_emb_xent_loss_grad", "tt_emb_xent_workspace_size", "tt_emb_xent_parts",
     "tt_emb_adamw_update", "tt_emb_adamw_state_size",
 )
 
@@ -40,6 +40,7 @@ def declare(L):
     L.tt_emb_xent_loss_grad.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i32, i64, p, p, p, i64, p, i64, p, size,
                                         p]
     L.tt_emb_xent_workspace_size.argtypes = [i64, i64, i64, i32, i32, sizes, sizes]
+    L.tt_emb_xent_parts.argtypes = [i64, i64, i64, i32, size, p, i64, C.POINTER(i64), C.POINTER(i32)]
     L.tt_emb_adamw_update.argtypes = [i32, p, p, i32, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64, p]
     L.tt_emb_adamw_state_size.argtypes = [i32, p, C.POINTER(i64)]
 
@@ -316,6 +317,24 @@ class LayerNorm(_Operator):
                                      rstd.data_ptr(), dx.data_ptr(), self.D, dgamma.data_ptr(),
                                      dbeta.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
         return dx, dgamma, dbeta
+
+
+class tt_emb_xent_part(C.Structure):
+    _fields_ = [("begin", C.c_int64), ("end", C.c_int64), ("slot", C.c_int32), ("first", C.c_int32)]
+
+
+def tt_emb_xent_parts(n: int, V: int, D: int, dtype: int, ws_bytes: int):
+    """The parts (begin, end, slot, first) of the vocabulary that
+    loss_and_grad sums the hidden rows' gradient over, in order, and how many
+    slots it adds up in the end (host-side; the launches use the same
+    functions)."""
+    _bind()
+    count, slots = C.c_int64(), C.c_int32()
+    args = (int(n), int(V), int(D), int(dtype), int(ws_bytes))
+    _check(_L.tt_emb_xent_parts(*args, None, 0, C.byref(count), C.byref(slots)), "tt_emb_xent_parts")
+    parts = (tt_emb_xent_part * count.value)()
+    _check(_L.tt_emb_xent_parts(*args, parts, count.value, C.byref(count), C.byref(slots)), "tt_emb_xent_parts")
+    return [(q.begin, q.end, q.slot, q.first) for q in parts], int(slots.value)
 
 
 class VocabCrossEntropy(_Operator):
