@@ -1432,6 +1432,7 @@ struct XentPlan {
     short *d;
     int64_t Kp, nr, piece;
     int splits, w_splits; // of the sums over the vocabulary (dH) and over the rows (dW)
+    int parts;            // of dH's splits, those that the first piece fills: later pieces add to these only
     size_t bytes;
 };
 
@@ -1548,6 +1549,7 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     } else if (piece) {
         if (PL == 2) p.h_all = (short *)take((size_t)PL * n * p.Kp * 2);
         p.splits = sum_splits(n, D, piece);
+        p.parts = sum_parts(V < piece ? V : piece, p.splits).parts;
         p.sum = (float *)take(4 * (size_t)p.splits * n * D);
         p.w_splits = piece >= V ? sum_splits(V, D, n) : 1;
         if (p.w_splits > 1) p.w_sum = (float *)take(4 * (size_t)p.w_splits * V * D);
@@ -1749,7 +1751,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         const Operand d{p.d, piece, p.nr * piece, p.nr, cols};
         o.sum = p.sum;
         o.sum_rows = a.n;
-        const SumParts over_v = sum_parts(here, p.splits);
+        const SumParts over_v = sum_parts(here, p.parts);
         o.splits = over_v.parts;
         o.split_k = over_v.each;
         product<PL, true, false, OUT_SUM>(wp, d, a.D, a.n, up(here, kPadK), o, s);
@@ -1768,8 +1770,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         product<PL, true, true, OUT_SUM>(h_all, d, a.D, a.V, rows, o, s);
         sum_up<T>(p.w_sum, over_n.parts, a.V, a.D, p.top_grad, PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
     }
-    sum_up<T>(p.sum, sum_parts(a.V < piece ? a.V : piece, p.splits).parts, a.n, a.D, p.top_grad,
-              PL == 2 ? p.w_exp : nullptr, a.dh, a.ld_dh, s);
+    sum_up<T>(p.sum, p.parts, a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr, a.dh, a.ld_dh, s);
     return hipGetLastError();
 }
 
@@ -1804,13 +1805,13 @@ int64_t xent_parts(int64_t n, int64_t V, int64_t D, int dtype, size_t ws_bytes, 
     }
     for (int64_t v0 = 0; v0 < V; v0 += p.piece) {
         const int64_t here = V - v0 < p.piece ? V - v0 : p.piece;
-        const SumParts over_v = sum_parts(here, p.splits);
+        const SumParts over_v = sum_parts(here, p.parts);
         for (int q = 0; q < over_v.parts; ++q) {
             const int64_t end = (q + 1) * over_v.each;
             add(v0 + q * over_v.each, v0 + (end < here ? end : here), q, v0 == 0);
         }
     }
-    *slots = sum_parts(V < p.piece ? V : p.piece, p.splits).parts;
+    *slots = p.parts;
     return count;
 }
 
