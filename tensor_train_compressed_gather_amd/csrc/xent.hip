@@ -554,14 +554,14 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         for (int j = 0; j < NJ; ++j) {
             keep_columns(acc, j);
             const int64_t i = n0 + wn * (TN / 2) + j * 32 + (lane & 31);
-            // rows that do not count, or lie past the last: d = 0 (exp - 0)
+            // rows that do not count (packed as zeros), or lie past the last: d = 0 (exp - 0)
             float lse = 0.f, g = 0.f, scale = 1.f;
             int64_t t = -1;
             if (OUT == OUT_D && i < o.n) {
                 const int64_t target = o.targets[i];
                 lse = o.lse[i];
-                if constexpr (PL == 2) scale = ldexpf(1.f, -(o.h_exp[i] + *o.w_exp));
                 if (row_counts(target, o.ignore, o.V)) {
+                    if constexpr (PL == 2) scale = ldexpf(1.f, -(o.h_exp[i] + *o.w_exp));
                     t = target - o.v0 - m0;
                     g = o.grad[i] / unit * (PL == 2 ? (float)(1 << kUnitExp) : 1.f);
                 } else {
@@ -724,6 +724,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
             if constexpr (PL == 2) scale[b] = ldexpf(1.f, -(o.h_exp[ic] + *o.w_exp));
             if constexpr (MODE == ROW_GRAD) {
                 const bool counts = i < own.rows && row_counts(target, o.ignore, o.V);
+                if (!counts) scale[b] = 1.f;
                 lse[b] = counts ? o.lse[ic] : INFINITY;
                 g[b] = counts ? o.grad[ic] / unit * (PL == 2 ? (float)(1 << kUnitExp) : 1.f) : 0.f;
                 takes = takes && counts;
@@ -1166,10 +1167,8 @@ __global__ __launch_bounds__(F::threads) void k_jobs(F f)
 }
 
 // Hidden rows as planes with `ld` columns, zero past D; a wave per row.  fp16
-// terms: each row scaled by a power of two of its own, and the largest
-// magnitude of each row that counts left in `tops`.  With targets: a row that
-// is ignored and holds a value that is not finite is taken as zeros, so that
-// its zero gradient stays zero.
+// terms: each row scaled by a power of two of its own, and with targets the
+// largest magnitude of each row that counts left in `tops`.
 template <class T, int PL>
 struct PackRows {
     static constexpr int threads = 256;
@@ -1188,31 +1187,50 @@ struct PackRows {
         for (int64_t r = (int64_t)block * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)blocks * 4) {
             const T *row = src + r * ld_src;
             int e = 0;
-            bool clear = false;
-            if (PL == 2 || targets) {
+            if constexpr (PL == 2) {
                 float top = 0.f;
-                bool odd = false;
                 for (int64_t k = lane * 8; k < D; k += 512) {
                     float x[8];
                     load_part<T, 8>(row + k, (int)(D - k < 8 ? D - k : 8), x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        top = fmaxf(top, finite_abs(x[i]));
-                        odd = odd || !(fabsf(x[i]) < INFINITY);
-                    }
+                    for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(x[i]));
                 }
 #pragma unroll
                 for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-                if (targets) {
-                    const bool counts = row_counts(targets[r], ignore, V);
-                    clear = __any(odd) && !counts;
-                    if (PL == 2 && lane == 0) tops[r] = counts ? top : 0.f;
+                e = scale_exp(top);
+                if (lane == 0) {
+                    exps[r] = e;
+                    if (targets) tops[r] = row_counts(targets[r], ignore, V) ? top : 0.f;
                 }
-                e = PL == 2 && !clear ? scale_exp(top) : 0;
-                if (PL == 2 && lane == 0) exps[r] = e;
             }
             for (int64_t k = lane * 8; k < ld; k += 512)
-                pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, clear, dst + r * ld + k, plane);
+                pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
+        }
+    }
+};
+
+// Packed rows that do not count become zeros once their statistics are known:
+// whatever they held (NaN, or a finite value whose logits overflow), their
+// logits are then 0, d is 0 and so is what they add to the weight's gradient.
+// A wave per row.
+template <int PL>
+struct ClearRows {
+    static constexpr int threads = 1024;
+    short *dst;
+    int64_t ld, plane, rows;
+    const int64_t *targets;
+    int64_t ignore, V;
+
+    __device__ void operator()(int block, int blocks) const
+    {
+        const int lane = threadIdx.x & 63;
+        for (int64_t r = (int64_t)block * 16 + (threadIdx.x >> 6); r < rows; r += (int64_t)blocks * 16) {
+            if (row_counts(targets[r], ignore, V)) continue;
+            const s16x8 none = {};
+#pragma unroll
+            for (int q = 0; q < PL; ++q)
+                for (int64_t k = lane * 8; k < ld; k += 512)
+                    *reinterpret_cast<s16x8 *>(dst + q * plane + r * ld + k) = none;
         }
     }
 };
@@ -1403,8 +1421,9 @@ struct Join {
         lse[i] = z;
         loss[i] = in && t != ignore ? z - target_logit[i] : 0.f;
         if (!rows) return;
-        float4 c = make_float4(h_exp ? ldexpf(1.f, -(h_exp[i] + *w_exp)) : 1.f, INFINITY, 0.f, 0.f);
+        float4 c = make_float4(1.f, INFINITY, 0.f, 0.f);
         if (in && t != ignore) {
+            if (h_exp) c.x = ldexpf(1.f, -(h_exp[i] + *w_exp));
             c.y = z;
             c.z = grad[i] / *unit;
             // (a row of zeros has a scale of its own, and no part in the sum)
@@ -1713,17 +1732,24 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         }
     }
     const int join_blocks = (int)((a.n + 15) / 16);
+    if (!grad) {
+        run_jobs(join_job, join_blocks, NoJobOf<1024>(), 0, s);
+        return hipGetLastError();
+    }
+    const ClearRows<PL> clear_job{p.h, p.Kp, a.n * p.Kp, a.n, a.targets, a.ignore, a.V};
+    typedef Both<Join, ClearRows<PL>> Stats;
+    const Stats stats_job{join_job, clear_job, join_blocks};
+    const int stats_blocks = join_blocks + (join_blocks < 1024 ? join_blocks : 1024);
     Operand h_all = h;
     if constexpr (PL == 2) {
         h_all.p = p.h_all;
         const PackCounting count_job{hs, a.ld_h, a.n, a.D, p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.targets, a.ignore,
                                      a.V};
-        run_jobs(join_job, join_blocks, count_job,
+        run_jobs(stats_job, stats_blocks, count_job,
                  piece > 0 ? (int)((blocks_for(a.n * (p.Kp / 8)) + 3) / 4) : 0, s);
     } else {
-        run_jobs(join_job, join_blocks, NoJobOf<1024>(), 0, s);
+        run_jobs(stats_job, stats_blocks, NoJobOf<1024>(), 0, s);
     }
-    if (!grad) return hipGetLastError();
     if (piece < 0) {
         o.rows = p.rows;
         o.sum = p.sum;
