@@ -47,13 +47,13 @@ def declare(L):
 
 torch = None       # imported with the first operator: the package itself does without
 _L = _check = None  # the loaded library, the status check
-_raw_stream = None
+_raw_stream = _capturing = None
 _DTYPES = {}
 
 
 def _bind():
     """Import torch, load the library (once)."""
-    global torch, _L, _check, _raw_stream
+    global torch, _L, _check, _raw_stream, _capturing
     if _L is None:
         import torch as t
 
@@ -64,6 +64,8 @@ def _bind():
         # the current stream's handle without a Stream object around it
         _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: t.cuda.current_stream(index).cuda_stream)
+        # whether the current stream is being captured into a graph
+        _capturing = getattr(t._C, "_cuda_isCurrentStreamCapturing", None) or t.cuda.is_current_stream_capturing
         _L = lib()
 
 
@@ -135,32 +137,51 @@ def _guard(device, stream, where: str):
 
 class _Operator:
     """What the operators with a workspace share: one growing buffer per
-    (device, stream), whose status words are zero from the start."""
+    (device, stream), whose status words are zero from the start.
+
+    A buffer that a captured graph writes to is kept for as long as the
+    operator, also when a later call needs a larger one: keep the operator as
+    long as the graph.  Make one ordinary call on the stream before the
+    capture; a buffer that is first made inside a capture has its status
+    cleared by each replay."""
 
     def __init__(self, device):
         _bind()
         self.device = torch.device(device)
         self._ws = {}
+        self._in_graph = set()  # keys whose present buffer a graph writes to
+        self._kept = []         # (key, buffer) that graphs write to and no other call any more
 
     def _workspace(self, device, handle: int, need: int):
         key = (device.index, handle)
         ws = self._ws.get(key)
+        capturing = _capturing()
         if ws is None or ws.numel() < need:
             new = torch.empty(need, dtype=torch.uint8, device=device)
+            if ws is not None and (capturing or key in self._in_graph):
+                # recorded copies and kernels would meet freed memory
+                self._kept.append((key, ws))
+                self._in_graph.discard(key)
+                ws = None
             # the status of earlier calls stays readable
             if ws is None:
                 new[:TT_EMB_STATUS_BYTES].zero_()
             else:
                 new[:TT_EMB_STATUS_BYTES].copy_(ws[:TT_EMB_STATUS_BYTES])
             self._ws[key] = ws = new
+        if capturing:
+            self._in_graph.add(key)
         return ws
 
     def poll_error(self) -> int:
         """Synchronises; the first device-detected error of any stream's
         calls since the last poll (0 = ok), cleared by reading it."""
         rc = 0
-        for (index, handle), ws in self._ws.items():
+        for key, ws in [*self._kept, *self._ws.items()]:
+            index, handle = key
             with torch.cuda.device(index):
+                if key in self._in_graph or self._ws[key] is not ws:
+                    torch.cuda.synchronize()  # a graph is replayed on any stream
                 got = int(_L.tt_emb_poll_status(ws.data_ptr(), handle))
             rc = rc or got
         return rc
