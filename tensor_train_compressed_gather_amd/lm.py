@@ -468,6 +468,7 @@ class AdamW:
         self.lr, self.betas, self.eps, self.weight_decay = float(lr), tuple(betas), float(eps), float(weight_decay)
         self.state_bits, self.seed, self.steps, self.device = int(state_bits), int(seed), 0, device
         n = len(self.params)
+        self._array = C.c_void_p * n
         self._numel = (C.c_int64 * n)(*[p.numel() for p in self.params])
         self._shapes = [p.shape for p in self.params]
         total = C.c_int64()
@@ -495,6 +496,20 @@ class AdamW:
             raise _bad(where, f"{name}: not contiguous")
         _on(t, where, name, device)
 
+    def _whole(self, tensors, name, dtype):
+        """Check that the kernel can take these for the parameters' elements."""
+        tensor, index = torch.Tensor, self.device.index
+        if len(tensors) != len(self._shapes):
+            raise _bad("AdamW", f"{len(tensors)} {name} for {len(self._shapes)} parameters")
+        for t, shape in zip(tensors, self._shapes):
+            if (not isinstance(t, tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                    or t.get_device() != index):
+                break
+        else:
+            return
+        for i, (t, shape) in enumerate(zip(tensors, self._shapes)):
+            self._tensor(t, f"{name}[{i}]", dtype, shape, self.device)
+
     def load_state(self, exp_avg, exp_avg_sq, steps: int, exp_avg_scale=None, exp_avg_sq_scale=None):
         """Copies of a saved state: the moments (and scales) as this class
         keeps them, and the number of steps taken."""
@@ -518,20 +533,17 @@ class AdamW:
         type: fp32, bf16 or fp16)."""
         where = "AdamW.step"
         grads = list(grads)
-        n = len(self.params)
+        n = len(self._shapes)
         if len(grads) != n:
             raise _bad(where, f"{len(grads)} gradients for {n} parameters")
-        tensor, index = torch.Tensor, self.device.index
         first = getattr(grads[0], "dtype", None)
-        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
-            if not isinstance(g, tensor):
-                raise _bad(where, "grads: expected torch tensors")
-            if g.dtype is not first or g.shape != shape or not g.is_contiguous() or g.get_device() != index:
-                self._tensor(g, f"grads[{i}]", first, shape, self.device)
+        self._whole(grads, "grads", first)
         dt = _dtype(grads[0], where, "grads[0]")
-        # parameters may have been replaced (param.data = ...): their addresses are read anew
-        array = C.c_void_p * n
-        address = tensor.data_ptr
+        # parameters may have been replaced (param.data = ...): they are checked and their addresses read anew
+        self._whole(self.params, "params", torch.float32)
+        if self.copies is not None:
+            self._whole(self.copies, "copies", torch.bfloat16)
+        array, address = self._array, torch.Tensor.data_ptr
         params = array(*map(address, self.params))
         pointers = array(*map(address, grads))
         copies = None if self.copies is None else array(*map(address, self.copies))
