@@ -11,6 +11,7 @@ than their columns; the last axis has to be contiguous.
 from __future__ import annotations
 
 import ctypes as C
+import threading
 
 TT_EMB_DTYPE_FLOAT, TT_EMB_DTYPE_BFLOAT, TT_EMB_DTYPE_HALF = 0, 1, 2
 TT_EMB_STATUS_BYTES = 256
@@ -143,11 +144,15 @@ class _Operator:
     operator, also when a later call needs a larger one: keep the operator as
     long as the graph.  Make one ordinary call on the stream before the
     capture; a buffer that is first made inside a capture has its status
-    cleared by each replay."""
+    cleared by each replay.
+
+    Threads may share an operator: a call's kernels are enqueued together, so
+    that calls of one stream do not meet in its buffer."""
 
     def __init__(self, device):
         _bind()
         self.device = torch.device(device)
+        self._lock = threading.Lock()
         self._ws = {}
         self._in_graph = set()  # keys whose present buffer a graph writes to
         self._kept = []         # (key, buffer) that graphs write to and no other call any more
@@ -173,14 +178,23 @@ class _Operator:
             self._in_graph.add(key)
         return ws
 
+    def _run(self, fn, where: str, device, handle: int, need: int, *args):
+        """Enqueue a call that takes (ws, ws_bytes, stream) behind args."""
+        with self._lock:
+            ws = self._workspace(device, handle, need)
+            rc = fn(*args, ws.data_ptr(), ws.numel(), handle)
+        _check(rc, where)
+
     def poll_error(self) -> int:
         """Synchronises; the first device-detected error of any stream's
         calls since the last poll (0 = ok), cleared by reading it."""
         rc = 0
-        for key, ws in [*self._kept, *self._ws.items()]:
-            index, handle = key
+        with self._lock:
+            buffers = [(key, ws, True) for key, ws in self._kept]
+            buffers += [(key, ws, key in self._in_graph) for key, ws in self._ws.items()]
+        for (index, handle), ws, in_graph in buffers:
             with torch.cuda.device(index):
-                if key in self._in_graph or self._ws[key] is not ws:
+                if in_graph:
                     torch.cuda.synchronize()  # a graph is replayed on any stream
                 got = int(_L.tt_emb_poll_status(ws.data_ptr(), handle))
             rc = rc or got
@@ -232,9 +246,8 @@ class TokenEmbedding(_Operator):
             out, ld_o = weight.new_empty((n, self.D)), self.D
         else:
             ld_o = _matrix(out, where, "out", self.D, n, weight.dtype, device)
-        ws = self._workspace(device, s, TT_EMB_STATUS_BYTES)
-        _check(_L.tt_emb_lookup_forward(weight.data_ptr(), ld_w, tokens.data_ptr(), n, self.V, self.D, dt,
-                                      self.scale, out.data_ptr(), ld_o, ws.data_ptr(), ws.numel(), s), where)
+        self._run(_L.tt_emb_lookup_forward, where, device, s, TT_EMB_STATUS_BYTES, weight.data_ptr(), ld_w,
+                  tokens.data_ptr(), n, self.V, self.D, dt, self.scale, out.data_ptr(), ld_o)
         return out.view(*tokens.shape, self.D) if made and tokens.dim() != 1 else out
 
     def backward(self, grad_out, tokens, grad_weight=None, accumulate: bool = False, stream=None):
@@ -260,10 +273,9 @@ class TokenEmbedding(_Operator):
         if grad_weight is None:
             grad_weight = torch.empty((self.V, self.D), dtype=grad_out.dtype, device=device)
         ld_w = _matrix(grad_weight, where, "grad_weight", self.D, self.V, grad_out.dtype, device)
-        ws = self._workspace(device, s, need)
-        _check(_L.tt_emb_lookup_backward(grad_out.data_ptr(), ld_g, tokens.data_ptr(), n, self.V, self.D, dt,
-                                       self.scale, self.padding_idx, 1 if accumulate else 0,
-                                       grad_weight.data_ptr(), ld_w, ws.data_ptr(), ws.numel(), s), where)
+        self._run(_L.tt_emb_lookup_backward, where, device, s, need, grad_out.data_ptr(), ld_g, tokens.data_ptr(), n,
+                  self.V, self.D, dt, self.scale, self.padding_idx, 1 if accumulate else 0, grad_weight.data_ptr(),
+                  ld_w)
         return grad_weight
 
 
@@ -332,11 +344,9 @@ class LayerNorm(_Operator):
         kind = torch.float32 if gamma is None else gamma.dtype
         dgamma = torch.empty(self.D, dtype=kind, device=device)
         dbeta = torch.empty(self.D, dtype=kind, device=device)
-        ws = self._workspace(device, s, need)
-        _check(_L.tt_emb_norm_backward(grad_y.data_ptr(), ld_g, x.data_ptr(), ld_x, n, self.D, dt,
-                                     None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(),
-                                     rstd.data_ptr(), dx.data_ptr(), self.D, dgamma.data_ptr(),
-                                     dbeta.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
+        self._run(_L.tt_emb_norm_backward, where, device, s, need, grad_y.data_ptr(), ld_g, x.data_ptr(), ld_x, n,
+                  self.D, dt, None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(), rstd.data_ptr(),
+                  dx.data_ptr(), self.D, dgamma.data_ptr(), dbeta.data_ptr())
         return dx, dgamma, dbeta
 
 
@@ -404,10 +414,8 @@ class VocabCrossEntropy(_Operator):
         s = _raw_stream(device.index)
         loss = torch.empty(n, dtype=torch.float32, device=device)
         lse = torch.empty(n, dtype=torch.float32, device=device)
-        ws = self._workspace(device, s, need)
-        _check(_L.tt_emb_xent_forward(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(), n,
-                                    self.V, self.D, dt, self.ignore_index, loss.data_ptr(),
-                                    lse.data_ptr(), ws.data_ptr(), ws.numel(), s), where)
+        self._run(_L.tt_emb_xent_forward, where, device, s, need, hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w,
+                  targets.data_ptr(), n, self.V, self.D, dt, self.ignore_index, loss.data_ptr(), lse.data_ptr())
         return loss, lse
 
     def loss_and_grad(self, hidden, weight, targets, grad_loss, grad_weight=None, stream=None):
@@ -426,11 +434,9 @@ class VocabCrossEntropy(_Operator):
         if grad_weight is None:
             grad_weight = torch.empty((self.V, self.D), dtype=hidden.dtype, device=device)
         ld_dw = _matrix(grad_weight, where, "grad_weight", self.D, self.V, hidden.dtype, device)
-        ws = self._workspace(device, s, need)
-        _check(_L.tt_emb_xent_loss_grad(hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, targets.data_ptr(),
-                                      grad_loss.data_ptr(), n, self.V, self.D, dt, self.ignore_index,
-                                      loss.data_ptr(), lse.data_ptr(), dh.data_ptr(), self.D,
-                                      grad_weight.data_ptr(), ld_dw, ws.data_ptr(), ws.numel(), s), where)
+        self._run(_L.tt_emb_xent_loss_grad, where, device, s, need, hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w,
+                  targets.data_ptr(), grad_loss.data_ptr(), n, self.V, self.D, dt, self.ignore_index, loss.data_ptr(),
+                  lse.data_ptr(), dh.data_ptr(), self.D, grad_weight.data_ptr(), ld_dw)
         return loss, lse, dh, grad_weight
 
 
