@@ -113,8 +113,9 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_fwd(NormArgs a
         row_sum<TPR, 2>(q, sm, slot);
         // what the first mean's rounding left: it matters where a row's
         // offset is large beside its spread
-        const float slip = q[0] / (float)D, mean = mean0 + slip;
-        const float rstd = 1.f / sqrtf(fmaxf(fmaf(-slip, slip, q[1] / (float)D), 0.f) + a.eps);
+        const float slip = q[0] / (float)D, mean = slip == slip ? mean0 + slip : mean0; // (an infinite mean has none)
+        const float var = fmaf(-slip, slip, q[1] / (float)D);
+        const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps); // (a maximum would pass NaN over)
         if (r >= a.n) continue;
         T *y = static_cast<T *>(a.y) + r * a.ld_y;
 #pragma unroll
