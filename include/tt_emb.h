@@ -439,9 +439,10 @@ int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weigh
  * ws (D <= 128: d is not kept at all): bf16 for bf16 inputs, two fp16 terms, 22
  * bits, for fp32 inputs, whose own values are scaled by powers of two and split
  * the same way; sums are fp32.  fp32 inputs: a value of the weight keeps 22 bits
- * or an absolute 2^-39 of the weight's largest, whichever is more, and d 22 bits
- * or an absolute 2^-39 of the largest |grad_loss_i| (probabilities below 2^-17
- * lose bits).  An ignored row's hidden values do not reach the gradients,
+ * or an absolute 2^-39 of the weight's largest, whichever is more; a d_iv 22 bits
+ * or an absolute 2^-39 of its own row's grad_loss_i (probabilities below 2^-17
+ * lose bits); in grad_weight a grad_loss_i hidden_i 22 bits or an absolute 2^-39
+ * of the largest of all rows'.  An ignored row's hidden values do not reach the gradients,
  * whatever they hold.  A larger
  * ws allows larger pieces: any ws_bytes from *least of
  * tt_emb_xent_workspace_size on is accepted, *bytes is the size past which

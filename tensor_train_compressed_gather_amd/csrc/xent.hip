@@ -16,12 +16,14 @@
 // at 1350 TFLOP/s; 5 rows, loss only: 179 us, 6.0 TB/s.
 //
 // fp32 inputs are scaled by powers of two (to a largest magnitude in
-// [2^14, 2^15): each hidden row for the logits, the hidden rows that count as a
-// whole for the weight's gradient, the weight as a whole) and split into two
-// fp16 terms of 11 bits each, and the three products of terms above 2^-22 are
-// added up: five times the rate of the fp32 matrix instructions.  d, at most 1
-// in its units, is split the same way in units of 2^-15.  A value keeps 22
-// bits, or an absolute 2^-39 of the largest where that is more.
+// [2^14, 2^15): each hidden row for the logits, the hidden rows that count times
+// their dL/dloss as a whole for the weight's gradient, the weight as a whole) and
+// split into two fp16 terms of 11 bits each, and the three products of terms
+// above 2^-22 are added up: five times the rate of the fp32 matrix instructions.
+// d without dL/dloss (at most 1) is split the same way in units of 2^-15; the
+// sums of dH take dL/dloss at the end, so a row's precision does not depend on
+// the other rows' gradients.  A value keeps 22 bits, or an absolute 2^-39 of the
+// largest where that is more.
 #include "lm.h"
 #include "primitives.h"
 
@@ -114,11 +116,11 @@ struct Output {
     float2 *part;             // [vocabulary tiles][n] maximum and sum
     float *target_logit;      // [n]
     const float *lse, *grad;  // [n]
-    const float *top_grad;    // the unit of d
+    const float *top_grad;    // the unit of d (bf16)
     // fp16 terms: exponents by which each row (for the logits), all rows (for
     // the weight's gradient) and the weight were scaled
     const int *h_exp, *all_exp, *w_exp;
-    const float4 *rows;       // [n] scale, lse and gradient in the unit of d, of rows that are streamed
+    const float4 *rows;       // [n] scale, lse and factor of d, of rows that are streamed
     short *d;                 // [planes][rows][ldd]
     int64_t ldd, plane_d;
     float *sum;               // fp32 sums, [splits][sum_rows][D]
@@ -545,9 +547,8 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
         // 64 rows at a time pass through LDS, so that they are written in whole
         // lines: a lane holds four columns of one row, a wave 32 rows
         float unit = 1.f;
-        if constexpr (OUT == OUT_D) unit = *o.top_grad;
-        if constexpr (OUT == OUT_WEIGHT)
-            unit = PL == 2 ? ldexpf(*o.top_grad, -(kUnitExp + *o.all_exp)) : *o.top_grad;
+        if constexpr (OUT == OUT_D && PL == 1) unit = *o.top_grad;
+        if constexpr (OUT == OUT_WEIGHT) unit = PL == 2 ? ldexpf(1.f, -(kUnitExp + *o.all_exp)) : *o.top_grad;
         const int64_t left = o.V - o.v0 - m0; // of the vocabulary, in d
         __syncthreads();
 #pragma unroll
@@ -563,7 +564,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
                 if (row_counts(target, o.ignore, o.V)) {
                     if constexpr (PL == 2) scale = ldexpf(1.f, -(o.h_exp[i] + *o.w_exp));
                     t = target - o.v0 - m0;
-                    g = o.grad[i] / unit * (PL == 2 ? (float)(1 << kUnitExp) : 1.f);
+                    g = PL == 2 ? (float)(1 << kUnitExp) : o.grad[i] / unit;
                 } else {
                     lse = INFINITY;
                 }
@@ -664,8 +665,8 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
 // which five sums of three products are 5.2 at the card's rate (10.7 by the
 // products above); bf16 2.7 ms, where the exponentials' vector instructions take
 // as long as the products.  fp16 terms: the hidden rows keep their own scales in
-// dW's product too, so there d_i carries the ratio to the largest row's scale,
-// at most 1.
+// dW's product too, so there d_i carries dL/dloss and the ratio of the row's
+// scale to that of the largest product of the two, at most 1.
 enum { ROW_STATS, ROW_GRAD, VOC_GRAD };
 constexpr int kNarrowStep = 32;
 constexpr int64_t kNarrowSteps = 8;    // least steps of a split
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
     s16x8 of[PL][NO][KB];
     float scale[NO], lse[NO], g[NO], top[NO], sum[NO];
     int hit[NO], hit_row_of[NO]; // step of this row's target and its row there
-    const float unit = MODE != ROW_STATS ? *o.top_grad : 1.f;
+    const float unit = MODE != ROW_STATS && PL == 1 ? *o.top_grad : 1.f;
 #pragma unroll
     for (int b = 0; b < NO; ++b) {
         const int64_t i = own0 + b * 32 + (lane & 31), ic = i < own.rows ? i : own.rows - 1;
@@ -726,7 +727,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
                 const bool counts = i < own.rows && row_counts(target, o.ignore, o.V);
                 if (!counts) scale[b] = 1.f;
                 lse[b] = counts ? o.lse[ic] : INFINITY;
-                g[b] = counts ? o.grad[ic] / unit * (PL == 2 ? (float)(1 << kUnitExp) : 1.f) : 0.f;
+                g[b] = !counts ? 0.f : PL == 2 ? (float)(1 << kUnitExp) : o.grad[ic] / unit;
                 takes = takes && counts;
             }
             if (takes) {
@@ -951,7 +952,7 @@ __global__ __launch_bounds__(256, 2) void k_narrow(Operand own, Operand str, int
             if (lane < 32 && i < own.rows) o.part[sp * o.n + i] = both;
         }
     } else {
-        const float by = PL == 2 && VOC ? ldexpf(unit, -(kUnitExp + *o.all_exp)) : unit;
+        const float by = PL == 2 && VOC ? ldexpf(1.f, -(kUnitExp + *o.all_exp)) : unit;
         for (int first = 0; first < steps; first += kNarrowChain) {
             const int last = PL == 2 && steps - first > kNarrowChain ? first + kNarrowChain : steps;
 #pragma unroll
@@ -1067,19 +1068,28 @@ __global__ __launch_bounds__(256) void k_xent_few(const float *w, int64_t ld_w, 
     }
 }
 
-// A gradient from its splits' sums, in units of the loss (`exp`: of the
-// operand's scale, for fp16 terms).  `groups` (a power of two) threads share
+// What a gradient's sums are in: bf16 inputs, the unit of d; fp16 terms, the
+// operand's scale, and for the hidden rows their own dL/dloss.
+struct SumUnit {
+    const float *top_grad; // bf16
+    const int *exp;        // fp16 terms
+    const float *grad;     // with targets: of rows that count
+    const int64_t *targets;
+    int64_t ignore, V;
+};
+
+// A gradient from its splits' sums.  `groups` (a power of two) threads share
 // four values and the splits, so that many splits of few rows are not one
 // thread's chain (512 of 40 x 64: 129 us by one, 10 by 32); their sums meet in
 // LDS in order.
 template <class T>
 __global__ __launch_bounds__(256) void k_xent_sum(const float *sum, int splits, int groups, int64_t rows, int64_t D,
-                                                  const float *top_grad, const int *exp, T *out, int64_t ld)
+                                                  SumUnit u, T *out, int64_t ld)
 {
     __shared__ float4 part[256];
     const int each = 256 / groups, grp = threadIdx.x / each, in = threadIdx.x % each;
     const int64_t chunks = (D + 3) / 4, all = rows * chunks, step = (int64_t)gridDim.x * each;
-    const float unit = exp ? ldexpf(*top_grad, -(kUnitExp + *exp)) : *top_grad;
+    const float unit = u.exp ? ldexpf(1.f, -(kUnitExp + *u.exp)) : *u.top_grad;
     for (int64_t c0 = (int64_t)blockIdx.x * each; c0 < all; c0 += step) {
         const int64_t c = c0 + in < all ? c0 + in : all - 1;
         const int64_t i = c / chunks, k = (c - i * chunks) * 4;
@@ -1104,8 +1114,10 @@ __global__ __launch_bounds__(256) void k_xent_sum(const float *sum, int splits, 
                 x[3] += y.w;
             }
         }
+        // the sums of a row that does not count are 0 whatever its dL/dloss
+        const float g = u.targets && row_counts(u.targets[i], u.ignore, u.V) ? u.grad[i] : 1.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] *= unit;
+        for (int r = 0; r < 4; ++r) x[r] = x[r] * unit * g;
         if (grp == 0 && c0 + in < all) store_part<T, 4>(out + i * ld + k, left, x);
     }
 }
@@ -1121,9 +1133,10 @@ __device__ __forceinline__ float finite_abs(float x)
     return a < INFINITY ? a : 0.f;
 }
 
-// One piece of a row, scaled and split.
+// One piece of a row, times `by` and scaled, split; zeros where it is cleared.
 template <class T, int PL>
-__device__ __forceinline__ void pack_piece(const T *src, int64_t left, int e, bool clear, short *dst, int64_t plane)
+__device__ __forceinline__ void pack_piece(const T *src, int64_t left, float by, int e, bool clear, short *dst,
+                                           int64_t plane)
 {
     float x[8];
     load_part<T, 8>(src, (int)(left < 0 ? 0 : left < 8 ? left : 8), x);
@@ -1131,7 +1144,7 @@ __device__ __forceinline__ void pack_piece(const T *src, int64_t left, int e, bo
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         short s[PL];
-        split<PL>(clear ? 0.f : PL == 2 ? ldexpf(x[i], e) : x[i], s);
+        split<PL>(clear ? 0.f : PL == 2 ? ldexpf(x[i] * by, e) : x[i], s);
 #pragma unroll
         for (int q = 0; q < PL; ++q) w[q][i] = s[q];
     }
@@ -1204,7 +1217,7 @@ struct PackRows {
                 }
             }
             for (int64_t k = lane * 8; k < ld; k += 512)
-                pack_piece<T, PL>(row + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
+                pack_piece<T, PL>(row + (k < D ? k : 0), D - k, 1.f, e, false, dst + r * ld + k, plane);
         }
     }
 };
@@ -1235,8 +1248,8 @@ struct ClearRows {
     }
 };
 
-// The rows that count as fp16 planes scaled by one power of two, the others as
-// zeros: the operand of the weight's gradient.
+// The rows that count times their dL/dloss as fp16 planes scaled by one power of
+// two, the others as zeros: the operand of the weight's gradient.
 struct PackCounting {
     static constexpr int threads = 1024;
     const float *src;
@@ -1244,6 +1257,7 @@ struct PackCounting {
     short *dst;
     int64_t ld, plane;
     const int *exp;
+    const float *grad;
     const int64_t *targets;
     int64_t ignore, V;
 
@@ -1253,7 +1267,10 @@ struct PackCounting {
         const int e = *exp;
         for (int64_t c = (int64_t)block * threads + threadIdx.x; c < rows * chunks; c += step) {
             const int64_t r = c / chunks, k = (c - r * chunks) * 8;
-            pack_piece<float, 2>(src + r * ld_src + (k < D ? k : 0), D - k, e, !row_counts(targets[r], ignore, V),
+            // the factor's exponent goes with the scale: their product may pass what fp32 holds
+            const float g = grad[r];
+            pack_piece<float, 2>(src + r * ld_src + (k < D ? k : 0), D - k, __builtin_amdgcn_frexp_mantf(g),
+                                 e + __builtin_amdgcn_frexp_expf(g), !row_counts(targets[r], ignore, V),
                                  dst + r * ld + k, plane);
         }
     }
@@ -1313,29 +1330,33 @@ struct PackWeight {
         const int64_t chunks = ld / 8, step = (int64_t)blocks * 256;
         for (int64_t c = (int64_t)block * 256 + threadIdx.x; c < rows * chunks; c += step) {
             const int64_t r = c / chunks, k = (c - r * chunks) * 8;
-            pack_piece<T, PL>(src + r * ld_src + (k < D ? k : 0), D - k, e, false, dst + r * ld + k, plane);
+            pack_piece<T, PL>(src + r * ld_src + (k < D ? k : 0), D - k, 1.f, e, false, dst + r * ld + k, plane);
         }
     }
 };
 
-// The unit of d: the largest |grad_loss| of the rows that count.  With equal
-// gradients (a mean over the rows) d is exp(z - lse) - [v = target] in this
+// bf16: the unit of d, the largest |grad_loss| of the rows that count.  With
+// equal gradients (a mean over the rows) d is exp(z - lse) - [v = target] in this
 // unit, and the target's -1 + p, the largest term of both gradients, rounds to
 // bf16 without error for small p.  1 where there is nothing to scale.  fp16
-// terms: also the exponent for all rows together, from their largest.  One block.
+// terms: the exponent for all rows together, from the largest exponent of a
+// row's gradient and its largest value together.  One block.
 struct Units {
     static constexpr int threads = 256;
+    static constexpr int kNone = -(1 << 20);
     const float *grad;
     const int64_t *targets;
     int64_t ignore, n, V;
-    const float *tops;
+    const float *tops; // null for bf16
     float *unit;
     int *all_exp;
 
     __device__ void operator()(int, int) const
     {
-        __shared__ float sm[2][4];
-        float m = 0.f, h = 0.f;
+        __shared__ float sm[4];
+        __shared__ int se[4];
+        float m = 0.f;
+        int e = kNone;
         constexpr int U = 16; // loads in flight: their latency is what the one block waits for
         for (int64_t i0 = threadIdx.x; i0 < n; i0 += 256 * U) {
             int64_t t[U];
@@ -1344,32 +1365,37 @@ struct Units {
             for (int u = 0; u < U; ++u) {
                 const int64_t i = i0 + u * 256 < n ? i0 + u * 256 : i0;
                 t[u] = targets[i];
-                a[u] = grad[i];
+                a[u] = finite_abs(grad[i]);
                 b[u] = tops ? tops[i] : 0.f;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (row_counts(t[u], ignore, V)) m = fmaxf(m, fabsf(a[u]));
-                h = fmaxf(h, b[u]);
+                if (!row_counts(t[u], ignore, V)) continue;
+                m = fmaxf(m, a[u]);
+                if (a[u] > 0.f && b[u] > 0.f) {
+                    const int both = __builtin_amdgcn_frexp_expf(a[u]) + __builtin_amdgcn_frexp_expf(b[u]);
+                    e = e > both ? e : both;
+                }
             }
         }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) {
             m = fmaxf(m, __shfl_xor(m, o, 64));
-            h = fmaxf(h, __shfl_xor(h, o, 64));
+            const int other = __shfl_xor(e, o, 64);
+            e = e > other ? e : other;
         }
         if ((threadIdx.x & 63) == 0) {
-            sm[0][threadIdx.x >> 6] = m;
-            sm[1][threadIdx.x >> 6] = h;
+            sm[threadIdx.x >> 6] = m;
+            se[threadIdx.x >> 6] = e;
         }
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int w = 1; w < 4; ++w) {
-                m = fmaxf(m, sm[0][w]);
-                h = fmaxf(h, sm[1][w]);
+                m = fmaxf(m, sm[w]);
+                e = e > se[w] ? e : se[w];
             }
-            *unit = m > 0.f && m < INFINITY ? m : 1.f;
-            *all_exp = scale_exp(h);
+            *unit = m > 0.f ? m : 1.f;
+            *all_exp = e == kNone ? 0 : 15 - e;
         }
     }
 };
@@ -1388,7 +1414,8 @@ struct Join {
     // with `rows`: what the streamed rows of the weight's gradient need, too
     float4 *rows;
     const float *grad, *unit;
-    const int *h_exp, *w_exp, *all_exp; // null for bf16
+    const float *tops; // null for bf16
+    const int *h_exp, *w_exp, *all_exp;
 
     __device__ void operator()(int block, int) const
     {
@@ -1423,11 +1450,14 @@ struct Join {
         if (!rows) return;
         float4 c = make_float4(1.f, INFINITY, 0.f, 0.f);
         if (in && t != ignore) {
-            if (h_exp) c.x = ldexpf(1.f, -(h_exp[i] + *w_exp));
             c.y = z;
-            c.z = grad[i] / *unit;
-            // (a row of zeros has a scale of its own, and no part in the sum)
-            if (h_exp) c.z = ldexpf(c.z, kUnitExp + (*all_exp < h_exp[i] ? *all_exp - h_exp[i] : 0));
+            if (tops) {
+                c.x = ldexpf(1.f, -(h_exp[i] + *w_exp));
+                // (a row of zeros has no scale, and no part in the sum)
+                c.z = tops[i] > 0.f ? ldexpf(grad[i], kUnitExp + *all_exp - h_exp[i]) : grad[i] * 0.f;
+            } else {
+                c.z = grad[i] / *unit;
+            }
         }
         rows[i] = c;
     }
@@ -1616,12 +1646,12 @@ int64_t product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_
 }
 
 template <class T>
-void sum_up(const float *sum, int splits, int64_t rows, int64_t D, const float *unit, const int *exp, void *out,
-            int64_t ld, hipStream_t s)
+void sum_up(const float *sum, int splits, int64_t rows, int64_t D, const SumUnit &unit, void *out, int64_t ld,
+            hipStream_t s)
 {
     const int groups = splits >= 64 ? 32 : splits >= 8 ? 8 : 1;
     hipLaunchKernelGGL(k_xent_sum<T>, dim3(blocks_for(rows * ((D + 3) / 4) * groups)), dim3(256), 0, s, sum, splits,
-                       groups, rows, D, unit, exp, static_cast<T *>(out), ld);
+                       groups, rows, D, unit, static_cast<T *>(out), ld);
 }
 
 // A pass of the narrow kernels; `splits` as planned.
@@ -1726,6 +1756,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         join_job.grad = a.grad_loss;
         join_job.unit = p.top_grad;
         if constexpr (PL == 2) {
+            join_job.tops = p.tops;
             join_job.h_exp = p.h_exp;
             join_job.w_exp = p.w_exp;
             join_job.all_exp = p.all_exp;
@@ -1743,12 +1774,17 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     Operand h_all = h;
     if constexpr (PL == 2) {
         h_all.p = p.h_all;
-        const PackCounting count_job{hs, a.ld_h, a.n, a.D, p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.targets, a.ignore,
-                                     a.V};
+        const PackCounting count_job{hs, a.ld_h, a.n, a.D, p.h_all, p.Kp, a.n * p.Kp, p.all_exp, a.grad_loss, a.targets,
+                                     a.ignore, a.V};
         run_jobs(stats_job, stats_blocks, count_job,
                  piece > 0 ? (int)((blocks_for(a.n * (p.Kp / 8)) + 3) / 4) : 0, s);
     } else {
         run_jobs(stats_job, stats_blocks, NoJobOf<1024>(), 0, s);
+    }
+    SumUnit h_unit{p.top_grad}, w_unit{p.top_grad};
+    if constexpr (PL == 2) {
+        h_unit = SumUnit{nullptr, p.w_exp, a.grad_loss, a.targets, a.ignore, a.V};
+        w_unit = SumUnit{nullptr, p.all_exp};
     }
     if (piece < 0) {
         o.rows = p.rows;
@@ -1761,8 +1797,8 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         o.ld_out = a.ld_dw;
         narrow<T, PL, VOC_GRAD>(w, h, p.Kp, p.w_splits, o, s);
         if (p.w_splits > 1)
-            sum_up<T>(p.w_sum, p.w_splits, a.V, a.D, p.top_grad, PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
-        sum_up<T>(p.sum, p.splits, a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr, a.dh, a.ld_dh, s);
+            sum_up<T>(p.w_sum, p.w_splits, a.V, a.D, w_unit, a.dw, a.ld_dw, s);
+        sum_up<T>(p.sum, p.splits, a.n, a.D, h_unit, a.dh, a.ld_dh, s);
         return hipGetLastError();
     }
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
@@ -1794,9 +1830,9 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         o.splits = over_n.parts;
         o.split_k = over_n.each;
         product<PL, true, true, OUT_SUM>(h_all, d, a.D, a.V, rows, o, s);
-        sum_up<T>(p.w_sum, over_n.parts, a.V, a.D, p.top_grad, PL == 2 ? p.all_exp : nullptr, a.dw, a.ld_dw, s);
+        sum_up<T>(p.w_sum, over_n.parts, a.V, a.D, w_unit, a.dw, a.ld_dw, s);
     }
-    sum_up<T>(p.sum, p.parts, a.n, a.D, p.top_grad, PL == 2 ? p.w_exp : nullptr, a.dh, a.ld_dh, s);
+    sum_up<T>(p.sum, p.parts, a.n, a.D, h_unit, a.dh, a.ld_dh, s);
     return hipGetLastError();
 }
 

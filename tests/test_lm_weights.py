@@ -1,0 +1,70 @@
+"""The vocabulary cross entropy with dL/dloss of very different size per row:
+each row's gradient keeps its own precision."""
+
+import pytest
+import test_lm_ops as ops
+import torch
+
+import tensor_train_compressed_gather_amd as tt
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+U32 = ops.U32
+SIZES = [(64, 500, 64, 0), (64, 500, 128, 3), (200, 3000, 100, 0), (64, 500, 256, 0), (300, 3000, 200, 1)]
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("n,V,D,gap", SIZES)
+@pytest.mark.parametrize("largest", [0, 60, -60])
+def test_rows_keep_their_precision(n, V, D, gap, t, largest):
+    h, w, target, _ = ops.xent_inputs(n, V, D, t, gap, n + D)
+    grad = torch.exp2(torch.linspace(largest - 40, largest, n, device=ops.DEV))
+    grad[1::2] *= -1.3
+    grad[5], target[9] = 0.0, -100
+    z, lse, loss, d, mag = ops.xent_reference(h, w, target, grad, -100)
+    h64, w64 = h.double(), w.double()
+    got = tt.VocabCrossEntropy(V, D).loss_and_grad(h, w, target, grad)
+    ez = (6 * D + 8) * U32 * (h64.abs() @ w64.abs().t()).amax(1)
+    # d's rounding (two fp16 terms: 2^-22, and 2^-38 of the row's gradient for small probabilities; or bf16's)
+    size = (grad.double().abs() * (target != -100))[:, None]
+    ed = ((ops.u(BF16) if t == BF16 else 2.0 ** -21) + 2 * ez + 220 * U32)[:, None] * mag + 2.0 ** -38 * size
+    ref = d @ w64
+    ops.close(got[2], ref, ed @ w64.abs() + 6 * (V + 8) * U32 * (mag @ w64.abs()) + ops.u(t) * ref.abs(), "dh")
+    # two fp16 terms of a product that is scaled with the others: 2^-39 of the largest, of every row
+    ref = d.t() @ h64
+    floor = 2.0 ** -38 * (size * h64.abs()).amax() * (n + (mag / size.clamp(min=1e-300)).sum(0)[:, None])
+    ops.close(got[3], ref, ed.t() @ h64.abs() + 6 * (n + 8) * U32 * (mag.t() @ h64.abs()) + ops.u(t) * ref.abs()
+              + floor, "dw")
+    assert (got[2][5] == 0).all() and (got[2][9] == 0).all()
+
+
+@pytest.mark.parametrize("what", [float("inf"), float("nan")])
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("n,V,D,gap", SIZES)
+def test_a_gradient_that_is_not_finite_stays_in_its_row(n, V, D, gap, t, what):
+    h, w, target, grad = ops.xent_inputs(n, V, D, t, gap, n)
+    x = tt.VocabCrossEntropy(V, D)
+    grad = grad.round(decimals=3) * 1000  # beyond what fp16 holds in units of 2^-15
+    ref = x.loss_and_grad(h, w, target, grad)
+    grad[3] = what
+    got = x.loss_and_grad(h, w, target, grad)
+    rest = torch.arange(n, device=ops.DEV) != 3
+    assert not torch.isfinite(got[2][3]).any()
+    assert torch.isfinite(got[2][rest]).all()
+    close = (got[2][rest].double() - ref[2][rest].double()).abs() <= 8 * ops.u(t) * ref[2].double().abs().amax()
+    assert close.all()
+
+
+@pytest.mark.parametrize("n,V,D,gap", SIZES)
+def test_hidden_rows_of_zeros_beside_tiny_ones(n, V, D, gap):
+    h, w, target, grad = ops.xent_inputs(n, V, D, F32, gap, n)
+    h = h * 2.0 ** -100
+    h[::3] = 0
+    z, lse, loss, d, mag = ops.xent_reference(h, w, target, grad, -100)
+    got = tt.VocabCrossEntropy(V, D).loss_and_grad(h, w, target, grad)
+    ref = d.t() @ h.double()
+    h64 = h.double()
+    mag = mag + 2.0 ** -17 * grad.double()[:, None]  # d's own floor, as a part of 2^-21
+    bound = (2.0 ** -21 + (220 + 6 * (n + 8)) * U32) * (mag.t() @ h64.abs())
+    ops.close(got[3], ref, bound + 2.0 ** -38 * n * (grad.double()[:, None] * h64.abs()).max(), "dw")
+    assert torch.isfinite(got[2]).all()
