@@ -452,9 +452,16 @@ int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *wei
                           int32_t dtype, int64_t ignore_index, float *loss, float *lse, void *grad_hidden,
                           int64_t ld_grad_hidden, void *grad_weight, int64_t ld_grad_weight, void *ws,
                           size_t ws_bytes, void *stream);
-/* with_grad != 0: for tt_emb_xent_loss_grad, else for tt_emb_xent_forward
- * (one size: *least = *bytes).  Either pointer may be NULL. */
-int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t with_grad, size_t *bytes,
+/* Workspace of tt_emb_xent_loss_grad (what has TT_EMB_XENT_GRAD) or of
+ * tt_emb_xent_forward (one size: *least = *bytes).  With TT_EMB_XENT_ALIGNED the
+ * size is for hidden and weight whose first elements lie at multiples of 16
+ * bytes and whose ld are multiples of 8 of at most 2^20: bf16 rows of a multiple
+ * of 64 columns are then read in place where the operator can, and need no room
+ * for copies.  The calls find out by themselves how their operands lie, and
+ * return TT_EMB_ERR_WORKSPACE where ws is too small for that.  Either pointer may
+ * be NULL. */
+enum { TT_EMB_XENT_GRAD = 1, TT_EMB_XENT_ALIGNED = 2 };
+int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t what, size_t *bytes,
                                size_t *least);
 
 /* How tt_emb_xent_loss_grad sums grad_hidden over the vocabulary with a
@@ -462,15 +469,15 @@ int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, i
  * that go to `slot` of several partial sums, overwriting it (first != 0) or
  * adding to it; at the end slots 0 .. *slots - 1 are added up.  Writes the
  * first `cap` parts in the order they are taken and their number to *count.
- * The launches use the same functions; host only, no device work.  Sizes are
- * refused as by tt_emb_xent_workspace_size, n = 0 with TT_EMB_ERR_ARG, less
- * than *least bytes with TT_EMB_ERR_WORKSPACE. */
+ * The launches use the same functions; host only, no device work.  `what` as for
+ * tt_emb_xent_workspace_size, with TT_EMB_XENT_GRAD.  Sizes are refused as there,
+ * n = 0 with TT_EMB_ERR_ARG, less than *least bytes with TT_EMB_ERR_WORKSPACE. */
 typedef struct tt_emb_xent_part {
     int64_t begin, end;
     int32_t slot, first;
 } tt_emb_xent_part;
-int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, size_t ws_bytes, tt_emb_xent_part *parts,
-                      int64_t cap, int64_t *count, int32_t *slots);
+int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t what, size_t ws_bytes,
+                      tt_emb_xent_part *parts, int64_t cap, int64_t *count, int32_t *slots);
 
 /* One AdamW step (decoupled weight decay) over `count` fp32 tensors:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2

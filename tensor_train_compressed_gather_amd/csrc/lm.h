@@ -165,9 +165,10 @@ struct XentArgs {
 };
 hipError_t launch_xent_forward(const XentArgs &a, int dtype, hipStream_t s);
 hipError_t launch_xent_loss_grad(const XentArgs &a, int dtype, hipStream_t s);
-void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_t *best, size_t *least);
-int64_t xent_parts(int64_t n, int64_t V, int64_t D, int dtype, size_t ws_bytes, tt_emb_xent_part *parts, int64_t cap,
-                   int32_t *slots); // returns how many there are
+void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, int what, size_t *best, size_t *least);
+size_t xent_least(const XentArgs &a, int dtype, bool grad); // for these operands as they lie in memory
+int64_t xent_parts(int64_t n, int64_t V, int64_t D, int dtype, int what, size_t ws_bytes, tt_emb_xent_part *parts,
+                   int64_t cap, int32_t *slots); // returns how many there are
 
 constexpr int kAdamBlock = 256;   // elements that share one scale of an 8-bit state
 constexpr int kAdamTensors = 88;  // tensors per launch (their table is a kernel argument)

@@ -198,26 +198,26 @@ int tt_emb_norm_backward(const void *grad_y, int64_t ld_grad, const void *x, int
     return hip_status(launch_norm_backward(a, dtype, (hipStream_t)stream));
 }
 
-int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t with_grad, size_t *bytes,
+int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t what, size_t *bytes,
                                size_t *least)
 {
-    if (!bytes && !least) return TT_EMB_ERR_ARG;
+    if ((!bytes && !least) || (what & ~(TT_EMB_XENT_GRAD | TT_EMB_XENT_ALIGNED))) return TT_EMB_ERR_ARG;
     const int rc = check_xent(n, V, D, dtype);
     if (rc) return rc;
-    xent_workspace(n, V, D, dtype, with_grad != 0, bytes, least);
+    xent_workspace(n, V, D, dtype, what, bytes, least);
     return TT_EMB_OK;
 }
 
-int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, size_t ws_bytes, tt_emb_xent_part *parts,
-                      int64_t cap, int64_t *count, int32_t *slots)
+int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t what, size_t ws_bytes,
+                      tt_emb_xent_part *parts, int64_t cap, int64_t *count, int32_t *slots)
 {
     const int rc = check_xent(n, V, D, dtype);
     if (rc) return rc;
-    if (n == 0 || cap < 0 || (cap > 0 && !parts) || !count || !slots) return TT_EMB_ERR_ARG;
+    if (n == 0 || (what & ~TT_EMB_XENT_ALIGNED) != TT_EMB_XENT_GRAD || cap < 0 || (cap > 0 && !parts) || !count || !slots) return TT_EMB_ERR_ARG;
     size_t least = 0;
-    xent_workspace(n, V, D, dtype, true, nullptr, &least);
+    xent_workspace(n, V, D, dtype, what, nullptr, &least);
     if (ws_bytes < least) return TT_EMB_ERR_WORKSPACE;
-    *count = xent_parts(n, V, D, dtype, ws_bytes, parts, cap, slots);
+    *count = xent_parts(n, V, D, dtype, what, ws_bytes, parts, cap, slots);
     return TT_EMB_OK;
 }
 
@@ -230,9 +230,6 @@ int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weigh
     if (bad_matrix(hidden, ld_hidden, n, D, dtype) || bad_matrix(weight, ld_weight, V, D, dtype) ||
         (n > 0 && (!targets || !loss || !lse)))
         return TT_EMB_ERR_ARG;
-    size_t least = 0;
-    xent_workspace(n, V, D, dtype, false, nullptr, &least);
-    if ((rc = check_ws(ws, ws_bytes, least))) return rc;
     XentArgs a{};
     a.hidden = hidden;
     a.weight = weight;
@@ -247,6 +244,7 @@ int tt_emb_xent_forward(const void *hidden, int64_t ld_hidden, const void *weigh
     a.lse = lse;
     a.ws = static_cast<char *>(ws);
     a.ws_bytes = ws_bytes;
+    if ((rc = check_ws(ws, ws_bytes, xent_least(a, dtype, false)))) return rc;
     return hip_status(launch_xent_forward(a, dtype, (hipStream_t)stream));
 }
 
@@ -263,9 +261,6 @@ int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *wei
         bad_matrix(grad_weight, ld_grad_weight, V, D, dtype) ||
         (n > 0 && (!targets || !loss || !lse || !grad_loss)))
         return TT_EMB_ERR_ARG;
-    size_t least = 0;
-    xent_workspace(n, V, D, dtype, true, nullptr, &least);
-    if ((rc = check_ws(ws, ws_bytes, least))) return rc;
     XentArgs a{};
     a.hidden = hidden;
     a.weight = weight;
@@ -285,6 +280,7 @@ int tt_emb_xent_loss_grad(const void *hidden, int64_t ld_hidden, const void *wei
     a.ld_dw = ld_grad_weight;
     a.ws = static_cast<char *>(ws);
     a.ws_bytes = ws_bytes;
+    if ((rc = check_ws(ws, ws_bytes, xent_least(a, dtype, true)))) return rc;
     return hip_status(launch_xent_loss_grad(a, dtype, (hipStream_t)stream));
 }
 

@@ -1476,7 +1476,7 @@ struct XentPlan {
     int *h_exp, *all_exp, *w_exp;
     float2 *part;
     float4 *rows;
-    short *h, *h_all, *w; // packed operands (the weight's unused where it serves in place)
+    short *h, *h_all, *w; // packed operands, of those that are packed
     float *sum, *w_sum;
     short *d;
     int64_t Kp, nr, piece;
@@ -1563,11 +1563,22 @@ int64_t best_piece(int64_t n, int64_t V, int64_t D, int PL)
     return up(V < c ? V : c, kRound);
 }
 
+// Which operands are packed copies.  The statistics of few fp32 rows take none;
+// a bf16 weight serves in place where its rows are laid out as the loads need
+// them, and so do bf16 hidden rows without gradients (with them, rows that do
+// not count are cleared in the copy).
+struct Packed {
+    bool h, w;
+};
+Packed packed(int64_t n, int PL, bool grad, bool h_fits, bool w_fits)
+{
+    const bool few = PL == 2 && n <= kFewRows;
+    return {grad || (!few && !h_fits), (grad || !few) && !w_fits};
+}
+
 // `piece` columns of d (0: forward only; below 0: gradients by the narrow
-// kernels, -piece splits of dH).  Packed copies of the operands are planned
-// whether or not an aligned bf16 operand needs them, so that the size does not
-// depend on the pointers.
-XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char *base)
+// kernels, -piece splits of dH).
+XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, Packed pack, int64_t piece, char *base)
 {
     size_t off = TT_EMB_STATUS_BYTES;
     auto take = [&](size_t bytes) {
@@ -1587,8 +1598,8 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
     p.w_exp = (int *)take(4);
     p.all_exp = (int *)take(4);
     p.tops = (float *)take(4 * n);
-    p.h = (short *)take((size_t)PL * n * p.Kp * 2);
-    p.w = (short *)take((size_t)PL * V * p.Kp * 2);
+    if (pack.h) p.h = (short *)take((size_t)PL * n * p.Kp * 2);
+    if (pack.w) p.w = (short *)take((size_t)PL * V * p.Kp * 2);
     if (piece < 0) {
         p.rows = (float4 *)take(16 * (size_t)n);
         p.splits = (int)-piece;
@@ -1609,19 +1620,25 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, int64_t piece, char 
 }
 
 // The plan whose pieces fit the workspace.
-XentPlan fit_xent(int64_t n, int64_t V, int64_t D, int PL, bool grad, char *base, size_t ws_bytes)
+XentPlan fit_xent(int64_t n, int64_t V, int64_t D, int PL, Packed pack, bool grad, char *base, size_t ws_bytes)
 {
     int64_t piece = grad ? best_piece(n, V, D, PL) : 0;
-    while (piece < -1 && plan_xent(n, V, D, PL, piece, nullptr).bytes > ws_bytes) piece = -whole_splits(V, -piece / 2);
-    while (piece > kRound && plan_xent(n, V, D, PL, piece, nullptr).bytes > ws_bytes) piece = up(piece / 2, kRound);
-    return plan_xent(n, V, D, PL, piece, base);
+    auto fits = [&]() { return plan_xent(n, V, D, PL, pack, piece, nullptr).bytes <= ws_bytes; };
+    while (piece < -1 && !fits()) piece = -whole_splits(V, -piece / 2);
+    while (piece > kRound && !fits()) piece = up(piece / 2, kRound);
+    return plan_xent(n, V, D, PL, pack, piece, base);
 }
 
-template <class T, int PL>
-bool in_place(const T *src, int64_t ld, int64_t D, int64_t Kp)
+// Whether rows of an operand serve in place: bf16 rows of whole steps at
+// multiples of 16 bytes (rows further apart would pass the 31 bits of a tile's loads).
+bool fits_in_place(int PL, int64_t D) { return PL == 1 && D % kPadK == 0; }
+bool in_place(const void *src, int64_t ld, int64_t D, int PL)
 {
-    // (a tile of rows further apart would pass the 31 bits of its loads)
-    return PL == 1 && D == Kp && ld % 8 == 0 && ld <= (1 << 20) && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+    return fits_in_place(PL, D) && ld % 8 == 0 && ld <= (1 << 20) && (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+}
+Packed packed(const XentArgs &a, int PL, bool grad)
+{
+    return packed(a.n, PL, grad, in_place(a.hidden, a.ld_h, a.D, PL), in_place(a.weight, a.ld_w, a.D, PL));
 }
 
 unsigned blocks_for(int64_t threads)
@@ -1694,7 +1711,8 @@ template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
     const bool narrow_all = narrow_rows(a.n, a.V, a.D);
-    const XentPlan p = fit_xent(a.n, a.V, a.D, PL, grad, a.ws, a.ws_bytes);
+    const Packed pack = packed(a, PL, grad);
+    const XentPlan p = fit_xent(a.n, a.V, a.D, PL, pack, grad, a.ws, a.ws_bytes);
     const int64_t piece = p.piece;
     Output o{};
     o.n = a.n;
@@ -1717,13 +1735,11 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     const T *hs = static_cast<const T *>(a.hidden), *ws = static_cast<const T *>(a.weight);
     Operand h{reinterpret_cast<const short *>(hs), a.ld_h, 0, a.n, a.D};
     Operand w{reinterpret_cast<const short *>(ws), a.ld_w, 0, a.V, a.D};
-    const bool pack_h = grad || (!few && !in_place<T, PL>(hs, a.ld_h, a.D, p.Kp));
-    const bool pack_w = (grad || !few) && !in_place<T, PL>(ws, a.ld_w, a.D, p.Kp);
-    if (pack_h) h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
-    if (pack_w) w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
-    const int row_blocks = pack_h ? (int)blocks_for(a.n * 64) : 0;
+    if (pack.h) h = Operand{p.h, p.Kp, a.n * p.Kp, a.n, p.Kp};
+    if (pack.w) w = Operand{p.w, p.Kp, a.V * p.Kp, a.V, p.Kp};
+    const int row_blocks = pack.h ? (int)blocks_for(a.n * 64) : 0;
     const int unit_blocks = grad ? 1 : 0; // one block over all rows: begins first
-    const int w_blocks = pack_w ? (int)blocks_for(a.V * (p.Kp / 8)) : 0;
+    const int w_blocks = pack.w ? (int)blocks_for(a.V * (p.Kp / 8)) : 0;
     const PackRows<T, PL> rows_job{hs, a.ld_h, a.n, a.D, p.h, p.Kp, a.n * p.Kp, p.h_exp, p.tops,
                                    grad ? a.targets : nullptr, a.ignore, a.V};
     PackWeight<T, PL> w_job{ws, a.ld_w, a.V, a.D, p.w, p.Kp, a.V * p.Kp, p.w_part, 0, p.w_exp};
@@ -1731,7 +1747,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
                           p.all_exp};
     if constexpr (PL == 2) {
         // the rows and the weight's largest value, then the weight and the units
-        int parts = pack_w ? (int)blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1) : 0;
+        int parts = pack.w ? (int)blocks_for(a.V * ((a.D + 7) / 8) / 4 + 1) : 0;
         if (parts > kMaxParts) parts = kMaxParts;
         w_job.parts = parts;
         run_jobs(rows_job, row_blocks, WeightTop{ws, a.ld_w, a.V, a.D, p.w_part}, parts, s);
@@ -1838,19 +1854,35 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 
 } // namespace
 
-void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, bool grad, size_t *best, size_t *least)
+static void workspace_of(int64_t n, int64_t V, int64_t D, int PL, Packed pack, bool grad, size_t *best, size_t *least)
 {
-    const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1;
-    if (n < 1) n = 1; // no rows: the least workspace
     const int64_t most = grad ? best_piece(n, V, D, PL) : 0;
-    if (best) *best = plan_xent(n, V, D, PL, most, nullptr).bytes;
-    if (least) *least = plan_xent(n, V, D, PL, most < 0 ? -1 : most > 0 ? kRound : 0, nullptr).bytes;
+    if (best) *best = plan_xent(n, V, D, PL, pack, most, nullptr).bytes;
+    if (least) *least = plan_xent(n, V, D, PL, pack, most < 0 ? -1 : most > 0 ? kRound : 0, nullptr).bytes;
 }
 
-int64_t xent_parts(int64_t n, int64_t V, int64_t D, int dtype, size_t ws_bytes, tt_emb_xent_part *parts, int64_t cap,
-                   int32_t *slots)
+void xent_workspace(int64_t n, int64_t V, int64_t D, int dtype, int what, size_t *best, size_t *least)
 {
-    const XentPlan p = fit_xent(n, V, D, dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1, true, nullptr, ws_bytes);
+    const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1;
+    const bool grad = what & TT_EMB_XENT_GRAD, fits = (what & TT_EMB_XENT_ALIGNED) && fits_in_place(PL, D);
+    if (n < 1) n = 1; // no rows: the least workspace
+    workspace_of(n, V, D, PL, packed(n, PL, grad, fits, fits), grad, best, least);
+}
+
+size_t xent_least(const XentArgs &a, int dtype, bool grad)
+{
+    const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1;
+    size_t least = 0;
+    workspace_of(a.n < 1 ? 1 : a.n, a.V, a.D, PL, packed(a, PL, grad), grad, nullptr, &least);
+    return least;
+}
+
+int64_t xent_parts(int64_t n, int64_t V, int64_t D, int dtype, int what, size_t ws_bytes, tt_emb_xent_part *parts,
+                   int64_t cap, int32_t *slots)
+{
+    const int PL = dtype == TT_EMB_DTYPE_FLOAT ? 2 : 1;
+    const bool fits = (what & TT_EMB_XENT_ALIGNED) && fits_in_place(PL, D);
+    const XentPlan p = fit_xent(n, V, D, PL, packed(n, PL, true, fits, fits), true, nullptr, ws_bytes);
     int64_t count = 0;
     auto add = [&](int64_t begin, int64_t end, int slot, bool first) {
         if (count < cap) parts[count] = tt_emb_xent_part{begin, end, slot, first};

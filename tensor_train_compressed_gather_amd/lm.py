@@ -15,6 +15,7 @@ import threading
 
 TT_EMB_DTYPE_FLOAT, TT_EMB_DTYPE_BFLOAT, TT_EMB_DTYPE_HALF = 0, 1, 2
 TT_EMB_STATUS_BYTES = 256
+TT_EMB_XENT_GRAD, TT_EMB_XENT_ALIGNED = 1, 2
 
 LM_EXPORTED = (
     "tt_emb_poll_status",
@@ -41,7 +42,7 @@ def declare(L):
     L.tt_emb_xent_loss_grad.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i32, i64, p, p, p, i64, p, i64, p, size,
                                         p]
     L.tt_emb_xent_workspace_size.argtypes = [i64, i64, i64, i32, i32, sizes, sizes]
-    L.tt_emb_xent_parts.argtypes = [i64, i64, i64, i32, size, p, i64, C.POINTER(i64), C.POINTER(i32)]
+    L.tt_emb_xent_parts.argtypes = [i64, i64, i64, i32, i32, size, p, i64, C.POINTER(i64), C.POINTER(i32)]
     L.tt_emb_adamw_update.argtypes = [i32, p, p, i32, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64, p]
     L.tt_emb_adamw_state_size.argtypes = [i32, p, C.POINTER(i64)]
 
@@ -354,14 +355,15 @@ class tt_emb_xent_part(C.Structure):
     _fields_ = [("begin", C.c_int64), ("end", C.c_int64), ("slot", C.c_int32), ("first", C.c_int32)]
 
 
-def tt_emb_xent_parts(n: int, V: int, D: int, dtype: int, ws_bytes: int):
+def tt_emb_xent_parts(n: int, V: int, D: int, dtype: int, ws_bytes: int, aligned: bool = False):
     """The parts (begin, end, slot, first) of the vocabulary that
     loss_and_grad sums the hidden rows' gradient over, in order, and how many
     slots it adds up in the end (host-side; the launches use the same
     functions)."""
     _bind()
     count, slots = C.c_int64(), C.c_int32()
-    args = (int(n), int(V), int(D), int(dtype), int(ws_bytes))
+    what = TT_EMB_XENT_GRAD | (TT_EMB_XENT_ALIGNED if aligned else 0)
+    args = (int(n), int(V), int(D), int(dtype), what, int(ws_bytes))
     _check(_L.tt_emb_xent_parts(*args, None, 0, C.byref(count), C.byref(slots)), "tt_emb_xent_parts")
     parts = (tt_emb_xent_part * count.value)()
     _check(_L.tt_emb_xent_parts(*args, parts, count.value, C.byref(count), C.byref(slots)), "tt_emb_xent_parts")
@@ -385,10 +387,10 @@ class VocabCrossEntropy(_Operator):
         self.max_workspace = None if max_workspace is None else int(max_workspace)
         self._need(0, 0, False, "VocabCrossEntropy")
 
-    def _need(self, n: int, dt: int, grad: bool, where: str) -> int:
+    def _need(self, n: int, dt: int, grad: bool, where: str, aligned: bool = False) -> int:
         best, least = C.c_size_t(), C.c_size_t()
-        _check(_L.tt_emb_xent_workspace_size(n, self.V, self.D, dt, 1 if grad else 0, C.byref(best), C.byref(least)),
-              where)
+        what = (TT_EMB_XENT_GRAD if grad else 0) | (TT_EMB_XENT_ALIGNED if aligned else 0)
+        _check(_L.tt_emb_xent_workspace_size(n, self.V, self.D, dt, what, C.byref(best), C.byref(least)), where)
         if self.max_workspace is None or not grad:
             return int(best.value)
         if self.max_workspace < least.value:
@@ -401,12 +403,15 @@ class VocabCrossEntropy(_Operator):
         n, device = hidden.shape[0], hidden.device
         ld_w = _matrix(weight, where, "weight", self.D, self.V, hidden.dtype, device)
         _vector(targets, where, "targets", n, (torch.int64,), device)
-        return ld_h, ld_w, dt, n, device
+        # bf16 operands that lie like this are read in place and need no room for copies
+        aligned = (dt == 1 and not (ld_h | ld_w) & 7 and ld_h <= 1 << 20 and ld_w <= 1 << 20
+                   and not (hidden.data_ptr() | weight.data_ptr()) & 15)
+        return ld_h, ld_w, dt, n, device, aligned
 
     def forward(self, hidden, weight, targets, stream=None):
         where = "VocabCrossEntropy.forward"
-        ld_h, ld_w, dt, n, device = self._inputs(hidden, weight, targets, where)
-        need = self._need(n, dt, False, where)
+        ld_h, ld_w, dt, n, device, aligned = self._inputs(hidden, weight, targets, where)
+        need = self._need(n, dt, False, where, aligned)
         guard = _guard(device, stream, where)
         if guard is not None:
             with guard:
@@ -420,9 +425,9 @@ class VocabCrossEntropy(_Operator):
 
     def loss_and_grad(self, hidden, weight, targets, grad_loss, grad_weight=None, stream=None):
         where = "VocabCrossEntropy.loss_and_grad"
-        ld_h, ld_w, dt, n, device = self._inputs(hidden, weight, targets, where)
+        ld_h, ld_w, dt, n, device, aligned = self._inputs(hidden, weight, targets, where)
         _vector(grad_loss, where, "grad_loss", n, (torch.float32,), device)
-        need = self._need(n, dt, True, where)
+        need = self._need(n, dt, True, where, aligned)
         guard = _guard(device, stream, where)
         if guard is not None:
             with guard:

@@ -77,7 +77,9 @@ def test_parts_are_refused_like_the_call():
         assert e.value.status == code
     for bad in ((None, 1, C.byref(count), C.byref(slots)), (None, -1, C.byref(count), C.byref(slots)),
                 (None, 0, None, C.byref(slots)), (None, 0, C.byref(count), None)):
-        assert fn(10, 1000, 200, 1, best, *bad) == tt.TT_EMB_ERR_ARG
+        assert fn(10, 1000, 200, 1, 1, best, *bad) == tt.TT_EMB_ERR_ARG
+    for what in (0, 2, 4, 5):  # the parts are those of the call with gradients
+        assert fn(10, 1000, 200, 1, what, best, None, 0, C.byref(count), C.byref(slots)) == tt.TT_EMB_ERR_ARG
 
 
 @pytest.mark.gpu
