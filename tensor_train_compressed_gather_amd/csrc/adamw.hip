@@ -106,8 +106,11 @@ __global__ __launch_bounds__(256) void k_adamw(AdamTable t)
             M[i] = M[i] * t.beta1 + Gd[i] * t.one_minus_beta1;
             V[i] = V[i] * t.beta2 + (Gd[i] * t.one_minus_beta2) * Gd[i];
             // hardware square root and reciprocal (1 ulp each): p's own
-            // rounding is larger than what they add to it
-            const float den = __builtin_amdgcn_sqrtf(V[i]) * t.root + t.eps;
+            // rounding is larger than what they add to it.  The root takes
+            // values below 2^-126 for 0, so small ones are scaled up first.
+            const bool tiny = V[i] < 0x1p-96f;
+            const float root = __builtin_amdgcn_sqrtf(tiny ? V[i] * 0x1p64f : V[i]);
+            const float den = (tiny ? root * 0x1p-32f : root) * t.root + t.eps;
             P[i] = P[i] * t.decay - (M[i] * t.size) * __builtin_amdgcn_rcpf(den);
             if constexpr (BYTES) {
                 mmax = fmaxf(mmax, fabsf(M[i]));

@@ -65,3 +65,17 @@ def test_a_step_refuses_replaced_parameters_and_changes_nothing(wrong):
     p.data = good.clone()  # another place of the right kind is updated there
     opt.step(grads)
     assert torch.equal(good, keep[0]) and not torch.equal(p, keep[0]) and opt.steps == 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eps", [1e-8, 1e-15, 1e-20, 1e-30, 2e-38])
+def test_second_moments_below_the_normal_numbers(eps):
+    # v = g^2 / 1000 of gradients below 3e-18 is subnormal; its root is not
+    g = torch.tensor([1e-10, 1e-16, 1e-17, 4e-18, 3e-18, 1e-18, 3e-19, 1e-19, 3e-20, -1e-18], device="cuda")
+    p = torch.zeros_like(g)
+    opt = tt.AdamW([p], lr=1.0, eps=eps, weight_decay=0.0)
+    opt.step([g])
+    m, v = opt.exp_avg[:10].double(), opt.exp_avg_sq[:10].double()
+    assert (v > 0).all()
+    ref = -(m / (1 - 0.9)) / ((v / (1 - 0.999)).sqrt() + eps)
+    assert ((p.double() - ref).abs() <= 16 * 2.0 ** -24 * ref.abs()).all()
