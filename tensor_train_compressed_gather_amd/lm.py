@@ -212,7 +212,7 @@ class TokenEmbedding(_Operator):
     """Rows of a dense [V][D] table for token ids, times ``scale``.
 
     forward(weight, tokens) -> [*tokens.shape, D] of the weight's type.
-    backward(grad_out, tokens) -> the gradient of the weight, summed by sorted
+    backward(grad_out, tokens), grad_out [n, D] or [*tokens.shape, D] -> the gradient of the weight, summed by sorted
     tokens (bit-reproducible); tokens equal to ``padding_idx`` (negative: none)
     give none.  With accumulate=True it is added to ``grad_weight``, for a
     table that the output layer shares."""
@@ -253,10 +253,13 @@ class TokenEmbedding(_Operator):
 
     def backward(self, grad_out, tokens, grad_weight=None, accumulate: bool = False, stream=None):
         where = "TokenEmbedding.backward"
-        if torch.is_tensor(grad_out) and grad_out.dim() > 2:
+        if isinstance(grad_out, torch.Tensor) and grad_out.dim() != 2 and grad_out.dim() > 0:
             if grad_out.shape[:-1] != getattr(tokens, "shape", None):
                 raise _bad(where, f"grad_out: shape {tuple(grad_out.shape)}, not that of tokens and {self.D}")
-            grad_out = grad_out.view(-1, grad_out.shape[-1])
+            try:
+                grad_out = grad_out.view(tokens.numel(), grad_out.shape[-1])
+            except RuntimeError:
+                raise _bad(where, f"grad_out: strides {grad_out.stride()}, expected rows at one distance") from None
         ld_g = _matrix(grad_out, where, "grad_out", self.D)
         dt = _dtype(grad_out, where, "grad_out")
         device = grad_out.device
