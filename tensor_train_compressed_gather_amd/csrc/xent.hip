@@ -70,10 +70,14 @@ struct Terms<2> {
     }
 };
 
-// x as a sum of PL terms
+// x as a sum of PL terms.  What makes x is kept out of the conversions: fused
+// with a product, one of the two uses of a term rounded the exact product and
+// the other the rounded one, and where they differ (one value in some thousand)
+// the terms were off by a unit of the first.
 template <int PL>
 __device__ __forceinline__ void split(float x, short (&t)[PL])
 {
+    if constexpr (PL > 1) asm("" : "+v"(x));
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         const typename Terms<PL>::type y = (typename Terms<PL>::type)x;

@@ -68,3 +68,27 @@ def test_hidden_rows_of_zeros_beside_tiny_ones(n, V, D, gap):
     bound = (2.0 ** -21 + (220 + 6 * (n + 8)) * U32) * (mag.t() @ h64.abs())
     ops.close(got[3], ref, bound + 2.0 ** -38 * n * (grad.double()[:, None] * h64.abs()).max(), "dw")
     assert torch.isfinite(got[2]).all()
+
+
+def check_entries(n, V, D, gap, seed):
+    """Each entry of grad_weight within the roundings that it takes: no bound
+    here is near the 2^-11 of a single fp16 term."""
+    h, w, target, grad = ops.xent_inputs(n, V, D, F32, gap, seed)
+    got = tt.VocabCrossEntropy(V, D).loss_and_grad(h, w, target, grad)
+    z, lse, _, d, mag = ops.xent_reference(h, w, target, grad, -100)
+    h64, size = h.double(), grad.double()[:, None]
+    ez = (6 * D + 8) * U32 * (h64.abs() @ w.double().abs().t()).amax(1)
+    es = 2 * ez + U32 * (208 + V / 1024 + 4 * (z - lse[:, None]).abs().amax(1))
+    bound = (2.0 ** -21 + es[:, None]) * mag + 2.0 ** -38 * size
+    floor = 2.0 ** -38 * n * (size * h64.abs()).amax()
+    ref = d.t() @ h64
+    ops.close(got[3], ref, bound.t() @ h64.abs() + 6 * (n + 8) * U32 * (mag.t() @ h64.abs()) + U32 * ref.abs() + floor,
+              "dw")
+
+
+@pytest.mark.parametrize("n,V,D,gap", [(9, 796, 17, 0), (7, 10700, 19, 1), (134, 92616, 4, 8), (136, 116602, 36, 1),
+                                       (20, 40000, 128, 0), (60, 9000, 256, 0), (200, 3000, 600, 3)])
+def test_both_terms_of_every_entry(n, V, D, gap):
+    # gradients of the rows that are no powers of two, over many entries
+    for seed in range(4):
+        check_entries(n, V, D, gap, seed)
