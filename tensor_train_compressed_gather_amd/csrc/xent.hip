@@ -1476,7 +1476,7 @@ __global__ __launch_bounds__(256) void k_xent_clear(T *p, int64_t ld, int64_t ro
 }
 
 struct XentPlan {
-    float *target_logit, *top_grad, *w_part, *tops;
+    float *target_logit, *top_grad, *w_part, *tops, *lse;
     int *h_exp, *all_exp, *w_exp;
     float2 *part;
     float4 *rows;
@@ -1602,6 +1602,7 @@ XentPlan plan_xent(int64_t n, int64_t V, int64_t D, int PL, Packed pack, int64_t
     p.w_exp = (int *)take(4);
     p.all_exp = (int *)take(4);
     p.tops = (float *)take(4 * n);
+    if (piece && PL == 2 && n <= kFewRows) p.lse = (float *)take(4 * n);
     if (pack.h) p.h = (short *)take((size_t)PL * n * p.Kp * 2);
     if (pack.w) p.w = (short *)take((size_t)PL * V * p.Kp * 2);
     if (piece < 0) {
@@ -1726,7 +1727,6 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     o.ignore = a.ignore;
     o.part = p.part;
     o.target_logit = p.target_logit;
-    o.lse = a.lse;
     o.grad = a.grad_loss;
     o.top_grad = p.top_grad;
     o.h_exp = p.h_exp;
@@ -1761,7 +1761,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
         run_jobs(First{units_job, w_job, unit_blocks}, unit_blocks + w_blocks, rows_job, row_blocks, s);
     }
     int64_t tiles;
-    if (few) {
+    if (few && !grad) {
         tiles = few_rows(a, o, s);
     } else if (narrow_all) {
         tiles = narrow_splits(a.n, a.V, narrow_blocks(PL, ROW_STATS, p.Kp));
@@ -1769,7 +1769,7 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
     } else {
         tiles = product<PL, false, false, OUT_STATS>(w, h, a.V, a.n, p.Kp, o, s);
     }
-    Join join_job{p.part, tiles, a.n, a.V, a.targets, a.ignore, p.target_logit, a.loss, a.lse,
+    Join join_job{p.part, tiles, a.n, a.V, a.targets, a.ignore, p.target_logit, a.loss, few && grad ? p.lse : a.lse,
                   reinterpret_cast<int *>(a.ws)};
     if (piece < 0) {
         join_job.rows = p.rows;
@@ -1800,6 +1800,17 @@ hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
                  piece > 0 ? (int)((blocks_for(a.n * (p.Kp / 8)) + 3) / 4) : 0, s);
     } else {
         run_jobs(stats_job, stats_blocks, NoJobOf<1024>(), 0, s);
+    }
+    o.lse = join_job.lse;
+    if (few) {
+        // d takes the lse of its own logits: the errors of the two then cancel
+        // where a row is peaked (25 rows against 1437 x 870: gradients 2.3e-6
+        // from 64 bits with the lse of the other sums, 3.5e-7 with this one).  What
+        // the caller gets is what the call without gradients gives.
+        tiles = few_rows(a, o, s);
+        const Join out_job{p.part, tiles, a.n, a.V, a.targets, a.ignore, p.target_logit, a.loss, a.lse,
+                           reinterpret_cast<int *>(a.ws)};
+        run_jobs(out_job, join_blocks, NoJobOf<1024>(), 0, s);
     }
     SumUnit h_unit{p.top_grad}, w_unit{p.top_grad};
     if constexpr (PL == 2) {

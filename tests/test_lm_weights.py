@@ -92,3 +92,32 @@ def test_both_terms_of_every_entry(n, V, D, gap):
     # gradients of the rows that are no powers of two, over many entries
     for seed in range(4):
         check_entries(n, V, D, gap, seed)
+
+
+@pytest.mark.parametrize("n", [1, 5, 33, 64, 128, 129, 300])
+@pytest.mark.parametrize("V,D", [(2000, 40), (2000, 128), (2000, 160), (900, 600)])
+def test_probabilities_add_up_where_logits_are_inexact(n, V, D):
+    # d is exp(z - lse) - [v = target]: its sum over the vocabulary, which a
+    # column of ones in the weight gives, is 0 whatever the rounding of z, as
+    # long as lse is that of the same z.  Hidden rows share a large part u that
+    # the weight's rows have (almost) nothing of: z is small, its terms are not.
+    g = ops.gen(n + D)
+    u = torch.randn(D, device=ops.DEV, generator=g, dtype=torch.float64)
+    u[D - 1] = 0
+    w = torch.randn((V, D), device=ops.DEV, generator=g, dtype=torch.float64) * 2 / D ** 0.5
+    w[:, D - 1] = 0
+    w -= (w @ u)[:, None] * u / (u @ u)
+    target = torch.randint(0, V, (n,), device=ops.DEV, generator=g)
+    h = torch.randn((n, D), device=ops.DEV, generator=g, dtype=torch.float64)
+    h += 14 * w[target] / w[target].square().sum(1, keepdim=True) + 5000 * u
+    h[:, D - 1], w[:, D - 1] = 0, 1
+    h, w, grad = h.float(), w.float(), torch.rand(n, device=ops.DEV, generator=g) + 0.5
+    z, lse, loss, d, _ = ops.xent_reference(h, w, target, grad, -100)
+    got = tt.VocabCrossEntropy(V, D).loss_and_grad(h, w, target, grad)
+    p = (z - lse[:, None]).exp()
+    size = d.abs().sum(1)
+    # the roundings of lse, of the exponentials on both sides, of d and of the sum over V
+    one = (208 + V / 1024 + 2 * lse.abs() + 4 * (p * ((z - lse[:, None]).abs() + 1)).sum(1)) * U32
+    bound = grad * (one + V * 2.0 ** -38) + (2.0 ** -21 + 6 * (V + 8) * U32) * size
+    off = got[2][:, D - 1].double().abs()
+    assert (off <= bound).all(), float((off - bound).max())
