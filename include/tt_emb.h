@@ -482,7 +482,8 @@ int tt_emb_xent_parts(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t wh
 /* One AdamW step (decoupled weight decay) over `count` fp32 tensors:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr mhat / (sqrt(vhat) + eps)
- * with mhat = m / (1 - beta1^step), vhat = v / (1 - beta2^step), step >= 1.
+ * with mhat = m / (1 - beta1^step), vhat = v / (1 - beta2^step), step >= 1,
+ * eps >= 2^-126.
  * params, grads, copies, numel are HOST arrays; grads are of grad_dtype;
  * copies (bf16 tensors that receive the updated values, rounded) may be NULL.
  * exp_avg (m) and exp_avg_sq (v) are single device buffers in which each

@@ -15,6 +15,11 @@
 // with both gradients, four products (the logits are made twice) of 8.8 TFLOP
 // at 1350 TFLOP/s; 5 rows, loss only: 179 us, 6.0 TB/s.
 //
+// bf16 inputs: d is rounded to bf16, by at most 2^-8 of each value, because two
+// terms of it would double both gradients' products.  The gradients' own rounding
+// to bf16 is as large: 8192 rows against 131072 x 4096 are 1.9e-3 from 64 bits,
+// 1.7e-3 with d in fp32.
+//
 // fp32 inputs are scaled by powers of two (to a largest magnitude in
 // [2^14, 2^15): each hidden row for the logits, the hidden rows that count times
 // their dL/dloss as a whole for the weight's gradient, the weight as a whole) and
@@ -678,7 +683,6 @@ constexpr int64_t kNarrowSteps = 8;    // least steps of a split
 // accumulator would round 10^6 rows' sum to 2^-19.6, in parts of 8192 rows to 2^-21.
 constexpr int kNarrowChain = 256;
 constexpr int64_t kNarrow = 128;       // longest rows
-constexpr int64_t kNarrowRows = 1ll << 31;
 
 // Which of a streamed row's 16-byte pieces change places: sixteen rows' equal
 // pieces, and the 64 bytes of four neighbouring rows, lie in different banks.
@@ -1540,7 +1544,7 @@ constexpr int narrow_blocks(int PL, int mode, int64_t Kp)
 {
     return mode == ROW_STATS || (PL == 1 && Kp == 64) ? 2 : 1;
 }
-inline bool narrow_rows(int64_t n, int64_t V, int64_t D) { return D <= kNarrow && n < kNarrowRows && V < kNarrowRows; }
+inline bool narrow_rows(int64_t D) { return D <= kNarrow; }
 inline int whole_splits(int64_t streamed, int64_t s) // s, less the splits that equal parts leave empty
 {
     const int64_t steps = (streamed + kNarrowStep - 1) / kNarrowStep;
@@ -1561,7 +1565,7 @@ int narrow_splits(int64_t own, int64_t streamed, int blocks)
 
 int64_t best_piece(int64_t n, int64_t V, int64_t D, int PL)
 {
-    if (narrow_rows(n, V, D)) return -narrow_splits(n, V, narrow_blocks(PL, ROW_GRAD, up(D, kPadK)));
+    if (narrow_rows(D)) return -narrow_splits(n, V, narrow_blocks(PL, ROW_GRAD, up(D, kPadK)));
     int64_t c = (int64_t)(kPieceBytes / ((size_t)PL * d_rows(n) * 2)) / kRound * kRound;
     if (c < 8 * kRound) c = 8 * kRound;
     return up(V < c ? V : c, kRound);
@@ -1715,7 +1719,7 @@ int64_t few_rows(const XentArgs &a, const Output &o, hipStream_t s)
 template <class T, int PL>
 hipError_t xent(const XentArgs &a, bool grad, hipStream_t s)
 {
-    const bool narrow_all = narrow_rows(a.n, a.V, a.D);
+    const bool narrow_all = narrow_rows(a.D);
     const Packed pack = packed(a, PL, grad);
     const XentPlan p = fit_xent(a.n, a.V, a.D, PL, pack, grad, a.ws, a.ws_bytes);
     const int64_t piece = p.piece;

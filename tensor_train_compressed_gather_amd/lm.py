@@ -145,7 +145,8 @@ class _Operator:
     operator, also when a later call needs a larger one: keep the operator as
     long as the graph.  Make one ordinary call on the stream before the
     capture; a buffer that is first made inside a capture has its status
-    cleared by each replay.
+    cleared by each replay.  Graphs and calls of one stream share its buffer, so
+    they may not run at the same time; give graphs that do an operator each.
 
     Threads may share an operator: a call's kernels are enqueued together, so
     that calls of one stream do not meet in its buffer."""
@@ -382,7 +383,13 @@ class VocabCrossEntropy(_Operator):
     loss_and_grad(hidden, weight, targets, grad_loss) -> (loss, lse,
     grad_hidden, grad_weight) for fp32 grad_loss [n] = dL/dloss.
     ``max_workspace`` bounds the scratch of loss_and_grad in bytes (smaller
-    pieces of the vocabulary at a time)."""
+    pieces of the vocabulary at a time).
+
+    fp32 inputs are taken as two fp16 terms, 22 bits: the weight's values with
+    one scale for all of them, so beside one of 2^k a value of 1 keeps no more
+    than 39 - k bits.  bf16 rows of a multiple of 64 columns that begin at
+    multiples of 16 bytes are read in place; other weights are copied by each
+    call."""
 
     def __init__(self, V: int, D: int, ignore_index: int = -100, device="cuda", max_workspace: int | None = None):
         super().__init__(device)
@@ -456,7 +463,9 @@ class AdamW:
     ``seed`` and the step's number.  ``copies``: bf16 tensors of the same
     shapes that receive the updated values.  The state is ``exp_avg``,
     ``exp_avg_sq`` (flat; each tensor begins at a multiple of 256 elements),
-    ``exp_avg_scale``, ``exp_avg_sq_scale`` and ``steps``."""
+    ``exp_avg_scale``, ``exp_avg_sq_scale`` and ``steps``.  ``eps`` is at least
+    2^-126.  Parameters may be replaced (``param.data = ...``) by tensors of the
+    same shape; every step needs a gradient for each."""
 
     BLOCK = 256
 
