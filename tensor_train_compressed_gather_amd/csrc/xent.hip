@@ -11,9 +11,9 @@
 // 128 values take kernels of their own, which never write d.
 //
 // Matrix instructions bound the large sizes, the weight's bytes those of few
-// rows, launches the smallest.  8192 rows against 131072 x 4096 in bf16: 26.1 ms
+// rows, launches the smallest.  8192 rows against 131072 x 4096 in bf16: 26.7 ms
 // with both gradients, four products (the logits are made twice) of 8.8 TFLOP
-// at 1350 TFLOP/s; 5 rows, loss only: 179 us, 6.0 TB/s.
+// at 1320 TFLOP/s; 5 rows, loss only: 179 us, 6.0 TB/s.
 //
 // bf16 inputs: d is rounded to bf16, by at most 2^-8 of each value, because two
 // terms of it would double both gradients' products.  The gradients' own rounding

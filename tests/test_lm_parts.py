@@ -14,9 +14,10 @@ import tensor_train_compressed_gather_amd as tt
 F32, BF16 = torch.float32, torch.bfloat16
 
 
-def workspace(n, V, D, dtype):
+def workspace(n, V, D, dtype, aligned=False):
     best, least = C.c_size_t(), C.c_size_t()
-    assert tt.lib().tt_emb_xent_workspace_size(n, V, D, dtype, 1, C.byref(best), C.byref(least)) == 0
+    what = 3 if aligned else 1
+    assert tt.lib().tt_emb_xent_workspace_size(n, V, D, dtype, what, C.byref(best), C.byref(least)) == 0
     return best.value, least.value
 
 
@@ -39,20 +40,20 @@ def sizes():
     return got
 
 
-@pytest.mark.parametrize("dtype", [0, 1])
-def test_every_part_begins_in_the_vocabulary(dtype):
+@pytest.mark.parametrize("dtype,aligned", [(0, False), (1, False), (1, True)])
+def test_every_part_begins_in_the_vocabulary(dtype, aligned):
     for n, V, D, share in sizes():
-        best, least = workspace(n, V, D, dtype)
-        parts, _ = tt.tt_emb_xent_parts(n, V, D, dtype, least + int(share * (best - least)))
+        best, least = workspace(n, V, D, dtype, aligned)
+        parts, _ = tt.tt_emb_xent_parts(n, V, D, dtype, least + int(share * (best - least)), aligned)
         assert parts and all(0 <= begin < end <= V for begin, end, _, _ in parts), (n, V, D, share)
 
 
-@pytest.mark.parametrize("dtype", [0, 1])
-def test_every_row_is_in_one_part_and_every_part_is_summed(dtype):
+@pytest.mark.parametrize("dtype,aligned", [(0, False), (1, False), (1, True)])
+def test_every_row_is_in_one_part_and_every_part_is_summed(dtype, aligned):
     several = 0
     for n, V, D, share in sizes():
-        best, least = workspace(n, V, D, dtype)
-        parts, slots = tt.tt_emb_xent_parts(n, V, D, dtype, least + int(share * (best - least)))
+        best, least = workspace(n, V, D, dtype, aligned)
+        parts, slots = tt.tt_emb_xent_parts(n, V, D, dtype, least + int(share * (best - least)), aligned)
         at, written = 0, set()
         for begin, end, slot, first in parts:
             assert begin == at, (n, V, D, share)
