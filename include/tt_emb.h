@@ -506,6 +506,29 @@ int tt_emb_adamw_update(int32_t count, float *const *params, const void *const *
                         void *stream);
 int tt_emb_adamw_state_size(int32_t count, const int64_t *numel, int64_t *elements);
 
+/* The same step with every gradient multiplied by *grad_scale (one fp32 value
+ * on the device; NULL: 1), such as the factor of tt_emb_clip_norm. */
+int tt_emb_adamw_update_scaled(int32_t count, float *const *params, const void *const *grads, int32_t grad_dtype,
+                               const float *grad_scale, void *const *copies, const int64_t *numel, void *exp_avg,
+                               void *exp_avg_sq, float *exp_avg_scale, float *exp_avg_sq_scale, int32_t state_bits,
+                               double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                               uint64_t seed, void *stream);
+
+/* Global norm of the gradients of `count` tensors, and their bound:
+ *   N = sqrt(sum of all g^2),  factor = 1 where N + eps <= max_norm, else max_norm / (N + eps)
+ * grads, dtypes (TT_EMB_DTYPE_*, mixed as they come) and numel are HOST arrays;
+ * norm and factor are single fp32 values on the device, each may be NULL.
+ * max_norm >= 0 (infinity: no bound), eps >= 0.  Squares are added in fp64, in an
+ * order that depends on the sizes alone.  tt_emb_clip_norm reads the gradients;
+ * tt_emb_clip_scale also multiplies them by the factor in place, rounded to
+ * their type, and leaves them alone where it is 1; its tensors may not share memory.
+ * A NaN makes N and the factor NaN; an infinity makes N infinite and the factor 0. */
+int tt_emb_clip_norm(int32_t count, const void *const *grads, const int32_t *dtypes, const int64_t *numel,
+                     double max_norm, double eps, float *norm, float *factor, void *ws, size_t ws_bytes, void *stream);
+int tt_emb_clip_scale(int32_t count, void *const *grads, const int32_t *dtypes, const int64_t *numel,
+                      double max_norm, double eps, float *norm, float *factor, void *ws, size_t ws_bytes, void *stream);
+int tt_emb_clip_workspace_size(int32_t count, const int64_t *numel, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

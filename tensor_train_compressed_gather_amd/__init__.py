@@ -14,7 +14,7 @@ import os
 import threading
 
 from . import lm as _lm
-from .lm import (LM_EXPORTED, AdamW, LayerNorm, TokenEmbedding, VocabCrossEntropy,  # noqa: F401
+from .lm import (LM_EXPORTED, AdamW, GradientClip, LayerNorm, TokenEmbedding, VocabCrossEntropy,  # noqa: F401
                  tt_emb_xent_parts)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

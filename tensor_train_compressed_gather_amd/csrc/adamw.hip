@@ -71,6 +71,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamTable t)
     float *const p = t.p[lo];
     const G *const g = static_cast<const G *>(t.g[lo]);
     bf16 *const copy = t.copy[lo];
+    const float g_scale = t.g_scale ? *t.g_scale : 1.f; // (times 1 is exact)
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t q0 = (int64_t)((int)blockIdx.x - t.first[lo]) * kAdamSpan + wave;
 #pragma unroll
@@ -103,6 +104,7 @@ __global__ __launch_bounds__(256) void k_adamw(AdamTable t)
         bool mbad = false, vbad = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            Gd[i] *= g_scale;
             M[i] = M[i] * t.beta1 + Gd[i] * t.one_minus_beta1;
             V[i] = V[i] * t.beta2 + (Gd[i] * t.one_minus_beta2) * Gd[i];
             // hardware square root and reciprocal (1 ulp each): p's own

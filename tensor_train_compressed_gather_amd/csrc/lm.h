@@ -1,5 +1,5 @@
 // lm.h -- shared definitions of the operators around the table (lookup, norm,
-// xent, adamw): element types, vector access, block reductions, launchers.
+// xent, adamw, clip): element types, vector access, block reductions, launchers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -179,6 +179,7 @@ struct AdamTable {
     float decay, size, root, eps;     // 1 - lr wd, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
     void *m, *v;
     float *m_scale, *v_scale;
+    const float *g_scale;             // what multiplies the gradients, null for 1
     int32_t first[kAdamTensors + 1];  // first thread block of each tensor
     int32_t qb[kAdamTensors];         // first block of kAdamBlock elements in the states
     float *p[kAdamTensors];
@@ -189,5 +190,28 @@ struct AdamTable {
 static_assert(sizeof(AdamTable) <= 4096, "the table is passed as a kernel argument");
 hipError_t launch_adamw(AdamTable &t, int32_t count, float *const *p, const void *const *g, int grad_dtype,
                         void *const *copies, const int64_t *numel, int bits, hipStream_t s);
+
+constexpr int kClipTensors = 160; // tensors per launch (their table is a kernel argument)
+constexpr int kClipBlocks = 8 * kCUs; // blocks of a launch, at most
+struct ClipTable {
+    int n;
+    int32_t first[kClipTensors + 1]; // first chunk of each tensor
+    void *g[kClipTensors];
+    int64_t cnt[kClipTensors];
+    uint8_t dtype[kClipTensors];
+};
+struct ClipBound {
+    double max_norm, eps;
+    float *norm, *factor;
+};
+static_assert(sizeof(ClipTable) + sizeof(ClipBound) + 16 <= 4096, "the table is passed as a kernel argument");
+struct ClipPlan {
+    int64_t chunks;
+    int launches;
+    int64_t parts; // partial sums
+};
+ClipPlan plan_clip(int32_t count, const int64_t *numel);
+hipError_t launch_clip(int32_t count, void *const *grads, const int32_t *dtypes, const int64_t *numel,
+                       const ClipBound &b, bool scale, char *ws, hipStream_t s);
 
 } // namespace ttemb

@@ -1,8 +1,11 @@
 // lm_api.hip -- host side of the operators around the table (lookup, norm,
-// xent, adamw): argument checks before anything is enqueued, then the
-// stream-ordered launches.  Nothing here allocates, and no exception leaves.
+// xent, adamw, clip): argument checks before anything is enqueued, then the
+// stream-ordered launches.  Nothing here allocates device memory, and no exception
+// leaves.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <new>
 
 #include "lm.h"
 
@@ -29,6 +32,7 @@ int hip_status(hipError_t e) { return e == hipSuccess ? TT_EMB_OK : TT_EMB_ERR_H
 constexpr int64_t kMaxRows = 0x7ffffffe;
 constexpr int64_t kMaxLookupCols = 65536, kMaxNormCols = 16384, kMaxXentCols = 16384;
 constexpr int64_t kMaxXentTiles = (int64_t)1 << 23;
+constexpr int64_t kMaxClipValues = (int64_t)1 << 42;
 
 int check_lookup(int64_t n, int64_t V, int64_t D, int32_t dtype)
 {
@@ -53,6 +57,63 @@ int check_xent(int64_t n, int64_t V, int64_t D, int32_t dtype)
     // tiles of the logits: the blocks of one launch stay below 2^24
     if (((n + 127) / 128) * ((V + 127) / 128) > kMaxXentTiles) return TT_EMB_ERR_UNSUPPORTED;
     return TT_EMB_OK;
+}
+
+int check_clip(int32_t count, const int64_t *numel)
+{
+    if (count < 0 || (count > 0 && !numel)) return TT_EMB_ERR_ARG;
+    int64_t all = 0;
+    for (int32_t k = 0; k < count; ++k) {
+        if (numel[k] < 0) return TT_EMB_ERR_ARG;
+        // the chunks of a launch and the partial sums of all stay below 2^31
+        all += numel[k] > kMaxClipValues ? kMaxClipValues + 1 : numel[k];
+        if (all > kMaxClipValues) return TT_EMB_ERR_UNSUPPORTED;
+    }
+    return TT_EMB_OK;
+}
+
+size_t clip_workspace(int32_t count, const int64_t *numel)
+{
+    return TT_EMB_STATUS_BYTES + round256((size_t)plan_clip(count, numel).parts * sizeof(double));
+}
+
+// Whether two of the tensors share memory: each is scaled once.
+int check_apart(int32_t count, void *const *grads, const int32_t *dtypes, const int64_t *numel)
+{
+    struct Range {
+        uintptr_t begin, end;
+    };
+    Range *r = new (std::nothrow) Range[count];
+    if (!r) return TT_EMB_ERR_NOMEM;
+    int32_t n = 0;
+    for (int32_t k = 0; k < count; ++k) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(grads[k]);
+        if (numel[k]) r[n++] = {p, p + (uintptr_t)numel[k] * dtype_size(dtypes[k])};
+    }
+    std::sort(r, r + n, [](const Range &a, const Range &b) { return a.begin < b.begin; });
+    bool apart = true;
+    for (int32_t k = 1; k < n; ++k) apart = apart && r[k - 1].end <= r[k].begin;
+    delete[] r;
+    return apart ? TT_EMB_OK : TT_EMB_ERR_ARG;
+}
+
+int clip(int32_t count, void *const *grads, const int32_t *dtypes, const int64_t *numel, double max_norm, double eps,
+         float *norm, float *factor, bool scale, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = check_clip(count, numel);
+    if (rc) return rc;
+    if (!(max_norm >= 0.0) || !(eps >= 0.0) || !std::isfinite(eps)) return TT_EMB_ERR_ARG;
+    if (off_grid(norm, TT_EMB_DTYPE_FLOAT) || off_grid(factor, TT_EMB_DTYPE_FLOAT)) return TT_EMB_ERR_ARG;
+    if (count > 0 && (!grads || !dtypes)) return TT_EMB_ERR_ARG;
+    for (int32_t k = 0; k < count; ++k) {
+        if (bad_dtype(dtypes[k])) return TT_EMB_ERR_ARG;
+        if (numel[k] && (!grads[k] || off_grid(grads[k], dtypes[k]))) return TT_EMB_ERR_ARG;
+    }
+    if (scale && (rc = check_apart(count, grads, dtypes, numel))) return rc;
+    if ((rc = check_ws(ws, ws_bytes, clip_workspace(count, numel)))) return rc;
+    const ClipBound b{max_norm, eps, norm, factor};
+    return hip_status(launch_clip(count, grads, dtypes, numel, b, scale, static_cast<char *>(ws),
+                                  (hipStream_t)stream));
 }
 
 } // namespace
@@ -305,6 +366,17 @@ int tt_emb_adamw_update(int32_t count, float *const *params, const void *const *
                         double beta1, double beta2, double eps, double weight_decay, int64_t step, uint64_t seed,
                         void *stream)
 {
+    return tt_emb_adamw_update_scaled(count, params, grads, grad_dtype, nullptr, copies, numel, exp_avg, exp_avg_sq,
+                                      exp_avg_scale, exp_avg_sq_scale, state_bits, lr, beta1, beta2, eps,
+                                      weight_decay, step, seed, stream);
+}
+
+int tt_emb_adamw_update_scaled(int32_t count, float *const *params, const void *const *grads, int32_t grad_dtype,
+                               const float *grad_scale, void *const *copies, const int64_t *numel, void *exp_avg,
+                               void *exp_avg_sq, float *exp_avg_scale, float *exp_avg_sq_scale, int32_t state_bits,
+                               double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                               uint64_t seed, void *stream)
+{
     int64_t elements = 0;
     const int rc = tt_emb_adamw_state_size(count, numel, &elements);
     if (rc) return rc;
@@ -312,6 +384,7 @@ int tt_emb_adamw_update(int32_t count, float *const *params, const void *const *
     if (!(lr >= 0.0) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !((float)eps >= FLT_MIN) ||
         !(weight_decay >= 0.0))
         return TT_EMB_ERR_ARG;
+    if (off_grid(grad_scale, TT_EMB_DTYPE_FLOAT)) return TT_EMB_ERR_ARG;
     if (elements == 0) return TT_EMB_OK;
     if (!params || !grads) return TT_EMB_ERR_ARG;
     for (int32_t k = 0; k < count; ++k) {
@@ -340,8 +413,31 @@ int tt_emb_adamw_update(int32_t count, float *const *params, const void *const *
     t.v = exp_avg_sq;
     t.m_scale = exp_avg_scale;
     t.v_scale = exp_avg_sq_scale;
+    t.g_scale = grad_scale;
     return hip_status(launch_adamw(t, count, params, grads, grad_dtype, copies, numel, state_bits,
                                    (hipStream_t)stream));
+}
+
+int tt_emb_clip_workspace_size(int32_t count, const int64_t *numel, size_t *bytes)
+{
+    if (!bytes) return TT_EMB_ERR_ARG;
+    const int rc = check_clip(count, numel);
+    if (rc) return rc;
+    *bytes = clip_workspace(count, numel);
+    return TT_EMB_OK;
+}
+
+int tt_emb_clip_norm(int32_t count, const void *const *grads, const int32_t *dtypes, const int64_t *numel,
+                     double max_norm, double eps, float *norm, float *factor, void *ws, size_t ws_bytes, void *stream)
+{
+    return clip(count, const_cast<void *const *>(grads), dtypes, numel, max_norm, eps, norm, factor, false, ws,
+                ws_bytes, stream);
+}
+
+int tt_emb_clip_scale(int32_t count, void *const *grads, const int32_t *dtypes, const int64_t *numel,
+                      double max_norm, double eps, float *norm, float *factor, void *ws, size_t ws_bytes, void *stream)
+{
+    return clip(count, grads, dtypes, numel, max_norm, eps, norm, factor, true, ws, ws_bytes, stream);
 }
 
 } // extern "C"

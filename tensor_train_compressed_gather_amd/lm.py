@@ -1,6 +1,6 @@
 """Operators around the table, from token ids to the update of the weights:
 embedding lookup with its gradient, layer norm, softmax cross entropy over a
-large vocabulary and AdamW (C ABI in ``include/tt_emb.h``).
+large vocabulary, the gradients' global norm and AdamW (C ABI in ``include/tt_emb.h``).
 
 The classes marshal arguments only: they check what the library cannot see
 from raw pointers, allocate outputs on the stream the work runs on, and keep
@@ -22,7 +22,8 @@ LM_EXPORTED = (
     "tt_emb_lookup_forward", "tt_emb_lookup_backward", "tt_emb_lookup_workspace_size",
     "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_norm_workspace_size",
     "tt_emb_xent_forward", "tt_emb_xent_loss_grad", "tt_emb_xent_workspace_size", "tt_emb_xent_parts",
-    "tt_emb_adamw_update", "tt_emb_adamw_state_size",
+    "tt_emb_adamw_update", "tt_emb_adamw_update_scaled", "tt_emb_adamw_state_size",
+    "tt_emb_clip_norm", "tt_emb_clip_scale", "tt_emb_clip_workspace_size",
 )
 
 
@@ -44,6 +45,11 @@ def declare(L):
     L.tt_emb_xent_workspace_size.argtypes = [i64, i64, i64, i32, i32, sizes, sizes]
     L.tt_emb_xent_parts.argtypes = [i64, i64, i64, i32, i32, size, p, i64, C.POINTER(i64), C.POINTER(i32)]
     L.tt_emb_adamw_update.argtypes = [i32, p, p, i32, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64, p]
+    L.tt_emb_adamw_update_scaled.argtypes = [i32, p, p, i32, p, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64,
+                                             p]
+    L.tt_emb_clip_norm.argtypes = [i32, p, p, p, f64, f64, p, p, p, size, p]
+    L.tt_emb_clip_scale.argtypes = [i32, p, p, p, f64, f64, p, p, p, size, p]
+    L.tt_emb_clip_workspace_size.argtypes = [i32, p, sizes]
     L.tt_emb_adamw_state_size.argtypes = [i32, p, C.POINTER(i64)]
 
 
@@ -551,9 +557,10 @@ class AdamW:
             self.exp_avg_sq_scale.copy_(exp_avg_sq_scale)
         self.steps = int(steps)
 
-    def step(self, grads, lr: float | None = None, stream=None):
+    def step(self, grads, lr: float | None = None, stream=None, grad_scale=None):
         """One update from gradients shaped like the parameters (all of one
-        type: fp32, bf16 or fp16)."""
+        type: fp32, bf16 or fp16), times ``grad_scale`` where it is given: an
+        fp32 tensor of one element, such as GradientClip.norm's factor."""
         where = "AdamW.step"
         grads = list(grads)
         n = len(self._shapes)
@@ -566,6 +573,11 @@ class AdamW:
         self._whole(self.params, "params", torch.float32)
         if self.copies is not None:
             self._whole(self.copies, "copies", torch.bfloat16)
+        if grad_scale is not None:
+            if not isinstance(grad_scale, torch.Tensor) or grad_scale.dtype is not torch.float32 \
+                    or grad_scale.numel() != 1:
+                raise _bad(where, "grad_scale: expected an fp32 tensor of one element")
+            _on(grad_scale, where, "grad_scale", self.device)
         array, address = self._array, torch.Tensor.data_ptr
         params = array(*map(address, self.params))
         pointers = array(*map(address, grads))
@@ -573,12 +585,69 @@ class AdamW:
         guard = _guard(self.device, stream, where)
         if guard is not None:
             with guard:
-                return self.step(grads, lr)
+                return self.step(grads, lr, None, grad_scale)
         s = _raw_stream(self.device.index)
-        _check(_L.tt_emb_adamw_update(
-            n, params, pointers, dt, copies, self._numel, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
+        _check(_L.tt_emb_adamw_update_scaled(
+            n, params, pointers, dt, None if grad_scale is None else grad_scale.data_ptr(), copies, self._numel, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
             None if self.exp_avg_scale is None else self.exp_avg_scale.data_ptr(),
             None if self.exp_avg_sq_scale is None else self.exp_avg_sq_scale.data_ptr(), self.state_bits,
             self.lr if lr is None else float(lr), self.betas[0], self.betas[1], self.eps, self.weight_decay,
             self.steps + 1, self.seed & 0xFFFFFFFFFFFFFFFF, s), where)
         self.steps += 1
+
+
+class GradientClip(_Operator):
+    """The global norm N of the gradients of many tensors, and their bound.
+
+    norm(grads) -> (N, factor), fp32 tensors of one element, for
+    factor = min(1, max_norm / (N + eps)): AdamW.step(grads, grad_scale=factor)
+    takes the bound without another pass over the gradients.
+    clip(grads) -> N multiplies the gradients by the factor in place (they are
+    not written where it is 1).
+
+    Gradients are contiguous and fp32, bf16 or fp16, mixed as they come; their
+    squares are added in fp64, in an order that depends on the sizes alone.  A
+    NaN makes N and the factor NaN; an infinity makes N infinite and the factor
+    0 (NaN where it meets the infinity)."""
+
+    def __init__(self, max_norm: float, eps: float = 1e-6, device="cuda"):
+        super().__init__(device)
+        self.max_norm, self.eps = float(max_norm), float(eps)
+        if not self.max_norm >= 0 or not 0 <= self.eps < float("inf"):
+            raise _bad("GradientClip", f"max_norm {max_norm}, eps {eps}: expected max_norm >= 0 and a finite eps >= 0")
+
+    def _call(self, fn, where, grads, max_norm, stream):
+        grads = list(grads)
+        n = len(grads)
+        if not n:
+            raise _bad(where, "no gradients")
+        max_norm = self.max_norm if max_norm is None else float(max_norm)
+        tensor, kinds, device = torch.Tensor, [], getattr(grads[0], "device", None)
+        for i, g in enumerate(grads):
+            if not isinstance(g, tensor):
+                raise _bad(where, f"grads[{i}]: expected a torch tensor, got {type(g).__name__}")
+            kinds.append(_DTYPES.get(g.dtype, -1))
+            if kinds[i] < 0:
+                _dtype(g, where, f"grads[{i}]")
+            if not g.is_contiguous():
+                raise _bad(where, f"grads[{i}]: not contiguous")
+            if not g.is_cuda or g.device != device:
+                _on(g, where, f"grads[{i}]", device)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self._call(fn, where, grads, max_norm, None)
+        numel = (C.c_int64 * n)(*map(tensor.numel, grads))
+        need = _size(_L.tt_emb_clip_workspace_size, where, n, numel)
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        factor = torch.empty((), dtype=torch.float32, device=device)
+        self._run(fn, where, device, _raw_stream(device.index), need, n,
+                  (C.c_void_p * n)(*map(tensor.data_ptr, grads)), (C.c_int32 * n)(*kinds), numel, max_norm, self.eps,
+                  norm.data_ptr(), factor.data_ptr())
+        return norm, factor
+
+    def norm(self, grads, max_norm: float | None = None, stream=None):
+        return self._call(_L.tt_emb_clip_norm, "GradientClip.norm", grads, max_norm, stream)
+
+    def clip(self, grads, max_norm: float | None = None, stream=None):
+        return self._call(_L.tt_emb_clip_scale, "GradientClip.clip", grads, max_norm, stream)[0]
