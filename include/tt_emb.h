@@ -418,6 +418,46 @@ int tt_emb_norm_backward(const void *grad_y, int64_t ld_grad, const void *x, int
                          size_t ws_bytes, void *stream);
 int tt_emb_norm_workspace_size(int64_t n, int64_t D, size_t *bytes);
 
+/* What stands between two blocks of a model: the norm of a block's output x, its
+ * gate and scale, the residual sum h, and the norm before the next block:
+ *   u = N(x) post_gamma + post_beta  (TT_EMB_BLOCK_POST; else u = x)
+ *   h = residual_scale residual + block_scale gate u
+ *   y = N(h) gamma + beta
+ * N(v) = (v - mean) rstd as above, or with TT_EMB_BLOCK_RMS v rstd for
+ * rstd = 1 / sqrt(sum_j v_j^2 / D + eps), which has no betas.  D <= 16384.
+ * x, y [n][D] of `dtype`; residual, h [n][D] of `residual_dtype` (dtype or fp32);
+ * gammas and betas [D] of `param_dtype` (dtype or fp32), each may be NULL (1 and
+ * 0); gate [D] of param_dtype, or with TT_EMB_BLOCK_GATE_ROWS [n][D] of dtype;
+ * NULL: 1 (ld_gate is that of rows).  y and the statistics are those of h before
+ * it is rounded.  stats fp32 [n][4]: mean and rstd of x (0 and 1 without POST), mean
+ * and rstd of h (a mean is 0 with RMS); may be NULL.  h may be residual and y may be
+ * x, with the same ld. */
+enum { TT_EMB_BLOCK_RMS = 1, TT_EMB_BLOCK_POST = 2, TT_EMB_BLOCK_GATE_ROWS = 4 };
+int tt_emb_block_forward(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n,
+                         int64_t D, int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
+                         const void *post_gamma, const void *post_beta, const void *gamma, const void *beta,
+                         int32_t param_dtype, int32_t kind, float eps, float residual_scale, float block_scale,
+                         void *y, int64_t ld_y, void *h, int64_t ld_h, float *stats, void *stream);
+
+/* Its gradients, from those of y (grad_y, of dtype) and of h (grad_h, of
+ * residual_dtype, NULL: 0), with J the Jacobian of N as in tt_emb_norm_backward:
+ *   dh = grad_h + J_h (grad_y gamma),  grad_residual = residual_scale dh
+ *   du = block_scale gate dh,  grad_x = J_x (du post_gamma)  (or du)
+ *   grad_gate = block_scale u dh, for a gate [D] its sum over the rows
+ *   dgamma = sum_i grad_y N(h), dbeta = sum_i grad_y, dpost_gamma = sum_i du N(x), dpost_beta = sum_i du
+ * h is made again from x and residual, in fp32.  Sums over the rows are fp32 in a
+ * fixed order, of param_dtype, overwritten, each may be NULL (so may a grad_gate [D]).
+ * What is written may not share memory with what is read. */
+int tt_emb_block_backward(const void *grad_y, int64_t ld_grad_y, const void *grad_h, int64_t ld_grad_h, const void *x,
+                          int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n, int64_t D,
+                          int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
+                          const void *post_gamma, const void *post_beta, const void *gamma, int32_t param_dtype,
+                          int32_t kind, float residual_scale, float block_scale, const float *stats, void *grad_x,
+                          int64_t ld_grad_x, void *grad_residual, int64_t ld_grad_residual, void *grad_gate,
+                          int64_t ld_grad_gate, void *dpost_gamma, void *dpost_beta, void *dgamma, void *dbeta,
+                          void *ws, size_t ws_bytes, void *stream);
+int tt_emb_block_workspace_size(int64_t n, int64_t D, size_t *bytes);
+
 /* Softmax cross entropy of n hidden rows against a vocabulary of V rows:
  *   z_iv = hidden_i . weight_v,  lse_i = log sum_v exp(z_iv)
  *   loss_i = lse_i - z_{i,target_i}, or 0 where target_i = ignore_index

@@ -1,5 +1,5 @@
 // lm.h -- shared definitions of the operators around the table (lookup, norm,
-// xent, adamw, clip): element types, vector access, block reductions, launchers.
+// blocknorm, xent, adamw, clip): element types, vector access, block reductions, launchers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -149,6 +149,29 @@ struct NormArgs {
 hipError_t launch_norm_forward(const NormArgs &a, int dtype, hipStream_t s);
 hipError_t launch_norm_backward(const NormArgs &a, int dtype, hipStream_t s);
 size_t norm_workspace(int64_t n, int64_t D);
+
+struct BlockNormArgs {
+    const void *x, *residual, *gate; // gate: [D] of param_dtype, or rows of x's type
+    int64_t ld_x, ld_r, ld_gate, n, D;
+    int gate_rows, layer, post;
+    const void *gamma, *beta, *post_gamma, *post_beta;
+    int param_dtype;
+    float eps, scale_residual, scale_block;
+    float *stats;                    // [n][4] mean and rstd of x, of h
+    void *y, *h;                     // forward
+    int64_t ld_y, ld_h;
+    const void *grad_y, *grad_h;     // backward
+    int64_t ld_gy, ld_gh;
+    void *grad_x, *grad_r, *grad_gate;
+    int64_t ld_gx, ld_gr, ld_gg;
+    void *sums[5];                   // dgamma, dbeta, dpost_gamma, dpost_beta, dgate [D]; null for none
+    char *ws;
+};
+hipError_t launch_block_forward(const BlockNormArgs &a, int dtype, int res_dtype, hipStream_t s);
+hipError_t launch_block_backward(const BlockNormArgs &a, int dtype, int res_dtype, hipStream_t s);
+size_t block_workspace(int64_t n, int64_t D);
+size_t block_parts_bytes(int64_t n, int64_t D);
+int block_col_parts(int64_t n, int64_t D);
 
 struct XentArgs {
     const void *hidden, *weight;

@@ -1,5 +1,5 @@
 // lm_api.hip -- host side of the operators around the table (lookup, norm,
-// xent, adamw, clip): argument checks before anything is enqueued, then the
+// blocknorm, xent, adamw, clip): argument checks before anything is enqueued, then the
 // stream-ordered launches.  Nothing here allocates device memory, and no exception
 // leaves.
 #include <algorithm>
@@ -56,6 +56,55 @@ int check_xent(int64_t n, int64_t V, int64_t D, int32_t dtype)
     if (n > kMaxRows || V > kMaxRows || D > kMaxXentCols) return TT_EMB_ERR_UNSUPPORTED;
     // tiles of the logits: the blocks of one launch stay below 2^24
     if (((n + 127) / 128) * ((V + 127) / 128) > kMaxXentTiles) return TT_EMB_ERR_UNSUPPORTED;
+    return TT_EMB_OK;
+}
+
+int check_block(int64_t n, int64_t D, int32_t dtype, int32_t residual_dtype, int32_t param_dtype, int32_t kind)
+{
+    const int rc = check_norm(n, D, dtype, param_dtype);
+    if (rc) return rc;
+    if (residual_dtype != TT_EMB_DTYPE_FLOAT && residual_dtype != dtype) return TT_EMB_ERR_ARG;
+    if ((kind & ~(TT_EMB_BLOCK_RMS | TT_EMB_BLOCK_POST | TT_EMB_BLOCK_GATE_ROWS)) != 0) return TT_EMB_ERR_ARG;
+    return TT_EMB_OK;
+}
+
+// What both directions read, and its checks.
+int block_args(BlockNormArgs &a, const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n,
+               int64_t D, int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
+               const void *post_gamma, const void *post_beta, const void *gamma, const void *beta,
+               int32_t param_dtype, int32_t kind, float residual_scale, float block_scale)
+{
+    const int rc = check_block(n, D, dtype, residual_dtype, param_dtype, kind);
+    if (rc) return rc;
+    if (bad_matrix(x, ld_x, n, D, dtype) || bad_matrix(residual, ld_residual, n, D, residual_dtype))
+        return TT_EMB_ERR_ARG;
+    for (const void *p : {post_gamma, post_beta, gamma, beta})
+        if (off_grid(p, param_dtype)) return TT_EMB_ERR_ARG;
+    if ((kind & TT_EMB_BLOCK_RMS) && (beta || post_beta)) return TT_EMB_ERR_ARG;
+    if (!(kind & TT_EMB_BLOCK_POST) && (post_gamma || post_beta)) return TT_EMB_ERR_ARG;
+    if (kind & TT_EMB_BLOCK_GATE_ROWS) {
+        if (bad_matrix(gate, ld_gate, n, D, dtype)) return TT_EMB_ERR_ARG;
+    } else if (off_grid(gate, param_dtype)) {
+        return TT_EMB_ERR_ARG;
+    }
+    a.x = x;
+    a.residual = residual;
+    a.gate = gate;
+    a.ld_x = ld_x;
+    a.ld_r = ld_residual;
+    a.ld_gate = ld_gate;
+    a.n = n;
+    a.D = D;
+    a.gate_rows = (kind & TT_EMB_BLOCK_GATE_ROWS) != 0;
+    a.layer = !(kind & TT_EMB_BLOCK_RMS);
+    a.post = (kind & TT_EMB_BLOCK_POST) != 0;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.post_gamma = post_gamma;
+    a.post_beta = post_beta;
+    a.param_dtype = param_dtype;
+    a.scale_residual = residual_scale;
+    a.scale_block = block_scale;
     return TT_EMB_OK;
 }
 
@@ -257,6 +306,80 @@ int tt_emb_norm_backward(const void *grad_y, int64_t ld_grad, const void *x, int
     a.dbeta = dbeta;
     a.ws = static_cast<char *>(ws);
     return hip_status(launch_norm_backward(a, dtype, (hipStream_t)stream));
+}
+
+int tt_emb_block_workspace_size(int64_t n, int64_t D, size_t *bytes)
+{
+    if (!bytes) return TT_EMB_ERR_ARG;
+    const int rc = check_norm(n, D, TT_EMB_DTYPE_FLOAT, TT_EMB_DTYPE_FLOAT);
+    if (rc) return rc;
+    *bytes = block_workspace(n, D);
+    return TT_EMB_OK;
+}
+
+int tt_emb_block_forward(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n,
+                         int64_t D, int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
+                         const void *post_gamma, const void *post_beta, const void *gamma, const void *beta,
+                         int32_t param_dtype, int32_t kind, float eps, float residual_scale, float block_scale,
+                         void *y, int64_t ld_y, void *h, int64_t ld_h, float *stats, void *stream)
+{
+    BlockNormArgs a{};
+    const int rc = block_args(a, x, ld_x, residual, ld_residual, n, D, dtype, residual_dtype, gate, ld_gate, post_gamma,
+                              post_beta, gamma, beta, param_dtype, kind, residual_scale, block_scale);
+    if (rc) return rc;
+    if (bad_matrix(y, ld_y, n, D, dtype) || bad_matrix(h, ld_h, n, D, residual_dtype) || !(eps >= 0.f) ||
+        off_grid(stats, TT_EMB_DTYPE_FLOAT))
+        return TT_EMB_ERR_ARG;
+    a.eps = eps;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.h = h;
+    a.ld_h = ld_h;
+    a.stats = stats;
+    return hip_status(launch_block_forward(a, dtype, residual_dtype, (hipStream_t)stream));
+}
+
+int tt_emb_block_backward(const void *grad_y, int64_t ld_grad_y, const void *grad_h, int64_t ld_grad_h, const void *x,
+                          int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n, int64_t D,
+                          int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
+                          const void *post_gamma, const void *post_beta, const void *gamma, int32_t param_dtype,
+                          int32_t kind, float residual_scale, float block_scale, const float *stats, void *grad_x,
+                          int64_t ld_grad_x, void *grad_residual, int64_t ld_grad_residual, void *grad_gate,
+                          int64_t ld_grad_gate, void *dpost_gamma, void *dpost_beta, void *dgamma, void *dbeta,
+                          void *ws, size_t ws_bytes, void *stream)
+{
+    BlockNormArgs a{};
+    int rc = block_args(a, x, ld_x, residual, ld_residual, n, D, dtype, residual_dtype, gate, ld_gate, post_gamma,
+                        post_beta, gamma, nullptr, param_dtype, kind, residual_scale, block_scale);
+    if (rc) return rc;
+    if (bad_matrix(grad_y, ld_grad_y, n, D, dtype) || (grad_h && bad_matrix(grad_h, ld_grad_h, n, D, residual_dtype)) ||
+        bad_matrix(grad_x, ld_grad_x, n, D, dtype) || bad_matrix(grad_residual, ld_grad_residual, n, D, residual_dtype) ||
+        (n > 0 && (!stats || off_grid(stats, TT_EMB_DTYPE_FLOAT))))
+        return TT_EMB_ERR_ARG;
+    if (a.gate_rows ? bad_matrix(grad_gate, ld_grad_gate, n, D, dtype) : off_grid(grad_gate, param_dtype))
+        return TT_EMB_ERR_ARG;
+    for (const void *p : {dpost_gamma, dpost_beta, dgamma, dbeta})
+        if (off_grid(p, param_dtype)) return TT_EMB_ERR_ARG;
+    if (!a.post && (dpost_gamma || dpost_beta)) return TT_EMB_ERR_ARG;
+    if ((rc = check_ws(ws, ws_bytes, block_workspace(n, D)))) return rc;
+    a.grad_y = grad_y;
+    a.ld_gy = ld_grad_y;
+    a.grad_h = grad_h;
+    a.ld_gh = ld_grad_h;
+    a.stats = const_cast<float *>(stats);
+    a.grad_x = grad_x;
+    a.ld_gx = ld_grad_x;
+    a.grad_r = grad_residual;
+    a.ld_gr = ld_grad_residual;
+    a.grad_gate = a.gate_rows ? grad_gate : nullptr;
+    a.ld_gg = ld_grad_gate;
+    a.sums[0] = dgamma;
+    a.sums[1] = dbeta;
+    a.sums[2] = dpost_gamma;
+    a.sums[3] = dpost_beta;
+    a.sums[4] = a.gate_rows ? nullptr : grad_gate;
+    a.ws = static_cast<char *>(ws);
+    return hip_status(launch_block_backward(a, dtype, residual_dtype, (hipStream_t)stream));
 }
 
 int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t what, size_t *bytes,

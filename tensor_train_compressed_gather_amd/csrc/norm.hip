@@ -10,7 +10,7 @@
 // Memory bounds it: 16384 rows of 4096 bf16 in 49 us forward (268 MB, 5.5 TB/s)
 // and 87 backward (403 MB), 32768 rows of 128 fp32 in 10 and 15 us; 4 rows cost a
 // launch, 4 us.
-#include "lm.h"
+#include "norm.h"
 #include "primitives.h"
 
 namespace ttemb {
@@ -24,40 +24,6 @@ constexpr int kNormBlocks = 5 * kCUs;      // forward: blocks at most, all of th
 constexpr int kNormGradBlocks = 4 * kCUs;
 template <int TPR>
 constexpr int norm_grad_blocks() { return TPR >= 256 ? 2 * kCUs : kNormGradBlocks; }
-
-template <int TPR>
-struct NormShape {
-    static constexpr int threads = TPR > 256 ? TPR : 256;
-    static constexpr int rows = threads / TPR; // rows a block holds at a time
-};
-
-// Sum over the TPR threads of a row of K values each.  TPR <= 64: shuffles
-// inside the wave.  Larger rows own the block: wave sums meet in LDS, in one
-// of two slots in turn, so one barrier per reduction is enough.
-template <int TPR, int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float (*sm)[16][2], int &slot)
-{
-    constexpr int W = TPR < 64 ? TPR : 64;
-#pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], o, 64);
-    if constexpr (TPR > 64) {
-        constexpr int NW = TPR / 64;
-        if ((threadIdx.x & 63) == 0)
-#pragma unroll
-            for (int k = 0; k < K; ++k) sm[slot][threadIdx.x >> 6][k] = v[k];
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) s += sm[slot][w][k];
-            v[k] = s;
-        }
-        slot ^= 1;
-    }
-}
 
 // The next row is on its way while this one is reduced.
 template <class T, int TPR, int NV, bool WHOLE>
@@ -272,68 +238,6 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_norm_bwd(NormArgs a
     }
 }
 
-// Column sums of the blocks' partials: 64 columns per block, four per lane, 64
-// groups of rows; the four groups of a wave meet in shuffles, the waves in LDS,
-// always in the same order.
-template <bool WHOLE>
-__global__ __launch_bounds__(1024) void k_norm_cols(const float *part, int blocks, int D, void *dgamma, void *dbeta,
-                                                    int param_dtype)
-{
-    __shared__ float sm[16][64];
-    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane * 4;
-    const float *p = part + (int64_t)blockIdx.y * blocks * D;
-    void *dst = blockIdx.y ? dbeta : dgamma;
-    if (!dst) return;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int b = grp; b < blocks; b += 64) {
-        const VecOf<float, 4>::raw v = load_row<float, 4, WHOLE>(p + (int64_t)b * D, c, D);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += v[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        s[i] += __shfl_xor(s[i], 16, 64);
-        s[i] += __shfl_xor(s[i], 32, 64);
-        if ((threadIdx.x & 63) < 16) sm[wave][lane * 4 + i] = s[i];
-    }
-    __syncthreads();
-    const int col = blockIdx.x * 64 + threadIdx.x;
-    if (threadIdx.x < 64 && col < D) {
-        float t = 0.f;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) t += sm[w][threadIdx.x];
-        store_param(dst, param_dtype, col, t);
-    }
-}
-
-// Threads per row and vectors per thread: the fewest threads that hold a row
-// of nv vectors with at most 16 elements each (80 registers in the backward).
-template <class T, class F>
-hipError_t norm_shape(int64_t D, F &&g)
-{
-    auto f = [&](auto tpr, auto nv) {
-        if (D % (16 / (int)sizeof(T)) == 0) return g(tpr, nv, std::true_type());
-        return g(tpr, nv, std::false_type());
-    };
-    constexpr int VEC = 16 / (int)sizeof(T), MAX = 16 / VEC;
-    const int64_t nv = (D + VEC - 1) / VEC;
-    auto one = [&](auto tpr) {
-        constexpr int TPR = decltype(tpr)::value;
-        if constexpr (MAX == 4) {
-            if (nv > 2 * TPR) return f(tpr, std::integral_constant<int, 4>());
-        }
-        if (nv > TPR) return f(tpr, std::integral_constant<int, 2>());
-        return f(tpr, std::integral_constant<int, 1>());
-    };
-    if (nv <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-    if (nv <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-    if (nv <= 64 * MAX) return one(std::integral_constant<int, 64>());
-    if (nv <= 256 * MAX) return one(std::integral_constant<int, 256>());
-    return one(std::integral_constant<int, 1024>());
-}
-
 template <class T>
 hipError_t norm_forward(const NormArgs &a, hipStream_t s)
 {
@@ -358,13 +262,8 @@ hipError_t norm_backward(const NormArgs &a, hipStream_t s)
         hipLaunchKernelGGL((k_norm_bwd<T, TPR, NV, decltype(whole)::value>), dim3(grid),
                            dim3(NormShape<TPR>::threads), 0, s, a, part);
         if (part) {
-            const dim3 cols((unsigned)((a.D + 63) / 64), 2);
-            if (a.D % 4 == 0)
-                hipLaunchKernelGGL(k_norm_cols<true>, cols, dim3(1024), 0, s, part, grid, (int)a.D, a.dgamma, a.dbeta,
-                                   a.param_dtype);
-            else
-                hipLaunchKernelGGL(k_norm_cols<false>, cols, dim3(1024), 0, s, part, grid, (int)a.D, a.dgamma, a.dbeta,
-                                   a.param_dtype);
+            const ColumnSums sums{{a.dgamma, a.dbeta}, {a.param_dtype, a.param_dtype}};
+            norm_cols(part, grid, a.D, 2, sums, s);
         }
         return hipGetLastError();
     });

@@ -1,5 +1,6 @@
 """Operators around the table, from token ids to the update of the weights:
-embedding lookup with its gradient, layer norm, softmax cross entropy over a
+embedding lookup with its gradient, layer norm, the norms between two blocks
+with gate and residual, softmax cross entropy over a
 large vocabulary, the gradients' global norm and AdamW (C ABI in ``include/tt_emb.h``).
 
 The classes marshal arguments only: they check what the library cannot see
@@ -16,11 +17,13 @@ import threading
 TT_EMB_DTYPE_FLOAT, TT_EMB_DTYPE_BFLOAT, TT_EMB_DTYPE_HALF = 0, 1, 2
 TT_EMB_STATUS_BYTES = 256
 TT_EMB_XENT_GRAD, TT_EMB_XENT_ALIGNED = 1, 2
+TT_EMB_BLOCK_RMS, TT_EMB_BLOCK_POST, TT_EMB_BLOCK_GATE_ROWS = 1, 2, 4
 
 LM_EXPORTED = (
     "tt_emb_poll_status",
     "tt_emb_lookup_forward", "tt_emb_lookup_backward", "tt_emb_lookup_workspace_size",
     "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_norm_workspace_size",
+    "tt_emb_block_forward", "tt_emb_block_backward", "tt_emb_block_workspace_size",
     "tt_emb_xent_forward", "tt_emb_xent_loss_grad", "tt_emb_xent_workspace_size", "tt_emb_xent_parts",
     "tt_emb_adamw_update", "tt_emb_adamw_update_scaled", "tt_emb_adamw_state_size",
     "tt_emb_clip_norm", "tt_emb_clip_scale", "tt_emb_clip_workspace_size",
@@ -39,6 +42,11 @@ def declare(L):
     L.tt_emb_norm_forward.argtypes = [p, i64, i64, i64, i32, p, p, i32, f32, p, i64, p, p, p]
     L.tt_emb_norm_backward.argtypes = [p, i64, p, i64, i64, i64, i32, p, i32, p, p, p, i64, p, p, p, size, p]
     L.tt_emb_norm_workspace_size.argtypes = [i64, i64, sizes]
+    L.tt_emb_block_forward.argtypes = [p, i64, p, i64, i64, i64, i32, i32, p, i64, p, p, p, p, i32, i32, f32, f32, f32,
+                                       p, i64, p, i64, p, p]
+    L.tt_emb_block_backward.argtypes = [p, i64, p, i64, p, i64, p, i64, i64, i64, i32, i32, p, i64, p, p, p, i32, i32,
+                                        f32, f32, p, p, i64, p, i64, p, i64, p, p, p, p, p, size, p]
+    L.tt_emb_block_workspace_size.argtypes = [i64, i64, sizes]
     L.tt_emb_xent_forward.argtypes = [p, i64, p, i64, p, i64, i64, i64, i32, i64, p, p, p, size, p]
     L.tt_emb_xent_loss_grad.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i32, i64, p, p, p, i64, p, i64, p, size,
                                         p]
@@ -127,6 +135,10 @@ def _on(t, where: str, name: str, device):
         raise _bad(where, f"{name}: on {t.device}, expected a GPU tensor")
     if device is not None and t.device != device:
         raise _bad(where, f"{name}: on {t.device}, expected {device} like the others")
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _guard(device, stream, where: str):
@@ -359,6 +371,126 @@ class LayerNorm(_Operator):
                   self.D, dt, None if gamma is None else gamma.data_ptr(), pdt, mean.data_ptr(), rstd.data_ptr(),
                   dx.data_ptr(), self.D, dgamma.data_ptr(), dbeta.data_ptr())
         return dx, dgamma, dbeta
+
+
+class BlockNorm(_Operator):
+    """What stands between two blocks, over rows of D elements:
+
+        u = N(x) post_gamma + post_beta  (``post``; else u = x)
+        h = residual_scale * residual + block_scale * gate * u
+        y = N(h) gamma + beta
+
+    for a block's output x and the residual stream.  N is the division by the
+    root of the mean square (``kind`` "rms", no betas) or the layer norm
+    ("layer").
+
+    forward(x, residual, gate, gamma, beta, post_gamma, post_beta) -> (y, h,
+    stats): y of x's type, h of the residual's (x's type or fp32), stats fp32
+    [n, 4] for the backward.  gammas and betas [D] (x's type or fp32, all of
+    one) may be None; gate is None, [D] of their type, or [n, D] of x's.
+    ``out`` may be x and ``out_h`` the residual itself.
+    backward(grad_y, grad_h, x, residual, stats, gate, gamma, post_gamma,
+    post_beta) -> (grad_x, grad_residual, grad_gate, dgamma, dbeta,
+    dpost_gamma, dpost_beta), None where there is no such parameter (without a
+    gamma its gradient is still given, in fp32); grad_h may be None."""
+
+    def __init__(self, D: int, kind: str = "rms", post: bool = False, eps: float = 1e-5, residual_scale: float = 1.0,
+                 block_scale: float = 1.0, device="cuda"):
+        super().__init__(device)
+        if kind not in ("rms", "layer"):
+            raise _bad("BlockNorm", f"kind {kind!r}, expected 'rms' or 'layer'")
+        self.D, self.layer, self.post, self.eps = int(D), kind == "layer", bool(post), float(eps)
+        self.residual_scale, self.block_scale = float(residual_scale), float(block_scale)
+        self._kind = (0 if self.layer else TT_EMB_BLOCK_RMS) | (TT_EMB_BLOCK_POST if self.post else 0)
+        _size(_L.tt_emb_block_workspace_size, "BlockNorm", 0, self.D)
+
+    def _inputs(self, x, residual, gate, params, where):
+        ld_x = _matrix(x, where, "x", self.D)
+        dt = _dtype(x, where, "x")
+        n, device = x.shape[0], x.device
+        ld_r = _matrix(residual, where, "residual", self.D, n, None, device)
+        rdt = _dtype(residual, where, "residual")
+        if rdt not in (0, dt):
+            raise _bad(where, f"residual: dtype {residual.dtype}, expected {x.dtype} or {torch.float32}")
+        kinds, dtype = (torch.float32, x.dtype), None
+        for name, p in params:
+            if p is None:
+                continue
+            if "beta" in name and not self.layer:
+                raise _bad(where, f"{name}: the root mean square has no beta")
+            if "post" in name and not self.post:
+                raise _bad(where, f"{name}: there is no norm of the block's output")
+            _vector(p, where, name, self.D, kinds, device)
+            if dtype is not None and p.dtype != dtype:
+                raise _bad(where, f"{name}: dtype {p.dtype}, expected {dtype} like the other parameters")
+            dtype = p.dtype
+        kind, ld_g = self._kind, 0
+        if gate is not None:
+            if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+                ld_g = _matrix(gate, where, "gate", self.D, n, x.dtype, device)
+                kind |= TT_EMB_BLOCK_GATE_ROWS
+            else:
+                _vector(gate, where, "gate", self.D, kinds if dtype is None else (dtype,), device)
+                dtype = gate.dtype
+        return ld_x, ld_r, ld_g, dt, rdt, n, device, dtype, kind
+
+    def forward(self, x, residual, gate=None, gamma=None, beta=None, post_gamma=None, post_beta=None, out=None,
+                out_h=None, stream=None):
+        where = "BlockNorm.forward"
+        params = (("gamma", gamma), ("beta", beta), ("post_gamma", post_gamma), ("post_beta", post_beta))
+        ld_x, ld_r, ld_g, dt, rdt, n, device, dtype, kind = self._inputs(x, residual, gate, params, where)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.forward(x, residual, gate, gamma, beta, post_gamma, post_beta, out, out_h)
+        if out is None:
+            out, ld_y = x.new_empty((n, self.D)), self.D
+        else:
+            ld_y = _matrix(out, where, "out", self.D, n, x.dtype, device)
+        if out_h is None:
+            out_h, ld_h = residual.new_empty((n, self.D)), self.D
+        else:
+            ld_h = _matrix(out_h, where, "out_h", self.D, n, residual.dtype, device)
+        stats = torch.empty((n, 4), dtype=torch.float32, device=device)
+        _check(_L.tt_emb_block_forward(
+            x.data_ptr(), ld_x, residual.data_ptr(), ld_r, n, self.D, dt, rdt, _address(gate), ld_g,
+            _address(post_gamma), _address(post_beta), _address(gamma), _address(beta), _DTYPES.get(dtype, 0), kind,
+            self.eps, self.residual_scale, self.block_scale, out.data_ptr(), ld_y, out_h.data_ptr(), ld_h,
+            stats.data_ptr(), _raw_stream(device.index)), where)
+        return out, out_h, stats
+
+    def backward(self, grad_y, grad_h, x, residual, stats, gate=None, gamma=None, post_gamma=None, post_beta=None,
+                 stream=None):
+        where = "BlockNorm.backward"
+        params = (("gamma", gamma), ("post_gamma", post_gamma), ("post_beta", post_beta))
+        ld_x, ld_r, ld_g, dt, rdt, n, device, dtype, kind = self._inputs(x, residual, gate, params, where)
+        ld_gy = _matrix(grad_y, where, "grad_y", self.D, n, x.dtype, device)
+        ld_gh = 0 if grad_h is None else _matrix(grad_h, where, "grad_h", self.D, n, residual.dtype, device)
+        _matrix(stats, where, "stats", 4, n, torch.float32, device)
+        if not stats.is_contiguous():
+            raise _bad(where, "stats: not contiguous")
+        need = _size(_L.tt_emb_block_workspace_size, where, n, self.D)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.backward(grad_y, grad_h, x, residual, stats, gate, gamma, post_gamma, post_beta)
+        dx, dr = x.new_empty((n, self.D)), residual.new_empty((n, self.D))
+        dgate = None
+        if gate is not None:
+            dgate = x.new_empty((n, self.D)) if gate.dim() == 2 else torch.empty_like(gate)
+
+        def sums(wanted):
+            return torch.empty(self.D, dtype=dtype or torch.float32, device=device) if wanted else None
+
+        dgamma, dbeta = sums(True), sums(self.layer)
+        dpost_gamma, dpost_beta = sums(self.post), sums(self.post and self.layer)
+        self._run(_L.tt_emb_block_backward, where, device, _raw_stream(device.index), need, grad_y.data_ptr(), ld_gy,
+                  _address(grad_h), ld_gh, x.data_ptr(), ld_x, residual.data_ptr(), ld_r, n, self.D, dt, rdt,
+                  _address(gate), ld_g, _address(post_gamma), _address(post_beta), _address(gamma),
+                  _DTYPES.get(dtype, 0), kind, self.residual_scale, self.block_scale, stats.data_ptr(), dx.data_ptr(),
+                  self.D, dr.data_ptr(), self.D, _address(dgate), self.D, _address(dpost_gamma),
+                  _address(dpost_beta), _address(dgamma), _address(dbeta))
+        return dx, dr, dgate, dgamma, dbeta, dpost_gamma, dpost_beta
 
 
 class tt_emb_xent_part(C.Structure):
