@@ -458,6 +458,42 @@ int tt_emb_block_backward(const void *grad_y, int64_t ld_grad_y, const void *gra
                           void *ws, size_t ws_bytes, void *stream);
 int tt_emb_block_workspace_size(int64_t n, int64_t D, size_t *bytes);
 
+/* The gated feed-forward block:
+ *   p = x w_in^T [n][2F],  a_ij = act(p_ij) p_i,F+j,  y = a w_out^T
+ * x, y [n][D], w_in [2F][D] (the gate's F rows, then the other projection's),
+ * w_out [D][F], all of `dtype`; D, F <= 65536.  pre, fp32 [n][2F], receives p for the
+ * backward (NULL: not kept); rounded to 16 bits it would cost the gradients half
+ * of their error.  act: silu(z) = z sigmoid(z), gelu(z) = z Phi(z), or
+ * gelu's tanh form z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
+ * bf16 and fp16: sums are fp32, a is rounded to dtype (so in fp16 an |a| past 65504
+ * is infinite).  fp32: operands are taken as three bf16 terms, 24 bits; a NaN or an
+ * infinity in x or a weight makes what it takes part in NaN. */
+enum { TT_EMB_ACT_SILU = 0, TT_EMB_ACT_GELU = 1, TT_EMB_ACT_GELU_TANH = 2 };
+int tt_emb_ffn_forward(const void *x, int64_t ld_x, const void *w_in, int64_t ld_in, const void *w_out, int64_t ld_out,
+                       int64_t n, int64_t D, int64_t F, int32_t dtype, int32_t activation, float *pre, int64_t ld_pre,
+                       void *y, int64_t ld_y, void *ws, size_t ws_bytes, void *stream);
+
+/* Its gradients, from grad_y [n][D] and the forward's pre:
+ *   da = grad_y w_out,  dp_ij = da_ij p_i,F+j act'(p_ij),  dp_i,F+j = da_ij act(p_ij)
+ *   grad_x = dp w_in,  grad_w_in = dp^T x,  grad_w_out = grad_y^T a
+ * all of dtype, overwritten; dp and a are rounded like a in the forward.  Sums over
+ * the rows are taken in a fixed order (bit-reproducible).  What is written may not
+ * share memory with what is read. */
+int tt_emb_ffn_backward(const void *grad_y, int64_t ld_grad_y, const void *x, int64_t ld_x, const float *pre,
+                        int64_t ld_pre, const void *w_in, int64_t ld_in, const void *w_out, int64_t ld_out, int64_t n,
+                        int64_t D, int64_t F, int32_t dtype, int32_t activation, void *grad_x, int64_t ld_grad_x,
+                        void *grad_w_in, int64_t ld_grad_in, void *grad_w_out, int64_t ld_grad_out, void *ws,
+                        size_t ws_bytes, void *stream);
+/* Workspace of tt_emb_ffn_backward (what has TT_EMB_FFN_GRAD) or of
+ * tt_emb_ffn_forward.  With TT_EMB_FFN_ALIGNED the size is for x, w_in, w_out and
+ * grad_y whose first elements lie at multiples of 16 bytes and whose ld are
+ * multiples of 8 of at most 2^20: 16-bit operands whose rows have a multiple of 8
+ * columns (where they lie along a sum: of 64) are then read in place and need no
+ * room for copies.  The calls find out by themselves how their operands lie, and return
+ * TT_EMB_ERR_WORKSPACE where ws is too small for that. */
+enum { TT_EMB_FFN_GRAD = 1, TT_EMB_FFN_ALIGNED = 2 };
+int tt_emb_ffn_workspace_size(int64_t n, int64_t D, int64_t F, int32_t dtype, int32_t what, size_t *bytes);
+
 /* Softmax cross entropy of n hidden rows against a vocabulary of V rows:
  *   z_iv = hidden_i . weight_v,  lse_i = log sum_v exp(z_iv)
  *   loss_i = lse_i - z_{i,target_i}, or 0 where target_i = ignore_index

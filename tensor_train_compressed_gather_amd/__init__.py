@@ -14,8 +14,8 @@ import os
 import threading
 
 from . import lm as _lm
-from .lm import (LM_EXPORTED, AdamW, BlockNorm, GradientClip, LayerNorm, TokenEmbedding,  # noqa: F401
-                 VocabCrossEntropy, tt_emb_xent_parts)
+from .lm import (LM_EXPORTED, AdamW, BlockNorm, GatedFeedForward, GradientClip, LayerNorm,  # noqa: F401
+                 TokenEmbedding, VocabCrossEntropy, tt_emb_xent_parts)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # TT_EMB_LIB names another build of the same library (the host-sanitizer build

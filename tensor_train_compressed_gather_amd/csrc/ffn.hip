@@ -1,0 +1,707 @@
+// ffn.hip -- the gated feed-forward block, forward and backward (gfx950).
+//
+//   p = x W_in^T [n][2F] (the gate's F columns, then the other projection's)
+//   a = act(p_g) p_u,  y = a W_out^T
+//   da = gy W_out,  dp_g = da p_u act'(p_g),  dp_u = da act(p_g)
+//   dx = dp W_in,  dW_in = dp^T x,  dW_out = gy^T a
+//
+// Six products by the tiles of tiles.h.  A tile of the first has rows of the
+// gate and of the other projection in turn, 32 of each, so that both halves of
+// a value of `a` meet in one thread: p leaves the registers only where the
+// caller keeps it for the backward.  The backward's first product makes da, and
+// dp and a from it and p, in the tile that holds da.  Matrix instructions bound
+// the large sizes.
+//
+// bf16 and fp16: a and dp are rounded to the inputs' type, half a step each,
+// because the products that take them have operands of 16 bits; two terms of
+// them would double two thirds of the products.  Both are made from p before its
+// rounding in the forward, after it in the backward.
+//
+// fp32: every operand is split into three bf16 terms (24 bits, the range of
+// fp32), and the six products of terms above 2^-25 are added up: the rounding of
+// fp32 products, at 1 / 6 of the bf16 rate, where the fp32 matrix instructions
+// have 1 / 16 of it.
+#include "tiles.h"
+
+#include <utility>
+
+namespace ttemb {
+
+namespace {
+
+constexpr int64_t kPad = 64;       // summed values of packed rows are padded to this
+constexpr int64_t kSplit = 512;    // least summed values of a split
+constexpr int kPacks = 5;          // copies that one launch makes, at most
+
+template <class T>
+struct FfnTerms {
+    typedef T type;
+    static constexpr int planes = 1;
+};
+template <>
+struct FfnTerms<float> {
+    typedef bf16 type;
+    static constexpr int planes = 3;
+};
+
+// ------------------------------------------------------------- activations
+
+// The values of the activation at z, and its slopes.  gelu's tanh form is z times
+// the sigmoid of twice the argument, 2 sqrt(2 / pi) (z + 0.044715 z^3).
+__device__ __forceinline__ void activations(int act, const float (&z)[8], float (&value)[8], float (&slope)[8])
+{
+    if (act == TT_EMB_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float c = 0.5f * erfcf(-0.70710678f * z[i]); // (1 + erf would lose the small values)
+            value[i] = z[i] * c;
+            slope[i] = fmaf(z[i], 0.39894228f * expf(-0.5f * z[i] * z[i]), c);
+        }
+        return;
+    }
+    const float cube = act == TT_EMB_ACT_GELU_TANH ? 0.044715f : 0.f, by = cube ? 1.59576912f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float zz = cube * z[i] * z[i], x = by * fmaf(zz, z[i], z[i]), dx = by * fmaf(3.f, zz, 1.f);
+        const float e = expf(-fabsf(x)), r = 1.f / (1.f + e);
+        const float sg = x < 0.f ? e * r : r, other = x < 0.f ? r : e * r; // sigmoid of x and of -x
+        value[i] = z[i] * sg;
+        slope[i] = fmaf(z[i] * dx, sg * other, sg);
+    }
+}
+
+// ------------------------------------------------------------------ copies
+
+// A matrix as planes of 16-bit terms whose rows of `ld` columns are zero past
+// the source's.  pair > 0: the source has 2 x pair rows, and 32 of the first
+// half and 32 of the second follow each other; rows past them are zeros.  No
+// source: zeros.
+struct Pack {
+    const void *src;
+    int64_t ld_src, rows, cols;
+    short *dst;
+    int64_t width, ld, plane, pair; // width: columns that are written
+};
+struct Packs {
+    Pack job[kPacks];
+    int first[kPacks + 1]; // first block of each
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_pack(Packs p)
+{
+    typedef typename FfnTerms<T>::type E;
+    constexpr int PL = FfnTerms<T>::planes;
+    int k = 0;
+    while (k + 1 < kPacks && (int)blockIdx.x >= p.first[k + 1]) ++k;
+    const Pack &j = p.job[k];
+    const int64_t chunks = j.width / 8, all = j.rows * chunks, step = (int64_t)(p.first[k + 1] - p.first[k]) * 256;
+    for (int64_t c = (int64_t)((int)blockIdx.x - p.first[k]) * 256 + threadIdx.x; c < all; c += step) {
+        const int64_t q = c / chunks, col = (c - q * chunks) * 8;
+        int64_t r = q;
+        bool in = true;
+        if (j.pair) {
+            const int64_t f = q / 64 * 32 + q % 32;
+            in = f < j.pair;
+            r = in ? f + (q & 32 ? j.pair : 0) : 0;
+        }
+        const int64_t left = in ? j.cols - col : 0;
+        float x[8];
+        load_part<T, 8>(static_cast<const T *>(j.src) + r * j.ld_src + (left > 0 ? col : 0),
+                        (int)(left < 0 ? 0 : left < 8 ? left : 8), x);
+        s16x8 w[PL];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            short s[PL];
+            split_terms<E, PL>(x[i], s);
+#pragma unroll
+            for (int t = 0; t < PL; ++t) w[t][i] = s[t];
+        }
+#pragma unroll
+        for (int t = 0; t < PL; ++t) *reinterpret_cast<s16x8 *>(j.dst + t * j.plane + q * j.ld + col) = w[t];
+    }
+}
+
+// ---------------------------------------------------------------- products
+
+// What a product's tiles become: a (and p), dp and a, rows of an output, or
+// partial sums.
+enum { FFN_IN, FFN_MID, FFN_OUT, FFN_SUM };
+
+struct FfnOut {
+    int64_t rows, cols; // of the output
+    void *out;
+    int64_t ld_out;
+    float *sum; // [splits][rows][cols]
+    int splits;
+    int64_t split_k;
+    int64_t F;
+    int act;
+    float *pre; // [rows][2F]
+    int64_t ld_pre;
+    short *mid; // planes of [rows][ld_mid]
+    int64_t ld_mid, plane_mid;
+    short *dpre; // planes of [rows][ld_dpre]
+    int64_t ld_dpre, plane_dpre;
+};
+
+// Rows of both projections as they lie in memory, 32 of the one and 32 of the
+// other in turn: one load of a wave group fills 32 rows of a stage of 64 values.
+template <int R>
+struct PairLoader {
+    typedef TileLds<false, R, 64> L;
+    static constexpr int N = L::vecs;
+    const short *gate, *up;
+    int whole;
+    unsigned bytes;
+    int off, step, to;
+
+    __device__ __forceinline__ PairLoader(const Operand &a, int64_t F, int64_t r0, int stages)
+    {
+        const int ld = (int)a.ld;
+        const int64_t f0 = r0 / 2;
+        const int rows = (int)(F - f0 < R / 2 ? F - f0 : R / 2);
+        gate = a.p + f0 * a.ld;
+        up = gate + F * a.ld;
+        whole = rows > 0 ? stages : 0;
+        bytes = (unsigned)((rows - 1) * ld + (int)a.cols) * 2;
+        const int t = threadIdx.x, row = t / 8;
+        off = (row * ld + ((t % 8) ^ L::turn(row)) * 8) * 2;
+        step = 32 * ld * 2;
+        to = __builtin_amdgcn_readfirstlane(t >> 6) * 1024;
+    }
+    __device__ __forceinline__ void load(char *lds)
+    {
+        const unsigned now = whole > 0 ? bytes : 0;
+        const __amdgpu_buffer_rsrc_t g =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(gate), 0, now, 0x00027000);
+        const __amdgpu_buffer_rsrc_t u = __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(up), 0, now, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(i & 1 ? u : g, (lds_void)(lds + i * 4096 + to), 16, off,
+                                                     i / 2 * step, 0, 0);
+        gate += 64;
+        up += 64;
+        --whole;
+        bytes -= 128;
+    }
+};
+
+// Eight values of a row as they leave.
+template <class T, int PL>
+__device__ __forceinline__ void store_terms(short *p, int64_t plane, int left, const float (&x)[8])
+{
+    typedef typename FfnTerms<T>::type E;
+    short w[PL][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        short s[PL];
+        split_terms<E, PL>(x[i], s);
+#pragma unroll
+        for (int q = 0; q < PL; ++q) w[q][i] = s[q];
+    }
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+        if (left >= 8) {
+            typedef s16x8 __attribute__((aligned(2))) any8;
+            s16x8 v;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = w[q][i];
+            *reinterpret_cast<any8 *>(p + q * plane) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) p[q * plane + i] = w[q][i];
+        }
+    }
+}
+
+// f for each of the numbers, as constants: a long loop's body may be left as a
+// loop, whose registers would then be memory.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// One product: M outputs (along X's rows or columns) in each of N rows, K summed
+// values.  PAIRED: X is W_in as it lies in memory.
+template <class T, bool XT, bool YT, int OUT, bool PAIRED, int NI, int NJ>
+__global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K, int64_t mt, int64_t nt, FfnOut o)
+{
+    typedef typename FfnTerms<T>::type E;
+    constexpr int PL = FfnTerms<T>::planes;
+    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Stages<PL, XT>::values, NB = Stages<PL, XT>::buffers;
+    constexpr int STAGE = PL * (TileLds<XT, TM, BK>::bytes + TileLds<YT, TN, BK>::bytes);
+    // a tile leaves through LDS in fp32, in parts of 64 rows and BP blocks of 32
+    // columns of each half (as many as leave room for two blocks of small tiles)
+    constexpr int BP = NB == 4 && NI == 2 ? 1 : 2, PM = NI / BP, PW = 32 * BP;
+    constexpr int P = 2 * PW * 4 + 16, PART = 64 * P, BUFFER = PART > STAGE ? PART : STAGE;
+    __shared__ __align__(16) char lds0[BUFFER];
+    __shared__ __align__(16) char lds1[BUFFER];
+    __shared__ __align__(16) char lds2[NB == 4 ? STAGE : 16];
+    __shared__ __align__(16) char lds3[NB == 4 ? STAGE : 16];
+    int64_t mi, ni;
+    int sp;
+    if (!tile_of(mt, nt, OUT == FFN_SUM ? o.splits : 1, mi, ni, sp)) return;
+    if constexpr (OUT == FFN_SUM) { // this split's part of the sum
+        const int64_t k0 = sp * o.split_k;
+        if (k0 >= K) return;
+        auto from = [&](Operand &a, bool turned) {
+            a.p += turned ? k0 * a.ld : k0;
+            (turned ? a.rows : a.cols) -= k0;
+        };
+        from(X, XT);
+        from(Y, YT);
+        K = K - k0 < o.split_k ? K - k0 : o.split_k;
+        o.sum += sp * o.rows * o.cols;
+    }
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
+    const int64_t m0 = mi * TM, n0 = ni * TN;
+    f32x16 acc[NI][NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    {
+        const int stages = (int)(K / BK);
+        TileLoader<YT, TN, BK, PL> y(Y, n0, stages);
+        if constexpr (PAIRED) {
+            PairLoader<TM> x(X, o.F, m0, stages);
+            multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+        } else {
+            TileLoader<XT, TM, BK, PL> x(X, m0, stages);
+            multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+        }
+    }
+    // eight values of a row per thread at a time; FFN_IN: of both projections
+    constexpr int ROWV = (OUT == FFN_IN ? PW : 2 * PW) / 8, ITEMS = 64 * ROWV / 256, PARTS = NJ * PM;
+    auto row_at = [&](int j, int k) {
+        const int r = (tid + k * 256) / ROWV;
+        return n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31);
+    };
+    auto col_at = [&](int h, int k) { // (of the output; FFN_IN: of a)
+        const int at = (tid + k * 256) % ROWV * 8;
+        if constexpr (OUT == FFN_IN) return m0 / 2 + at / 32 * (TM / 4) + h * 32 + at % 32;
+        else return m0 + at / PW * (TM / 2) + h * PW + at % PW;
+    };
+    // p of the next part is on its way while this part is worked on
+    float pre[OUT == FFN_MID ? 2 : 1][OUT == FFN_MID ? ITEMS : 1][2][8];
+    auto load_pre = [&](auto which) {
+        constexpr int part = decltype(which)::value;
+        if constexpr (OUT == FFN_MID && part < PARTS) {
+            const int j = part / PM, h = part % PM;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const int64_t i = row_at(j, k), m = col_at(h, k);
+                // (from the last row and columns where there is none)
+                const float *from = o.pre + (i < o.rows ? i : o.rows - 1) * o.ld_pre;
+                const int left = m >= o.F ? 0 : o.F - m < 8 ? (int)(o.F - m) : 8;
+                if (o.F >= 8) {
+                    const int64_t c = left == 8 ? m : o.F - 8; // the last eight, moved into place when they are used
+                    load_vec<float, 8>(from + c, pre[part & 1][k][0]);
+                    load_vec<float, 8>(from + o.F + c, pre[part & 1][k][1]);
+                } else {
+                    load_part<float, 8>(from + (left ? m : 0), left, pre[part & 1][k][0]);
+                    load_part<float, 8>(from + o.F + (left ? m : 0), left, pre[part & 1][k][1]);
+                }
+            }
+        }
+    };
+    load_pre(std::integral_constant<int, 0>());
+    __syncthreads();
+    each_of(std::make_integer_sequence<int, PARTS>(), [&](auto which) {
+        constexpr int p = decltype(which)::value, j = p / PM, h = p % PM;
+        char *part = p & 1 ? lds1 : lds0; // one is written while the last is read
+        if (h == 0) keep_columns(acc, j);
+        load_pre(std::integral_constant<int, p + 1>());
+#pragma unroll
+        for (int b = 0; b < BP; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x16 &v = acc[h * BP + b][j];
+                const int col = wm * PW + b * 32 + 8 * q + 4 * (lane >> 5);
+                *reinterpret_cast<float4 *>(part + (wn * 32 + (lane & 31)) * P + col * 4) =
+                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int c = tid + k * 256, at = c % ROWV * 8;
+            const char *from = part + c / ROWV * P;
+            const int64_t i = row_at(j, k), m = col_at(h, k);
+            if constexpr (OUT == FFN_IN) {
+                float g[8], u[8], a[8], slope[8];
+                const char *gate = from + (at / 32 * PW + at % 32) * 4;
+                load_vec<float, 8>(reinterpret_cast<const float *>(gate), g);
+                load_vec<float, 8>(reinterpret_cast<const float *>(gate + 128), u);
+                activations(o.act, g, a, slope);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a[e] = m + e < o.F ? a[e] * u[e] : 0.f;
+                if (i >= o.rows || m >= o.ld_mid) continue;
+                store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, 8, a);
+                if (o.pre && m < o.F) {
+                    float *to = o.pre + i * o.ld_pre + m;
+                    const int left = (int)(o.F - m < 8 ? o.F - m : 8);
+                    store_part<float, 8>(to, left, g);
+                    store_part<float, 8>(to + o.F, left, u);
+                }
+            } else {
+                const int left = (int)(o.cols - m < 8 ? o.cols - m : 8);
+                float x[8];
+                load_vec<float, 8>(reinterpret_cast<const float *>(from + at * 4), x);
+                if constexpr (OUT == FFN_MID) {
+                    float g[8], u[8], a[8], slope[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        g[e] = pre[p & 1][k][0][e];
+                        u[e] = pre[p & 1][k][1][e];
+                    }
+                    if (left > 0 && left < 8 && o.F >= 8) { // the last columns, from the last eight values
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            g[e] = 0.f;
+                            u[e] = 0.f;
+#pragma unroll
+                            for (int q = e + 1; q < 8; ++q)
+                                if (q - e == 8 - left) {
+                                    g[e] = pre[p & 1][k][0][q];
+                                    u[e] = pre[p & 1][k][1][q];
+                                }
+                        }
+                    }
+                    activations(o.act, g, a, slope);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        g[e] = x[e] * u[e] * slope[e];
+                        slope[e] = a[e] * u[e];
+                        u[e] = x[e] * a[e];
+                    }
+                    if (i >= o.rows || left <= 0) continue;
+                    store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, left, slope);
+                    short *d = o.dpre + i * o.ld_dpre + m;
+                    store_terms<T, PL>(d, o.plane_dpre, left, g);
+                    store_terms<T, PL>(d + o.F, o.plane_dpre, left, u);
+                } else {
+                    if (i >= o.rows || left <= 0) continue;
+                    if constexpr (OUT == FFN_OUT)
+                        store_part<T, 8>(static_cast<T *>(o.out) + i * o.ld_out + m, left, x);
+                    else store_part<float, 8>(o.sum + i * o.cols + m, left, x);
+                }
+            }
+        }
+    });
+}
+
+// An output from its splits' sums.
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_join(const float *sum, int splits, int64_t rows, int64_t cols, T *out,
+                                                  int64_t ld)
+{
+    const int64_t chunks = (cols + 3) / 4, all = rows * chunks, step = (int64_t)gridDim.x * 256;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < all; c += step) {
+        const int64_t i = c / chunks, k = (c - i * chunks) * 4;
+        const int left = (int)(cols - k < 4 ? cols - k : 4);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int q = 0; q < splits; ++q) {
+            float y[4];
+            load_part<float, 4>(sum + ((int64_t)q * rows + i) * cols + k, left, y);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] += y[r];
+        }
+        store_part<T, 4>(out + i * ld + k, left, x);
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_clear(T *p, int64_t ld, int64_t rows, int64_t cols)
+{
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < rows * cols; c += step)
+        p[c / cols * ld + c % cols] = (T)0.f;
+}
+
+// ------------------------------------------------------------ host: plans
+
+unsigned blocks_for(int64_t threads)
+{
+    const int64_t b = (threads + 255) / 256;
+    return (unsigned)(b < 16384 ? b : 16384);
+}
+
+// Side of a product's tiles: 256 where such tiles fill the compute units.
+template <int PL>
+int64_t ffn_side(int64_t M, int64_t N, int splits)
+{
+    if (PL > 1 || M <= 128 || N <= 128) return 128;
+    return ((M + 255) / 256) * ((N + 255) / 256) * splits < kCUs ? 128 : 256;
+}
+
+// Parts of the summed index: where the tiles are fewer than the compute units
+// take at a time, the sum is shared out.
+struct FfnSplit {
+    int parts;
+    int64_t each;
+};
+FfnSplit ffn_split(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    int64_t s = 2 * kCUs / tiles;
+    if (s > K / kSplit) s = K / kSplit;
+    if (s < 1) s = 1;
+    const int64_t each = up((K + s - 1) / s, kPad);
+    return {(int)((K + each - 1) / each), each};
+}
+size_t split_bytes(int64_t M, int64_t N, int64_t K)
+{
+    const FfnSplit s = ffn_split(M, N, K);
+    return s.parts > 1 ? (size_t)s.parts * M * N * sizeof(float) : 0;
+}
+
+// Whether an operand serves as it lies in memory: 16-bit rows at multiples of 16
+// bytes (further apart they would pass the 31 bits of a tile's loads) and of whole
+// pieces of 16 bytes, or where they lie along the sum of whole steps: a piece that
+// the last row's end cuts would be read past it.
+bool lies_well(const void *p, int64_t ld)
+{
+    return ld % 8 == 0 && ld <= (1 << 20) && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+// Which operands are copied.
+struct FfnCopies {
+    bool x, w_in, w_out, gy;
+};
+FfnCopies ffn_copies(bool fp32, bool grad, int64_t D, int64_t F, bool x, bool w_in, bool w_out, bool gy)
+{
+    const bool d = D % kPad == 0, f = F % kPad == 0;
+    if (fp32) return {true, true, true, true};
+    if (grad) return {!x || D % 8, !w_in || D % 8, !w_out || F % 8, !gy || !d}; // only gy lies along a sum
+    return {!x || !d, !w_in || !d, !w_out || !f, false};
+}
+
+struct FfnPlan {
+    short *x, *w_in, *w_out, *gy, *mid, *dpre;
+    float *sum;
+    int64_t Dp, Fp, Pp; // padded columns of x and gy, of a, of dp
+    size_t bytes;
+};
+FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCopies &c, char *base)
+{
+    size_t off = TT_EMB_STATUS_BYTES;
+    auto take = [&](int64_t rows, int64_t cols) {
+        char *r = base ? base + off : nullptr;
+        off += round256((size_t)PL * rows * cols * 2);
+        return reinterpret_cast<short *>(r);
+    };
+    FfnPlan p{};
+    if (n < 1) n = 1; // no rows: the least workspace
+    p.Dp = up(D, kPad);
+    p.Fp = up(F, kPad);
+    p.Pp = up(2 * F, kPad);
+    if (c.x) p.x = take(n, p.Dp);
+    if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.Dp);
+    if (c.w_out) p.w_out = take(D, p.Fp);
+    if (c.gy) p.gy = take(n, p.Dp);
+    p.mid = take(n, p.Fp);
+    size_t sums = 0;
+    auto most = [&](int64_t M, int64_t N, int64_t K) {
+        const size_t b = split_bytes(M, N, K);
+        sums = sums < b ? b : sums;
+    };
+    if (grad) {
+        p.dpre = take(n, p.Pp);
+        most(D, n, p.Pp);
+        most(D, 2 * F, up(n, kPad));
+        most(F, D, up(n, kPad));
+    } else {
+        most(D, n, p.Fp);
+    }
+    p.sum = reinterpret_cast<float *>(base ? base + off : nullptr);
+    off += round256(sums);
+    p.bytes = off;
+    return p;
+}
+FfnCopies copies_of(const FfnArgs &a, int dtype, bool grad)
+{
+    return ffn_copies(dtype == TT_EMB_DTYPE_FLOAT, grad, a.D, a.F, lies_well(a.x, a.ld_x), lies_well(a.w_in, a.ld_in),
+                      lies_well(a.w_out, a.ld_out), lies_well(a.gy, a.ld_gy));
+}
+
+// ---------------------------------------------------------- host: launches
+
+template <class T>
+struct Packing {
+    Packs p{};
+    int n = 0;
+
+    // The operand that a copy (where there is one) or the matrix itself makes.
+    Operand operator()(const void *src, int64_t ld, int64_t rows, int64_t cols, short *dst, int64_t ldp, int64_t pair)
+    {
+        if (!dst) return Operand{static_cast<const short *>(src), ld, 0, rows, cols};
+        const int64_t to = pair ? 2 * up(pair, 32) : rows;
+        add(Pack{src, ld, to, cols, dst, ldp, ldp, to * ldp, pair});
+        return Operand{dst, ldp, to * ldp, to, ldp};
+    }
+    void add(const Pack &job)
+    {
+        p.job[n] = job;
+        p.first[n + 1] = p.first[n] + (int)blocks_for(job.rows * (job.width / 8));
+        ++n;
+    }
+    void run(hipStream_t s)
+    {
+        if (!n) return;
+        for (int k = n; k < kPacks; ++k) p.first[k + 1] = p.first[k];
+        hipLaunchKernelGGL(k_ffn_pack<T>, dim3((unsigned)p.first[n]), dim3(256), 0, s, p);
+    }
+};
+
+template <class T, bool XT, bool YT, int OUT, bool PAIRED>
+void product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const FfnOut &o, hipStream_t s)
+{
+    constexpr int PL = FfnTerms<T>::planes;
+    const int splits = OUT == FFN_SUM ? o.splits : 1;
+    const int64_t side = ffn_side<PL>(M, N, splits), mt = (M + side - 1) / side, nt = (N + side - 1) / side;
+    const dim3 grid(tile_grid(mt, nt, splits));
+    if constexpr (PL == 1) {
+        if (side == 256) {
+            hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, 4, 4>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, 2, 2>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
+}
+
+// An output [N][M] of T, its sum split where that fills the card.
+template <class T, bool XT, bool YT>
+void output(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, float *sum, void *out, int64_t ld,
+            hipStream_t s)
+{
+    FfnOut o{};
+    o.rows = N;
+    o.cols = M;
+    o.out = out;
+    o.ld_out = ld;
+    const FfnSplit split = ffn_split(M, N, K);
+    if (split.parts == 1) {
+        product<T, XT, YT, FFN_OUT, false>(x, y, M, N, K, o, s);
+        return;
+    }
+    o.sum = sum;
+    o.splits = split.parts;
+    o.split_k = split.each;
+    product<T, XT, YT, FFN_SUM, false>(x, y, M, N, K, o, s);
+    hipLaunchKernelGGL(k_ffn_join<T>, dim3(blocks_for(N * ((M + 3) / 4))), dim3(256), 0, s, sum, split.parts, N, M,
+                       static_cast<T *>(out), ld);
+}
+
+template <class T>
+hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
+{
+    constexpr int PL = FfnTerms<T>::planes;
+    const FfnPlan p = plan_ffn(a.n, a.D, a.F, PL, false, copies_of(a, dtype, false), a.ws);
+    Packing<T> pack;
+    const Operand x = pack(a.x, a.ld_x, a.n, a.D, p.x, p.Dp, 0);
+    const Operand w_in = pack(a.w_in, a.ld_in, 2 * a.F, a.D, p.w_in, p.Dp, a.F);
+    const Operand w_out = pack(a.w_out, a.ld_out, a.D, a.F, p.w_out, p.Fp, 0);
+    pack.run(s);
+    FfnOut o{};
+    o.rows = a.n;
+    o.F = a.F;
+    o.act = a.act;
+    o.pre = a.pre;
+    o.ld_pre = a.ld_pre;
+    o.mid = p.mid;
+    o.ld_mid = p.Fp;
+    o.plane_mid = a.n * p.Fp;
+    const int64_t M = 2 * up(a.F, 32);
+    bool done = false;
+    if constexpr (PL == 1) {
+        if (!p.w_in) {
+            product<T, false, false, FFN_IN, true>(w_in, x, M, a.n, p.Dp, o, s);
+            done = true;
+        }
+    }
+    if (!done) product<T, false, false, FFN_IN, false>(w_in, x, M, a.n, p.Dp, o, s);
+    const Operand mid{p.mid, p.Fp, a.n * p.Fp, a.n, p.Fp};
+    output<T, false, false>(w_out, mid, a.D, a.n, p.Fp, p.sum, a.y, a.ld_y, s);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t ffn_backward(const FfnArgs &a, int dtype, hipStream_t s)
+{
+    constexpr int PL = FfnTerms<T>::planes;
+    const FfnPlan p = plan_ffn(a.n, a.D, a.F, PL, true, copies_of(a, dtype, true), a.ws);
+    Packing<T> pack;
+    const Operand gy = pack(a.gy, a.ld_gy, a.n, a.D, p.gy, p.Dp, 0);
+    const Operand x = pack(a.x, a.ld_x, a.n, a.D, p.x, p.Dp, 0);
+    const Operand w_in = pack(a.w_in, a.ld_in, 2 * a.F, a.D, p.w_in, p.Dp, 0);
+    const Operand w_out = pack(a.w_out, a.ld_out, a.D, a.F, p.w_out, p.Fp, 0);
+    // the products along dp's columns meet its padding
+    if (p.Pp > 2 * a.F) pack.add(Pack{nullptr, 0, a.n, 0, p.dpre + p.Pp - kPad, kPad, p.Pp, a.n * p.Pp, 0});
+    pack.run(s);
+    FfnOut o{};
+    o.rows = a.n;
+    o.cols = o.F = a.F;
+    o.act = a.act;
+    o.pre = a.pre;
+    o.ld_pre = a.ld_pre;
+    o.mid = p.mid;
+    o.ld_mid = p.Fp;
+    o.plane_mid = a.n * p.Fp;
+    o.dpre = p.dpre;
+    o.ld_dpre = p.Pp;
+    o.plane_dpre = a.n * p.Pp;
+    product<T, true, false, FFN_MID, false>(w_out, gy, a.F, a.n, p.Dp, o, s);
+    const Operand mid{p.mid, p.Fp, o.plane_mid, a.n, p.Fp}, dpre{p.dpre, p.Pp, o.plane_dpre, a.n, p.Pp};
+    const int64_t rows = up(a.n, kPad);
+    output<T, true, false>(w_in, dpre, a.D, a.n, p.Pp, p.sum, a.gx, a.ld_gx, s);
+    output<T, true, true>(x, dpre, a.D, 2 * a.F, rows, p.sum, a.gw_in, a.ld_gin, s);
+    output<T, true, true>(mid, gy, a.F, a.D, rows, p.sum, a.gw_out, a.ld_gout, s);
+    return hipGetLastError();
+}
+
+// No rows: the weights' gradients are zero.
+template <class T>
+hipError_t ffn_clear(const FfnArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL(k_ffn_clear<T>, dim3(blocks_for(2 * a.F * a.D)), dim3(256), 0, s, static_cast<T *>(a.gw_in),
+                       a.ld_gin, 2 * a.F, a.D);
+    hipLaunchKernelGGL(k_ffn_clear<T>, dim3(blocks_for(a.D * a.F)), dim3(256), 0, s, static_cast<T *>(a.gw_out),
+                       a.ld_gout, a.D, a.F);
+    return hipGetLastError();
+}
+
+} // namespace
+
+// what: TT_EMB_FFN_GRAD and TT_EMB_FFN_ALIGNED.
+size_t ffn_workspace(int64_t n, int64_t D, int64_t F, int dtype, int what)
+{
+    const bool fp32 = dtype == TT_EMB_DTYPE_FLOAT, grad = what & TT_EMB_FFN_GRAD, well = what & TT_EMB_FFN_ALIGNED;
+    return plan_ffn(n, D, F, fp32 ? 3 : 1, grad, ffn_copies(fp32, grad, D, F, well, well, well, well), nullptr).bytes;
+}
+
+size_t ffn_needs(const FfnArgs &a, int dtype, bool grad)
+{
+    return plan_ffn(a.n, a.D, a.F, dtype == TT_EMB_DTYPE_FLOAT ? 3 : 1, grad, copies_of(a, dtype, grad), nullptr).bytes;
+}
+
+hipError_t launch_ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
+{
+    if (a.n == 0) return hipSuccess;
+    if (dtype == TT_EMB_DTYPE_FLOAT) return ffn_forward<float>(a, dtype, s);
+    if (dtype == TT_EMB_DTYPE_BFLOAT) return ffn_forward<bf16>(a, dtype, s);
+    return ffn_forward<f16>(a, dtype, s);
+}
+
+hipError_t launch_ffn_backward(const FfnArgs &a, int dtype, hipStream_t s)
+{
+    if (dtype == TT_EMB_DTYPE_FLOAT) return a.n == 0 ? ffn_clear<float>(a, s) : ffn_backward<float>(a, dtype, s);
+    if (dtype == TT_EMB_DTYPE_BFLOAT) return a.n == 0 ? ffn_clear<bf16>(a, s) : ffn_backward<bf16>(a, dtype, s);
+    return a.n == 0 ? ffn_clear<f16>(a, s) : ffn_backward<f16>(a, dtype, s);
+}
+
+} // namespace ttemb

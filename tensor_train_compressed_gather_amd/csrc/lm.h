@@ -1,5 +1,5 @@
 // lm.h -- shared definitions of the operators around the table (lookup, norm,
-// blocknorm, xent, adamw, clip): element types, vector access, block reductions, launchers.
+// blocknorm, ffn, xent, adamw, clip): element types, vector access, block reductions, launchers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -172,6 +172,25 @@ hipError_t launch_block_backward(const BlockNormArgs &a, int dtype, int res_dtyp
 size_t block_workspace(int64_t n, int64_t D);
 size_t block_parts_bytes(int64_t n, int64_t D);
 int block_col_parts(int64_t n, int64_t D);
+
+struct FfnArgs {
+    const void *x, *w_in, *w_out;
+    int64_t ld_x, ld_in, ld_out, n, D, F;
+    int act;
+    float *pre; // written (forward, or null) or read (backward)
+    int64_t ld_pre;
+    void *y; // forward
+    int64_t ld_y;
+    const void *gy; // backward
+    int64_t ld_gy;
+    void *gx, *gw_in, *gw_out;
+    int64_t ld_gx, ld_gin, ld_gout;
+    char *ws;
+};
+hipError_t launch_ffn_forward(const FfnArgs &a, int dtype, hipStream_t s);
+hipError_t launch_ffn_backward(const FfnArgs &a, int dtype, hipStream_t s);
+size_t ffn_workspace(int64_t n, int64_t D, int64_t F, int dtype, int what);
+size_t ffn_needs(const FfnArgs &a, int dtype, bool grad); // for these operands as they lie in memory
 
 struct XentArgs {
     const void *hidden, *weight;

@@ -1,5 +1,5 @@
 // lm_api.hip -- host side of the operators around the table (lookup, norm,
-// blocknorm, xent, adamw, clip): argument checks before anything is enqueued, then the
+// blocknorm, ffn, xent, adamw, clip): argument checks before anything is enqueued, then the
 // stream-ordered launches.  Nothing here allocates device memory, and no exception
 // leaves.
 #include <algorithm>
@@ -32,6 +32,7 @@ int hip_status(hipError_t e) { return e == hipSuccess ? TT_EMB_OK : TT_EMB_ERR_H
 constexpr int64_t kMaxRows = 0x7ffffffe;
 constexpr int64_t kMaxLookupCols = 65536, kMaxNormCols = 16384, kMaxXentCols = 16384;
 constexpr int64_t kMaxXentTiles = (int64_t)1 << 23;
+constexpr int64_t kMaxFfnCols = 65536, kMaxFfnTiles = (int64_t)1 << 23;
 constexpr int64_t kMaxClipValues = (int64_t)1 << 42;
 
 int check_lookup(int64_t n, int64_t V, int64_t D, int32_t dtype)
@@ -105,6 +106,17 @@ int block_args(BlockNormArgs &a, const void *x, int64_t ld_x, const void *residu
     a.param_dtype = param_dtype;
     a.scale_residual = residual_scale;
     a.scale_block = block_scale;
+    return TT_EMB_OK;
+}
+
+int check_ffn(int64_t n, int64_t D, int64_t F, int32_t dtype, int32_t act)
+{
+    if (n < 0 || D <= 0 || F <= 0 || bad_dtype(dtype)) return TT_EMB_ERR_ARG;
+    if (act != TT_EMB_ACT_SILU && act != TT_EMB_ACT_GELU && act != TT_EMB_ACT_GELU_TANH) return TT_EMB_ERR_ARG;
+    if (n > kMaxRows || D > kMaxFfnCols || F > kMaxFfnCols) return TT_EMB_ERR_UNSUPPORTED;
+    // tiles of p: the blocks of one launch stay below 2^24
+    const int64_t wide = 2 * F > D ? 2 * F : D;
+    if (((n + 127) / 128) * ((wide + 127) / 128) > kMaxFfnTiles) return TT_EMB_ERR_UNSUPPORTED;
     return TT_EMB_OK;
 }
 
@@ -353,7 +365,8 @@ int tt_emb_block_backward(const void *grad_y, int64_t ld_grad_y, const void *gra
                         post_beta, gamma, nullptr, param_dtype, kind, residual_scale, block_scale);
     if (rc) return rc;
     if (bad_matrix(grad_y, ld_grad_y, n, D, dtype) || (grad_h && bad_matrix(grad_h, ld_grad_h, n, D, residual_dtype)) ||
-        bad_matrix(grad_x, ld_grad_x, n, D, dtype) || bad_matrix(grad_residual, ld_grad_residual, n, D, residual_dtype) ||
+        bad_matrix(grad_x, ld_grad_x, n, D, dtype) ||
+        bad_matrix(grad_residual, ld_grad_residual, n, D, residual_dtype) ||
         (n > 0 && (!stats || off_grid(stats, TT_EMB_DTYPE_FLOAT))))
         return TT_EMB_ERR_ARG;
     if (a.gate_rows ? bad_matrix(grad_gate, ld_grad_gate, n, D, dtype) : off_grid(grad_gate, param_dtype))
@@ -380,6 +393,84 @@ int tt_emb_block_backward(const void *grad_y, int64_t ld_grad_y, const void *gra
     a.sums[4] = a.gate_rows ? nullptr : grad_gate;
     a.ws = static_cast<char *>(ws);
     return hip_status(launch_block_backward(a, dtype, residual_dtype, (hipStream_t)stream));
+}
+
+int tt_emb_ffn_workspace_size(int64_t n, int64_t D, int64_t F, int32_t dtype, int32_t what, size_t *bytes)
+{
+    if (!bytes || (what & ~(TT_EMB_FFN_GRAD | TT_EMB_FFN_ALIGNED))) return TT_EMB_ERR_ARG;
+    const int rc = check_ffn(n, D, F, dtype, TT_EMB_ACT_SILU);
+    if (rc) return rc;
+    *bytes = ffn_workspace(n, D, F, dtype, what);
+    return TT_EMB_OK;
+}
+
+int tt_emb_ffn_forward(const void *x, int64_t ld_x, const void *w_in, int64_t ld_in, const void *w_out, int64_t ld_out,
+                       int64_t n, int64_t D, int64_t F, int32_t dtype, int32_t activation, float *pre, int64_t ld_pre,
+                       void *y, int64_t ld_y, void *ws, size_t ws_bytes, void *stream)
+{
+    int rc = check_ffn(n, D, F, dtype, activation);
+    if (rc) return rc;
+    if (bad_matrix(x, ld_x, n, D, dtype) || bad_matrix(w_in, ld_in, 2 * F, D, dtype) ||
+        bad_matrix(w_out, ld_out, D, F, dtype) || bad_matrix(y, ld_y, n, D, dtype) ||
+        (pre && bad_matrix(pre, ld_pre, n, 2 * F, TT_EMB_DTYPE_FLOAT)))
+        return TT_EMB_ERR_ARG;
+    FfnArgs a{};
+    a.x = x;
+    a.w_in = w_in;
+    a.w_out = w_out;
+    a.ld_x = ld_x;
+    a.ld_in = ld_in;
+    a.ld_out = ld_out;
+    a.n = n;
+    a.D = D;
+    a.F = F;
+    a.act = activation;
+    a.pre = pre;
+    a.ld_pre = ld_pre;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.ws = static_cast<char *>(ws);
+    if ((rc = check_ws(ws, ws_bytes, ffn_needs(a, dtype, false)))) return rc;
+    return hip_status(launch_ffn_forward(a, dtype, (hipStream_t)stream));
+}
+
+int tt_emb_ffn_backward(const void *grad_y, int64_t ld_grad_y, const void *x, int64_t ld_x, const float *pre,
+                        int64_t ld_pre, const void *w_in, int64_t ld_in, const void *w_out, int64_t ld_out, int64_t n,
+                        int64_t D, int64_t F, int32_t dtype, int32_t activation, void *grad_x, int64_t ld_grad_x,
+                        void *grad_w_in, int64_t ld_grad_in, void *grad_w_out, int64_t ld_grad_out, void *ws,
+                        size_t ws_bytes, void *stream)
+{
+    int rc = check_ffn(n, D, F, dtype, activation);
+    if (rc) return rc;
+    if (bad_matrix(grad_y, ld_grad_y, n, D, dtype) || bad_matrix(x, ld_x, n, D, dtype) ||
+        bad_matrix(pre, ld_pre, n, 2 * F, TT_EMB_DTYPE_FLOAT) || bad_matrix(w_in, ld_in, 2 * F, D, dtype) ||
+        bad_matrix(w_out, ld_out, D, F, dtype) || bad_matrix(grad_x, ld_grad_x, n, D, dtype) ||
+        bad_matrix(grad_w_in, ld_grad_in, 2 * F, D, dtype) || bad_matrix(grad_w_out, ld_grad_out, D, F, dtype))
+        return TT_EMB_ERR_ARG;
+    FfnArgs a{};
+    a.gy = grad_y;
+    a.ld_gy = ld_grad_y;
+    a.x = x;
+    a.w_in = w_in;
+    a.w_out = w_out;
+    a.ld_x = ld_x;
+    a.ld_in = ld_in;
+    a.ld_out = ld_out;
+    a.n = n;
+    a.D = D;
+    a.F = F;
+    a.act = activation;
+    a.pre = const_cast<float *>(pre);
+    a.ld_pre = ld_pre;
+    a.gx = grad_x;
+    a.ld_gx = ld_grad_x;
+    a.gw_in = grad_w_in;
+    a.ld_gin = ld_grad_in;
+    a.gw_out = grad_w_out;
+    a.ld_gout = ld_grad_out;
+    a.ws = static_cast<char *>(ws);
+    if ((rc = check_ws(ws, ws_bytes, ffn_needs(a, dtype, true)))) return rc;
+    return hip_status(launch_ffn_backward(a, dtype, (hipStream_t)stream));
 }
 
 int tt_emb_xent_workspace_size(int64_t n, int64_t V, int64_t D, int32_t dtype, int32_t what, size_t *bytes,

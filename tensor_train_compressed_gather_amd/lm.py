@@ -1,6 +1,6 @@
 """Operators around the table, from token ids to the update of the weights:
 embedding lookup with its gradient, layer norm, the norms between two blocks
-with gate and residual, softmax cross entropy over a
+with gate and residual, the gated feed-forward block, softmax cross entropy over a
 large vocabulary, the gradients' global norm and AdamW (C ABI in ``include/tt_emb.h``).
 
 The classes marshal arguments only: they check what the library cannot see
@@ -17,6 +17,8 @@ import threading
 TT_EMB_DTYPE_FLOAT, TT_EMB_DTYPE_BFLOAT, TT_EMB_DTYPE_HALF = 0, 1, 2
 TT_EMB_STATUS_BYTES = 256
 TT_EMB_XENT_GRAD, TT_EMB_XENT_ALIGNED = 1, 2
+TT_EMB_FFN_GRAD, TT_EMB_FFN_ALIGNED = 1, 2
+TT_EMB_ACT_SILU, TT_EMB_ACT_GELU, TT_EMB_ACT_GELU_TANH = 0, 1, 2
 TT_EMB_BLOCK_RMS, TT_EMB_BLOCK_POST, TT_EMB_BLOCK_GATE_ROWS = 1, 2, 4
 
 LM_EXPORTED = (
@@ -24,6 +26,7 @@ LM_EXPORTED = (
     "tt_emb_lookup_forward", "tt_emb_lookup_backward", "tt_emb_lookup_workspace_size",
     "tt_emb_norm_forward", "tt_emb_norm_backward", "tt_emb_norm_workspace_size",
     "tt_emb_block_forward", "tt_emb_block_backward", "tt_emb_block_workspace_size",
+    "tt_emb_ffn_forward", "tt_emb_ffn_backward", "tt_emb_ffn_workspace_size",
     "tt_emb_xent_forward", "tt_emb_xent_loss_grad", "tt_emb_xent_workspace_size", "tt_emb_xent_parts",
     "tt_emb_adamw_update", "tt_emb_adamw_update_scaled", "tt_emb_adamw_state_size",
     "tt_emb_clip_norm", "tt_emb_clip_scale", "tt_emb_clip_workspace_size",
@@ -47,14 +50,18 @@ def declare(L):
     L.tt_emb_block_backward.argtypes = [p, i64, p, i64, p, i64, p, i64, i64, i64, i32, i32, p, i64, p, p, p, i32, i32,
                                         f32, f32, p, p, i64, p, i64, p, i64, p, p, p, p, p, size, p]
     L.tt_emb_block_workspace_size.argtypes = [i64, i64, sizes]
+    L.tt_emb_ffn_forward.argtypes = [p, i64, p, i64, p, i64, i64, i64, i64, i32, i32, p, i64, p, i64, p, size, p]
+    L.tt_emb_ffn_backward.argtypes = [p, i64, p, i64, p, i64, p, i64, p, i64, i64, i64, i64, i32, i32, p, i64, p, i64,
+                                      p, i64, p, size, p]
+    L.tt_emb_ffn_workspace_size.argtypes = [i64, i64, i64, i32, i32, sizes]
     L.tt_emb_xent_forward.argtypes = [p, i64, p, i64, p, i64, i64, i64, i32, i64, p, p, p, size, p]
     L.tt_emb_xent_loss_grad.argtypes = [p, i64, p, i64, p, p, i64, i64, i64, i32, i64, p, p, p, i64, p, i64, p, size,
                                         p]
     L.tt_emb_xent_workspace_size.argtypes = [i64, i64, i64, i32, i32, sizes, sizes]
     L.tt_emb_xent_parts.argtypes = [i64, i64, i64, i32, i32, size, p, i64, C.POINTER(i64), C.POINTER(i32)]
     L.tt_emb_adamw_update.argtypes = [i32, p, p, i32, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64, p]
-    L.tt_emb_adamw_update_scaled.argtypes = [i32, p, p, i32, p, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64, u64,
-                                             p]
+    L.tt_emb_adamw_update_scaled.argtypes = [i32, p, p, i32, p, p, p, p, p, p, p, i32, f64, f64, f64, f64, f64, i64,
+                                             u64, p]
     L.tt_emb_clip_norm.argtypes = [i32, p, p, p, f64, f64, p, p, p, size, p]
     L.tt_emb_clip_scale.argtypes = [i32, p, p, p, f64, f64, p, p, p, size, p]
     L.tt_emb_clip_workspace_size.argtypes = [i32, p, sizes]
@@ -493,6 +500,89 @@ class BlockNorm(_Operator):
         return dx, dr, dgate, dgamma, dbeta, dpost_gamma, dpost_beta
 
 
+class GatedFeedForward(_Operator):
+    """The gated feed-forward block over rows of D elements:
+
+        p = x w_in^T,  a = act(p[:, :F]) * p[:, F:],  y = a w_out^T
+
+    w_in [2F, D] (the gate's F rows, then the other projection's) and w_out
+    [D, F] of x's type; ``activation`` "silu", "gelu" or "gelu_tanh".
+
+    forward(x, w_in, w_out) -> y, or (y, p) with keep=True, p fp32 [n, 2F] for
+    the backward.
+    backward(grad_y, x, p, w_in, w_out) -> (grad_x, grad_w_in, grad_w_out).
+
+    bf16 and fp16: sums are fp32, a and p's gradient are rounded to the type
+    between the products.  fp32: operands are taken as three bf16 terms, 24
+    bits.  16-bit rows of a multiple of 8 columns (along a sum: of 64) that begin
+    at multiples of 16 bytes are read in place; others are copied by each call."""
+
+    ACTIVATIONS = {"silu": TT_EMB_ACT_SILU, "gelu": TT_EMB_ACT_GELU, "gelu_tanh": TT_EMB_ACT_GELU_TANH}
+
+    def __init__(self, D: int, F: int, activation: str = "silu", device="cuda"):
+        super().__init__(device)
+        self.D, self.F = int(D), int(F)
+        if activation not in self.ACTIVATIONS:
+            raise _bad("GatedFeedForward", f"activation {activation!r}, expected one of {', '.join(self.ACTIVATIONS)}")
+        self._act = self.ACTIVATIONS[activation]
+        self._need(0, 0, 0, "GatedFeedForward")
+
+    def _need(self, n: int, dt: int, what: int, where: str) -> int:
+        return _size(_L.tt_emb_ffn_workspace_size, where, n, self.D, self.F, dt, what)
+
+    def _inputs(self, x, w_in, w_out, where):
+        ld_x = _matrix(x, where, "x", self.D)
+        dt, n, device = _dtype(x, where, "x"), x.shape[0], x.device
+        ld_in = _matrix(w_in, where, "w_in", self.D, 2 * self.F, x.dtype, device)
+        ld_out = _matrix(w_out, where, "w_out", self.F, self.D, x.dtype, device)
+        # 16-bit operands that lie like this are read in place and need no room for copies
+        lds, addresses = ld_x | ld_in | ld_out, x.data_ptr() | w_in.data_ptr() | w_out.data_ptr()
+        aligned = not lds & 7 and max(ld_x, ld_in, ld_out) <= 1 << 20 and not addresses & 15
+        return ld_x, ld_in, ld_out, dt, n, device, aligned
+
+    def forward(self, x, w_in, w_out, keep: bool = False, out=None, stream=None):
+        where = "GatedFeedForward.forward"
+        ld_x, ld_in, ld_out, dt, n, device, aligned = self._inputs(x, w_in, w_out, where)
+        need = self._need(n, dt, TT_EMB_FFN_ALIGNED if aligned else 0, where)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.forward(x, w_in, w_out, keep, out)
+        if out is None:
+            out, ld_y = x.new_empty((n, self.D)), self.D
+        else:
+            ld_y = _matrix(out, where, "out", self.D, n, x.dtype, device)
+        pre = torch.empty((n, 2 * self.F), dtype=torch.float32, device=device) if keep else None
+        self._run(_L.tt_emb_ffn_forward, where, device, _raw_stream(device.index), need, x.data_ptr(), ld_x,
+                  w_in.data_ptr(), ld_in, w_out.data_ptr(), ld_out, n, self.D, self.F, dt, self._act, _address(pre),
+                  2 * self.F, out.data_ptr(), ld_y)
+        return (out, pre) if keep else out
+
+    def backward(self, grad_y, x, pre, w_in, w_out, grad_w_in=None, grad_w_out=None, stream=None):
+        where = "GatedFeedForward.backward"
+        ld_x, ld_in, ld_out, dt, n, device, aligned = self._inputs(x, w_in, w_out, where)
+        ld_gy = _matrix(grad_y, where, "grad_y", self.D, n, x.dtype, device)
+        ld_pre = _matrix(pre, where, "pre", 2 * self.F, n, torch.float32, device)
+        aligned = aligned and not ld_gy & 7 and ld_gy <= 1 << 20 and not grad_y.data_ptr() & 15
+        need = self._need(n, dt, TT_EMB_FFN_GRAD | (TT_EMB_FFN_ALIGNED if aligned else 0), where)
+        guard = _guard(device, stream, where)
+        if guard is not None:
+            with guard:
+                return self.backward(grad_y, x, pre, w_in, w_out, grad_w_in, grad_w_out)
+        dx = x.new_empty((n, self.D))
+        if grad_w_in is None:
+            grad_w_in = x.new_empty((2 * self.F, self.D))
+        if grad_w_out is None:
+            grad_w_out = x.new_empty((self.D, self.F))
+        ld_gin = _matrix(grad_w_in, where, "grad_w_in", self.D, 2 * self.F, x.dtype, device)
+        ld_gout = _matrix(grad_w_out, where, "grad_w_out", self.F, self.D, x.dtype, device)
+        self._run(_L.tt_emb_ffn_backward, where, device, _raw_stream(device.index), need, grad_y.data_ptr(), ld_gy,
+                  x.data_ptr(), ld_x, pre.data_ptr(), ld_pre, w_in.data_ptr(), ld_in, w_out.data_ptr(), ld_out, n,
+                  self.D, self.F, dt, self._act, dx.data_ptr(), self.D, grad_w_in.data_ptr(), ld_gin,
+                  grad_w_out.data_ptr(), ld_gout)
+        return dx, grad_w_in, grad_w_out
+
+
 class tt_emb_xent_part(C.Structure):
     _fields_ = [("begin", C.c_int64), ("end", C.c_int64), ("slot", C.c_int32), ("first", C.c_int32)]
 
@@ -720,7 +810,8 @@ class AdamW:
                 return self.step(grads, lr, None, grad_scale)
         s = _raw_stream(self.device.index)
         _check(_L.tt_emb_adamw_update_scaled(
-            n, params, pointers, dt, None if grad_scale is None else grad_scale.data_ptr(), copies, self._numel, self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(),
+            n, params, pointers, dt, _address(grad_scale), copies, self._numel, self.exp_avg.data_ptr(),
+            self.exp_avg_sq.data_ptr(),
             None if self.exp_avg_scale is None else self.exp_avg_scale.data_ptr(),
             None if self.exp_avg_sq_scale is None else self.exp_avg_sq_scale.data_ptr(), self.state_bits,
             self.lr if lr is None else float(lr), self.betas[0], self.betas[1], self.eps, self.weight_decay,
