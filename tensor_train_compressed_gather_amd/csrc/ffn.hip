@@ -47,15 +47,31 @@ struct FfnTerms<float> {
 // ------------------------------------------------------------- activations
 
 // The values of the activation at z, and its slopes.  gelu's tanh form is z times
-// the sigmoid of twice the argument, 2 sqrt(2 / pi) (z + 0.044715 z^3).
+// the sigmoid of twice the argument, 2 sqrt(2 / pi) (z + 0.044715 z^3).  NEAR: for
+// results that are rounded to 16 bits, with the hardware's exponential and
+// reciprocal (off by some 2^-22 of the value) and, for the normal distribution's
+// integral, formula 7.1.26 of Abramowitz and Stegun (off by 1.5e-7).
+template <bool NEAR>
 __device__ __forceinline__ void activations(int act, const float (&z)[8], float (&value)[8], float (&slope)[8])
 {
     if (act == TT_EMB_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float c = 0.5f * erfcf(-0.70710678f * z[i]); // (1 + erf would lose the small values)
+            float c, e;
+            if constexpr (NEAR) {
+                e = __builtin_amdgcn_exp2f(-0.72134752f * z[i] * z[i]);
+                const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678f, fabsf(z[i]), 1.f));
+                float q = fmaf(t, 1.061405429f, -1.453152027f);
+                q = fmaf(t, q, 1.421413741f);
+                q = fmaf(t, q, -0.284496736f);
+                q = fmaf(t, q, 0.254829592f) * t * 0.5f * e;
+                c = z[i] < 0.f ? q : 1.f - q;
+            } else {
+                e = expf(-0.5f * z[i] * z[i]);
+                c = 0.5f * erfcf(-0.70710678f * z[i]); // (1 + erf would lose the small values)
+            }
             value[i] = z[i] * c;
-            slope[i] = fmaf(z[i], 0.39894228f * expf(-0.5f * z[i] * z[i]), c);
+            slope[i] = fmaf(z[i], 0.39894228f * e, c);
         }
         return;
     }
@@ -63,7 +79,8 @@ __device__ __forceinline__ void activations(int act, const float (&z)[8], float 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float zz = cube * z[i] * z[i], x = by * fmaf(zz, z[i], z[i]), dx = by * fmaf(3.f, zz, 1.f);
-        const float e = expf(-fabsf(x)), r = 1.f / (1.f + e);
+        const float e = NEAR ? __builtin_amdgcn_exp2f(-1.44269504f * fabsf(x)) : expf(-fabsf(x));
+        const float r = NEAR ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
         const float sg = x < 0.f ? e * r : r, other = x < 0.f ? r : e * r; // sigmoid of x and of -x
         value[i] = z[i] * sg;
         slope[i] = fmaf(z[i] * dx, sg * other, sg);
@@ -124,9 +141,9 @@ __global__ __launch_bounds__(256) void k_ffn_pack(Packs p)
 
 // ---------------------------------------------------------------- products
 
-// What a product's tiles become: a (and p), dp and a, rows of an output, or
-// partial sums.
-enum { FFN_IN, FFN_MID, FFN_OUT, FFN_SUM };
+// What a product's tiles become: a (and p), dp and a, or rows of an output (or
+// of a partial sum of it, where `sum` is set).
+enum { FFN_IN, FFN_MID, FFN_OUT };
 
 struct FfnOut {
     int64_t rows, cols; // of the output
@@ -224,27 +241,41 @@ __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
     (f(std::integral_constant<int, I>()), ...);
 }
 
-// One product: M outputs (along X's rows or columns) in each of N rows, K summed
-// values.  PAIRED: X is W_in as it lies in memory.
+// LDS of a product's tiles.  A tile leaves through LDS in fp32, in parts of 64
+// rows and BP blocks of 32 columns of each half (as many as leave room for two
+// blocks of small tiles on a compute unit).
+template <int PL, bool XT, bool YT, int NI, int NJ>
+struct FfnLds {
+    static constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Stages<PL, XT>::values, NB = Stages<PL, XT>::buffers;
+    static constexpr int stage = PL * (TileLds<XT, TM, BK>::bytes + TileLds<YT, TN, BK>::bytes);
+    static constexpr int BP = NB == 4 && NI == 2 ? 1 : 2, PW = 32 * BP, P = 2 * PW * 4 + 16, part = 64 * P;
+    static constexpr int first = part > stage ? part : stage, more = NB == 4 ? stage : 16; // of two buffers each
+};
+
+// A tile of one product: M outputs (along X's rows or columns) in each of N rows,
+// K summed values, mt x nt tiles taken by `grid` blocks.  PAIRED: X is W_in as it
+// lies in memory.
+struct FfnJob {
+    Operand X, Y;
+    int64_t K, mt, nt;
+    unsigned grid;
+    FfnOut o;
+};
 template <class T, bool XT, bool YT, int OUT, bool PAIRED, int NI, int NJ>
-__global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K, int64_t mt, int64_t nt, FfnOut o)
+__device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char *lds0, char *lds1, char *lds2,
+                                         char *lds3)
 {
     typedef typename FfnTerms<T>::type E;
     constexpr int PL = FfnTerms<T>::planes;
-    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Stages<PL, XT>::values, NB = Stages<PL, XT>::buffers;
-    constexpr int STAGE = PL * (TileLds<XT, TM, BK>::bytes + TileLds<YT, TN, BK>::bytes);
-    // a tile leaves through LDS in fp32, in parts of 64 rows and BP blocks of 32
-    // columns of each half (as many as leave room for two blocks of small tiles)
-    constexpr int BP = NB == 4 && NI == 2 ? 1 : 2, PM = NI / BP, PW = 32 * BP;
-    constexpr int P = 2 * PW * 4 + 16, PART = 64 * P, BUFFER = PART > STAGE ? PART : STAGE;
-    __shared__ __align__(16) char lds0[BUFFER];
-    __shared__ __align__(16) char lds1[BUFFER];
-    __shared__ __align__(16) char lds2[NB == 4 ? STAGE : 16];
-    __shared__ __align__(16) char lds3[NB == 4 ? STAGE : 16];
-    int64_t mi, ni;
+    typedef FfnLds<PL, XT, YT, NI, NJ> Lds;
+    constexpr int TM = Lds::TM, TN = Lds::TN, BK = Lds::BK, BP = Lds::BP, PM = NI / BP, PW = Lds::PW, P = Lds::P;
+    Operand X = job.X, Y = job.Y;
+    const FfnOut &o = job.o;
+    int64_t mi, ni, K = job.K;
     int sp;
-    if (!tile_of(mt, nt, OUT == FFN_SUM ? o.splits : 1, mi, ni, sp)) return;
-    if constexpr (OUT == FFN_SUM) { // this split's part of the sum
+    if (!tile_of(block, job.grid, job.mt, job.nt, OUT == FFN_OUT ? o.splits : 1, mi, ni, sp)) return;
+    float *sum = nullptr;
+    if (OUT == FFN_OUT && o.sum) { // this split's part of the sum
         const int64_t k0 = sp * o.split_k;
         if (k0 >= K) return;
         auto from = [&](Operand &a, bool turned) {
@@ -254,7 +285,7 @@ __global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K,
         from(X, XT);
         from(Y, YT);
         K = K - k0 < o.split_k ? K - k0 : o.split_k;
-        o.sum += sp * o.rows * o.cols;
+        sum = o.sum + sp * o.rows * o.cols;
     }
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
     const int64_t m0 = mi * TM, n0 = ni * TN;
@@ -265,17 +296,6 @@ __global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K,
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    {
-        const int stages = (int)(K / BK);
-        TileLoader<YT, TN, BK, PL> y(Y, n0, stages);
-        if constexpr (PAIRED) {
-            PairLoader<TM> x(X, o.F, m0, stages);
-            multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
-        } else {
-            TileLoader<XT, TM, BK, PL> x(X, m0, stages);
-            multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
-        }
-    }
     // eight values of a row per thread at a time; FFN_IN: of both projections
     constexpr int ROWV = (OUT == FFN_IN ? PW : 2 * PW) / 8, ITEMS = 64 * ROWV / 256, PARTS = NJ * PM;
     auto row_at = [&](int j, int k) {
@@ -310,7 +330,18 @@ __global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K,
             }
         }
     };
-    load_pre(std::integral_constant<int, 0>());
+    load_pre(std::integral_constant<int, 0>()); // (there long before the products are)
+    {
+        const int stages = (int)(K / BK);
+        TileLoader<YT, TN, BK, PL> y(Y, n0, stages);
+        if constexpr (PAIRED) {
+            PairLoader<TM> x(X, o.F, m0, stages);
+            multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+        } else {
+            TileLoader<XT, TM, BK, PL> x(X, m0, stages);
+            multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+        }
+    }
     __syncthreads();
     each_of(std::make_integer_sequence<int, PARTS>(), [&](auto which) {
         constexpr int p = decltype(which)::value, j = p / PM, h = p % PM;
@@ -337,7 +368,7 @@ __global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K,
                 const char *gate = from + (at / 32 * PW + at % 32) * 4;
                 load_vec<float, 8>(reinterpret_cast<const float *>(gate), g);
                 load_vec<float, 8>(reinterpret_cast<const float *>(gate + 128), u);
-                activations(o.act, g, a, slope);
+                activations<PL == 1>(o.act, g, a, slope);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] = m + e < o.F ? a[e] * u[e] : 0.f;
                 if (i >= o.rows || m >= o.ld_mid) continue;
@@ -372,7 +403,7 @@ __global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K,
                                 }
                         }
                     }
-                    activations(o.act, g, a, slope);
+                    activations<PL == 1>(o.act, g, a, slope);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         g[e] = x[e] * u[e] * slope[e];
@@ -386,33 +417,82 @@ __global__ __launch_bounds__(256, 1) void k_ffn(Operand X, Operand Y, int64_t K,
                     store_terms<T, PL>(d + o.F, o.plane_dpre, left, u);
                 } else {
                     if (i >= o.rows || left <= 0) continue;
-                    if constexpr (OUT == FFN_OUT)
-                        store_part<T, 8>(static_cast<T *>(o.out) + i * o.ld_out + m, left, x);
-                    else store_part<float, 8>(o.sum + i * o.cols + m, left, x);
+                    if (sum) store_part<float, 8>(sum + i * o.cols + m, left, x);
+                    else store_part<T, 8>(static_cast<T *>(o.out) + i * o.ld_out + m, left, x);
                 }
             }
         }
     });
 }
 
-// An output from its splits' sums.
-template <class T>
-__global__ __launch_bounds__(256) void k_ffn_join(const float *sum, int splits, int64_t rows, int64_t cols, T *out,
-                                                  int64_t ld)
+template <class T, bool XT, bool YT, int OUT, bool PAIRED, int NI, int NJ>
+__global__ __launch_bounds__(256, 1) void k_ffn(FfnJob job)
 {
-    const int64_t chunks = (cols + 3) / 4, all = rows * chunks, step = (int64_t)gridDim.x * 256;
-    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < all; c += step) {
-        const int64_t i = c / chunks, k = (c - i * chunks) * 4;
-        const int left = (int)(cols - k < 4 ? cols - k : 4);
+    typedef FfnLds<FfnTerms<T>::planes, XT, YT, NI, NJ> Lds;
+    __shared__ __align__(16) char lds0[Lds::first];
+    __shared__ __align__(16) char lds1[Lds::first];
+    __shared__ __align__(16) char lds2[Lds::more];
+    __shared__ __align__(16) char lds3[Lds::more];
+    ffn_tile<T, XT, YT, OUT, PAIRED, NI, NJ>(job, blockIdx.x, lds0, lds1, lds2, lds3);
+}
+
+// The backward's three outputs, which do not wait for each other, in one launch:
+// at small sizes each alone leaves most of the card idle, and a launch costs as
+// much as a product.
+struct FfnGrads {
+    FfnJob x, w_in, w_out;
+};
+template <class T, int NI, int NJ>
+__global__ __launch_bounds__(256, 1) void k_ffn_grads(FfnGrads g)
+{
+    constexpr int PL = FfnTerms<T>::planes;
+    typedef FfnLds<PL, true, false, NI, NJ> A;
+    typedef FfnLds<PL, true, true, NI, NJ> B;
+    __shared__ __align__(16) char lds0[A::first > B::first ? A::first : B::first];
+    __shared__ __align__(16) char lds1[A::first > B::first ? A::first : B::first];
+    __shared__ __align__(16) char lds2[A::more > B::more ? A::more : B::more];
+    __shared__ __align__(16) char lds3[A::more > B::more ? A::more : B::more];
+    unsigned b = blockIdx.x;
+    if (b < g.x.grid) {
+        ffn_tile<T, true, false, FFN_OUT, false, NI, NJ>(g.x, b, lds0, lds1, lds2, lds3);
+        return;
+    }
+    b -= g.x.grid;
+    const bool in = b < g.w_in.grid;
+    ffn_tile<T, true, true, FFN_OUT, false, NI, NJ>(in ? g.w_in : g.w_out, in ? b : b - g.w_in.grid, lds0, lds1, lds2,
+                                                    lds3);
+}
+
+// Outputs from their splits' sums.
+struct Join {
+    const float *sum;
+    int splits;
+    int64_t rows, cols;
+    void *out;
+    int64_t ld;
+};
+struct Joins {
+    Join job[3];
+    int first[4]; // first block of each
+};
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_join(Joins p)
+{
+    const int k = (int)blockIdx.x < p.first[1] ? 0 : (int)blockIdx.x < p.first[2] ? 1 : 2;
+    const Join &j = p.job[k];
+    const int64_t chunks = (j.cols + 3) / 4, all = j.rows * chunks, step = (int64_t)(p.first[k + 1] - p.first[k]) * 256;
+    for (int64_t c = (int64_t)((int)blockIdx.x - p.first[k]) * 256 + threadIdx.x; c < all; c += step) {
+        const int64_t i = c / chunks, m = (c - i * chunks) * 4;
+        const int left = (int)(j.cols - m < 4 ? j.cols - m : 4);
         float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-        for (int q = 0; q < splits; ++q) {
+        for (int q = 0; q < j.splits; ++q) {
             float y[4];
-            load_part<float, 4>(sum + ((int64_t)q * rows + i) * cols + k, left, y);
+            load_part<float, 4>(j.sum + ((int64_t)q * j.rows + i) * j.cols + m, left, y);
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] += y[r];
         }
-        store_part<T, 4>(out + i * ld + k, left, x);
+        store_part<T, 4>(static_cast<T *>(j.out) + i * j.ld + m, left, x);
     }
 }
 
@@ -458,7 +538,7 @@ FfnSplit ffn_split(int64_t M, int64_t N, int64_t K)
 size_t split_bytes(int64_t M, int64_t N, int64_t K)
 {
     const FfnSplit s = ffn_split(M, N, K);
-    return s.parts > 1 ? (size_t)s.parts * M * N * sizeof(float) : 0;
+    return s.parts > 1 ? round256((size_t)s.parts * M * N * sizeof(float)) : 0;
 }
 
 // Whether an operand serves as it lies in memory: 16-bit rows at multiples of 16
@@ -485,8 +565,14 @@ struct FfnPlan {
     short *x, *w_in, *w_out, *gy, *mid, *dpre;
     float *sum;
     int64_t Dp, Fp, Pp; // padded columns of x and gy, of a, of dp
+    int64_t ldD, ldF, ldP;
     size_t bytes;
 };
+// Distance of rows of so many columns: an odd number of cache lines where it would
+// be a multiple of 1 KB, at which a tile's rows meet in few channels of the L2
+// (8192 x 4096 x 16384, rows of a 32 KB apart: y in 997 us, 902 with one line more).
+inline int64_t apart(int64_t cols) { return cols % 512 ? cols : cols + 64; }
+
 FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCopies &c, char *base)
 {
     size_t off = TT_EMB_STATUS_BYTES;
@@ -500,26 +586,23 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
     p.Dp = up(D, kPad);
     p.Fp = up(F, kPad);
     p.Pp = up(2 * F, kPad);
-    if (c.x) p.x = take(n, p.Dp);
-    if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.Dp);
-    if (c.w_out) p.w_out = take(D, p.Fp);
-    if (c.gy) p.gy = take(n, p.Dp);
-    p.mid = take(n, p.Fp);
-    size_t sums = 0;
-    auto most = [&](int64_t M, int64_t N, int64_t K) {
-        const size_t b = split_bytes(M, N, K);
-        sums = sums < b ? b : sums;
-    };
+    p.ldD = apart(p.Dp);
+    p.ldF = apart(p.Fp);
+    p.ldP = apart(p.Pp);
+    if (c.x) p.x = take(n, p.ldD);
+    if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.ldD);
+    if (c.w_out) p.w_out = take(D, p.ldF);
+    if (c.gy) p.gy = take(n, p.ldD);
+    p.mid = take(n, p.ldF);
+    size_t sums;
     if (grad) {
-        p.dpre = take(n, p.Pp);
-        most(D, n, p.Pp);
-        most(D, 2 * F, up(n, kPad));
-        most(F, D, up(n, kPad));
+        p.dpre = take(n, p.ldP);
+        sums = split_bytes(D, n, p.Pp) + split_bytes(D, 2 * F, up(n, kPad)) + split_bytes(F, D, up(n, kPad));
     } else {
-        most(D, n, p.Fp);
+        sums = split_bytes(D, n, p.Fp);
     }
     p.sum = reinterpret_cast<float *>(base ? base + off : nullptr);
-    off += round256(sums);
+    off += sums;
     p.bytes = off;
     return p;
 }
@@ -537,12 +620,12 @@ struct Packing {
     int n = 0;
 
     // The operand that a copy (where there is one) or the matrix itself makes.
-    Operand operator()(const void *src, int64_t ld, int64_t rows, int64_t cols, short *dst, int64_t ldp, int64_t pair)
+    Operand operator()(const void *src, int64_t ld, int64_t rows, int64_t cols, short *dst, int64_t width, int64_t pair)
     {
         if (!dst) return Operand{static_cast<const short *>(src), ld, 0, rows, cols};
-        const int64_t to = pair ? 2 * up(pair, 32) : rows;
-        add(Pack{src, ld, to, cols, dst, ldp, ldp, to * ldp, pair});
-        return Operand{dst, ldp, to * ldp, to, ldp};
+        const int64_t to = pair ? 2 * up(pair, 32) : rows, ldp = apart(width);
+        add(Pack{src, ld, to, cols, dst, width, ldp, to * ldp, pair});
+        return Operand{dst, ldp, to * ldp, to, width};
     }
     void add(const Pack &job)
     {
@@ -558,44 +641,67 @@ struct Packing {
     }
 };
 
-template <class T, bool XT, bool YT, int OUT, bool PAIRED>
-void product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const FfnOut &o, hipStream_t s)
+FfnJob job_of(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, int64_t side, const FfnOut &o)
 {
-    constexpr int PL = FfnTerms<T>::planes;
-    const int splits = OUT == FFN_SUM ? o.splits : 1;
-    const int64_t side = ffn_side<PL>(M, N, splits), mt = (M + side - 1) / side, nt = (N + side - 1) / side;
-    const dim3 grid(tile_grid(mt, nt, splits));
-    if constexpr (PL == 1) {
+    const int64_t mt = (M + side - 1) / side, nt = (N + side - 1) / side;
+    return FfnJob{x, y, K, mt, nt, tile_grid(mt, nt, o.splits), o};
+}
+
+template <class T, bool XT, bool YT, int OUT, bool PAIRED>
+void launch(const FfnJob &job, int64_t side, hipStream_t s)
+{
+    if constexpr (FfnTerms<T>::planes == 1) {
         if (side == 256) {
-            hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, 4, 4>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
+            hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, 4, 4>), dim3(job.grid), dim3(256), 0, s, job);
             return;
         }
     }
-    hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, 2, 2>), grid, dim3(256), 0, s, x, y, K, mt, nt, o);
+    hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, 2, 2>), dim3(job.grid), dim3(256), 0, s, job);
 }
 
-// An output [N][M] of T, its sum split where that fills the card.
-template <class T, bool XT, bool YT>
-void output(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, float *sum, void *out, int64_t ld,
-            hipStream_t s)
+template <class T, bool XT, bool YT, int OUT, bool PAIRED>
+void product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const FfnOut &o, hipStream_t s)
 {
-    FfnOut o{};
-    o.rows = N;
-    o.cols = M;
-    o.out = out;
-    o.ld_out = ld;
-    const FfnSplit split = ffn_split(M, N, K);
-    if (split.parts == 1) {
-        product<T, XT, YT, FFN_OUT, false>(x, y, M, N, K, o, s);
-        return;
-    }
-    o.sum = sum;
-    o.splits = split.parts;
-    o.split_k = split.each;
-    product<T, XT, YT, FFN_SUM, false>(x, y, M, N, K, o, s);
-    hipLaunchKernelGGL(k_ffn_join<T>, dim3(blocks_for(N * ((M + 3) / 4))), dim3(256), 0, s, sum, split.parts, N, M,
-                       static_cast<T *>(out), ld);
+    const int64_t side = ffn_side<FfnTerms<T>::planes>(M, N, o.splits);
+    launch<T, XT, YT, OUT, PAIRED>(job_of(x, y, M, N, K, side, o), side, s);
 }
+
+// Outputs [N][M] of T, whose sums are split where that fills the card: each job
+// takes what it needs of the room for partial sums.
+template <class T>
+struct Outputs {
+    float *sum;
+    Joins joins{};
+    int n = 0;
+
+    FfnJob operator()(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, void *out, int64_t ld,
+                      int64_t &side)
+    {
+        FfnOut o{};
+        o.rows = N;
+        o.cols = M;
+        o.out = out;
+        o.ld_out = ld;
+        const FfnSplit split = ffn_split(M, N, K);
+        o.splits = split.parts;
+        if (split.parts > 1) {
+            o.sum = sum;
+            o.split_k = split.each;
+            sum += split_bytes(M, N, K) / sizeof(float);
+            joins.job[n] = Join{o.sum, split.parts, N, M, out, ld};
+            joins.first[n + 1] = joins.first[n] + (int)blocks_for(N * ((M + 3) / 4));
+            ++n;
+        }
+        side = ffn_side<FfnTerms<T>::planes>(M, N, o.splits);
+        return job_of(x, y, M, N, K, side, o);
+    }
+    void join(hipStream_t s)
+    {
+        if (!n) return;
+        for (int k = n; k < 3; ++k) joins.first[k + 1] = joins.first[k];
+        hipLaunchKernelGGL(k_ffn_join<T>, dim3((unsigned)joins.first[n]), dim3(256), 0, s, joins);
+    }
+};
 
 template <class T>
 hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
@@ -609,13 +715,14 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
     pack.run(s);
     FfnOut o{};
     o.rows = a.n;
+    o.splits = 1;
     o.F = a.F;
     o.act = a.act;
     o.pre = a.pre;
     o.ld_pre = a.ld_pre;
     o.mid = p.mid;
-    o.ld_mid = p.Fp;
-    o.plane_mid = a.n * p.Fp;
+    o.ld_mid = p.ldF;
+    o.plane_mid = a.n * p.ldF;
     const int64_t M = 2 * up(a.F, 32);
     bool done = false;
     if constexpr (PL == 1) {
@@ -625,8 +732,12 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
         }
     }
     if (!done) product<T, false, false, FFN_IN, false>(w_in, x, M, a.n, p.Dp, o, s);
-    const Operand mid{p.mid, p.Fp, a.n * p.Fp, a.n, p.Fp};
-    output<T, false, false>(w_out, mid, a.D, a.n, p.Fp, p.sum, a.y, a.ld_y, s);
+    const Operand mid{p.mid, p.ldF, o.plane_mid, a.n, p.Fp};
+    Outputs<T> out{p.sum};
+    int64_t side;
+    const FfnJob y = out(w_out, mid, a.D, a.n, p.Fp, a.y, a.ld_y, side);
+    launch<T, false, false, FFN_OUT, false>(y, side, s);
+    out.join(s);
     return hipGetLastError();
 }
 
@@ -641,26 +752,37 @@ hipError_t ffn_backward(const FfnArgs &a, int dtype, hipStream_t s)
     const Operand w_in = pack(a.w_in, a.ld_in, 2 * a.F, a.D, p.w_in, p.Dp, 0);
     const Operand w_out = pack(a.w_out, a.ld_out, a.D, a.F, p.w_out, p.Fp, 0);
     // the products along dp's columns meet its padding
-    if (p.Pp > 2 * a.F) pack.add(Pack{nullptr, 0, a.n, 0, p.dpre + p.Pp - kPad, kPad, p.Pp, a.n * p.Pp, 0});
+    if (p.Pp > 2 * a.F) pack.add(Pack{nullptr, 0, a.n, 0, p.dpre + p.Pp - kPad, kPad, p.ldP, a.n * p.ldP, 0});
     pack.run(s);
     FfnOut o{};
     o.rows = a.n;
+    o.splits = 1;
     o.cols = o.F = a.F;
     o.act = a.act;
     o.pre = a.pre;
     o.ld_pre = a.ld_pre;
     o.mid = p.mid;
-    o.ld_mid = p.Fp;
-    o.plane_mid = a.n * p.Fp;
+    o.ld_mid = p.ldF;
+    o.plane_mid = a.n * p.ldF;
     o.dpre = p.dpre;
-    o.ld_dpre = p.Pp;
-    o.plane_dpre = a.n * p.Pp;
+    o.ld_dpre = p.ldP;
+    o.plane_dpre = a.n * p.ldP;
     product<T, true, false, FFN_MID, false>(w_out, gy, a.F, a.n, p.Dp, o, s);
-    const Operand mid{p.mid, p.Fp, o.plane_mid, a.n, p.Fp}, dpre{p.dpre, p.Pp, o.plane_dpre, a.n, p.Pp};
+    const Operand mid{p.mid, p.ldF, o.plane_mid, a.n, p.Fp}, dpre{p.dpre, p.ldP, o.plane_dpre, a.n, p.Pp};
     const int64_t rows = up(a.n, kPad);
-    output<T, true, false>(w_in, dpre, a.D, a.n, p.Pp, p.sum, a.gx, a.ld_gx, s);
-    output<T, true, true>(x, dpre, a.D, 2 * a.F, rows, p.sum, a.gw_in, a.ld_gin, s);
-    output<T, true, true>(mid, gy, a.F, a.D, rows, p.sum, a.gw_out, a.ld_gout, s);
+    Outputs<T> out{p.sum};
+    int64_t side_x, side_in, side_out;
+    const FfnGrads g{out(w_in, dpre, a.D, a.n, p.Pp, a.gx, a.ld_gx, side_x),
+                     out(x, dpre, a.D, 2 * a.F, rows, a.gw_in, a.ld_gin, side_in),
+                     out(mid, gy, a.F, a.D, rows, a.gw_out, a.ld_gout, side_out)};
+    if (side_x == 128 && side_in == 128 && side_out == 128) {
+        hipLaunchKernelGGL((k_ffn_grads<T, 2, 2>), dim3(g.x.grid + g.w_in.grid + g.w_out.grid), dim3(256), 0, s, g);
+    } else {
+        launch<T, true, false, FFN_OUT, false>(g.x, side_x, s);
+        launch<T, true, true, FFN_OUT, false>(g.w_in, side_in, s);
+        launch<T, true, true, FFN_OUT, false>(g.w_out, side_out, s);
+    }
+    out.join(s);
     return hipGetLastError();
 }
 

@@ -189,7 +189,7 @@ __device__ __forceinline__ void fragments(const char *lds, int r0, int ks, s16x8
 
 constexpr int kPatchM = 8, kPatchN = 4; // tiles that one XCD works on at a time
 
-// Tile (and split of the sum) of a thread block.  Consecutive blocks go to the
+// Tile (and split of the sum) of block b of a grid.  Consecutive blocks go to the
 // eight XCDs in turn.  Grids of many rounds: each XCD takes patches of kPatchM x
 // kPatchN tiles (its 32 compute units) whose operands meet in its L2, and the
 // patches that run at the same time lie along n, where they share the X operand
@@ -199,9 +199,10 @@ __host__ __device__ inline bool in_patches(int64_t mt, int64_t nt)
 {
     return mt >= kPatchM && nt >= kPatchN && mt * nt >= 4 * kCUs;
 }
-__device__ __forceinline__ bool tile_of(int64_t mt, int64_t nt, int splits, int64_t &m, int64_t &n, int &split)
+__device__ __forceinline__ bool tile_of(int64_t b, int64_t grid, int64_t mt, int64_t nt, int splits, int64_t &m,
+                                        int64_t &n, int &split)
 {
-    const int64_t b = blockIdx.x, local = b >> 3;
+    const int64_t local = b >> 3;
     split = 0;
     if (in_patches(mt, nt)) {
         constexpr int P = kPatchM * kPatchN;
@@ -211,7 +212,7 @@ __device__ __forceinline__ bool tile_of(int64_t mt, int64_t nt, int splits, int6
         n = patch % pn * kPatchN + in / kPatchM;
         return m < mt && n < nt;
     }
-    const int64_t id = (b & 7) * (gridDim.x >> 3) + local, t = id % (mt * nt);
+    const int64_t id = (b & 7) * (grid >> 3) + local, t = id % (mt * nt);
     split = (int)(id / (mt * nt));
     m = t % mt;
     n = t / mt;

@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256, 1) void k_product(Operand X, Operand Y, int64_
     __shared__ __align__(16) char lds3[NB == 4 ? STAGE : 16];
     int64_t mi, ni;
     int sp;
-    if (!tile_of(mt, nt, OUT == OUT_SUM ? o.splits : 1, mi, ni, sp)) return;
+    if (!tile_of(blockIdx.x, gridDim.x, mt, nt, OUT == OUT_SUM ? o.splits : 1, mi, ni, sp)) return;
     if constexpr (OUT == OUT_SUM) { // this split's part of the sum (X is turned)
         const int64_t k0 = sp * o.split_k;
         if (k0 >= K) return;
