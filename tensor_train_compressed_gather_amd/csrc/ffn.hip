@@ -169,19 +169,21 @@ struct PairLoader {
     typedef TileLds<false, R, 64> L;
     static constexpr int N = L::vecs;
     const short *gate, *up;
-    int whole;
+    int at, all, todo; // as in TileLoader, going round
     unsigned bytes;
     int off, step, to;
 
-    __device__ __forceinline__ PairLoader(const Operand &a, int64_t F, int64_t r0, int stages)
+    __device__ __forceinline__ PairLoader(const Operand &a, int64_t F, int64_t r0, int stages, int first)
     {
         const int ld = (int)a.ld;
         const int64_t f0 = r0 / 2;
         const int rows = (int)(F - f0 < R / 2 ? F - f0 : R / 2);
-        gate = a.p + f0 * a.ld;
+        gate = a.p + f0 * a.ld + first * 64;
         up = gate + F * a.ld;
-        whole = rows > 0 ? stages : 0;
-        bytes = (unsigned)((rows - 1) * ld + (int)a.cols) * 2;
+        at = first;
+        all = stages;
+        todo = rows > 0 ? stages : 0;
+        bytes = (unsigned)((rows - 1) * ld + (int)a.cols) * 2 - first * 128;
         const int t = threadIdx.x, row = t / 8;
         off = (row * ld + ((t % 8) ^ L::turn(row)) * 8) * 2;
         step = 32 * ld * 2;
@@ -189,7 +191,7 @@ struct PairLoader {
     }
     __device__ __forceinline__ void load(char *lds)
     {
-        const unsigned now = whole > 0 ? bytes : 0;
+        const unsigned now = todo > 0 ? bytes : 0;
         const __amdgpu_buffer_rsrc_t g =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(gate), 0, now, 0x00027000);
         const __amdgpu_buffer_rsrc_t u = __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(up), 0, now, 0x00027000);
@@ -199,8 +201,14 @@ struct PairLoader {
                                                      i / 2 * step, 0, 0);
         gate += 64;
         up += 64;
-        --whole;
         bytes -= 128;
+        --todo;
+        if (++at == all) {
+            at = 0;
+            gate -= all * 64;
+            up -= all * 64;
+            bytes += all * 128;
+        }
     }
 };
 
@@ -252,6 +260,43 @@ struct FfnLds {
     static constexpr int first = part > stage ? part : stage, more = NB == 4 ? stage : 16; // of two buffers each
 };
 
+// Which of the eight XCDs takes which tiles of a small grid: ranges of the tiles
+// along m (p of them) and n (q) and of the sum's splits (r), p q r = 8, so that an
+// XCD's L2 reads few rows of both operands.
+struct XcdParts {
+    int p, q, r;
+};
+__device__ __forceinline__ bool xcd_tile(const XcdParts &x, unsigned block, int mt, int nt, int splits, int64_t &m,
+                                         int64_t &n, int &split)
+{
+    const int xcd = block & 7, local = (int)(block >> 3);
+    const int ri = xcd % x.r, qi = xcd / x.r % x.q, pi = xcd / (x.r * x.q);
+    const int m0 = pi * mt / x.p, n0 = qi * nt / x.q, s0 = ri * splits / x.r;
+    const int dm = (pi + 1) * mt / x.p - m0, dn = (qi + 1) * nt / x.q - n0, ds = (ri + 1) * splits / x.r - s0;
+    if (local >= dm * dn * ds) return false;
+    m = m0 + local % dm;
+    n = n0 + local / dm % dn;
+    split = s0 + local / (dm * dn);
+    return true;
+}
+inline XcdParts xcd_parts(int64_t mt, int64_t nt, int64_t splits, unsigned &grid)
+{
+    XcdParts best{1, 1, 8};
+    int64_t cost = -1;
+    for (int p = 1; p <= 8; p *= 2)
+        for (int q = 1; p * q <= 8; q *= 2) {
+            const int r = 8 / (p * q);
+            const int64_t dm = (mt + p - 1) / p, dn = (nt + q - 1) / q, ds = (splits + r - 1) / r;
+            // the longest XCD's work, then the operands' rows that it reads
+            const int64_t c = (dm * dn * ds * 8 + 31) / 32 * 4096 + (dm + dn) * ds;
+            if (cost >= 0 && c >= cost) continue;
+            cost = c;
+            best = {p, q, r};
+            grid = (unsigned)(8 * dm * dn * ds);
+        }
+    return best;
+}
+
 // A tile of one product: M outputs (along X's rows or columns) in each of N rows,
 // K summed values, mt x nt tiles taken by `grid` blocks.  PAIRED: X is W_in as it
 // lies in memory.
@@ -259,6 +304,7 @@ struct FfnJob {
     Operand X, Y;
     int64_t K, mt, nt;
     unsigned grid;
+    XcdParts xcds;
     FfnOut o;
 };
 template <class T, bool XT, bool YT, int OUT, bool PAIRED, int NI, int NJ>
@@ -273,7 +319,11 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
     const FfnOut &o = job.o;
     int64_t mi, ni, K = job.K;
     int sp;
-    if (!tile_of(block, job.grid, job.mt, job.nt, OUT == FFN_OUT ? o.splits : 1, mi, ni, sp)) return;
+    if (in_patches(job.mt, job.nt)) {
+        if (!tile_of(block, job.grid, job.mt, job.nt, 1, mi, ni, sp)) return;
+    } else if (!xcd_tile(job.xcds, block, (int)job.mt, (int)job.nt, OUT == FFN_OUT ? o.splits : 1, mi, ni, sp)) {
+        return;
+    }
     float *sum = nullptr;
     if (OUT == FFN_OUT && o.sum) { // this split's part of the sum
         const int64_t k0 = sp * o.split_k;
@@ -333,12 +383,17 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
     load_pre(std::integral_constant<int, 0>()); // (there long before the products are)
     {
         const int stages = (int)(K / BK);
-        TileLoader<YT, TN, BK, PL> y(Y, n0, stages);
+        // Tiles begin at different places of the sum where rows lie along it: rows a
+        // multiple of a KB apart meet in few channels of the L2 (8192 x 4096 x 16384:
+        // p and a 2.06 -> 1.94 ms, y 1.09 -> 0.98).  Small grids gain nothing.
+        constexpr bool ROT = !YT && NI == 4;
+        const int first = ROT ? (int)((8 * mi + ni) & 31) % stages : 0;
+        TileLoader<YT, TN, BK, PL, ROT> y(Y, n0, stages, first);
         if constexpr (PAIRED) {
-            PairLoader<TM> x(X, o.F, m0, stages);
+            PairLoader<TM> x(X, o.F, m0, stages, first);
             multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
         } else {
-            TileLoader<XT, TM, BK, PL> x(X, m0, stages);
+            TileLoader<XT, TM, BK, PL, ROT> x(X, m0, stages, first);
             multiply<E, PL, XT, YT>(x, y, stages, lds0, lds1, lds2, lds3, acc);
         }
     }
@@ -504,6 +559,178 @@ __global__ __launch_bounds__(256) void k_ffn_clear(T *p, int64_t ld, int64_t row
         p[c / cols * ld + c % cols] = (T)0.f;
 }
 
+// --------------------------------------------------------------- few rows
+
+// Products of few rows, forward: the weight's bytes bound them, so it is read
+// once, as it lies in memory, straight into the registers of the matrix
+// instructions (16x16x32, fp32 16x16x4), and rows of any place and length serve.
+// A block has 16 rows of the weight (PAIR: 16 of each projection) and 16 NB rows
+// of the operand; its waves take chunks of the sum in turn, the next chunk's
+// loads in flight while one is multiplied, and meet in LDS.  Lane l holds row l %
+// 16 and the l / 16-th 16 bytes of each 64 of a chunk.
+//
+// Blocks begin at different places of the sum: rows lie a multiple of a KB apart
+// as a rule, and equal columns of all of them meet in few channels of the L2 (4
+// rows of 4096 x 16384 bf16: 84 us when all begin with the first, 72 so, 5.6 TB/s).
+struct FewArgs {
+    const void *w, *x;
+    int64_t ld_w, ld_x;
+    int64_t K, split_k; // summed values, of a block
+    int64_t n, rows;    // operand rows; outputs (PAIR: of each projection)
+    int act;
+    float *pre;
+    int64_t ld_pre;
+    void *out;          // a (PAIR) or y
+    int64_t ld_out;
+    float *sum;         // [splits][n][rows]
+};
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <class T>
+struct FewStep {
+    static constexpr int VEC = 16 / (int)sizeof(T), K = 4 * VEC; // values of a load, of a step
+    typedef typename VecOf<T, VEC>::raw raw;
+    static __device__ __forceinline__ f32x4 mma(raw a, raw b, f32x4 c)
+    {
+        if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+            return c;
+        } else if constexpr (std::is_same<T, bf16>::value) {
+            return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+        } else {
+            return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+        }
+    }
+};
+
+template <class T, bool PAIR, int NB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
+{
+    typedef FewStep<T> Step;
+    typedef typename VecOf<T, Step::VEC>::type vec;
+    constexpr int MB = PAIR ? 2 : 1, U = NB > 4 ? 2 : 4, CHUNK = U * Step::K, P = 16 * MB + 4;
+    __shared__ __align__(16) float red[WAVES][16 * NB][P];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m0 = (int64_t)blockIdx.x * 16, k0 = blockIdx.y * a.split_k;
+    const int64_t K = a.K - k0 < a.split_k ? a.K - k0 : a.split_k;
+    const int at = (lane >> 4) * Step::VEC;
+    const T *w[MB], *x[NB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        const int64_t r = m0 + (lane & 15);
+        w[b] = static_cast<const T *>(a.w) + ((r < a.rows ? r : a.rows - 1) + b * a.rows) * a.ld_w + k0 + at;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int64_t r = b * 16 + (lane & 15);
+        x[b] = static_cast<const T *>(a.x) + (r < a.n ? r : a.n - 1) * a.ld_x + k0 + at;
+    }
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Regs {
+        typename Step::raw w[MB][U], x[NB][U];
+    };
+    auto load = [&](int64_t k, Regs &r) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int b = 0; b < MB; ++b) r.w[b][u] = *reinterpret_cast<const vec *>(w[b] + k + u * Step::K);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) r.x[b][u] = *reinterpret_cast<const vec *>(x[b] + k + u * Step::K);
+        }
+    };
+    auto mma = [&](const Regs &r) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = Step::mma(r.w[i][u], r.x[j][u], acc[i][j]);
+    };
+    const int chunks = (int)(K / CHUNK), first = chunks ? (int)(blockIdx.x * 5 % (unsigned)chunks) : 0;
+    auto place = [&](int c) { return (int64_t)(c + first < chunks ? c + first : c + first - chunks) * CHUNK; };
+    Regs one, two;
+    int c = wave;
+    if (c < chunks) load(place(c), one);
+    while (c < chunks) { // (a chunk past the last is the last again, and not used)
+        const int c1 = c + WAVES, c2 = c + 2 * WAVES;
+        load(place(c1 < chunks ? c1 : c), two);
+        __builtin_amdgcn_sched_barrier(0); // (the loads would be moved behind the products, to save registers)
+        mma(one);
+        if (c1 >= chunks) break;
+        load(place(c2 < chunks ? c2 : c1), one);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(two);
+        c = c2;
+    }
+    if (wave == chunks % WAVES) { // the rest of the sum, zeros past its end
+        for (int64_t k = (int64_t)chunks * CHUNK; k < K; k += Step::K) {
+            const int64_t left = K - k - at;
+            typename Step::raw p[MB], q[NB];
+            auto part = [&](const T *row) {
+                typename Step::raw v;
+#pragma unroll
+                for (int e = 0; e < Step::VEC; ++e) v[e] = e < left ? row[k + e] : (T)0.f;
+                return v;
+            };
+#pragma unroll
+            for (int b = 0; b < MB; ++b) p[b] = part(w[b]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) q[b] = part(x[b]);
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) acc[i][j] = Step::mma(p[i], q[j], acc[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            *reinterpret_cast<f32x4 *>(&red[wave][j * 16 + (lane & 15)][i * 16 + (lane >> 4) * 4]) = acc[i][j];
+    __syncthreads();
+    // eight outputs of a row per thread
+    for (int e = threadIdx.x; e < 16 * NB * 2; e += 64 * WAVES) {
+        const int64_t i = e >> 1, m = m0 + (e & 1) * 8;
+        const int left = (int)(a.rows - m < 8 ? a.rows - m : 8);
+        if (i >= a.n || left <= 0) continue;
+        float v[MB][8];
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[b][q] = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < WAVES; ++s)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                float y[8];
+                load_vec<float, 8>(&red[s][i][b * 16 + (e & 1) * 8], y);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[b][q] += y[q];
+            }
+        if constexpr (PAIR) {
+            if (a.pre) {
+                store_part<float, 8>(a.pre + i * a.ld_pre + m, left, v[0]);
+                store_part<float, 8>(a.pre + i * a.ld_pre + a.rows + m, left, v[1]);
+            }
+            float value[8], slope[8];
+            activations<sizeof(T) == 2>(a.act, v[0], value, slope);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) value[q] *= v[1][q];
+            store_part<T, 8>(static_cast<T *>(a.out) + i * a.ld_out + m, left, value);
+        } else if (a.sum) {
+            store_part<float, 8>(a.sum + (blockIdx.y * a.n + i) * a.rows + m, left, v[0]);
+        } else {
+            store_part<T, 8>(static_cast<T *>(a.out) + i * a.ld_out + m, left, v[0]);
+        }
+    }
+}
+
 // ------------------------------------------------------------ host: plans
 
 unsigned blocks_for(int64_t threads)
@@ -541,6 +768,27 @@ size_t split_bytes(int64_t M, int64_t N, int64_t K)
     return s.parts > 1 ? round256((size_t)s.parts * M * N * sizeof(float)) : 0;
 }
 
+// Forward products of few rows take kernels of their own: 16-bit rows up to 16
+// (4096 x 16384: 1 row 72 us, 16 rows 90, 17 rows 124 and by tiles 106), fp32 rows
+// up to 128, whose tiles take a split copy of the weights (4 rows 147 us).
+inline bool few_rows(int64_t n, bool fp32) { return n <= (fp32 ? 128 : 16); }
+// Parts of a sum of K values that leave through `rows` columns: a block for each
+// compute unit, of 256 summed values at least.
+FfnSplit few_split(int64_t rows, int64_t K)
+{
+    const int64_t blocks = (rows + 15) / 16;
+    int64_t s = kCUs / blocks;
+    if (s > K / 256) s = K / 256;
+    if (s < 1) s = 1;
+    const int64_t each = up((K + s - 1) / s, 128);
+    return {(int)((K + each - 1) / each), each};
+}
+size_t few_bytes(int64_t n, int64_t rows, int64_t K)
+{
+    const FfnSplit s = few_split(rows, K);
+    return s.parts > 1 ? round256((size_t)s.parts * n * rows * sizeof(float)) : 0;
+}
+
 // Whether an operand serves as it lies in memory: 16-bit rows at multiples of 16
 // bytes (further apart they would pass the 31 bits of a tile's loads) and of whole
 // pieces of 16 bytes, or where they lie along the sum of whole steps: a piece that
@@ -553,9 +801,10 @@ bool lies_well(const void *p, int64_t ld)
 struct FfnCopies {
     bool x, w_in, w_out, gy;
 };
-FfnCopies ffn_copies(bool fp32, bool grad, int64_t D, int64_t F, bool x, bool w_in, bool w_out, bool gy)
+FfnCopies ffn_copies(bool fp32, bool grad, int64_t n, int64_t D, int64_t F, bool x, bool w_in, bool w_out, bool gy)
 {
     const bool d = D % kPad == 0, f = F % kPad == 0;
+    if (!grad && few_rows(n, fp32)) return {false, false, false, false};
     if (fp32) return {true, true, true, true};
     if (grad) return {!x || D % 8, !w_in || D % 8, !w_out || F % 8, !gy || !d}; // only gy lies along a sum
     return {!x || !d, !w_in || !d, !w_out || !f, false};
@@ -599,7 +848,7 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
         p.dpre = take(n, p.ldP);
         sums = split_bytes(D, n, p.Pp) + split_bytes(D, 2 * F, up(n, kPad)) + split_bytes(F, D, up(n, kPad));
     } else {
-        sums = split_bytes(D, n, p.Fp);
+        sums = few_rows(n, PL > 1) ? few_bytes(n, D, F) : split_bytes(D, n, p.Fp);
     }
     p.sum = reinterpret_cast<float *>(base ? base + off : nullptr);
     off += sums;
@@ -608,7 +857,7 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
 }
 FfnCopies copies_of(const FfnArgs &a, int dtype, bool grad)
 {
-    return ffn_copies(dtype == TT_EMB_DTYPE_FLOAT, grad, a.D, a.F, lies_well(a.x, a.ld_x), lies_well(a.w_in, a.ld_in),
+    return ffn_copies(dtype == TT_EMB_DTYPE_FLOAT, grad, a.n, a.D, a.F, lies_well(a.x, a.ld_x), lies_well(a.w_in, a.ld_in),
                       lies_well(a.w_out, a.ld_out), lies_well(a.gy, a.ld_gy));
 }
 
@@ -644,7 +893,10 @@ struct Packing {
 FfnJob job_of(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, int64_t side, const FfnOut &o)
 {
     const int64_t mt = (M + side - 1) / side, nt = (N + side - 1) / side;
-    return FfnJob{x, y, K, mt, nt, tile_grid(mt, nt, o.splits), o};
+    FfnJob job{x, y, K, mt, nt, 0, {}, o};
+    if (in_patches(mt, nt)) job.grid = tile_grid(mt, nt, 1);
+    else job.xcds = xcd_parts(mt, nt, o.splits, job.grid);
+    return job;
 }
 
 template <class T, bool XT, bool YT, int OUT, bool PAIRED>
@@ -703,9 +955,71 @@ struct Outputs {
     }
 };
 
+template <class T, bool PAIR>
+void few(const FewArgs &a, int splits, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.rows + 15) / 16), (unsigned)splits);
+    constexpr std::integral_constant<int, 4> four;
+    constexpr std::integral_constant<int, 8> eight;
+    const bool idle = (int64_t)grid.x * splits <= 2 * kCUs; // few blocks: more waves in each
+    auto run = [&](auto nb, auto waves) {
+        constexpr int NB = decltype(nb)::value, WAVES = decltype(waves)::value;
+        hipLaunchKernelGGL((k_ffn_few<T, PAIR, NB, WAVES>), grid, dim3(64 * WAVES), 0, s, a);
+    };
+    if constexpr (sizeof(T) == 4) {
+        if (a.n > 64) return run(std::integral_constant<int, 8>(), four);
+        if (a.n > 32) return idle ? run(four, eight) : run(four, four);
+        if (a.n > 16) return idle ? run(std::integral_constant<int, 2>(), eight) : run(std::integral_constant<int, 2>(), four);
+    }
+    constexpr std::integral_constant<int, 1> one;
+    return idle ? run(one, eight) : run(one, four);
+}
+
+template <class T>
+hipError_t ffn_few(const FfnArgs &a, int dtype, hipStream_t s)
+{
+    const FfnPlan p = plan_ffn(a.n, a.D, a.F, FfnTerms<T>::planes, false, copies_of(a, dtype, false), a.ws);
+    FewArgs in{};
+    in.w = a.w_in;
+    in.ld_w = a.ld_in;
+    in.x = a.x;
+    in.ld_x = a.ld_x;
+    in.K = in.split_k = a.D;
+    in.n = a.n;
+    in.rows = a.F;
+    in.act = a.act;
+    in.pre = a.pre;
+    in.ld_pre = a.ld_pre;
+    in.out = p.mid;
+    in.ld_out = p.ldF;
+    few<T, true>(in, 1, s);
+    FewArgs out{};
+    out.w = a.w_out;
+    out.ld_w = a.ld_out;
+    out.x = p.mid;
+    out.ld_x = p.ldF;
+    out.K = a.F;
+    out.n = a.n;
+    out.rows = a.D;
+    out.out = a.y;
+    out.ld_out = a.ld_y;
+    const FfnSplit split = few_split(a.D, a.F);
+    out.split_k = split.each;
+    if (split.parts > 1) out.sum = p.sum;
+    few<T, false>(out, split.parts, s);
+    if (split.parts > 1) {
+        Joins j{};
+        j.job[0] = Join{p.sum, split.parts, a.n, a.D, a.y, a.ld_y};
+        j.first[1] = j.first[2] = j.first[3] = (int)blocks_for(a.n * ((a.D + 3) / 4));
+        hipLaunchKernelGGL(k_ffn_join<T>, dim3((unsigned)j.first[1]), dim3(256), 0, s, j);
+    }
+    return hipGetLastError();
+}
+
 template <class T>
 hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
 {
+    if (few_rows(a.n, FfnTerms<T>::planes > 1)) return ffn_few<T>(a, dtype, s);
     constexpr int PL = FfnTerms<T>::planes;
     const FfnPlan p = plan_ffn(a.n, a.D, a.F, PL, false, copies_of(a, dtype, false), a.ws);
     Packing<T> pack;
@@ -803,7 +1117,7 @@ hipError_t ffn_clear(const FfnArgs &a, hipStream_t s)
 size_t ffn_workspace(int64_t n, int64_t D, int64_t F, int dtype, int what)
 {
     const bool fp32 = dtype == TT_EMB_DTYPE_FLOAT, grad = what & TT_EMB_FFN_GRAD, well = what & TT_EMB_FFN_ALIGNED;
-    return plan_ffn(n, D, F, fp32 ? 3 : 1, grad, ffn_copies(fp32, grad, D, F, well, well, well, well), nullptr).bytes;
+    return plan_ffn(n, D, F, fp32 ? 3 : 1, grad, ffn_copies(fp32, grad, n, D, F, well, well, well, well), nullptr).bytes;
 }
 
 size_t ffn_needs(const FfnArgs &a, int dtype, bool grad)

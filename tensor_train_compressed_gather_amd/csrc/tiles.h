@@ -89,7 +89,8 @@ typedef __attribute__((address_space(3))) void *lds_void;
 // that ends with the matrix, so rows past it (of the outputs or of the summed
 // index) are written as zeros and no address needs a clamp; so are stages past
 // the last.  What a stage's descriptor takes is kept up by additions.
-template <bool TURNED, int R, int BK, int PL>
+// ROT: the stages begin with `first` and go round.
+template <bool TURNED, int R, int BK, int PL, bool ROT = false>
 struct TileLoader {
     typedef TileLds<TURNED, R, BK> L;
     static constexpr int N = L::vecs, ROWV = L::pitch / 16; // pieces in a tile's row
@@ -99,8 +100,9 @@ struct TileLoader {
     unsigned bytes, rest; // of those, of the one at the matrix's end (turned)
     int off;            // byte offset of this thread's first piece; the others are 256 / ROWV rows apart
     int step, to;       // to: the wave's place in LDS
+    int at, all, todo;  // ROT: the next stage's number, of how many, stages to come (whole: those before the rest)
 
-    __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0, int stages)
+    __device__ __forceinline__ TileLoader(const Operand &a, int64_t r0, int stages, int first = 0)
     {
         const int ld = (int)a.ld;
         plane = a.plane;
@@ -122,10 +124,18 @@ struct TileLoader {
         off = (row * ld + ((t % ROWV) ^ L::turn(row)) * 8) * 2;
         step = 256 / ROWV * ld * 2;
         to = __builtin_amdgcn_readfirstlane(t >> 6) * 1024;
+        if constexpr (ROT) {
+            at = first;
+            all = todo = stages;
+            p += first * next;
+            if constexpr (!TURNED) bytes -= first * BK * 2;
+        }
     }
     __device__ __forceinline__ void load(char *lds)
     {
-        const unsigned now = whole > 0 ? bytes : whole == 0 ? rest : 0;
+        unsigned now;
+        if constexpr (ROT) now = todo <= 0 ? 0 : at < whole ? bytes : at == whole ? rest : 0;
+        else now = whole > 0 ? bytes : whole == 0 ? rest : 0;
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
             const __amdgpu_buffer_rsrc_t r =
@@ -136,8 +146,17 @@ struct TileLoader {
                                                          i * step, 0, 0);
         }
         p += next;
-        --whole;
         if constexpr (!TURNED) bytes -= BK * 2;
+        if constexpr (ROT) {
+            --todo;
+            if (++at == all) {
+                at = 0;
+                p -= all * next;
+                if constexpr (!TURNED) bytes += all * BK * 2;
+            }
+        } else {
+            --whole;
+        }
     }
 };
 

@@ -147,9 +147,9 @@ def check(n, D, F, t, gap, kind, seed=None):
 
 
 SHAPES = [(1, 1, 1, 0), (1, 64, 64, 0), (2, 8, 40, 0), (3, 17, 5, 3), (5, 100, 33, 1), (31, 128, 64, 0),
-          (64, 64, 128, 8), (65, 130, 250, 0), (127, 256, 129, 0), (128, 72, 96, 0), (129, 264, 320, 8),
+          (64, 64, 128, 8), (12, 1000, 4096, 0), (65, 130, 250, 0), (127, 256, 129, 0), (128, 72, 96, 0), (129, 264, 320, 8),
           (200, 1000, 70, 0), (257, 520, 300, 5), (600, 96, 1100, 0), (40, 2000, 3000, 0), (1030, 200, 200, 1),
-          (16, 640, 1280, 0), (17, 192, 2048, 0), (9, 4096, 100, 0)]
+          (16, 640, 1280, 0), (17, 192, 2048, 0), (9, 4096, 100, 0), (33, 200, 5000, 0), (100, 1024, 1500, 0), (4, 130, 9000, 3)]
 
 
 @pytest.mark.gpu
