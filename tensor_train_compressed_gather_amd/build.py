@@ -13,7 +13,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtt_emb.so")
 SOURCES = ["api.hip", "group.hip", "forward.hip", "backward.hip", "kcores.hip", "misc.hip", "peak.hip",
            "lookup.hip", "norm.hip", "blocknorm.hip", "blocknorm_bwd.hip", "adamw.hip", "clip.hip", "xent.hip",
-           "ffn.hip", "lm_api.hip"]
+           "ffn.hip", "ffn_bwd.hip", "lm_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "-O3", "--offload-arch=gfx950", "-fPIC", "-std=c++17",

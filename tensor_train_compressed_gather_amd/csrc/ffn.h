@@ -1,0 +1,809 @@
+// ffn.h -- the gated feed-forward block (gfx950): the products of its forward and
+// its backward.
+//
+//   p = x W_in^T [n][2F] (the gate's F columns, then the other projection's)
+//   a = act(p_g) p_u,  y = a W_out^T
+//   da = gy W_out,  dp_g = da p_u act'(p_g),  dp_u = da act(p_g)
+//   dx = dp W_in,  dW_in = dp^T x,  dW_out = gy^T a
+//
+// Six products by the tiles of tiles.h.  A tile of the first has rows of the
+// gate and of the other projection in turn, 32 of each, so that both halves of
+// a value of `a` meet in one thread: p leaves the registers only where the
+// caller keeps it for the backward.  The backward's first product makes da, and
+// dp and a from it and p, in the tile that holds da.  Matrix instructions bound
+// the large sizes.
+//
+// bf16 and fp16: a and dp are rounded to the inputs' type, half a step each,
+// because the products that take them have operands of 16 bits; two terms of
+// them would double two thirds of the products.  Both are made from p before its
+// rounding in the forward, after it in the backward.
+//
+// fp32: every operand is split into three bf16 terms (24 bits, the range of
+// fp32), and the six products of terms above 2^-25 are added up: the rounding of
+// fp32 products, at 1 / 6 of the bf16 rate, where the fp32 matrix instructions
+// have 1 / 16 of it.
+#pragma once
+
+#include "tiles.h"
+
+#include <utility>
+
+namespace ttemb {
+
+namespace {
+
+constexpr int64_t kPad = 64;       // summed values of packed rows are padded to this
+constexpr int64_t kSplit = 512;    // least summed values of a split
+constexpr int kPacks = 5;          // copies that one launch makes, at most
+
+template <class T>
+struct FfnTerms {
+    typedef T type;
+    static constexpr int planes = 1;
+};
+template <>
+struct FfnTerms<float> {
+    typedef bf16 type;
+    static constexpr int planes = 3;
+};
+
+// ------------------------------------------------------------- activations
+
+// The values of the activation at z, and its slopes.  gelu's tanh form is z times
+// the sigmoid of twice the argument, 2 sqrt(2 / pi) (z + 0.044715 z^3).  NEAR: for
+// results that are rounded to 16 bits, with the hardware's exponential and
+// reciprocal (off by some 2^-22 of the value) and, for the normal distribution's
+// integral, formula 7.1.26 of Abramowitz and Stegun (off by 1.5e-7).
+template <bool NEAR>
+__device__ __forceinline__ void activations(int act, const float (&z)[8], float (&value)[8], float (&slope)[8])
+{
+    if (act == TT_EMB_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float c, e;
+            if constexpr (NEAR) {
+                e = __builtin_amdgcn_exp2f(-0.72134752f * z[i] * z[i]);
+                const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678f, fabsf(z[i]), 1.f));
+                float q = fmaf(t, 1.061405429f, -1.453152027f);
+                q = fmaf(t, q, 1.421413741f);
+                q = fmaf(t, q, -0.284496736f);
+                q = fmaf(t, q, 0.254829592f) * t * 0.5f * e;
+                c = z[i] < 0.f ? q : 1.f - q;
+            } else {
+                e = expf(-0.5f * z[i] * z[i]);
+                c = 0.5f * erfcf(-0.70710678f * z[i]); // (1 + erf would lose the small values)
+            }
+            value[i] = z[i] * c;
+            slope[i] = fmaf(z[i], 0.39894228f * e, c);
+        }
+        return;
+    }
+    const float cube = act == TT_EMB_ACT_GELU_TANH ? 0.044715f : 0.f, by = cube ? 1.59576912f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float zz = cube * z[i] * z[i], x = by * fmaf(zz, z[i], z[i]), dx = by * fmaf(3.f, zz, 1.f);
+        const float e = NEAR ? __builtin_amdgcn_exp2f(-1.44269504f * fabsf(x)) : expf(-fabsf(x));
+        const float r = NEAR ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
+        const float sg = x < 0.f ? e * r : r, other = x < 0.f ? r : e * r; // sigmoid of x and of -x
+        value[i] = z[i] * sg;
+        slope[i] = fmaf(z[i] * dx, sg * other, sg);
+    }
+}
+
+// ------------------------------------------------------------------ copies
+
+// A matrix as planes of 16-bit terms whose rows of `ld` columns are zero past
+// the source's.  pair > 0: the source has 2 x pair rows, and 32 of the first
+// half and 32 of the second follow each other; rows past them are zeros.  No
+// source: zeros.
+struct Pack {
+    const void *src;
+    int64_t ld_src, rows, cols;
+    short *dst;
+    int64_t width, ld, plane, pair; // width: columns that are written
+};
+struct Packs {
+    Pack job[kPacks];
+    int first[kPacks + 1]; // first block of each
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_pack(Packs p)
+{
+    typedef typename FfnTerms<T>::type E;
+    constexpr int PL = FfnTerms<T>::planes;
+    int k = 0;
+    while (k + 1 < kPacks && (int)blockIdx.x >= p.first[k + 1]) ++k;
+    const Pack &j = p.job[k];
+    const int64_t chunks = j.width / 8, all = j.rows * chunks, step = (int64_t)(p.first[k + 1] - p.first[k]) * 256;
+    for (int64_t c = (int64_t)((int)blockIdx.x - p.first[k]) * 256 + threadIdx.x; c < all; c += step) {
+        const int64_t q = c / chunks, col = (c - q * chunks) * 8;
+        int64_t r = q;
+        bool in = true;
+        if (j.pair) {
+            const int64_t f = q / 64 * 32 + q % 32;
+            in = f < j.pair;
+            r = in ? f + (q & 32 ? j.pair : 0) : 0;
+        }
+        const int64_t left = in ? j.cols - col : 0;
+        float x[8];
+        load_part<T, 8>(static_cast<const T *>(j.src) + r * j.ld_src + (left > 0 ? col : 0),
+                        (int)(left < 0 ? 0 : left < 8 ? left : 8), x);
+        s16x8 w[PL];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            short s[PL];
+            split_terms<E, PL>(x[i], s);
+#pragma unroll
+            for (int t = 0; t < PL; ++t) w[t][i] = s[t];
+        }
+#pragma unroll
+        for (int t = 0; t < PL; ++t) *reinterpret_cast<s16x8 *>(j.dst + t * j.plane + q * j.ld + col) = w[t];
+    }
+}
+
+// ---------------------------------------------------------------- products
+
+// What a product's tiles become: a (and p), dp and a, or rows of an output (or
+// of a partial sum of it, where `sum` is set).
+enum { FFN_IN, FFN_MID, FFN_OUT };
+
+struct FfnOut {
+    int64_t rows, cols; // of the output
+    void *out;
+    int64_t ld_out;
+    float *sum; // [splits][rows][cols]
+    int splits;
+    int64_t split_k;
+    int64_t F;
+    int act;
+    float *pre; // [rows][2F]
+    int64_t ld_pre;
+    short *mid; // planes of [rows][ld_mid]
+    int64_t ld_mid, plane_mid;
+    short *dpre; // planes of [rows][ld_dpre]
+    int64_t ld_dpre, plane_dpre;
+};
+
+// Rows of both projections as they lie in memory, 32 of the one and 32 of the
+// other in turn: one load of a wave group fills 32 rows of a stage of 64 values.
+template <int R>
+struct PairLoader {
+    typedef TileLds<false, R, 64> L;
+    static constexpr int N = L::vecs;
+    const short *gate, *up;
+    int at, all, todo; // as in TileLoader, going round
+    unsigned bytes;
+    int off, step, to;
+
+    __device__ __forceinline__ PairLoader(const Operand &a, int64_t F, int64_t r0, int stages, int first)
+    {
+        const int ld = (int)a.ld;
+        const int64_t f0 = r0 / 2;
+        const int rows = (int)(F - f0 < R / 2 ? F - f0 : R / 2);
+        gate = a.p + f0 * a.ld + first * 64;
+        up = gate + F * a.ld;
+        at = first;
+        all = stages;
+        todo = rows > 0 ? stages : 0;
+        bytes = (unsigned)((rows - 1) * ld + (int)a.cols) * 2 - first * 128;
+        const int t = threadIdx.x, row = t / 8;
+        off = (row * ld + ((t % 8) ^ L::turn(row)) * 8) * 2;
+        step = 32 * ld * 2;
+        to = __builtin_amdgcn_readfirstlane(t >> 6) * 1024;
+    }
+    __device__ __forceinline__ void load(char *lds)
+    {
+        const unsigned now = todo > 0 ? bytes : 0;
+        const __amdgpu_buffer_rsrc_t g =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(gate), 0, now, 0x00027000);
+        const __amdgpu_buffer_rsrc_t u = __builtin_amdgcn_make_buffer_rsrc(const_cast<short *>(up), 0, now, 0x00027000);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(i & 1 ? u : g, (lds_void)(lds + i * 4096 + to), 16, off,
+                                                     i / 2 * step, 0, 0);
+        gate += 64;
+        up += 64;
+        bytes -= 128;
+        --todo;
+        if (++at == all) {
+            at = 0;
+            gate -= all * 64;
+            up -= all * 64;
+            bytes += all * 128;
+        }
+    }
+};
+
+// Eight values of a row as they leave.
+template <class T, int PL>
+__device__ __forceinline__ void store_terms(short *p, int64_t plane, int left, const float (&x)[8])
+{
+    typedef typename FfnTerms<T>::type E;
+    short w[PL][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        short s[PL];
+        split_terms<E, PL>(x[i], s);
+#pragma unroll
+        for (int q = 0; q < PL; ++q) w[q][i] = s[q];
+    }
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+        if (left >= 8) {
+            typedef s16x8 __attribute__((aligned(2))) any8;
+            s16x8 v;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = w[q][i];
+            *reinterpret_cast<any8 *>(p + q * plane) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) p[q * plane + i] = w[q][i];
+        }
+    }
+}
+
+// f for each of the numbers, as constants: a long loop's body may be left as a
+// loop, whose registers would then be memory.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// Shapes of a product's tiles, (64 NI) x (64 NJ).  BIG ones read each operand
+// least often.  Of SMALL ones a compute unit holds two, which hide each other's
+// loads, starts and ends; of DEEP ones, for grids that leave it no second, one
+// with more loads in flight.  Three terms take three times the LDS (and no DEEP
+// ones, which measured as SMALL ones do).
+enum { BIG, SMALL, DEEP };
+template <int PL, int SHAPE>
+struct FfnShape {
+    static constexpr int NI = SHAPE == BIG ? 4 : 2, NJ = PL == 1 ? NI : NI / 2, TM = 64 * NI, TN = 64 * NJ;
+};
+
+// LDS of a product's tiles.  A tile leaves through LDS in fp32, in parts of 64
+// rows and BP blocks of 32 columns of each half (as many as leave room for two
+// blocks of small tiles on a compute unit).
+template <int PL, bool XT, bool YT, int SHAPE>
+struct FfnLds : FfnShape<PL, SHAPE> {
+    typedef FfnShape<PL, SHAPE> S;
+    typedef Stages<PL, XT, SHAPE == DEEP> Stage;
+    static constexpr int BK = Stage::values, NB = Stage::buffers;
+    static constexpr int stage = PL * (TileLds<XT, S::TM, BK>::bytes + TileLds<YT, S::TN, BK>::bytes);
+    static constexpr int BP = NB == 4 && SHAPE == SMALL ? 1 : 2, PW = 32 * BP, P = 2 * PW * 4 + 16, part = 64 * P;
+    static constexpr int first = part > stage ? part : stage, more = NB == 4 ? stage : 16; // of two buffers each
+};
+
+// Which of the eight XCDs takes which tiles of a small grid: ranges of the tiles
+// along m (p of them) and n (q) and of the sum's splits (r), p q r = 8, so that an
+// XCD's L2 reads few rows of both operands.
+struct XcdParts {
+    int p, q, r;
+};
+__device__ __forceinline__ bool xcd_tile(const XcdParts &x, unsigned block, int mt, int nt, int splits, int64_t &m,
+                                         int64_t &n, int &split)
+{
+    const int xcd = block & 7, local = (int)(block >> 3);
+    const int ri = xcd % x.r, qi = xcd / x.r % x.q, pi = xcd / (x.r * x.q);
+    const int m0 = pi * mt / x.p, n0 = qi * nt / x.q, s0 = ri * splits / x.r;
+    const int dm = (pi + 1) * mt / x.p - m0, dn = (qi + 1) * nt / x.q - n0, ds = (ri + 1) * splits / x.r - s0;
+    if (local >= dm * dn * ds) return false;
+    m = m0 + local % dm;
+    n = n0 + local / dm % dn;
+    split = s0 + local / (dm * dn);
+    return true;
+}
+inline XcdParts xcd_parts(int64_t mt, int64_t nt, int64_t splits, unsigned &grid)
+{
+    XcdParts best{1, 1, 8};
+    int64_t cost = -1;
+    for (int p = 1; p <= 8; p *= 2)
+        for (int q = 1; p * q <= 8; q *= 2) {
+            const int r = 8 / (p * q);
+            const int64_t dm = (mt + p - 1) / p, dn = (nt + q - 1) / q, ds = (splits + r - 1) / r;
+            // the longest XCD's work, then the operands' rows that it reads
+            const int64_t c = (dm * dn * ds * 8 + 31) / 32 * 4096 + (dm + dn) * ds;
+            if (cost >= 0 && c >= cost) continue;
+            cost = c;
+            best = {p, q, r};
+            grid = (unsigned)(8 * dm * dn * ds);
+        }
+    return best;
+}
+
+// A tile of one product: M outputs (along X's rows or columns) in each of N rows,
+// K summed values, mt x nt tiles taken by `grid` blocks.  PAIRED: X is W_in as it
+// lies in memory.
+struct FfnJob {
+    Operand X, Y;
+    int64_t K, mt, nt;
+    unsigned grid;
+    XcdParts xcds;
+    FfnOut o;
+};
+template <class T, bool XT, bool YT, int OUT, bool PAIRED, int SHAPE>
+__device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char *lds0, char *lds1, char *lds2,
+                                         char *lds3)
+{
+    typedef typename FfnTerms<T>::type E;
+    constexpr int PL = FfnTerms<T>::planes;
+    typedef FfnLds<PL, XT, YT, SHAPE> Lds;
+    constexpr int NI = Lds::NI, NJ = Lds::NJ, TM = Lds::TM, TN = Lds::TN, BK = Lds::BK, BP = Lds::BP, PM = NI / BP, PW = Lds::PW, P = Lds::P;
+    Operand X = job.X, Y = job.Y;
+    const FfnOut &o = job.o;
+    int64_t mi, ni, K = job.K;
+    int sp;
+    if (in_patches(job.mt, job.nt)) {
+        if (!tile_of(block, job.grid, job.mt, job.nt, 1, mi, ni, sp)) return;
+    } else if (!xcd_tile(job.xcds, block, (int)job.mt, (int)job.nt, OUT == FFN_OUT ? o.splits : 1, mi, ni, sp)) {
+        return;
+    }
+    float *sum = nullptr;
+    if (OUT == FFN_OUT && o.sum) { // this split's part of the sum
+        const int64_t k0 = sp * o.split_k;
+        if (k0 >= K) return;
+        auto from = [&](Operand &a, bool turned) {
+            a.p += turned ? k0 * a.ld : k0;
+            (turned ? a.rows : a.cols) -= k0;
+        };
+        from(X, XT);
+        from(Y, YT);
+        K = K - k0 < o.split_k ? K - k0 : o.split_k;
+        sum = o.sum + sp * o.rows * o.cols;
+    }
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
+    const int64_t m0 = mi * TM, n0 = ni * TN;
+    f32x16 acc[NI][NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    // eight values of a row per thread at a time; FFN_IN: of both projections
+    constexpr int ROWV = (OUT == FFN_IN ? PW : 2 * PW) / 8, ITEMS = 64 * ROWV / 256, PARTS = NJ * PM;
+    auto row_at = [&](int j, int k) {
+        const int r = (tid + k * 256) / ROWV;
+        return n0 + (r >> 5) * (TN / 2) + j * 32 + (r & 31);
+    };
+    auto col_at = [&](int h, int k) { // (of the output; FFN_IN: of a)
+        const int at = (tid + k * 256) % ROWV * 8;
+        if constexpr (OUT == FFN_IN) return m0 / 2 + at / 32 * (TM / 4) + h * 32 + at % 32;
+        else return m0 + at / PW * (TM / 2) + h * PW + at % PW;
+    };
+    // p of the next part is on its way while this part is worked on
+    float pre[OUT == FFN_MID ? 2 : 1][OUT == FFN_MID ? ITEMS : 1][2][8];
+    auto load_pre = [&](auto which) {
+        constexpr int part = decltype(which)::value;
+        if constexpr (OUT == FFN_MID && part < PARTS) {
+            const int j = part / PM, h = part % PM;
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k) {
+                const int64_t i = row_at(j, k), m = col_at(h, k);
+                // (from the last row and columns where there is none)
+                const float *from = o.pre + (i < o.rows ? i : o.rows - 1) * o.ld_pre;
+                const int left = m >= o.F ? 0 : o.F - m < 8 ? (int)(o.F - m) : 8;
+                if (o.F >= 8) {
+                    const int64_t c = left == 8 ? m : o.F - 8; // the last eight, moved into place when they are used
+                    load_vec<float, 8>(from + c, pre[part & 1][k][0]);
+                    load_vec<float, 8>(from + o.F + c, pre[part & 1][k][1]);
+                } else {
+                    load_part<float, 8>(from + (left ? m : 0), left, pre[part & 1][k][0]);
+                    load_part<float, 8>(from + o.F + (left ? m : 0), left, pre[part & 1][k][1]);
+                }
+            }
+        }
+    };
+    load_pre(std::integral_constant<int, 0>()); // (there long before the products are)
+    {
+        const int stages = (int)(K / BK);
+        // Tiles begin at different places of the sum where rows lie along it: rows a
+        // multiple of a KB apart meet in few channels of the L2 (8192 x 4096 x 16384:
+        // p and a 2.06 -> 1.94 ms, y 1.09 -> 0.98).  Small grids gain nothing.
+        constexpr bool ROT = !YT && SHAPE == BIG;
+        const int first = ROT ? (int)((8 * mi + ni) & 31) % stages : 0;
+        TileLoader<YT, TN, BK, PL, ROT> y(Y, n0, stages, first);
+        if constexpr (PAIRED) {
+            PairLoader<TM> x(X, o.F, m0, stages, first);
+            multiply<E, PL, XT, YT, SHAPE == DEEP>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+        } else {
+            TileLoader<XT, TM, BK, PL, ROT> x(X, m0, stages, first);
+            multiply<E, PL, XT, YT, SHAPE == DEEP>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+        }
+    }
+    __syncthreads();
+    each_of(std::make_integer_sequence<int, PARTS>(), [&](auto which) {
+        constexpr int p = decltype(which)::value, j = p / PM, h = p % PM;
+        char *part = p & 1 ? lds1 : lds0; // one is written while the last is read
+        if (h == 0) keep_columns(acc, j);
+        load_pre(std::integral_constant<int, p + 1>());
+#pragma unroll
+        for (int b = 0; b < BP; ++b)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const f32x16 &v = acc[h * BP + b][j];
+                const int col = wm * PW + b * 32 + 8 * q + 4 * (lane >> 5);
+                *reinterpret_cast<float4 *>(part + (wn * 32 + (lane & 31)) * P + col * 4) =
+                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const int c = tid + k * 256, at = c % ROWV * 8;
+            const char *from = part + c / ROWV * P;
+            const int64_t i = row_at(j, k), m = col_at(h, k);
+            if constexpr (OUT == FFN_IN) {
+                float g[8], u[8], a[8], slope[8];
+                const char *gate = from + (at / 32 * PW + at % 32) * 4;
+                load_vec<float, 8>(reinterpret_cast<const float *>(gate), g);
+                load_vec<float, 8>(reinterpret_cast<const float *>(gate + 128), u);
+                activations<PL == 1>(o.act, g, a, slope);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a[e] = m + e < o.F ? a[e] * u[e] : 0.f;
+                if (i >= o.rows || m >= o.ld_mid) continue;
+                store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, 8, a);
+                if (o.pre && m < o.F) {
+                    float *to = o.pre + i * o.ld_pre + m;
+                    const int left = (int)(o.F - m < 8 ? o.F - m : 8);
+                    store_part<float, 8>(to, left, g);
+                    store_part<float, 8>(to + o.F, left, u);
+                }
+            } else {
+                const int left = (int)(o.cols - m < 8 ? o.cols - m : 8);
+                float x[8];
+                load_vec<float, 8>(reinterpret_cast<const float *>(from + at * 4), x);
+                if constexpr (OUT == FFN_MID) {
+                    float g[8], u[8], a[8], slope[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        g[e] = pre[p & 1][k][0][e];
+                        u[e] = pre[p & 1][k][1][e];
+                    }
+                    if (left > 0 && left < 8 && o.F >= 8) { // the last columns, from the last eight values
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            g[e] = 0.f;
+                            u[e] = 0.f;
+#pragma unroll
+                            for (int q = e + 1; q < 8; ++q)
+                                if (q - e == 8 - left) {
+                                    g[e] = pre[p & 1][k][0][q];
+                                    u[e] = pre[p & 1][k][1][q];
+                                }
+                        }
+                    }
+                    activations<PL == 1>(o.act, g, a, slope);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        g[e] = x[e] * u[e] * slope[e];
+                        slope[e] = a[e] * u[e];
+                        u[e] = x[e] * a[e];
+                    }
+                    if (i >= o.rows || left <= 0) continue;
+                    store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, left, slope);
+                    short *d = o.dpre + i * o.ld_dpre + m;
+                    store_terms<T, PL>(d, o.plane_dpre, left, g);
+                    store_terms<T, PL>(d + o.F, o.plane_dpre, left, u);
+                } else {
+                    if (i >= o.rows || left <= 0) continue;
+                    if (sum) store_part<float, 8>(sum + i * o.cols + m, left, x);
+                    else store_part<T, 8>(static_cast<T *>(o.out) + i * o.ld_out + m, left, x);
+                }
+            }
+        }
+    });
+}
+
+template <class T, bool XT, bool YT, int OUT, bool PAIRED, int SHAPE>
+__global__ __launch_bounds__(256, 1) void k_ffn(FfnJob job)
+{
+    typedef FfnLds<FfnTerms<T>::planes, XT, YT, SHAPE> Lds;
+    __shared__ __align__(16) char lds0[Lds::first];
+    __shared__ __align__(16) char lds1[Lds::first];
+    __shared__ __align__(16) char lds2[Lds::more];
+    __shared__ __align__(16) char lds3[Lds::more];
+    ffn_tile<T, XT, YT, OUT, PAIRED, SHAPE>(job, blockIdx.x, lds0, lds1, lds2, lds3);
+}
+
+// Outputs from their splits' sums.
+struct Join {
+    const float *sum;
+    int splits;
+    int64_t rows, cols;
+    void *out;
+    int64_t ld;
+};
+struct Joins {
+    Join job[3];
+    int first[4]; // first block of each
+};
+template <class T>
+__global__ __launch_bounds__(256) void k_ffn_join(Joins p)
+{
+    const int k = (int)blockIdx.x < p.first[1] ? 0 : (int)blockIdx.x < p.first[2] ? 1 : 2;
+    const Join &j = p.job[k];
+    const int64_t chunks = (j.cols + 3) / 4, all = j.rows * chunks, step = (int64_t)(p.first[k + 1] - p.first[k]) * 256;
+    for (int64_t c = (int64_t)((int)blockIdx.x - p.first[k]) * 256 + threadIdx.x; c < all; c += step) {
+        const int64_t i = c / chunks, m = (c - i * chunks) * 4;
+        const int left = (int)(j.cols - m < 4 ? j.cols - m : 4);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int q = 0; q < j.splits; ++q) {
+            float y[4];
+            load_part<float, 4>(j.sum + ((int64_t)q * j.rows + i) * j.cols + m, left, y);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] += y[r];
+        }
+        store_part<T, 4>(static_cast<T *>(j.out) + i * j.ld + m, left, x);
+    }
+}
+
+// ------------------------------------------------------------ host: plans
+
+unsigned blocks_for(int64_t threads)
+{
+    const int64_t b = (threads + 255) / 256;
+    return (unsigned)(b < 16384 ? b : 16384);
+}
+
+// A product's sizes: M outputs in each of N rows, K summed values in `splits`
+// parts of `each`.
+struct FfnSize {
+    int64_t M, N, K;
+    int splits;
+    int64_t each;
+
+    size_t bytes() const { return splits > 1 ? round256((size_t)splits * M * N * sizeof(float)) : 0; }
+};
+inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
+{
+    const int64_t TM = shape == BIG ? 256 : 128, TN = PL == 1 ? TM : TM / 2;
+    return ((z.M + TM - 1) / TM) * ((z.N + TN - 1) / TN);
+}
+
+// The shape of the tiles of a launch of products, and how often each product's
+// sum is split (may_split).
+//
+// 16 bits: BIG for two rounds of the compute units (8192 x 4096 x 16384, y: 930
+// us, 1090 in SMALL ones; 2048 x 1024 x 4096, one round, p and a: 53 and 47), else
+// SMALL where some units get two of them (777 x 1024 x 2688, all outputs of the
+// backward: 34 us, 46 in DEEP ones), else DEEP (300 x 4096 x 1000, p and a: 28 us, 43
+// in SMALL ones).  fp32, whose products are six times as long: BIG for one round,
+// counting the splits of a long sum (2048 x 2048 x 4096, y: 188 us, 240 in SMALL
+// ones; 777 x 1024 x 2688: 47 and 41), else SMALL.
+//
+// Sums are split so that the units have equal work, one block each, two of SMALL
+// tiles, but not below kSplit values: joining the parts is a launch, 4 us or more.
+int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
+{
+    int64_t big = 0, small = 0, work = 0;
+    for (int i = 0; i < count; ++i) {
+        const int64_t parts = may_split && PL > 1 ? (z[i].K < 1024 ? 1 : z[i].K < 4096 ? z[i].K / 1024 : 4) : 1;
+        big += tiles_of(z[i], PL, BIG) * parts;
+        small += tiles_of(z[i], PL, SMALL);
+    }
+    const int shape = big >= (PL > 1 ? kCUs : 2 * kCUs) ? BIG : PL > 1 || small > kCUs ? SMALL : DEEP;
+    for (int i = 0; i < count; ++i) work += tiles_of(z[i], PL, shape) * z[i].K;
+    const int64_t blocks = shape == SMALL ? 2 * kCUs : kCUs, least = PL > 1 ? kSplit / 4 : kSplit;
+    for (int i = 0; i < count; ++i) {
+        int64_t s = may_split ? (z[i].K * blocks + work - 1) / work : 1;
+        if (s > z[i].K / least) s = z[i].K / least;
+        if (s < 1) s = 1;
+        z[i].each = up((z[i].K + s - 1) / s, kPad);
+        z[i].splits = (int)((z[i].K + z[i].each - 1) / z[i].each);
+    }
+    return shape;
+}
+struct FfnSplit {
+    int parts;
+    int64_t each;
+};
+
+// Forward products of few rows take kernels of their own: 16-bit rows up to 16
+// (4096 x 16384: 1 row 72 us, 16 rows 90, 17 rows 124 and by tiles 106), fp32 rows
+// up to 128, whose tiles take a split copy of the weights (4 rows 147 us).
+inline bool few_rows(int64_t n, bool fp32) { return n <= (fp32 ? 128 : 16); }
+// Parts of a sum of K values that leave through `rows` columns: a block for each
+// compute unit, of 256 summed values at least.
+FfnSplit few_split(int64_t rows, int64_t K)
+{
+    const int64_t blocks = (rows + 15) / 16;
+    int64_t s = kCUs / blocks;
+    if (s > K / 256) s = K / 256;
+    if (s < 1) s = 1;
+    const int64_t each = up((K + s - 1) / s, 128);
+    return {(int)((K + each - 1) / each), each};
+}
+size_t few_bytes(int64_t n, int64_t rows, int64_t K)
+{
+    const FfnSplit s = few_split(rows, K);
+    return s.parts > 1 ? round256((size_t)s.parts * n * rows * sizeof(float)) : 0;
+}
+
+// Whether an operand serves as it lies in memory: 16-bit rows at multiples of 16
+// bytes (further apart they would pass the 31 bits of a tile's loads) and of whole
+// pieces of 16 bytes, or where they lie along the sum of whole steps: a piece that
+// the last row's end cuts would be read past it.
+bool lies_well(const void *p, int64_t ld)
+{
+    return ld % 8 == 0 && ld <= (1 << 20) && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+// Which operands are copied.
+struct FfnCopies {
+    bool x, w_in, w_out, gy;
+};
+FfnCopies ffn_copies(bool fp32, bool grad, int64_t n, int64_t D, int64_t F, bool x, bool w_in, bool w_out, bool gy)
+{
+    const bool d = D % kPad == 0, f = F % kPad == 0;
+    if (!grad && few_rows(n, fp32)) return {false, false, false, false};
+    if (fp32) return {true, true, true, true};
+    if (grad) return {!x || D % 8, !w_in || D % 8, !w_out || F % 8, !gy || !d}; // only gy lies along a sum
+    return {!x || !d, !w_in || !d, !w_out || !f, false};
+}
+
+// The sums of y, and of the gradients of x, w_in and w_out.
+FfnSize y_size(int64_t n, int64_t D, int64_t F, int PL, int *shape = nullptr)
+{
+    FfnSize z{D, n, up(F, kPad)};
+    const int s = ffn_shape(&z, 1, PL, true);
+    if (shape) *shape = s;
+    return z;
+}
+int grad_sizes(FfnSize *z, int64_t n, int64_t D, int64_t F, int PL)
+{
+    z[0] = {D, n, up(2 * F, kPad)};
+    z[1] = {D, 2 * F, up(n, kPad)};
+    z[2] = {F, D, up(n, kPad)};
+    return ffn_shape(z, 3, PL, true);
+}
+
+struct FfnPlan {
+    short *x, *w_in, *w_out, *gy, *mid, *dpre;
+    float *sum;
+    int64_t Dp, Fp, Pp; // padded columns of x and gy, of a, of dp
+    int64_t ldD, ldF, ldP;
+    size_t bytes;
+};
+// Distance of rows of so many columns: an odd number of cache lines where it would
+// be a multiple of 1 KB, at which a tile's rows meet in few channels of the L2
+// (8192 x 4096 x 16384, rows of a 32 KB apart: y in 997 us, 902 with one line more).
+inline int64_t apart(int64_t cols) { return cols % 512 ? cols : cols + 64; }
+
+FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCopies &c, char *base)
+{
+    size_t off = TT_EMB_STATUS_BYTES;
+    auto take = [&](int64_t rows, int64_t cols) {
+        char *r = base ? base + off : nullptr;
+        off += round256((size_t)PL * rows * cols * 2);
+        return reinterpret_cast<short *>(r);
+    };
+    FfnPlan p{};
+    if (n < 1) n = 1; // no rows: the least workspace
+    p.Dp = up(D, kPad);
+    p.Fp = up(F, kPad);
+    p.Pp = up(2 * F, kPad);
+    p.ldD = apart(p.Dp);
+    p.ldF = apart(p.Fp);
+    p.ldP = apart(p.Pp);
+    if (c.x) p.x = take(n, p.ldD);
+    if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.ldD);
+    if (c.w_out) p.w_out = take(D, p.ldF);
+    if (c.gy) p.gy = take(n, p.ldD);
+    p.mid = take(n, p.ldF);
+    size_t sums;
+    if (grad) {
+        p.dpre = take(n, p.ldP);
+        FfnSize z[3];
+        grad_sizes(z, n, D, F, PL);
+        sums = z[0].bytes() + z[1].bytes() + z[2].bytes();
+    } else {
+        sums = few_rows(n, PL > 1) ? few_bytes(n, D, F) : y_size(n, D, F, PL).bytes();
+    }
+    p.sum = reinterpret_cast<float *>(base ? base + off : nullptr);
+    off += sums;
+    p.bytes = off;
+    return p;
+}
+FfnCopies copies_of(const FfnArgs &a, int dtype, bool grad)
+{
+    return ffn_copies(dtype == TT_EMB_DTYPE_FLOAT, grad, a.n, a.D, a.F, lies_well(a.x, a.ld_x), lies_well(a.w_in, a.ld_in),
+                      lies_well(a.w_out, a.ld_out), lies_well(a.gy, a.ld_gy));
+}
+
+// ---------------------------------------------------------- host: launches
+
+template <class T>
+struct Packing {
+    Packs p{};
+    int n = 0;
+
+    // The operand that a copy (where there is one) or the matrix itself makes.
+    Operand operator()(const void *src, int64_t ld, int64_t rows, int64_t cols, short *dst, int64_t width, int64_t pair)
+    {
+        if (!dst) return Operand{static_cast<const short *>(src), ld, 0, rows, cols};
+        const int64_t to = pair ? 2 * up(pair, 32) : rows, ldp = apart(width);
+        add(Pack{src, ld, to, cols, dst, width, ldp, to * ldp, pair});
+        return Operand{dst, ldp, to * ldp, to, width};
+    }
+    void add(const Pack &job)
+    {
+        p.job[n] = job;
+        p.first[n + 1] = p.first[n] + (int)blocks_for(job.rows * (job.width / 8));
+        ++n;
+    }
+    void run(hipStream_t s)
+    {
+        if (!n) return;
+        for (int k = n; k < kPacks; ++k) p.first[k + 1] = p.first[k];
+        hipLaunchKernelGGL(k_ffn_pack<T>, dim3((unsigned)p.first[n]), dim3(256), 0, s, p);
+    }
+};
+
+FfnJob job_of(const Operand &x, const Operand &y, const FfnSize &z, int PL, int shape, const FfnOut &o)
+{
+    const int64_t TM = shape == BIG ? 256 : 128, TN = PL == 1 ? TM : TM / 2;
+    const int64_t mt = (z.M + TM - 1) / TM, nt = (z.N + TN - 1) / TN;
+    FfnJob job{x, y, z.K, mt, nt, 0, {}, o};
+    if (in_patches(mt, nt)) job.grid = tile_grid(mt, nt, 1);
+    else job.xcds = xcd_parts(mt, nt, z.splits, job.grid);
+    return job;
+}
+
+template <class T, bool XT, bool YT, int OUT, bool PAIRED>
+void launch(const FfnJob &job, int shape, hipStream_t s)
+{
+    auto run = [&](auto c) {
+        hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, decltype(c)::value>), dim3(job.grid), dim3(256), 0, s, job);
+    };
+    if (shape == BIG) run(std::integral_constant<int, BIG>());
+    else if (shape == SMALL) run(std::integral_constant<int, SMALL>());
+    else if constexpr (FfnTerms<T>::planes == 1) run(std::integral_constant<int, DEEP>());
+}
+
+template <class T, bool XT, bool YT, int OUT, bool PAIRED>
+void product(const Operand &x, const Operand &y, int64_t M, int64_t N, int64_t K, const FfnOut &o, hipStream_t s)
+{
+    constexpr int PL = FfnTerms<T>::planes;
+    FfnSize z{M, N, K};
+    const int shape = ffn_shape(&z, 1, PL, false);
+    launch<T, XT, YT, OUT, PAIRED>(job_of(x, y, z, PL, shape, o), shape, s);
+}
+
+// Outputs [N][M] of T: each job takes what it needs of the room for partial sums.
+template <class T>
+struct Outputs {
+    float *sum;
+    Joins joins{};
+    int n = 0;
+
+    FfnJob operator()(const Operand &x, const Operand &y, const FfnSize &z, int shape, void *out, int64_t ld)
+    {
+        FfnOut o{};
+        o.rows = z.N;
+        o.cols = z.M;
+        o.out = out;
+        o.ld_out = ld;
+        o.splits = z.splits;
+        if (z.splits > 1) {
+            o.sum = sum;
+            o.split_k = z.each;
+            sum += z.bytes() / sizeof(float);
+            joins.job[n] = Join{o.sum, z.splits, z.N, z.M, out, ld};
+            joins.first[n + 1] = joins.first[n] + (int)blocks_for(z.N * ((z.M + 3) / 4));
+            ++n;
+        }
+        return job_of(x, y, z, FfnTerms<T>::planes, shape, o);
+    }
+    void join(hipStream_t s)
+    {
+        if (!n) return;
+        for (int k = n; k < 3; ++k) joins.first[k + 1] = joins.first[k];
+        hipLaunchKernelGGL(k_ffn_join<T>, dim3((unsigned)joins.first[n]), dim3(256), 0, s, joins);
+    }
+};
+
+} // namespace
+
+} // namespace ttemb

@@ -50,10 +50,11 @@ __device__ __forceinline__ void split_terms(float x, short (&t)[PL])
 // whole cache lines, and half the barriers; turned ones are lines anyway, and
 // more and shorter stages leave their loads more time (8192 rows, K = 4096 and
 // 8192: logits 7.24 ms with stages of 32, 6.86 of 64; the weight's gradient 770
-// and 826 us a piece).
-template <int PL, bool XT>
+// and 826 us a piece).  DEEP: three stages ahead, for grids that leave a compute
+// unit one block of small tiles, where a stage's loads take longer than its products.
+template <int PL, bool XT, bool DEEP = false>
 struct Stages {
-    static constexpr int values = PL == 1 && !XT ? 64 : 32, buffers = PL == 1 && XT ? 4 : 2;
+    static constexpr int values = PL == 1 && (DEEP || !XT) ? 64 : 32, buffers = DEEP || (PL == 1 && XT) ? 4 : 2;
 };
 
 // An operand of a product: PL matrices of 16-bit values.  Straight: row r holds
@@ -77,7 +78,8 @@ struct TileLds {
     static constexpr int vecs = R * BK / 8 / 256; // 16-byte pieces per thread
     static __device__ __forceinline__ int turn(int row)
     {
-        return TURNED ? (row & 3) << 2 : BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
+        if constexpr (TURNED) return R == 64 ? (row & 2) << 1 : (row & 3) << 2; // (rows of 64 have eight pieces)
+        else return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3;
     }
 };
 
@@ -302,12 +304,13 @@ struct TermPairs {
 // it.  The buffers are the caller's variables and a round of the loop passes all
 // of them, so that the compiler knows which one a load or a read means and does
 // not wait for the others.
-template <class E, int PL, bool XT, bool YT, int NI, int NJ, class LoadX, class LoadY>
+template <class E, int PL, bool XT, bool YT, bool DEEP = false, int NI, int NJ, class LoadX, class LoadY>
 __device__ __forceinline__ void multiply(LoadX &x, LoadY &y, int stages, char *lds0, char *lds1, char *lds2, char *lds3,
                                          f32x16 (&acc)[NI][NJ])
 {
     typedef TermPairs<PL> Pairs;
-    constexpr int TM = 64 * NI, TN = 64 * NJ, BK = Stages<PL, XT>::values, NB = Stages<PL, XT>::buffers;
+    constexpr int TM = 64 * NI, TN = 64 * NJ;
+    constexpr int BK = Stages<PL, XT, DEEP>::values, NB = Stages<PL, XT, DEEP>::buffers;
     constexpr int XB = PL * TileLds<XT, TM, BK>::bytes;
     const int wave = threadIdx.x >> 6, wm = wave & 1, wn = wave >> 1;
     auto load_x = [&](char *to) { x.load(to); };
@@ -374,6 +377,7 @@ __device__ __forceinline__ void multiply(LoadX &x, LoadY &y, int stages, char *l
         load_x(lds2);
         load_y(lds2);
         load_x(lds3);
+        if constexpr (PL > 1) load_y(lds3);
     }
     loads_meet<(NB - 1) * (LX + LY) - (PL == 1 ? LY : 0)>();
     read(lds0, 0, a0, b0);
