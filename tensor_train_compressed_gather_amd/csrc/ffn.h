@@ -244,8 +244,7 @@ __device__ __forceinline__ void store_terms(short *p, int64_t plane, int left, c
     }
 }
 
-// f for each of the numbers, as constants: a long loop's body may be left as a
-// loop, whose registers would then be memory.
+// f for each of the numbers, as constants.
 template <class F, int... I>
 __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
 {
@@ -373,11 +372,10 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
         if constexpr (OUT == FFN_IN) return m0 / 2 + at / 32 * (TM / 4) + h * 32 + at % 32;
         else return m0 + at / PW * (TM / 2) + h * PW + at % PW;
     };
-    // p of the next part is on its way while this part is worked on
-    float pre[OUT == FFN_MID ? 2 : 1][OUT == FFN_MID ? ITEMS : 1][2][8];
-    auto load_pre = [&](auto which) {
-        constexpr int part = decltype(which)::value;
-        if constexpr (OUT == FFN_MID && part < PARTS) {
+    // p of a part, asked for while the part before is worked on
+    float pre[OUT == FFN_MID ? ITEMS : 1][2][8];
+    auto load_pre = [&](int part) {
+        if constexpr (OUT == FFN_MID) {
             const int j = part / PM, h = part % PM;
 #pragma unroll
             for (int k = 0; k < ITEMS; ++k) {
@@ -387,16 +385,16 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
                 const int left = m >= o.F ? 0 : o.F - m < 8 ? (int)(o.F - m) : 8;
                 if (o.F >= 8) {
                     const int64_t c = left == 8 ? m : o.F - 8; // the last eight, moved into place when they are used
-                    load_vec<float, 8>(from + c, pre[part & 1][k][0]);
-                    load_vec<float, 8>(from + o.F + c, pre[part & 1][k][1]);
+                    load_vec<float, 8>(from + c, pre[k][0]);
+                    load_vec<float, 8>(from + o.F + c, pre[k][1]);
                 } else {
-                    load_part<float, 8>(from + (left ? m : 0), left, pre[part & 1][k][0]);
-                    load_part<float, 8>(from + o.F + (left ? m : 0), left, pre[part & 1][k][1]);
+                    load_part<float, 8>(from + (left ? m : 0), left, pre[k][0]);
+                    load_part<float, 8>(from + o.F + (left ? m : 0), left, pre[k][1]);
                 }
             }
         }
     };
-    load_pre(std::integral_constant<int, 0>()); // (there long before the products are)
+    load_pre(0); // (there long before the products are)
     {
         const int stages = (int)(K / BK);
         // Tiles begin at different places of the sum where rows lie along it: rows a
@@ -414,21 +412,38 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
         }
     }
     __syncthreads();
-    each_of(std::make_integer_sequence<int, PARTS>(), [&](auto which) {
-        constexpr int p = decltype(which)::value, j = p / PM, h = p % PM;
+    // One body for all parts, so that it stays in the instruction cache (unrolled,
+    // dp and a in BIG tiles were 150 KB of code); only the registers that leave
+    // have to be named.
+#pragma clang loop unroll(disable)
+    for (int p = 0; p < PARTS; ++p) {
         char *part = p & 1 ? lds1 : lds0; // one is written while the last is read
-        if (h == 0) keep_columns(acc, j);
-        load_pre(std::integral_constant<int, p + 1>());
+        each_of(std::make_integer_sequence<int, PARTS>(), [&](auto which) {
+            constexpr int c = decltype(which)::value, j = c / PM, h = c % PM;
+            if (p != c) return;
 #pragma unroll
-        for (int b = 0; b < BP; ++b)
+            for (int b = 0; b < BP; ++b)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const f32x16 &v = acc[h * BP + b][j];
-                const int col = wm * PW + b * 32 + 8 * q + 4 * (lane >> 5);
-                *reinterpret_cast<float4 *>(part + (wn * 32 + (lane & 31)) * P + col * 4) =
-                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-            }
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16 &v = acc[h * BP + b][j];
+                    const int col = wm * PW + b * 32 + 8 * q + 4 * (lane >> 5);
+                    *reinterpret_cast<float4 *>(part + (wn * 32 + (lane & 31)) * P + col * 4) =
+                        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+        });
+        float here[OUT == FFN_MID ? ITEMS : 1][2][8];
+        if constexpr (OUT == FFN_MID) {
+#pragma unroll
+            for (int k = 0; k < ITEMS; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    here[k][0][e] = pre[k][0][e];
+                    here[k][1][e] = pre[k][1][e];
+                }
+            if (p + 1 < PARTS) load_pre(p + 1);
+        }
         __syncthreads();
+        const int j = p / PM, h = p % PM;
 #pragma unroll
         for (int k = 0; k < ITEMS; ++k) {
             const int c = tid + k * 256, at = c % ROWV * 8;
@@ -458,20 +473,16 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
                     float g[8], u[8], a[8], slope[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        g[e] = pre[p & 1][k][0][e];
-                        u[e] = pre[p & 1][k][1][e];
+                        g[e] = here[k][0][e];
+                        u[e] = here[k][1][e];
                     }
                     if (left > 0 && left < 8 && o.F >= 8) { // the last columns, from the last eight values
+                        for (int shift = left; shift < 8; ++shift) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            g[e] = 0.f;
-                            u[e] = 0.f;
-#pragma unroll
-                            for (int q = e + 1; q < 8; ++q)
-                                if (q - e == 8 - left) {
-                                    g[e] = pre[p & 1][k][0][q];
-                                    u[e] = pre[p & 1][k][1][q];
-                                }
+                            for (int e = 0; e < 7; ++e) {
+                                g[e] = g[e + 1];
+                                u[e] = u[e + 1];
+                            }
                         }
                     }
                     activations<PL == 1>(o.act, g, a, slope);
@@ -493,7 +504,7 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
                 }
             }
         }
-    });
+    }
 }
 
 template <class T, bool XT, bool YT, int OUT, bool PAIRED, int SHAPE>
