@@ -10,16 +10,18 @@
 // (without the means of q where N is the root mean square).  It reads x and r,
 // from which it makes h again in fp32: as many bytes as reading h, which a
 // caller may then overwrite, and without its rounding.  The column sums of rows
-// of up to 4096 values stay in registers across a block's rows.  Longer rows
-// leave too few registers for five of them: a second kernel adds them up by
-// columns, from the same inputs and two sums of each row.
+// of up to 4096 values stay in registers across a block's rows.  Longer rows are
+// read again, from the caches, for each pair of sums, and a second kernel adds up
+// their columns, from the same inputs and two sums of each row.
 #include "blocknorm.h"
 
 namespace ttemb {
 
 namespace {
 
-constexpr int kBlockGradBlocks = 4 * kCUs; // rows of partial column sums, at most
+// Rows of partial column sums, at most: as many blocks as the registers let the
+// compute units hold (eight waves of them, in one block or in two).
+constexpr int kBlockGradBlocks = 2 * kCUs;
 constexpr int kBlockCols = 64 * kBlockVec; // columns of a block that adds up long rows
 constexpr int kBlockSums = 5;              // dgamma, dbeta, dpost_gamma, dpost_beta, dgate
 
@@ -39,187 +41,229 @@ __device__ __forceinline__ BlockGrad block_forward(const BlockNormArgs &a, const
 }
 
 // Gradients of a block's rows; its sums over its rows go to part[sum][block][D].
-// LEAN: no sums, the two sums of each row go to `dots`.
-template <class T, class R, int TPR, int NV, bool WHOLE>
-__global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_bwd(BlockNormArgs a, float *part, float2 *dots)
+template <class T, class R, int TPR, bool WHOLE>
+__global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_bwd(BlockNormArgs a, float *part)
 {
     constexpr int VEC = kBlockVec;
-    constexpr bool LEAN = TPR == 1024;
-    constexpr int SUMS = LEAN ? 1 : kBlockSums, SV = LEAN ? 1 : NV;
+    constexpr bool TWO = sizeof(T) == 2 && sizeof(R) == 2; // rows on their way (fp32 rows are as many bytes each)
     __shared__ float sm[2][16][2];
-    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    const int D = (int)a.D;
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, c = t * VEC;
+    const int D = (int)a.D, left = D - c;
     const float invD = 1.f / (float)D;
     const int64_t step = (int64_t)gridDim.x * NormShape<TPR>::rows, last = a.n - 1;
     int64_t r0 = (int64_t)blockIdx.x * NormShape<TPR>::rows;
-    typename VecOf<T, VEC>::raw nx[NV], ny[NV], ng[NV];
-    typename VecOf<R, VEC>::raw nr[NV], nh[NV];
-    float nst[4];
-    auto load = [&](int64_t row) {
+    struct Row {
+        typename VecOf<T, VEC>::raw x, gy, gate;
+        typename VecOf<R, VEC>::raw res, gh;
+        float st[4];
+    };
+    auto load = [&](int64_t row, Row &to) {
         const int64_t r = row < a.n ? row : last;
-        const T *x = static_cast<const T *>(a.x) + r * a.ld_x, *g = static_cast<const T *>(a.gate) + r * a.ld_gate;
-        const T *gy = static_cast<const T *>(a.grad_y) + r * a.ld_gy;
-        const R *res = static_cast<const R *>(a.residual) + r * a.ld_r;
-        const R *gh = static_cast<const R *>(a.grad_h) + r * a.ld_gh;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int64_t c = (t + j * TPR) * VEC;
-            nx[j] = load_row<T, VEC, WHOLE>(x, c, D);
-            nr[j] = load_row<R, VEC, WHOLE>(res, c, D);
-            ny[j] = load_row<T, VEC, WHOLE>(gy, c, D);
-            if (a.grad_h) nh[j] = load_row<R, VEC, WHOLE>(gh, c, D);
-            if (a.gate_rows) ng[j] = load_row<T, VEC, WHOLE>(g, c, D);
-        }
-        load_vec<float, 4>(a.stats + r * 4, nst);
+        to.x = load_cols<T, WHOLE>(static_cast<const T *>(a.x) + r * a.ld_x, c, D);
+        to.res = load_cols<R, WHOLE>(static_cast<const R *>(a.residual) + r * a.ld_r, c, D);
+        to.gy = load_cols<T, WHOLE>(static_cast<const T *>(a.grad_y) + r * a.ld_gy, c, D);
+        if (a.grad_h) to.gh = load_cols<R, WHOLE>(static_cast<const R *>(a.grad_h) + r * a.ld_gh, c, D);
+        if (a.gate_rows) to.gate = load_cols<T, WHOLE>(static_cast<const T *>(a.gate) + r * a.ld_gate, c, D);
+        load_vec<float, 4>(a.stats + r * 4, to.st);
     };
-    if constexpr (!LEAN) load(r0 + sub);
-    float sums[SUMS][SV][VEC];
-    constexpr int PV = LEAN ? 1 : NV;
-    float gam[PV][VEC], pgam[PV][VEC], pbet[PV][VEC], gate[PV][VEC];
-    auto params = [&](int j, int p) {
-        const int64_t c = (t + j * TPR) * VEC;
-        load_params<VEC, WHOLE>(a.gamma, a.param_dtype, c, D, 1.f, gam[p]);
-        load_params<VEC, WHOLE>(a.post_gamma, a.param_dtype, c, D, 1.f, pgam[p]);
-        load_params<VEC, WHOLE>(a.post_beta, a.param_dtype, c, D, 0.f, pbet[p]);
-        load_params<VEC, WHOLE>(a.gate_rows ? nullptr : a.gate, a.param_dtype, c, D, 1.f, gate[p]);
-    };
-    int left[NV];
+    Row one, two;
+    load(r0 + sub, one);
+    if constexpr (TWO) load(r0 + step + sub, two);
+    float sums[kBlockSums][VEC], gam[VEC], pgam[VEC], pbet[VEC], gate[VEC];
+    load_params<VEC, WHOLE>(a.gamma, a.param_dtype, c, D, 1.f, gam);
+    load_params<VEC, WHOLE>(a.post_gamma, a.param_dtype, c, D, 1.f, pgam);
+    load_params<VEC, WHOLE>(a.post_beta, a.param_dtype, c, D, 0.f, pbet);
+    load_params<VEC, WHOLE>(a.gate_rows ? nullptr : a.gate, a.param_dtype, c, D, 1.f, gate);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        left[j] = D - (t + j * TPR) * VEC;
-        if constexpr (!LEAN) {
-            params(j, j);
+    for (int k = 0; k < kBlockSums; ++k)
 #pragma unroll
-            for (int k = 0; k < SUMS; ++k)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) sums[k][j][i] = 0.f;
-        }
-    }
+        for (int i = 0; i < VEC; ++i) sums[k][i] = 0.f;
     int slot = 0;
-    for (; r0 < a.n; r0 += step) {
-        const int64_t r = r0 + sub;
+    auto pass = [&](int64_t r, Row &row) {
         const bool live = r < a.n;
-        if constexpr (LEAN) load(r);
-        float x[NV][VEC], res[NV][VEC], gy[NV][VEC], gh[NV][VEC], gr[NV][VEC], st[4];
+        float x[VEC], res[VEC], gy[VEC], gh[VEC], gr[VEC], st[4];
+        values<T, WHOLE>(row.x, left, D, x);
+        values<R, WHOLE>(row.res, left, D, res);
+        values<T, WHOLE>(row.gy, left, D, gy);
+        if (a.grad_h) values<R, WHOLE>(row.gh, left, D, gh);
+        if (a.gate_rows) values<T, WHOLE>(row.gate, left, D, gr);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int i = 0; i < VEC; ++i) {
+            gh[i] = a.grad_h ? gh[i] : 0.f;
+            gr[i] = a.gate_rows ? gr[i] : gate[i];
+        }
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                x[j][i] = (float)nx[j][i];
-                res[j][i] = (float)nr[j][i];
-                gy[j][i] = (float)ny[j][i];
-                gh[j][i] = a.grad_h ? (float)nh[j][i] : 0.f;
-                gr[j][i] = a.gate_rows ? (float)ng[j][i] : 1.f;
-            }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st[k] = nst[k];
-        if constexpr (!LEAN) load(r + step);
+        for (int k = 0; k < 4; ++k) st[k] = row.st[k];
+        load(r + (TWO ? 2 : 1) * step, row);
         float s[2] = {0.f, 0.f};
-        BlockGrad v[NV][VEC];
+        BlockGrad v[VEC];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if constexpr (LEAN) {
-                __builtin_amdgcn_sched_barrier(0);
-                params(j, 0);
+        for (int i = 0; i < VEC; ++i) {
+            v[i] = block_forward(a, st, x[i], res[i], gr[i], pgam[i], pbet[i]);
+            const float q = gy[i] * gam[i]; // 0 past the row's end
+            if (live && i < left) {
+                sums[0][i] = fmaf(gy[i], v[i].hhat, sums[0][i]);
+                sums[1][i] += gy[i];
             }
-            const int p = LEAN ? 0 : j;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                v[j][i] = block_forward(a, st, x[j][i], res[j][i], gate[p][i] * gr[j][i], pgam[p][i], pbet[p][i]);
-                const float q = gy[j][i] * gam[p][i]; // 0 past the row's end
-                if constexpr (!LEAN) {
-                    if (live && i < left[j]) {
-                        sums[0][j][i] = fmaf(gy[j][i], v[j][i].hhat, sums[0][j][i]);
-                        sums[1][j][i] += gy[j][i];
-                    }
-                }
-                gy[j][i] = q;
-                s[0] += q;
-                s[1] = fmaf(q, v[j][i].hhat, s[1]);
-            }
+            gy[i] = q;
+            s[0] += q;
+            s[1] = fmaf(q, v[i].hhat, s[1]);
         }
         row_sum<TPR, 2>(s, sm, slot);
         const float m0 = a.layer ? s[0] * invD : 0.f, m1 = s[1] * invD;
-        if (LEAN && live && t == 0) dots[r] = make_float2(m0, m1);
         float w[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if constexpr (LEAN) {
-                __builtin_amdgcn_sched_barrier(0);
-                params(j, 0);
+        for (int i = 0; i < VEC; ++i) {
+            const float dh = gh[i] + (gy[i] - m0 - v[i].hhat * m1) * st[3];
+            const float du = i < left ? v[i].weight * dh : 0.f;
+            gh[i] = dh;
+            if (live && i < left) {
+                sums[2][i] = fmaf(du, v[i].xhat, sums[2][i]);
+                sums[3][i] += du;
+                sums[4][i] = fmaf(a.scale_block * dh, v[i].u, sums[4][i]);
             }
-            const int p = LEAN ? 0 : j;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float dh = gh[j][i] + (gy[j][i] - m0 - v[j][i].hhat * m1) * st[3];
-                const float du = i < left[j] ? v[j][i].weight * dh : 0.f;
-                gh[j][i] = dh;
-                if constexpr (!LEAN) {
-                    if (live && i < left[j]) {
-                        sums[2][j][i] = fmaf(du, v[j][i].xhat, sums[2][j][i]);
-                        sums[3][j][i] += du;
-                        sums[4][j][i] = fmaf(a.scale_block * dh, v[j][i].u, sums[4][j][i]);
-                    }
-                }
-                gy[j][i] = a.post ? du * pgam[p][i] : du;
-                w[0] += gy[j][i];
-                w[1] = fmaf(gy[j][i], v[j][i].xhat, w[1]);
-            }
+            gy[i] = a.post ? du * pgam[i] : du;
+            w[0] += gy[i];
+            w[1] = fmaf(gy[i], v[i].xhat, w[1]);
         }
         if (a.post) row_sum<TPR, 2>(w, sm, slot);
-        if (!live) continue;
-        const float n0 = a.post && a.layer ? w[0] * invD : 0.f, n1 = a.post ? w[1] * invD : 0.f;
-        T *dx = static_cast<T *>(a.grad_x) + r * a.ld_gx, *dg = static_cast<T *>(a.grad_gate) + r * a.ld_gg;
-        R *dr = static_cast<R *>(a.grad_r) + r * a.ld_gr;
+        if (!live) return;
+        const float n0 = a.layer ? w[0] * invD : 0.f, n1 = w[1] * invD;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int64_t c = (t + j * TPR) * VEC;
-            float o[VEC];
+        for (int i = 0; i < VEC; ++i) x[i] = a.post ? (gy[i] - n0 - v[i].xhat * n1) * st[1] : gy[i];
+        store_part<T, VEC>(static_cast<T *>(a.grad_x) + r * a.ld_gx + c, left, x);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                o[i] = a.post ? (gy[j][i] - n0 - v[j][i].xhat * n1) * st[1] : gy[j][i];
-            store_part<T, VEC>(dx + c, left[j], o);
+        for (int i = 0; i < VEC; ++i) x[i] = a.scale_residual * gh[i];
+        store_part<R, VEC>(static_cast<R *>(a.grad_r) + r * a.ld_gr + c, left, x);
+        if (a.gate_rows) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = a.scale_residual * gh[j][i];
-            store_part<R, VEC>(dr + c, left[j], o);
-            if (a.gate_rows) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = a.scale_block * gh[j][i] * v[j][i].u;
-                store_part<T, VEC>(dg + c, left[j], o);
-            }
+            for (int i = 0; i < VEC; ++i) x[i] = a.scale_block * gh[i] * v[i].u;
+            store_part<T, VEC>(static_cast<T *>(a.grad_gate) + r * a.ld_gg + c, left, x);
+        }
+    };
+    while (r0 < a.n) {
+        pass(r0 + sub, one);
+        r0 += step;
+        if constexpr (TWO) {
+            if (r0 >= a.n) break;
+            pass(r0 + sub, two);
+            r0 += step;
         }
     }
-    if constexpr (!LEAN) {
-        // the block's sums: sub-rows of one wave by shuffles, the waves through LDS
-        constexpr int W = TPR < 64 ? TPR : 64, COLS = TPR * NV * VEC, WAVES = NormShape<TPR>::threads / 64;
-        constexpr bool JOIN = NormShape<TPR>::rows > 1;
-        __shared__ float col[JOIN ? WAVES : 1][JOIN ? COLS : 1];
+    // the block's sums: sub-rows of one wave by shuffles, the others through LDS
+    constexpr int W = TPR < 64 ? TPR : 64, COLS = TPR * VEC;
+    constexpr bool JOIN = NormShape<TPR>::rows > 1;
+    constexpr int PARTS = TPR <= 64 ? NormShape<TPR>::threads / 64 : NormShape<TPR>::rows;
+    const int mine = TPR <= 64 ? threadIdx.x >> 6 : sub;
+    __shared__ float col[JOIN ? PARTS : 1][JOIN ? COLS : 1];
 #pragma unroll
-        for (int k = 0; k < kBlockSums; ++k) {
-            if (!a.sums[k]) continue;
-            float *to = part + ((int64_t)k * gridDim.x + blockIdx.x) * D;
-            if constexpr (JOIN) {
-                __syncthreads(); // the last sum's columns have been read
+    for (int k = 0; k < kBlockSums; ++k) {
+        if (!a.sums[k]) continue;
+        float *to = part + ((int64_t)k * gridDim.x + blockIdx.x) * D;
+        if constexpr (JOIN) {
+            __syncthreads(); // the last sum's columns have been read
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
+            for (int i = 0; i < VEC; ++i) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-                        for (int o = W; o < 64; o <<= 1) sums[k][j][i] += __shfl_xor(sums[k][j][i], o, 64);
-                        if ((threadIdx.x & 63) < W) col[threadIdx.x >> 6][(t + j * TPR) * VEC + i] = sums[k][j][i];
-                    }
-                __syncthreads();
-                for (int c = threadIdx.x; c < D; c += NormShape<TPR>::threads) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int w = 0; w < WAVES; ++w) s += col[w][c];
-                    to[c] = s;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < NV; ++j) store_part<float, VEC>(to + (t + j * TPR) * VEC, left[j], sums[k][j]);
+                for (int o = W; o < 64; o <<= 1) sums[k][i] += __shfl_xor(sums[k][i], o, 64);
+                if ((threadIdx.x & 63) < W) col[mine][c + i] = sums[k][i];
             }
+            __syncthreads();
+            for (int q = threadIdx.x; q < D; q += NormShape<TPR>::threads) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < PARTS; ++w) s += col[w][q];
+                to[q] = s;
+            }
+        } else {
+            store_part<float, VEC>(to + c, left, sums[k]);
         }
+    }
+}
+
+// Rows of more than 4096 values: a block's threads go over the row once for each
+// of the two pairs of sums, and once more for the gradients; the column sums are
+// another kernel's, which takes m0 and m1 of each row from `dots`.
+template <class T, class R, bool WHOLE>
+__global__ __launch_bounds__(kBlockLong) void k_block_bwd_long(BlockNormArgs a, float2 *dots)
+{
+    constexpr int VEC = kBlockVec;
+    __shared__ float sm[2][16][2];
+    const int D = (int)a.D;
+    const float invD = 1.f / (float)D;
+    int slot = 0;
+    for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
+        float st[4];
+        load_vec<float, 4>(a.stats + r * 4, st);
+        // f(column, elements that exist, N(x) .. N(h), grad_y gamma, grad_h, post_gamma)
+        auto each = [&](auto f) {
+#pragma clang loop unroll(disable)
+            for (int c = threadIdx.x * VEC; c < D; c += kBlockLong * VEC) {
+                const int left = D - c;
+                float x[VEC], res[VEC], q[VEC], gh[VEC], gate[VEC], gam[VEC], pgam[VEC], pbet[VEC];
+                values<T, WHOLE>(load_cols<T, WHOLE>(static_cast<const T *>(a.x) + r * a.ld_x, c, D), left, D, x);
+                values<R, WHOLE>(load_cols<R, WHOLE>(static_cast<const R *>(a.residual) + r * a.ld_r, c, D), left, D,
+                                 res);
+                values<T, WHOLE>(load_cols<T, WHOLE>(static_cast<const T *>(a.grad_y) + r * a.ld_gy, c, D), left, D, q);
+                if (a.grad_h)
+                    values<R, WHOLE>(load_cols<R, WHOLE>(static_cast<const R *>(a.grad_h) + r * a.ld_gh, c, D), left, D,
+                                     gh);
+                if (a.gate_rows)
+                    values<T, WHOLE>(load_cols<T, WHOLE>(static_cast<const T *>(a.gate) + r * a.ld_gate, c, D), left, D,
+                                     gate);
+                else load_params<VEC, WHOLE>(a.gate, a.param_dtype, c, D, 1.f, gate);
+                load_params<VEC, WHOLE>(a.gamma, a.param_dtype, c, D, 1.f, gam);
+                load_params<VEC, WHOLE>(a.post_gamma, a.param_dtype, c, D, 1.f, pgam);
+                load_params<VEC, WHOLE>(a.post_beta, a.param_dtype, c, D, 0.f, pbet);
+                BlockGrad v[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    v[i] = block_forward(a, st, x[i], res[i], gate[i], pgam[i], pbet[i]);
+                    q[i] *= gam[i];
+                    gh[i] = a.grad_h ? gh[i] : 0.f;
+                }
+                f(c, left, v, q, gh, pgam);
+            }
+        };
+        typedef BlockGrad(&Grads)[VEC];
+        typedef float(&Values)[VEC];
+        float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+        each([&](int, int, Grads v, Values q, Values, Values) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) { // (q is 0 past the row's end)
+                s[0] += q[i];
+                s[1] = fmaf(q[i], v[i].hhat, s[1]);
+            }
+        });
+        row_sum<kBlockLong, 2>(s, sm, slot);
+        const float m0 = a.layer ? s[0] * invD : 0.f, m1 = s[1] * invD;
+        if (threadIdx.x == 0) dots[r] = make_float2(m0, m1);
+        auto dh_of = [&](const BlockGrad &v, float q, float gh) { return gh + (q - m0 - v.hhat * m1) * st[3]; };
+        if (a.post) {
+            each([&](int, int left, Grads v, Values q, Values gh, Values pgam) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float p = i < left ? v[i].weight * dh_of(v[i], q[i], gh[i]) * pgam[i] : 0.f;
+                    w[0] += p;
+                    w[1] = fmaf(p, v[i].xhat, w[1]);
+                }
+            });
+            row_sum<kBlockLong, 2>(w, sm, slot);
+        }
+        const float n0 = a.layer ? w[0] * invD : 0.f, n1 = w[1] * invD;
+        each([&](int c, int left, Grads v, Values q, Values gh, Values pgam) {
+            float dx[VEC], dg[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float dh = dh_of(v[i], q[i], gh[i]), du = v[i].weight * dh;
+                dx[i] = a.post ? (du * pgam[i] - n0 - v[i].xhat * n1) * st[1] : du;
+                dg[i] = a.scale_block * dh * v[i].u;
+                q[i] = a.scale_residual * dh;
+            }
+            store_part<T, VEC>(static_cast<T *>(a.grad_x) + r * a.ld_gx + c, left, dx);
+            store_part<R, VEC>(static_cast<R *>(a.grad_r) + r * a.ld_gr + c, left, q);
+            if (a.gate_rows) store_part<T, VEC>(static_cast<T *>(a.grad_gate) + r * a.ld_gg + c, left, dg);
+        });
     }
 }
 
@@ -303,18 +347,25 @@ hipError_t block_backward(const BlockNormArgs &a, hipStream_t s)
     const ColumnSums out = block_sums(a);
     float *part = reinterpret_cast<float *>(a.ws + TT_EMB_STATUS_BYTES);
     float2 *dots = reinterpret_cast<float2 *>(a.ws + TT_EMB_STATUS_BYTES + block_parts_bytes(a.n, a.D));
-    return block_shape(a.D, [&](auto tpr, auto nv, auto whole) {
-        constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-        constexpr bool WHOLE = decltype(whole)::value;
+    if (a.D > kBlockRegs) {
+        const int parts = block_col_parts(a.n, a.D);
+        const dim3 rows(block_grid(a.n, 4 * kCUs)), cols((unsigned)((a.D + kBlockCols - 1) / kBlockCols), parts);
+        auto run = [&](auto whole) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            hipLaunchKernelGGL((k_block_bwd_long<T, R, WHOLE>), rows, dim3(kBlockLong), 0, s, a, dots);
+            hipLaunchKernelGGL((k_block_cols<T, R, WHOLE>), cols, dim3(256), 0, s, a, part, dots);
+        };
+        if (a.D % kBlockVec == 0) run(std::true_type());
+        else run(std::false_type());
+        norm_cols(part, parts, a.D, kBlockSums, out, s);
+        return hipGetLastError();
+    }
+    return block_shape(a.D, [&](auto tpr, auto whole) {
+        constexpr int TPR = decltype(tpr)::value;
         const int64_t need = (a.n + NormShape<TPR>::rows - 1) / NormShape<TPR>::rows;
-        int parts = (int)(need < kBlockGradBlocks ? need : kBlockGradBlocks);
-        hipLaunchKernelGGL((k_block_bwd<T, R, TPR, NV, WHOLE>), dim3(parts), dim3(NormShape<TPR>::threads), 0, s, a,
-                           part, dots);
-        if constexpr (TPR == 1024) {
-            parts = block_col_parts(a.n, a.D);
-            const dim3 grid((unsigned)((a.D + kBlockCols - 1) / kBlockCols), (unsigned)parts);
-            hipLaunchKernelGGL((k_block_cols<T, R, WHOLE>), grid, dim3(256), 0, s, a, part, dots);
-        }
+        const int parts = block_grid(need, TPR == 512 ? kCUs : kBlockGradBlocks);
+        hipLaunchKernelGGL((k_block_bwd<T, R, TPR, decltype(whole)::value>), dim3(parts),
+                           dim3(NormShape<TPR>::threads), 0, s, a, part);
         norm_cols(part, parts, a.D, kBlockSums, out, s);
         return hipGetLastError();
     });

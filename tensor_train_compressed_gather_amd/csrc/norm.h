@@ -15,8 +15,8 @@ struct NormShape {
 };
 
 // Sum over the TPR threads of a row of K values each.  TPR <= 64: shuffles
-// inside the wave.  Larger rows own the block: wave sums meet in LDS, in one
-// of two slots in turn, so one barrier per reduction is enough.
+// inside the wave.  Larger rows: the sums of a row's waves meet in LDS, in one of
+// two slots in turn, so one barrier per reduction is enough.
 template <int TPR, int K>
 __device__ __forceinline__ void row_sum(float (&v)[K], float (*sm)[16][2], int &slot)
 {
@@ -31,11 +31,12 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*sm)[16][2], int &
 #pragma unroll
             for (int k = 0; k < K; ++k) sm[slot][threadIdx.x >> 6][k] = v[k];
         __syncthreads();
+        const int first = NormShape<TPR>::rows > 1 ? (threadIdx.x >> 6) / NW * NW : 0; // the row's first wave
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) s += sm[slot][w][k];
+            for (int w = 0; w < NW; ++w) s += sm[slot][first + w][k];
             v[k] = s;
         }
         slot ^= 1;
