@@ -53,7 +53,6 @@ template <class T, class R, int TPR, bool WHOLE>
 __global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_fwd(BlockNormArgs a)
 {
     constexpr int VEC = kBlockVec;
-    constexpr bool TWO = sizeof(T) == 2 && sizeof(R) == 2; // rows on their way (fp32 rows are as many bytes each)
     __shared__ float sm[2][16][2];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, c = t * VEC;
     const int D = (int)a.D, left = D - c; // elements of the vector that exist
@@ -69,9 +68,8 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_fwd(BlockNorm
         to.res = load_cols<R, WHOLE>(static_cast<const R *>(a.residual) + r * a.ld_r, c, D);
         if (a.gate_rows) to.gate = load_cols<T, WHOLE>(static_cast<const T *>(a.gate) + r * a.ld_gate, c, D);
     };
-    Row one, two;
-    load(r0 + sub, one);
-    if constexpr (TWO) load(r0 + step + sub, two);
+    Row row;
+    load(r0 + sub, row);
     float gam[VEC], bet[VEC], pgam[VEC], pbet[VEC], gate[VEC];
     load_params<VEC, WHOLE>(a.gamma, a.param_dtype, c, D, 1.f, gam);
     load_params<VEC, WHOLE>(a.beta, a.param_dtype, c, D, 0.f, bet);
@@ -79,14 +77,15 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_fwd(BlockNorm
     load_params<VEC, WHOLE>(a.post_beta, a.param_dtype, c, D, 0.f, pbet);
     load_params<VEC, WHOLE>(a.gate_rows ? nullptr : a.gate, a.param_dtype, c, D, 1.f, gate);
     int slot = 0;
-    auto pass = [&](int64_t r, Row &row) {
+    for (; r0 < a.n; r0 += step) {
+        const int64_t r = r0 + sub;
         float v[VEC], res[VEC], w[VEC];
         values<T, WHOLE>(row.x, left, D, v);
         values<R, WHOLE>(row.res, left, D, res);
         if (a.gate_rows) values<T, WHOLE>(row.gate, left, D, w);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) w[i] = a.scale_block * (a.gate_rows ? w[i] : gate[i]);
-        load(r + (TWO ? 2 : 1) * step, row);
+        load(r + step, row); // the next row is on its way while this one is reduced
         float pmean = 0.f, prstd = 1.f, mean, rstd;
         if (a.post) normalise<TPR>(v, left, a.layer, D, a.eps, sm, slot, pmean, prstd);
 #pragma unroll
@@ -96,20 +95,11 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_fwd(BlockNorm
         }
         if (r < a.n) store_part<R, VEC>(static_cast<R *>(a.h) + r * a.ld_h + c, left, v);
         normalise<TPR>(v, left, a.layer, D, a.eps, sm, slot, mean, rstd);
-        if (r >= a.n) return;
+        if (r >= a.n) continue;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = fmaf(v[i], gam[i], bet[i]);
         store_part<T, VEC>(static_cast<T *>(a.y) + r * a.ld_y + c, left, v);
         if (t == 0 && a.stats) store_part<float, 4>(a.stats + r * 4, 4, {pmean, prstd, mean, rstd});
-    };
-    while (r0 < a.n) {
-        pass(r0 + sub, one);
-        r0 += step;
-        if constexpr (TWO) {
-            if (r0 >= a.n) break;
-            pass(r0 + sub, two);
-            r0 += step;
-        }
     }
 }
 

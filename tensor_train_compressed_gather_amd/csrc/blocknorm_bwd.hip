@@ -23,6 +23,8 @@ namespace {
 // compute units hold (eight waves of them, in one block or in two).
 constexpr int kBlockGradBlocks = 2 * kCUs;
 constexpr int kBlockCols = 64 * kBlockVec; // columns of a block that adds up long rows
+// Distance of the rows of partial sums: they are read four at a time.
+__host__ __device__ inline int64_t part_row(int64_t D) { return (D + 3) / 4 * 4; }
 constexpr int kBlockSums = 5;              // dgamma, dbeta, dpost_gamma, dpost_beta, dgate
 
 // What a thread knows of its elements of a row, and the gradient on the way.
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(NormShape<TPR>::threads) void k_block_bwd(BlockNorm
 #pragma unroll
     for (int k = 0; k < kBlockSums; ++k) {
         if (!a.sums[k]) continue;
-        float *to = part + ((int64_t)k * gridDim.x + blockIdx.x) * D;
+        float *to = part + ((int64_t)k * gridDim.x + blockIdx.x) * part_row(D);
         if constexpr (JOIN) {
             __syncthreads(); // the last sum's columns have been read
 #pragma unroll
@@ -316,7 +318,7 @@ __global__ __launch_bounds__(256) void k_block_cols(BlockNormArgs a, float *part
 #pragma unroll
         for (int i = 0; i < VEC; ++i) col[wave][lane * VEC + i] = sums[k][i];
         __syncthreads();
-        float *to = part + ((int64_t)k * gridDim.y + blockIdx.y) * D + (int64_t)blockIdx.x * 64 * VEC;
+        float *to = part + ((int64_t)k * gridDim.y + blockIdx.y) * part_row(D) + (int64_t)blockIdx.x * 64 * VEC;
         for (int i = threadIdx.x; i < 64 * VEC && (int64_t)blockIdx.x * 64 * VEC + i < D; i += 256)
             to[i] = (col[0][i] + col[1][i]) + (col[2][i] + col[3][i]);
     }
@@ -357,7 +359,7 @@ hipError_t block_backward(const BlockNormArgs &a, hipStream_t s)
         };
         if (a.D % kBlockVec == 0) run(std::true_type());
         else run(std::false_type());
-        norm_cols(part, parts, a.D, kBlockSums, out, s);
+        norm_cols(part, parts, a.D, part_row(a.D), kBlockSums, out, s);
         return hipGetLastError();
     }
     return block_shape(a.D, [&](auto tpr, auto whole) {
@@ -366,7 +368,7 @@ hipError_t block_backward(const BlockNormArgs &a, hipStream_t s)
         const int parts = block_grid(need, TPR == 512 ? kCUs : kBlockGradBlocks);
         hipLaunchKernelGGL((k_block_bwd<T, R, TPR, decltype(whole)::value>), dim3(parts),
                            dim3(NormShape<TPR>::threads), 0, s, a, part);
-        norm_cols(part, parts, a.D, kBlockSums, out, s);
+        norm_cols(part, parts, a.D, part_row(a.D), kBlockSums, out, s);
         return hipGetLastError();
     });
 }
@@ -387,7 +389,7 @@ size_t block_parts_bytes(int64_t n, int64_t D)
 {
     int64_t parts = n < kBlockGradBlocks ? n : kBlockGradBlocks;
     if (D > kBlockRegs) parts = block_col_parts(n, D);
-    return round256((size_t)(kBlockSums * parts * D) * sizeof(float));
+    return round256((size_t)(kBlockSums * parts * part_row(D)) * sizeof(float));
 }
 
 size_t block_workspace(int64_t n, int64_t D)

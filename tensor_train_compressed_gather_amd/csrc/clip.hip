@@ -17,7 +17,7 @@ namespace ttemb {
 
 namespace {
 
-constexpr int kClipChunk = 4096; // elements that a block takes at a time
+constexpr int kClipChunk = 8192; // elements that a block takes at a time
 constexpr int kClipOne = 4;      // chunks of all tensors up to which one block does everything
 
 // A chunk's values by this thread: 16 bytes at a time, zeros past the end.

@@ -49,22 +49,22 @@ struct ColumnSums {
     int dtype[5];
 };
 
-// Column sums of the blocks' partials: 64 columns per block, four per lane, 64
+// Column sums of the blocks' partials, rows of `ld`: 64 columns per block, four per lane, 64
 // groups of rows; the four groups of a wave meet in shuffles, the waves in LDS,
 // always in the same order.
 template <bool WHOLE>
-__global__ __launch_bounds__(1024) void k_norm_cols(const float *part, int blocks, int D, ColumnSums out)
+__global__ __launch_bounds__(1024) void k_norm_cols(const float *part, int blocks, int D, int ld, ColumnSums out)
 {
     __shared__ float sm[16][64];
     const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane * 4;
-    const float *p = part + (int64_t)blockIdx.y * blocks * D;
+    const float *p = part + (int64_t)blockIdx.y * blocks * ld;
     void *dst = out.dst[blockIdx.y];
     if (!dst) return;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
     for (int b = grp; b < blocks; b += 64) {
-        const VecOf<float, 4>::raw v = load_row<float, 4, WHOLE>(p + (int64_t)b * D, c, D);
+        const VecOf<float, 4>::raw v = load_row<float, 4, WHOLE>(p + (int64_t)b * ld, c, ld);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += v[i];
     }
@@ -84,11 +84,12 @@ __global__ __launch_bounds__(1024) void k_norm_cols(const float *part, int block
     }
 }
 
-inline void norm_cols(const float *part, int blocks, int64_t D, int sums, const ColumnSums &out, hipStream_t s)
+inline void norm_cols(const float *part, int blocks, int64_t D, int64_t ld, int sums, const ColumnSums &out,
+                      hipStream_t s)
 {
     const dim3 grid((unsigned)((D + 63) / 64), (unsigned)sums);
-    if (D % 4 == 0) hipLaunchKernelGGL(k_norm_cols<true>, grid, dim3(1024), 0, s, part, blocks, (int)D, out);
-    else hipLaunchKernelGGL(k_norm_cols<false>, grid, dim3(1024), 0, s, part, blocks, (int)D, out);
+    if (ld % 4 == 0) hipLaunchKernelGGL(k_norm_cols<true>, grid, dim3(1024), 0, s, part, blocks, (int)D, (int)ld, out);
+    else hipLaunchKernelGGL(k_norm_cols<false>, grid, dim3(1024), 0, s, part, blocks, (int)D, (int)ld, out);
 }
 
 // Threads per row and vectors per thread: the fewest threads that hold a row

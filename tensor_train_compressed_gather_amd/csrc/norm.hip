@@ -263,7 +263,7 @@ hipError_t norm_backward(const NormArgs &a, hipStream_t s)
                            dim3(NormShape<TPR>::threads), 0, s, a, part);
         if (part) {
             const ColumnSums sums{{a.dgamma, a.dbeta}, {a.param_dtype, a.param_dtype}};
-            norm_cols(part, grid, a.D, 2, sums, s);
+            norm_cols(part, grid, a.D, a.D, 2, sums, s);
         }
         return hipGetLastError();
     });
