@@ -409,42 +409,49 @@ class BlockNorm(_Operator):
         self.D, self.layer, self.post, self.eps = int(D), kind == "layer", bool(post), float(eps)
         self.residual_scale, self.block_scale = float(residual_scale), float(block_scale)
         self._kind = (0 if self.layer else TT_EMB_BLOCK_RMS) | (TT_EMB_BLOCK_POST if self.post else 0)
-        _size(_L.tt_emb_block_workspace_size, "BlockNorm", 0, self.D)
+        self._shape = torch.Size((self.D,))
+        self._needs = {0: _size(_L.tt_emb_block_workspace_size, "BlockNorm", 0, self.D)}  # bytes for so many rows
 
     def _inputs(self, x, residual, gate, params, where):
-        ld_x = _matrix(x, where, "x", self.D)
+        """Distances, types and what the parameters say; params are gamma,
+        beta, post_gamma, post_beta."""
+        D = self.D
+        ld_x = _matrix(x, where, "x", D)
         dt = _dtype(x, where, "x")
         n, device = x.shape[0], x.device
-        ld_r = _matrix(residual, where, "residual", self.D, n, None, device)
+        ld_r = _matrix(residual, where, "residual", D, n, None, device)
         rdt = _dtype(residual, where, "residual")
-        if rdt not in (0, dt):
+        if rdt and rdt != dt:
             raise _bad(where, f"residual: dtype {residual.dtype}, expected {x.dtype} or {torch.float32}")
-        kinds, dtype = (torch.float32, x.dtype), None
-        for name, p in params:
+        dtype, index = None, device.index
+        for i, p in enumerate(params):
             if p is None:
                 continue
-            if "beta" in name and not self.layer:
+            name = ("gamma", "beta", "post_gamma", "post_beta")[i]
+            if i & 1 and not self.layer:
                 raise _bad(where, f"{name}: the root mean square has no beta")
-            if "post" in name and not self.post:
+            if i > 1 and not self.post:
                 raise _bad(where, f"{name}: there is no norm of the block's output")
-            _vector(p, where, name, self.D, kinds, device)
-            if dtype is not None and p.dtype != dtype:
-                raise _bad(where, f"{name}: dtype {p.dtype}, expected {dtype} like the other parameters")
-            dtype = p.dtype
+            if dtype is None or not isinstance(p, torch.Tensor) or p.dtype is not dtype or p.shape != self._shape \
+                    or not p.is_contiguous() or p.get_device() != index:
+                _vector(p, where, name, D, (torch.float32, x.dtype), device)
+                if dtype is not None and p.dtype != dtype:
+                    raise _bad(where, f"{name}: dtype {p.dtype}, expected {dtype} like the other parameters")
+                dtype = p.dtype
         kind, ld_g = self._kind, 0
         if gate is not None:
             if isinstance(gate, torch.Tensor) and gate.dim() == 2:
-                ld_g = _matrix(gate, where, "gate", self.D, n, x.dtype, device)
+                ld_g = _matrix(gate, where, "gate", D, n, x.dtype, device)
                 kind |= TT_EMB_BLOCK_GATE_ROWS
             else:
-                _vector(gate, where, "gate", self.D, kinds if dtype is None else (dtype,), device)
+                _vector(gate, where, "gate", D, (torch.float32, x.dtype) if dtype is None else (dtype,), device)
                 dtype = gate.dtype
         return ld_x, ld_r, ld_g, dt, rdt, n, device, dtype, kind
 
     def forward(self, x, residual, gate=None, gamma=None, beta=None, post_gamma=None, post_beta=None, out=None,
                 out_h=None, stream=None):
         where = "BlockNorm.forward"
-        params = (("gamma", gamma), ("beta", beta), ("post_gamma", post_gamma), ("post_beta", post_beta))
+        params = (gamma, beta, post_gamma, post_beta)
         ld_x, ld_r, ld_g, dt, rdt, n, device, dtype, kind = self._inputs(x, residual, gate, params, where)
         guard = _guard(device, stream, where)
         if guard is not None:
@@ -469,28 +476,32 @@ class BlockNorm(_Operator):
     def backward(self, grad_y, grad_h, x, residual, stats, gate=None, gamma=None, post_gamma=None, post_beta=None,
                  stream=None):
         where = "BlockNorm.backward"
-        params = (("gamma", gamma), ("post_gamma", post_gamma), ("post_beta", post_beta))
+        params = (gamma, None, post_gamma, post_beta)
         ld_x, ld_r, ld_g, dt, rdt, n, device, dtype, kind = self._inputs(x, residual, gate, params, where)
         ld_gy = _matrix(grad_y, where, "grad_y", self.D, n, x.dtype, device)
         ld_gh = 0 if grad_h is None else _matrix(grad_h, where, "grad_h", self.D, n, residual.dtype, device)
         _matrix(stats, where, "stats", 4, n, torch.float32, device)
         if not stats.is_contiguous():
             raise _bad(where, "stats: not contiguous")
-        need = _size(_L.tt_emb_block_workspace_size, where, n, self.D)
+        need = self._needs.get(n)
+        if need is None:
+            need = self._needs[n] = _size(_L.tt_emb_block_workspace_size, where, n, self.D)
         guard = _guard(device, stream, where)
         if guard is not None:
             with guard:
                 return self.backward(grad_y, grad_h, x, residual, stats, gate, gamma, post_gamma, post_beta)
-        dx, dr = x.new_empty((n, self.D)), residual.new_empty((n, self.D))
-        dgate = None
+        empty, D, kind_of = torch.empty, self.D, dtype or torch.float32
+        dx, dr = x.new_empty((n, D)), residual.new_empty((n, D))
+        dgate = dbeta = dpost_gamma = dpost_beta = None
         if gate is not None:
-            dgate = x.new_empty((n, self.D)) if gate.dim() == 2 else torch.empty_like(gate)
-
-        def sums(wanted):
-            return torch.empty(self.D, dtype=dtype or torch.float32, device=device) if wanted else None
-
-        dgamma, dbeta = sums(True), sums(self.layer)
-        dpost_gamma, dpost_beta = sums(self.post), sums(self.post and self.layer)
+            dgate = x.new_empty((n, D)) if kind & TT_EMB_BLOCK_GATE_ROWS else empty(D, dtype=kind_of, device=device)
+        dgamma = empty(D, dtype=kind_of, device=device)
+        if self.layer:
+            dbeta = empty(D, dtype=kind_of, device=device)
+        if self.post:
+            dpost_gamma = empty(D, dtype=kind_of, device=device)
+            if self.layer:
+                dpost_beta = empty(D, dtype=kind_of, device=device)
         self._run(_L.tt_emb_block_backward, where, device, _raw_stream(device.index), need, grad_y.data_ptr(), ld_gy,
                   _address(grad_h), ld_gh, x.data_ptr(), ld_x, residual.data_ptr(), ld_r, n, self.D, dt, rdt,
                   _address(gate), ld_g, _address(post_gamma), _address(post_beta), _address(gamma),
