@@ -8,11 +8,18 @@ is normalised and scored against the whole vocabulary:
     y = layer norm(x)                                  LayerNorm
     loss = cross entropy(y W^T, next)                  VocabCrossEntropy
 
+With --hidden F a gated feed-forward block of F columns stands between the sum
+and the loss, and its output returns to the sum through a norm and a gate:
+
+    f = block(layer norm(x))                           LayerNorm, GatedFeedForward
+    y = layer norm(x + gate layer norm(f))             BlockNorm
+
 The gradients take the same way back (the dense table's two are added up in
-place) and one AdamW step updates the TT cores, the dense table and the norm.
+place) and one AdamW step updates the TT cores, the dense table and the norm;
+with --clip N it takes the gradients at a global norm of at most N (GradientClip).
 Tokens are synthetic: each follows its predecessor by a fixed table, with noise.
 
-    python examples/next_token.py [--steps 200] [--bits 8]
+    python examples/next_token.py [--steps 200] [--bits 8] [--hidden 128] [--clip 1.0]
 """
 
 from __future__ import annotations
@@ -33,7 +40,7 @@ IGNORE = -100
 
 class NextToken:
     def __init__(self, device="cuda", context: int = 4, rank: int = 16, state_bits: int = 32, lr: float = 5e-3,
-                 seed: int = 0):
+                 seed: int = 0, hidden: int = 0, clip: float | None = None):
         self.table = Table(1000, (10, 10, 10), (4, 4, 4), (1, rank, rank, 1), 0.1, "uniform")
         self.V, self.D, self.context, self.device = self.table.N, self.table.D, context, device
         g = torch.Generator(device=device)
@@ -50,6 +57,17 @@ class NextToken:
         self.norm = tt.LayerNorm(self.D, device=device)
         self.loss = tt.VocabCrossEntropy(self.V, self.D, ignore_index=IGNORE, device=device)
         self.params = [*self.cores, self.weight, self.gamma, self.beta]
+        self.hidden = hidden
+        if hidden:
+            self.w_in = normal((2 * hidden, self.D), 1.0 / math.sqrt(self.D))
+            self.w_out = normal((self.D, hidden), 1.0 / math.sqrt(hidden))
+            self.block = {"gate": torch.full((self.D,), 0.1, device=device), "gamma": torch.ones(self.D, device=device),
+                          "beta": torch.zeros(self.D, device=device), "post_gamma": torch.ones(self.D, device=device),
+                          "post_beta": torch.zeros(self.D, device=device)}
+            self.feed = tt.GatedFeedForward(self.D, hidden, device=device)
+            self.between = tt.BlockNorm(self.D, kind="layer", post=True, device=device)
+            self.params += [self.w_in, self.w_out, *self.block.values()]
+        self.clip = None if clip is None else tt.GradientClip(clip, device=device)
         self.opt = tt.AdamW(self.params, lr=lr, state_bits=state_bits, seed=seed)
 
     def step(self, context, target):
@@ -61,13 +79,29 @@ class NextToken:
         last = context[:, -1].contiguous()
         x = self.bag.forward(self.cores, tokens, offsets, B) + self.last.forward(self.weight, last)
         y, mean, rstd = self.norm.forward(x, self.gamma, self.beta)
+        if self.hidden:
+            a, block = y, self.block
+            f, pre = self.feed.forward(a, self.w_in, self.w_out, keep=True)
+            y, _, stats = self.between.forward(f, x, **block)
         counts = target != IGNORE
         grad_loss = counts / counts.sum().clamp(min=1)
         loss, _, dy, dweight = self.loss.loss_and_grad(y, self.weight, target, grad_loss)
+        more = []
+        if self.hidden:
+            back = {k: v for k, v in block.items() if k != "beta"}
+            df, dsum, dgate, *dnorms = self.between.backward(dy, None, f, x, stats, **back)
+            dy, dw_in, dw_out = self.feed.backward(df, a, pre, self.w_in, self.w_out)
+            more = [dw_in, dw_out, dgate, *dnorms]
         dx, dgamma, dbeta = self.norm.backward(dy, x, self.gamma, mean, rstd)
+        if self.hidden:
+            dx += dsum
         dcores = self.bag.backward(dx, self.cores, tokens, offsets, B, flags=tt.TT_EMB_REUSE_GROUPING)
         self.last.backward(dx, last, grad_weight=dweight, accumulate=True)
-        self.opt.step([*dcores, dweight, dgamma, dbeta])
+        grads = [*dcores, dweight, dgamma, dbeta, *more]
+        if self.clip is None:
+            self.opt.step(grads)
+        else:
+            self.opt.step(grads, grad_scale=self.clip.norm(grads)[1])
         return loss
 
     def check(self):
@@ -94,9 +128,10 @@ def batches(model: NextToken, B: int, seed: int = 1):
         yield context, torch.where(u > 1 - 1 / 16, IGNORE, target)
 
 
-def train(steps: int, state_bits: int = 32, B: int = 4096, report: int = 0):
+def train(steps: int, state_bits: int = 32, B: int = 4096, report: int = 0, hidden: int = 0,
+          clip: float | None = None):
     """Mean loss of the first and of the last step."""
-    model = NextToken(state_bits=state_bits)
+    model = NextToken(state_bits=state_bits, hidden=hidden, clip=clip)
     first = last = None
     for i, (context, target) in zip(range(steps), batches(model, B)):
         loss = model.step(context, target)
@@ -113,5 +148,7 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--bits", type=int, choices=(8, 32), default=32, help="bits of the AdamW states")
+    ap.add_argument("--hidden", type=int, default=0, help="columns of the gated feed-forward block (0: none)")
+    ap.add_argument("--clip", type=float, default=None, help="largest global norm of the gradients")
     a = ap.parse_args()
-    train(a.steps, a.bits, report=20)
+    train(a.steps, a.bits, report=20, hidden=a.hidden, clip=a.clip)
