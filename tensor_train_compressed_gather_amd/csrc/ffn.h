@@ -57,7 +57,29 @@ struct FfnTerms<float> {
 template <bool NEAR>
 __device__ __forceinline__ void activations(int act, const float (&z)[8], float (&value)[8], float (&slope)[8])
 {
-    if (act == TT_EMB_ACT_GELU) {
+    // z times the sigmoid of x, dx the slope of x
+    auto of_sigmoid = [&](int i, float x, float dx) {
+        if constexpr (NEAR) {
+            const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+            value[i] = z[i] * sg;
+            slope[i] = fmaf(value[i] * dx, 1.f - sg, sg);
+        } else {
+            const float e = expf(-fabsf(x)), r = 1.f / (1.f + e);
+            const float sg = x < 0.f ? e * r : r, other = x < 0.f ? r : e * r; // sigmoid of x and of -x
+            value[i] = z[i] * sg;
+            slope[i] = fmaf(value[i] * dx, other, sg);
+        }
+    };
+    if (act == TT_EMB_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) of_sigmoid(i, z[i], 1.f);
+    } else if (act == TT_EMB_ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float zz = z[i] * z[i];
+            of_sigmoid(i, z[i] * fmaf(0.0713548163f, zz, 1.59576912f), fmaf(0.214064449f, zz, 1.59576912f));
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float c, e;
@@ -76,17 +98,6 @@ __device__ __forceinline__ void activations(int act, const float (&z)[8], float 
             value[i] = z[i] * c;
             slope[i] = fmaf(z[i], 0.39894228f * e, c);
         }
-        return;
-    }
-    const float cube = act == TT_EMB_ACT_GELU_TANH ? 0.044715f : 0.f, by = cube ? 1.59576912f : 1.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float zz = cube * z[i] * z[i], x = by * fmaf(zz, z[i], z[i]), dx = by * fmaf(3.f, zz, 1.f);
-        const float e = NEAR ? __builtin_amdgcn_exp2f(-1.44269504f * fabsf(x)) : expf(-fabsf(x));
-        const float r = NEAR ? __builtin_amdgcn_rcpf(1.f + e) : 1.f / (1.f + e);
-        const float sg = x < 0.f ? e * r : r, other = x < 0.f ? r : e * r; // sigmoid of x and of -x
-        value[i] = z[i] * sg;
-        slope[i] = fmaf(z[i] * dx, sg * other, sg);
     }
 }
 
@@ -253,14 +264,18 @@ __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f)
 
 // Shapes of a product's tiles, (64 NI) x (64 NJ).  BIG ones read each operand
 // least often.  Of SMALL ones a compute unit holds two, which hide each other's
-// loads, starts and ends; of DEEP ones, for grids that leave it no second, one
-// with more loads in flight.  Three terms take three times the LDS (and no DEEP
+// loads, starts and ends; of DEEP and SLIM ones, for grids that leave it no second,
+// one with more loads in flight.  Three terms take three times the LDS (and no DEEP
 // ones, which measured as SMALL ones do).
-enum { BIG, SMALL, DEEP };
+enum { BIG, SMALL, DEEP, SLIM };
 template <int PL, int SHAPE>
 struct FfnShape {
-    static constexpr int NI = SHAPE == BIG ? 4 : 2, NJ = PL == 1 ? NI : NI / 2, TM = 64 * NI, TN = 64 * NJ;
+    static constexpr bool ahead = SHAPE == DEEP || SHAPE == SLIM;
+    static constexpr int NI = SHAPE == BIG ? 4 : 2, NJ = PL > 1 ? NI / 2 : SHAPE == SLIM ? 1 : NI;
+    static constexpr int TM = 64 * NI, TN = 64 * NJ;
 };
+inline int64_t tile_m(int shape) { return shape == BIG ? 256 : 128; }
+inline int64_t tile_n(int PL, int shape) { return PL > 1 || shape == SLIM ? tile_m(shape) / 2 : tile_m(shape); }
 
 // LDS of a product's tiles.  A tile leaves through LDS in fp32, in parts of 64
 // rows and BP blocks of 32 columns of each half (as many as leave room for two
@@ -268,7 +283,7 @@ struct FfnShape {
 template <int PL, bool XT, bool YT, int SHAPE>
 struct FfnLds : FfnShape<PL, SHAPE> {
     typedef FfnShape<PL, SHAPE> S;
-    typedef Stages<PL, XT, SHAPE == DEEP> Stage;
+    typedef Stages<PL, XT, S::ahead> Stage;
     static constexpr int BK = Stage::values, NB = Stage::buffers;
     static constexpr int stage = PL * (TileLds<XT, S::TM, BK>::bytes + TileLds<YT, S::TN, BK>::bytes);
     static constexpr int BP = NB == 4 && SHAPE == SMALL ? 1 : 2, PW = 32 * BP, P = 2 * PW * 4 + 16, part = 64 * P;
@@ -279,31 +294,33 @@ struct FfnLds : FfnShape<PL, SHAPE> {
 // along m (p of them) and n (q) and of the sum's splits (r), p q r = 8, so that an
 // XCD's L2 reads few rows of both operands.
 struct XcdParts {
-    int p, q, r;
+    int p, q, r; // their logarithms
 };
 __device__ __forceinline__ bool xcd_tile(const XcdParts &x, unsigned block, int mt, int nt, int splits, int64_t &m,
                                          int64_t &n, int &split)
 {
     const int xcd = block & 7, local = (int)(block >> 3);
-    const int ri = xcd % x.r, qi = xcd / x.r % x.q, pi = xcd / (x.r * x.q);
-    const int m0 = pi * mt / x.p, n0 = qi * nt / x.q, s0 = ri * splits / x.r;
-    const int dm = (pi + 1) * mt / x.p - m0, dn = (qi + 1) * nt / x.q - n0, ds = (ri + 1) * splits / x.r - s0;
+    const int ri = xcd & ((1 << x.r) - 1), qi = xcd >> x.r & ((1 << x.q) - 1), pi = xcd >> (x.r + x.q);
+    const int m0 = pi * mt >> x.p, n0 = qi * nt >> x.q, s0 = ri * splits >> x.r;
+    const int dm = ((pi + 1) * mt >> x.p) - m0, dn = ((qi + 1) * nt >> x.q) - n0, ds = ((ri + 1) * splits >> x.r) - s0;
     if (local >= dm * dn * ds) return false;
-    m = m0 + local % dm;
-    n = n0 + local / dm % dn;
-    split = s0 + local / (dm * dn);
+    const int row = (int)((unsigned)local / (unsigned)dm), part = (int)((unsigned)row / (unsigned)dn);
+    m = m0 + local - row * dm;
+    n = n0 + row - part * dn;
+    split = s0 + part;
     return true;
 }
 inline XcdParts xcd_parts(int64_t mt, int64_t nt, int64_t splits, unsigned &grid)
 {
-    XcdParts best{1, 1, 8};
+    XcdParts best{0, 0, 3};
     int64_t cost = -1;
-    for (int p = 1; p <= 8; p *= 2)
-        for (int q = 1; p * q <= 8; q *= 2) {
-            const int r = 8 / (p * q);
-            const int64_t dm = (mt + p - 1) / p, dn = (nt + q - 1) / q, ds = (splits + r - 1) / r;
+    for (int p = 0; p <= 3; ++p)
+        for (int q = 0; p + q <= 3; ++q) {
+            const int r = 3 - p - q;
+            auto share = [](int64_t of, int log) { return (of + (1 << log) - 1) >> log; };
+            const int64_t dm = share(mt, p), dn = share(nt, q), ds = share(splits, r);
             // the longest XCD's work, then the operands' rows that it reads
-            const int64_t c = (dm * dn * ds * 8 + 31) / 32 * 4096 + (dm + dn) * ds;
+            const int64_t c = (dm * dn * ds + 3) / 4 * 4096 + (dm + dn) * ds;
             if (cost >= 0 && c >= cost) continue;
             cost = c;
             best = {p, q, r};
@@ -405,10 +422,10 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
         TileLoader<YT, TN, BK, PL, ROT> y(Y, n0, stages, first);
         if constexpr (PAIRED) {
             PairLoader<TM> x(X, o.F, m0, stages, first);
-            multiply<E, PL, XT, YT, SHAPE == DEEP>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+            multiply<E, PL, XT, YT, Lds::ahead>(x, y, stages, lds0, lds1, lds2, lds3, acc);
         } else {
             TileLoader<XT, TM, BK, PL, ROT> x(X, m0, stages, first);
-            multiply<E, PL, XT, YT, SHAPE == DEEP>(x, y, stages, lds0, lds1, lds2, lds3, acc);
+            multiply<E, PL, XT, YT, Lds::ahead>(x, y, stages, lds0, lds1, lds2, lds3, acc);
         }
     }
     __syncthreads();
@@ -570,7 +587,7 @@ struct FfnSize {
 };
 inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
 {
-    const int64_t TM = shape == BIG ? 256 : 128, TN = PL == 1 ? TM : TM / 2;
+    const int64_t TM = tile_m(shape), TN = tile_n(PL, shape);
     return ((z.M + TM - 1) / TM) * ((z.N + TN - 1) / TN);
 }
 
@@ -589,13 +606,16 @@ inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
 // tiles, but not below kSplit values: joining the parts is a launch, 4 us or more.
 int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
 {
-    int64_t big = 0, small = 0, work = 0;
+    int64_t big = 0, small = 0, slim = 0, work = 0;
     for (int i = 0; i < count; ++i) {
         const int64_t parts = may_split && PL > 1 ? (z[i].K < 1024 ? 1 : z[i].K < 4096 ? z[i].K / 1024 : 4) : 1;
         big += tiles_of(z[i], PL, BIG) * parts;
         small += tiles_of(z[i], PL, SMALL);
+        slim += tiles_of(z[i], PL, SLIM);
     }
-    const int shape = big >= (PL > 1 ? kCUs : 2 * kCUs) ? BIG : PL > 1 || small > kCUs ? SMALL : DEEP;
+    const int shape = big >= (PL > 1 ? kCUs : 2 * kCUs) ? BIG
+                      : PL > 1 || small > kCUs          ? SMALL
+                                                        : slim > kCUs ? DEEP : SLIM;
     for (int i = 0; i < count; ++i) work += tiles_of(z[i], PL, shape) * z[i].K;
     const int64_t blocks = shape == SMALL ? 2 * kCUs : kCUs, least = PL > 1 ? kSplit / 4 : kSplit;
     for (int i = 0; i < count; ++i) {
@@ -754,7 +774,7 @@ struct Packing {
 
 FfnJob job_of(const Operand &x, const Operand &y, const FfnSize &z, int PL, int shape, const FfnOut &o)
 {
-    const int64_t TM = shape == BIG ? 256 : 128, TN = PL == 1 ? TM : TM / 2;
+    const int64_t TM = tile_m(shape), TN = tile_n(PL, shape);
     const int64_t mt = (z.M + TM - 1) / TM, nt = (z.N + TN - 1) / TN;
     FfnJob job{x, y, z.K, mt, nt, 0, {}, o};
     if (in_patches(mt, nt)) job.grid = tile_grid(mt, nt, 1);
@@ -769,8 +789,11 @@ void launch(const FfnJob &job, int shape, hipStream_t s)
         hipLaunchKernelGGL((k_ffn<T, XT, YT, OUT, PAIRED, decltype(c)::value>), dim3(job.grid), dim3(256), 0, s, job);
     };
     if (shape == BIG) run(std::integral_constant<int, BIG>());
-    else if (shape == SMALL) run(std::integral_constant<int, SMALL>());
-    else if constexpr (FfnTerms<T>::planes == 1) run(std::integral_constant<int, DEEP>());
+    if (shape == SMALL) run(std::integral_constant<int, SMALL>());
+    if constexpr (FfnTerms<T>::planes == 1) {
+        if (shape == DEEP) run(std::integral_constant<int, DEEP>());
+        if (shape == SLIM) run(std::integral_constant<int, SLIM>());
+    }
 }
 
 template <class T, bool XT, bool YT, int OUT, bool PAIRED>

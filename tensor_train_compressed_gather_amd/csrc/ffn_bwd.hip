@@ -75,8 +75,11 @@ hipError_t ffn_backward(const FfnArgs &a, int dtype, hipStream_t s)
                      out(mid, gy, z[2], shape, a.gw_out, a.ld_gout)};
     const dim3 grid(g.x.grid + g.w_in.grid + g.w_out.grid);
     if (shape == BIG) hipLaunchKernelGGL((k_ffn_grads<T, BIG>), grid, dim3(256), 0, s, g);
-    else if (shape == SMALL) hipLaunchKernelGGL((k_ffn_grads<T, SMALL>), grid, dim3(256), 0, s, g);
-    else if constexpr (PL == 1) hipLaunchKernelGGL((k_ffn_grads<T, DEEP>), grid, dim3(256), 0, s, g);
+    if (shape == SMALL) hipLaunchKernelGGL((k_ffn_grads<T, SMALL>), grid, dim3(256), 0, s, g);
+    if constexpr (PL == 1) {
+        if (shape == DEEP) hipLaunchKernelGGL((k_ffn_grads<T, DEEP>), grid, dim3(256), 0, s, g);
+        if (shape == SLIM) hipLaunchKernelGGL((k_ffn_grads<T, SLIM>), grid, dim3(256), 0, s, g);
+    }
     out.join(s);
     return hipGetLastError();
 }
