@@ -594,16 +594,17 @@ inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
 // The shape of the tiles of a launch of products, and how often each product's
 // sum is split (may_split).
 //
-// 16 bits: BIG for two rounds of the compute units (8192 x 4096 x 16384, y: 930
-// us, 1090 in SMALL ones; 2048 x 1024 x 4096, one round, p and a: 53 and 47), else
-// SMALL where some units get two of them (777 x 1024 x 2688, all outputs of the
-// backward: 34 us, 46 in DEEP ones), else DEEP (300 x 4096 x 1000, p and a: 28 us, 43
-// in SMALL ones).  fp32, whose products are six times as long: BIG for one round,
+// 16 bits: BIG for two rounds of the compute units (2048 x 1024 x 4096, one round,
+// p and a: 53 us, 47 in SMALL ones), else SMALL where some units get two of them (777
+// x 1024 x 2688, all outputs of the backward: 34 us, 46 in DEEP ones), else DEEP (300 x
+// 4096 x 1000, p and a: 28 us, 43 in SMALL ones), or SLIM where there are units for
+// them, too (21 us; 128 x 1024 x 4096: 9.5, 12.8 in DEEP ones).  fp32, whose products are six times as long: BIG for one round,
 // counting the splits of a long sum (2048 x 2048 x 4096, y: 188 us, 240 in SMALL
 // ones; 777 x 1024 x 2688: 47 and 41), else SMALL.
 //
-// Sums are split so that the units have equal work, one block each, two of SMALL
-// tiles, but not below kSplit values: joining the parts is a launch, 4 us or more.
+// Sums are split so that the units have equal work, one block each (of the
+// backward's SMALL tiles two), but not below kSplit values, a quarter of them for
+// fp32: joining the parts is a launch, 4 us or more.
 int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
 {
     int64_t big = 0, small = 0, slim = 0, work = 0;
@@ -617,7 +618,7 @@ int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
                       : PL > 1 || small > kCUs          ? SMALL
                                                         : slim > kCUs ? DEEP : SLIM;
     for (int i = 0; i < count; ++i) work += tiles_of(z[i], PL, shape) * z[i].K;
-    const int64_t blocks = shape == SMALL ? 2 * kCUs : kCUs, least = PL > 1 ? kSplit / 4 : kSplit;
+    const int64_t blocks = shape == SMALL && count > 1 ? 2 * kCUs : kCUs, least = PL > 1 ? kSplit / 4 : kSplit;
     for (int i = 0; i < count; ++i) {
         int64_t s = may_split ? (z[i].K * blocks + work - 1) / work : 1;
         if (s > z[i].K / least) s = z[i].K / least;
