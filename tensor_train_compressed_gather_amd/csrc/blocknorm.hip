@@ -119,7 +119,9 @@ __global__ __launch_bounds__(kBlockLong) void k_block_fwd_long(BlockNormArgs a)
 #pragma clang loop unroll(disable)
             for (int c = threadIdx.x * VEC; c < D; c += kBlockLong * VEC) f(c, D - c);
         };
-        auto take_x = [&](int c, int left, float(&v)[VEC]) { values<T, WHOLE>(load_cols<T, WHOLE>(x, c, D), left, D, v); };
+        auto take_x = [&](int c, int left, float(&v)[VEC]) {
+            values<T, WHOLE>(load_cols<T, WHOLE>(x, c, D), left, D, v);
+        };
         // mean and rstd of what take(c, left, v) gives
         auto stats = [&](auto take, float &mean, float &rstd) {
             mean = 0.f;

@@ -346,7 +346,8 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
     typedef typename FfnTerms<T>::type E;
     constexpr int PL = FfnTerms<T>::planes;
     typedef FfnLds<PL, XT, YT, SHAPE> Lds;
-    constexpr int NI = Lds::NI, NJ = Lds::NJ, TM = Lds::TM, TN = Lds::TN, BK = Lds::BK, BP = Lds::BP, PM = NI / BP, PW = Lds::PW, P = Lds::P;
+    constexpr int NI = Lds::NI, NJ = Lds::NJ, TM = Lds::TM, TN = Lds::TN, BK = Lds::BK;
+    constexpr int BP = Lds::BP, PM = NI / BP, PW = Lds::PW, P = Lds::P;
     Operand X = job.X, Y = job.Y;
     const FfnOut &o = job.o;
     int64_t mi, ni, K = job.K;
@@ -595,12 +596,13 @@ inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
 // sum is split (may_split).
 //
 // 16 bits: BIG for two rounds of the compute units (2048 x 1024 x 4096, one round,
-// p and a: 53 us, 47 in SMALL ones), else SMALL where some units get two of them (777
-// x 1024 x 2688, all outputs of the backward: 34 us, 46 in DEEP ones), else DEEP (300 x
-// 4096 x 1000, p and a: 28 us, 43 in SMALL ones), or SLIM where there are units for
-// them, too (21 us; 128 x 1024 x 4096: 9.5, 12.8 in DEEP ones).  fp32, whose products are six times as long: BIG for one round,
-// counting the splits of a long sum (2048 x 2048 x 4096, y: 188 us, 240 in SMALL
-// ones; 777 x 1024 x 2688: 47 and 41), else SMALL.
+// p and a: 53 us, 47 in SMALL ones), else SMALL where some units get two of them
+// (777 x 1024 x 2688, all outputs of the backward: 34 us, 46 in DEEP ones), else
+// DEEP (300 x 4096 x 1000, p and a: 28 us, 43 in SMALL ones), or SLIM where there
+// are units for them, too (21 us; 128 x 1024 x 4096: 9.5, 12.8 in DEEP ones).  fp32,
+// whose products are six times as long: BIG for one round, counting the splits of a
+// long sum (2048 x 2048 x 4096, y: 188 us, 240 in SMALL ones; 777 x 1024 x 2688: 47
+// and 41), else SMALL.
 //
 // Sums are split so that the units have equal work, one block each (of the
 // backward's SMALL tiles two), but not below kSplit values, a quarter of them for
@@ -740,8 +742,8 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
 }
 FfnCopies copies_of(const FfnArgs &a, int dtype, bool grad)
 {
-    return ffn_copies(dtype == TT_EMB_DTYPE_FLOAT, grad, a.n, a.D, a.F, lies_well(a.x, a.ld_x), lies_well(a.w_in, a.ld_in),
-                      lies_well(a.w_out, a.ld_out), lies_well(a.gy, a.ld_gy));
+    return ffn_copies(dtype == TT_EMB_DTYPE_FLOAT, grad, a.n, a.D, a.F, lies_well(a.x, a.ld_x),
+                      lies_well(a.w_in, a.ld_in), lies_well(a.w_out, a.ld_out), lies_well(a.gy, a.ld_gy));
 }
 
 // ---------------------------------------------------------- host: launches

@@ -192,7 +192,8 @@ void few(const FewArgs &a, int splits, hipStream_t s)
     if constexpr (sizeof(T) == 4) {
         if (a.n > 64) return run(std::integral_constant<int, 8>(), four);
         if (a.n > 32) return idle ? run(four, eight) : run(four, four);
-        if (a.n > 16) return idle ? run(std::integral_constant<int, 2>(), eight) : run(std::integral_constant<int, 2>(), four);
+        constexpr std::integral_constant<int, 2> two;
+        if (a.n > 16) return idle ? run(two, eight) : run(two, four);
     }
     constexpr std::integral_constant<int, 1> one;
     return idle ? run(one, eight) : run(one, four);
@@ -284,7 +285,8 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
 size_t ffn_workspace(int64_t n, int64_t D, int64_t F, int dtype, int what)
 {
     const bool fp32 = dtype == TT_EMB_DTYPE_FLOAT, grad = what & TT_EMB_FFN_GRAD, well = what & TT_EMB_FFN_ALIGNED;
-    return plan_ffn(n, D, F, fp32 ? 3 : 1, grad, ffn_copies(fp32, grad, n, D, F, well, well, well, well), nullptr).bytes;
+    const FfnCopies copies = ffn_copies(fp32, grad, n, D, F, well, well, well, well);
+    return plan_ffn(n, D, F, fp32 ? 3 : 1, grad, copies, nullptr).bytes;
 }
 
 size_t ffn_needs(const FfnArgs &a, int dtype, bool grad)

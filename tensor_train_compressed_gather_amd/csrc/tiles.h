@@ -111,7 +111,8 @@ struct TileLoader {
         p = a.p + (TURNED ? r0 : r0 * a.ld);
         next = TURNED ? BK * a.ld : BK;
         if constexpr (TURNED) {
-            const int64_t have = a.rows > 0 ? a.rows : 0, full = have / BK; // (a part that begins past the rows has none)
+            const int64_t have = a.rows > 0 ? a.rows : 0; // (a part that begins past the rows has none)
+            const int64_t full = have / BK;
             const int cols = (int)(a.cols - r0 < R ? a.cols - r0 : R), left = (int)(have - full * BK);
             whole = cols > 0 ? (int)(full < stages ? full : stages) : 0;
             bytes = (unsigned)((BK - 1) * ld + cols) * 2;

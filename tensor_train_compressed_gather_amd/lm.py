@@ -398,8 +398,10 @@ class BlockNorm(_Operator):
     ``out`` may be x and ``out_h`` the residual itself.
     backward(grad_y, grad_h, x, residual, stats, gate, gamma, post_gamma,
     post_beta) -> (grad_x, grad_residual, grad_gate, dgamma, dbeta,
-    dpost_gamma, dpost_beta), None where there is no such parameter (without a
-    gamma its gradient is still given, in fp32); grad_h may be None."""
+    dpost_gamma, dpost_beta), None where ``kind`` and ``post`` have no such
+    parameter or there is no gate (a gamma or beta of None counts as 1 or 0 and
+    has a gradient), of the parameters' type, fp32 where all are None; grad_h
+    may be None."""
 
     def __init__(self, D: int, kind: str = "rms", post: bool = False, eps: float = 1e-5, residual_scale: float = 1.0,
                  block_scale: float = 1.0, device="cuda"):
@@ -410,7 +412,7 @@ class BlockNorm(_Operator):
         self.residual_scale, self.block_scale = float(residual_scale), float(block_scale)
         self._kind = (0 if self.layer else TT_EMB_BLOCK_RMS) | (TT_EMB_BLOCK_POST if self.post else 0)
         self._shape = torch.Size((self.D,))
-        self._needs = {0: _size(_L.tt_emb_block_workspace_size, "BlockNorm", 0, self.D)}  # bytes for so many rows
+        _size(_L.tt_emb_block_workspace_size, "BlockNorm", 0, self.D)
 
     def _inputs(self, x, residual, gate, params, where):
         """Distances, types and what the parameters say; params are gamma,
@@ -483,9 +485,7 @@ class BlockNorm(_Operator):
         _matrix(stats, where, "stats", 4, n, torch.float32, device)
         if not stats.is_contiguous():
             raise _bad(where, "stats: not contiguous")
-        need = self._needs.get(n)
-        if need is None:
-            need = self._needs[n] = _size(_L.tt_emb_block_workspace_size, where, n, self.D)
+        need = _size(_L.tt_emb_block_workspace_size, where, n, self.D)
         guard = _guard(device, stream, where)
         if guard is not None:
             with guard:
@@ -524,9 +524,11 @@ class GatedFeedForward(_Operator):
     backward(grad_y, x, p, w_in, w_out) -> (grad_x, grad_w_in, grad_w_out).
 
     bf16 and fp16: sums are fp32, a and p's gradient are rounded to the type
-    between the products.  fp32: operands are taken as three bf16 terms, 24
-    bits.  16-bit rows of a multiple of 8 columns (along a sum: of 64) that begin
-    at multiples of 16 bytes are read in place; others are copied by each call."""
+    between the products.  fp32: from 129 rows on, and in the backward, operands
+    are taken as three bf16 terms, 24 bits (less below 2^-100).  16-bit rows of
+    a multiple of 8 columns (along a sum: of 64) that begin at multiples of 16
+    bytes are read in place, and so are up to 16 rows' operands in the forward (up
+    to 128 in fp32); others are copied by each call."""
 
     ACTIVATIONS = {"silu": TT_EMB_ACT_SILU, "gelu": TT_EMB_ACT_GELU, "gelu_tanh": TT_EMB_ACT_GELU_TANH}
 

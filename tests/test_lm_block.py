@@ -108,8 +108,9 @@ def forward64(x, res, kw, layer, post, a, b):
     return y, h, my + (k["beta"].abs() if k["beta"] is not None else 0.0), mh
 
 
-CASES = [(1, 1, 0), (3, 2, 0), (5, 7, 3), (17, 128, 0), (33, 129, 1), (4, 512, 0), (70, 513, 0), (9, 1001, 5), (700, 1024, 0), (1300, 640, 2),
-         (20, 2048, 0), (6, 2049, 0), (7, 4096, 0), (40, 4100, 4), (3, 8192, 0), (5, 8200, 8), (2, 16384, 0),
+CASES = [(1, 1, 0), (3, 2, 0), (5, 7, 3), (17, 128, 0), (33, 129, 1), (4, 512, 0), (70, 513, 0), (9, 1001, 5),
+         (700, 1024, 0), (1300, 640, 2), (20, 2048, 0), (6, 2049, 0), (7, 4096, 0), (40, 4100, 4),
+         (3, 8192, 0), (5, 8200, 8), (2, 16384, 0),
          (35, 9999, 0), (3000, 24, 0), (1500, 300, 0), (2, 5, 1), (1100, 3000, 0), (2100, 4099, 0)]
 KINDS = [(F32, F32, F32), (BF16, BF16, F32), (BF16, F32, BF16), (F16, F16, F16), (F16, F32, F32)]
 

@@ -11,6 +11,7 @@ p's gradient are rounded once (u of the value), and so is what is returned (p to
 import pytest
 import test_lm_abi as abi
 import test_lm_ops as ops
+import test_lm_threads as threads
 import torch
 
 import tensor_train_compressed_gather_amd as tt
@@ -147,9 +148,11 @@ def check(n, D, F, t, gap, kind, seed=None):
 
 
 SHAPES = [(1, 1, 1, 0), (1, 64, 64, 0), (2, 8, 40, 0), (3, 17, 5, 3), (5, 100, 33, 1), (31, 128, 64, 0),
-          (64, 64, 128, 8), (12, 1000, 4096, 0), (65, 130, 250, 0), (127, 256, 129, 0), (128, 72, 96, 0), (129, 264, 320, 8),
+          (64, 64, 128, 8), (12, 1000, 4096, 0), (65, 130, 250, 0), (127, 256, 129, 0),
+          (128, 72, 96, 0), (129, 264, 320, 8),
           (200, 1000, 70, 0), (257, 520, 300, 5), (600, 96, 1100, 0), (40, 2000, 3000, 0), (1030, 200, 200, 1),
-          (16, 640, 1280, 0), (17, 192, 2048, 0), (9, 4096, 100, 0), (33, 200, 5000, 0), (100, 1024, 1500, 0), (4, 130, 9000, 3)]
+          (16, 640, 1280, 0), (17, 192, 2048, 0), (9, 4096, 100, 0), (33, 200, 5000, 0),
+          (100, 1024, 1500, 0), (4, 130, 9000, 3)]
 
 
 @pytest.mark.gpu
@@ -169,6 +172,32 @@ def test_large_tiles(n, D, F, t):
         n, D, F = n // 2, D // 2, F // 2
     print(f"[case] ffn n={n} D={D} F={F} {t}", flush=True)
     check(n, D, F, t, 0, "silu")
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("n,D,F", [(0, 1, 1), (1, 65536, 65536), (2 ** 28, 100, 100), (129, 64, 65536),
+                                   (2 ** 20, 128, 512), (17, 1, 1), (10 ** 6, 4096, 1)])
+def test_workspace_of_any_size(n, D, F, dtype):
+    for what in (0, 1):
+        assert 256 <= size(n, D, F, dtype, what | 2) <= size(n, D, F, dtype, what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [9, 200])
+@pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** 30])
+def test_fp32_keeps_its_precision_at_any_size(n, scale):
+    # x times a power of two and the weight by it: the same p; the same for y and
+    # the gradient.  All products are those of scale 1, bit for bit
+    D, F = 100, 72
+    x, w_in, w_out, gy = make(n, D, F, F32, 0, 8)
+    op = tt.GatedFeedForward(D, F)
+    y, pre = op.forward(x, w_in, w_out, keep=True)
+    dx, dw_in, dw_out = op.backward(gy, x, pre, w_in, w_out)
+    y2, pre2 = op.forward(x * scale, w_in / scale, w_out * scale, keep=True)
+    assert torch.equal(pre, pre2) and torch.equal(y * scale, y2)
+    got = op.backward(gy / scale, x * scale, pre2, w_in / scale, w_out * scale)
+    assert torch.equal(got[0], dx / scale) and torch.equal(got[1], dw_in * scale)
+    assert torch.equal(got[2], dw_out / scale)
 
 
 @pytest.mark.gpu
@@ -221,7 +250,7 @@ def test_gradients_against_differences(n, D, F, kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("t", [F32, BF16])
-@pytest.mark.parametrize("n", [20, 300])
+@pytest.mark.parametrize("n", [8, 20, 300])
 def test_rows_do_not_meet(n, t):
     D, F = 72, 100
     x, w_in, w_out, gy = make(n, D, F, t, 0, 1)
@@ -288,6 +317,33 @@ def test_arguments_that_do_not_fit():
     abi.refused(op.backward, gy, x, pre[:, :F], w_in, w_out, msg="shape")
     abi.refused(op.backward, gy, x, pre.bfloat16(), w_in, w_out, msg="dtype")
     abi.refused(op.backward, gy, x, pre, w_in, w_out, grad_w_in=w_out, msg="shape")
+
+
+@pytest.mark.gpu
+def test_threads_share_an_operator():
+    D, F = 64, 200
+    op, clip = tt.GatedFeedForward(D, F), tt.GradientClip(0.5)
+    cases = [make(n, D, F, BF16, 0, n) for n in (3, 140, 700)]
+    refs = []
+
+    def step(x, w_in, w_out, gy):
+        y, pre = op.forward(x, w_in, w_out, keep=True)
+        grads = list(op.backward(gy, x, pre, w_in, w_out))
+        norm = clip.clip(grads)
+        return [y, pre, norm, *grads]
+
+    for c in cases:
+        refs.append(step(*c))
+    torch.cuda.synchronize()
+
+    def work(k):
+        for _ in range(15):
+            got = step(*cases[k])
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(got, refs[k]))
+
+    threads.in_threads(work, 3)
+    assert op.poll_error() == 0 and clip.poll_error() == 0
 
 
 @pytest.mark.gpu
