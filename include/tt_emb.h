@@ -461,9 +461,9 @@ int tt_emb_block_workspace_size(int64_t n, int64_t D, size_t *bytes);
 /* The gated feed-forward block:
  *   p = x w_in^T [n][2F],  a_ij = act(p_ij) p_i,F+j,  y = a w_out^T
  * x, y [n][D], w_in [2F][D] (the gate's F rows, then the other projection's),
- * w_out [D][F], all of `dtype`; D, F <= 65536, n < 2^31, n max(2F, D) below 2^37.  pre, fp32 [n][2F], receives p for the
- * backward (NULL: not kept); rounded to 16 bits it would cost the gradients half
- * of their error.  act: silu(z) = z sigmoid(z), gelu(z) = z Phi(z), or
+ * w_out [D][F], all of `dtype`; D, F <= 65536, n < 2^31, n max(2F, D) below 2^37.
+ * pre, fp32 [n][2F], receives p for the backward (NULL: not kept); in 16 bits it
+ * would raise the gradients' error by half.  act: silu(z) = z sigmoid(z), gelu(z) = z Phi(z), or
  * gelu's tanh form z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
  * bf16 and fp16: sums are fp32, a is rounded to dtype (so in fp16 an |a| past 65504
  * is infinite).  fp32: from 129 rows on, and in the backward, operands are taken as

@@ -8,6 +8,11 @@
 // up to 4096 values are held in registers: x and r are read once and y and h
 // written once, and the second norm works on h before it is rounded.  Longer
 // rows are read again, from the caches, for each of the norms' sums.
+//
+// Memory bounds it: 16384 x 4096 bf16 in 115 us (4.7 TB/s), 32768 x 128 fp32 in
+// 14.8 (4.5 TB/s), 3001 x 1001 fp16 beside an fp32 residual and a gate per row in
+// 16.8.  Each thread has the next row's loads in flight while it reduces one; two
+// rows ahead cost a wave in four and 152 us for the first of these.
 #include "blocknorm.h"
 
 namespace ttemb {

@@ -4,8 +4,10 @@
 // N = sqrt(sum g^2) over all tensors, factor = min(1, max_norm / (N + eps)).
 // The squares are taken and added in fp64: those of fp32 values are exact
 // there, none over- or underflows, and a sum of 10^9 of them is off by 2^-53
-// times its few hundred additions per thread.  Memory bounds the kernels, so
-// fp64 costs nothing.
+// its few hundred additions per thread.  Memory bounds the kernels: 25.2 M fp32
+// values are read in 17.3 us (5.8 TB/s) and scaled in 33.5 (6.0 TB/s).  Of 16-bit
+// values fp64 takes the same instructions for half the bytes (159 M of bf16: 82
+// us, 3.9 TB/s), the price of sums that no value can overflow.
 //
 // Each block adds up the chunks it owns and leaves one partial sum; the next
 // launch begins by adding up the partial sums, every block for itself in the
@@ -18,7 +20,10 @@ namespace ttemb {
 namespace {
 
 constexpr int kClipChunk = 8192; // elements that a block takes at a time
-constexpr int kClipOne = 4;      // chunks of all tensors up to which one block does everything
+// Chunks of all tensors up to which one block does everything (the 3 cores of a
+// 1000-row table, 1760 values: 9 us of one launch; two launches take 3.5 and 4 us
+// and the way between them).
+constexpr int kClipOne = 4;
 
 // A chunk's values by this thread: 16 bytes at a time, zeros past the end.
 template <class T>

@@ -10,13 +10,16 @@
 // gate and of the other projection in turn, 32 of each, so that both halves of
 // a value of `a` meet in one thread: p leaves the registers only where the
 // caller keeps it for the backward.  The backward's first product makes da, and
-// dp and a from it and p, in the tile that holds da.  Matrix instructions bound
-// the large sizes.
+// dp and a from it and p, in the tile that holds da.  Matrix instructions and the
+// power that they take bound the large sizes (8192 x 4096 x 16384 bf16: p and a in
+// 1.96 ms, 1120 TFLOP/s with 1.3 GB written, y in 0.91, dp and a in 1.17, the three
+// gradients in 4.0, 1370 TFLOP/s; the clock is at 1.5 to 1.8 GHz meanwhile).
 //
 // bf16 and fp16: a and dp are rounded to the inputs' type, half a step each,
 // because the products that take them have operands of 16 bits; two terms of
-// them would double two thirds of the products.  Both are made from p before its
-// rounding in the forward, after it in the backward.
+// them would double two thirds of the products.  Both are made from p in fp32,
+// in the backward too: rounded to 16 bits there, p alone would add as much to the
+// gradients' error (bf16: 3.5e-3 of their size, 2.3e-3 so).
 //
 // fp32: every operand is split into three bf16 terms (24 bits, the range of
 // fp32), and the six products of terms above 2^-25 are added up: the rounding of

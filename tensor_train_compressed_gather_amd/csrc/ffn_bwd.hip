@@ -7,7 +7,8 @@ namespace {
 
 // The backward's three outputs, which do not wait for each other, in one launch:
 // at small sizes each alone leaves most of the card idle, and a launch costs as
-// much as a product.
+// much as a product (777 x 1001 x 2731 bf16: 34 us, 51 in three launches; 8192 x
+// 128 x 512 fp32: 44 us, 71).
 struct FfnGrads {
     FfnJob x, w_in, w_out;
 };
