@@ -17,9 +17,10 @@
 //
 // bf16 and fp16: a and dp are rounded to the inputs' type, half a step each,
 // because the products that take them have operands of 16 bits; two terms of
-// them would double two thirds of the products.  Both are made from p in fp32,
-// in the backward too: rounded to 16 bits there, p alone would add as much to the
-// gradients' error (bf16: 3.5e-3 of their size, 2.3e-3 so).
+// them, which they have where they are few (two_terms), double two thirds of the
+// products.  Both are made from p in fp32, in the backward too: rounded to 16 bits
+// there, p alone would add as much to the gradients' error (bf16: 3.5e-3 of their
+// size, 2.3e-3 so).
 //
 // fp32: every operand is split into three bf16 terms (24 bits, the range of
 // fp32), and the six products of terms above 2^-25 are added up: the rounding of
@@ -37,7 +38,7 @@ namespace {
 
 constexpr int64_t kPad = 64;       // summed values of packed rows are padded to this
 constexpr int64_t kSplit = 512;    // least summed values of a split
-constexpr int kPacks = 5;          // copies that one launch makes, at most
+constexpr int kPacks = 6;          // copies that one launch makes, at most
 
 template <class T>
 struct FfnTerms {
@@ -177,6 +178,7 @@ struct FfnOut {
     int64_t ld_mid, plane_mid;
     short *dpre; // planes of [rows][ld_dpre]
     int64_t ld_dpre, plane_dpre;
+    bool two; // a and dp have two terms (16-bit types), the latter half of an output's parts are the second's
 };
 
 // Rows of both projections as they lie in memory, 32 of the one and 32 of the
@@ -241,6 +243,8 @@ __device__ __forceinline__ void store_terms(short *p, int64_t plane, int left, c
         split_terms<E, PL>(x[i], s);
 #pragma unroll
         for (int q = 0; q < PL; ++q) w[q][i] = s[q];
+        // what rounds to infinity stays that
+        if (PL == 2 && !(fabsf((float)__builtin_bit_cast(E, w[0][i])) < INFINITY)) w[1][i] = 0;
     }
 #pragma unroll
     for (int q = 0; q < PL; ++q) {
@@ -256,6 +260,13 @@ __device__ __forceinline__ void store_terms(short *p, int64_t plane, int left, c
                 if (i < left) p[q * plane + i] = w[q][i];
         }
     }
+}
+
+template <class T, int PL>
+__device__ __forceinline__ void store_terms(short *p, int64_t plane, int left, const float (&x)[8], bool two)
+{
+    if (PL == 1 && two) store_terms<T, 2>(p, plane, left, x);
+    else store_terms<T, PL>(p, plane, left, x);
 }
 
 // f for each of the numbers, as constants.
@@ -362,10 +373,10 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
     }
     float *sum = nullptr;
     if (OUT == FFN_OUT && o.sum) { // this split's part of the sum
-        const int64_t k0 = sp * o.split_k;
-        if (k0 >= K) return;
+        const int parts = o.two ? o.splits / 2 : o.splits, second = sp >= parts;
+        const int64_t k0 = (sp - second * parts) * o.split_k;
         auto from = [&](Operand &a, bool turned) {
-            a.p += turned ? k0 * a.ld : k0;
+            a.p += (turned ? k0 * a.ld : k0) + second * a.plane;
             (turned ? a.rows : a.cols) -= k0;
         };
         from(X, XT);
@@ -479,7 +490,7 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] = m + e < o.F ? a[e] * u[e] : 0.f;
                 if (i >= o.rows || m >= o.ld_mid) continue;
-                store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, 8, a);
+                store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, 8, a, SHAPE != BIG && o.two);
                 if (o.pre && m < o.F) {
                     float *to = o.pre + i * o.ld_pre + m;
                     const int left = (int)(o.F - m < 8 ? o.F - m : 8);
@@ -514,10 +525,10 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
                         u[e] = x[e] * a[e];
                     }
                     if (i >= o.rows || left <= 0) continue;
-                    store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, left, slope);
+                    store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, left, slope, SHAPE != BIG && o.two);
                     short *d = o.dpre + i * o.ld_dpre + m;
-                    store_terms<T, PL>(d, o.plane_dpre, left, g);
-                    store_terms<T, PL>(d + o.F, o.plane_dpre, left, u);
+                    store_terms<T, PL>(d, o.plane_dpre, left, g, SHAPE != BIG && o.two);
+                    store_terms<T, PL>(d + o.F, o.plane_dpre, left, u, SHAPE != BIG && o.two);
                 } else {
                     if (i >= o.rows || left <= 0) continue;
                     if (sum) store_part<float, 8>(sum + i * o.cols + m, left, x);
@@ -610,7 +621,9 @@ inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
 // Sums are split so that the units have equal work, one block each (of the
 // backward's SMALL tiles two), but not below kSplit values, a quarter of them for
 // fp32: joining the parts is a launch, 4 us or more.
-int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
+//
+// two: each part is there for both terms of an operand.
+int ffn_shape(FfnSize *z, int count, int PL, bool may_split, bool two = false)
 {
     int64_t big = 0, small = 0, slim = 0, work = 0;
     for (int i = 0; i < count; ++i) {
@@ -626,10 +639,11 @@ int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
     const int64_t blocks = shape == SMALL && count > 1 ? 2 * kCUs : kCUs, least = PL > 1 ? kSplit / 4 : kSplit;
     for (int i = 0; i < count; ++i) {
         int64_t s = may_split ? (z[i].K * blocks + work - 1) / work : 1;
+        if (two) s /= 2;
         if (s > z[i].K / least) s = z[i].K / least;
         if (s < 1) s = 1;
         z[i].each = up((z[i].K + s - 1) / s, kPad);
-        z[i].splits = (int)((z[i].K + z[i].each - 1) / z[i].each);
+        z[i].splits = (int)((z[i].K + z[i].each - 1) / z[i].each) * (two ? 2 : 1);
     }
     return shape;
 }
@@ -680,11 +694,22 @@ FfnCopies ffn_copies(bool fp32, bool grad, int64_t n, int64_t D, int64_t F, bool
     return {!x || !d, !w_in || !d, !w_out || !f, false};
 }
 
+// Whether a and dp of 16-bit inputs have two terms, 16 bits or more.  One term's
+// roundings bring the outputs' error to 1.4 times their own rounding where they are
+// many; few do not average out (14 x 53 x 19 bf16: 1.5 times).  The second term
+// doubles an output's products and adds the join of their parts, 0 to 6 us of a call
+// where there are so few values of a (14 x 53 x 19, backward: 26 us, 22 with one
+// term), but 14 us of 24 for 4 x 300 x 2000 and 21 of 27 for 64 x 2048 x 1024.
+// Grids in patches are not split, so the outputs have few tiles.
+bool two_terms(int64_t n, int64_t D, int64_t F)
+{
+    return n * F <= 1 << 11 && D * (n > 2 * F ? n : 2 * F) <= 1 << 22;
+}
 // The sums of y, and of the gradients of x, w_in and w_out.
 FfnSize y_size(int64_t n, int64_t D, int64_t F, int PL, int *shape = nullptr)
 {
     FfnSize z{D, n, up(F, kPad)};
-    const int s = ffn_shape(&z, 1, PL, true);
+    const int s = ffn_shape(&z, 1, PL, true, PL == 1 && two_terms(n, D, F));
     if (shape) *shape = s;
     return z;
 }
@@ -693,7 +718,7 @@ int grad_sizes(FfnSize *z, int64_t n, int64_t D, int64_t F, int PL)
     z[0] = {D, n, up(2 * F, kPad)};
     z[1] = {D, 2 * F, up(n, kPad)};
     z[2] = {F, D, up(n, kPad)};
-    return ffn_shape(z, 3, PL, true);
+    return ffn_shape(z, 3, PL, true, PL == 1 && two_terms(n, D, F));
 }
 
 struct FfnPlan {
@@ -701,6 +726,7 @@ struct FfnPlan {
     float *sum;
     int64_t Dp, Fp, Pp; // padded columns of x and gy, of a, of dp
     int64_t ldD, ldF, ldP;
+    bool two;
     size_t bytes;
 };
 // Distance of rows of so many columns: an odd number of cache lines where it would
@@ -711,9 +737,9 @@ inline int64_t apart(int64_t cols) { return cols % 512 ? cols : cols + 64; }
 FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCopies &c, char *base)
 {
     size_t off = TT_EMB_STATUS_BYTES;
-    auto take = [&](int64_t rows, int64_t cols) {
+    auto take = [&](int64_t rows, int64_t cols, int planes) {
         char *r = base ? base + off : nullptr;
-        off += round256((size_t)PL * rows * cols * 2);
+        off += round256((size_t)planes * rows * cols * 2);
         return reinterpret_cast<short *>(r);
     };
     FfnPlan p{};
@@ -724,14 +750,16 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
     p.ldD = apart(p.Dp);
     p.ldF = apart(p.Fp);
     p.ldP = apart(p.Pp);
-    if (c.x) p.x = take(n, p.ldD);
-    if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.ldD);
-    if (c.w_out) p.w_out = take(D, p.ldF);
-    if (c.gy) p.gy = take(n, p.ldD);
-    p.mid = take(n, p.ldF);
+    if (c.x) p.x = take(n, p.ldD, PL);
+    if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.ldD, PL);
+    if (c.w_out) p.w_out = take(D, p.ldF, PL);
+    if (c.gy) p.gy = take(n, p.ldD, PL);
+    p.two = PL == 1 && two_terms(n, D, F);
+    const int terms = p.two ? 2 : PL;
+    p.mid = take(n, p.ldF, terms);
     size_t sums;
     if (grad) {
-        p.dpre = take(n, p.ldP);
+        p.dpre = take(n, p.ldP, terms);
         FfnSize z[3];
         grad_sizes(z, n, D, F, PL);
         sums = z[0].bytes() + z[1].bytes() + z[2].bytes();
@@ -762,7 +790,7 @@ struct Packing {
         if (!dst) return Operand{static_cast<const short *>(src), ld, 0, rows, cols};
         const int64_t to = pair ? 2 * up(pair, 32) : rows, ldp = apart(width);
         add(Pack{src, ld, to, cols, dst, width, ldp, to * ldp, pair});
-        return Operand{dst, ldp, to * ldp, to, width};
+        return Operand{dst, ldp, FfnTerms<T>::planes > 1 ? to * ldp : 0, to, width};
     }
     void add(const Pack &job)
     {
@@ -816,6 +844,7 @@ template <class T>
 struct Outputs {
     float *sum;
     Joins joins{};
+    bool two; // (operands without a second term have a plane of 0)
     int n = 0;
 
     FfnJob operator()(const Operand &x, const Operand &y, const FfnSize &z, int shape, void *out, int64_t ld)
@@ -829,6 +858,7 @@ struct Outputs {
         if (z.splits > 1) {
             o.sum = sum;
             o.split_k = z.each;
+            o.two = two;
             sum += z.bytes() / sizeof(float);
             joins.job[n] = Join{o.sum, z.splits, z.N, z.M, out, ld};
             joins.first[n + 1] = joins.first[n] + (int)blocks_for(z.N * ((z.M + 3) / 4));

@@ -16,6 +16,8 @@ namespace {
 // loads in flight while one is multiplied, and meet in LDS.  Lane l holds row l %
 // 16 and the l / 16-th 16 bytes of each 64 of a chunk.
 //
+// TWO: a has two terms (two_terms), whose products meet in one sum.
+//
 // Blocks begin at different places of the sum: rows lie a multiple of a KB apart
 // as a rule, and equal columns of all of them meet in few channels of the L2 (4
 // rows of 4096 x 16384 bf16: 84 us when all begin with the first, 72 so, 5.6 TB/s).
@@ -30,6 +32,7 @@ struct FewArgs {
     void *out;          // a (PAIR) or y
     int64_t ld_out;
     float *sum;         // [splits][n][rows]
+    int64_t second;     // elements from a (out, PAIR; else x) to its second term, 0 for none
 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -52,18 +55,19 @@ struct FewStep {
     }
 };
 
-template <class T, bool PAIR, int NB, int WAVES>
+template <class T, bool PAIR, bool TWO, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
 {
     typedef FewStep<T> Step;
     typedef typename VecOf<T, Step::VEC>::type vec;
     constexpr int MB = PAIR ? 2 : 1, U = NB > 4 ? 2 : 4, CHUNK = U * Step::K, P = 16 * MB + 4;
+    constexpr int NX = TWO ? 2 * NB : NB;
     __shared__ __align__(16) float red[WAVES][16 * NB][P];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m0 = (int64_t)blockIdx.x * 16, k0 = blockIdx.y * a.split_k;
     const int64_t K = a.K - k0 < a.split_k ? a.K - k0 : a.split_k;
     const int at = (lane >> 4) * Step::VEC;
-    const T *w[MB], *x[NB];
+    const T *w[MB], *x[NX];
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
         const int64_t r = m0 + (lane & 15);
@@ -73,6 +77,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
     for (int b = 0; b < NB; ++b) {
         const int64_t r = b * 16 + (lane & 15);
         x[b] = static_cast<const T *>(a.x) + (r < a.n ? r : a.n - 1) * a.ld_x + k0 + at;
+        if constexpr (TWO) x[NB + b] = x[b] + a.second;
     }
     f32x4 acc[MB][NB];
 #pragma unroll
@@ -80,7 +85,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     struct Regs {
-        typename Step::raw w[MB][U], x[NB][U];
+        typename Step::raw w[MB][U], x[NX][U];
     };
     auto load = [&](int64_t k, Regs &r) {
 #pragma unroll
@@ -88,7 +93,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
 #pragma unroll
             for (int b = 0; b < MB; ++b) r.w[b][u] = *reinterpret_cast<const vec *>(w[b] + k + u * Step::K);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) r.x[b][u] = *reinterpret_cast<const vec *>(x[b] + k + u * Step::K);
+            for (int b = 0; b < NX; ++b) r.x[b][u] = *reinterpret_cast<const vec *>(x[b] + k + u * Step::K);
         }
     };
     auto mma = [&](const Regs &r) {
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
 #pragma unroll
             for (int i = 0; i < MB; ++i)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = Step::mma(r.w[i][u], r.x[j][u], acc[i][j]);
+                for (int j = 0; j < NX; ++j) acc[i][j % NB] = Step::mma(r.w[i][u], r.x[j][u], acc[i][j % NB]);
     };
     const int chunks = (int)(K / CHUNK), first = chunks ? (int)(blockIdx.x * 5 % (unsigned)chunks) : 0;
     auto place = [&](int c) { return (int64_t)(c + first < chunks ? c + first : c + first - chunks) * CHUNK; };
@@ -118,7 +123,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
     if (wave == chunks % WAVES) { // the rest of the sum, zeros past its end
         for (int64_t k = (int64_t)chunks * CHUNK; k < K; k += Step::K) {
             const int64_t left = K - k - at;
-            typename Step::raw p[MB], q[NB];
+            typename Step::raw p[MB], q[NX];
             auto part = [&](const T *row) {
                 typename Step::raw v;
 #pragma unroll
@@ -128,11 +133,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
 #pragma unroll
             for (int b = 0; b < MB; ++b) p[b] = part(w[b]);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) q[b] = part(x[b]);
+            for (int b = 0; b < NX; ++b) q[b] = part(x[b]);
 #pragma unroll
             for (int i = 0; i < MB; ++i)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) acc[i][j] = Step::mma(p[i], q[j], acc[i][j]);
+                for (int j = 0; j < NX; ++j) acc[i][j % NB] = Step::mma(p[i], q[j], acc[i][j % NB]);
         }
     }
 #pragma unroll
@@ -169,7 +174,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
             activations<sizeof(T) == 2>(a.act, v[0], value, slope);
 #pragma unroll
             for (int q = 0; q < 8; ++q) value[q] *= v[1][q];
-            store_part<T, 8>(static_cast<T *>(a.out) + i * a.ld_out + m, left, value);
+            if (sizeof(T) == 2 && a.second)
+                store_terms<T, 2>(static_cast<short *>(a.out) + i * a.ld_out + m, a.second, left, value);
+            else store_part<T, 8>(static_cast<T *>(a.out) + i * a.ld_out + m, left, value);
         } else if (a.sum) {
             store_part<float, 8>(a.sum + (blockIdx.y * a.n + i) * a.rows + m, left, v[0]);
         } else {
@@ -185,15 +192,18 @@ void few(const FewArgs &a, int splits, hipStream_t s)
     constexpr std::integral_constant<int, 4> four;
     constexpr std::integral_constant<int, 8> eight;
     const bool idle = (int64_t)grid.x * splits <= 2 * kCUs; // few blocks: more waves in each
-    auto run = [&](auto nb, auto waves) {
+    auto launch = [&](auto two, auto nb, auto waves) {
         constexpr int NB = decltype(nb)::value, WAVES = decltype(waves)::value;
-        hipLaunchKernelGGL((k_ffn_few<T, PAIR, NB, WAVES>), grid, dim3(64 * WAVES), 0, s, a);
+        hipLaunchKernelGGL((k_ffn_few<T, PAIR, decltype(two)::value, NB, WAVES>), grid, dim3(64 * WAVES), 0, s, a);
     };
+    auto run = [&](auto nb, auto waves) { launch(std::false_type(), nb, waves); };
     if constexpr (sizeof(T) == 4) {
         if (a.n > 64) return run(std::integral_constant<int, 8>(), four);
         if (a.n > 32) return idle ? run(four, eight) : run(four, four);
         constexpr std::integral_constant<int, 2> two;
         if (a.n > 16) return idle ? run(two, eight) : run(two, four);
+    } else if constexpr (!PAIR) {
+        if (a.second) return launch(std::true_type(), std::integral_constant<int, 1>(), eight);
     }
     constexpr std::integral_constant<int, 1> one;
     return idle ? run(one, eight) : run(one, four);
@@ -203,7 +213,7 @@ template <class T>
 hipError_t ffn_few(const FfnArgs &a, int dtype, hipStream_t s)
 {
     const FfnPlan p = plan_ffn(a.n, a.D, a.F, FfnTerms<T>::planes, false, copies_of(a, dtype, false), a.ws);
-    FewArgs in{};
+    FewArgs in{}, out{};
     in.w = a.w_in;
     in.ld_w = a.ld_in;
     in.x = a.x;
@@ -216,8 +226,8 @@ hipError_t ffn_few(const FfnArgs &a, int dtype, hipStream_t s)
     in.ld_pre = a.ld_pre;
     in.out = p.mid;
     in.ld_out = p.ldF;
+    in.second = out.second = p.two ? a.n * p.ldF : 0;
     few<T, true>(in, 1, s);
-    FewArgs out{};
     out.w = a.w_out;
     out.ld_w = a.ld_out;
     out.x = p.mid;
@@ -261,6 +271,7 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
     o.mid = p.mid;
     o.ld_mid = p.ldF;
     o.plane_mid = a.n * p.ldF;
+    o.two = p.two;
     const int64_t M = 2 * up(a.F, 32);
     bool done = false;
     if constexpr (PL == 1) {
@@ -271,7 +282,7 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
     }
     if (!done) product<T, false, false, FFN_IN, false>(w_in, x, M, a.n, p.Dp, o, s);
     const Operand mid{p.mid, p.ldF, o.plane_mid, a.n, p.Fp};
-    Outputs<T> out{p.sum};
+    Outputs<T> out{p.sum, {}, p.two};
     int shape;
     const FfnSize z = y_size(a.n, a.D, a.F, PL, &shape);
     launch<T, false, false, FFN_OUT, false>(out(w_out, mid, z, shape, a.y, a.ld_y), shape, s);

@@ -102,12 +102,13 @@ def make(n, D, F, t, gap, seed, std=1.0):
     return (x, ops.rows(g, 2 * F, D, t, gap, std / D ** 0.5), ops.rows(g, D, F, t, gap, 1.0 / F ** 0.5), gy)
 
 
-def check(n, D, F, t, gap, kind, seed=None):
+def check(n, D, F, t, gap, kind, seed=None, terms=1):
     x, w_in, w_out, gy = make(n, D, F, t, gap, n + D + F if seed is None else seed, 2.0)
     op = tt.GatedFeedForward(D, F, activation=kind)
     y, pre = op.forward(x, w_in, w_out, keep=True)
     assert torch.equal(op.forward(x, w_in, w_out), y)
     u, tiny = max(ops.u(t), U32) * 1.01, 2.0 ** -25 if t == F16 else 0.0
+    ua = u ** terms  # a and dp: what a term leaves is rounded once more
     X, WI, WO, GY = (v.double() for v in (x, w_in, w_out, gy))
     p = X @ WI.t()
     size_p = X.abs() @ WI.abs().t()
@@ -117,7 +118,7 @@ def check(n, D, F, t, gap, kind, seed=None):
     a64 = act64(kind, p[:, :F])
     a = a64 * p[:, F:]
     da = 1.13 * dp[:, :F] * p[:, F:].abs() + (a64.abs() + dp[:, :F]) * dp[:, F:] \
-        + 32 * U32 * (p[:, :F] * p[:, F:]).abs() + u * a.abs() + tiny
+        + 32 * U32 * (p[:, :F] * p[:, F:]).abs() + ua * a.abs() + tiny
     ops.close(y, a @ WO.t(), da @ WO.abs().t() + (F + 8) * U32 * (a.abs() @ WO.abs().t())
               + u * (a @ WO.t()).abs() + tiny, "y")
     del p, size_p, dp, a64, a, da
@@ -131,10 +132,10 @@ def check(n, D, F, t, gap, kind, seed=None):
     G = GY @ WO
     eG = (D + 8) * U32 * (GY.abs() @ WO.abs())
     g, h = G * up * slope, G * v
-    eg = eG * (up * slope).abs() + 32 * U32 * (G * up).abs() * (1 + z.abs()) + u * g.abs() + tiny
-    eh = eG * v.abs() + 32 * U32 * (G * z).abs() + u * h.abs() + tiny
+    eg = eG * (up * slope).abs() + 32 * U32 * (G * up).abs() * (1 + z.abs()) + ua * g.abs() + tiny
+    eh = eG * v.abs() + 32 * U32 * (G * z).abs() + ua * h.abs() + tiny
     dP, eP = torch.cat([g, h], 1), torch.cat([eg, eh], 1)
-    mid, emid = v * up, (u + 32 * U32) * (v * up).abs() + 32 * U32 * (z * up).abs() + tiny
+    mid, emid = v * up, (ua + 32 * U32) * (v * up).abs() + 32 * U32 * (z * up).abs() + tiny
     for name, value, ref, bound in (
             ("grad_x", got[0], dP @ WI, eP @ WI.abs() + (2 * F + 8) * U32 * (dP.abs() @ WI.abs())),
             ("grad_w_in", got[1], dP.t() @ X, eP.t() @ X.abs() + (n + 8) * U32 * (dP.abs().t() @ X.abs())),
@@ -172,6 +173,34 @@ def test_large_tiles(n, D, F, t):
         n, D, F = n // 2, D // 2, F // 2
     print(f"[case] ffn n={n} D={D} F={F} {t}", flush=True)
     check(n, D, F, t, 0, "silu")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("n,D,F,gap", [(1, 1, 1, 0), (14, 53, 19, 0), (3, 17, 5, 3), (64, 64, 32, 8), (17, 130, 120, 1),
+                                       (16, 640, 128, 0), (1, 4096, 8192, 0), (1, 2000, 1000, 8), (300, 1000, 6, 0),
+                                       (2048, 64, 1, 0), (30, 1024, 68, 8), (4, 300, 512, 0)])
+def test_few_values_of_a_have_two_terms(n, D, F, gap, t):
+    print(f"[case] ffn two terms n={n} D={D} F={F} gap={gap} {t}", flush=True)
+    # up to 2^11 values of a, no gradient of more than 2^22 (1 x 4096 x 8192: a has 2^13, w_in's
+    # gradient 4096 x 2 x 8192 = 2^26, so one term, whose half step is `u` and not its square)
+    check(n, D, F, t, gap, ACTS[n % 3], terms=2 if n * F <= 1 << 11 and D * max(n, 2 * F) <= 1 << 22 else 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 20])
+def test_an_infinite_a_stays_infinite(n):
+    # silu(400) 400 is past fp16; the second term of an infinite a is nothing, not a NaN
+    D, F = 8, 16
+    x = torch.ones((n, D), device=DEV, dtype=F16)
+    w_in, w_out = torch.full((2 * F, D), 50.0, device=DEV, dtype=F16), torch.ones((D, F), device=DEV, dtype=F16)
+    op = tt.GatedFeedForward(D, F)
+    y, pre = op.forward(x, w_in, w_out, keep=True)
+    assert (pre == 400).all() and (y == float("inf")).all()
+    dx, dw_in, dw_out = op.backward(x, x, pre, w_in, w_out)
+    assert (dw_out == float("inf")).all()
+    # dp: 8 x 400 of both projections, as silu(400) is 400 and its slope 1
+    assert (dw_in == n * 3200.0).all()
 
 
 @pytest.mark.parametrize("dtype", [0, 1, 2])
