@@ -188,6 +188,27 @@ def test_few_values_of_a_have_two_terms(n, D, F, gap, t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 40])
+def test_long_fp32_sums_are_rounded_once_a_step(n):
+    # da sums D = 4000 products, 16 a step: 250 roundings of half a step, 2^-24 at most, of partial sums whose
+    # mean square grows evenly: sqrt(250 / 3 / 2) 2^-24 = 3.8e-7 of da.  Four roundings of dp: 2.4e-7; the sum of
+    # 120 values, the terms left out (2^-25) and the result's rounding: 2^-23 = 1.2e-7.  Six roundings a step
+    # would be 9.5e-7 for da alone
+    D, F = 4000, 60
+    x, w_in, w_out, gy = make(n, D, F, F32, 0, 4)
+    op = tt.GatedFeedForward(D, F)
+    _, pre = op.forward(x, w_in, w_out, keep=True)
+    dx, dw_in, _ = op.backward(gy, x, pre, w_in, w_out)
+    z = pre.double()[:, :F].requires_grad_()
+    v = act64("silu", z)
+    slope, = torch.autograd.grad(v.sum(), z)
+    G = gy.double() @ w_out.double()
+    dP = torch.cat([G * pre.double()[:, F:] * slope, G * v.detach()], 1)
+    for got, ref in ((dx, dP @ w_in.double()), (dw_in, dP.t() @ x.double())):
+        assert (got.double() - ref).norm() <= 8e-7 * ref.norm()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [2, 20])
 def test_an_infinite_a_stays_infinite(n):
     # silu(400) 400 is past fp16; the second term of an infinite a is nothing, not a NaN
