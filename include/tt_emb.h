@@ -466,9 +466,11 @@ int tt_emb_block_workspace_size(int64_t n, int64_t D, size_t *bytes);
  * would raise the gradients' error by half.  act: silu(z) = z sigmoid(z), gelu(z) = z Phi(z), or
  * gelu's tanh form z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
  * bf16 and fp16: sums are fp32, a is rounded to dtype (so in fp16 an |a| past 65504
- * is infinite); up to n F = 2^11, where D max(n, 2F) is no more than 2^22, to two
- * terms of dtype (and an infinity in a weight or in grad_y then makes what it meets
- * infinite or NaN).  fp32: from 129 rows on, and in the backward, operands are taken as
+ * is infinite).  Of an output of few values (y and grad_x n D, grad_w_in 2 F D,
+ * grad_w_out D F), or made of few (n F), 2^11 of either at most, a and dp have two
+ * terms of dtype, since their roundings would not average out there (for n F up to 2^20,
+ * n up to 2^16 and up to 2^22 values of the output; an infinity in a weight, x or
+ * grad_y then makes what it meets infinite or NaN).  fp32: from 129 rows on, and in the backward, operands are taken as
  * three bf16 terms: 24 bits of values from 2^-100 on, the last bits of smaller ones
  * may be lost; a NaN, an infinity or a magnitude past bf16's largest (3.39e38) in x or
  * a weight makes what it takes part in NaN. */

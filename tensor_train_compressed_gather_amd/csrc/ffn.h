@@ -178,7 +178,8 @@ struct FfnOut {
     int64_t ld_mid, plane_mid;
     short *dpre; // planes of [rows][ld_dpre]
     int64_t ld_dpre, plane_dpre;
-    bool two; // a and dp have two terms (16-bit types), the latter half of an output's parts are the second's
+    bool two_mid, two_dpre; // a, dp have two terms (16-bit types)
+    bool two;               // an operand has: the latter half of the parts are the second's
 };
 
 // Rows of both projections as they lie in memory, 32 of the one and 32 of the
@@ -490,7 +491,7 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a[e] = m + e < o.F ? a[e] * u[e] : 0.f;
                 if (i >= o.rows || m >= o.ld_mid) continue;
-                store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, 8, a, SHAPE != BIG && o.two);
+                store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, 8, a, SHAPE != BIG && o.two_mid);
                 if (o.pre && m < o.F) {
                     float *to = o.pre + i * o.ld_pre + m;
                     const int left = (int)(o.F - m < 8 ? o.F - m : 8);
@@ -525,10 +526,10 @@ __device__ __forceinline__ void ffn_tile(const FfnJob &job, unsigned block, char
                         u[e] = x[e] * a[e];
                     }
                     if (i >= o.rows || left <= 0) continue;
-                    store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, left, slope, SHAPE != BIG && o.two);
+                    store_terms<T, PL>(o.mid + i * o.ld_mid + m, o.plane_mid, left, slope, SHAPE != BIG && o.two_mid);
                     short *d = o.dpre + i * o.ld_dpre + m;
-                    store_terms<T, PL>(d, o.plane_dpre, left, g, SHAPE != BIG && o.two);
-                    store_terms<T, PL>(d + o.F, o.plane_dpre, left, u, SHAPE != BIG && o.two);
+                    store_terms<T, PL>(d, o.plane_dpre, left, g, SHAPE != BIG && o.two_dpre);
+                    store_terms<T, PL>(d + o.F, o.plane_dpre, left, u, SHAPE != BIG && o.two_dpre);
                 } else {
                     if (i >= o.rows || left <= 0) continue;
                     if (sum) store_part<float, 8>(sum + i * o.cols + m, left, x);
@@ -592,9 +593,10 @@ unsigned blocks_for(int64_t threads)
 }
 
 // A product's sizes: M outputs in each of N rows, K summed values in `splits`
-// parts of `each`.
+// parts of `each`; two: each part is there for both terms of an operand.
 struct FfnSize {
     int64_t M, N, K;
+    bool two;
     int splits;
     int64_t each;
 
@@ -621,9 +623,7 @@ inline int64_t tiles_of(const FfnSize &z, int PL, int shape)
 // Sums are split so that the units have equal work, one block each (of the
 // backward's SMALL tiles two), but not below kSplit values, a quarter of them for
 // fp32: joining the parts is a launch, 4 us or more.
-//
-// two: each part is there for both terms of an operand.
-int ffn_shape(FfnSize *z, int count, int PL, bool may_split, bool two = false)
+int ffn_shape(FfnSize *z, int count, int PL, bool may_split)
 {
     int64_t big = 0, small = 0, slim = 0, work = 0;
     for (int i = 0; i < count; ++i) {
@@ -639,11 +639,11 @@ int ffn_shape(FfnSize *z, int count, int PL, bool may_split, bool two = false)
     const int64_t blocks = shape == SMALL && count > 1 ? 2 * kCUs : kCUs, least = PL > 1 ? kSplit / 4 : kSplit;
     for (int i = 0; i < count; ++i) {
         int64_t s = may_split ? (z[i].K * blocks + work - 1) / work : 1;
-        if (two) s /= 2;
+        if (z[i].two) s /= 2;
         if (s > z[i].K / least) s = z[i].K / least;
         if (s < 1) s = 1;
         z[i].each = up((z[i].K + s - 1) / s, kPad);
-        z[i].splits = (int)((z[i].K + z[i].each - 1) / z[i].each) * (two ? 2 : 1);
+        z[i].splits = (int)((z[i].K + z[i].each - 1) / z[i].each) * (z[i].two ? 2 : 1);
     }
     return shape;
 }
@@ -694,31 +694,36 @@ FfnCopies ffn_copies(bool fp32, bool grad, int64_t n, int64_t D, int64_t F, bool
     return {!x || !d, !w_in || !d, !w_out || !f, false};
 }
 
-// Whether a and dp of 16-bit inputs have two terms, 16 bits or more.  One term's
-// roundings bring the outputs' error to 1.4 times their own rounding where they are
-// many; few do not average out (14 x 53 x 19 bf16: 1.5 times).  The second term
-// doubles an output's products and adds the join of their parts, 0 to 6 us of a call
-// where there are so few values of a (14 x 53 x 19, backward: 26 us, 22 with one
-// term), but 14 us of 24 for 4 x 300 x 2000 and 21 of 27 for 64 x 2048 x 1024.
-// Grids in patches are not split, so the outputs have few tiles.
-bool two_terms(int64_t n, int64_t D, int64_t F)
+// Products that take a or dp of 16-bit inputs in two terms, 16 bits or more.  One term's
+// roundings bring the outputs' error to 1.41 times their own rounding where both are
+// many; few of either do not average out: of 400 draws of y the largest were 1.6 times
+// with 2^11 outputs or values of a, 1.8 with 742 and 266 (14 x 53 x 19), 3.4 with 16 outputs
+// of 16384 values.  So the fewer of the two decides, for each product by itself: a second
+// term doubles the product and adds the join of its parts, 0 to 6 us of a call where
+// the outputs are few, 14 us of 24 if the 1.2 million outputs of w_in's gradient at
+// 4 x 300 x 2000 had it too, 21 of 27 at 64 x 2048 x 1024.
+//
+// outputs: grids in patches are not split, so a product with two terms has few tiles.
+// n F and n: the tiles that store two terms are not BIG ones (never 512 of those).
+bool two_terms(int64_t n, int64_t F, int64_t outputs)
 {
-    return n * F <= 1 << 11 && D * (n > 2 * F ? n : 2 * F) <= 1 << 22;
+    const int64_t values = n * F;
+    return (values < outputs ? values : outputs) <= 1 << 11 && outputs <= 1 << 22 && values <= 1 << 20 && n <= 1 << 16;
 }
 // The sums of y, and of the gradients of x, w_in and w_out.
 FfnSize y_size(int64_t n, int64_t D, int64_t F, int PL, int *shape = nullptr)
 {
-    FfnSize z{D, n, up(F, kPad)};
-    const int s = ffn_shape(&z, 1, PL, true, PL == 1 && two_terms(n, D, F));
+    FfnSize z{D, n, up(F, kPad), PL == 1 && two_terms(n, F, n * D)};
+    const int s = ffn_shape(&z, 1, PL, true);
     if (shape) *shape = s;
     return z;
 }
 int grad_sizes(FfnSize *z, int64_t n, int64_t D, int64_t F, int PL)
 {
-    z[0] = {D, n, up(2 * F, kPad)};
-    z[1] = {D, 2 * F, up(n, kPad)};
-    z[2] = {F, D, up(n, kPad)};
-    return ffn_shape(z, 3, PL, true, PL == 1 && two_terms(n, D, F));
+    z[0] = {D, n, up(2 * F, kPad), PL == 1 && two_terms(n, F, n * D)};
+    z[1] = {D, 2 * F, up(n, kPad), PL == 1 && two_terms(n, F, 2 * F * D)};
+    z[2] = {F, D, up(n, kPad), PL == 1 && two_terms(n, F, F * D)};
+    return ffn_shape(z, 3, PL, true);
 }
 
 struct FfnPlan {
@@ -726,7 +731,7 @@ struct FfnPlan {
     float *sum;
     int64_t Dp, Fp, Pp; // padded columns of x and gy, of a, of dp
     int64_t ldD, ldF, ldP;
-    bool two;
+    bool two_mid, two_dpre;
     size_t bytes;
 };
 // Distance of rows of so many columns: an odd number of cache lines where it would
@@ -754,18 +759,23 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
     if (c.w_in) p.w_in = take(grad ? 2 * F : 2 * up(F, 32), p.ldD, PL);
     if (c.w_out) p.w_out = take(D, p.ldF, PL);
     if (c.gy) p.gy = take(n, p.ldD, PL);
-    p.two = PL == 1 && two_terms(n, D, F);
-    const int terms = p.two ? 2 : PL;
-    p.mid = take(n, p.ldF, terms);
     size_t sums;
     if (grad) {
-        p.dpre = take(n, p.ldP, terms);
         FfnSize z[3];
         grad_sizes(z, n, D, F, PL);
+        p.two_dpre = z[0].two || z[1].two;
+        p.two_mid = z[2].two;
+        p.dpre = take(n, p.ldP, p.two_dpre ? 2 : PL);
         sums = z[0].bytes() + z[1].bytes() + z[2].bytes();
+    } else if (few_rows(n, PL > 1)) {
+        p.two_mid = PL == 1 && two_terms(n, F, n * D);
+        sums = few_bytes(n, D, F);
     } else {
-        sums = few_rows(n, PL > 1) ? few_bytes(n, D, F) : y_size(n, D, F, PL).bytes();
+        const FfnSize z = y_size(n, D, F, PL);
+        p.two_mid = z.two;
+        sums = z.bytes();
     }
+    p.mid = take(n, p.ldF, p.two_mid ? 2 : PL);
     p.sum = reinterpret_cast<float *>(base ? base + off : nullptr);
     off += sums;
     p.bytes = off;
@@ -844,7 +854,6 @@ template <class T>
 struct Outputs {
     float *sum;
     Joins joins{};
-    bool two; // (operands without a second term have a plane of 0)
     int n = 0;
 
     FfnJob operator()(const Operand &x, const Operand &y, const FfnSize &z, int shape, void *out, int64_t ld)
@@ -858,7 +867,7 @@ struct Outputs {
         if (z.splits > 1) {
             o.sum = sum;
             o.split_k = z.each;
-            o.two = two;
+            o.two = z.two; // (operands without a second term have a plane of 0)
             sum += z.bytes() / sizeof(float);
             joins.job[n] = Join{o.sum, z.splits, z.N, z.M, out, ld};
             joins.first[n + 1] = joins.first[n] + (int)blocks_for(z.N * ((z.M + 3) / 4));

@@ -16,7 +16,10 @@ namespace {
 // loads in flight while one is multiplied, and meet in LDS.  Lane l holds row l %
 // 16 and the l / 16-th 16 bytes of each 64 of a chunk.
 //
-// TWO: a has two terms (two_terms), whose products meet in one sum.
+// TERMS: where a has two terms (two_terms), they are rows i and 8 + i of one operand
+// up to 8 rows, and their products meet where the waves' do; with more rows they are
+// an operand each.  (4096 x 16384 bf16 with one term and with two: 1 row 72.5 and 72.7 us,
+// 8 rows 77 and 83, 16 rows 86 and 101: what the blocks read of a, not the products.)
 //
 // Blocks begin at different places of the sum: rows lie a multiple of a KB apart
 // as a rule, and equal columns of all of them meet in few channels of the L2 (4
@@ -55,13 +58,16 @@ struct FewStep {
     }
 };
 
-template <class T, bool PAIR, bool TWO, int NB, int WAVES>
+enum { ONE, ROWS_OF_ONE, TWO }; // terms of the operand
+
+template <class T, bool PAIR, int TERMS, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
 {
     typedef FewStep<T> Step;
     typedef typename VecOf<T, Step::VEC>::type vec;
     constexpr int MB = PAIR ? 2 : 1, U = NB > 4 ? 2 : 4, CHUNK = U * Step::K, P = 16 * MB + 4;
-    constexpr int NX = TWO ? 2 * NB : NB;
+    constexpr int NX = TERMS == TWO ? 2 * NB : NB;
+    constexpr bool ROWS = TERMS == ROWS_OF_ONE;
     __shared__ __align__(16) float red[WAVES][16 * NB][P];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m0 = (int64_t)blockIdx.x * 16, k0 = blockIdx.y * a.split_k;
@@ -75,9 +81,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        const int64_t r = b * 16 + (lane & 15);
+        const int64_t r = b * 16 + (lane & (ROWS ? 7 : 15));
         x[b] = static_cast<const T *>(a.x) + (r < a.n ? r : a.n - 1) * a.ld_x + k0 + at;
-        if constexpr (TWO) x[NB + b] = x[b] + a.second;
+        if constexpr (ROWS) x[b] += lane & 8 ? a.second : 0;
+        if constexpr (TERMS == TWO) x[NB + b] = x[b] + a.second;
     }
     f32x4 acc[MB][NB];
 #pragma unroll
@@ -164,6 +171,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_ffn_few(FewArgs a)
                 load_vec<float, 8>(&red[s][i][b * 16 + (e & 1) * 8], y);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[b][q] += y[q];
+                if constexpr (ROWS) {
+                    load_vec<float, 8>(&red[s][8 + i][b * 16 + (e & 1) * 8], y);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[b][q] += y[q];
+                }
             }
         if constexpr (PAIR) {
             if (a.pre) {
@@ -192,20 +204,24 @@ void few(const FewArgs &a, int splits, hipStream_t s)
     constexpr std::integral_constant<int, 4> four;
     constexpr std::integral_constant<int, 8> eight;
     const bool idle = (int64_t)grid.x * splits <= 2 * kCUs; // few blocks: more waves in each
-    auto launch = [&](auto two, auto nb, auto waves) {
-        constexpr int NB = decltype(nb)::value, WAVES = decltype(waves)::value;
-        hipLaunchKernelGGL((k_ffn_few<T, PAIR, decltype(two)::value, NB, WAVES>), grid, dim3(64 * WAVES), 0, s, a);
+    auto launch = [&](auto terms, auto nb, auto waves) {
+        constexpr int TERMS = decltype(terms)::value, NB = decltype(nb)::value, WAVES = decltype(waves)::value;
+        hipLaunchKernelGGL((k_ffn_few<T, PAIR, TERMS, NB, WAVES>), grid, dim3(64 * WAVES), 0, s, a);
     };
-    auto run = [&](auto nb, auto waves) { launch(std::false_type(), nb, waves); };
+    auto run = [&](auto nb, auto waves) { launch(std::integral_constant<int, ONE>(), nb, waves); };
     if constexpr (sizeof(T) == 4) {
         if (a.n > 64) return run(std::integral_constant<int, 8>(), four);
         if (a.n > 32) return idle ? run(four, eight) : run(four, four);
         constexpr std::integral_constant<int, 2> two;
         if (a.n > 16) return idle ? run(two, eight) : run(two, four);
-    } else if constexpr (!PAIR) {
-        if (a.second) return launch(std::true_type(), std::integral_constant<int, 1>(), eight);
     }
     constexpr std::integral_constant<int, 1> one;
+    if constexpr (sizeof(T) == 2 && !PAIR) {
+        constexpr std::integral_constant<int, ROWS_OF_ONE> rows;
+        constexpr std::integral_constant<int, TWO> two;
+        if (a.second && a.n <= 8) return idle ? launch(rows, one, eight) : launch(rows, one, four);
+        if (a.second) return idle ? launch(two, one, eight) : launch(two, one, four);
+    }
     return idle ? run(one, eight) : run(one, four);
 }
 
@@ -226,7 +242,7 @@ hipError_t ffn_few(const FfnArgs &a, int dtype, hipStream_t s)
     in.ld_pre = a.ld_pre;
     in.out = p.mid;
     in.ld_out = p.ldF;
-    in.second = out.second = p.two ? a.n * p.ldF : 0;
+    in.second = out.second = p.two_mid ? a.n * p.ldF : 0;
     few<T, true>(in, 1, s);
     out.w = a.w_out;
     out.ld_w = a.ld_out;
@@ -271,7 +287,7 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
     o.mid = p.mid;
     o.ld_mid = p.ldF;
     o.plane_mid = a.n * p.ldF;
-    o.two = p.two;
+    o.two_mid = p.two_mid;
     const int64_t M = 2 * up(a.F, 32);
     bool done = false;
     if constexpr (PL == 1) {
@@ -282,7 +298,7 @@ hipError_t ffn_forward(const FfnArgs &a, int dtype, hipStream_t s)
     }
     if (!done) product<T, false, false, FFN_IN, false>(w_in, x, M, a.n, p.Dp, o, s);
     const Operand mid{p.mid, p.ldF, o.plane_mid, a.n, p.Fp};
-    Outputs<T> out{p.sum, {}, p.two};
+    Outputs<T> out{p.sum};
     int shape;
     const FfnSize z = y_size(a.n, a.D, a.F, PL, &shape);
     launch<T, false, false, FFN_OUT, false>(out(w_out, mid, z, shape, a.y, a.ld_y), shape, s);

@@ -52,7 +52,7 @@ hipError_t ffn_backward(const FfnArgs &a, int dtype, hipStream_t s)
     const Operand w_in = pack(a.w_in, a.ld_in, 2 * a.F, a.D, p.w_in, p.Dp, 0);
     const Operand w_out = pack(a.w_out, a.ld_out, a.D, a.F, p.w_out, p.Fp, 0);
     // the products along dp's columns meet its padding
-    for (int term = 0; term < (p.two ? 2 : 1) && p.Pp > 2 * a.F; ++term)
+    for (int term = 0; term < (p.two_dpre ? 2 : 1) && p.Pp > 2 * a.F; ++term)
         pack.add(Pack{nullptr, 0, a.n, 0, p.dpre + term * a.n * p.ldP + p.Pp - kPad, kPad, p.ldP, a.n * p.ldP, 0});
     pack.run(s);
     FfnOut o{};
@@ -68,10 +68,11 @@ hipError_t ffn_backward(const FfnArgs &a, int dtype, hipStream_t s)
     o.dpre = p.dpre;
     o.ld_dpre = p.ldP;
     o.plane_dpre = a.n * p.ldP;
-    o.two = p.two;
+    o.two_mid = p.two_mid;
+    o.two_dpre = p.two_dpre;
     product<T, true, false, FFN_MID, false>(w_out, gy, a.F, a.n, p.Dp, o, s);
     const Operand mid{p.mid, p.ldF, o.plane_mid, a.n, p.Fp}, dpre{p.dpre, p.ldP, o.plane_dpre, a.n, p.Pp};
-    Outputs<T> out{p.sum, {}, p.two};
+    Outputs<T> out{p.sum};
     FfnSize z[3];
     const int shape = grad_sizes(z, a.n, a.D, a.F, PL);
     const FfnGrads g{out(w_in, dpre, z[0], shape, a.gx, a.ld_gx), out(x, dpre, z[1], shape, a.gw_in, a.ld_gin),

@@ -524,7 +524,9 @@ class GatedFeedForward(_Operator):
     backward(grad_y, x, p, w_in, w_out) -> (grad_x, grad_w_in, grad_w_out).
 
     bf16 and fp16: sums are fp32, a and p's gradient are rounded to the type
-    between the products (to two terms of it up to n F = 2^11).  fp32: from 129 rows on, and in the backward, operands
+    between the products: outputs are off by some 1.4 times their own rounding.
+    For an output of up to 2^11 values, or made of up to 2^11 values of a, they
+    have two terms of it.  fp32: from 129 rows on, and in the backward, operands
     are taken as three bf16 terms, 24 bits (less below 2^-100).  16-bit rows of
     a multiple of 8 columns (along a sum: of 64) that begin at multiples of 16
     bytes are read in place, and so are up to 16 rows' operands in the forward (up
