@@ -61,17 +61,18 @@ struct FfnTerms<float> {
 template <bool NEAR>
 __device__ __forceinline__ void activations(int act, const float (&z)[8], float (&value)[8], float (&slope)[8])
 {
-    // z times the sigmoid of x, dx the slope of x
+    // z times the sigmoid of x, dx the slope of x.  (What vanishes at the sigmoid's ends is
+    // multiplied first: value times dx passes fp32 from z = 1.2e13 on in gelu's tanh form.)
     auto of_sigmoid = [&](int i, float x, float dx) {
         if constexpr (NEAR) {
             const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
             value[i] = z[i] * sg;
-            slope[i] = fmaf(value[i] * dx, 1.f - sg, sg);
+            slope[i] = fmaf(value[i] * (1.f - sg), dx, sg);
         } else {
             const float e = expf(-fabsf(x)), r = 1.f / (1.f + e);
             const float sg = x < 0.f ? e * r : r, other = x < 0.f ? r : e * r; // sigmoid of x and of -x
             value[i] = z[i] * sg;
-            slope[i] = fmaf(value[i] * dx, other, sg);
+            slope[i] = fmaf(value[i] * other, dx, sg);
         }
     };
     if (act == TT_EMB_ACT_SILU) {
@@ -80,7 +81,7 @@ __device__ __forceinline__ void activations(int act, const float (&z)[8], float 
     } else if (act == TT_EMB_ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float zz = z[i] * z[i];
+            const float zz = fminf(z[i] * z[i], 1e30f); // (x and dx stay finite)
             of_sigmoid(i, z[i] * fmaf(0.0713548163f, zz, 1.59576912f), fmaf(0.214064449f, zz, 1.59576912f));
         }
     } else {
