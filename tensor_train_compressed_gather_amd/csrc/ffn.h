@@ -766,7 +766,6 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
         grad_sizes(z, n, D, F, PL);
         p.two_dpre = z[0].two || z[1].two;
         p.two_mid = z[2].two;
-        p.dpre = take(n, p.ldP, p.two_dpre ? 2 : PL);
         sums = z[0].bytes() + z[1].bytes() + z[2].bytes();
     } else if (few_rows(n, PL > 1)) {
         p.two_mid = PL == 1 && two_terms(n, F, n * D);
@@ -777,6 +776,7 @@ FfnPlan plan_ffn(int64_t n, int64_t D, int64_t F, int PL, bool grad, const FfnCo
         sums = z.bytes();
     }
     p.mid = take(n, p.ldF, p.two_mid ? 2 : PL);
+    if (grad) p.dpre = take(n, p.ldP, p.two_dpre ? 2 : PL);
     p.sum = reinterpret_cast<float *>(base ? base + off : nullptr);
     off += sums;
     p.bytes = off;
