@@ -346,6 +346,23 @@ ColumnSums block_sums(const BlockNormArgs &a)
     return c;
 }
 
+// Shares of the rows in the kernel that adds up long rows' columns: some four
+// blocks for each compute unit, of sixteen rows at least.
+int block_col_parts(int64_t n, int64_t D)
+{
+    const int64_t strips = (D + kBlockCols - 1) / kBlockCols, most = (n + 15) / 16;
+    int64_t parts = (4 * kCUs + strips - 1) / strips;
+    if (parts > most) parts = most;
+    return (int)(parts < 1 ? 1 : parts);
+}
+
+size_t block_parts_bytes(int64_t n, int64_t D)
+{
+    int64_t parts = n < kBlockGradBlocks ? n : kBlockGradBlocks;
+    if (D > kBlockRegs) parts = block_col_parts(n, D);
+    return round256((size_t)(kBlockSums * parts * part_row(D)) * sizeof(float));
+}
+
 template <class T, class R>
 hipError_t block_backward(const BlockNormArgs &a, hipStream_t s)
 {
@@ -377,23 +394,6 @@ hipError_t block_backward(const BlockNormArgs &a, hipStream_t s)
 }
 
 } // namespace
-
-// Shares of the rows in the kernel that adds up long rows' columns: some four
-// blocks for each compute unit, of sixteen rows at least.
-int block_col_parts(int64_t n, int64_t D)
-{
-    const int64_t strips = (D + kBlockCols - 1) / kBlockCols, most = (n + 15) / 16;
-    int64_t parts = (4 * kCUs + strips - 1) / strips;
-    if (parts > most) parts = most;
-    return (int)(parts < 1 ? 1 : parts);
-}
-
-size_t block_parts_bytes(int64_t n, int64_t D)
-{
-    int64_t parts = n < kBlockGradBlocks ? n : kBlockGradBlocks;
-    if (D > kBlockRegs) parts = block_col_parts(n, D);
-    return round256((size_t)(kBlockSums * parts * part_row(D)) * sizeof(float));
-}
 
 size_t block_workspace(int64_t n, int64_t D)
 {

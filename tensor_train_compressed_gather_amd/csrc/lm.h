@@ -170,8 +170,6 @@ struct BlockNormArgs {
 hipError_t launch_block_forward(const BlockNormArgs &a, int dtype, int res_dtype, hipStream_t s);
 hipError_t launch_block_backward(const BlockNormArgs &a, int dtype, int res_dtype, hipStream_t s);
 size_t block_workspace(int64_t n, int64_t D);
-size_t block_parts_bytes(int64_t n, int64_t D);
-int block_col_parts(int64_t n, int64_t D);
 
 struct FfnArgs {
     const void *x, *w_in, *w_out;

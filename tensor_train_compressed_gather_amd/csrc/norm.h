@@ -92,32 +92,6 @@ inline void norm_cols(const float *part, int blocks, int64_t D, int64_t ld, int 
     else hipLaunchKernelGGL(k_norm_cols<false>, grid, dim3(1024), 0, s, part, blocks, (int)D, (int)ld, out);
 }
 
-// Threads per row and vectors per thread: the fewest threads that hold a row
-// of nv vectors with at most 16 elements each (80 registers in the backward).
-template <class T, class F>
-hipError_t norm_shape(int64_t D, F &&g)
-{
-    auto f = [&](auto tpr, auto nv) {
-        if (D % (16 / (int)sizeof(T)) == 0) return g(tpr, nv, std::true_type());
-        return g(tpr, nv, std::false_type());
-    };
-    constexpr int VEC = 16 / (int)sizeof(T), MAX = 16 / VEC;
-    const int64_t nv = (D + VEC - 1) / VEC;
-    auto one = [&](auto tpr) {
-        constexpr int TPR = decltype(tpr)::value;
-        if constexpr (MAX == 4) {
-            if (nv > 2 * TPR) return f(tpr, std::integral_constant<int, 4>());
-        }
-        if (nv > TPR) return f(tpr, std::integral_constant<int, 2>());
-        return f(tpr, std::integral_constant<int, 1>());
-    };
-    if (nv <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-    if (nv <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-    if (nv <= 64 * MAX) return one(std::integral_constant<int, 64>());
-    if (nv <= 256 * MAX) return one(std::integral_constant<int, 256>());
-    return one(std::integral_constant<int, 1024>());
-}
-
 } // namespace
 
 } // namespace ttemb
