@@ -431,7 +431,7 @@ int tt_emb_norm_workspace_size(int64_t n, int64_t D, size_t *bytes);
  * NULL: 1 (ld_gate is that of rows).  y and the statistics are those of h before
  * it is rounded.  stats fp32 [n][4]: mean and rstd of x (0 and 1 without POST), mean
  * and rstd of h (a mean is 0 with RMS); may be NULL.  h may be residual and y may be
- * x, with the same ld. */
+ * x, with the same ld; the backward then needs copies of both from before the call. */
 enum { TT_EMB_BLOCK_RMS = 1, TT_EMB_BLOCK_POST = 2, TT_EMB_BLOCK_GATE_ROWS = 4 };
 int tt_emb_block_forward(const void *x, int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n,
                          int64_t D, int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
@@ -445,9 +445,11 @@ int tt_emb_block_forward(const void *x, int64_t ld_x, const void *residual, int6
  *   du = block_scale gate dh,  grad_x = J_x (du post_gamma)  (or du)
  *   grad_gate = block_scale u dh, for a gate [D] its sum over the rows
  *   dgamma = sum_i grad_y N(h), dbeta = sum_i grad_y, dpost_gamma = sum_i du N(x), dpost_beta = sum_i du
- * h is made again from x and residual, in fp32.  Sums over the rows are fp32 in a
- * fixed order, of param_dtype, overwritten, each may be NULL (so may a grad_gate [D]).
- * What is written may not share memory with what is read. */
+ * h is made again in fp32 from x and residual, which are those that the forward was
+ * given: overwritten by a forward in place they give wrong gradients and no error.
+ * Sums over the rows are fp32 in a fixed order, of param_dtype, overwritten, each may be
+ * NULL (so may a grad_gate [D]).  What is written may not share memory with what is
+ * read. */
 int tt_emb_block_backward(const void *grad_y, int64_t ld_grad_y, const void *grad_h, int64_t ld_grad_h, const void *x,
                           int64_t ld_x, const void *residual, int64_t ld_residual, int64_t n, int64_t D,
                           int32_t dtype, int32_t residual_dtype, const void *gate, int64_t ld_gate,
@@ -470,10 +472,11 @@ int tt_emb_block_workspace_size(int64_t n, int64_t D, size_t *bytes);
  * grad_w_out D F), or made of few (n F), 2^11 of either at most, a and dp have two
  * terms of dtype, since their roundings would not average out there (for n F up to 2^20,
  * n up to 2^16 and up to 2^22 values of the output; an infinity in a weight, x or
- * grad_y then makes what it meets infinite or NaN).  fp32: from 129 rows on, and in the backward, operands are taken as
- * three bf16 terms: 24 bits of values from 2^-100 on, the last bits of smaller ones
- * may be lost; a NaN, an infinity or a magnitude past bf16's largest (3.39e38) in x or
- * a weight makes what it takes part in NaN. */
+ * grad_y then makes what it meets infinite or NaN).  fp32: from 129 rows on, and in
+ * the backward, operands are taken as three bf16 terms: 24 bits of values from 2^-100
+ * on, the last bits of smaller ones may be lost; a NaN, an infinity or a magnitude past bf16's largest (3.39e38) in x, a
+ * weight, grad_y, a or dp makes what it takes part in NaN.  What is written may not
+ * share memory with what is read. */
 enum { TT_EMB_ACT_SILU = 0, TT_EMB_ACT_GELU = 1, TT_EMB_ACT_GELU_TANH = 2 };
 int tt_emb_ffn_forward(const void *x, int64_t ld_x, const void *w_in, int64_t ld_in, const void *w_out, int64_t ld_out,
                        int64_t n, int64_t D, int64_t F, int32_t dtype, int32_t activation, float *pre, int64_t ld_pre,
@@ -482,9 +485,10 @@ int tt_emb_ffn_forward(const void *x, int64_t ld_x, const void *w_in, int64_t ld
 /* Its gradients, from grad_y [n][D] and the forward's pre:
  *   da = grad_y w_out,  dp_ij = da_ij p_i,F+j act'(p_ij),  dp_i,F+j = da_ij act(p_ij)
  *   grad_x = dp w_in,  grad_w_in = dp^T x,  grad_w_out = grad_y^T a
- * all of dtype, overwritten; dp and a are rounded like a in the forward.  Sums over
- * the rows are taken in a fixed order (bit-reproducible).  What is written may not
- * share memory with what is read. */
+ * all of dtype, overwritten; dp and a are rounded like a in the forward (in fp16 to
+ * multiples of 2^-24 where they are small: gradients below 2^-14 want a loss scale).
+ * Sums over the rows are taken in a fixed order (bit-reproducible).  What is written
+ * may not share memory with what is read. */
 int tt_emb_ffn_backward(const void *grad_y, int64_t ld_grad_y, const void *x, int64_t ld_x, const float *pre,
                         int64_t ld_pre, const void *w_in, int64_t ld_in, const void *w_out, int64_t ld_out, int64_t n,
                         int64_t D, int64_t F, int32_t dtype, int32_t activation, void *grad_x, int64_t ld_grad_x,
@@ -604,7 +608,8 @@ int tt_emb_adamw_update_scaled(int32_t count, float *const *params, const void *
  * order that depends on the sizes alone.  tt_emb_clip_norm reads the gradients;
  * tt_emb_clip_scale also multiplies them by the factor in place, rounded to
  * their type, and leaves them alone where it is 1; its tensors may not share memory.
- * A NaN makes N and the factor NaN; an infinity makes N infinite and the factor 0. */
+ * A NaN makes N and the factor NaN; an infinity makes N infinite and the factor 0 (1
+ * where there is no bound). */
 int tt_emb_clip_norm(int32_t count, const void *const *grads, const int32_t *dtypes, const int64_t *numel,
                      double max_norm, double eps, float *norm, float *factor, void *ws, size_t ws_bytes, void *stream);
 int tt_emb_clip_scale(int32_t count, void *const *grads, const int32_t *dtypes, const int64_t *numel,

@@ -8,11 +8,12 @@
 //   dx = the same of du gp and N(x);  column sums of gy hhat, gy, du N(x), du, b u dh
 //
 // (without the means of q where N is the root mean square).  It reads x and r,
-// from which it makes h again in fp32: as many bytes as reading h, which a
-// caller may then overwrite, and without its rounding.  The column sums of rows
-// of up to 4096 values stay in registers across a block's rows.  Longer rows are
-// read again, from the caches, for each pair of sums, and a second kernel adds up
-// their columns, from the same inputs and two sums of each row.
+// those that the forward was given, and makes h again in fp32: as many bytes as
+// reading h, which a caller may overwrite after the forward, and without its
+// rounding.  The column sums of rows of up to 4096 values stay in registers across
+// a block's rows.  Longer rows are read again, from the caches, for each pair of
+// sums, and a second kernel adds up their columns, from the same inputs and two
+// sums of each row.
 //
 // Memory bounds it: 16384 x 4096 bf16 in 153 us (six tensors, 5.3 TB/s) and 5 for
 // the sums of the blocks' columns; 32768 x 128 fp32 in 22 (4.6 TB/s) and 3.8.

@@ -395,7 +395,9 @@ class BlockNorm(_Operator):
     stats): y of x's type, h of the residual's (x's type or fp32), stats fp32
     [n, 4] for the backward.  gammas and betas [D] (x's type or fp32, all of
     one) may be None; gate is None, [D] of their type, or [n, D] of x's.
-    ``out`` may be x and ``out_h`` the residual itself.
+    ``out`` may be x and ``out_h`` the residual itself, as when nothing is
+    trained: the backward takes x and the residual as they were before the forward,
+    and what it would give for the overwritten ones is wrong, with no error.
     backward(grad_y, grad_h, x, residual, stats, gate, gamma, post_gamma,
     post_beta) -> (grad_x, grad_residual, grad_gate, dgamma, dbeta,
     dpost_gamma, dpost_beta), None where ``kind`` and ``post`` have no such
@@ -846,7 +848,7 @@ class GradientClip(_Operator):
     Gradients are contiguous and fp32, bf16 or fp16, mixed as they come; their
     squares are added in fp64, in an order that depends on the sizes alone.  A
     NaN makes N and the factor NaN; an infinity makes N infinite and the factor
-    0 (NaN where it meets the infinity)."""
+    0 (NaN where it meets the infinity; 1 for a ``max_norm`` of infinity, no bound)."""
 
     def __init__(self, max_norm: float, eps: float = 1e-6, device="cuda"):
         super().__init__(device)
