@@ -84,7 +84,7 @@ __device__ __forceinline__ void activations(int act, const float (&z)[8], float 
     } else if (act == TT_EMB_ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float zz = fminf(z[i] * z[i], 1e30f); // (x and dx stay finite)
+            const float zz = fminf(z[i] * z[i], 1e30f); // (dx stays finite)
             of_sigmoid(i, z[i] * fmaf(0.0713548163f, zz, 1.59576912f), fmaf(0.214064449f, zz, 1.59576912f));
         }
     } else {
